@@ -114,6 +114,19 @@ EOU_DECODER = DecoderConfig()
 TINY_DECODER = DecoderConfig(vocab=30, pred_dim=64, joint_dim=64, max_symbols=3)
 
 
+@dataclass(frozen=True)
+class Kv8Config:
+    """Shape of a paged 8-bit K/V cache (include/cac_kv8.h)."""
+    n_layers: int
+    kv_heads: int
+    head_dim: int                 # multiple of 16, at most 256
+    page_tokens: int              # multiple of 16, at most 1024
+    n_pages: int                  # pages of the pool, shared by all sequences
+    max_seqs: int                 # sequence ids 0 .. max_seqs-1
+    max_pages: int                # pages of one sequence
+    code: str = "int8"            # "int8" or "e4m3"
+
+
 def subsampled_len(t_mel: int) -> int:
     """Encoder frames produced from t_mel mel frames: ceil(.) three times."""
     t = t_mel

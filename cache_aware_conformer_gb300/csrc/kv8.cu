@@ -1,0 +1,777 @@
+// The paged 8-bit K/V cache (include/cac_kv8.h): quantising writes, reads, and
+// the page operations.  Every kernel reads lengths, tables and free pages on the
+// device, so the calls queue (or replay from a graph) without the host.
+//
+// All of it moves bytes; nothing here has arithmetic that could bound it.  The
+// writers and readers take one block of 16 tokens and one head per warp, because
+// a block's scale is the maximum over exactly that.
+#include <algorithm>
+
+#include "kv8.cuh"
+#include "status.cuh"
+
+namespace cac {
+
+int kv_check_shape(const cac_kv8* c) {
+    if (!c || c->n_layers < 1 || c->kv_heads < 1 || c->kv_heads > 65535 || c->head_dim < 16 || c->page_tokens < 16 ||
+        c->n_pages < 1 || c->max_seqs < 1 || c->max_pages < 1)
+        return CAC_E_INVAL;
+    if (c->head_dim % 16 || c->head_dim > 256 || c->page_tokens % KV_BLOCK || c->page_tokens > 1024 ||
+        (c->code != CAC_KV8_INT8 && c->code != CAC_KV8_E4M3))
+        return CAC_E_UNSUPPORTED;
+    if ((long long)c->max_pages * c->page_tokens >= (1ll << 30) || c->n_pages >= (1 << 30) || c->max_seqs >= (1 << 28))
+        return CAC_E_UNSUPPORTED;
+    return CAC_OK;
+}
+
+int kv_check_cache(const cac_kv8* c) {
+    const int r = kv_check_shape(c);
+    if (r != CAC_OK) return r;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->table || !c->lens || !c->refs || !c->free_list ||
+        !c->n_free || !c->pending || !c->work || !c->status)
+        return CAC_E_INVAL;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) |
+                            reinterpret_cast<uintptr_t>(c->table) | reinterpret_cast<uintptr_t>(c->lens) |
+                            reinterpret_cast<uintptr_t>(c->refs) | reinterpret_cast<uintptr_t>(c->free_list) |
+                            reinterpret_cast<uintptr_t>(c->n_free) | reinterpret_cast<uintptr_t>(c->pending) |
+                            reinterpret_cast<uintptr_t>(c->work) | reinterpret_cast<uintptr_t>(c->status);
+    if (((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) || (words & 3))
+        return CAC_E_ALIGN;
+    return CAC_OK;
+}
+
+namespace {
+
+constexpr int PLAN_T = 1024;
+
+__device__ __forceinline__ int pages_of(int tokens, int page_tokens) {
+    return (int)(((long long)tokens + page_tokens - 1) / page_tokens);
+}
+
+// Exclusive prefix sum over the block of two counts at once, and their totals.
+struct Two {
+    int a, b;
+};
+__device__ Two block_scan(Two x, Two* total) {
+    __shared__ int sa[32], sb[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int a = x.a, b = x.b;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int ua = __shfl_up_sync(0xffffffffu, a, d), ub = __shfl_up_sync(0xffffffffu, b, d);
+        if (lane >= d) a += ua, b += ub;
+    }
+    __syncthreads();  // the arrays may still be read from an earlier call
+    if (lane == 31) sa[warp] = a, sb[warp] = b;
+    __syncthreads();
+    int oa = 0, ob = 0, ta = 0, tb = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) oa += sa[w], ob += sb[w];
+        ta += sa[w], tb += sb[w];
+    }
+    *total = Two{ta, tb};
+    return Two{oa + a - x.a, ob + b - x.b};
+}
+
+// ---------------------------------------------------------------------------
+// init
+// ---------------------------------------------------------------------------
+__global__ void kv_init_kernel(cac_kv8 c, long long work_ints) {
+    pdl_trigger();
+    pdl_wait();
+    const long long t = blockIdx.x * (long long)blockDim.x + threadIdx.x, step = (long long)gridDim.x * blockDim.x;
+    for (long long i = t; i < (long long)c.max_seqs * c.max_pages; i += step) c.table[i] = -1;
+    for (long long i = t; i < c.max_seqs; i += step) c.lens[i] = 0, c.pending[2 * i] = 0, c.pending[2 * i + 1] = 0;
+    for (long long i = t; i < c.n_pages; i += step) c.refs[i] = 0, c.free_list[i] = (int)(c.n_pages - 1 - i);
+    for (long long i = t; i < work_ints; i += step) c.work[i] = 0;
+    if (t == 0) *c.n_free = c.n_pages, *c.status = 0;
+}
+
+// ---------------------------------------------------------------------------
+// extend.  One block decides for all sequences of the call: it needs the sum of
+// what they ask before it may change anything.  Latency bounds it (a few
+// dependent reads and two scans).
+// ---------------------------------------------------------------------------
+struct Want {
+    int id, len, count, have, fresh;  // pages it has, pages it needs past those
+    int last;                         // a last page that is not full, or -1
+    bool copy;                        // ... which has to be copied first
+};
+
+__device__ __forceinline__ Want want_of(const cac_kv8& c, const KvRows& rows, const int32_t* ids, int i) {
+    Want w;
+    w.id = ids[i];
+    w.count = rows.at(i + 1) - rows.at(i);
+    w.len = c.lens[w.id];
+    w.have = pages_of(w.len, c.page_tokens);
+    w.fresh = pages_of(w.len + w.count, c.page_tokens) - w.have;
+    w.last = -1;
+    w.copy = false;
+    if (w.count > 0 && w.len % c.page_tokens) w.last = c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens];
+    return w;
+}
+
+__global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, const KvRows rows, const int32_t* ids) {
+    __shared__ int error;
+    __shared__ int s_place[PLAN_T], s_have[PLAN_T], s_fresh[PLAN_T], s_id[PLAN_T];
+    pdl_trigger();
+    pdl_wait();
+    const KvWork work = kv_work(c);
+    const int n = rows.n, tid = threadIdx.x;
+    const long long most = (long long)c.max_pages * c.page_tokens;
+    if (tid == 0) error = 0, work.count[0] = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += PLAN_T) {
+        const int id = ids[i];
+        const long long count = (long long)rows.at(i + 1) - rows.at(i);
+        if (id < 0 || id >= c.max_seqs || count < 0) {
+            atomicCAS(&error, 0, CAC_E_BOUNDS);
+            continue;
+        }
+        c.pending[2 * id + 1] = i;  // its place in this call; an id listed twice finds another place there
+        if (c.lens[id] + count > most) atomicCAS(&error, 0, CAC_E_LIMIT);
+    }
+    __syncthreads();
+    if (!error) {
+        // pages that are not full: how many of this call's sequences end in each, and the last of those
+        for (int i = tid; i < n; i += PLAN_T) {
+            if (c.pending[2 * ids[i] + 1] != i) atomicCAS(&error, 0, CAC_E_INVAL);
+            const Want w = want_of(c, rows, ids, i);
+            if (w.count > 0 && w.len % c.page_tokens && w.last < 0) atomicCAS(&error, 0, CAC_E_STATE);
+            if (w.last >= 0) {
+                atomicAdd(work.named + w.last, 1);
+                atomicMax(work.keeper + w.last, i + 1);
+            }
+        }
+    }
+    __syncthreads();
+    const bool counted = !error || error == CAC_E_INVAL || error == CAC_E_STATE;
+    // A shared page stays with the last of this call's sequences that end in it when no other table names it; the
+    // others (all of them, when one does) get a copy.  Neither depends on the order of the atomics.
+    auto decide = [&](int i) {
+        Want w = want_of(c, rows, ids, i);
+        if (w.last >= 0)
+            w.copy = __ldcg(c.refs + w.last) > __ldcg(work.named + w.last) || __ldcg(work.keeper + w.last) != i + 1;
+        return w;
+    };
+    int pages = 0, copies = 0;
+    const int n_free = *c.n_free;
+    if (!error) {
+        long long sum = 0;
+        for (int base = 0; base < n; base += PLAN_T) {
+            Want w{};
+            if (base + tid < n) w = decide(base + tid);
+            Two total;
+            block_scan(Two{w.fresh, w.copy}, &total);
+            sum += (long long)total.a + total.b;
+            if (sum > n_free) break;  // the same for every thread
+        }
+        if (tid == 0 && sum > n_free) error = CAC_E_NOMEM;
+    }
+    __syncthreads();
+    const int failed = error;
+    for (int base = 0; base < n; base += PLAN_T) {
+        const int i = base + tid;
+        Want w{};
+        if (i < n && !failed) w = decide(i);
+        Two total = {0, 0}, at = {0, 0};
+        if (!failed) at = block_scan(Two{w.fresh, w.copy}, &total);
+        // pages leave the end of the free list: first this chunk's copies, then its fresh pages
+        const int top = n_free - pages - copies - 1;
+        __syncthreads();
+        s_fresh[tid] = 0;
+        if (i < n && !failed) {
+            if (w.copy) {
+                const int to = c.free_list[top - at.b];
+                work.copy_from[copies + at.b] = w.last;
+                work.copy_to[copies + at.b] = to;
+                c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens] = to;
+                c.refs[to] = 1;
+            }
+            s_place[tid] = top - total.b - at.a, s_have[tid] = w.have, s_fresh[tid] = w.fresh, s_id[tid] = w.id;
+        }
+        __syncthreads();
+        // a warp to a sequence, so that a long prompt's pages are entered 32 at a time
+        for (int s = tid >> 5; s < min(PLAN_T, n - base); s += PLAN_T / 32)
+            for (int k = tid & 31; k < s_fresh[s]; k += 32) {
+                const int page = c.free_list[s_place[s] - k];
+                c.table[(long long)s_id[s] * c.max_pages + s_have[s] + k] = page;
+                c.refs[page] = 1;
+            }
+        pages += total.a;
+        copies += total.b;
+    }
+    __syncthreads();
+    for (int k = tid; k < copies; k += PLAN_T) atomicSub(c.refs + work.copy_from[k], 1);
+    // lengths, and the counters back to zero
+    for (int i = tid; i < n; i += PLAN_T) {
+        const int id = ids[i];
+        if (id < 0 || id >= c.max_seqs) continue;
+        if (failed) {
+            if (counted) {
+                const Want w = want_of(c, rows, ids, i);
+                if (w.last >= 0) work.named[w.last] = 0, work.keeper[w.last] = 0;
+            }
+            c.pending[2 * id] = 0;
+            continue;
+        }
+        const int len = c.lens[id], count = rows.at(i + 1) - rows.at(i);
+        c.pending[2 * id] = count;
+        c.lens[id] = len + count;
+    }
+    if (!failed)
+        for (int k = tid; k < copies; k += PLAN_T) work.named[work.copy_from[k]] = 0, work.keeper[work.copy_from[k]] = 0;
+    __syncthreads();
+    if (!failed)  // pages that were kept
+        for (int i = tid; i < n; i += PLAN_T) {
+            const int id = ids[i], count = c.pending[2 * id], len = c.lens[id] - count;
+            if (count > 0 && len % c.page_tokens) {
+                const int last = c.table[(long long)id * c.max_pages + len / c.page_tokens];
+                work.named[last] = 0, work.keeper[last] = 0;
+            }
+        }
+    if (tid == 0) {
+        if (failed) latch_error(c.status, failed);
+        else *c.n_free = n_free - pages - copies, work.count[0] = copies;
+    }
+}
+
+// Whole pages, all layers: K, V and their scales.  Unit u of a copy is (layer, K or V).
+__device__ __forceinline__ void copy_page(const cac_kv8& c, int from, int to, int u) {
+    const int layer = u >> 1;
+    uint8_t* codes = static_cast<uint8_t*>(u & 1 ? c.v : c.k);
+    float* scales = u & 1 ? c.v_scale : c.k_scale;
+    const uint4* a = reinterpret_cast<const uint4*>(codes + kv_head_at(c, layer, from, 0));
+    uint4* b = reinterpret_cast<uint4*>(codes + kv_head_at(c, layer, to, 0));
+    const int vecs = c.kv_heads * (c.page_tokens * c.head_dim / 16);  // < 2^31: 65535 heads * 1024 * 256 / 16 = 2^30
+    int i = threadIdx.x;
+    for (; i + 3 * (int)blockDim.x < vecs; i += 4 * blockDim.x) {
+        uint4 x[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = __ldcs(a + i + k * blockDim.x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) b[i + k * blockDim.x] = x[k];
+    }
+    for (; i < vecs; i += blockDim.x) b[i] = a[i];
+    const float* sa = scales + kv_scale_at(c, layer, from, 0);
+    float* sb = scales + kv_scale_at(c, layer, to, 0);
+    for (int k = threadIdx.x; k < c.kv_heads * (c.page_tokens / KV_BLOCK); k += blockDim.x) sb[k] = sa[k];
+}
+
+__global__ void __launch_bounds__(256) kv_copy_kernel(const cac_kv8 c) {
+    pdl_trigger();
+    pdl_wait();
+    const KvWork work = kv_work(c);
+    const long long units = (long long)work.count[0] * c.n_layers * 2;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int k = (int)(u / (c.n_layers * 2));
+        copy_page(c, work.copy_from[k], work.copy_to[k], (int)(u % (c.n_layers * 2)));
+    }
+}
+
+// ---------------------------------------------------------------------------
+// write
+// ---------------------------------------------------------------------------
+constexpr int WRITE_WARPS = 8;
+
+// eight consecutive values as floats
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const bf16* p, float (&x)[8]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[2 * k] = __uint_as_float(w[k] << 16);
+        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <int CODE> __device__ __forceinline__ uint2 encode8(const float (&x)[8], float f) {
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k >> 2] |= kv_encode<CODE>(x[k] * f) << (8 * (k & 3));
+    return make_uint2(w[0], w[1]);
+}
+template <int CODE> __device__ __forceinline__ void decode8(uint2 w, float (&x)[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = kv_decode<CODE>(((k < 4 ? w.x : w.y) >> (8 * (k & 3))) & 255u);
+}
+
+struct KvWrite {
+    cac_kv8 c;
+    KvRows rows;
+    const int32_t* ids;
+    const void *k, *v;
+    long long k_stride, v_stride;
+    int layer, blocks;
+};
+
+// One warp per (block of 16 tokens, head, K or V); NIT = ceil(head_dim / 16)
+// passes of 32 lanes x 8 values cover the block.  Block number b of the call
+// belongs to the sequence i with first(i) = starts(i) / 16 + 2 i <= b < first(i + 1):
+// m new tokens touch at most (m + 30) / 16 blocks, and first(i + 1) - first(i) >=
+// m / 16 + 2, so no scan over the lengths is needed to deal the blocks out.
+template <class T, int CODE, int NIT>
+__global__ void __launch_bounds__(WRITE_WARPS * 32) kv_write_kernel(const __grid_constant__ KvWrite a) {
+    pdl_trigger();
+    pdl_wait();
+    const cac_kv8& c = a.c;
+    const int lane = threadIdx.x & 31;
+    const long long u = (long long)blockIdx.x * WRITE_WARPS + (threadIdx.x >> 5);
+    const int per_block = 2 * c.kv_heads;
+    const int b = (int)(u / per_block);
+    if (b >= a.blocks) return;
+    const int head = (int)(u % per_block) >> 1, which = (int)(u & 1);
+    const int i = warp_last_le(a.rows.n, b, [&](int s) { return a.rows.at(s) / KV_BLOCK + 2ll * s; });
+    if (i < 0) return;
+    const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0, id = a.ids[i];
+    const int nth = b - (row0 / KV_BLOCK + 2 * i);
+    if (m == 0) return;
+    if (id < 0 || id >= c.max_seqs || row0 < 0 || m < 0 || row0 + (long long)m > a.rows.rows) {
+        if (lane == 0) latch_error(c.status, CAC_E_BOUNDS);
+        return;
+    }
+    if (c.pending[2 * id] != m || c.pending[2 * id + 1] != i) {
+        if (lane == 0) latch_error(c.status, CAC_E_STATE);
+        return;
+    }
+    const int base = c.lens[id] - m;                         // first new token
+    const int t0 = (base / KV_BLOCK + nth) * KV_BLOCK;       // first token of the block
+    const int lo = max(base - t0, 0), hi = min(base + m - t0, KV_BLOCK);  // new rows [lo, hi), older ones before lo
+    if (hi <= lo) return;
+    const int page = c.table[(long long)id * c.max_pages + t0 / c.page_tokens];
+    if (page < 0) return;  // trimmed before it was written: no query sees it
+    const int in_page = t0 % c.page_tokens;
+    const int D = c.head_dim, vec = D >> 3;
+    const T* src = static_cast<const T*>(which ? a.v : a.k) + (long long)head * D;
+    const long long stride = which ? a.v_stride : a.k_stride;
+    uint8_t* codes = static_cast<uint8_t*>(which ? c.v : c.k) + kv_head_at(c, a.layer, page, head) + in_page * D;
+    float* scale_at = (which ? c.v_scale : c.k_scale) + kv_scale_at(c, a.layer, page, head) + in_page / KV_BLOCK;
+
+    float x[NIT][8];
+    float amax = 0.f;
+    bool bad = false;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+        const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
+        if (row >= lo && row < hi) {
+            load8(src + (row0 + (long long)(t0 + row - base)) * stride + col, x[it]);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const float y = fabsf(x[it][k]);
+                if (y <= FLT_MAX) amax = fmaxf(amax, y);
+                else bad = true;
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    if (__any_sync(0xffffffffu, bad) && lane == 0) latch_error(c.status, CAC_E_NONFINITE);
+    float scale = fmaxf(amax * (1.f / kv_top<CODE>()), KV_MIN_SCALE);
+    if (lo > 0) {
+        const float before = *scale_at;
+        if (before >= scale) {
+            scale = before;
+        } else {  // the older codes at the larger scale
+            const float r = before / scale;
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+                const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
+                if (row < lo) {
+                    uint2* p = reinterpret_cast<uint2*>(codes + row * D + col);
+                    float y[8];
+                    decode8<CODE>(*p, y);
+                    *p = encode8<CODE>(y, r);
+                }
+            }
+        }
+    }
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+        const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
+        if (row >= lo && row < hi) *reinterpret_cast<uint2*>(codes + row * D + col) = encode8<CODE>(x[it], inv);
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale_at = scale;
+}
+
+// ---------------------------------------------------------------------------
+// read: a thread takes eight values of a token's head
+// ---------------------------------------------------------------------------
+struct KvRead {
+    cac_kv8 c;
+    const int32_t *ids, *first;
+    void *k, *v;
+    int layer, n, count;
+};
+
+template <class T, int CODE> __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRead a) {
+    pdl_trigger();
+    pdl_wait();
+    const cac_kv8& c = a.c;
+    const int vec = c.head_dim >> 3, per_token = c.kv_heads * vec;
+    const long long items = (long long)a.n * a.count * per_token;
+    for (long long e = blockIdx.x * 256ll + threadIdx.x; e < items; e += gridDim.x * 256ll) {
+        const long long token = e / per_token;
+        const int r = (int)(e - token * per_token), head = r / vec, col = (r - head * vec) * 8;
+        const int i = (int)(token / a.count), id = a.ids[i];
+        const long long t = (long long)a.first[i] + (token - (long long)i * a.count);
+        int page = -1;
+        if (id < 0 || id >= c.max_seqs) latch_error(c.status, CAC_E_BOUNDS);
+        else if (t >= 0 && t < c.lens[id]) page = c.table[(long long)id * c.max_pages + t / c.page_tokens];
+        const long long out = token * ((long long)c.kv_heads * c.head_dim) + head * c.head_dim + col;
+        const int in_page = page < 0 ? 0 : (int)(t % c.page_tokens);
+        const long long at = page < 0 ? 0 : kv_head_at(c, a.layer, page, head) + (long long)in_page * c.head_dim + col;
+        const long long sc = page < 0 ? 0 : kv_scale_at(c, a.layer, page, head) + in_page / KV_BLOCK;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            T* dst = static_cast<T*>(which ? a.v : a.k);
+            if (!dst) continue;
+            float y[8] = {};
+            if (page >= 0) {
+                decode8<CODE>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? c.v : c.k) + at), y);
+                const float f = (which ? c.v_scale : c.k_scale)[sc];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] *= f;
+            }
+            store8(dst + out, y);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// fork, truncate, trim: one block per sequence
+// ---------------------------------------------------------------------------
+constexpr int SEQ_T = 256;
+
+// One table less names `page` (-1: none); the last one puts it on the free list.
+// A whole warp calls it.
+__device__ __forceinline__ void release(const cac_kv8& c, int page) {
+    const bool gone = page >= 0 && atomicSub(c.refs + page, 1) == 1;
+    const unsigned m = __ballot_sync(0xffffffffu, gone);
+    if (!m) return;
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(c.n_free, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0);
+    if (gone) c.free_list[at + __popc(m & ((1u << lane) - 1))] = page;
+}
+
+// Whether entry i's id stands anywhere else in ids, or at all in other (null: none)
+__device__ __forceinline__ bool listed_twice(const int32_t* ids, const int32_t* other, int n, int i) {
+    const int id = ids[i];
+    bool hit = false;
+    for (int j = threadIdx.x; j < n; j += blockDim.x) hit |= (j != i && ids[j] == id) || (other && other[j] == id);
+    return __syncthreads_or(hit) != 0;
+}
+
+__global__ void __launch_bounds__(SEQ_T) kv_fork_kernel(const cac_kv8 c, int n, const int32_t* src, const int32_t* dst) {
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x, from = src[i], to = dst[i];
+    if (from < 0 || from >= c.max_seqs || to < 0 || to >= c.max_seqs) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_BOUNDS);
+        return;
+    }
+    if (listed_twice(dst, src, n, i)) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_INVAL);
+        return;
+    }
+    const int len = c.lens[from], have = pages_of(len, c.page_tokens), had = pages_of(c.lens[to], c.page_tokens);
+    int32_t* row = c.table + (long long)to * c.max_pages;
+    const int32_t* of = c.table + (long long)from * c.max_pages;
+    // A page that both name cannot reach zero here: the source names it throughout.
+    for (int j0 = 0; j0 < max(have, had); j0 += SEQ_T) {
+        const int j = j0 + threadIdx.x;
+        const int now = j < have ? of[j] : -1;
+        if (now >= 0) atomicAdd(c.refs + now, 1);
+        release(c, j < had ? row[j] : -1);
+        if (j < max(have, had)) row[j] = now;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) c.lens[to] = len, c.pending[2 * to] = 0, c.pending[2 * from] = 0;
+}
+
+__global__ void __launch_bounds__(SEQ_T)
+    kv_truncate_kernel(const cac_kv8 c, int n, const int32_t* ids, const int32_t* new_len, int each) {
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x, id = ids[i], asked = new_len ? new_len[i] : each;
+    if (id < 0 || id >= c.max_seqs || asked < 0) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_BOUNDS);
+        return;
+    }
+    if (listed_twice(ids, nullptr, n, i)) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_INVAL);
+        return;
+    }
+    const int len = c.lens[id], to = min(asked, len), had = pages_of(len, c.page_tokens);
+    int32_t* row = c.table + (long long)id * c.max_pages;
+    for (int j0 = pages_of(to, c.page_tokens); j0 < had; j0 += SEQ_T) {
+        const int j = j0 + threadIdx.x;
+        release(c, j < had ? row[j] : -1);
+        if (j < had) row[j] = -1;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) c.lens[id] = to, c.pending[2 * id] = 0;
+}
+
+__global__ void __launch_bounds__(SEQ_T) kv_trim_kernel(const cac_kv8 c, int n, const int32_t* ids, KvWindow win) {
+    pdl_trigger();
+    pdl_wait();
+    const int i = blockIdx.x, id = ids[i];
+    if (id < 0 || id >= c.max_seqs) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_BOUNDS);
+        return;
+    }
+    if (listed_twice(ids, nullptr, n, i)) {
+        if (threadIdx.x == 0) latch_error(c.status, CAC_E_INVAL);
+        return;
+    }
+    const int begin = pages_of(win.sinks, c.page_tokens), end = win.low(c.lens[id]) / c.page_tokens;
+    int32_t* row = c.table + (long long)id * c.max_pages;
+    for (int j0 = begin; j0 < end; j0 += SEQ_T) {
+        const int j = j0 + threadIdx.x;
+        release(c, j < end ? row[j] : -1);
+        if (j < end) row[j] = -1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// compact.  With `used` pages in use, the moves are the k-th page in use at or
+// past `used` into the k-th free page before it: as many of one as of the other.
+// ---------------------------------------------------------------------------
+__global__ void __launch_bounds__(PLAN_T, 1) kv_compact_plan_kernel(const cac_kv8 c) {
+    pdl_trigger();
+    pdl_wait();
+    const KvWork work = kv_work(c);
+    const int used = c.n_pages - *c.n_free;
+    int32_t *places = work.list, *movers = work.list + (c.n_pages / 2 + 1);
+    int holes = 0, moves = 0;
+    for (int base = 0; base < c.n_pages; base += PLAN_T) {
+        const int p = base + threadIdx.x;
+        const bool in_use = p < c.n_pages && c.refs[p] > 0;
+        const Two x = {p < used && !in_use, p >= used && in_use};
+        Two total;
+        const Two at = block_scan(x, &total);
+        const int room = c.n_pages / 2 + 1;  // there are at most min(used, n_pages - used) of either
+        if (x.a && holes + at.a < room) places[holes + at.a] = p;
+        if (x.b && moves + at.b < room) movers[moves + at.b] = p;
+        holes += total.a;
+        moves += total.b;
+    }
+    __syncthreads();
+    moves = min(min(moves, holes), c.n_pages / 2 + 1);  // equal by construction
+    for (int k = threadIdx.x; k < moves; k += PLAN_T) {
+        work.name[movers[k]] = places[k];
+        c.refs[places[k]] = c.refs[movers[k]];
+        c.refs[movers[k]] = 0;
+    }
+    for (int k = threadIdx.x; k < c.n_pages - used; k += PLAN_T) c.free_list[k] = c.n_pages - 1 - k;
+    if (threadIdx.x == 0) work.count[1] = moves, work.count[2] = used;
+}
+
+__global__ void __launch_bounds__(256) kv_compact_kernel(const cac_kv8 c) {
+    pdl_trigger();
+    pdl_wait();
+    const KvWork work = kv_work(c);
+    const int32_t *places = work.list, *movers = work.list + (c.n_pages / 2 + 1);
+    const int moves = work.count[1], used = work.count[2];
+    if (moves == 0) return;
+    for (int s = blockIdx.x; s < c.max_seqs; s += gridDim.x) {
+        int32_t* row = c.table + (long long)s * c.max_pages;
+        for (int j = threadIdx.x; j < pages_of(c.lens[s], c.page_tokens); j += blockDim.x)
+            if (row[j] >= used) row[j] = work.name[row[j]];
+    }
+    const long long units = (long long)moves * c.n_layers * 2;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int k = (int)(u / (c.n_layers * 2));
+        copy_page(c, movers[k], places[k], (int)(u % (c.n_layers * 2)));
+    }
+}
+
+int launched(cudaError_t e) { return e == cudaSuccess ? CAC_OK : CAC_E_CUDA; }
+
+// Checks that the calls over a list of sequences share.
+int check_list(const cac_kv8* c, int n, const void* ids) {
+    const int r = kv_check_cache(c);
+    if (r != CAC_OK) return r;
+    if (n < 0 || (n > 0 && !ids)) return CAC_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(ids) & 3) return CAC_E_ALIGN;
+    return CAC_OK;
+}
+
+constexpr int COPY_BLOCKS = 152 * 8;
+
+template <class T, int CODE> cudaError_t launch_write(const KvWrite& a, unsigned grid, cudaStream_t s) {
+    const dim3 g(grid), b(WRITE_WARPS * 32);
+    if (a.c.head_dim <= 64) return launch_k(kv_write_kernel<T, CODE, 4>, g, b, 0, s, 1, a);
+    if (a.c.head_dim <= 128) return launch_k(kv_write_kernel<T, CODE, 8>, g, b, 0, s, 1, a);
+    return launch_k(kv_write_kernel<T, CODE, 16>, g, b, 0, s, 1, a);
+}
+
+}  // namespace
+}  // namespace cac
+
+using namespace cac;
+
+extern "C" size_t cac_kv8_work_ints(const cac_kv8* c) { return kv_check_shape(c) == CAC_OK ? kv_work_ints(*c) : 0; }
+
+extern "C" int cac_kv8_init(const cac_kv8* c, void* stream) {
+    const int r = kv_check_cache(c);
+    if (r != CAC_OK) return r;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    return launched(launch_k(kv_init_kernel, dim3(304), dim3(256), 0, static_cast<cudaStream_t>(stream), 1, *c,
+                             (long long)kv_work_ints(*c)));
+}
+
+extern "C" int cac_kv8_extend(const cac_kv8* c, int n, const int32_t* ids, const int32_t* starts, int each,
+                              void* stream) {
+    int r = check_list(c, n, ids);
+    if (r != CAC_OK) return r;
+    if ((!starts && each < 0) || n > c->max_seqs) return CAC_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(starts) & 3) return CAC_E_ALIGN;
+    if (!starts && each > c->max_pages * c->page_tokens) return CAC_E_LIMIT;
+    if (!starts && (long long)n * each > INT32_MAX) return CAC_E_LIMIT;
+    if (n == 0) return CAC_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const KvRows rows{starts, each, n, INT32_MAX};
+    r = launched(launch_k(kv_extend_kernel, dim3(1), dim3(PLAN_T), 0, s, 1, *c, rows, ids));
+    if (r != CAC_OK) return r;
+    const long long units = (long long)n * c->n_layers * 2;
+    return launched(launch_k(kv_copy_kernel, dim3((unsigned)std::min<long long>(units, COPY_BLOCKS)), dim3(256), 0, s,
+                             1, *c));
+}
+
+extern "C" int cac_kv8_write(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
+                             const void* k, const void* v, long long k_stride, long long v_stride, int dtype,
+                             void* stream) {
+    const int r = check_list(c, n, ids);
+    if (r != CAC_OK) return r;
+    if (layer < 0 || layer >= c->n_layers || rows < 0 || n > c->max_seqs ||
+        (dtype != CAC_DTYPE_F32 && dtype != CAC_DTYPE_BF16))
+        return CAC_E_INVAL;
+    if (n == 0 || rows == 0) return CAC_OK;
+    if (!starts && rows % n) return CAC_E_INVAL;
+    const long long width = (long long)c->kv_heads * c->head_dim, size = dtype == CAC_DTYPE_BF16 ? 2 : 4;
+    if (!k || !v || k_stride < width || v_stride < width) return CAC_E_INVAL;
+    if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) ||
+        ((k_stride * size | v_stride * size) & 15) || (reinterpret_cast<uintptr_t>(starts) & 3))
+        return CAC_E_ALIGN;
+    const long long blocks = (long long)rows / KV_BLOCK + 2ll * n;
+    const long long grid = (blocks * 2 * c->kv_heads + WRITE_WARPS - 1) / WRITE_WARPS;
+    if (grid > INT32_MAX) return CAC_E_LIMIT;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const KvWrite a{*c, {starts, rows / n, n, rows}, ids, k, v, k_stride, v_stride, layer, (int)blocks};
+    if (c->code == CAC_KV8_INT8)
+        return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_INT8>(a, (unsigned)grid, s)
+                                                : launch_write<float, CAC_KV8_INT8>(a, (unsigned)grid, s));
+    return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_E4M3>(a, (unsigned)grid, s)
+                                            : launch_write<float, CAC_KV8_E4M3>(a, (unsigned)grid, s));
+}
+
+extern "C" int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* first, int count,
+                            void* k, void* v, int dtype, void* stream) {
+    const int r = check_list(c, n, ids);
+    if (r != CAC_OK) return r;
+    if (layer < 0 || layer >= c->n_layers || count < 0 || (dtype != CAC_DTYPE_F32 && dtype != CAC_DTYPE_BF16))
+        return CAC_E_INVAL;
+    if (n == 0 || count == 0 || (!k && !v)) return CAC_OK;
+    if (!first) return CAC_E_INVAL;
+    if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) ||
+        (reinterpret_cast<uintptr_t>(first) & 3))
+        return CAC_E_ALIGN;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    const long long items = (long long)n * count * c->kv_heads * (c->head_dim / 8);
+    const dim3 grid((unsigned)std::min<long long>((items + 255) / 256, 152 * 64)), block(256);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const KvRead a{*c, ids, first, k, v, layer, n, count};
+    if (c->code == CAC_KV8_INT8)
+        return launched(dtype == CAC_DTYPE_BF16
+                            ? launch_k(kv_read_kernel<bf16, CAC_KV8_INT8>, grid, block, 0, s, 1, a)
+                            : launch_k(kv_read_kernel<float, CAC_KV8_INT8>, grid, block, 0, s, 1, a));
+    return launched(dtype == CAC_DTYPE_BF16 ? launch_k(kv_read_kernel<bf16, CAC_KV8_E4M3>, grid, block, 0, s, 1, a)
+                                            : launch_k(kv_read_kernel<float, CAC_KV8_E4M3>, grid, block, 0, s, 1, a));
+}
+
+extern "C" int cac_kv8_fork(const cac_kv8* c, int n, const int32_t* src, const int32_t* dst, void* stream) {
+    const int r = check_list(c, n, src);
+    if (r != CAC_OK) return r;
+    if (n > 0 && !dst) return CAC_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(dst) & 3) return CAC_E_ALIGN;
+    if (n == 0) return CAC_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    return launched(launch_k(kv_fork_kernel, dim3(n), dim3(SEQ_T), 0, static_cast<cudaStream_t>(stream), 1, *c, n, src,
+                             dst));
+}
+
+extern "C" int cac_kv8_truncate(const cac_kv8* c, int n, const int32_t* ids, const int32_t* new_len, int each,
+                                void* stream) {
+    const int r = check_list(c, n, ids);
+    if (r != CAC_OK) return r;
+    if (!new_len && each < 0) return CAC_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(new_len) & 3) return CAC_E_ALIGN;
+    if (n == 0) return CAC_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    return launched(launch_k(kv_truncate_kernel, dim3(n), dim3(SEQ_T), 0, static_cast<cudaStream_t>(stream), 1, *c, n,
+                             ids, new_len, each));
+}
+
+extern "C" int cac_kv8_trim(const cac_kv8* c, int n, const int32_t* ids, int att_left, int att_chunk, int sinks,
+                            void* stream) {
+    const int r = check_list(c, n, ids);
+    if (r != CAC_OK) return r;
+    if (att_chunk < 1 || sinks < 0) return CAC_E_INVAL;
+    if (n == 0 || att_left < 0) return CAC_OK;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    return launched(launch_k(kv_trim_kernel, dim3(n), dim3(SEQ_T), 0, static_cast<cudaStream_t>(stream), 1, *c, n, ids,
+                             KvWindow{att_left, att_chunk, sinks}));
+}
+
+extern "C" int cac_kv8_compact(const cac_kv8* c, void* stream) {
+    int r = kv_check_cache(c);
+    if (r != CAC_OK) return r;
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    r = launched(launch_k(kv_compact_plan_kernel, dim3(1), dim3(PLAN_T), 0, s, 1, *c));
+    if (r != CAC_OK) return r;
+    return launched(launch_k(kv_compact_kernel, dim3(COPY_BLOCKS), dim3(256), 0, s, 1, *c));
+}
+
+extern "C" int cac_kv8_check(const cac_kv8* c) {
+    const int r = kv_check_cache(c);
+    if (r != CAC_OK) return r;
+    DeviceScope dev(c->device);
+    if (!dev.ok || cudaDeviceSynchronize() != cudaSuccess) return CAC_E_CUDA;
+    int st = 0;
+    if (cudaMemcpy(&st, c->status, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return CAC_E_CUDA;
+    if (st != 0 && cudaMemset(c->status, 0, 4) != cudaSuccess) return CAC_E_CUDA;
+    return st;
+}

@@ -23,7 +23,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
 CAC_OK = 0
 ERRORS = {-1: "CAC_E_INVAL", -2: "CAC_E_ALIGN", -3: "CAC_E_STATE", -4: "CAC_E_NOMEM", -5: "CAC_E_CUDA",
           -6: "CAC_E_DEVICE", -7: "CAC_E_NONFINITE", -8: "CAC_E_TIMEOUT", -9: "CAC_E_UNSUPPORTED",
-          -10: "CAC_E_LIMIT"}
+          -10: "CAC_E_LIMIT", -11: "CAC_E_BOUNDS"}
 
 # every symbol include/cac.h declares
 SYMBOLS = ["cac_weights_size", "cac_model_create", "cac_model_create_palette", "cac_model_destroy", "cac_pool_create", "cac_pool_destroy",
@@ -46,6 +46,11 @@ SYMBOLS = ["cac_weights_size", "cac_model_create", "cac_model_create_palette", "
            "cac_beam_create", "cac_beam_destroy", "cac_beam_reset", "cac_beam_step", "cac_beam_check",
            "cac_beam_get"]
 
+# every symbol include/cac_kv8.h declares
+KV8_SYMBOLS = ["cac_kv8_work_ints", "cac_kv8_init", "cac_kv8_extend", "cac_kv8_write", "cac_kv8_read",
+               "cac_kv8_attend", "cac_kv8_attend_workspace", "cac_kv8_fork", "cac_kv8_truncate", "cac_kv8_trim",
+               "cac_kv8_compact", "cac_kv8_check"]
+
 
 class CacError(RuntimeError):
     def __init__(self, code: int, what: str):
@@ -67,6 +72,13 @@ class CacStreamState(ctypes.Structure):
     _fields_ = [("subT", c_int32), ("Lc", c_int32), ("finished", c_int32), ("x0_rows", c_int32),
                 ("mel_tail", POINTER(c_float)), ("k_cache", POINTER(c_float)), ("v_cache", POINTER(c_float)),
                 ("conv_cache", POINTER(c_float)), ("x0", POINTER(c_float))]
+
+
+class CacKv8(ctypes.Structure):
+    _fields_ = ([(n, c_int32) for n in ("n_layers", "kv_heads", "head_dim", "page_tokens", "n_pages", "max_seqs",
+                                        "max_pages", "code", "device", "reserved")] +
+                [(n, c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lens", "refs", "free_list", "n_free",
+                                         "pending", "work", "status")])
 
 
 _LIB = None
@@ -137,6 +149,19 @@ def _lib():
             "cac_beam_step": (c_int, [vp, c_int, ip, vp, c_longlong, c_int, c_int, vp]),
             "cac_beam_check": (c_int, [vp]),
             "cac_beam_get": (c_int, [vp, c_int, c_int, fp, ip, ip, ip]),
+            "cac_kv8_work_ints": (c_size_t, [vp]),
+            "cac_kv8_init": (c_int, [vp, vp]),
+            "cac_kv8_extend": (c_int, [vp, c_int, vp, vp, c_int, vp]),
+            "cac_kv8_write": (c_int, [vp, c_int, c_int, vp, vp, c_int, vp, vp, c_longlong, c_longlong, c_int, vp]),
+            "cac_kv8_read": (c_int, [vp, c_int, c_int, vp, vp, c_int, vp, vp, c_int, vp]),
+            "cac_kv8_attend": (c_int, [vp, c_int, c_int, vp, vp, c_int, c_int, c_int, c_float, c_int, c_int, c_int, vp,
+                                       c_longlong, vp, c_longlong, vp, c_int, vp, c_size_t, vp]),
+            "cac_kv8_attend_workspace": (c_size_t, [vp, c_int, c_int, c_int, c_int]),
+            "cac_kv8_fork": (c_int, [vp, c_int, vp, vp, vp]),
+            "cac_kv8_truncate": (c_int, [vp, c_int, vp, vp, c_int, vp]),
+            "cac_kv8_trim": (c_int, [vp, c_int, vp, c_int, c_int, c_int, vp]),
+            "cac_kv8_compact": (c_int, [vp, vp]),
+            "cac_kv8_check": (c_int, [vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -700,3 +725,172 @@ class BeamDecoder:
         slots = [None if not np.isfinite(sc[k]) else (tuple(int(t) for t in tok[k, :ln[k]]), float(sc[k]))
                  for k in range(K)]
         return slots, best.value
+
+
+class Kv8Cache:
+    """A paged 8-bit K/V cache shared by many sequences, and attention over it
+    (include/cac_kv8.h).  The cache lives in torch tensors of this object (k, v
+    int8 [layers, pages, kv_heads, page_tokens, head_dim]; k_scale, v_scale fp32
+    [layers, pages, kv_heads, page_tokens / 16]; table, lens, refs, free, n_free
+    int32); `tensors` adopts existing ones, left as they are.
+
+    Sequences are named by int32 cuda tensors.  A call's rows lie one after
+    another in its k, v, q and outputs: the same number for each sequence, or
+    starts[i] .. starts[i+1]-1 with `starts` an int32 cuda tensor [n + 1] and
+    `max_new` no less than the longest.  Calls queue on `stream` (the current one
+    by default), never wait, and can be captured into CUDA graphs; errors that
+    only the device sees are raised by check()."""
+
+    def __init__(self, cfg, device=None, tensors=None):
+        import torch
+        if cfg.code not in ("int8", "e4m3"):
+            raise ValueError(f"code {cfg.code!r}: int8 or e4m3")
+        self.cfg = cfg
+        tensors = dict(tensors or {})
+        if device is None:
+            device = next(iter(tensors.values())).device if tensors else "cuda"
+        self.device = torch.device(device)
+        if self.device.type != "cuda":
+            raise ValueError("a Kv8Cache lives on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        L, P, H, PT, D = cfg.n_layers, cfg.n_pages, cfg.kv_heads, cfg.page_tokens, cfg.head_dim
+        self._c = CacKv8(L, H, D, PT, P, cfg.max_seqs, cfg.max_pages, 0 if cfg.code == "int8" else 1,
+                         self.device.index, 0)
+        self._ref = ctypes.addressof(self._c)
+        ints = int(_lib().cac_kv8_work_ints(self._ref))
+        if ints == 0:
+            raise ValueError(f"{cfg}: a shape outside what the kernels implement")
+        i8, f32, i32 = torch.int8, torch.float32, torch.int32
+        shapes = {"k": (i8, (L, P, H, PT, D)), "v": (i8, (L, P, H, PT, D)),
+                  "k_scale": (f32, (L, P, H, PT // 16)), "v_scale": (f32, (L, P, H, PT // 16)),
+                  "table": (i32, (cfg.max_seqs, cfg.max_pages)), "lens": (i32, (cfg.max_seqs,)), "refs": (i32, (P,)),
+                  "free": (i32, (P,)), "n_free": (i32, (1,)), "pending": (i32, (cfg.max_seqs, 2)), "work": (i32, (ints,)),
+                  "status": (i32, (1,))}
+        unknown = set(tensors) - set(shapes)
+        if unknown:
+            raise ValueError(f"no such tensors: {sorted(unknown)}")
+        for name, (dt, shape) in shapes.items():
+            t = tensors.get(name)
+            if t is None:
+                make = torch.zeros if name in ("pending", "work", "status") else torch.empty
+                t = make(shape, dtype=dt, device=self.device)
+            elif t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
+                raise ValueError(f"{name}: a contiguous {dt} tensor {shape} on {self.device} is needed")
+            setattr(self, name, t)
+            setattr(self._c, "free_list" if name == "free" else name, t.data_ptr())
+        if not tensors:
+            self.init()
+        elif not {"table", "lens", "refs", "free", "n_free"} <= set(tensors):
+            raise ValueError("adopted tensors include table, lens, refs, free and n_free")
+
+    def _on(self, stream):
+        import torch
+        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+
+    def _ints(self, t, n, what):
+        import torch
+        if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or \
+                not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous int32 tensor [{n}] on {self.device} is needed")
+        return t.data_ptr()
+
+    def _list(self, ids, starts):
+        n = ids.shape[0]
+        return n, self._ints(ids, n, "ids"), None if starts is None else self._ints(starts, n + 1, "starts")
+
+    def _act(self, t, heads, what, like=None):
+        """Row stride and dtype code of an activation [rows, heads, head_dim]."""
+        import torch
+        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.cfg.head_dim or t.device != self.device:
+            raise ValueError(f"{what}: a tensor [rows, {heads}, {self.cfg.head_dim}] on {self.device} is needed")
+        row, head, one = t.stride()
+        if one != 1 or (heads > 1 and head != t.shape[2]):
+            raise ValueError(f"{what}: the heads of a row have to lie one after another")
+        if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+            raise ValueError(f"{what}: bfloat16 or float32")
+        if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0]):
+            raise ValueError(f"{what}: the type and rows of the other operand")
+        return (row if t.shape[0] > 1 else heads * t.shape[2]), 1 if t.dtype is torch.bfloat16 else 0
+
+    def init(self, stream=None):
+        """Empty the cache (cac_kv8_init)."""
+        _check(_lib().cac_kv8_init(self._ref, self._on(stream)), "cac_kv8_init")
+
+    def extend(self, ids, each: int = 1, starts=None, max_new=None, stream=None):
+        """Room for `each` (or starts[i+1] - starts[i]) new tokens of each sequence (cac_kv8_extend)."""
+        n, p, s = self._list(ids, starts)
+        _check(_lib().cac_kv8_extend(self._ref, n, p, s, each, self._on(stream)), "cac_kv8_extend")
+
+    def write(self, layer: int, ids, k, v, starts=None, max_new=None, stream=None):
+        """Quantise one layer's k, v [rows, kv_heads, head_dim] of the tokens of the last extend (cac_kv8_write)."""
+        n, p, s = self._list(ids, starts)
+        ks, dt = self._act(k, self.cfg.kv_heads, "k")
+        vs, _ = self._act(v, self.cfg.kv_heads, "v", k)
+        _check(_lib().cac_kv8_write(self._ref, layer, n, p, s, k.shape[0], k.data_ptr(), v.data_ptr(), ks, vs, dt,
+                                    self._on(stream)), "cac_kv8_write")
+
+    def read(self, layer: int, ids, first, count: int, dtype=None, stream=None):
+        """(k, v) [n, count, kv_heads, head_dim]: the values of tokens first[i] .. first[i] + count - 1 (cac_kv8_read)."""
+        import torch
+        n, p, _ = self._list(ids, None)
+        dtype = dtype or torch.float32
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("dtype: bfloat16 or float32")
+        with torch.cuda.stream(stream):  # the outputs belong to the stream that fills them
+            k, v = (torch.empty(n, count, self.cfg.kv_heads, self.cfg.head_dim, dtype=dtype, device=self.device)
+                    for _ in range(2))
+        _check(_lib().cac_kv8_read(self._ref, layer, n, p, self._ints(first, n, "first"), count, k.data_ptr(),
+                                   v.data_ptr(), 1 if dtype is torch.bfloat16 else 0, self._on(stream)),
+               "cac_kv8_read")
+        return k, v
+
+    def attend(self, layer: int, ids, q, att_left: int = -1, att_chunk: int = 1, sinks: int = 0, scale=None, starts=None,
+               max_new=None, lse: bool = False, out=None, stream=None):
+        """Attention of each sequence's last tokens, q [rows, heads, head_dim], over its cache (cac_kv8_attend);
+        returns out, or (out, lse [rows, heads]).  scale: 1 / sqrt(head_dim) by default."""
+        import torch
+        n, p, s = self._list(ids, starts)
+        rows, heads = q.shape[0], q.shape[1]
+        qs, dt = self._act(q, heads, "q")
+        if max_new is None:
+            max_new = rows
+        L = _lib()
+        need = int(L.cac_kv8_attend_workspace(self._ref, n, rows, max_new if s else (rows // n if n else 0), heads))
+        with torch.cuda.stream(stream):  # the outputs and the workspace belong to the stream that runs the call
+            if out is None:
+                out = torch.empty(rows, heads, self.cfg.head_dim, dtype=q.dtype, device=self.device)
+            sums = torch.empty(rows, heads, dtype=torch.float32, device=self.device) if lse else None
+            space = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        os_, _ = self._act(out, heads, "out", q)
+        _check(L.cac_kv8_attend(self._ref, layer, n, p, s, rows, max_new, heads,
+                                scale if scale is not None else self.cfg.head_dim ** -0.5, att_left, att_chunk, sinks,
+                                q.data_ptr(), qs, out.data_ptr(), os_, _ptr(sums), dt, _ptr(space), need,
+                                self._on(stream)), "cac_kv8_attend")
+        return (out, sums) if lse else out
+
+    def fork(self, src, dst, stream=None):
+        """Sequence dst[i] becomes a copy of src[i] that shares its pages (cac_kv8_fork)."""
+        n = src.shape[0]
+        _check(_lib().cac_kv8_fork(self._ref, n, self._ints(src, n, "src"), self._ints(dst, n, "dst"),
+                                   self._on(stream)), "cac_kv8_fork")
+
+    def truncate(self, ids, new_len=0, stream=None):
+        """Shorten to new_len tokens (an int, or int32 cuda tensor [n]); 0 frees the sequence (cac_kv8_truncate)."""
+        n, p, _ = self._list(ids, None)
+        one = isinstance(new_len, int)
+        _check(_lib().cac_kv8_truncate(self._ref, n, p, None if one else self._ints(new_len, n, "new_len"),
+                                       new_len if one else 0, self._on(stream)), "cac_kv8_truncate")
+
+    def trim(self, ids, att_left: int, att_chunk: int = 1, sinks: int = 0, stream=None):
+        """Release the pages that no later query sees under this window (cac_kv8_trim)."""
+        n, p, _ = self._list(ids, None)
+        _check(_lib().cac_kv8_trim(self._ref, n, p, att_left, att_chunk, sinks, self._on(stream)), "cac_kv8_trim")
+
+    def compact(self, stream=None):
+        """Move the pages in use to the front of the pool (cac_kv8_compact)."""
+        _check(_lib().cac_kv8_compact(self._ref, self._on(stream)), "cac_kv8_compact")
+
+    def check(self):
+        """Wait for the device and raise the error that it latched, if any (cac_kv8_check)."""
+        _check(_lib().cac_kv8_check(self._ref), "cac_kv8_check")
