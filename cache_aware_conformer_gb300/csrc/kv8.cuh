@@ -33,12 +33,12 @@ template <int CODE> __device__ __forceinline__ uint32_t kv_encode(float x) {
 
 // ---------------------------------------------------------------------------
 // rows of a ragged call: sequence i has rows starts[i] .. starts[i+1]-1, or
-// each * i .. each * (i + 1) - 1 where starts is null
+// base + each * i .. base + each * (i + 1) - 1 where starts is null
 // ---------------------------------------------------------------------------
 struct KvRows {
     const int32_t* starts;
-    int each, n, rows;
-    __device__ __forceinline__ int at(int i) const { return starts ? __ldg(starts + i) : each * i; }
+    int each, n, rows, base = 0;
+    __device__ __forceinline__ int at(int i) const { return starts ? __ldg(starts + i) : base + each * i; }
 };
 
 // The last i in [0, n) with f(i) <= x, for a function that never falls; -1 where

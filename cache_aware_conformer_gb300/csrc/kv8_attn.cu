@@ -1,78 +1,712 @@
-// Attention over the paged 8-bit K/V cache (include/cac_kv8.h).
+// Attention over the paged 8-bit K/V cache (include/cac_kv8.h) for calls with few
+// query rows to a K/V head: single tokens and short pushes.
 //
-//   t_j = scale log2(e) ks_b (q . kc_j)     kc: codes of the token, ks_b: scale of its block
-//   out = sum_j 2^(t_j - m) vs_b vc_j / sum_j 2^(t_j - m),   m = max_j t_j
+//   t_j = scale log2(e) ks_b (q . kc_j)      kc, vc: codes of token j; ks_b, vs_b: scales of its block of 16
+//   w_j = 2^(t_j + log2(vs_b) - m),  m the running maximum of t_j + log2(vs_b)
+//   out = sum_j w_j vc_j / sum_j w_j / vs_b
+//
+// With the value scale inside the exponent, the codes enter both products as they
+// are (whole numbers or e4m3 values, exact in fp16), no product of a weight and a
+// scale can leave the range of fp16, and the scales cost one multiply and one add per
+// block.  Queries enter as fp16 after a power of two that brings the row's largest
+// value under 2^15: a bf16 query is exact but for elements 2^29 smaller than the
+// row's largest; an fp32 query enters as hi + lo.  Weights are rounded to fp16 (11 bits, against
+// the 8 of a bf16 result) or, for fp32 results, enter as hi + lo.  Maxima, sums and
+// accumulators are fp32.
+//
+// The work is one pass over the cache's bytes, so memory bounds it.  A unit is (sequence, K/V head, 16 query rows); its tiles are the
+// 16-token blocks that any of its rows sees.  All tiles of the call, in order, are
+// dealt out evenly to the warps of one block per SM, wherever that cuts a
+// sequence; a warp that holds all of a unit writes its rows, the others leave partial
+// sums that kv_join_kernel adds up in order.  So one sequence of 120,000 tokens and
+// 64 of unlike lengths both keep every SM busy to the end, and the result does not
+// depend on timing.
+//
+// Each warp streams its tiles through a ring of its own in shared memory with
+// 16-byte asynchronous copies, several tiles ahead of the mathematics, across
+// the borders of units: there is no barrier between warps and nothing to wait for
+// but its own copies.
 #include <algorithm>
+#include <atomic>
 
 #include "kv8.cuh"
 
 namespace cac {
 namespace {
 
-constexpr int SA_WARPS = 4;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LIFT = 15.f;     // weights are held times 2^15: the largest is then 32,768, and fp16 keeps 11 bits of every
+                                 // weight down to 2^-29 of it (a small weight may meet a large value)
+constexpr int TA_WARPS = 8;      // warps of a block where tiles are dealt out
+constexpr int TU_WARPS = 4;      // ... and where a warp takes a unit
+constexpr int TA_SEQS = 512;     // sequences of one launch
 
-// One block per (row, head); its warps take the tokens in turn, a lane eight of
-// the head's values at most.
-template <class T, int CODE> __global__ void __launch_bounds__(SA_WARPS * 32)
-    kv_attend_simple_kernel(const __grid_constant__ KvAttend a) {
-    __shared__ float sm[SA_WARPS], sl[SA_WARPS], so[SA_WARPS][256];
-    pdl_trigger();
-    pdl_wait();
-    const cac_kv8& c = a.c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x, head = blockIdx.y;
-    const int i = warp_last_le(a.rows.n, row, [&](int s) { return (long long)a.rows.at(s); });
-    if (i < 0 || row >= a.rows.at(i + 1)) return;
-    const int m = a.rows.at(i + 1) - a.rows.at(i), id = a.ids[i], D = c.head_dim;
-    const bool fits = id >= 0 && id < c.max_seqs && m <= a.max_new;
-    if (!fits && threadIdx.x == 0) latch_error(c.status, CAC_E_BOUNDS);
-    const int len = fits ? c.lens[id] : 0, pos = len - m + (row - a.rows.at(i));
-    const T* q = static_cast<const T*>(a.q) + row * a.q_stride + (long long)head * D;
-    float qf[8], o[8] = {}, mx = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) qf[k] = lane + 32 * k < D ? to_f(q[lane + 32 * k]) * a.scale * 1.4426950408889634f : 0.f;
-    const int kvh = head / a.group;
-    if (pos >= 0 && len > 0) {
-        const int low = a.win.low(pos), high = a.win.high(pos, len), sink = min(a.win.sinks, low);
-        for (int t = warp; t < sink + high - low; t += SA_WARPS) {
-            const int j = t < sink ? t : low + t - sink;
-            const int page = c.table[(long long)id * c.max_pages + j / c.page_tokens];
-            if (page < 0) continue;
-            const int in_page = j % c.page_tokens;
-            const long long at = kv_head_at(c, a.layer, page, kvh) + (long long)in_page * D;
-            const long long sc = kv_scale_at(c, a.layer, page, kvh) + in_page / KV_BLOCK;
-            const uint8_t *kc = static_cast<const uint8_t*>(c.k) + at, *vc = static_cast<const uint8_t*>(c.v) + at;
-            float s = 0.f;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (lane + 32 * k < D) s += qf[k] * kv_decode<CODE>(kc[lane + 32 * k]);
-#pragma unroll
-            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-            s *= c.k_scale[sc];
-            const float now = fmaxf(mx, s), f = exp2f(mx - now), p = exp2f(s - now), pv = p * c.v_scale[sc];
-            l = l * f + p;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (lane + 32 * k < D) o[k] = o[k] * f + pv * kv_decode<CODE>(vc[lane + 32 * k]);
-            mx = now;
+// ---------------------------------------------------------------------------
+// codes to fp16: the four bytes of a word as two pairs, scaled by 2^-8 for e4m3
+// (its bits, moved into place, are fp16 bits with the smaller bias; subnormals and
+// the NaN code included, so that nothing a page may hold turns into a NaN)
+// ---------------------------------------------------------------------------
+template <int CODE> __device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (CODE == CAC_KV8_INT8) {
+        w ^= 0x80808080u;  // u = code + 128; 0x6400 | u is 1024 + u
+        uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));  // - 1152
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+    } else {
+        const uint32_t top = ((w & 0x7f7f7f7fu) >> 1 & 0x7f7f7f7fu) | (w & 0x80808080u);
+        const uint32_t low = (w << 7) & 0x80808080u;
+        lo = __byte_perm(low, top, 0x5140);
+        hi = __byte_perm(low, top, 0x7362);
+    }
+}
+template <int CODE> __device__ __forceinline__ constexpr float code_unit() { return CODE == CAC_KV8_INT8 ? 1.f : 256.f; }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// what the rounding in pack_half left over, rounded
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return pack_half(a - f.x, b - f.y);
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Where chunk c (16 bytes) of token row r of a tile lies: every quarter-warp of the
+// fragment reads below touches all 32 banks once.
+template <int HDP> __device__ __forceinline__ int tile_at(int r, int c) {
+    if constexpr (HDP == 64) return ((r & ~1) | ((r ^ (r >> 2)) & 1)) * 64 + ((c ^ (r & 2)) << 4);
+    return r * HDP + ((c ^ (r & 7)) << 4);
+}
+
+// What a sequence of the call asks for.
+struct SeqWork {
+    int id, len, m, row0;      // len 0: nothing is seen
+    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1)
+};
+__device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
+    SeqWork s;
+    s.row0 = a.rows.at(i);
+    s.m = a.rows.at(i + 1) - s.row0;
+    s.id = a.ids[i];
+    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1;
+    const bool rows_ok = s.m >= 0 && s.row0 >= 0 && s.row0 + (long long)s.m <= a.rows.rows;
+    if (!rows_ok) s.m = 0;
+    if (s.id >= 0 && s.id < a.c.max_seqs && s.m <= a.max_new && rows_ok) {
+        s.len = a.c.lens[s.id];
+    } else {
+        latch_error(a.c.status, CAC_E_BOUNDS);
+    }
+    if (s.len > 0 && s.m > 0) {
+        const int low = a.win.low(max(s.len - s.m, 0)), high = a.win.high(s.len - 1, s.len);
+        s.lot = low / KV_BLOCK;
+        s.skt = min((min(a.win.sinks, high) + KV_BLOCK - 1) / KV_BLOCK, s.lot);
+        s.tiles = s.skt + (high + KV_BLOCK - 1) / KV_BLOCK - s.lot;
+    }
+    return s;
+}
+
+struct Tile {
+    long long at;              // its codes (K and V alike), -1: nothing there
+    float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale, all for codes as half4 gives them
+    int j0;                    // its first token
+};
+template <int CODE>
+__device__ __forceinline__ Tile tile_of(const KvAttend& a, int id, int len, int lot, int skt, int kt, int head) {
+    Tile t{-1, 0.f, 0.f, 0.f, 0};
+    t.j0 = (kt < skt ? kt : lot + kt - skt) * KV_BLOCK;
+    if (t.j0 < len) {
+        const int page = a.c.table[(long long)id * a.c.max_pages + t.j0 / a.c.page_tokens];
+        if (page >= 0) {
+            const int in_page = t.j0 % a.c.page_tokens;
+            const long long sc = kv_scale_at(a.c, a.layer, page, head) + in_page / KV_BLOCK;
+            t.at = kv_head_at(a.c, a.layer, page, head) + (long long)in_page * a.c.head_dim;
+            t.ks = a.c.k_scale[sc] * code_unit<CODE>();
+            t.lv = log2f(a.c.v_scale[sc]) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
+            t.iv = ex2(-t.lv);  // of the rounded logarithm, so that weight and norm have the same factor
         }
     }
-    if (lane == 0) sm[warp] = mx, sl[warp] = l;
+    return t;
+}
+__device__ __forceinline__ Tile tile_from(const Tile& t, int lane) {
+    Tile r;
+    r.at = __shfl_sync(0xffffffffu, t.at, lane);
+    r.ks = __shfl_sync(0xffffffffu, t.ks, lane);
+    r.lv = __shfl_sync(0xffffffffu, t.lv, lane);
+    r.iv = __shfl_sync(0xffffffffu, t.iv, lane);
+    r.j0 = __shfl_sync(0xffffffffu, t.j0, lane);
+    return r;
+}
+
+// Sixteen query rows and their running sums, spread over a warp as the tensor core's
+// fragments: a thread has rows g and g + 8 (g = lane / 4, t = lane % 4).
+template <class T, int CODE, int HDP> struct Rows {
+    static constexpr bool WIDE = sizeof(T) == 4;          // hi + lo
+    static constexpr int STEPS = HDP / 16, NT = HDP / 8;
+    uint32_t q[STEPS][4], ql[WIDE ? STEPS : 1][4];
+    float o[NT][4];
+    float m[2], l[2], f[2];                               // maximum, sum, score factor of rows g, g + 8
+    int low[2], high[2];
+    int lo_max, hi_min, lo_min, hi_max;                   // over the rows
+
+    // Queries of K/V head `head`, rows r0 .. r0 + 15 of the sequence's m * group.
+    // Contraction step s = 4 j + x, thread t: elements 64 j + 16 t + 4 x + {0, 1} and + {2, 3}.
+    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim, R = s.m * a.group;
+        // rows in order of their positions: the first and last bound the windows
+        const int p0 = s.len - s.m + r0 / a.group, p1 = s.len - s.m + (min(r0 + 16, R) - 1) / a.group;
+        const bool any = s.len > 0 && p1 >= 0;
+        hi_min = any && p0 >= 0 ? a.win.high(p0, s.len) : 0;
+        hi_max = any ? a.win.high(p1, s.len) : 0;
+        lo_max = any ? a.win.low(p1) : 0;
+        lo_min = any ? a.win.low(max(p0, 0)) : 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (lane + 32 * k < D) so[warp][lane + 32 * k] = o[k];
-    __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < SA_WARPS; ++w) top = fmaxf(top, sm[w]);
-    if (top == -INFINITY) top = 0.f;  // nothing seen
-    for (int w = 0; w < SA_WARPS; ++w) sum += sl[w] * exp2f(sm[w] - top);
-    T* out = static_cast<T*>(a.out) + row * a.out_stride + (long long)head * D;
-    for (int d = threadIdx.x; d < D; d += blockDim.x) {
-        float v = 0.f;
-        for (int w = 0; w < SA_WARPS; ++w) v += so[w][d] * exp2f(sm[w] - top);
-        out[d] = from_f<T>(sum != 0.f ? v / sum : 0.f);
+        for (int h = 0; h < 2; ++h) {
+            const int r = r0 + g + 8 * h, query = r / a.group, p = s.len - s.m + query;
+            const bool on = r < R;
+            m[h] = -INFINITY, l[h] = 0.f;
+            low[h] = on && p >= 0 ? a.win.low(p) : 0;
+            high[h] = on && p >= 0 && s.len > 0 ? a.win.high(p, s.len) : 0;
+            const T* src = static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
+                           (long long)(head * a.group + r - query * a.group) * D;
+            float x[STEPS][4];
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < HDP / 64; ++j) {
+                const int e = 64 * j + 16 * t;
+                if (on && e < D) {
+                    if constexpr (WIDE) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 v = *reinterpret_cast<const float4*>(src + e + 4 * k);
+                            x[4 * j + k][0] = v.x, x[4 * j + k][1] = v.y, x[4 * j + k][2] = v.z, x[4 * j + k][3] = v.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(src + e + 8 * k);
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) {
+                                x[4 * j + 2 * k + (b >> 1)][2 * (b & 1)] = __uint_as_float(w[b] << 16);
+                                x[4 * j + 2 * k + (b >> 1)][2 * (b & 1) + 1] = __uint_as_float(w[b] & 0xffff0000u);
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[4 * j + k][0] = x[4 * j + k][1] = x[4 * j + k][2] = x[4 * j + k][3] = 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[4 * j + (k >> 2)][k & 3]));
+            }
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^(14 - floor(log2 amax)), within the exponents that fp32 has
+            const int e = min(268 - (int)(__float_as_uint(amax) >> 23), 254);
+            const float up = __uint_as_float((uint32_t)e << 23);
+            f[h] = a.scale * LOG2E * __uint_as_float((uint32_t)max(254 - e, 1) << 23) * (e == 254 ? 0.5f : 1.f);
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k) {
+                q[k][h] = pack_half(x[k][0] * up, x[k][1] * up);
+                q[k][2 + h] = pack_half(x[k][2] * up, x[k][3] * up);
+                if constexpr (WIDE) {
+                    ql[k][h] = pack_rest(x[k][0] * up, x[k][1] * up, q[k][h]);
+                    ql[k][2 + h] = pack_rest(x[k][2] * up, x[k][3] * up, q[k][2 + h]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[(long long)row * a.heads + head] = (top + log2f(sum)) * 0.6931471805599453f;
+
+    // One tile of 16 tokens, codes at shared addresses k and v.  Column n of score tile i is token
+    // (n / 2) + 4 (2 i + n % 2), so that a thread's four weights of a row are tokens t, t + 4, t + 8, t + 12.
+    __device__ __forceinline__ void tile(const Tile& d, const uint8_t* k, const uint8_t* v, int sinks) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        if (d.j0 >= hi_max || (d.j0 + KV_BLOCK <= lo_min && d.j0 >= sinks)) return;
+        float s[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            const int r = (g >> 1) + 4 * (2 * i + (g & 1));
+#pragma unroll
+            for (int j = 0; j < HDP / 64; ++j) {
+                const uint4 w = *reinterpret_cast<const uint4*>(k + tile_at<HDP>(r, 4 * j + t));
+                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t b0, b1;
+                    half4<CODE>(ww[x], b0, b1);
+                    mma_f16(s[i], q[4 * j + x], b0, b1);
+                    if constexpr (WIDE) mma_f16(s[i], ql[4 * j + x], b0, b1);
+                }
+            }
+        }
+        const bool full = d.j0 + KV_BLOCK <= hi_min && (d.j0 >= lo_max || d.j0 + KV_BLOCK <= sinks);
+        float top[2];
+        uint32_t p[4], pl[4];
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float c = f[h] * d.ks;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float& x = s[i][2 * h + b];
+                    x = fmaf(x, c, d.lv);
+                    if (!full) {
+                        const int j = d.j0 + t + 4 * (2 * i + b);
+                        if (!(j < high[h] && (j >= low[h] || j < sinks))) x = -INFINITY;
+                    }
+                }
+            float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            top[h] = fmaxf(m[h], mx);
+            moved |= top[h] > m[h];
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float r = top[h] == -INFINITY ? 1.f : ex2(m[h] - top[h]);
+                m[h] = top[h];
+                l[h] *= r;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) o[n][2 * h] *= r, o[n][2 * h + 1] *= r;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float base = m[h] == -INFINITY ? 0.f : m[h] - LIFT;
+            float w[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[i][2 * h + b] - base);
+            l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), d.iv, l[h]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                p[2 * i + h] = pack_half(w[i][0], w[i][1]);
+                if constexpr (WIDE) pl[2 * i + h] = pack_rest(w[i][0], w[i][1], p[2 * i + h]);
+            }
+        }
+        // value columns: column n of output tile y is element first(n) + y (see `element`)
+        constexpr int PER = HDP == 64 ? 8 : 16;
+#pragma unroll
+        for (int z = 0; z < HDP / (8 * PER); ++z) {
+            const int c = HDP == 64 ? g >> 1 : (((g & 1) << 2) | (g >> 1)) + 8 * z;
+            uint32_t w[4][PER / 4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const uint8_t* at = v + tile_at<HDP>(t + 4 * y, c);
+                if constexpr (HDP == 64) {
+                    const uint2 u = *reinterpret_cast<const uint2*>(at + (g & 1) * 8);
+                    w[y][0] = u.x, w[y][1] = u.y;
+                } else {
+                    const uint4 u = *reinterpret_cast<const uint4*>(at);
+                    w[y][0] = u.x, w[y][1] = u.y, w[y][2] = u.z, w[y][3] = u.w;
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < PER / 4; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {  // elements 4 x + 2 y and 4 x + 2 y + 1 of four tokens
+                    const uint32_t sel = y ? 0x7362 : 0x5140;
+                    uint32_t a0, a1, b0, b1;
+                    half4<CODE>(__byte_perm(w[0][x], w[1][x], sel), a0, b0);
+                    half4<CODE>(__byte_perm(w[2][x], w[3][x], sel), a1, b1);
+                    const int n = z * PER + 4 * x + 2 * y;
+                    mma_f16(o[n], p, a0, a1);
+                    mma_f16(o[n + 1], p, b0, b1);
+                    if constexpr (WIDE) {
+                        mma_f16(o[n], pl, a0, a1);
+                        mma_f16(o[n + 1], pl, b0, b1);
+                    }
+                }
+        }
+    }
+    // first element of column n's run in piece z
+    static __device__ __forceinline__ int element(int n, int z) {
+        if constexpr (HDP == 64) return n * 8;
+        return (((n & 1) << 2) | (n >> 1)) * 16 + 128 * z;
+    }
+    static constexpr int RUN = HDP == 64 ? 8 : 16;
+
+    // the sums of a row's four threads
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+        }
+    }
+};
+
+// RUN consecutive results of a row
+template <class T, int RUN> __device__ __forceinline__ void store_run(T* dst, const float (&x)[RUN]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < RUN; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < RUN; k += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[k + 2 * b], x[k + 2 * b + 1]);
+                w[b] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// The call's split over warps: tile x of `total` belongs to the warp w with
+// begin(w) <= x < begin(w + 1).
+// A share has LEAST tiles at least: fewer cost more to join than they save.
+constexpr int LEAST = 4;
+struct Deal {
+    long long total;
+    int warps;
+    __device__ __forceinline__ Deal(long long tiles, int most)
+        : total(tiles), warps(tiles >= (long long)most * LEAST ? most : max((int)(tiles / LEAST), 1)) {}
+    __device__ __forceinline__ long long begin(int w) const { return w < warps ? total * w / warps : total; }
+    __device__ __forceinline__ int owner(long long x) const {
+        int w = (int)(x * warps / total);
+        while (begin(w) > x) --w;
+        while (begin(w + 1) <= x) ++w;
+        return w;
+    }
+};
+
+// Partial sums: slot 2 w holds the unit that warp w's share begins in, slot 2 w + 1
+// the one that its share ends in when that is another.
+struct Partials {
+    float *o, *ml;               // [slot][16][HDP], [slot][16][2]
+    long long* first;            // [TA_SEQS + 1] tiles before each sequence
+};
+template <int HDP> __host__ __device__ inline size_t partial_bytes(int warps) {
+    return (size_t)warps * 2 * 16 * (HDP + 2) * 4 + (TA_SEQS + 2) * 8;
+}
+template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, int warps) {
+    Partials p;
+    p.first = static_cast<long long*>(space);
+    p.o = reinterpret_cast<float*>(p.first + TA_SEQS + 2);
+    p.ml = p.o + (size_t)warps * 2 * 16 * HDP;
+    return p;
+}
+
+template <int HDP, bool SPLIT> struct Ring {
+    static constexpr int WARPS = SPLIT ? TA_WARPS : TU_WARPS;
+    static constexpr int STAGE = 2 * KV_BLOCK * HDP;
+    static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : HDP == 256 ? 3 : HDP == 128 ? 6 : 8;
+    static constexpr int BYTES = WARPS * STAGES * STAGE;
+};
+
+// SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
+// whole unit (short windows, where a unit has a handful of tiles): nothing has to be joined.
+template <class T, int CODE, int HDP, bool SPLIT>
+__global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
+    kv_attend_kernel(const __grid_constant__ KvAttend a, int row_tiles, void* space) {
+    using R = Rows<T, CODE, HDP>;
+    constexpr int STAGES = Ring<HDP, SPLIT>::STAGES, STAGE = Ring<HDP, SPLIT>::STAGE, CH = HDP / 16;
+    constexpr int WARPS = Ring<HDP, SPLIT>::WARPS;
+    extern __shared__ __align__(128) uint8_t ring_all[];
+    __shared__ long long s_first[SPLIT ? TA_SEQS + 1 : 1];
+    __shared__ long long s_part[WARPS];
+    __shared__ int s_tiles[SPLIT ? TA_SEQS : 1], s_lot[SPLIT ? TA_SEQS : 1], s_skt[SPLIT ? TA_SEQS : 1];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.rows.n, kvh = a.c.kv_heads;
+    uint8_t* ring = ring_all + warp * STAGES * STAGE;
+    const int D = a.c.head_dim;
+
+    long long x0 = 0, x1 = 0;   // this warp's share of the tiles
+    int i = 0, unit = 0;        // SPLIT = false: its unit
+    SeqWork s{};
+    if constexpr (SPLIT) {
+        // tiles before each sequence
+        long long before = 0;
+        for (int base = 0; base < n; base += WARPS * 32) {
+            const int k = base + threadIdx.x;
+            long long mine = 0;
+            if (k < n) {
+                const SeqWork w = seq_work(a, k);
+                s_tiles[k] = w.tiles, s_lot[k] = w.lot, s_skt[k] = w.skt;
+                mine = (long long)w.tiles * kvh * ((w.m * a.group + 15) / 16);
+            }
+            long long sum = mine;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const long long u = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += u;
+            }
+            if (lane == 31) s_part[warp] = sum;
+            __syncthreads();
+            long long add = before;
+            for (int w = 0; w < WARPS; ++w) {
+                if (w < warp) add += s_part[w];
+                before += s_part[w];
+            }
+            if (k < n) s_first[k] = add + sum - mine;
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) s_first[n] = before;
+        __syncthreads();
+        const int warps = gridDim.x * WARPS;
+        if (blockIdx.x == 0)
+            for (int k = threadIdx.x; k <= n; k += WARPS * 32) partials_at<HDP>(space, warps).first[k] = s_first[k];
+        const Deal deal(before, warps);
+        if (before == 0) return;
+        x0 = deal.begin(blockIdx.x * WARPS + warp), x1 = deal.begin(blockIdx.x * WARPS + warp + 1);
+    } else {
+        const long long u = (long long)blockIdx.x * WARPS + warp;
+        const int per = kvh * row_tiles;
+        i = (int)(u / per), unit = (int)(u - (long long)i * per);   // unit = row tile * kv_heads + head
+        if (i >= n) return;
+        s = seq_work(a, i);
+        if (unit / kvh * 16 >= s.m * a.group) return;
+        x1 = s.tiles;
+    }
+    if (x0 >= x1) return;
+
+    // Lane l knows tile base + l of the share (now) and the 32 after those (next).
+    auto look = [&](long long x) {
+        if (x >= x1) return Tile{-1, 0.f, 0.f, 0.f, 0};
+        if constexpr (SPLIT) {
+            int lo = 0, hi = n - 1;  // the last sequence with s_first <= x (empty ones have no tiles)
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (s_first[mid] <= x) lo = mid;
+                else hi = mid - 1;
+            }
+            const int id = a.ids[lo];
+            const bool ok = id >= 0 && id < a.c.max_seqs && a.rows.at(lo + 1) - a.rows.at(lo) <= a.max_new;
+            const long long in = x - s_first[lo];
+            const int u = (int)(in / s_tiles[lo]), kt = (int)(in - (long long)u * s_tiles[lo]);
+            return tile_of<CODE>(a, id, ok ? a.c.lens[id] : 0, s_lot[lo], s_skt[lo], kt, u % kvh);
+        } else {
+            return tile_of<CODE>(a, s.id, s.len, s.lot, s.skt, (int)x, unit % kvh);
+        }
+    };
+    Tile now = look(x0 + lane), next = look(x0 + 32 + lane);
+    long long base = x0;
+
+    auto fetch = [&](long long x) {  // queue the copies of tile x; always one group
+        const int k = (int)(x - base);
+        const long long at = __shfl_sync(0xffffffffu, k < 32 ? now.at : next.at, k & 31);
+        if (x < x1 && at >= 0) {
+            const uint32_t dst = smem_u32(ring + (int)((x - x0) % STAGES) * STAGE);
+            const uint8_t *ks = static_cast<const uint8_t*>(a.c.k) + at, *vs = static_cast<const uint8_t*>(a.c.v) + at;
+#pragma unroll
+            for (int e0 = 0; e0 < KV_BLOCK * CH; e0 += 32) {
+                const int e = e0 + lane, r = e / CH, c = e % CH;
+                if (c * 16 < D) {
+                    cp16(dst + tile_at<HDP>(r, c), ks + r * D + c * 16);
+                    cp16(dst + KV_BLOCK * HDP + tile_at<HDP>(r, c), vs + r * D + c * 16);
+                }
+            }
+        }
+        cp_commit();
+    };
+    if (D < HDP) {  // chunks past the head's width stay zero
+        for (int st = 0; st < STAGES; ++st)
+            for (int e = lane; e < 2 * KV_BLOCK * CH; e += 32) {
+                const int r = e / CH % KV_BLOCK, c = e % CH;
+                if (c * 16 >= D)
+                    *reinterpret_cast<uint4*>(ring + st * STAGE + e / (KV_BLOCK * CH) * (KV_BLOCK * HDP) +
+                                              tile_at<HDP>(r, c)) = make_uint4(0, 0, 0, 0);
+            }
+        __syncwarp();
+    }
+#pragma unroll 1
+    for (int k = 0; k < STAGES - 1; ++k) fetch(x0 + k);
+
+    R r;
+    long long x = x0;
+    while (x < x1) {
+        // the unit that tile x belongs to, and this warp's part of it
+        long long u0 = 0, u1 = x1;
+        if constexpr (SPLIT) {
+            i = warp_last_le(n, x, [&](int k) { return s_first[k]; });
+            s = seq_work(a, i);
+            unit = (int)((x - s_first[i]) / s.tiles);
+            u0 = s_first[i] + (long long)unit * s.tiles, u1 = u0 + s.tiles;
+        }
+        const long long end = min(u1, x1), from = x;
+        const int head = unit % kvh, r0 = unit / kvh * 16;
+        r.load(a, s, head, r0);
+        for (; x < end; ++x) {
+            if (x - base >= 32) {
+                base += 32;
+                now = next;
+                next = look(base + 32 + lane);
+            }
+            fetch(x + STAGES - 1);
+            cp_wait<STAGES - 1>();
+            __syncwarp();
+            const Tile d = tile_from(now, (int)(x - base));
+            const uint8_t* k = ring + (int)((x - x0) % STAGES) * STAGE;
+            if (d.at >= 0) r.tile(d, k, k + KV_BLOCK * HDP, a.win.sinks);
+            __syncwarp();  // the stage is read before its next copy is queued
+        }
+        r.finish();
+        const int g = lane >> 2, t = lane & 3;
+        const bool whole = from == u0 && end == u1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = r0 + g + 8 * h;
+            if (row >= s.m * a.group) continue;
+            const int query = row / a.group, qh = head * a.group + row - query * a.group;
+            const float inv = r.l[h] > 0.f || r.l[h] != r.l[h] ? 1.f / r.l[h] : 0.f;
+            const int slot = whole ? 0 : 2 * (blockIdx.x * WARPS + warp) + (from != x0);
+            const Partials part = partials_at<HDP>(space, gridDim.x * WARPS);
+#pragma unroll
+            for (int z = 0; z < HDP / (8 * R::RUN); ++z)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int e = R::element(2 * t + b, z);
+                    float y[R::RUN];
+#pragma unroll
+                    for (int k = 0; k < R::RUN; ++k) y[k] = r.o[z * R::RUN + k][2 * h + b];
+                    if (whole) {
+                        if (e >= D) continue;
+#pragma unroll
+                        for (int k = 0; k < R::RUN; ++k) y[k] *= inv;
+                        store_run<T, R::RUN>(static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride +
+                                                 (long long)qh * D + e, y);
+                    } else {
+                        store_run<float, R::RUN>(part.o + ((size_t)slot * 16 + g + 8 * h) * HDP + e, y);
+                    }
+                }
+            if (t == 0) {
+                if (whole) {
+                    if (a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] =
+                        r.l[h] > 0.f || r.l[h] != r.l[h] ? (r.m[h] - LIFT + log2f(r.l[h])) * LN2 : -INFINITY;
+                } else {
+                    part.ml[((size_t)slot * 16 + g + 8 * h) * 2] = r.m[h];
+                    part.ml[((size_t)slot * 16 + g + 8 * h) * 2 + 1] = r.l[h];
+                }
+            }
+        }
+        if constexpr (!SPLIT) {
+            // rows that a count above max_new adds: they see nothing, and are written as that
+            unit += kvh * row_tiles;
+            if (unit / kvh * 16 < s.m * a.group) x = 0;
+        }
+    }
+    cp_wait<0>();
+}
+
+// Adds up the parts of the units that were cut, in the order of the tiles.  Block (w - 1, row) looks at the border before
+// warp w's share and does the unit that it is the first to cut; a thread per element.
+template <class T, int HDP>
+__global__ void __launch_bounds__(HDP) kv_join_kernel(const __grid_constant__ KvAttend a, int warps, void* space) {
+    __shared__ float s_red[HDP / 32];
+    pdl_trigger();
+    pdl_wait();
+    const Partials part = partials_at<HDP>(space, warps);
+    const int kvh = a.c.kv_heads, n = a.rows.n, w0 = blockIdx.x;
+    const Deal deal(part.first[n], warps);
+    const long long cut = deal.begin(w0 + 1);
+    if (cut >= deal.total) return;
+    const int i = warp_last_le(n, cut, [&](int k) { return part.first[k]; });
+    const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0;
+    const long long first = part.first[i];
+    const int units = kvh * ((m * a.group + 15) / 16);
+    const long long tiles = (part.first[i + 1] - first) / units;
+    const int unit = (int)((cut - first) / tiles);
+    const long long u0 = first + unit * tiles;
+    if (u0 == cut || deal.begin(w0) > u0) return;
+    const int row = unit / kvh * 16 + blockIdx.y, head = unit % kvh;
+    if (row >= m * a.group) return;
+    const int w1 = deal.owner(u0 + tiles - 1), odd = deal.begin(w0) != u0;
+    auto slot = [&](int w) { return (size_t)(2 * w + (w == w0 ? odd : 0)) * 16 + blockIdx.y; };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float top = -INFINITY;
+    for (int w = w0 + threadIdx.x; w <= w1; w += HDP) top = fmaxf(top, part.ml[slot(w) * 2]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    if (lane == 0) s_red[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < HDP / 32; ++k) top = fmaxf(top, s_red[k]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float l = 0.f, o = 0.f;
+#pragma unroll 4
+    for (int w = w0; w <= w1; ++w) {
+        const float f = ex2(part.ml[slot(w) * 2] - base);
+        l = fmaf(part.ml[slot(w) * 2 + 1], f, l);
+        o = fmaf(part.o[slot(w) * HDP + threadIdx.x], f, o);
+    }
+    const bool seen = l > 0.f || l != l;
+    const int query = row / a.group, qh = head * a.group + row - query * a.group;
+    if ((int)threadIdx.x < a.c.head_dim)
+        static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + threadIdx.x] =
+            from_f<T>(seen ? o / l : 0.f);
+    if (threadIdx.x == 0 && a.lse)
+        a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return 0;
+    return sms;
+}
+
+template <class T, int CODE, int HDP>
+cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
+    const int smem = split ? Ring<HDP, true>::BYTES : Ring<HDP, false>::BYTES;
+    const auto kernel = split ? kv_attend_kernel<T, CODE, HDP, true> : kv_attend_kernel<T, CODE, HDP, false>;
+    static std::atomic<uint64_t> ready[2];  // devices on which the kernels may use their shared memory
+    const uint64_t bit = 1ull << (a.c.device & 63);
+    cudaError_t e = cudaSuccess;
+    if (!(ready[split].load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        ready[split].fetch_or(bit, std::memory_order_relaxed);
+    }
+    if (!split) {
+        const long long units = (long long)a.rows.n * a.c.kv_heads * row_tiles;
+        return launch_k(kernel, dim3((unsigned)((units + TU_WARPS - 1) / TU_WARPS)), dim3(TU_WARPS * 32), smem, s, 1, a,
+                        row_tiles, space);
+    }
+    e = launch_k(kernel, dim3(sms), dim3(TA_WARPS * 32), smem, s, 1, a, row_tiles, space);
+    if (e != cudaSuccess) return e;
+    return launch_k(kv_join_kernel<T, HDP>, dim3(sms * TA_WARPS - 1, std::min(16, a.max_new * a.group)), dim3(HDP), 0, s,
+                    1, a, sms * TA_WARPS, space);
+}
+template <class T, int CODE>
+cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
+    if (a.c.head_dim <= 64) return launch_attend<T, CODE, 64>(a, split, row_tiles, sms, space, s);
+    if (a.c.head_dim <= 128) return launch_attend<T, CODE, 128>(a, split, row_tiles, sms, space, s);
+    return launch_attend<T, CODE, 256>(a, split, row_tiles, sms, space, s);
+}
+
+// Whether units are cut: not where the window leaves at most SHORT tiles to any of them.
+constexpr int SHORT = 16;
+bool splits(const cac_kv8& c, int max_new, int left, int chunk, int sinks) {
+    long long tokens = (long long)c.max_pages * c.page_tokens;
+    if (left >= 0) tokens = std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);
+    return tokens > SHORT * KV_BLOCK;
 }
 
 }  // namespace
@@ -81,8 +715,12 @@ template <class T, int CODE> __global__ void __launch_bounds__(SA_WARPS * 32)
 using namespace cac;
 
 extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads) {
-    (void)c, (void)n, (void)rows, (void)max_new, (void)heads;
-    return 0;
+    (void)rows, (void)max_new, (void)heads;
+    if (kv_check_shape(c) != CAC_OK || n < 1) return 0;
+    DeviceScope dev(c->device);
+    const int warps = (dev.ok ? sm_count() : 0) * TA_WARPS;
+    return ((c->head_dim <= 64 ? partial_bytes<64>(warps) : c->head_dim <= 128 ? partial_bytes<128>(warps)
+                                                                                 : partial_bytes<256>(warps)) + 255) & ~(size_t)255;
 }
 
 extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
@@ -104,19 +742,31 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
         ((q_stride * size | out_stride * size) & 15) || (words & 3))
         return CAC_E_ALIGN;
+    const int group = heads / c->kv_heads, most = starts ? std::min(max_new, rows) : rows / n;
+    const bool split = splits(*c, most, att_left, att_chunk, sinks);
+    if (split && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
+                  workspace_bytes < cac_kv8_attend_workspace(c, n, rows, max_new, heads)))
+        return CAC_E_INVAL;
+    const long long tiles = ((long long)most * group + 15) / 16;
+    if (tiles == 0) return CAC_OK;
+    if (tiles * std::min(n, TA_SEQS) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    KvAttend a{*c, {starts, rows / n, n, rows}, {att_left, att_chunk, sinks}, ids, q, out, lse, q_stride, out_stride,
-               scale, layer, heads, heads / c->kv_heads, starts ? max_new : rows / n};
+    const int sms = sm_count();
+    if (sms < 1) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 g(rows, heads), b(SA_WARPS * 32);
-    cudaError_t e;
-    if (c->code == CAC_KV8_INT8)
-        e = dtype == CAC_DTYPE_BF16 ? launch_k(kv_attend_simple_kernel<bf16, CAC_KV8_INT8>, g, b, 0, s, 1, a)
-                                    : launch_k(kv_attend_simple_kernel<float, CAC_KV8_INT8>, g, b, 0, s, 1, a);
-    else
-        e = dtype == CAC_DTYPE_BF16 ? launch_k(kv_attend_simple_kernel<bf16, CAC_KV8_E4M3>, g, b, 0, s, 1, a)
-                                    : launch_k(kv_attend_simple_kernel<float, CAC_KV8_E4M3>, g, b, 0, s, 1, a);
-    (void)workspace, (void)workspace_bytes;
-    return e == cudaSuccess ? CAC_OK : CAC_E_CUDA;
+    for (int i0 = 0; i0 < n; i0 += TA_SEQS) {
+        const int each = rows / n, part = std::min(n - i0, TA_SEQS);
+        const KvAttend a{*c, {starts ? starts + i0 : nullptr, each, part, rows, each * i0}, {att_left, att_chunk, sinks},
+                         ids + i0, q, out, lse, q_stride, out_stride, scale, layer, heads, group, most};
+        cudaError_t e;
+        if (c->code == CAC_KV8_INT8)
+            e = dtype == CAC_DTYPE_BF16 ? launch_attend<bf16, CAC_KV8_INT8>(a, split, (int)tiles, sms, workspace, s)
+                                        : launch_attend<float, CAC_KV8_INT8>(a, split, (int)tiles, sms, workspace, s);
+        else
+            e = dtype == CAC_DTYPE_BF16 ? launch_attend<bf16, CAC_KV8_E4M3>(a, split, (int)tiles, sms, workspace, s)
+                                        : launch_attend<float, CAC_KV8_E4M3>(a, split, (int)tiles, sms, workspace, s);
+        if (e != cudaSuccess) return CAC_E_CUDA;
+    }
+    return CAC_OK;
 }
