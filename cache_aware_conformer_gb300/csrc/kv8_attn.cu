@@ -714,9 +714,12 @@ bool splits(const cac_kv8& c, int max_new, int left, int chunk, int sinks) {
 
 using namespace cac;
 
-extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads) {
-    (void)rows, (void)max_new, (void)heads;
-    if (kv_check_shape(c) != CAC_OK || n < 1) return 0;
+extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
+                                           int att_chunk, int sinks) {
+    (void)heads;
+    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 1 || att_chunk < 1 || sinks < 0 ||
+        !splits(*c, std::min(max_new, rows), att_left, att_chunk, sinks))
+        return 0;
     DeviceScope dev(c->device);
     const int warps = (dev.ok ? sm_count() : 0) * TA_WARPS;
     return ((c->head_dim <= 64 ? partial_bytes<64>(warps) : c->head_dim <= 128 ? partial_bytes<128>(warps)
@@ -745,7 +748,7 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     const int group = heads / c->kv_heads, most = starts ? std::min(max_new, rows) : rows / n;
     const bool split = splits(*c, most, att_left, att_chunk, sinks);
     if (split && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
-                  workspace_bytes < cac_kv8_attend_workspace(c, n, rows, max_new, heads)))
+                  workspace_bytes < cac_kv8_attend_workspace(c, n, rows, most, heads, att_left, att_chunk, sinks)))
         return CAC_E_INVAL;
     const long long tiles = ((long long)most * group + 15) / 16;
     if (tiles == 0) return CAC_OK;

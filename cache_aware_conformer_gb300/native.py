@@ -156,7 +156,7 @@ def _lib():
             "cac_kv8_read": (c_int, [vp, c_int, c_int, vp, vp, c_int, vp, vp, c_int, vp]),
             "cac_kv8_attend": (c_int, [vp, c_int, c_int, vp, vp, c_int, c_int, c_int, c_float, c_int, c_int, c_int, vp,
                                        c_longlong, vp, c_longlong, vp, c_int, vp, c_size_t, vp]),
-            "cac_kv8_attend_workspace": (c_size_t, [vp, c_int, c_int, c_int, c_int]),
+            "cac_kv8_attend_workspace": (c_size_t, [vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
             "cac_kv8_fork": (c_int, [vp, c_int, vp, vp, vp]),
             "cac_kv8_truncate": (c_int, [vp, c_int, vp, vp, c_int, vp]),
             "cac_kv8_trim": (c_int, [vp, c_int, vp, c_int, c_int, c_int, vp]),
@@ -758,6 +758,8 @@ class Kv8Cache:
         self._c = CacKv8(L, H, D, PT, P, cfg.max_seqs, cfg.max_pages, 0 if cfg.code == "int8" else 1,
                          self.device.index, 0)
         self._ref = ctypes.addressof(self._c)
+        self._current = torch._C._cuda_getCurrentRawStream
+        self._space = {}   # workspace bytes of the calls seen, by their sizes
         ints = int(_lib().cac_kv8_work_ints(self._ref))
         if ints == 0:
             raise ValueError(f"{cfg}: a shape outside what the kernels implement")
@@ -785,8 +787,15 @@ class Kv8Cache:
             raise ValueError("adopted tensors include table, lens, refs, free and n_free")
 
     def _on(self, stream):
+        return stream.cuda_stream if stream is not None else self._current(self._c.device)
+
+    def _empty(self, stream, *specs):
+        """Uninitialised tensors (shape, dtype) that belong to the stream that the call runs on."""
         import torch
-        return (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        if stream is None:
+            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
+        with torch.cuda.stream(stream):
+            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
 
     def _ints(self, t, n, what):
         import torch
@@ -837,9 +846,7 @@ class Kv8Cache:
         dtype = dtype or torch.float32
         if dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype: bfloat16 or float32")
-        with torch.cuda.stream(stream):  # the outputs belong to the stream that fills them
-            k, v = (torch.empty(n, count, self.cfg.kv_heads, self.cfg.head_dim, dtype=dtype, device=self.device)
-                    for _ in range(2))
+        k, v = self._empty(stream, *[((n, count, self.cfg.kv_heads, self.cfg.head_dim), dtype)] * 2)
         _check(_lib().cac_kv8_read(self._ref, layer, n, p, self._ints(first, n, "first"), count, k.data_ptr(),
                                    v.data_ptr(), 1 if dtype is torch.bfloat16 else 0, self._on(stream)),
                "cac_kv8_read")
@@ -853,16 +860,29 @@ class Kv8Cache:
         n, p, s = self._list(ids, starts)
         rows, heads = q.shape[0], q.shape[1]
         qs, dt = self._act(q, heads, "q")
-        if max_new is None:
+        if starts is None:
+            max_new = rows // n if n else 0
+        elif max_new is None:
             max_new = rows
         L = _lib()
-        need = int(L.cac_kv8_attend_workspace(self._ref, n, rows, max_new if s else (rows // n if n else 0), heads))
-        with torch.cuda.stream(stream):  # the outputs and the workspace belong to the stream that runs the call
-            if out is None:
-                out = torch.empty(rows, heads, self.cfg.head_dim, dtype=q.dtype, device=self.device)
-            sums = torch.empty(rows, heads, dtype=torch.float32, device=self.device) if lse else None
-            space = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
-        os_, _ = self._act(out, heads, "out", q)
+        key = (n, rows, max_new, heads, att_left, att_chunk, sinks)
+        need = self._space.get(key)
+        if need is None:
+            if len(self._space) >= 256:
+                self._space.clear()
+            need = self._space[key] = int(L.cac_kv8_attend_workspace(self._ref, *key))
+        specs = [(q.shape, q.dtype)] if out is None else []
+        if lse:
+            specs.append(((rows, heads), torch.float32))
+        if need:
+            specs.append(((need,), torch.uint8))
+        made = self._empty(stream, *specs)
+        space = made.pop() if need else None
+        sums = made.pop() if lse else None
+        if out is None:
+            out, os_ = made[0], heads * self.cfg.head_dim
+        else:
+            os_, _ = self._act(out, heads, "out", q)
         _check(L.cac_kv8_attend(self._ref, layer, n, p, s, rows, max_new, heads,
                                 scale if scale is not None else self.cfg.head_dim ** -0.5, att_left, att_chunk, sinks,
                                 q.data_ptr(), qs, out.data_ptr(), os_, _ptr(sums), dt, _ptr(space), need,

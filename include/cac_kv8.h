@@ -139,7 +139,8 @@ int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const
                    int max_new, int heads, float scale, int att_left, int att_chunk, int sinks, const void* q,
                    long long q_stride, void* out, long long out_stride, float* lse, int dtype, void* workspace,
                    size_t workspace_bytes, void* stream);
-size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads);
+size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
+                                int att_chunk, int sinks);
 
 /* Make sequence dst[i] a copy of src[i] (device int32 [n]) that shares its
  * pages; what dst[i] held is released.  A source may be forked several times.
