@@ -33,9 +33,10 @@ int kv_check_cache(const cac_kv8* c) {
     const uintptr_t words = reinterpret_cast<uintptr_t>(c->k_scale) | reinterpret_cast<uintptr_t>(c->v_scale) |
                             reinterpret_cast<uintptr_t>(c->table) | reinterpret_cast<uintptr_t>(c->lens) |
                             reinterpret_cast<uintptr_t>(c->refs) | reinterpret_cast<uintptr_t>(c->free_list) |
-                            reinterpret_cast<uintptr_t>(c->n_free) | reinterpret_cast<uintptr_t>(c->pending) |
+                            reinterpret_cast<uintptr_t>(c->n_free) |
                             reinterpret_cast<uintptr_t>(c->work) | reinterpret_cast<uintptr_t>(c->status);
-    if (((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) || (words & 3))
+    if (((reinterpret_cast<uintptr_t>(c->k) | reinterpret_cast<uintptr_t>(c->v)) & 15) || (words & 3) ||
+        (reinterpret_cast<uintptr_t>(c->pending) & 7))
         return CAC_E_ALIGN;
     return CAC_OK;
 }
@@ -95,7 +96,7 @@ __global__ void kv_init_kernel(cac_kv8 c, long long work_ints) {
 struct Want {
     int id, len, count, have, fresh;  // pages it has, pages it needs past those
     int last;                         // a last page that is not full, or -1
-    bool copy;                        // ... which has to be copied first
+    bool shared, copy;                // ... that other tables name too; that has to be copied
 };
 
 __device__ __forceinline__ Want want_of(const cac_kv8& c, const KvRows& rows, const int32_t* ids, int i) {
@@ -106,21 +107,26 @@ __device__ __forceinline__ Want want_of(const cac_kv8& c, const KvRows& rows, co
     w.have = pages_of(w.len, c.page_tokens);
     w.fresh = pages_of(w.len + w.count, c.page_tokens) - w.have;
     w.last = -1;
-    w.copy = false;
-    if (w.count > 0 && w.len % c.page_tokens) w.last = c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens];
+    w.shared = w.copy = false;
+    if (w.count > 0 && w.len % c.page_tokens) {
+        w.last = c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens];
+        w.shared = w.last >= 0 && __ldcg(c.refs + w.last) > 1;
+    }
     return w;
 }
 
 __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, const KvRows rows, const int32_t* ids) {
-    __shared__ int error;
+    __shared__ int error, any_shared;
     __shared__ int s_place[PLAN_T], s_have[PLAN_T], s_fresh[PLAN_T], s_id[PLAN_T];
     pdl_trigger();
     pdl_wait();
     const KvWork work = kv_work(c);
     const int n = rows.n, tid = threadIdx.x;
     const long long most = (long long)c.max_pages * c.page_tokens;
-    if (tid == 0) error = 0, work.count[0] = 0;
+    const int n_free = *c.n_free;
+    if (tid == 0) error = 0, any_shared = 0;
     __syncthreads();
+    Want mine{};  // entry tid, which is all of them in a call of up to PLAN_T sequences
     for (int i = tid; i < n; i += PLAN_T) {
         const int id = ids[i];
         const long long count = (long long)rows.at(i + 1) - rows.at(i);
@@ -129,58 +135,63 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
             continue;
         }
         c.pending[2 * id + 1] = i;  // its place in this call; an id listed twice finds another place there
-        if (c.lens[id] + count > most) atomicCAS(&error, 0, CAC_E_LIMIT);
+        if (c.lens[id] + count > most) {
+            atomicCAS(&error, 0, CAC_E_LIMIT);
+            continue;
+        }
+        const Want w = want_of(c, rows, ids, i);
+        if (i == tid) mine = w;
+        if (w.count > 0 && w.len % c.page_tokens && w.last < 0) atomicCAS(&error, 0, CAC_E_STATE);
+        if (w.shared) any_shared = 1;
     }
+    auto want = [&](int i) { return i == tid ? mine : want_of(c, rows, ids, i); };
     __syncthreads();
-    if (!error) {
-        // pages that are not full: how many of this call's sequences end in each, and the last of those
+    int failed = error;
+    const bool count_shared = any_shared && !failed;
+    __syncthreads();
+    if (!failed)
         for (int i = tid; i < n; i += PLAN_T) {
-            if (c.pending[2 * ids[i] + 1] != i) atomicCAS(&error, 0, CAC_E_INVAL);
-            const Want w = want_of(c, rows, ids, i);
-            if (w.count > 0 && w.len % c.page_tokens && w.last < 0) atomicCAS(&error, 0, CAC_E_STATE);
-            if (w.last >= 0) {
+            const Want w = want(i);
+            if (c.pending[2 * w.id + 1] != i) atomicCAS(&error, 0, CAC_E_INVAL);
+            if (w.shared) {  // how many of this call's sequences end in the page, and the last of those
                 atomicAdd(work.named + w.last, 1);
                 atomicMax(work.keeper + w.last, i + 1);
             }
         }
-    }
     __syncthreads();
-    const bool counted = !error || error == CAC_E_INVAL || error == CAC_E_STATE;
+    failed = error;
     // A shared page stays with the last of this call's sequences that end in it when no other table names it; the
     // others (all of them, when one does) get a copy.  Neither depends on the order of the atomics.
     auto decide = [&](int i) {
-        Want w = want_of(c, rows, ids, i);
-        if (w.last >= 0)
+        Want w = want(i);
+        if (w.shared)
             w.copy = __ldcg(c.refs + w.last) > __ldcg(work.named + w.last) || __ldcg(work.keeper + w.last) != i + 1;
         return w;
     };
-    int pages = 0, copies = 0;
-    const int n_free = *c.n_free;
-    if (!error) {
-        long long sum = 0;
-        for (int base = 0; base < n; base += PLAN_T) {
-            Want w{};
-            if (base + tid < n) w = decide(base + tid);
-            Two total;
-            block_scan(Two{w.fresh, w.copy}, &total);
-            sum += (long long)total.a + total.b;
-            if (sum > n_free) break;  // the same for every thread
-        }
-        if (tid == 0 && sum > n_free) error = CAC_E_NOMEM;
-    }
-    __syncthreads();
-    const int failed = error;
-    for (int base = 0; base < n; base += PLAN_T) {
-        const int i = base + tid;
+    long long sum = 0;
+    Two total = {0, 0}, at = {0, 0};
+    for (int base = 0; !failed && base < n && sum <= n_free; base += PLAN_T) {
         Want w{};
-        if (i < n && !failed) w = decide(i);
-        Two total = {0, 0}, at = {0, 0};
-        if (!failed) at = block_scan(Two{w.fresh, w.copy}, &total);
+        if (base + tid < n) w = decide(base + tid);
+        at = block_scan(Two{w.fresh, w.copy}, &total);
+        sum += (long long)total.a + total.b;
+        if (base == 0) mine = w;
+    }
+    if (!failed && sum > n_free) failed = CAC_E_NOMEM;  // the same for every thread
+    int pages = 0, copies = 0;
+    for (int base = 0; !failed && base < n; base += PLAN_T) {
+        const int i = base + tid;
+        Want w = mine;
+        if (n > PLAN_T) {
+            w = Want{};
+            if (i < n) w = decide(i);
+            at = block_scan(Two{w.fresh, w.copy}, &total);
+        }
         // pages leave the end of the free list: first this chunk's copies, then its fresh pages
         const int top = n_free - pages - copies - 1;
         __syncthreads();
         s_fresh[tid] = 0;
-        if (i < n && !failed) {
+        if (i < n) {
             if (w.copy) {
                 const int to = c.free_list[top - at.b];
                 work.copy_from[copies + at.b] = w.last;
@@ -188,7 +199,17 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
                 c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens] = to;
                 c.refs[to] = 1;
             }
-            s_place[tid] = top - total.b - at.a, s_have[tid] = w.have, s_fresh[tid] = w.fresh, s_id[tid] = w.id;
+            const int place = top - total.b - at.a;
+            int32_t* row = c.table + (long long)w.id * c.max_pages + w.have;
+            if (w.fresh == 1) {
+                const int page = c.free_list[place];
+                row[0] = page;
+                c.refs[page] = 1;
+            } else {
+                s_place[tid] = place, s_have[tid] = w.have, s_fresh[tid] = w.fresh, s_id[tid] = w.id;
+            }
+            c.pending[2 * w.id] = w.count;
+            c.lens[w.id] = w.len + w.count;
         }
         __syncthreads();
         // a warp to a sequence, so that a long prompt's pages are entered 32 at a time
@@ -201,38 +222,32 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
         pages += total.a;
         copies += total.b;
     }
-    __syncthreads();
-    for (int k = tid; k < copies; k += PLAN_T) atomicSub(c.refs + work.copy_from[k], 1);
-    // lengths, and the counters back to zero
-    for (int i = tid; i < n; i += PLAN_T) {
-        const int id = ids[i];
-        if (id < 0 || id >= c.max_seqs) continue;
-        if (failed) {
-            if (counted) {
-                const Want w = want_of(c, rows, ids, i);
-                if (w.last >= 0) work.named[w.last] = 0, work.keeper[w.last] = 0;
-            }
-            c.pending[2 * id] = 0;
-            continue;
-        }
-        const int len = c.lens[id], count = rows.at(i + 1) - rows.at(i);
-        c.pending[2 * id] = count;
-        c.lens[id] = len + count;
+    if (failed) {
+        for (int i = tid; i < n; i += PLAN_T)
+            if (ids[i] >= 0 && ids[i] < c.max_seqs) c.pending[2 * ids[i]] = 0;
+        if (tid == 0) latch_error(c.status, failed);
+    } else {
+        __syncthreads();
+        for (int k = tid; k < copies; k += PLAN_T) atomicSub(c.refs + work.copy_from[k], 1);
     }
-    if (!failed)
-        for (int k = tid; k < copies; k += PLAN_T) work.named[work.copy_from[k]] = 0, work.keeper[work.copy_from[k]] = 0;
-    __syncthreads();
-    if (!failed)  // pages that were kept
-        for (int i = tid; i < n; i += PLAN_T) {
-            const int id = ids[i], count = c.pending[2 * id], len = c.lens[id] - count;
-            if (count > 0 && len % c.page_tokens) {
-                const int last = c.table[(long long)id * c.max_pages + len / c.page_tokens];
-                work.named[last] = 0, work.keeper[last] = 0;
-            }
-        }
     if (tid == 0) {
-        if (failed) latch_error(c.status, failed);
-        else *c.n_free = n_free - pages - copies, work.count[0] = copies;
+        work.count[0] = copies;
+        if (!failed) *c.n_free = n_free - pages - copies;
+    }
+    if (count_shared) {  // the counters back to zero; lengths are the new ones by now, so the entry's own place is asked
+        __syncthreads();
+        for (int i = tid; i < n; i += PLAN_T) {
+            int last = mine.last;
+            bool shared = mine.shared;
+            if (i != tid) {
+                const int id = ids[i], count = rows.at(i + 1) - rows.at(i), len = c.lens[id] - (failed ? 0 : count);
+                shared = count > 0 && len % c.page_tokens;
+                last = shared ? c.table[(long long)id * c.max_pages + len / c.page_tokens] : -1;
+                shared = shared && last >= 0;
+            }
+            if (shared) work.named[last] = 0, work.keeper[last] = 0;
+        }
+        for (int k = tid; k < copies; k += PLAN_T) work.named[work.copy_from[k]] = 0, work.keeper[work.copy_from[k]] = 0;
     }
 }
 
@@ -274,23 +289,32 @@ __global__ void __launch_bounds__(256) kv_copy_kernel(const cac_kv8 c) {
 // ---------------------------------------------------------------------------
 constexpr int WRITE_WARPS = 8;
 
-// eight consecutive values as floats
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const bf16* p, float (&x)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        x[2 * k] = __uint_as_float(w[k] << 16);
-        x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+// Eight consecutive values as they lie in memory, and as floats
+template <class T> struct Eight;
+template <> struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
     }
-}
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+};
+template <> struct Eight<bf16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const bf16* p) { a = __ldcs(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            x[2 * k] = __uint_as_float(w[k] << 16);
+            x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        }
+    }
+};
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
 __device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
     uint32_t w[4];
@@ -299,13 +323,26 @@ __device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
         w[k] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
 }
 
+// The codes of eight finite values with |x f| rounded no further than the largest code.  For whole numbers, adding 1.5 * 2^23
+// leaves the nearest one (ties to even) in the low byte: one addition where a conversion runs at a quarter of that rate.
 template <int CODE> __device__ __forceinline__ uint2 encode8(const float (&x)[8], float f) {
-    uint32_t w[2] = {0, 0};
+    uint32_t w[2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) w[k >> 2] |= kv_encode<CODE>(x[k] * f) << (8 * (k & 3));
+    for (int h = 0; h < 2; ++h) {
+        if constexpr (CODE == CAC_KV8_INT8) {
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = __float_as_uint(__fadd_rn(__fmul_rn(x[4 * h + k], f), 12582912.f));
+            w[h] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+        } else {
+            const uint32_t a = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h] * f, x[4 * h + 1] * f), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t b = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * h + 2] * f, x[4 * h + 3] * f), __NV_SATFINITE, __NV_E4M3);
+            w[h] = a | b << 16;
+        }
+    }
     return make_uint2(w[0], w[1]);
 }
 template <int CODE> __device__ __forceinline__ void decode8(uint2 w, float (&x)[8]) {
@@ -322,136 +359,214 @@ struct KvWrite {
     int layer, blocks;
 };
 
-// One warp per (block of 16 tokens, head, K or V); NIT = ceil(head_dim / 16)
-// passes of 32 lanes x 8 values cover the block.  Block number b of the call
-// belongs to the sequence i with first(i) = starts(i) / 16 + 2 i <= b < first(i + 1):
-// m new tokens touch at most (m + 30) / 16 blocks, and first(i + 1) - first(i) >=
-// m / 16 + 2, so no scan over the lengths is needed to deal the blocks out.
+// Where a block of the call lies: rows [lo, hi) of it are new, the first of them row `row` of k and v; nothing to do where
+// hi is 0.
+struct KvPlace {
+    int lo, hi, page, in_page;
+    long long row;
+};
+
+// Block number b of the call belongs to the sequence i with first(i) = starts(i) / 16 + 2 i <= b < first(i + 1): m new
+// tokens touch at most (m + 30) / 16 blocks, and first(i + 1) - first(i) >= m / 16 + 2, so no scan over the
+// lengths is needed to deal the blocks out.
+__device__ __forceinline__ KvPlace place_of(const KvWrite& a, int b) {
+    const cac_kv8& c = a.c;
+    KvPlace p{0, 0, -1, 0, 0};
+    const int i = warp_last_le(a.rows.n, b, [&](int s) { return a.rows.at(s) / KV_BLOCK + 2ll * s; });
+    if (i < 0) return p;
+    const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0, id = a.ids[i];
+    if (m == 0) return p;
+    int error = 0;
+    if (id < 0 || id >= c.max_seqs || row0 < 0 || m < 0 || row0 + (long long)m > a.rows.rows) {
+        error = CAC_E_BOUNDS;
+    } else {
+        const int2 pending = *reinterpret_cast<const int2*>(c.pending + 2 * id);
+        const int base = c.lens[id] - m;                                     // first new token
+        const int t0 = (base / KV_BLOCK + b - (row0 / KV_BLOCK + 2 * i)) * KV_BLOCK;  // first token of the block
+        if (pending.x != m || pending.y != i) {
+            error = CAC_E_STATE;
+        } else if (t0 < base + m) {
+            p.lo = max(base - t0, 0), p.hi = min(base + m - t0, KV_BLOCK);
+            p.page = c.table[(long long)id * c.max_pages + t0 / c.page_tokens];
+            p.in_page = t0 % c.page_tokens;
+            p.row = row0 + (long long)(t0 + p.lo - base);
+        }
+    }
+    if (error && (threadIdx.x & 31) == 0) latch_error(c.status, error);
+    return p;
+}
+
+// A warp takes a block of 16 tokens of a head at a time, BOTH: K and V of it, else one of them.  NIT = ceil(head_dim / 16)
+// passes of 32 lanes x 8 values cover the block; all of a task's loads are queued before the first is used, and the
+// next task's place is looked up (four dependent reads) while they are under way.
 template <class T, int CODE, int NIT>
-__global__ void __launch_bounds__(WRITE_WARPS * 32) kv_write_kernel(const __grid_constant__ KvWrite a) {
+__global__ void __launch_bounds__(WRITE_WARPS * 32, NIT <= 8 ? 2 : 1) kv_write_kernel(const __grid_constant__ KvWrite a) {
+    constexpr bool BOTH = NIT * sizeof(T) <= 16;
+    constexpr int KV = BOTH ? 2 : 1;
     pdl_trigger();
     pdl_wait();
     const cac_kv8& c = a.c;
-    const int lane = threadIdx.x & 31;
-    const long long u = (long long)blockIdx.x * WRITE_WARPS + (threadIdx.x >> 5);
-    const int per_block = 2 * c.kv_heads;
-    const int b = (int)(u / per_block);
-    if (b >= a.blocks) return;
-    const int head = (int)(u % per_block) >> 1, which = (int)(u & 1);
-    const int i = warp_last_le(a.rows.n, b, [&](int s) { return a.rows.at(s) / KV_BLOCK + 2ll * s; });
-    if (i < 0) return;
-    const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0, id = a.ids[i];
-    const int nth = b - (row0 / KV_BLOCK + 2 * i);
-    if (m == 0) return;
-    if (id < 0 || id >= c.max_seqs || row0 < 0 || m < 0 || row0 + (long long)m > a.rows.rows) {
-        if (lane == 0) latch_error(c.status, CAC_E_BOUNDS);
-        return;
-    }
-    if (c.pending[2 * id] != m || c.pending[2 * id + 1] != i) {
-        if (lane == 0) latch_error(c.status, CAC_E_STATE);
-        return;
-    }
-    const int base = c.lens[id] - m;                         // first new token
-    const int t0 = (base / KV_BLOCK + nth) * KV_BLOCK;       // first token of the block
-    const int lo = max(base - t0, 0), hi = min(base + m - t0, KV_BLOCK);  // new rows [lo, hi), older ones before lo
-    if (hi <= lo) return;
-    const int page = c.table[(long long)id * c.max_pages + t0 / c.page_tokens];
-    if (page < 0) return;  // trimmed before it was written: no query sees it
-    const int in_page = t0 % c.page_tokens;
-    const int D = c.head_dim, vec = D >> 3;
-    const T* src = static_cast<const T*>(which ? a.v : a.k) + (long long)head * D;
-    const long long stride = which ? a.v_stride : a.k_stride;
-    uint8_t* codes = static_cast<uint8_t*>(which ? c.v : c.k) + kv_head_at(c, a.layer, page, head) + in_page * D;
-    float* scale_at = (which ? c.v_scale : c.k_scale) + kv_scale_at(c, a.layer, page, head) + in_page / KV_BLOCK;
-
-    float x[NIT][8];
-    float amax = 0.f;
-    bool bad = false;
+    const int lane = threadIdx.x & 31, D = c.head_dim, vec = D >> 3, per_block = (3 - KV) * c.kv_heads;
+    const unsigned mul = (65536u + vec - 1) / vec;  // e / vec = e * mul >> 16 for e < 512, vec <= 32
+    const long long tasks = (long long)a.blocks * per_block, step = (long long)gridDim.x * WRITE_WARPS;
+    long long u = (long long)blockIdx.x * WRITE_WARPS + (threadIdx.x >> 5);
+    if (u >= tasks) return;
+    KvPlace p = place_of(a, (int)(u / per_block));
+    for (; u < tasks; u += step) {
+        const int part = (int)(u % per_block), head = part / (3 - KV);
+        const bool on = p.hi > p.lo && p.page >= 0;  // a page trimmed before it was written: no query sees it
+        const long long at = kv_head_at(c, a.layer, on ? p.page : 0, head) + p.in_page * D;
+        const long long sc = kv_scale_at(c, a.layer, on ? p.page : 0, head) + p.in_page / KV_BLOCK;
+        Eight<T> raw[KV][NIT];
+        float before[KV];
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-        const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
-        if (row >= lo && row < hi) {
-            load8(src + (row0 + (long long)(t0 + row - base)) * stride + col, x[it]);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float y = fabsf(x[it][k]);
-                if (y <= FLT_MAX) amax = fmaxf(amax, y);
-                else bad = true;
-            }
-        }
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
-    if (__any_sync(0xffffffffu, bad) && lane == 0) latch_error(c.status, CAC_E_NONFINITE);
-    float scale = fmaxf(amax * (1.f / kv_top<CODE>()), KV_MIN_SCALE);
-    if (lo > 0) {
-        const float before = *scale_at;
-        if (before >= scale) {
-            scale = before;
-        } else {  // the older codes at the larger scale
-            const float r = before / scale;
+        for (int w = 0; w < KV; ++w) {
+            const bool v = BOTH ? w : part & 1;
+            const long long stride = v ? a.v_stride : a.k_stride;
+            const T* src = static_cast<const T*>(v ? a.v : a.k) + p.row * stride + (long long)head * D;
 #pragma unroll
             for (int it = 0; it < NIT; ++it) {
-                const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
-                if (row < lo) {
-                    uint2* p = reinterpret_cast<uint2*>(codes + row * D + col);
-                    float y[8];
-                    decode8<CODE>(*p, y);
-                    *p = encode8<CODE>(y, r);
+                const int e = lane + 32 * it, row = (int)(e * mul >> 16), col = (e - row * vec) * 8;
+                if (on && row >= p.lo && row < p.hi) raw[w][it].load(src + (row - p.lo) * stride + col);
+            }
+            before[w] = on && p.lo > 0 ? (v ? c.v_scale : c.k_scale)[sc] : 0.f;
+        }
+        const KvPlace next = u + step < tasks ? place_of(a, (int)((u + step) / per_block)) : p;
+#pragma unroll
+        for (int w = 0; w < KV; ++w) {
+            const bool v = BOTH ? w : part & 1;
+            uint8_t* codes = static_cast<uint8_t*>(v ? c.v : c.k) + at;
+            float x[8];
+            uint32_t top = 0;
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+                const int row = (int)((lane + 32 * it) * mul >> 16);
+                if (on && row >= p.lo && row < p.hi) {
+                    raw[w][it].get(x);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
                 }
             }
-        }
-    }
-    const float inv = 1.f / scale;
+            top = __reduce_max_sync(0xffffffffu, top);
+            const bool bad = top >= 0x7f800000u;
+            if (bad) {  // the largest finite one instead
+                if (lane == 0) latch_error(c.status, CAC_E_NONFINITE);
+                top = 0;
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-        const int e = lane + 32 * it, row = e / vec, col = (e - row * vec) * 8;
-        if (row >= lo && row < hi) *reinterpret_cast<uint2*>(codes + row * D + col) = encode8<CODE>(x[it], inv);
+                for (int it = 0; it < NIT; ++it) {
+                    const int row = (int)((lane + 32 * it) * mul >> 16);
+                    if (on && row >= p.lo && row < p.hi) {
+                        raw[w][it].get(x);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t y = __float_as_uint(x[k]) & 0x7fffffffu;
+                            if (y < 0x7f800000u) top = max(top, y);
+                        }
+                    }
+                }
+                top = __reduce_max_sync(0xffffffffu, top);
+            }
+            float scale = fmaxf(__uint_as_float(top) * (1.f / kv_top<CODE>()), KV_MIN_SCALE);
+            if (before[w] >= scale) {
+                scale = before[w];
+            } else if (on && p.lo > 0) {  // the older codes at the larger scale
+                const float r = before[w] / scale;
+#pragma unroll 1
+                for (int e = lane; e < p.lo * vec; e += 32) {
+                    uint2* q = reinterpret_cast<uint2*>(codes + e * 8);
+                    decode8<CODE>(*q, x);
+                    *q = encode8<CODE>(x, r);
+                }
+            }
+            const float inv = 1.f / scale;
+#pragma unroll
+            for (int it = 0; it < NIT; ++it) {
+                const int e = lane + 32 * it, row = (int)(e * mul >> 16), col = (e - row * vec) * 8;
+                if (on && row >= p.lo && row < p.hi) {
+                    raw[w][it].get(x);
+                    if (bad) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            x[k] = x[k] != x[k] ? 0.f : fminf(fmaxf(x[k] * inv, -kv_top<CODE>()), kv_top<CODE>());
+                    }
+                    *reinterpret_cast<uint2*>(codes + row * D + col) = encode8<CODE>(x, bad ? 1.f : inv);
+                }
+            }
+            if (on && lane == 0) (v ? c.v_scale : c.k_scale)[sc] = scale;
+        }
+        p = next;
     }
-    __syncwarp();  // every lane has read the old scale
-    if (lane == 0) *scale_at = scale;
 }
 
 // ---------------------------------------------------------------------------
-// read: a thread takes eight values of a token's head
+// read: a warp takes READ_T tokens of a sequence, a lane 16 values at a time
 // ---------------------------------------------------------------------------
+constexpr int READ_T = 4;
 struct KvRead {
     cac_kv8 c;
     const int32_t *ids, *first;
     void *k, *v;
-    int layer, n, count;
+    int layer, n, count, pieces;
 };
 
 template <class T, int CODE> __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRead a) {
     pdl_trigger();
     pdl_wait();
     const cac_kv8& c = a.c;
-    const int vec = c.head_dim >> 3, per_token = c.kv_heads * vec;
-    const long long items = (long long)a.n * a.count * per_token;
-    for (long long e = blockIdx.x * 256ll + threadIdx.x; e < items; e += gridDim.x * 256ll) {
-        const long long token = e / per_token;
-        const int r = (int)(e - token * per_token), head = r / vec, col = (r - head * vec) * 8;
-        const int i = (int)(token / a.count), id = a.ids[i];
-        const long long t = (long long)a.first[i] + (token - (long long)i * a.count);
-        int page = -1;
-        if (id < 0 || id >= c.max_seqs) latch_error(c.status, CAC_E_BOUNDS);
-        else if (t >= 0 && t < c.lens[id]) page = c.table[(long long)id * c.max_pages + t / c.page_tokens];
-        const long long out = token * ((long long)c.kv_heads * c.head_dim) + head * c.head_dim + col;
-        const int in_page = page < 0 ? 0 : (int)(t % c.page_tokens);
-        const long long at = page < 0 ? 0 : kv_head_at(c, a.layer, page, head) + (long long)in_page * c.head_dim + col;
-        const long long sc = page < 0 ? 0 : kv_scale_at(c, a.layer, page, head) + in_page / KV_BLOCK;
-#pragma unroll
-        for (int which = 0; which < 2; ++which) {
-            T* dst = static_cast<T*>(which ? a.v : a.k);
-            if (!dst) continue;
-            float y[8] = {};
+    const int lane = threadIdx.x & 31, D = c.head_dim, vec = D >> 4, per = c.kv_heads * vec;
+    const long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int i = (int)(u / a.pieces), t0 = (int)(u - (long long)i * a.pieces) * READ_T;
+    if (i >= a.n) return;
+    const int id = a.ids[i], tokens = min(READ_T, a.count - t0);
+    long long at = -1, sc = 0;  // lane l: token l's first codes and scale
+    if (id < 0 || id >= c.max_seqs) {
+        if (lane == 0) latch_error(c.status, CAC_E_BOUNDS);
+    } else if (lane < tokens) {
+        const long long t = (long long)a.first[i] + t0 + lane;
+        if (t >= 0 && t < c.lens[id]) {
+            const int page = c.table[(long long)id * c.max_pages + t / c.page_tokens], in_page = (int)(t % c.page_tokens);
             if (page >= 0) {
-                decode8<CODE>(*reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(which ? c.v : c.k) + at), y);
-                const float f = (which ? c.v_scale : c.k_scale)[sc];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] *= f;
+                at = kv_head_at(c, a.layer, page, 0) + (long long)in_page * D;
+                sc = kv_scale_at(c, a.layer, page, 0) + in_page / KV_BLOCK;
             }
-            store8(dst + out, y);
+        }
+    }
+    const long long out0 = ((long long)i * a.count + t0) * c.kv_heads * D;
+    for (int e0 = 0; e0 < tokens * per; e0 += 64) {
+        uint4 w[2][2];
+        float f[2][2];
+        long long from[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int e = e0 + 32 * x + lane, t = e / per, r = e - t * per, head = r / vec;
+            const long long tat = __shfl_sync(0xffffffffu, at, t & 31), tsc = __shfl_sync(0xffffffffu, sc, t & 31);
+            from[x] = e < tokens * per ? tat : -1;
+            if (from[x] >= 0) {
+                const long long k = tat + (long long)head * c.page_tokens * D + (r - head * vec) * 16;
+                const long long s = tsc + head * (c.page_tokens / KV_BLOCK);
+                if (a.k) w[x][0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + k)), f[x][0] = c.k_scale[s];
+                if (a.v) w[x][1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + k)), f[x][1] = c.v_scale[s];
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int e = e0 + 32 * x + lane;
+            if (e >= tokens * per) continue;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                T* dst = static_cast<T*>(v ? a.v : a.k);
+                if (!dst) continue;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float y[8] = {};
+                    if (from[x] >= 0) {
+                        decode8<CODE>(h ? make_uint2(w[x][v].z, w[x][v].w) : make_uint2(w[x][v].x, w[x][v].y), y);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] *= f[x][v];
+                    }
+                    store8(dst + out0 + (long long)e * 16 + 8 * h, y);
+                }
+            }
         }
     }
 }
@@ -620,11 +735,16 @@ int check_list(const cac_kv8* c, int n, const void* ids) {
 
 constexpr int COPY_BLOCKS = 152 * 8;
 
-template <class T, int CODE> cudaError_t launch_write(const KvWrite& a, unsigned grid, cudaStream_t s) {
-    const dim3 g(grid), b(WRITE_WARPS * 32);
-    if (a.c.head_dim <= 64) return launch_k(kv_write_kernel<T, CODE, 4>, g, b, 0, s, 1, a);
-    if (a.c.head_dim <= 128) return launch_k(kv_write_kernel<T, CODE, 8>, g, b, 0, s, 1, a);
-    return launch_k(kv_write_kernel<T, CODE, 16>, g, b, 0, s, 1, a);
+template <class T, int CODE, int NIT> cudaError_t launch_write(const KvWrite& a, cudaStream_t s) {
+    const long long tasks = (long long)a.blocks * a.c.kv_heads * (NIT * sizeof(T) <= 16 ? 1 : 2);
+    // as many blocks as the SMs hold at once (2 of each), which then take further tasks in turn
+    const dim3 g((unsigned)std::min<long long>((tasks + WRITE_WARPS - 1) / WRITE_WARPS, 152 * 2)), b(WRITE_WARPS * 32);
+    return launch_k(kv_write_kernel<T, CODE, NIT>, g, b, 0, s, 1, a);
+}
+template <class T, int CODE> cudaError_t launch_write(const KvWrite& a, cudaStream_t s) {
+    if (a.c.head_dim <= 64) return launch_write<T, CODE, 4>(a, s);
+    if (a.c.head_dim <= 128) return launch_write<T, CODE, 8>(a, s);
+    return launch_write<T, CODE, 16>(a, s);
 }
 
 }  // namespace
@@ -679,17 +799,16 @@ extern "C" int cac_kv8_write(const cac_kv8* c, int layer, int n, const int32_t* 
         ((k_stride * size | v_stride * size) & 15) || (reinterpret_cast<uintptr_t>(starts) & 3))
         return CAC_E_ALIGN;
     const long long blocks = (long long)rows / KV_BLOCK + 2ll * n;
-    const long long grid = (blocks * 2 * c->kv_heads + WRITE_WARPS - 1) / WRITE_WARPS;
-    if (grid > INT32_MAX) return CAC_E_LIMIT;
+    if (blocks > INT32_MAX) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const KvWrite a{*c, {starts, rows / n, n, rows}, ids, k, v, k_stride, v_stride, layer, (int)blocks};
     if (c->code == CAC_KV8_INT8)
-        return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_INT8>(a, (unsigned)grid, s)
-                                                : launch_write<float, CAC_KV8_INT8>(a, (unsigned)grid, s));
-    return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_E4M3>(a, (unsigned)grid, s)
-                                            : launch_write<float, CAC_KV8_E4M3>(a, (unsigned)grid, s));
+        return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_INT8>(a, s)
+                                                : launch_write<float, CAC_KV8_INT8>(a, s));
+    return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_E4M3>(a, s)
+                                            : launch_write<float, CAC_KV8_E4M3>(a, s));
 }
 
 extern "C" int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* first, int count,
@@ -705,10 +824,12 @@ extern "C" int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* i
         return CAC_E_ALIGN;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    const long long items = (long long)n * count * c->kv_heads * (c->head_dim / 8);
-    const dim3 grid((unsigned)std::min<long long>((items + 255) / 256, 152 * 64)), block(256);
+    const int pieces = (count + READ_T - 1) / READ_T;
+    const long long blocks = ((long long)n * pieces + 7) / 8;
+    if (blocks > INT32_MAX) return CAC_E_LIMIT;
+    const dim3 grid((unsigned)blocks), block(256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const KvRead a{*c, ids, first, k, v, layer, n, count};
+    const KvRead a{*c, ids, first, k, v, layer, n, count, pieces};
     if (c->code == CAC_KV8_INT8)
         return launched(dtype == CAC_DTYPE_BF16
                             ? launch_k(kv_read_kernel<bf16, CAC_KV8_INT8>, grid, block, 0, s, 1, a)

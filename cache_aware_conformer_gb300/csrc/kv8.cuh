@@ -24,13 +24,6 @@ template <int CODE> __device__ __forceinline__ float kv_decode(uint32_t byte) {
     return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3)));
 }
 
-// nearest code, ties to even; x within (or rounded into) the largest code; NaN gives 0
-template <int CODE> __device__ __forceinline__ uint32_t kv_encode(float x) {
-    x = x != x ? 0.f : fminf(fmaxf(x, -kv_top<CODE>()), kv_top<CODE>());
-    if constexpr (CODE == CAC_KV8_INT8) return (uint32_t)(uint8_t)(int8_t)__float2int_rn(x);
-    return (uint32_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-}
-
 // ---------------------------------------------------------------------------
 // rows of a ragged call: sequence i has rows starts[i] .. starts[i+1]-1, or
 // base + each * i .. base + each * (i + 1) - 1 where starts is null

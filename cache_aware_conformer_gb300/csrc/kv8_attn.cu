@@ -37,8 +37,6 @@ namespace {
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float LIFT = 15.f;     // weights are held times 2^15: the largest is then 32,768, and fp16 keeps 11 bits of every
                                  // weight down to 2^-29 of it (a small weight may meet a large value)
-constexpr int TA_WARPS = 8;      // warps of a block where tiles are dealt out
-constexpr int TU_WARPS = 4;      // ... and where a warp takes a unit
 constexpr int TA_SEQS = 512;     // sequences of one launch
 
 // ---------------------------------------------------------------------------
@@ -396,38 +394,89 @@ struct Deal {
     }
 };
 
-// Partial sums: slot 2 w holds the unit that warp w's share begins in, slot 2 w + 1
-// the one that its share ends in when that is another.
+constexpr int MOST_WARPS = 12;   // of a block
+
+// Partial sums of units that were cut.  Slot 2 w: the unit that warp w's share begins in; slot 2 w + 1: the one that it ends in,
+// when that is another.  After the warps' slots the same for the blocks.
 struct Partials {
     float *o, *ml;               // [slot][16][HDP], [slot][16][2]
     long long* first;            // [TA_SEQS + 1] tiles before each sequence
+    int warps;
 };
-template <int HDP> __host__ __device__ inline size_t partial_bytes(int warps) {
-    return (size_t)warps * 2 * 16 * (HDP + 2) * 4 + (TA_SEQS + 2) * 8;
+template <int HDP> inline size_t partial_bytes(int sms) {
+    return (size_t)sms * (MOST_WARPS + 1) * 2 * 16 * (HDP + 2) * 4 + (TA_SEQS + 2) * 8;
 }
-template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, int warps) {
+template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, int blocks, int warps) {
     Partials p;
     p.first = static_cast<long long*>(space);
     p.o = reinterpret_cast<float*>(p.first + TA_SEQS + 2);
-    p.ml = p.o + (size_t)warps * 2 * 16 * HDP;
+    p.ml = p.o + (size_t)(blocks + warps) * 2 * 16 * HDP;
+    p.warps = warps;
     return p;
 }
 
-template <int HDP, bool SPLIT> struct Ring {
-    static constexpr int WARPS = SPLIT ? TA_WARPS : TU_WARPS;
+// A warp adds up the parts in slots `first`, then next, next + 2, ... (`more` of those), and writes the unit's rows, or, with to
+// >= 0, one part in that slot.
+template <class T, int HDP>
+__device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more, int to) {
+    constexpr int PER = HDP / 32;
+    const int lane = threadIdx.x & 31, kvh = a.c.kv_heads, head = unit % kvh, r0 = unit / kvh * 16;
+    const int rows = min(16, s.m * a.group - r0);
+    const int mine = lane == 0 ? first : next + 2 * (lane - 1);
+    for (int r = 0; r < rows; ++r) {
+        float m = -INFINITY, l = 0.f;
+        if (lane <= more) m = __ldcg(p.ml + ((size_t)mine * 16 + r) * 2), l = __ldcg(p.ml + ((size_t)mine * 16 + r) * 2 + 1);
+        float top = m;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float f = ex2(m - (top == -INFINITY ? 0.f : top));
+        l = lane <= more ? l * f : 0.f;
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        float o[PER] = {};
+#pragma unroll 4
+        for (int k = 0; k <= more; ++k) {
+            const size_t slot = k == 0 ? first : next + 2 * (k - 1);
+            const float* src = p.o + (slot * 16 + r) * HDP + lane * PER;
+            const float w = __shfl_sync(0xffffffffu, f, k);
+#pragma unroll
+            for (int c = 0; c < PER; ++c) o[c] = fmaf(__ldcg(src + c), w, o[c]);
+        }
+        if (to >= 0) {
+#pragma unroll
+            for (int c = 0; c < PER; ++c) p.o[((size_t)to * 16 + r) * HDP + lane * PER + c] = o[c];
+            if (lane == 0) p.ml[((size_t)to * 16 + r) * 2] = top, p.ml[((size_t)to * 16 + r) * 2 + 1] = l;
+        } else {
+            const int row = r0 + r, query = row / a.group, qh = head * a.group + row - query * a.group, D = a.c.head_dim;
+            const bool seen = l > 0.f || l != l;
+            T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
+#pragma unroll
+            for (int c = 0; c < PER; ++c)
+                if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[c] / l : 0.f);
+            if (lane == 0 && a.lse)
+                a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+        }
+    }
+}
+
+// Warps of a block, and the tiles that each has in flight or at hand (two matrices of 16 rows of HDP bytes).  The sums of 16 rows
+// take HDP / 2 registers and an fp32 query's two halves HDP / 2 more, which leaves room for 12 warps, or 8.
+template <class T, int HDP, bool SPLIT> struct Shape {
+    static constexpr int WARPS = !SPLIT ? 4 : HDP == 64 || (HDP == 128 && sizeof(T) == 2) ? 12 : 8;
     static constexpr int STAGE = 2 * KV_BLOCK * HDP;
-    static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : HDP == 256 ? 3 : HDP == 128 ? 6 : 8;
+    static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : 196608 / (WARPS * STAGE);
     static constexpr int BYTES = WARPS * STAGES * STAGE;
+    static constexpr int BLOCKS = !SPLIT && HDP == 64 ? 4 : 1;  // of an SM
 };
 
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
 // whole unit (short windows, where a unit has a handful of tiles): nothing has to be joined.
 template <class T, int CODE, int HDP, bool SPLIT>
-__global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
+__global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HDP, SPLIT>::BLOCKS))
     kv_attend_kernel(const __grid_constant__ KvAttend a, int row_tiles, void* space) {
     using R = Rows<T, CODE, HDP>;
-    constexpr int STAGES = Ring<HDP, SPLIT>::STAGES, STAGE = Ring<HDP, SPLIT>::STAGE, CH = HDP / 16;
-    constexpr int WARPS = Ring<HDP, SPLIT>::WARPS;
+    using S = Shape<T, HDP, SPLIT>;
+    constexpr int STAGES = S::STAGES, STAGE = S::STAGE, WARPS = S::WARPS, CH = HDP / 16;
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ long long s_first[SPLIT ? TA_SEQS + 1 : 1];
     __shared__ long long s_part[WARPS];
@@ -437,6 +486,8 @@ __global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.rows.n, kvh = a.c.kv_heads;
     uint8_t* ring = ring_all + warp * STAGES * STAGE;
     const int D = a.c.head_dim;
+
+    const Partials part = partials_at<HDP>(space, gridDim.x, gridDim.x * WARPS);
 
     long long x0 = 0, x1 = 0;   // this warp's share of the tiles
     int i = 0, unit = 0;        // SPLIT = false: its unit
@@ -472,7 +523,7 @@ __global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
         __syncthreads();
         const int warps = gridDim.x * WARPS;
         if (blockIdx.x == 0)
-            for (int k = threadIdx.x; k <= n; k += WARPS * 32) partials_at<HDP>(space, warps).first[k] = s_first[k];
+            for (int k = threadIdx.x; k <= n; k += WARPS * 32) part.first[k] = s_first[k];
         const Deal deal(before, warps);
         if (before == 0) return;
         x0 = deal.begin(blockIdx.x * WARPS + warp), x1 = deal.begin(blockIdx.x * WARPS + warp + 1);
@@ -485,7 +536,6 @@ __global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
         if (unit / kvh * 16 >= s.m * a.group) return;
         x1 = s.tiles;
     }
-    if (x0 >= x1) return;
 
     // Lane l knows tile base + l of the share (now) and the 32 after those (next).
     auto look = [&](long long x) {
@@ -576,8 +626,7 @@ __global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
             if (row >= s.m * a.group) continue;
             const int query = row / a.group, qh = head * a.group + row - query * a.group;
             const float inv = r.l[h] > 0.f || r.l[h] != r.l[h] ? 1.f / r.l[h] : 0.f;
-            const int slot = whole ? 0 : 2 * (blockIdx.x * WARPS + warp) + (from != x0);
-            const Partials part = partials_at<HDP>(space, gridDim.x * WARPS);
+            const int slot = 2 * (blockIdx.x * WARPS + warp) + (from != x0);
 #pragma unroll
             for (int z = 0; z < HDP / (8 * R::RUN); ++z)
 #pragma unroll
@@ -613,19 +662,45 @@ __global__ void __launch_bounds__(Ring<HDP, SPLIT>::WARPS * 32, 1)
         }
     }
     cp_wait<0>();
+    if constexpr (SPLIT) {
+        __syncthreads();  // the warps' parts are visible to the block
+        const Deal deal(s_first[n], gridDim.x * WARPS);
+        const int w = blockIdx.x * WARPS + warp;
+        const long long b0 = deal.begin(blockIdx.x * WARPS), b1 = deal.begin((blockIdx.x + 1) * WARPS);
+        // the unit that the share begins in, then the one that it ends in; the first warp of the block that holds a
+        // part of a cut unit adds the block's parts up
+#pragma unroll 1
+        for (int which = 0; which < 2 && x0 < x1; ++which) {
+            const long long at = which ? x1 - 1 : x0;
+            i = warp_last_le(n, at, [&](int k) { return s_first[k]; });
+            const long long u0 = s_first[i] + (at - s_first[i]) / s_tiles[i] * s_tiles[i], u1 = u0 + s_tiles[i];
+            if (which ? u0 <= x0 || u1 <= x1 : x0 != b0 && x0 != u0) continue;
+            if (u0 >= x0 && u1 <= x1) continue;  // whole, and written
+            int w1 = w;
+            while (w1 + 1 < (int)(blockIdx.x + 1) * WARPS && deal.begin(w1 + 1) < u1 && deal.begin(w1 + 1) < b1) ++w1;
+            s = seq_work(a, i);
+            unit = (int)((u0 - s_first[i]) / s_tiles[i]);
+            const bool done = u0 >= b0 && u1 <= b1;
+            const int to = 2 * part.warps + 2 * blockIdx.x + (u0 > b0);
+            join_warp<T, HDP>(a, part, s, unit, 2 * w + (which && u0 > x0), 2 * (w + 1), w1 - w, done ? -1 : to);
+        }
+    }
 }
 
-// Adds up the parts of the units that were cut, in the order of the tiles.  Block (w - 1, row) looks at the border before
-// warp w's share and does the unit that it is the first to cut; a thread per element.
+// Adds up the blocks' parts of the units that were cut between blocks, in the order of the tiles.  Block (b, row) looks at the
+// border after block b's share and does the unit that it is the first to cut; a thread per element, in JOIN_Y groups
+// that take the parts in turn.
+constexpr int JOIN_Y = 4;
 template <class T, int HDP>
-__global__ void __launch_bounds__(HDP) kv_join_kernel(const __grid_constant__ KvAttend a, int warps, void* space) {
-    __shared__ float s_red[HDP / 32];
+__global__ void __launch_bounds__(HDP * JOIN_Y)
+    kv_join_kernel(const __grid_constant__ KvAttend a, int blocks, int block_warps, void* space) {
+    __shared__ float s_o[JOIN_Y][HDP], s_l[JOIN_Y], s_m[JOIN_Y];
     pdl_trigger();
     pdl_wait();
-    const Partials part = partials_at<HDP>(space, warps);
-    const int kvh = a.c.kv_heads, n = a.rows.n, w0 = blockIdx.x;
-    const Deal deal(part.first[n], warps);
-    const long long cut = deal.begin(w0 + 1);
+    const Partials part = partials_at<HDP>(space, blocks, blocks * block_warps);
+    const int kvh = a.c.kv_heads, n = a.rows.n, b0 = blockIdx.x;
+    const Deal deal(part.first[n], part.warps);
+    const long long cut = deal.begin((b0 + 1) * block_warps);
     if (cut >= deal.total) return;
     const int i = warp_last_le(n, cut, [&](int k) { return part.first[k]; });
     const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0;
@@ -634,34 +709,38 @@ __global__ void __launch_bounds__(HDP) kv_join_kernel(const __grid_constant__ Kv
     const long long tiles = (part.first[i + 1] - first) / units;
     const int unit = (int)((cut - first) / tiles);
     const long long u0 = first + unit * tiles;
-    if (u0 == cut || deal.begin(w0) > u0) return;
+    if (u0 == cut || deal.begin(b0 * block_warps) > u0) return;
     const int row = unit / kvh * 16 + blockIdx.y, head = unit % kvh;
     if (row >= m * a.group) return;
-    const int w1 = deal.owner(u0 + tiles - 1), odd = deal.begin(w0) != u0;
-    auto slot = [&](int w) { return (size_t)(2 * w + (w == w0 ? odd : 0)) * 16 + blockIdx.y; };
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    float top = -INFINITY;
-    for (int w = w0 + threadIdx.x; w <= w1; w += HDP) top = fmaxf(top, part.ml[slot(w) * 2]);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    if (lane == 0) s_red[warp] = top;
+    const int b1 = deal.owner(u0 + tiles - 1) / block_warps, odd = deal.begin(b0 * block_warps) != u0;
+    auto slot = [&](int b) { return (size_t)(2 * part.warps + 2 * b + (b == b0 ? odd : 0)) * 16 + blockIdx.y; };
+    const int d = threadIdx.x, y = threadIdx.y;
+    float top = -INFINITY, l = 0.f, o = 0.f;
+    for (int b = b0 + y; b <= b1; b += JOIN_Y) top = fmaxf(top, __ldcg(part.ml + slot(b) * 2));
+    if (d == 0) s_m[y] = top;
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < HDP / 32; ++k) top = fmaxf(top, s_red[k]);
+    for (int k = 0; k < JOIN_Y; ++k) top = fmaxf(top, s_m[k]);
     const float base = top == -INFINITY ? 0.f : top;
-    float l = 0.f, o = 0.f;
 #pragma unroll 4
-    for (int w = w0; w <= w1; ++w) {
-        const float f = ex2(part.ml[slot(w) * 2] - base);
-        l = fmaf(part.ml[slot(w) * 2 + 1], f, l);
-        o = fmaf(part.o[slot(w) * HDP + threadIdx.x], f, o);
+    for (int b = b0 + y; b <= b1; b += JOIN_Y) {
+        const float f = ex2(__ldcg(part.ml + slot(b) * 2) - base);
+        l = fmaf(__ldcg(part.ml + slot(b) * 2 + 1), f, l);
+        o = fmaf(__ldcg(part.o + slot(b) * HDP + d), f, o);
     }
+    s_o[y][d] = o;
+    if (d == 0) s_l[y] = l;
+    __syncthreads();
+    if (y) return;
+    o = l = 0.f;
+#pragma unroll
+    for (int k = 0; k < JOIN_Y; ++k) o += s_o[k][d], l += s_l[k];
     const bool seen = l > 0.f || l != l;
     const int query = row / a.group, qh = head * a.group + row - query * a.group;
-    if ((int)threadIdx.x < a.c.head_dim)
-        static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + threadIdx.x] =
+    if (d < a.c.head_dim)
+        static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + d] =
             from_f<T>(seen ? o / l : 0.f);
-    if (threadIdx.x == 0 && a.lse)
+    if (d == 0 && a.lse)
         a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
 }
 
@@ -674,7 +753,9 @@ int sm_count() {
 
 template <class T, int CODE, int HDP>
 cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
-    const int smem = split ? Ring<HDP, true>::BYTES : Ring<HDP, false>::BYTES;
+    using S1 = Shape<T, HDP, true>;
+    using S0 = Shape<T, HDP, false>;
+    const int smem = split ? S1::BYTES : S0::BYTES;
     const auto kernel = split ? kv_attend_kernel<T, CODE, HDP, true> : kv_attend_kernel<T, CODE, HDP, false>;
     static std::atomic<uint64_t> ready[2];  // devices on which the kernels may use their shared memory
     const uint64_t bit = 1ull << (a.c.device & 63);
@@ -686,13 +767,13 @@ cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms,
     }
     if (!split) {
         const long long units = (long long)a.rows.n * a.c.kv_heads * row_tiles;
-        return launch_k(kernel, dim3((unsigned)((units + TU_WARPS - 1) / TU_WARPS)), dim3(TU_WARPS * 32), smem, s, 1, a,
+        return launch_k(kernel, dim3((unsigned)((units + S0::WARPS - 1) / S0::WARPS)), dim3(S0::WARPS * 32), smem, s, 1, a,
                         row_tiles, space);
     }
-    e = launch_k(kernel, dim3(sms), dim3(TA_WARPS * 32), smem, s, 1, a, row_tiles, space);
-    if (e != cudaSuccess) return e;
-    return launch_k(kv_join_kernel<T, HDP>, dim3(sms * TA_WARPS - 1, std::min(16, a.max_new * a.group)), dim3(HDP), 0, s,
-                    1, a, sms * TA_WARPS, space);
+    e = launch_k(kernel, dim3(sms), dim3(S1::WARPS * 32), smem, s, 1, a, row_tiles, space);
+    if (e != cudaSuccess || sms < 2) return e;
+    return launch_k(kv_join_kernel<T, HDP>, dim3(sms - 1, std::min(16, a.max_new * a.group)), dim3(HDP, JOIN_Y), 0, s, 1, a,
+                    sms, S1::WARPS, space);
 }
 template <class T, int CODE>
 cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
@@ -721,9 +802,8 @@ extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, in
         !splits(*c, std::min(max_new, rows), att_left, att_chunk, sinks))
         return 0;
     DeviceScope dev(c->device);
-    const int warps = (dev.ok ? sm_count() : 0) * TA_WARPS;
-    return ((c->head_dim <= 64 ? partial_bytes<64>(warps) : c->head_dim <= 128 ? partial_bytes<128>(warps)
-                                                                                 : partial_bytes<256>(warps)) + 255) & ~(size_t)255;
+    const int sms = dev.ok ? sm_count() : 0;
+    return c->head_dim <= 64 ? partial_bytes<64>(sms) : c->head_dim <= 128 ? partial_bytes<128>(sms) : partial_bytes<256>(sms);
 }
 
 extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,

@@ -74,7 +74,8 @@ typedef struct cac_kv8 {
     int32_t* refs;         /* [n_pages] tables that name the page */
     int32_t* free_list;    /* [n_pages]; the first *n_free entries are the free pages */
     int32_t* n_free;       /* [1] */
-    int32_t* pending;      /* [max_seqs][2] what the last extend made room for, and its place in that call */
+    int32_t* pending;      /* [max_seqs][2], 8-byte aligned: what the last extend made room for, and its place
+                              in that call */
     int32_t* work;         /* cac_kv8_work_ints ints, zero before the first call */
     int32_t* status;       /* [1] */
 } cac_kv8;
