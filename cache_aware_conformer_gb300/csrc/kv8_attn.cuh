@@ -1,0 +1,76 @@
+// What the attention kernels over the 8-bit cache share: the codes in fp16, and what a sequence of a call asks for.
+#pragma once
+
+#include "kv8.cuh"
+
+namespace cac {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------------------
+// codes to fp16: the four bytes of a word as two pairs, scaled by 2^-8 for e4m3
+// (its bits, moved into place, are fp16 bits with the smaller bias; subnormals and
+// the NaN code included, so that nothing a page may hold turns into a NaN)
+// ---------------------------------------------------------------------------
+template <int CODE> __device__ __forceinline__ void half4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if constexpr (CODE == CAC_KV8_INT8) {
+        w ^= 0x80808080u;  // u = code + 128; 0x6400 | u is 1024 + u
+        uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));  // - 1152
+        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
+    } else {
+        const uint32_t top = ((w & 0x7f7f7f7fu) >> 1 & 0x7f7f7f7fu) | (w & 0x80808080u);
+        const uint32_t low = (w << 7) & 0x80808080u;
+        lo = __byte_perm(low, top, 0x5140);
+        hi = __byte_perm(low, top, 0x7362);
+    }
+}
+template <int CODE> __device__ __forceinline__ constexpr float code_unit() { return CODE == CAC_KV8_INT8 ? 1.f : 256.f; }
+
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// what the rounding in pack_half left over, rounded
+__device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    return pack_half(a - f.x, b - f.y);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// What a sequence of the call asks for.
+struct SeqWork {
+    int id, len, m, row0;      // len 0: nothing is seen
+    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1)
+};
+__device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
+    SeqWork s;
+    s.row0 = a.rows.at(i);
+    s.m = a.rows.at(i + 1) - s.row0;
+    s.id = a.ids[i];
+    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1;
+    const bool rows_ok = s.m >= 0 && s.row0 >= 0 && s.row0 + (long long)s.m <= a.rows.rows;
+    if (!rows_ok) s.m = 0;
+    if (s.id >= 0 && s.id < a.c.max_seqs && s.m <= a.max_new && rows_ok) {
+        s.len = a.c.lens[s.id];
+    } else {
+        latch_error(a.c.status, CAC_E_BOUNDS);
+    }
+    if (s.len > 0 && s.m > 0) {
+        const int low = a.win.low(max(s.len - s.m, 0)), high = a.win.high(s.len - 1, s.len);
+        s.lot = low / KV_BLOCK;
+        s.skt = min((min(a.win.sinks, high) + KV_BLOCK - 1) / KV_BLOCK, s.lot);
+        s.tiles = s.skt + (high + KV_BLOCK - 1) / KV_BLOCK - s.lot;
+    }
+    return s;
+}
+
+// kv8_prompt.cu
+bool kv_prompt_takes(const KvAttend& a, int dtype);
+cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s);
+
+}  // namespace cac
