@@ -5,13 +5,14 @@
 // Arithmetic bounds it: 4 * head_dim operations a pair of query and token.  A block takes
 // NM tiles of 128 query rows (row = query * group + head of the group, so the heads that share K and V
 // share the tile too) of one sequence and K/V head, and walks over its 128-token tiles:
-//   converters  4 warps: 16-byte loads of codes, a tile ahead, turned into fp16 in the
-//               128-byte-swizzled layout that the tensor core reads (K as [token][element]: its rows are the
-//               columns of the scores; V the same way, read with the token as the
-//               contracted index), a ring of two tiles each
+//   converters  7 warps, 16 tokens of K or of V at a time in turn: 16-byte loads of codes, the next piece
+//               under way, turned into fp16 in the 128-byte-swizzled layout that the tensor core reads
+//               (K as [token][element]: its rows are the columns of the scores; V the same
+//               way, read with the token as the contracted index), a ring of two tiles each
 //   MMA         1 thread: S = Q K^T into TMEM, O += P V with P from TMEM
-//   softmax     4 warps for each row tile, a thread per row: scores from TMEM, maximum, weights
-//               back into TMEM in place of the scores, row sums
+//   softmax     4 warps for each row tile, a thread per row: the 128 scores from TMEM into registers, maximum, weights
+//               back into TMEM in place of the scores, row sums.  These threads take over registers
+//               of the others (setmaxnreg), so that the scores are read once.
 // With two row tiles the tensor core works on one while the softmax of the other runs.  A
 // row's sums are only rescaled when its maximum has grown by more than 2^SLACK since the last
 // time, which after the first tiles is hardly ever; until then weights may pass 1, and
@@ -33,7 +34,7 @@ constexpr int PT_ROWS = 128, PT_KEYS = 128;
 
 template <class T, int HDP> struct PShape {
     static constexpr bool WIDE = sizeof(T) == 4;             // queries and weights as hi + lo
-    static constexpr int NM = WIDE ? 1 : 2;                  // row tiles of a block
+    static constexpr int NM = WIDE && HDP == 128 ? 1 : 2;    // row tiles of a block: what shared memory and TMEM hold
     static constexpr int PARTS = WIDE ? 2 : 1;
     static constexpr int PANEL = 128 * 128;                  // 128 rows of 64 fp16
     static constexpr int TILE = HDP / 64 * PANEL;
@@ -41,11 +42,19 @@ template <class T, int HDP> struct PShape {
     static constexpr int OFF_BAR = OFF_SC + 4 * 24 * 4;      // [4 tiles][K scale, log2 and reciprocal of V scale][8]
     static constexpr int BYTES = OFF_BAR + 16 * 8 + 16 + 1024;
     static constexpr int SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;  // one block an SM
-    static constexpr int SOFT = NM * 4, WARPS = SOFT + 5, THREADS = WARPS * 32;
-    // TMEM columns: scores (128 each), sums (HDP each), fp32's low halves of the weights
+    static constexpr int SOFT = NM * 4, CONV = 7, WARPS = SOFT + CONV + 1, THREADS = WARPS * 32;
+    // registers: a launch gets 65,536 / THREADS each, in steps of 8 (128 of 512 threads, 168 of 384); the split may not pass that sum
+    static constexpr int LAUNCH = NM == 2 ? 128 : 168, R_SOFT = NM == 2 ? 200 : 232, R_REST = NM == 2 ? 56 : 136;
+    static_assert(SOFT * R_SOFT + (WARPS - SOFT) * R_REST <= WARPS * LAUNCH, "registers");
+    static_assert(WARPS * 32 * LAUNCH <= 65536 && WARPS % 4 == 0, "registers");
+    // TMEM columns: scores (128 each), sums (HDP each), fp32's low halves of the weights (64 each)
     static constexpr int COL_S = 0, COL_O = NM * 128, COL_L = COL_O + NM * HDP;
+    static_assert(COL_L + (WIDE ? NM * 64 : 0) <= 512, "TMEM");
     static constexpr float SLACK = WIDE ? 2.f : 8.f, LIFT = 15.f - SLACK;
 };
+
+template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // D[tmem] (+)= A[smem] B[smem], fp16 operands
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -74,6 +83,44 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
+}
+// 32 columns of the thread's lane, not yet there: tmem_arrived() makes them so
+__device__ __forceinline__ void tmem_ld32_start(uint32_t addr, float* v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
+}
+template <int N> __device__ __forceinline__ void tmem_arrived(float (&v)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int k = 0; k < N; k += 16)  // no use of them may move above the wait
+        asm volatile("" : "+f"(v[k]), "+f"(v[k + 1]), "+f"(v[k + 2]), "+f"(v[k + 3]), "+f"(v[k + 4]), "+f"(v[k + 5]),
+                          "+f"(v[k + 6]), "+f"(v[k + 7]), "+f"(v[k + 8]), "+f"(v[k + 9]), "+f"(v[k + 10]), "+f"(v[k + 11]),
+                          "+f"(v[k + 12]), "+f"(v[k + 13]), "+f"(v[k + 14]), "+f"(v[k + 15]));
+}
+// two at once
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -140,8 +187,8 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(q_full, nm * 128);
         for (int k = 0; k < 2; ++k) {
-            mbar_init(k_full + k, 128);
-            mbar_init(v_full + k, 128);
+            mbar_init(k_full + k, 8);
+            mbar_init(v_full + k, 8);
             mbar_init(k_empty + k, 1);
             mbar_init(v_empty + k, 1);
             mbar_init(s_full + k, 1);
@@ -159,6 +206,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     bool ok = true;
 
     if (warp < S::SOFT) {
+        take_registers<S::R_SOFT>();
         // -------------------------------------------------------------- softmax: a thread per row
         const int x = warp >> 2, r = (warp & 3) * 32 + lane, row = w.r0 + x * PT_ROWS + r;
         if (x < nm) {
@@ -172,21 +220,29 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             float f;
             {
                 const T* src = static_cast<const T*>(a.q) + (out0 + query) * a.q_stride + (long long)qh * D;
-                auto at = [&](int e) { return on && e < D ? to_f(src[e]) : 0.f; };
-                float amax = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < HDP; c += 8)
+                constexpr int VEC = 16 / sizeof(T);  // values of a 16-byte load
+                uint4 raw[HDP / VEC];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) amax = fmaxf(amax, fabsf(at(c + k)));
+                for (int c = 0; c < HDP / VEC; ++c)
+                    raw[c] = on && c * VEC < D ? *reinterpret_cast<const uint4*>(src + c * VEC) : make_uint4(0, 0, 0, 0);
+                auto value = [&](int e) {
+                    const uint4& q = raw[e / VEC];
+                    const int k = e % VEC, wd = S::WIDE ? k : k >> 1;
+                    const uint32_t u = wd == 0 ? q.x : wd == 1 ? q.y : wd == 2 ? q.z : q.w;
+                    return __uint_as_float(S::WIDE ? u : k & 1 ? u & 0xffff0000u : u << 16);
+                };
+                float amax = 0.f;
+#pragma unroll
+                for (int e = 0; e < HDP; ++e) amax = fmaxf(amax, fabsf(value(e)));
                 const int e = min(268 - (int)(__float_as_uint(amax) >> 23), 254);
                 const float up = __uint_as_float((uint32_t)e << 23) * (a.scale < 0.f ? -1.f : 1.f);
                 f = fabsf(a.scale) * LOG2E * __uint_as_float((uint32_t)max(254 - e, 1) << 23) * (e == 254 ? 0.5f : 1.f);
-#pragma unroll 2
+#pragma unroll
                 for (int c = 0; c < HDP / 8; ++c) {
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float y0 = at(8 * c + 2 * k) * up, y1 = at(8 * c + 2 * k + 1) * up;
+                        const float y0 = value(8 * c + 2 * k) * up, y1 = value(8 * c + 2 * k + 1) * up;
                         hi[k] = pack_half(y0, y1);
                         if constexpr (S::WIDE) lo[k] = pack_rest(y0, y1, hi[k]);
                     }
@@ -204,29 +260,28 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 const float* sc = s_scale + (j & 3) * 24;
                 if (!warp_wait(s_full + x, j & 1)) { ok = false; break; }
                 tc_fence_after();
-                const bool full = __all_sync(0xffffffffu, tok + PT_KEYS <= high && (tok >= low || tok + PT_KEYS <= a.win.sinks));
-                // a token that the row does not see scores -inf
-                auto hide = [&](float (&v)[32], int c) {
+                float v[PT_KEYS];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const int t = tok + c * 32 + k;
+                for (int c = 0; c < 4; ++c) tmem_ld32_start(col_s + c * 32, v + c * 32);
+                tmem_arrived(v);
+                // a token that the row does not see scores -inf
+                if (!__all_sync(0xffffffffu, tok + PT_KEYS <= high && (tok >= low || tok + PT_KEYS <= a.win.sinks))) {
+#pragma unroll
+                    for (int k = 0; k < PT_KEYS; ++k) {
+                        const int t = tok + k;
                         if (!(t < high && (t >= low || t < a.win.sinks))) v[k] = -INFINITY;
                     }
-                };
+                }
                 float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float v[32];
-                    tmem_ld32(col_s + c * 32, v);
-                    if (!full) hide(v, c);
+                for (int b = 0; b < 8; ++b) {
+                    float m0 = fmaxf(v[16 * b], v[16 * b + 1]), m1 = fmaxf(v[16 * b + 2], v[16 * b + 3]);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float mx = v[16 * b];
-#pragma unroll
-                        for (int k = 1; k < 16; ++k) mx = fmaxf(mx, v[16 * b + k]);
-                        // a hidden block stays -inf even where its scale is 0 (no page)
-                        if (mx != -INFINITY) top = fmaxf(top, fmaf(mx, f * sc[2 * c + b], sc[8 + 2 * c + b]));
+                    for (int k = 4; k < 16; k += 4) {
+                        m0 = fmaxf(fmaxf(m0, v[16 * b + k]), v[16 * b + k + 1]);
+                        m1 = fmaxf(fmaxf(m1, v[16 * b + k + 2]), v[16 * b + k + 3]);
                     }
+                    top = fmaxf(top, fmaf(fmaxf(m0, m1), f * sc[b], sc[8 + b]));
                 }
                 const bool grown = top > m + S::SLACK || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grown)) {
@@ -250,31 +305,25 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 const float base = m == -INFINITY ? -S::LIFT : m - S::LIFT;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    float v[32];
                     uint32_t hi[16], lo[16];
-                    tmem_ld32(col_s + c * 32, v);
-                    if (!full) hide(v, c);
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float ck = f * sc[2 * c + b], off = sc[8 + 2 * c + b] - base;
-                        float sum = 0.f;
+                    for (int b = 2 * c; b < 2 * c + 2; ++b) {
+                        const float ck = f * sc[b], off = sc[8 + b] - base;
+                        const float2 ck2 = make_float2(ck, ck), off2 = make_float2(off, off);
+                        float2 sum[2];
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            // (-inf) * 0 for a hidden token of a missing page is no number: max() makes it -inf again
-                            float y0 = fmaf(v[16 * b + k], ck, off), y1 = fmaf(v[16 * b + k + 1], ck, off);
-                            if (!full) {
-                                y0 = v[16 * b + k] == -INFINITY ? -INFINITY : y0;
-                                y1 = v[16 * b + k + 1] == -INFINITY ? -INFINITY : y1;
-                            }
-                            y0 = ex2(y0), y1 = ex2(y1);
-                            sum += y0 + y1;
-                            hi[8 * b + k / 2] = pack_half(y0, y1);
-                            if constexpr (S::WIDE) lo[8 * b + k / 2] = pack_rest(y0, y1, hi[8 * b + k / 2]);
+                        for (int k = 0; k < 8; ++k) {
+                            float2 y = fma2(make_float2(v[16 * b + 2 * k], v[16 * b + 2 * k + 1]), ck2, off2);
+                            y.x = ex2(y.x), y.y = ex2(y.y);
+                            sum[k & 1] = k < 2 ? y : add2(sum[k & 1], y);
+                            hi[8 * (b & 1) + k] = pack_half(y.x, y.y);
+                            if constexpr (S::WIDE) lo[8 * (b & 1) + k] = pack_rest(y.x, y.y, hi[8 * (b & 1) + k]);
                         }
-                        l = fmaf(sum, sc[16 + 2 * c + b], l);
+                        const float2 all = add2(sum[0], sum[1]);
+                        l = fmaf(all.x + all.y, sc[16 + b], l);
                     }
                     tmem_st16(col_s + c * 16, hi);
-                    if constexpr (S::WIDE) tmem_st16(tmem + lanes + S::COL_L + c * 16, lo);
+                    if constexpr (S::WIDE) tmem_st16(tmem + lanes + S::COL_L + x * 64 + c * 16, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -318,80 +367,72 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 if (on && a.lse) a.lse[(out0 + query) * a.heads + qh] = seen ? (m - S::LIFT + log2f(l)) * LN2 : -INFINITY;
             }
         }
-    } else if (warp < S::SOFT + 4) {
+    } else if (warp < S::SOFT + S::CONV) {
+        give_registers<S::R_REST>();
         // -------------------------------------------------------------- converters
-        const int cw = warp - S::SOFT;
-        struct Meta {
-            long long at;
-            float ks, lv, iv;
+        // piece n: 16 tokens (block n % 8) of tile n / 16, K where n / 8 is even, else V; warp cw takes every seventh
+        const int cw = warp - S::SOFT, pieces = w.tiles * 16;
+        const int sub = lane >> 2, c4 = lane & 3;   // token % 8 and chunk % 4 of a lane's loads
+        constexpr int NL = HDP / 32;
+        auto page_of = [&](int n) {  // -1: past the end, or released
+            const int tok = n < pieces ? w.token(n >> 4) + (n & 7) * KV_BLOCK : w.s.len;
+            return tok < w.s.len ? a.c.table[(long long)w.s.id * a.c.max_pages + tok / a.c.page_tokens] : -1;
         };
-        auto meta = [&](int j) {  // lane l < 8: block l of tile j
-            Meta t{-1, 0.f, -INFINITY, 0.f};
-            const int tok = j < w.tiles ? w.token(j) + (lane & 7) * KV_BLOCK : w.s.len;
-            if (tok < w.s.len) {
-                const int page = a.c.table[(long long)w.s.id * a.c.max_pages + tok / a.c.page_tokens];
-                if (page >= 0) {
-                    const int in_page = tok % a.c.page_tokens;
-                    const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
-                    t.at = kv_head_at(a.c, a.layer, page, w.head) + (long long)in_page * D;
-                    t.ks = a.c.k_scale[sc] * code_unit<CODE>();
-                    t.lv = log2f(a.c.v_scale[sc]) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
-                    t.iv = ex2(-t.lv);
-                }
+        auto load = [&](int n, int page, uint4 (&raw)[NL], float2& scale) {
+            const int in_page = (w.token(n >> 4) + (n & 7) * KV_BLOCK) % a.c.page_tokens;
+            const uint8_t* from = static_cast<const uint8_t*>(n & 8 ? a.c.v : a.c.k);
+            if (page >= 0) {
+                from += kv_head_at(a.c, a.layer, page, w.head) + (long long)(in_page + sub) * D + c4 * 16;
+                const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
+                if (!(n & 8)) scale = make_float2(a.c.k_scale[sc], a.c.v_scale[sc]);
             }
-            return t;
+#pragma unroll
+            for (int y = 0; y < NL; ++y)  // rows sub and sub + 8, elements of each 64
+                raw[y] = page >= 0 && ((y >> 1) * 4 + c4) * 16 < D
+                             ? *reinterpret_cast<const uint4*>(from + (y & 1) * 8 * D + (y >> 1) * 64)
+                             : make_uint4(0, 0, 0, 0);
         };
-        // this warp's 32 tokens of a tile, 8 at a time: lane = token % 8 * 4 + chunk % 4
-        const int sub = lane >> 2, c4 = lane & 3;
-        constexpr int NL = 4 * (HDP / 64);  // loads of a lane
-        auto load = [&](const void* from, long long at, uint4 (&raw)[NL]) {
+        int page = page_of(cw), page1 = page_of(cw + S::CONV);
+        uint4 raw[NL], next[NL];
+        float2 scale = make_float2(0.f, 0.f), scale1 = scale;
+        load(cw, page, raw, scale);
+#pragma unroll 1
+        for (int n = cw; n < pieces; n += S::CONV) {
+            const int page2 = page_of(n + 2 * S::CONV);
+            load(min(n + S::CONV, pieces - 1), n + S::CONV < pieces ? page1 : -1, next, scale1);
+            const int j = n >> 4, st = j & 1, block = n & 7;
+            const bool v = n & 8;
+            if (j >= 2 && !warp_wait((v ? v_empty : k_empty) + st, (j / 2 - 1) & 1)) { ok = false; break; }
+            uint8_t* to = smem + (v ? S::OFF_V : S::OFF_K) + st * S::TILE + (block * 16 + sub) * 128;
 #pragma unroll
             for (int y = 0; y < NL; ++y) {
-                const int g = y & 3, c = (y >> 2) * 4 + c4;
-                const long long block = __shfl_sync(0xffffffffu, at, cw * 2 + (g >> 1));
-                raw[y] = make_uint4(0, 0, 0, 0);
-                if (block >= 0 && c * 16 < D)
-                    raw[y] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(from) + block +
-                                                             (long long)((g & 1) * 8 + sub) * D + c * 16);
-            }
-        };
-        auto convert = [&](uint8_t* to, const uint4 (&raw)[NL]) {
-#pragma unroll
-            for (int y = 0; y < NL; ++y) {
-                const int row = cw * 32 + (y & 3) * 8 + sub;
                 const uint32_t u[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
-                uint32_t v[8];
+                uint32_t h[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) half4<CODE>(u[k], v[2 * k], v[2 * k + 1]);
-                uint8_t* dst = to + (y >> 2) * S::PANEL + row * 128;
-                *reinterpret_cast<uint4*>(dst + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(dst + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(v[4], v[5], v[6], v[7]);
+                for (int k = 0; k < 4; ++k) half4<CODE>(u[k], h[2 * k], h[2 * k + 1]);
+                uint8_t* dst = to + (y >> 1) * S::PANEL + (y & 1) * 1024;
+                *reinterpret_cast<uint4*>(dst + (((2 * c4) ^ sub) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(dst + (((2 * c4 + 1) ^ sub) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
-        };
-        Meta now = meta(0);
-        uint4 kr[NL], vr[NL];
-        load(a.c.k, now.at, kr);
-        load(a.c.v, now.at, vr);
-        for (int j = 0; j < w.tiles; ++j) {
-            const int st = j & 1;
-            const Meta next = meta(j + 1);
-            if (j >= 2 && !warp_wait(k_empty + st, (j / 2 - 1) & 1)) { ok = false; break; }
-            if (cw == 0 && lane < 8) {
-                float* sc = s_scale + (j & 3) * 24;
-                sc[lane] = now.ks, sc[8 + lane] = now.lv, sc[16 + lane] = now.iv;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (!v) {  // both scales with K: the scores need them.  A block without a page: weights of 2^-inf
+                    float* sc = s_scale + (j & 3) * 24 + block;
+                    const float lv = log2f(scale.y) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
+                    sc[0] = page >= 0 ? scale.x * code_unit<CODE>() : 1.f;
+                    sc[8] = page >= 0 ? lv : -INFINITY;
+                    sc[16] = page >= 0 ? ex2(-lv) : 0.f;
+                }
+                mbar_arrive((v ? v_full : k_full) + st);
             }
-            convert(smem + S::OFF_K + st * S::TILE, kr);
-            fence_proxy_async_smem();
-            mbar_arrive(k_full + st);
-            load(a.c.k, next.at, kr);
-            if (j >= 2 && !warp_wait(v_empty + st, (j / 2 - 1) & 1)) { ok = false; break; }
-            convert(smem + S::OFF_V + st * S::TILE, vr);
-            fence_proxy_async_smem();
-            mbar_arrive(v_full + st);
-            load(a.c.v, next.at, vr);
-            now = next;
+            page = page1, page1 = page2, scale = scale1;
+#pragma unroll
+            for (int y = 0; y < NL; ++y) raw[y] = next[y];
         }
-    } else if (lane == 0) {
+    } else {
+        give_registers<S::R_REST>();
+        if (lane == 0) {
         // -------------------------------------------------------------- MMA
         constexpr uint32_t qk = idesc_f16(128, 128, false), pv = idesc_f16(128, HDP, true);
         auto scores = [&](int x, int st) {
@@ -423,7 +464,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 for (int part = 0; part < S::PARTS; ++part)
 #pragma unroll
                     for (int k = 0; k < PT_KEYS / 16; ++k)
-                        mma_ts(tmem + S::COL_O + x * HDP, tmem + (part ? S::COL_L : S::COL_S + x * 128) + 8 * k,
+                        mma_ts(tmem + S::COL_O + x * HDP, tmem + (part ? S::COL_L + x * 64 : S::COL_S + x * 128) + 8 * k,
                                vd + k * (2048 >> 4), pv, j > 0 || part > 0 || k > 0);
                 if (x == nm - 1) tc_commit(v_empty + st);
                 if (j + 1 < w.tiles) {
@@ -435,6 +476,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             }
         }
         tc_commit(o_full);
+        }
     }
     if (!ok) latch_error(a.c.status, CAC_E_TIMEOUT);
     __syncwarp();
