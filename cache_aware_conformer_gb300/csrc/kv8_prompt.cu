@@ -5,18 +5,17 @@
 // Arithmetic bounds it: 4 * head_dim operations a pair of query and token.  A block takes
 // NM tiles of 128 query rows (row = query * group + head of the group, so the heads that share K and V
 // share the tile too) of one sequence and K/V head, and walks over its 128-token tiles:
-//   converters  7 warps, 16 tokens of K or of V at a time in turn: 16-byte loads of codes, the next piece
+//   converters  6 warps, 16 tokens of K or of V at a time in turn: 16-byte loads of codes, the next piece
 //               under way, turned into fp16 in the 128-byte-swizzled layout that the tensor core reads
 //               (K as [token][element]: its rows are the columns of the scores; V the same
 //               way, read with the token as the contracted index), a ring of two tiles each
-//   MMA         1 thread: S = Q K^T into TMEM, O += P V with P from TMEM
-//   softmax     4 warps for each row tile, a thread per row: the 128 scores from TMEM into registers, maximum, weights
-//               back into TMEM in place of the scores, row sums.  These threads take over registers
-//               of the others (setmaxnreg), so that the scores are read once.
-// With two row tiles the tensor core works on one while the softmax of the other runs.  A
-// row's sums are only rescaled when its maximum has grown by more than 2^SLACK since the last
-// time, which after the first tiles is hardly ever; until then weights may pass 1, and
-// their lift leaves room for it.
+//   MMA         a thread for each row tile: S = Q K^T into TMEM, O += P V with P from TMEM, 64 tokens at a time
+//   softmax     4 warps for each row tile, a thread per row: 64 scores from TMEM into registers, maximum, weights
+//               back into TMEM in place of the scores, row sums
+// A row tile has two places for scores, so that those of the next 64 tokens are there when the softmax of these is done;
+// with two row tiles the tensor core always has one to work on.  A row's sums are only rescaled when its
+// maximum has grown by more than 2^SLACK since the last time, which after the first tiles is hardly ever;
+// until then weights may pass 1, and their lift leaves room for it.
 //
 // Every wait is bounded; one that gives up latches CAC_E_TIMEOUT, and the block unwinds.
 // Shared and tensor memory allow one block an SM.  The TMEM is taken after the wait on the
@@ -30,7 +29,7 @@
 namespace cac {
 namespace {
 
-constexpr int PT_ROWS = 128, PT_KEYS = 128;
+constexpr int PT_ROWS = 128, PT_KEYS = 128, PT_HALF = 64;
 
 template <class T, int HDP> struct PShape {
     static constexpr bool WIDE = sizeof(T) == 4;             // queries and weights as hi + lo
@@ -40,21 +39,15 @@ template <class T, int HDP> struct PShape {
     static constexpr int TILE = HDP / 64 * PANEL;
     static constexpr int OFF_K = NM * PARTS * TILE, OFF_V = OFF_K + 2 * TILE, OFF_SC = OFF_V + 2 * TILE;
     static constexpr int OFF_BAR = OFF_SC + 4 * 24 * 4;      // [4 tiles][K scale, log2 and reciprocal of V scale][8]
-    static constexpr int BYTES = OFF_BAR + 16 * 8 + 16 + 1024;
+    static constexpr int BYTES = OFF_BAR + 21 * 8 + 16 + 1024;
     static constexpr int SMEM = BYTES > 120 * 1024 ? BYTES : 120 * 1024;  // one block an SM
-    static constexpr int SOFT = NM * 4, CONV = 7, WARPS = SOFT + CONV + 1, THREADS = WARPS * 32;
-    // registers: a launch gets 65,536 / THREADS each, in steps of 8 (128 of 512 threads, 168 of 384); the split may not pass that sum
-    static constexpr int LAUNCH = NM == 2 ? 128 : 168, R_SOFT = NM == 2 ? 200 : 232, R_REST = NM == 2 ? 56 : 136;
-    static_assert(SOFT * R_SOFT + (WARPS - SOFT) * R_REST <= WARPS * LAUNCH, "registers");
-    static_assert(WARPS * 32 * LAUNCH <= 65536 && WARPS % 4 == 0, "registers");
-    // TMEM columns: scores (128 each), sums (HDP each), fp32's low halves of the weights (64 each)
-    static constexpr int COL_S = 0, COL_O = NM * 128, COL_L = COL_O + NM * HDP;
-    static_assert(COL_L + (WIDE ? NM * 64 : 0) <= 512, "TMEM");
+    static constexpr int SOFT = NM * 4, CONV = 6, WARPS = SOFT + CONV + 2, THREADS = WARPS * 32;
+    // TMEM columns: scores (two times 64 a row tile, the weights of 64 tokens in their first 32 and, for fp32, the low halves in the
+    // other 32), sums (HDP a row tile)
+    static constexpr int COL_S = 0, COL_O = NM * 128;
+    static_assert(COL_O + NM * HDP <= 512, "TMEM");
     static constexpr float SLACK = WIDE ? 2.f : 8.f, LIFT = 15.f - SLACK;
 };
-
-template <int N> __device__ __forceinline__ void take_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void give_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // D[tmem] (+)= A[smem] B[smem], fp16 operands
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
@@ -84,26 +77,36 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-// 32 columns of the thread's lane, not yet there: tmem_arrived() makes them so
-__device__ __forceinline__ void tmem_ld32_start(uint32_t addr, float* v) {
+// 64 or 16 columns of the thread's lane.  The wait stands in the same statement: between the two the compiler could move a value
+// that has not arrived.
+__device__ __forceinline__ void tmem_ld64(uint32_t addr, float (&v)[64]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
-          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
-          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
-          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+        "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+        "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31]),
+          "=f"(v[32]), "=f"(v[33]), "=f"(v[34]), "=f"(v[35]), "=f"(v[36]), "=f"(v[37]), "=f"(v[38]), "=f"(v[39]),
+          "=f"(v[40]), "=f"(v[41]), "=f"(v[42]), "=f"(v[43]), "=f"(v[44]), "=f"(v[45]), "=f"(v[46]), "=f"(v[47]),
+          "=f"(v[48]), "=f"(v[49]), "=f"(v[50]), "=f"(v[51]), "=f"(v[52]), "=f"(v[53]), "=f"(v[54]), "=f"(v[55]),
+          "=f"(v[56]), "=f"(v[57]), "=f"(v[58]), "=f"(v[59]), "=f"(v[60]), "=f"(v[61]), "=f"(v[62]), "=f"(v[63])
         : "r"(addr)
         : "memory");
 }
-template <int N> __device__ __forceinline__ void tmem_arrived(float (&v)[N]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int k = 0; k < N; k += 16)  // no use of them may move above the wait
-        asm volatile("" : "+f"(v[k]), "+f"(v[k + 1]), "+f"(v[k + 2]), "+f"(v[k + 3]), "+f"(v[k + 4]), "+f"(v[k + 5]),
-                          "+f"(v[k + 6]), "+f"(v[k + 7]), "+f"(v[k + 8]), "+f"(v[k + 9]), "+f"(v[k + 10]), "+f"(v[k + 11]),
-                          "+f"(v[k + 12]), "+f"(v[k + 13]), "+f"(v[k + 14]), "+f"(v[k + 15]));
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+        "%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(addr)
+        : "memory");
 }
 // two at once
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -122,11 +125,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// mbar_wait by a whole warp, with one answer for all of it
+// mbar_wait and mbar_arrive for a whole warp, with one answer for all of it.  All lanes poll (one polling for the others measured 3 %
+// slower); one arrives.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // The block's rows and the tokens that any of them sees, in tiles of 128.
@@ -134,6 +147,7 @@ struct PWork {
     SeqWork s;
     int head, r0, rows;        // rows r0 .. r0 + rows - 1 of the sequence's m * group
     int lot, skt, tiles;       // the window's first tile, sink tiles before it, tiles in all (0: nothing is seen)
+    int halves;                // pieces of 64 tokens in them: the last tile may need one only
     __device__ __forceinline__ int token(int j) const { return (j < skt ? j : lot + j - skt) * PT_KEYS; }
 };
 
@@ -146,8 +160,8 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     float* s_scale = reinterpret_cast<float*>(smem + S::OFF_SC);
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
     uint64_t *q_full = bar, *k_full = bar + 1, *k_empty = bar + 3, *v_full = bar + 5, *v_empty = bar + 7;
-    uint64_t *s_full = bar + 9, *p_full = bar + 11, *o_full = bar + 13;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 16);
+    uint64_t *s_full = bar + 9, *p_full = bar + 13, *o_done = bar + 17;  // s_full, p_full, o_done: [row tile][place]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.head_dim, kvh = a.c.kv_heads;
     pdl_wait();
 
@@ -160,7 +174,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     const int R = w.s.m * a.group;
     w.r0 = tile * S::NM * PT_ROWS;
     w.rows = min(S::NM * PT_ROWS, R - w.r0);
-    w.lot = w.skt = w.tiles = 0;
+    w.lot = w.skt = w.tiles = w.halves = 0;
     if (w.rows > 0 && w.s.len > 0) {
         const int p0 = w.s.len - w.s.m + w.r0 / a.group, p1 = w.s.len - w.s.m + (w.r0 + w.rows - 1) / a.group;
         if (p1 >= 0) {
@@ -168,6 +182,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             w.lot = low / PT_KEYS;
             w.skt = min((min(a.win.sinks, high) + PT_KEYS - 1) / PT_KEYS, w.lot);
             w.tiles = w.skt + (high + PT_KEYS - 1) / PT_KEYS - w.lot;
+            w.halves = 2 * w.tiles - (w.token(w.tiles - 1) + PT_HALF >= high);
         }
     }
     const long long out0 = w.s.row0;
@@ -185,16 +200,19 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     const int nm = w.rows > PT_ROWS ? 2 : 1;
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, nm * 128);
+        mbar_init(q_full, nm * 4);
         for (int k = 0; k < 2; ++k) {
             mbar_init(k_full + k, 8);
             mbar_init(v_full + k, 8);
-            mbar_init(k_empty + k, 1);
-            mbar_init(v_empty + k, 1);
+            mbar_init(k_empty + k, nm);
+            mbar_init(v_empty + k, nm);
             mbar_init(s_full + k, 1);
-            mbar_init(p_full + k, 128);
+            mbar_init(s_full + 2 + k, 1);
+            mbar_init(p_full + k, 4);
+            mbar_init(p_full + 2 + k, 4);
+            mbar_init(o_done + k, 1);
+            mbar_init(o_done + 2 + k, 1);
         }
-        mbar_init(o_full, 1);
         fence_mbar_init();
     }
     if (warp == S::WARPS - 1) tmem_alloc(tmem_slot, 512);
@@ -206,7 +224,6 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     bool ok = true;
 
     if (warp < S::SOFT) {
-        take_registers<S::R_SOFT>();
         // -------------------------------------------------------------- softmax: a thread per row
         const int x = warp >> 2, r = (warp & 3) * 32 + lane, row = w.r0 + x * PT_ROWS + r;
         if (x < nm) {
@@ -220,116 +237,145 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             float f;
             {
                 const T* src = static_cast<const T*>(a.q) + (out0 + query) * a.q_stride + (long long)qh * D;
-                constexpr int VEC = 16 / sizeof(T);  // values of a 16-byte load
-                uint4 raw[HDP / VEC];
+                constexpr int VEC = 16 / sizeof(T), STEP = 32;  // values of a 16-byte load; values at a time (twice: the second from L1)
+                float y[STEP];
+                auto get = [&](int e0) {
 #pragma unroll
-                for (int c = 0; c < HDP / VEC; ++c)
-                    raw[c] = on && c * VEC < D ? *reinterpret_cast<const uint4*>(src + c * VEC) : make_uint4(0, 0, 0, 0);
-                auto value = [&](int e) {
-                    const uint4& q = raw[e / VEC];
-                    const int k = e % VEC, wd = S::WIDE ? k : k >> 1;
-                    const uint32_t u = wd == 0 ? q.x : wd == 1 ? q.y : wd == 2 ? q.z : q.w;
-                    return __uint_as_float(S::WIDE ? u : k & 1 ? u & 0xffff0000u : u << 16);
+                    for (int c = 0; c < STEP; c += VEC) {
+                        const uint4 q = on && e0 + c < D ? *reinterpret_cast<const uint4*>(src + e0 + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (S::WIDE) {
+                                y[c + k] = __uint_as_float(u[k]);
+                            } else {
+                                y[c + 2 * k] = __uint_as_float(u[k] << 16);
+                                y[c + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+                            }
+                        }
+                    }
                 };
                 float amax = 0.f;
+#pragma unroll 2
+                for (int e0 = 0; e0 < HDP; e0 += STEP) {
+                    get(e0);
 #pragma unroll
-                for (int e = 0; e < HDP; ++e) amax = fmaxf(amax, fabsf(value(e)));
+                    for (int k = 0; k < STEP; ++k) amax = fmaxf(amax, fabsf(y[k]));
+                }
                 const int e = min(268 - (int)(__float_as_uint(amax) >> 23), 254);
                 const float up = __uint_as_float((uint32_t)e << 23) * (a.scale < 0.f ? -1.f : 1.f);
                 f = fabsf(a.scale) * LOG2E * __uint_as_float((uint32_t)max(254 - e, 1) << 23) * (e == 254 ? 0.5f : 1.f);
+#pragma unroll 1
+                for (int e0 = 0; e0 < HDP; e0 += STEP) {
+                    get(e0);
 #pragma unroll
-                for (int c = 0; c < HDP / 8; ++c) {
-                    uint32_t hi[4], lo[4];
+                    for (int k8 = 0; k8 < STEP / 8; ++k8) {
+                        const int c = e0 / 8 + k8;
+                        uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float y0 = value(8 * c + 2 * k) * up, y1 = value(8 * c + 2 * k + 1) * up;
-                        hi[k] = pack_half(y0, y1);
-                        if constexpr (S::WIDE) lo[k] = pack_rest(y0, y1, hi[k]);
+                        for (int k = 0; k < 4; ++k) {
+                            const float y0 = y[8 * k8 + 2 * k] * up, y1 = y[8 * k8 + 2 * k + 1] * up;
+                            hi[k] = pack_half(y0, y1);
+                            if constexpr (S::WIDE) lo[k] = pack_rest(y0, y1, hi[k]);
+                        }
+                        uint8_t* dst = smem + x * S::PARTS * S::TILE + (c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if constexpr (S::WIDE) *reinterpret_cast<uint4*>(dst + S::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    uint8_t* dst = smem + x * S::PARTS * S::TILE + (c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                    *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if constexpr (S::WIDE) *reinterpret_cast<uint4*>(dst + S::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             fence_proxy_async_smem();
-            mbar_arrive(q_full);
+            warp_arrive(q_full);
 
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < w.tiles; ++j) {
-                const int tok = w.token(j);
-                const float* sc = s_scale + (j & 3) * 24;
-                if (!warp_wait(s_full + x, j & 1)) { ok = false; break; }
+            for (int h = 0; h < w.halves; ++h) {
+                const int j = h >> 1, tok = w.token(j) + (h & 1) * PT_HALF;
+                const uint32_t col = col_s + (h & 1) * PT_HALF;
+                const float4* sc = reinterpret_cast<const float4*>(s_scale + (j & 3) * 24 + (h & 1) * 4);
+                if (!warp_wait(s_full + 2 * x + (h & 1), j & 1)) { ok = false; break; }
                 tc_fence_after();
-                float v[PT_KEYS];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32_start(col_s + c * 32, v + c * 32);
-                tmem_arrived(v);
+                const float4 ks4 = sc[0], lv4 = sc[2], iv4 = sc[4];
+                const float ks[4] = {ks4.x * f, ks4.y * f, ks4.z * f, ks4.w * f}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w},
+                            iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                float v[PT_HALF];
+                tmem_ld64(col, v);
                 // a token that the row does not see scores -inf
-                if (!__all_sync(0xffffffffu, tok + PT_KEYS <= high && (tok >= low || tok + PT_KEYS <= a.win.sinks))) {
+                if (!__all_sync(0xffffffffu, tok + PT_HALF <= high && (tok >= low || tok + PT_HALF <= a.win.sinks))) {
 #pragma unroll
-                    for (int k = 0; k < PT_KEYS; ++k) {
+                    for (int k = 0; k < PT_HALF; ++k) {
                         const int t = tok + k;
                         if (!(t < high && (t >= low || t < a.win.sinks))) v[k] = -INFINITY;
                     }
                 }
-                float top = -INFINITY;
+                float top = -INFINITY, mb[4];
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    float m0 = fmaxf(v[16 * b], v[16 * b + 1]), m1 = fmaxf(v[16 * b + 2], v[16 * b + 3]);
+                for (int b = 0; b < 4; ++b) mb[b] = fmaxf(v[16 * b], v[16 * b + 1]);
 #pragma unroll
-                    for (int k = 4; k < 16; k += 4) {
-                        m0 = fmaxf(fmaxf(m0, v[16 * b + k]), v[16 * b + k + 1]);
-                        m1 = fmaxf(fmaxf(m1, v[16 * b + k + 2]), v[16 * b + k + 3]);
-                    }
-                    top = fmaxf(top, fmaf(fmaxf(m0, m1), f * sc[b], sc[8 + b]));
-                }
+                for (int k = 2; k < 16; k += 2)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) mb[b] = max3(mb[b], v[16 * b + k], v[16 * b + k + 1]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) top = fmaxf(top, fmaf(mb[b], ks[b], lv[b]));
                 const bool grown = top > m + S::SLACK || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grown)) {
                     const float r = grown ? ex2(m - top) : 1.f;
                     if (grown) m = top, l *= r;
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < HDP / 32; ++c) {
-                            float v[32];
-                            tmem_ld32(col_o + c * 32, v);
+                    if (h > 0) {
+                        if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }  // the sums so far are in
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < HDP; c += 16) {
+                            float o[16];
                             uint32_t u[16];
+                            tmem_ld16(col_o + c, o);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                                for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(v[16 * h + k] * r);
-                                tmem_st16(col_o + c * 32 + 16 * h, u);
-                            }
+                            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * r);
+                            tmem_st16(col_o + c, u);
                         }
                     }
                 }
                 const float base = m == -INFINITY ? -S::LIFT : m - S::LIFT;
+                // one kind of instruction at a time, none of which waits for another of its kind: a warp has little else to hide
+                // their latencies behind
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
+                for (int b = 0; b < 4; ++b) {
+                    const float off = lv[b] - base;
+#pragma unroll
+                    for (int k = 16 * b; k < 16 * b + 16; k += 2) {
+                        const float2 y = fma2(make_float2(v[k], v[k + 1]), make_float2(ks[b], ks[b]), make_float2(off, off));
+                        v[k] = y.x, v[k + 1] = y.y;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int k = 32 * c; k < 32 * c + 32; ++k) v[k] = ex2(v[k]);
                     uint32_t hi[16], lo[16];
 #pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        hi[k] = pack_half(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]);
+                        if constexpr (S::WIDE) lo[k] = pack_rest(v[32 * c + 2 * k], v[32 * c + 2 * k + 1], hi[k]);
+                    }
+                    tmem_st16(col + c * 16, hi);
+                    if constexpr (S::WIDE) tmem_st16(col + 32 + c * 16, lo);
+#pragma unroll
                     for (int b = 2 * c; b < 2 * c + 2; ++b) {
-                        const float ck = f * sc[b], off = sc[8 + b] - base;
-                        const float2 ck2 = make_float2(ck, ck), off2 = make_float2(off, off);
-                        float2 sum[2];
+                        float2 sum[4];
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            float2 y = fma2(make_float2(v[16 * b + 2 * k], v[16 * b + 2 * k + 1]), ck2, off2);
-                            y.x = ex2(y.x), y.y = ex2(y.y);
-                            sum[k & 1] = k < 2 ? y : add2(sum[k & 1], y);
-                            hi[8 * (b & 1) + k] = pack_half(y.x, y.y);
-                            if constexpr (S::WIDE) lo[8 * (b & 1) + k] = pack_rest(y.x, y.y, hi[8 * (b & 1) + k]);
+                            const float2 y = make_float2(v[16 * b + 2 * k], v[16 * b + 2 * k + 1]);
+                            sum[k & 3] = k < 4 ? y : add2(sum[k & 3], y);
                         }
-                        const float2 all = add2(sum[0], sum[1]);
-                        l = fmaf(all.x + all.y, sc[16 + b], l);
+                        const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                        l = fmaf(all.x + all.y, iv[b], l);
                     }
-                    tmem_st16(col_s + c * 16, hi);
-                    if constexpr (S::WIDE) tmem_st16(tmem + lanes + S::COL_L + x * 64 + c * 16, lo);
                 }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(p_full + x);
+                warp_arrive(p_full + 2 * x + (h & 1));
             }
-            if (ok && !warp_wait(o_full, 0)) ok = false;
+            for (int h = max(w.halves - 2, 0); h < w.halves; ++h)
+                if (ok && !warp_wait(o_done + 2 * x + (h & 1), h >> 1 & 1)) ok = false;
             tc_fence_after();
             if (ok) {
                 const bool seen = l > 0.f || l != l;
@@ -368,45 +414,65 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             }
         }
     } else if (warp < S::SOFT + S::CONV) {
-        give_registers<S::R_REST>();
         // -------------------------------------------------------------- converters
-        // piece n: 16 tokens (block n % 8) of tile n / 16, K where n / 8 is even, else V; warp cw takes every seventh
+        // piece n: 16 tokens (block n % 8) of tile n / 16, K where n / 8 is even, else V; warp cw takes every CONV-th
         const int cw = warp - S::SOFT, pieces = w.tiles * 16;
         const int sub = lane >> 2, c4 = lane & 3;   // token % 8 and chunk % 4 of a lane's loads
         constexpr int NL = HDP / 32;
-        auto page_of = [&](int n) {  // -1: past the end, or released
-            const int tok = n < pieces ? w.token(n >> 4) + (n & 7) * KV_BLOCK : w.s.len;
-            return tok < w.s.len ? a.c.table[(long long)w.s.id * a.c.max_pages + tok / a.c.page_tokens] : -1;
+        // Lane l knows where the warp's l-th piece of the next 32 lies, and its scales (with K: the scores need both).
+        struct Spot {
+            long long at;      // -1: past the end, or no page
+            float ks, lv, iv;
         };
-        auto load = [&](int n, int page, uint4 (&raw)[NL], float2& scale) {
-            const int in_page = (w.token(n >> 4) + (n & 7) * KV_BLOCK) % a.c.page_tokens;
-            const uint8_t* from = static_cast<const uint8_t*>(n & 8 ? a.c.v : a.c.k);
-            if (page >= 0) {
-                from += kv_head_at(a.c, a.layer, page, w.head) + (long long)(in_page + sub) * D + c4 * 16;
-                const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
-                if (!(n & 8)) scale = make_float2(a.c.k_scale[sc], a.c.v_scale[sc]);
+        auto look = [&](int n) {
+            Spot t{-1, 1.f, -INFINITY, 0.f};  // a block without a page: any K scale will do, its weights are 2^-inf
+            const int tok = n < pieces ? w.token(n >> 4) + (n & 7) * KV_BLOCK : w.s.len;
+            if (tok < w.s.len) {
+                const int page = a.c.table[(long long)w.s.id * a.c.max_pages + tok / a.c.page_tokens];
+                if (page >= 0) {
+                    const int in_page = tok % a.c.page_tokens;
+                    t.at = kv_head_at(a.c, a.layer, page, w.head) + (long long)in_page * D;
+                    if (!(n & 8)) {
+                        const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
+                        t.ks = a.c.k_scale[sc] * code_unit<CODE>();
+                        t.lv = log2f(a.c.v_scale[sc]) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
+                        t.iv = ex2(-t.lv);
+                    }
+                }
             }
+            return t;
+        };
+        Spot here = look(cw + S::CONV * lane);
+        const int lane_at = sub * D + c4 * 16;
+        const uint8_t *k_lane = static_cast<const uint8_t*>(a.c.k) + lane_at, *v_lane = static_cast<const uint8_t*>(a.c.v) + lane_at;
+        auto load = [&](int n, long long at, uint4 (&raw)[NL]) {
+            const uint8_t* from = (n & 8 ? v_lane : k_lane) + at;
 #pragma unroll
             for (int y = 0; y < NL; ++y)  // rows sub and sub + 8, elements of each 64
-                raw[y] = page >= 0 && ((y >> 1) * 4 + c4) * 16 < D
+                raw[y] = at >= 0 && ((y >> 1) * 4 + c4) * 16 < D
                              ? *reinterpret_cast<const uint4*>(from + (y & 1) * 8 * D + (y >> 1) * 64)
                              : make_uint4(0, 0, 0, 0);
         };
-        int page = page_of(cw), page1 = page_of(cw + S::CONV);
-        uint4 raw[NL], next[NL];
-        float2 scale = make_float2(0.f, 0.f), scale1 = scale;
-        load(cw, page, raw, scale);
-#pragma unroll 1
-        for (int n = cw; n < pieces; n += S::CONV) {
-            const int page2 = page_of(n + 2 * S::CONV);
-            load(min(n + S::CONV, pieces - 1), n + S::CONV < pieces ? page1 : -1, next, scale1);
+        uint4 raw[2][NL];
+        load(cw, __shfl_sync(0xffffffffu, here.at, 0), raw[0]);
+        Spot then = look(cw + S::CONV * (32 + lane));
+        int q = 0;  // the piece's place among the 32
+        auto piece = [&](int n, uint4 (&cur)[NL], uint4 (&nxt)[NL]) {
+            const float ks = __shfl_sync(0xffffffffu, here.ks, q), lv = __shfl_sync(0xffffffffu, here.lv, q),
+                        iv = __shfl_sync(0xffffffffu, here.iv, q);
+            if (++q == 32) {
+                q = 0;
+                here = then;
+                then = look(n + S::CONV * (33 + lane));
+            }
+            load(n + S::CONV, __shfl_sync(0xffffffffu, here.at, q), nxt);
             const int j = n >> 4, st = j & 1, block = n & 7;
             const bool v = n & 8;
-            if (j >= 2 && !warp_wait((v ? v_empty : k_empty) + st, (j / 2 - 1) & 1)) { ok = false; break; }
+            if (j >= 2 && !warp_wait((v ? v_empty : k_empty) + st, (j / 2 - 1) & 1)) return false;
             uint8_t* to = smem + (v ? S::OFF_V : S::OFF_K) + st * S::TILE + (block * 16 + sub) * 128;
 #pragma unroll
             for (int y = 0; y < NL; ++y) {
-                const uint32_t u[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
+                const uint32_t u[4] = {cur[y].x, cur[y].y, cur[y].z, cur[y].w};
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) half4<CODE>(u[k], h[2 * k], h[2 * k + 1]);
@@ -417,65 +483,71 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (!v) {  // both scales with K: the scores need them.  A block without a page: weights of 2^-inf
+                if (!v) {
                     float* sc = s_scale + (j & 3) * 24 + block;
-                    const float lv = log2f(scale.y) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
-                    sc[0] = page >= 0 ? scale.x * code_unit<CODE>() : 1.f;
-                    sc[8] = page >= 0 ? lv : -INFINITY;
-                    sc[16] = page >= 0 ? ex2(-lv) : 0.f;
+                    sc[0] = ks, sc[8] = lv, sc[16] = iv;
                 }
                 mbar_arrive((v ? v_full : k_full) + st);
             }
-            page = page1, page1 = page2, scale = scale1;
-#pragma unroll
-            for (int y = 0; y < NL; ++y) raw[y] = next[y];
+            return true;
+        };
+#pragma unroll 1
+        for (int n = cw; n < pieces; n += 2 * S::CONV) {
+            if (!piece(n, raw[0], raw[1])) { ok = false; break; }
+            if (n + S::CONV < pieces && !piece(n + S::CONV, raw[1], raw[0])) { ok = false; break; }
         }
     } else {
-        give_registers<S::R_REST>();
-        if (lane == 0) {
-        // -------------------------------------------------------------- MMA
-        constexpr uint32_t qk = idesc_f16(128, 128, false), pv = idesc_f16(128, HDP, true);
-        auto scores = [&](int x, int st) {
-            const uint64_t kd = sdesc_k_sw128(smem + S::OFF_K + st * S::TILE);
+        // -------------------------------------------------------------- MMA: a thread per row tile
+        const int x = warp - S::SOFT - S::CONV;
+        if (lane == 0 && x < nm) {
+            constexpr uint32_t qk = idesc_f16(128, PT_HALF, false), pv = idesc_f16(128, HDP, true);
+            auto scores = [&](int h) {
+                const uint64_t kd = sdesc_k_sw128(smem + S::OFF_K + (h >> 1 & 1) * S::TILE + (h & 1) * (PT_HALF * 128));
 #pragma unroll
-            for (int part = 0; part < S::PARTS; ++part) {
-                const uint64_t qd = sdesc_k_sw128(smem + (x * S::PARTS + part) * S::TILE);
+                for (int part = 0; part < S::PARTS; ++part) {
+                    const uint64_t qd = sdesc_k_sw128(smem + (x * S::PARTS + part) * S::TILE);
 #pragma unroll
-                for (int k = 0; k < HDP / 16; ++k) {
-                    const uint32_t step = (k >> 2) * (S::PANEL >> 4) + 2 * (k & 3);
-                    mma_ss(tmem + S::COL_S + x * 128, qd + step, kd + step, qk, part > 0 || k > 0);
+                    for (int k = 0; k < HDP / 16; ++k) {
+                        const uint32_t step = (k >> 2) * (S::PANEL >> 4) + 2 * (k & 3);
+                        mma_ss(tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF, qd + step, kd + step, qk, part > 0 || k > 0);
+                    }
                 }
-            }
-            tc_commit(s_full + x);
-        };
-        if (!mbar_wait(q_full, 0) || !mbar_wait(k_full, 0)) ok = false;
-        if (ok) {
-            tc_fence_after();
-            for (int x = 0; x < nm; ++x) scores(x, 0);
-            tc_commit(k_empty);
-        }
-        for (int j = 0; ok && j < w.tiles; ++j) {
-            const int st = j & 1, sn = st ^ 1;
-            for (int x = 0; ok && x < nm; ++x) {
-                if ((x == 0 && !mbar_wait(v_full + st, (j / 2) & 1)) || !mbar_wait(p_full + x, j & 1)) { ok = false; break; }
+                tc_commit(s_full + 2 * x + (h & 1));
+                if (h & 1) tc_commit(k_empty + (h >> 1 & 1));
+            };
+            ok = mbar_wait(q_full, 0) && mbar_wait(k_full, 0);
+            if (ok) {
                 tc_fence_after();
-                const uint64_t vd = sdesc_mn_sw128(smem + S::OFF_V + st * S::TILE, S::PANEL);
+                scores(0);
+            }
+            for (int h = 0; ok && h < w.halves; ++h) {
+                const int st = h >> 1 & 1, next = h + 1;
+                if (next < w.halves) {
+                    // the next scores take the place of the weights before these: products into other accumulators need
+                    // not run in order
+                    if ((!(next & 1) && !mbar_wait(k_full + (next >> 1 & 1), next >> 2 & 1)) ||
+                        (h > 0 && !mbar_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    scores(next);
+                }
+                if ((!(h & 1) && !mbar_wait(v_full + st, h >> 2 & 1)) || !mbar_wait(p_full + 2 * x + (h & 1), h >> 1 & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t vd = sdesc_mn_sw128(smem + S::OFF_V + st * S::TILE + (h & 1) * (PT_HALF * 128), S::PANEL);
 #pragma unroll
                 for (int part = 0; part < S::PARTS; ++part)
 #pragma unroll
-                    for (int k = 0; k < PT_KEYS / 16; ++k)
-                        mma_ts(tmem + S::COL_O + x * HDP, tmem + (part ? S::COL_L + x * 64 : S::COL_S + x * 128) + 8 * k,
-                               vd + k * (2048 >> 4), pv, j > 0 || part > 0 || k > 0);
-                if (x == nm - 1) tc_commit(v_empty + st);
-                if (j + 1 < w.tiles) {
-                    if (x == 0 && !mbar_wait(k_full + sn, ((j + 1) / 2) & 1)) { ok = false; break; }
-                    tc_fence_after();
-                    scores(x, sn);
-                    if (x == nm - 1) tc_commit(k_empty + sn);
-                }
+                    for (int k = 0; k < PT_HALF / 16; ++k)
+                        mma_ts(tmem + S::COL_O + x * HDP, tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF + part * 32 + 8 * k,
+                               vd + k * (2048 >> 4), pv, h > 0 || part > 0 || k > 0);
+                tc_commit(o_done + 2 * x + (h & 1));
+                if (h & 1) tc_commit(v_empty + st);
             }
-        }
-        tc_commit(o_full);
         }
     }
     if (!ok) latch_error(a.c.status, CAC_E_TIMEOUT);

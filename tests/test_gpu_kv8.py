@@ -114,7 +114,7 @@ class Both:
         rag = {} if uniform else {"starts": self.starts(counts), "max_new": max(counts, default=0)}
         out, lse = self.cache.attend(layer, self.ids(ids), q.cuda(), att_left=left, att_chunk=chunk, sinks=sinks, scale=scale,
                                      lse=True, **rag, **kw)
-        torch.cuda.synchronize()
+        self.cache.check()
         assert out.dtype == q.dtype and out.shape == q.shape and lse.shape == (T, heads)
         sc = scale if scale is not None else cfg.head_dim ** -0.5
         at = 0
