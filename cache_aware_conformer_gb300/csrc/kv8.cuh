@@ -111,6 +111,13 @@ struct KvAttend {
     long long q_stride, out_stride;
     float scale;
     int layer, heads, group, max_new;
+    uint32_t group_mul;  // 2^32 / group, rounded down, + 1 (0 for a group of 1)
+    // row / group of a row below 2^32: the product is the quotient or one more
+    __device__ __forceinline__ int query_of(int row) const {
+        if (group_mul == 0) return row;
+        const int q = (int)__umulhi((uint32_t)row, group_mul);
+        return q - (q * group > row);
+    }
 };
 
 // The device of a cache as the current one for the life of this object.

@@ -31,18 +31,29 @@
 
 #include "kv8_attn.cuh"
 
+#ifndef KV8_ATTN_CODE
+#define KV8_ATTN_CODE 0  // CAC_KV8_INT8
+#endif
+
 namespace cac {
 namespace {
 
 constexpr float LIFT = 15.f;     // weights are held times 2^15: the largest is then 32,768, and fp16 keeps 11 bits of every
                                  // weight down to 2^-29 of it (a small weight may meet a large value)
-constexpr int TA_SEQS = 512;     // sequences of one launch
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// with A's rows 8 .. 15 zero
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
+    const uint32_t full[4] = {a[0], 0u, a[1], 0u};
+    mma_f16(d, full, b0, b1);
+}
+template <int N> __device__ __forceinline__ void mma_rows(float (&d)[4], const uint32_t (&a)[N], uint32_t b0, uint32_t b1) {
+    mma_f16(d, a, b0, b1);
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -90,13 +101,15 @@ __device__ __forceinline__ Tile tile_from(const Tile& t, int lane) {
 
 // Sixteen query rows and their running sums, spread over a warp as the tensor core's
 // fragments: a thread has rows g and g + 8 (g = lane / 4, t = lane % 4).
-template <class T, int CODE, int HDP> struct Rows {
+template <class T, int CODE, int HDP, bool LOW> struct Rows {
+    static constexpr int H = LOW ? 1 : 2;                 // row halves: LOW holds rows 0 .. 7 only, the other eight are zero
+
     static constexpr bool WIDE = sizeof(T) == 4;          // hi + lo
     static constexpr int STEPS = HDP / 16, NT = HDP / 8;
-    uint32_t q[STEPS][4], ql[WIDE ? STEPS : 1][4];
+    uint32_t q[STEPS][2 * H], ql[WIDE ? STEPS : 1][2 * H];
     float o[NT][4];
-    float m[2], l[2], f[2];                               // maximum, sum, score factor of rows g, g + 8
-    int low[2], high[2];
+    float m[H], l[H], f[H];                               // maximum, sum, score factor of rows g, g + 8
+    int low[H], high[H];
     int lo_max, hi_min, lo_min, hi_max;                   // over the rows
 
     // Queries of K/V head `head`, rows r0 .. r0 + 15 of the sequence's m * group.
@@ -104,15 +117,15 @@ template <class T, int CODE, int HDP> struct Rows {
     __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim, R = s.m * a.group;
         // rows in order of their positions: the first and last bound the windows
-        const int p0 = s.len - s.m + r0 / a.group, p1 = s.len - s.m + (min(r0 + 16, R) - 1) / a.group;
+        const int p0 = s.len - s.m + a.query_of(r0), p1 = s.len - s.m + a.query_of(min(r0 + 16, R) - 1);
         const bool any = s.len > 0 && p1 >= 0;
         hi_min = any && p0 >= 0 ? a.win.high(p0, s.len) : 0;
         hi_max = any ? a.win.high(p1, s.len) : 0;
         lo_max = any ? a.win.low(p1) : 0;
         lo_min = any ? a.win.low(max(p0, 0)) : 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = r0 + g + 8 * h, query = r / a.group, p = s.len - s.m + query;
+        for (int h = 0; h < H; ++h) {
+            const int r = r0 + g + 8 * h, query = a.query_of(r), p = s.len - s.m + query;
             const bool on = r < R;
             m[h] = -INFINITY, l[h] = 0.f;
             low[h] = on && p >= 0 ? a.win.low(p) : 0;
@@ -159,10 +172,10 @@ template <class T, int CODE, int HDP> struct Rows {
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
                 q[k][h] = pack_half(x[k][0] * up, x[k][1] * up);
-                q[k][2 + h] = pack_half(x[k][2] * up, x[k][3] * up);
+                q[k][H + h] = pack_half(x[k][2] * up, x[k][3] * up);
                 if constexpr (WIDE) {
                     ql[k][h] = pack_rest(x[k][0] * up, x[k][1] * up, q[k][h]);
-                    ql[k][2 + h] = pack_rest(x[k][2] * up, x[k][3] * up, q[k][2 + h]);
+                    ql[k][H + h] = pack_rest(x[k][2] * up, x[k][3] * up, q[k][H + h]);
                 }
             }
         }
@@ -170,48 +183,64 @@ template <class T, int CODE, int HDP> struct Rows {
         for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
-    // One tile of 16 tokens, codes at shared addresses k and v.  Column n of score tile i is token
-    // (n / 2) + 4 (2 i + n % 2), so that a thread's four weights of a row are tokens t, t + 4, t + 8, t + 12.
-    __device__ __forceinline__ void tile(const Tile& d, const uint8_t* k, const uint8_t* v, int sinks) {
+    // Whether a tile holds a token that one of the rows sees
+    __device__ __forceinline__ bool sees(const Tile& d, int sinks) const {
+        return d.at >= 0 && d.j0 < hi_max && (d.j0 + KV_BLOCK > lo_min || d.j0 < sinks);
+    }
+
+    // Two tiles of 16 tokens, their codes at shared addresses k[u] (V after K); on[u]: take part.  Column n of score tile i is
+    // token (n / 2) + 4 (2 i + n % 2), so that a thread's four weights of a row are tokens t, t + 4, t + 8, t + 12.
+    __device__ __forceinline__ void tiles(const Tile (&d)[2], const uint8_t* const (&k)[2], const bool (&on)[2], int sinks) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-        if (d.j0 >= hi_max || (d.j0 + KV_BLOCK <= lo_min && d.j0 >= sinks)) return;
-        float s[2][4];
+        float s[2][2][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
-            const int r = (g >> 1) + 4 * (2 * i + (g & 1));
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[u][i][0] = s[u][i][1] = s[u][i][2] = s[u][i][3] = on[u] ? 0.f : -INFINITY;
+            if (!on[u]) continue;
 #pragma unroll
             for (int j = 0; j < HDP / 64; ++j) {
-                const uint4 w = *reinterpret_cast<const uint4*>(k + tile_at<HDP>(r, 4 * j + t));
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint32_t b0, b1;
-                    half4<CODE>(ww[x], b0, b1);
-                    mma_f16(s[i], q[4 * j + x], b0, b1);
-                    if constexpr (WIDE) mma_f16(s[i], ql[4 * j + x], b0, b1);
-                }
-            }
-        }
-        const bool full = d.j0 + KV_BLOCK <= hi_min && (d.j0 >= lo_max || d.j0 + KV_BLOCK <= sinks);
-        float top[2];
-        uint32_t p[4], pl[4];
-        bool moved = false;
+                for (int i = 0; i < 2; ++i) {
+                    const int r = (g >> 1) + 4 * (2 * i + (g & 1));
+                    const uint4 w = *reinterpret_cast<const uint4*>(k[u] + tile_at<HDP>(r, 4 * j + t));
+                    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float c = f[h] * d.ks;
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    float& x = s[i][2 * h + b];
-                    x = fmaf(x, c, d.lv);
-                    if (!full) {
-                        const int j = d.j0 + t + 4 * (2 * i + b);
-                        if (!(j < high[h] && (j >= low[h] || j < sinks))) x = -INFINITY;
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t b0, b1;
+                        half4<CODE>(ww[x], b0, b1);
+                        mma_rows(s[u][i], q[4 * j + x], b0, b1);
+                        if constexpr (WIDE) mma_rows(s[u][i], ql[4 * j + x], b0, b1);
                     }
                 }
-            float mx = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
+            }
+            const bool full = d[u].j0 + KV_BLOCK <= hi_min && (d[u].j0 >= lo_max || d[u].j0 + KV_BLOCK <= sinks);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                const float c = f[h] * d[u].ks;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) s[u][i][2 * h + b] = fmaf(s[u][i][2 * h + b], c, d[u].lv);
+            }
+            if (!full) {
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            const int j = d[u].j0 + t + 4 * (2 * i + b);
+                            if (!(j < high[h] && (j >= low[h] || j < sinks))) s[u][i][2 * h + b] = -INFINITY;
+                        }
+            }
+        }
+        float top[H];
+        bool moved = false;
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float mx = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
+            mx = fmaxf(mx, fmaxf(fmaxf(s[1][0][2 * h], s[1][0][2 * h + 1]), fmaxf(s[1][1][2 * h], s[1][1][2 * h + 1])));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             top[h] = fmaxf(m[h], mx);
@@ -219,7 +248,7 @@ template <class T, int CODE, int HDP> struct Rows {
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < H; ++h) {
                 const float r = top[h] == -INFINITY ? 1.f : ex2(m[h] - top[h]);
                 m[h] = top[h];
                 l[h] *= r;
@@ -227,54 +256,63 @@ template <class T, int CODE, int HDP> struct Rows {
                 for (int n = 0; n < NT; ++n) o[n][2 * h] *= r, o[n][2 * h + 1] *= r;
             }
         }
+        uint32_t p[2][2 * H], pl[2][2 * H];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
             const float base = m[h] == -INFINITY ? 0.f : m[h] - LIFT;
-            float w[2][2];
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int u = 0; u < 2; ++u) {
+                float w[2][2];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[i][2 * h + b] - base);
-            l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), d.iv, l[h]);
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                p[2 * i + h] = pack_half(w[i][0], w[i][1]);
-                if constexpr (WIDE) pl[2 * i + h] = pack_rest(w[i][0], w[i][1], p[2 * i + h]);
+                    for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[u][i][2 * h + b] - base);
+                l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), d[u].iv, l[h]);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    p[u][H * i + h] = pack_half(w[i][0], w[i][1]);
+                    if constexpr (WIDE) pl[u][H * i + h] = pack_rest(w[i][0], w[i][1], p[u][H * i + h]);
+                }
             }
         }
         // value columns: column n of output tile y is element first(n) + y (see `element`)
         constexpr int PER = HDP == 64 ? 8 : 16;
 #pragma unroll
-        for (int z = 0; z < HDP / (8 * PER); ++z) {
-            const int c = HDP == 64 ? g >> 1 : (((g & 1) << 2) | (g >> 1)) + 8 * z;
-            uint32_t w[4][PER / 4];
+        for (int u = 0; u < 2; ++u) {
+            if (!on[u]) continue;
+            const uint8_t* v = k[u] + KV_BLOCK * HDP;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                const uint8_t* at = v + tile_at<HDP>(t + 4 * y, c);
-                if constexpr (HDP == 64) {
-                    const uint2 u = *reinterpret_cast<const uint2*>(at + (g & 1) * 8);
-                    w[y][0] = u.x, w[y][1] = u.y;
-                } else {
-                    const uint4 u = *reinterpret_cast<const uint4*>(at);
-                    w[y][0] = u.x, w[y][1] = u.y, w[y][2] = u.z, w[y][3] = u.w;
-                }
-            }
+            for (int z = 0; z < HDP / (8 * PER); ++z) {
+                const int c = HDP == 64 ? g >> 1 : (((g & 1) << 2) | (g >> 1)) + 8 * z;
+                uint32_t w[4][PER / 4];
 #pragma unroll
-            for (int x = 0; x < PER / 4; ++x)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {  // elements 4 x + 2 y and 4 x + 2 y + 1 of four tokens
-                    const uint32_t sel = y ? 0x7362 : 0x5140;
-                    uint32_t a0, a1, b0, b1;
-                    half4<CODE>(__byte_perm(w[0][x], w[1][x], sel), a0, b0);
-                    half4<CODE>(__byte_perm(w[2][x], w[3][x], sel), a1, b1);
-                    const int n = z * PER + 4 * x + 2 * y;
-                    mma_f16(o[n], p, a0, a1);
-                    mma_f16(o[n + 1], p, b0, b1);
-                    if constexpr (WIDE) {
-                        mma_f16(o[n], pl, a0, a1);
-                        mma_f16(o[n + 1], pl, b0, b1);
+                for (int y = 0; y < 4; ++y) {
+                    const uint8_t* at = v + tile_at<HDP>(t + 4 * y, c);
+                    if constexpr (HDP == 64) {
+                        const uint2 e = *reinterpret_cast<const uint2*>(at + (g & 1) * 8);
+                        w[y][0] = e.x, w[y][1] = e.y;
+                    } else {
+                        const uint4 e = *reinterpret_cast<const uint4*>(at);
+                        w[y][0] = e.x, w[y][1] = e.y, w[y][2] = e.z, w[y][3] = e.w;
                     }
                 }
+#pragma unroll
+                for (int x = 0; x < PER / 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {  // elements 4 x + 2 y and 4 x + 2 y + 1 of four tokens
+                        const uint32_t sel = y ? 0x7362 : 0x5140;
+                        uint32_t a0, a1, b0, b1;
+                        half4<CODE>(__byte_perm(w[0][x], w[1][x], sel), a0, b0);
+                        half4<CODE>(__byte_perm(w[2][x], w[3][x], sel), a1, b1);
+                        const int n = z * PER + 4 * x + 2 * y;
+                        mma_rows(o[n], p[u], a0, a1);
+                        mma_rows(o[n + 1], p[u], b0, b1);
+                        if constexpr (WIDE) {
+                            mma_rows(o[n], pl[u], a0, a1);
+                            mma_rows(o[n + 1], pl[u], b0, b1);
+                        }
+                    }
+            }
         }
     }
     // first element of column n's run in piece z
@@ -287,7 +325,7 @@ template <class T, int CODE, int HDP> struct Rows {
     // the sums of a row's four threads
     __device__ __forceinline__ void finish() {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < H; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
         }
@@ -384,7 +422,7 @@ __device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s
             for (int c = 0; c < PER; ++c) p.o[((size_t)to * 16 + r) * HDP + lane * PER + c] = o[c];
             if (lane == 0) p.ml[((size_t)to * 16 + r) * 2] = top, p.ml[((size_t)to * 16 + r) * 2 + 1] = l;
         } else {
-            const int row = r0 + r, query = row / a.group, qh = head * a.group + row - query * a.group, D = a.c.head_dim;
+            const int row = r0 + r, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
             const bool seen = l > 0.f || l != l;
             T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
@@ -399,7 +437,7 @@ __device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s
 // Warps of a block, and the tiles that each has in flight or at hand (two matrices of 16 rows of HDP bytes).  The sums of 16 rows
 // take HDP / 2 registers and an fp32 query's two halves HDP / 2 more, which leaves room for 12 warps, or 8.
 template <class T, int HDP, bool SPLIT> struct Shape {
-    static constexpr int WARPS = !SPLIT ? 4 : HDP == 64 || (HDP == 128 && sizeof(T) == 2) ? 12 : 8;
+    static constexpr int WARPS = !SPLIT ? 4 : HDP == 64 ? 12 : 8;
     static constexpr int STAGE = 2 * KV_BLOCK * HDP;
     static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : 196608 / (WARPS * STAGE);
     static constexpr int BYTES = WARPS * STAGES * STAGE;
@@ -408,10 +446,10 @@ template <class T, int HDP, bool SPLIT> struct Shape {
 
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
 // whole unit (short windows, where a unit has a handful of tiles): nothing has to be joined.
-template <class T, int CODE, int HDP, bool SPLIT>
+template <class T, int CODE, int HDP, bool LOW, bool SPLIT>
 __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HDP, SPLIT>::BLOCKS))
     kv_attend_kernel(const __grid_constant__ KvAttend a, int row_tiles, void* space) {
-    using R = Rows<T, CODE, HDP>;
+    using R = Rows<T, CODE, HDP, LOW>;
     using S = Shape<T, HDP, SPLIT>;
     constexpr int STAGES = S::STAGES, STAGE = S::STAGE, WARPS = S::WARPS, CH = HDP / 16;
     extern __shared__ __align__(128) uint8_t ring_all[];
@@ -493,14 +531,16 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             return tile_of<CODE>(a, s.id, s.len, s.lot, s.skt, (int)x, unit % kvh);
         }
     };
-    Tile now = look(x0 + lane), next = look(x0 + 32 + lane);
+    Tile now = look(x0 + lane), next = now;
+    if constexpr (SPLIT) next = look(x0 + 32 + lane);
     long long base = x0;
 
+    int into = 0;  // the stage that the next copies go to
     auto fetch = [&](long long x) {  // queue the copies of tile x; always one group
         const int k = (int)(x - base);
         const long long at = __shfl_sync(0xffffffffu, k < 32 ? now.at : next.at, k & 31);
         if (x < x1 && at >= 0) {
-            const uint32_t dst = smem_u32(ring + (int)((x - x0) % STAGES) * STAGE);
+            const uint32_t dst = smem_u32(ring) + into * STAGE;
             const uint8_t *ks = static_cast<const uint8_t*>(a.c.k) + at, *vs = static_cast<const uint8_t*>(a.c.v) + at;
 #pragma unroll
             for (int e0 = 0; e0 < KV_BLOCK * CH; e0 += 32) {
@@ -512,6 +552,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             }
         }
         cp_commit();
+        into = into + 1 == STAGES ? 0 : into + 1;
     };
     if (D < HDP) {  // chunks past the head's width stay zero
         for (int st = 0; st < STAGES; ++st)
@@ -524,7 +565,8 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
         __syncwarp();
     }
 #pragma unroll 1
-    for (int k = 0; k < STAGES - 1; ++k) fetch(x0 + k);
+    for (int k = 0; k < STAGES; ++k) fetch(x0 + k);
+    int from_stage = 0;
 
     R r;
     long long x = x0;
@@ -540,28 +582,34 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
         const long long end = min(u1, x1), from = x;
         const int head = unit % kvh, r0 = unit / kvh * 16;
         r.load(a, s, head, r0);
-        for (; x < end; ++x) {
-            if (x - base >= 32) {
+        while (x < end) {
+            if (SPLIT && x - base >= 32) {
                 base += 32;
                 now = next;
                 next = look(base + 32 + lane);
             }
-            fetch(x + STAGES - 1);
-            cp_wait<STAGES - 1>();
+            cp_wait<STAGES - 2>();  // tiles x and x + 1 are there
             __syncwarp();
-            const Tile d = tile_from(now, (int)(x - base));
-            const uint8_t* k = ring + (int)((x - x0) % STAGES) * STAGE;
-            if (d.at >= 0) r.tile(d, k, k + KV_BLOCK * HDP, a.win.sinks);
-            __syncwarp();  // the stage is read before its next copy is queued
+            const bool two = x + 1 < end;
+            const int k0 = (int)(x - base), s1 = from_stage + 1 == STAGES ? 0 : from_stage + 1;
+            const Tile d[2] = {tile_from(now, k0), k0 < 31 ? tile_from(now, k0 + 1) : tile_from(next, 0)};
+            const uint8_t* const k[2] = {ring + from_stage * STAGE, ring + s1 * STAGE};
+            const bool on[2] = {r.sees(d[0], a.win.sinks), two && r.sees(d[1], a.win.sinks)};
+            if (on[0] || on[1]) r.tiles(d, k, on, a.win.sinks);
+            __syncwarp();  // the stages are read before their next copies are queued
+            fetch(x + STAGES);
+            if (two) fetch(x + STAGES + 1);
+            x += 1 + two;
+            from_stage = two ? (s1 + 1 == STAGES ? 0 : s1 + 1) : s1;
         }
         r.finish();
         const int g = lane >> 2, t = lane & 3;
         const bool whole = from == u0 && end == u1;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < R::H; ++h) {
             const int row = r0 + g + 8 * h;
             if (row >= s.m * a.group) continue;
-            const int query = row / a.group, qh = head * a.group + row - query * a.group;
+            const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
             const float inv = r.l[h] > 0.f || r.l[h] != r.l[h] ? 1.f / r.l[h] : 0.f;
             const int slot = 2 * (blockIdx.x * WARPS + warp) + (from != x0);
 #pragma unroll
@@ -592,10 +640,19 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
                 }
             }
         }
+        if constexpr (LOW) {
+            const int row = r0 + 8 + g;  // only a sequence with more rows than max_new has any: they see nothing
+            if (row < s.m * a.group) {
+                const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+                T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D;
+                for (int e = t; e < D; e += 4) dst[e] = from_f<T>(0.f);
+                if (t == 0 && a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] = -INFINITY;
+            }
+        }
         if constexpr (!SPLIT) {
             // rows that a count above max_new adds: they see nothing, and are written as that
             unit += kvh * row_tiles;
-            if (unit / kvh * 16 < s.m * a.group) x = 0;
+            if (unit / kvh * 16 < s.m * a.group) x = 0;  // their one tile holds nothing
         }
     }
     cp_wait<0>();
@@ -673,7 +730,7 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
 #pragma unroll
     for (int k = 0; k < JOIN_Y; ++k) o += s_o[k][d], l += s_l[k];
     const bool seen = l > 0.f || l != l;
-    const int query = row / a.group, qh = head * a.group + row - query * a.group;
+    const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
     if (d < a.c.head_dim)
         static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + d] =
             from_f<T>(seen ? o / l : 0.f);
@@ -681,19 +738,12 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
         a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
 }
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return sms;
-}
-
-template <class T, int CODE, int HDP>
+template <class T, int CODE, int HDP, bool LOW>
 cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
     using S1 = Shape<T, HDP, true>;
     using S0 = Shape<T, HDP, false>;
     const int smem = split ? S1::BYTES : S0::BYTES;
-    const auto kernel = split ? kv_attend_kernel<T, CODE, HDP, true> : kv_attend_kernel<T, CODE, HDP, false>;
+    const auto kernel = split ? kv_attend_kernel<T, CODE, HDP, LOW, true> : kv_attend_kernel<T, CODE, HDP, LOW, false>;
     static std::atomic<uint64_t> ready[2];  // devices on which the kernels may use their shared memory
     const uint64_t bit = 1ull << (a.c.device & 63);
     cudaError_t e = cudaSuccess;
@@ -712,83 +762,32 @@ cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms,
     return launch_k(kv_join_kernel<T, HDP>, dim3(sms - 1, std::min(16, a.max_new * a.group)), dim3(HDP, JOIN_Y), 0, s, 1, a,
                     sms, S1::WARPS, space);
 }
-template <class T, int CODE>
+template <class T, int CODE, int HDP>
 cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
-    if (a.c.head_dim <= 64) return launch_attend<T, CODE, 64>(a, split, row_tiles, sms, space, s);
-    if (a.c.head_dim <= 128) return launch_attend<T, CODE, 128>(a, split, row_tiles, sms, space, s);
-    return launch_attend<T, CODE, 256>(a, split, row_tiles, sms, space, s);
-}
-
-// Whether units are cut: not where the window leaves at most SHORT tiles to any of them.
-constexpr int SHORT = 16;
-bool splits(const cac_kv8& c, int max_new, int left, int chunk, int sinks) {
-    long long tokens = (long long)c.max_pages * c.page_tokens;
-    if (left >= 0) tokens = std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);
-    return tokens > SHORT * KV_BLOCK;
+    return (long long)a.max_new * a.group <= 8 ? launch_attend<T, CODE, HDP, true>(a, split, row_tiles, sms, space, s)
+                                               : launch_attend<T, CODE, HDP, false>(a, split, row_tiles, sms, space, s);
 }
 
 }  // namespace
+
+// kv8_attn.cu is compiled once for each kind of code (kv8_attn_e4m3.cu includes it)
+template <int CODE>
+cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
+    const int d = a.c.head_dim;
+    if (dtype == CAC_DTYPE_BF16)
+        return d <= 64    ? launch_attend<bf16, CODE, 64>(a, split, row_tiles, sms, space, s)
+               : d <= 128 ? launch_attend<bf16, CODE, 128>(a, split, row_tiles, sms, space, s)
+                          : launch_attend<bf16, CODE, 256>(a, split, row_tiles, sms, space, s);
+    return d <= 64    ? launch_attend<float, CODE, 64>(a, split, row_tiles, sms, space, s)
+           : d <= 128 ? launch_attend<float, CODE, 128>(a, split, row_tiles, sms, space, s)
+                      : launch_attend<float, CODE, 256>(a, split, row_tiles, sms, space, s);
+}
+template cudaError_t kv_launch_attend<KV8_ATTN_CODE>(const KvAttend&, int, bool, int, int, void*, cudaStream_t);
+
+#if KV8_ATTN_CODE == 0
+size_t kv_attend_bytes(int head_dim, int sms) {
+    return head_dim <= 64 ? partial_bytes<64>(sms) : head_dim <= 128 ? partial_bytes<128>(sms) : partial_bytes<256>(sms);
+}
+#endif
+
 }  // namespace cac
-
-using namespace cac;
-
-extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
-                                           int att_chunk, int sinks) {
-    (void)heads;
-    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 1 || att_chunk < 1 || sinks < 0 ||
-        !splits(*c, std::min(max_new, rows), att_left, att_chunk, sinks))
-        return 0;
-    DeviceScope dev(c->device);
-    const int sms = dev.ok ? sm_count() : 0;
-    return c->head_dim <= 64 ? partial_bytes<64>(sms) : c->head_dim <= 128 ? partial_bytes<128>(sms) : partial_bytes<256>(sms);
-}
-
-extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
-                              int max_new, int heads, float scale, int att_left, int att_chunk, int sinks,
-                              const void* q, long long q_stride, void* out, long long out_stride, float* lse,
-                              int dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    const int r = kv_check_cache(c);
-    if (r != CAC_OK) return r;
-    if (n < 0 || (n > 0 && !ids) || layer < 0 || layer >= c->n_layers || rows < 0 || heads < 1 || att_chunk < 1 ||
-        sinks < 0 || (dtype != CAC_DTYPE_F32 && dtype != CAC_DTYPE_BF16) || !(scale - scale == 0.f))
-        return CAC_E_INVAL;
-    if (heads % c->kv_heads || heads > 65535) return CAC_E_INVAL;
-    if (n == 0 || rows == 0) return CAC_OK;
-    if ((!starts && rows % n) || (starts && max_new < 0)) return CAC_E_INVAL;
-    const long long width = (long long)heads * c->head_dim, size = dtype == CAC_DTYPE_BF16 ? 2 : 4;
-    if (!q || !out || q == out || q_stride < width || out_stride < width) return CAC_E_INVAL;
-    const uintptr_t words = reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(starts) |
-                            reinterpret_cast<uintptr_t>(lse);
-    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
-        ((q_stride * size | out_stride * size) & 15) || (words & 3))
-        return CAC_E_ALIGN;
-    const int group = heads / c->kv_heads, most = starts ? std::min(max_new, rows) : rows / n;
-    const bool split = splits(*c, most, att_left, att_chunk, sinks);
-    if (split && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
-                  workspace_bytes < cac_kv8_attend_workspace(c, n, rows, most, heads, att_left, att_chunk, sinks)))
-        return CAC_E_INVAL;
-    const long long tiles = ((long long)most * group + 15) / 16;
-    if (tiles == 0) return CAC_OK;
-    if (tiles * std::min(n, TA_SEQS) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
-    DeviceScope dev(c->device);
-    if (!dev.ok) return CAC_E_CUDA;
-    const int sms = sm_count();
-    if (sms < 1) return CAC_E_CUDA;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    for (int i0 = 0; i0 < n; i0 += TA_SEQS) {
-        const int each = rows / n, part = std::min(n - i0, TA_SEQS);
-        const KvAttend a{*c, {starts ? starts + i0 : nullptr, each, part, rows, each * i0}, {att_left, att_chunk, sinks},
-                         ids + i0, q, out, lse, q_stride, out_stride, scale, layer, heads, group, most};
-        cudaError_t e;
-        if (kv_prompt_takes(a, dtype))
-            e = kv_launch_prompt(a, dtype, s);
-        else if (c->code == CAC_KV8_INT8)
-            e = dtype == CAC_DTYPE_BF16 ? launch_attend<bf16, CAC_KV8_INT8>(a, split, (int)tiles, sms, workspace, s)
-                                        : launch_attend<float, CAC_KV8_INT8>(a, split, (int)tiles, sms, workspace, s);
-        else
-            e = dtype == CAC_DTYPE_BF16 ? launch_attend<bf16, CAC_KV8_E4M3>(a, split, (int)tiles, sms, workspace, s)
-                                        : launch_attend<float, CAC_KV8_E4M3>(a, split, (int)tiles, sms, workspace, s);
-        if (e != cudaSuccess) return CAC_E_CUDA;
-    }
-    return CAC_OK;
-}

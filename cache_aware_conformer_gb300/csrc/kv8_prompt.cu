@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
         const int step = w.s.len > 0 ? 1 << 30 : row_tiles * S::NM * PT_ROWS;  // a count above max_new has rows past the last tile
         for (long long r0 = w.r0; r0 < R; r0 += step)
             for (int e = threadIdx.x; e < min(S::NM * PT_ROWS, (int)(R - r0)) * D; e += S::THREADS) {
-                const int row = (int)r0 + e / D, query = row / a.group, qh = w.head * a.group + row - query * a.group;
+                const int row = (int)r0 + e / D, query = a.query_of(row), qh = w.head * a.group + row - query * a.group;
                 static_cast<T*>(a.out)[(out0 + query) * a.out_stride + (long long)qh * D + e % D] = from_f<T>(0.f);
                 if (a.lse && e % D == 0) a.lse[(out0 + query) * a.heads + qh] = -INFINITY;
             }
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
         const int x = warp >> 2, r = (warp & 3) * 32 + lane, row = w.r0 + x * PT_ROWS + r;
         if (x < nm) {
             const bool on = row < R;
-            const int query = on ? row / a.group : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
+            const int query = on ? a.query_of(row) : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
             const int p = w.s.len - w.s.m + query;
             const int low = on && p >= 0 ? a.win.low(p) : 0, high = on && p >= 0 ? a.win.high(p, w.s.len) : 0;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;

@@ -468,6 +468,22 @@ def test_bad_ids_and_counts_give_zero_rows():
         assert (out[bad] == 0).all() and (lse[bad] == -np.inf).all()
 
 
+@pytest.mark.parametrize("left", [-1, 8])
+@pytest.mark.parametrize("max_new,rows", [(1, 9), (2, 40), (40, 300)])
+def test_counts_above_max_new_give_zero_rows(left, max_new, rows):
+    """Every row of such a sequence, however many tiles of rows it has."""
+    b = Both(dim=64, page=16)
+    b.append([0, 1], [30, 9])
+    q = torch.randn(rows + 1, 4, 64, device="cuda")
+    out = torch.full_like(q, 5.0)
+    _, lse = b.cache.attend(0, b.ids([0, 1]), q, starts=b.ids([0, 1, rows + 1]), max_new=max_new, att_left=left, out=out,
+                            lse=True)
+    with pytest.raises(b.native.CacError) as e:
+        b.cache.check()
+    assert e.value.code == BOUNDS
+    assert (out[1:] == 0).all() and (lse[1:] == -np.inf).all() and (out[0] != 5).any()
+
+
 def test_unlike_scales_of_blocks():
     """Blocks whose V values differ by many powers of two, and logits far apart."""
     b = Both(dim=64, page=16, dtype=F32)
