@@ -758,7 +758,11 @@ class Kv8Cache:
         self._c = CacKv8(L, H, D, PT, P, cfg.max_seqs, cfg.max_pages, 0 if cfg.code == "int8" else 1,
                          self.device.index, 0)
         self._ref = ctypes.addressof(self._c)
-        self._current = torch._C._cuda_getCurrentRawStream
+        self._torch, self._dev, self._current = torch, self.device.index, torch._C._cuda_getCurrentRawStream
+        self._i32, self._f32, self._bf16 = torch.int32, torch.float32, torch.bfloat16
+        lib = _lib()
+        self._extend, self._write, self._attend, self._truncate = (
+            lib.cac_kv8_extend, lib.cac_kv8_write, lib.cac_kv8_attend, lib.cac_kv8_truncate)
         self._space = {}   # workspace bytes of the calls seen, by their sizes
         ints = int(_lib().cac_kv8_work_ints(self._ref))
         if ints == 0:
@@ -786,41 +790,46 @@ class Kv8Cache:
         elif not {"table", "lens", "refs", "free", "n_free"} <= set(tensors):
             raise ValueError("adopted tensors include table, lens, refs, free and n_free")
 
+    # The checks below stand on the path of every call of a step, so they avoid what is slow in Python: building shape
+    # tuples and device objects, stream contexts, looking functions up.
     def _on(self, stream):
-        return stream.cuda_stream if stream is not None else self._current(self._c.device)
+        return stream.cuda_stream if stream is not None else self._current(self._dev)
 
     def _empty(self, stream, *specs):
         """Uninitialised tensors (shape, dtype) that belong to the stream that the call runs on."""
-        import torch
+        empty = self._torch.empty
         if stream is None:
-            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
-        with torch.cuda.stream(stream):
-            return [torch.empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
+            return [empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
+        with self._torch.cuda.stream(stream):
+            return [empty(shape, dtype=dt, device=self.device) for shape, dt in specs]
 
     def _ints(self, t, n, what):
-        import torch
-        if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or t.device != self.device or \
+        if t.dtype is not self._i32 or t.dim() != 1 or t.numel() != n or t.get_device() != self._dev or \
                 not t.is_contiguous():
             raise ValueError(f"{what}: a contiguous int32 tensor [{n}] on {self.device} is needed")
         return t.data_ptr()
 
     def _list(self, ids, starts):
-        n = ids.shape[0]
+        n = ids.numel()
         return n, self._ints(ids, n, "ids"), None if starts is None else self._ints(starts, n + 1, "starts")
 
-    def _act(self, t, heads, what, like=None):
+    def _act(self, t, heads, what):
         """Row stride and dtype code of an activation [rows, heads, head_dim]."""
-        import torch
-        if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != self.cfg.head_dim or t.device != self.device:
-            raise ValueError(f"{what}: a tensor [rows, {heads}, {self.cfg.head_dim}] on {self.device} is needed")
+        D = self._c.head_dim
+        if t.dim() != 3 or t.size(1) != heads or t.size(2) != D or t.get_device() != self._dev:
+            raise ValueError(f"{what}: a tensor [rows, {heads}, {D}] on {self.device} is needed")
         row, head, one = t.stride()
-        if one != 1 or (heads > 1 and head != t.shape[2]):
+        if one != 1 or (heads > 1 and head != D):
             raise ValueError(f"{what}: the heads of a row have to lie one after another")
-        if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        dt = t.dtype
+        if dt is not self._bf16 and dt is not self._f32:
             raise ValueError(f"{what}: bfloat16 or float32")
-        if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0]):
+        return (row if t.size(0) > 1 else heads * D), 1 if dt is self._bf16 else 0
+
+    @staticmethod
+    def _alike(t, like, what):
+        if t.dtype is not like.dtype or t.size(0) != like.size(0):
             raise ValueError(f"{what}: the type and rows of the other operand")
-        return (row if t.shape[0] > 1 else heads * t.shape[2]), 1 if t.dtype is torch.bfloat16 else 0
 
     def init(self, stream=None):
         """Empty the cache (cac_kv8_init)."""
@@ -829,15 +838,20 @@ class Kv8Cache:
     def extend(self, ids, each: int = 1, starts=None, max_new=None, stream=None):
         """Room for `each` (or starts[i+1] - starts[i]) new tokens of each sequence (cac_kv8_extend)."""
         n, p, s = self._list(ids, starts)
-        _check(_lib().cac_kv8_extend(self._ref, n, p, s, each, self._on(stream)), "cac_kv8_extend")
+        r = self._extend(self._ref, n, p, s, each, self._on(stream))
+        if r:
+            _check(r, "cac_kv8_extend")
 
     def write(self, layer: int, ids, k, v, starts=None, max_new=None, stream=None):
         """Quantise one layer's k, v [rows, kv_heads, head_dim] of the tokens of the last extend (cac_kv8_write)."""
         n, p, s = self._list(ids, starts)
-        ks, dt = self._act(k, self.cfg.kv_heads, "k")
-        vs, _ = self._act(v, self.cfg.kv_heads, "v", k)
-        _check(_lib().cac_kv8_write(self._ref, layer, n, p, s, k.shape[0], k.data_ptr(), v.data_ptr(), ks, vs, dt,
-                                    self._on(stream)), "cac_kv8_write")
+        heads = self._c.kv_heads
+        ks, dt = self._act(k, heads, "k")
+        vs, _ = self._act(v, heads, "v")
+        self._alike(v, k, "v")
+        r = self._write(self._ref, layer, n, p, s, k.size(0), k.data_ptr(), v.data_ptr(), ks, vs, dt, self._on(stream))
+        if r:
+            _check(r, "cac_kv8_write")
 
     def read(self, layer: int, ids, first, count: int, dtype=None, stream=None):
         """(k, v) [n, count, kv_heads, head_dim]: the values of tokens first[i] .. first[i] + count - 1 (cac_kv8_read)."""
@@ -856,42 +870,40 @@ class Kv8Cache:
                max_new=None, lse: bool = False, out=None, stream=None):
         """Attention of each sequence's last tokens, q [rows, heads, head_dim], over its cache (cac_kv8_attend);
         returns out, or (out, lse [rows, heads]).  scale: 1 / sqrt(head_dim) by default."""
-        import torch
         n, p, s = self._list(ids, starts)
-        rows, heads = q.shape[0], q.shape[1]
+        rows, heads = (q.size(0), q.size(1)) if q.dim() == 3 else (0, 0)
         qs, dt = self._act(q, heads, "q")
-        if starts is None:
+        if s is None:
             max_new = rows // n if n else 0
         elif max_new is None:
             max_new = rows
-        L = _lib()
         key = (n, rows, max_new, heads, att_left, att_chunk, sinks)
         need = self._space.get(key)
         if need is None:
             if len(self._space) >= 256:
                 self._space.clear()
-            need = self._space[key] = int(L.cac_kv8_attend_workspace(self._ref, *key))
-        specs = [(q.shape, q.dtype)] if out is None else []
-        if lse:
-            specs.append(((rows, heads), torch.float32))
-        if need:
-            specs.append(((need,), torch.uint8))
-        made = self._empty(stream, *specs)
-        space = made.pop() if need else None
-        sums = made.pop() if lse else None
+            need = self._space[key] = int(_lib().cac_kv8_attend_workspace(self._ref, *key))
+        D = self._c.head_dim
+        space = sums = None
         if out is None:
-            out, os_ = made[0], heads * self.cfg.head_dim
+            out, os_ = self._empty(stream, ((rows, heads, D), q.dtype))[0], heads * D
         else:
-            os_, _ = self._act(out, heads, "out", q)
-        _check(L.cac_kv8_attend(self._ref, layer, n, p, s, rows, max_new, heads,
-                                scale if scale is not None else self.cfg.head_dim ** -0.5, att_left, att_chunk, sinks,
-                                q.data_ptr(), qs, out.data_ptr(), os_, _ptr(sums), dt, _ptr(space), need,
-                                self._on(stream)), "cac_kv8_attend")
+            os_, _ = self._act(out, heads, "out")
+            self._alike(out, q, "out")
+        if lse:
+            sums = self._empty(stream, ((rows, heads), self._f32))[0]
+        if need:
+            space = self._empty(stream, ((need,), self._torch.uint8))[0]
+        r = self._attend(self._ref, layer, n, p, s, rows, max_new, heads, D ** -0.5 if scale is None else scale, att_left,
+                         att_chunk, sinks, q.data_ptr(), qs, out.data_ptr(), os_, None if sums is None else sums.data_ptr(),
+                         dt, None if space is None else space.data_ptr(), need, self._on(stream))
+        if r:
+            _check(r, "cac_kv8_attend")
         return (out, sums) if lse else out
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] becomes a copy of src[i] that shares its pages (cac_kv8_fork)."""
-        n = src.shape[0]
+        n = src.numel()
         _check(_lib().cac_kv8_fork(self._ref, n, self._ints(src, n, "src"), self._ints(dst, n, "dst"),
                                    self._on(stream)), "cac_kv8_fork")
 
@@ -899,8 +911,10 @@ class Kv8Cache:
         """Shorten to new_len tokens (an int, or int32 cuda tensor [n]); 0 frees the sequence (cac_kv8_truncate)."""
         n, p, _ = self._list(ids, None)
         one = isinstance(new_len, int)
-        _check(_lib().cac_kv8_truncate(self._ref, n, p, None if one else self._ints(new_len, n, "new_len"),
-                                       new_len if one else 0, self._on(stream)), "cac_kv8_truncate")
+        r = self._truncate(self._ref, n, p, None if one else self._ints(new_len, n, "new_len"), new_len if one else 0,
+                           self._on(stream))
+        if r:
+            _check(r, "cac_kv8_truncate")
 
     def trim(self, ids, att_left: int, att_chunk: int = 1, sinks: int = 0, stream=None):
         """Release the pages that no later query sees under this window (cac_kv8_trim)."""
