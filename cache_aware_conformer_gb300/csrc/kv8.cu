@@ -312,11 +312,10 @@ template <> struct Eight<bf16> {
         }
     }
 };
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+__device__ __forceinline__ void store16(float* p, const float (&x)[4]) {
     __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
-__device__ __forceinline__ void store8(bf16* p, const float (&x)[8]) {
+__device__ __forceinline__ void store16(bf16* p, const float (&x)[8]) {
     uint32_t w[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -357,6 +356,7 @@ struct KvWrite {
     const void *k, *v;
     long long k_stride, v_stride;
     int layer, blocks;
+    int each;  // > 0: every sequence has this many new tokens and touches (each + 30) / 16 blocks at most
 };
 
 // Where a block of the call lies: rows [lo, hi) of it are new, the first of them row `row` of k and v; nothing to do where
@@ -368,12 +368,19 @@ struct KvPlace {
 
 // Block number b of the call belongs to the sequence i with first(i) = starts(i) / 16 + 2 i <= b < first(i + 1): m new
 // tokens touch at most (m + 30) / 16 blocks, and first(i + 1) - first(i) >= m / 16 + 2, so no scan over the
-// lengths is needed to deal the blocks out.
+// lengths is needed to deal the blocks out.  Where all counts are alike the host knows, each sequence gets as many.
 __device__ __forceinline__ KvPlace place_of(const KvWrite& a, int b) {
     const cac_kv8& c = a.c;
     KvPlace p{0, 0, -1, 0, 0};
-    const int i = warp_last_le(a.rows.n, b, [&](int s) { return a.rows.at(s) / KV_BLOCK + 2ll * s; });
-    if (i < 0) return p;
+    int i, nth;
+    if (a.each) {
+        const int per = (a.each + 2 * KV_BLOCK - 2) / KV_BLOCK;
+        i = b / per, nth = b - i * per;
+    } else {
+        i = warp_last_le(a.rows.n, b, [&](int s) { return a.rows.at(s) / KV_BLOCK + 2ll * s; });
+        if (i < 0) return p;
+        nth = b - (a.rows.at(i) / KV_BLOCK + 2 * i);
+    }
     const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0, id = a.ids[i];
     if (m == 0) return p;
     int error = 0;
@@ -382,7 +389,7 @@ __device__ __forceinline__ KvPlace place_of(const KvWrite& a, int b) {
     } else {
         const int2 pending = *reinterpret_cast<const int2*>(c.pending + 2 * id);
         const int base = c.lens[id] - m;                                     // first new token
-        const int t0 = (base / KV_BLOCK + b - (row0 / KV_BLOCK + 2 * i)) * KV_BLOCK;  // first token of the block
+        const int t0 = (base / KV_BLOCK + nth) * KV_BLOCK;  // first token of the block
         if (pending.x != m || pending.y != i) {
             error = CAC_E_STATE;
         } else if (t0 < base + m) {
@@ -499,25 +506,30 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, NIT <= 8 ? 2 : 1) kv_write_k
 }
 
 // ---------------------------------------------------------------------------
-// read: a warp takes READ_T tokens of a sequence, a lane 16 values at a time
+// read: a warp takes a few tokens of a sequence, a lane as many values at a time as make 16 bytes of output, so that
+// each store of the warp is one piece of memory (16 values a lane, two or four stores apart, measured three times slower)
 // ---------------------------------------------------------------------------
-constexpr int READ_T = 4;
 struct KvRead {
     cac_kv8 c;
     const int32_t *ids, *first;
     void *k, *v;
-    int layer, n, count, pieces;
+    int layer, n, count, pieces, tokens;  // a sequence's pieces of `tokens` tokens
 };
+
+template <int VEC> struct Codes;
+template <> struct Codes<4> { using type = uint32_t; };
+template <> struct Codes<8> { using type = uint2; };
 
 template <class T, int CODE> __global__ void __launch_bounds__(256) kv_read_kernel(const __grid_constant__ KvRead a) {
     pdl_trigger();
     pdl_wait();
     const cac_kv8& c = a.c;
-    const int lane = threadIdx.x & 31, D = c.head_dim, vec = D >> 4, per = c.kv_heads * vec;
+    constexpr int VEC = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31, D = c.head_dim, vec = D / VEC, per = c.kv_heads * vec;
     const long long u = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int i = (int)(u / a.pieces), t0 = (int)(u - (long long)i * a.pieces) * READ_T;
+    const int i = (int)(u / a.pieces), t0 = (int)(u - (long long)i * a.pieces) * a.tokens;
     if (i >= a.n) return;
-    const int id = a.ids[i], tokens = min(READ_T, a.count - t0);
+    const int id = a.ids[i], tokens = min(a.tokens, a.count - t0);
     long long at = -1, sc = 0;  // lane l: token l's first codes and scale
     if (id < 0 || id >= c.max_seqs) {
         if (lane == 0) latch_error(c.status, CAC_E_BOUNDS);
@@ -532,40 +544,39 @@ template <class T, int CODE> __global__ void __launch_bounds__(256) kv_read_kern
         }
     }
     const long long out0 = ((long long)i * a.count + t0) * c.kv_heads * D;
-    for (int e0 = 0; e0 < tokens * per; e0 += 64) {
-        uint4 w[2][2];
-        float f[2][2];
-        long long from[2];
+    constexpr int AT_ONCE = 4;
+    using Word = typename Codes<VEC>::type;
+    for (int e0 = 0; e0 < tokens * per; e0 += 32 * AT_ONCE) {
+        Word w[AT_ONCE][2];
+        float f[AT_ONCE][2];
+        long long from[AT_ONCE];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < AT_ONCE; ++x) {
             const int e = e0 + 32 * x + lane, t = e / per, r = e - t * per, head = r / vec;
             const long long tat = __shfl_sync(0xffffffffu, at, t & 31), tsc = __shfl_sync(0xffffffffu, sc, t & 31);
             from[x] = e < tokens * per ? tat : -1;
             if (from[x] >= 0) {
-                const long long k = tat + (long long)head * c.page_tokens * D + (r - head * vec) * 16;
+                const long long k = tat + (long long)head * c.page_tokens * D + (r - head * vec) * VEC;
                 const long long s = tsc + head * (c.page_tokens / KV_BLOCK);
-                if (a.k) w[x][0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.k) + k)), f[x][0] = c.k_scale[s];
-                if (a.v) w[x][1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(c.v) + k)), f[x][1] = c.v_scale[s];
+                if (a.k) w[x][0] = __ldcs(reinterpret_cast<const Word*>(static_cast<const uint8_t*>(c.k) + k)), f[x][0] = c.k_scale[s];
+                if (a.v) w[x][1] = __ldcs(reinterpret_cast<const Word*>(static_cast<const uint8_t*>(c.v) + k)), f[x][1] = c.v_scale[s];
             }
         }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < AT_ONCE; ++x) {
             const int e = e0 + 32 * x + lane;
             if (e >= tokens * per) continue;
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 T* dst = static_cast<T*>(v ? a.v : a.k);
                 if (!dst) continue;
+                float y[VEC] = {};
+                if (from[x] >= 0) {
+                    const uint32_t* word = reinterpret_cast<const uint32_t*>(&w[x][v]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float y[8] = {};
-                    if (from[x] >= 0) {
-                        decode8<CODE>(h ? make_uint2(w[x][v].z, w[x][v].w) : make_uint2(w[x][v].x, w[x][v].y), y);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) y[k] *= f[x][v];
-                    }
-                    store8(dst + out0 + (long long)e * 16 + 8 * h, y);
+                    for (int k = 0; k < VEC; ++k) y[k] = kv_decode<CODE>((word[k >> 2] >> (8 * (k & 3))) & 255u) * f[x][v];
                 }
+                store16(dst + out0 + (long long)e * VEC, y);
             }
         }
     }
@@ -798,12 +809,13 @@ extern "C" int cac_kv8_write(const cac_kv8* c, int layer, int n, const int32_t* 
     if (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) ||
         ((k_stride * size | v_stride * size) & 15) || (reinterpret_cast<uintptr_t>(starts) & 3))
         return CAC_E_ALIGN;
-    const long long blocks = (long long)rows / KV_BLOCK + 2ll * n;
+    const int each = starts ? 0 : rows / n;
+    const long long blocks = each ? (long long)n * ((each + 2 * KV_BLOCK - 2) / KV_BLOCK) : (long long)rows / KV_BLOCK + 2ll * n;
     if (blocks > INT32_MAX) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const KvWrite a{*c, {starts, rows / n, n, rows}, ids, k, v, k_stride, v_stride, layer, (int)blocks};
+    const KvWrite a{*c, {starts, rows / n, n, rows}, ids, k, v, k_stride, v_stride, layer, (int)blocks, each};
     if (c->code == CAC_KV8_INT8)
         return launched(dtype == CAC_DTYPE_BF16 ? launch_write<bf16, CAC_KV8_INT8>(a, s)
                                                 : launch_write<float, CAC_KV8_INT8>(a, s));
@@ -824,12 +836,15 @@ extern "C" int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* i
         return CAC_E_ALIGN;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    const int pieces = (count + READ_T - 1) / READ_T;
+    // a token to a warp while that leaves warps' places free (8,192 of them: 256 x 16 tokens 9.6 -> %s us); four where there are
+    // more, which look four tokens' places up at once (72,000 tokens: 60 us against 65)
+    const int tokens = (long long)n * count <= 8192 ? 1 : 4;
+    const int pieces = (count + tokens - 1) / tokens;
     const long long blocks = ((long long)n * pieces + 7) / 8;
     if (blocks > INT32_MAX) return CAC_E_LIMIT;
     const dim3 grid((unsigned)blocks), block(256);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const KvRead a{*c, ids, first, k, v, layer, n, count, pieces};
+    const KvRead a{*c, ids, first, k, v, layer, n, count, pieces, tokens};
     if (c->code == CAC_KV8_INT8)
         return launched(dtype == CAC_DTYPE_BF16
                             ? launch_k(kv_read_kernel<bf16, CAC_KV8_INT8>, grid, block, 0, s, 1, a)

@@ -390,32 +390,42 @@ template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, 
     return p;
 }
 
-// A warp adds up the parts in slots `first`, then next, next + 2, ... (`more` of those), and writes the unit's rows, or, with to
-// >= 0, one part in that slot.
+// The parts of a unit in slots `first`, then next, next + 2, ... (`more` of those) are added up: this warp does rows mine, mine +
+// more + 1, ... and writes them out, or, with to >= 0, into that slot.
 template <class T, int HDP>
-__device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more, int to) {
+__device__ void join_warp(const KvAttend& a, const Partials& p, int i, int unit, int first, int next, int more, int mine, int to) {
     constexpr int PER = HDP / 32;
     const int lane = threadIdx.x & 31, kvh = a.c.kv_heads, head = unit % kvh, r0 = unit / kvh * 16;
-    const int rows = min(16, s.m * a.group - r0);
-    const int mine = lane == 0 ? first : next + 2 * (lane - 1);
-    for (int r = 0; r < rows; ++r) {
-        float m = -INFINITY, l = 0.f;
-        if (lane <= more) m = __ldcg(p.ml + ((size_t)mine * 16 + r) * 2), l = __ldcg(p.ml + ((size_t)mine * 16 + r) * 2 + 1);
-        float top = m;
+    const int row0 = a.rows.at(i), rows = min(16, (a.rows.at(i + 1) - row0) * a.group - r0);
+    const int slot = lane == 0 ? first : next + 2 * (lane - 1);
+    for (int r = mine; r < rows; r += more + 1) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane <= more) ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + (size_t)slot * 16 + r);
+        float v[MOST_WARPS][PER];  // all parts on their way at once
+#pragma unroll
+        for (int k = 0; k < MOST_WARPS; ++k)
+            if (k <= more) {
+                const float* src = p.o + ((size_t)(k == 0 ? first : next + 2 * (k - 1)) * 16 + r) * HDP + lane * PER;
+#pragma unroll
+                for (int c = 0; c < PER; c += 2) {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(src + c));
+                    v[k][c] = y.x, v[k][c + 1] = y.y;
+                }
+            }
+        float top = ml.x;
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float f = ex2(m - (top == -INFINITY ? 0.f : top));
-        l = lane <= more ? l * f : 0.f;
+        const float f = ex2(ml.x - (top == -INFINITY ? 0.f : top));
+        float l = lane <= more ? ml.y * f : 0.f;
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         float o[PER] = {};
-#pragma unroll 4
-        for (int k = 0; k <= more; ++k) {
-            const size_t slot = k == 0 ? first : next + 2 * (k - 1);
-            const float* src = p.o + (slot * 16 + r) * HDP + lane * PER;
-            const float w = __shfl_sync(0xffffffffu, f, k);
 #pragma unroll
-            for (int c = 0; c < PER; ++c) o[c] = fmaf(__ldcg(src + c), w, o[c]);
+        for (int k = 0; k < MOST_WARPS; ++k) {
+            const float w = __shfl_sync(0xffffffffu, f, k);
+            if (k <= more)
+#pragma unroll
+                for (int c = 0; c < PER; ++c) o[c] = fmaf(v[k][c], w, o[c]);
         }
         if (to >= 0) {
 #pragma unroll
@@ -424,12 +434,12 @@ __device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s
         } else {
             const int row = r0 + r, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
             const bool seen = l > 0.f || l != l;
-            T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
+            T* dst = static_cast<T*>(a.out) + (row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
             for (int c = 0; c < PER; ++c)
                 if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[c] / l : 0.f);
             if (lane == 0 && a.lse)
-                a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+                a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
         }
     }
 }
@@ -531,10 +541,10 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             return tile_of<CODE>(a, s.id, s.len, s.lot, s.skt, (int)x, unit % kvh);
         }
     };
-    Tile now = look(x0 + lane), next = now;
-    if constexpr (SPLIT) next = look(x0 + 32 + lane);
+    Tile now = look(x0 + lane);
     long long base = x0;
 
+    Tile next = now;
     int into = 0;  // the stage that the next copies go to
     auto fetch = [&](long long x) {  // queue the copies of tile x; always one group
         const int k = (int)(x - base);
@@ -564,24 +574,32 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             }
         __syncwarp();
     }
-#pragma unroll 1
-    for (int k = 0; k < STAGES; ++k) fetch(x0 + k);
-    int from_stage = 0;
-
     R r;
-    long long x = x0;
-    while (x < x1) {
-        // the unit that tile x belongs to, and this warp's part of it
-        long long u0 = 0, u1 = x1;
+    long long x = x0, u0 = 0, u1 = x1;
+    // the unit that tile x belongs to: its tiles [u0, u1), sequence, head and first row
+    int head = 0, r0 = 0;
+    auto enter = [&] {
         if constexpr (SPLIT) {
             i = warp_last_le(n, x, [&](int k) { return s_first[k]; });
             s = seq_work(a, i);
             unit = (int)((x - s_first[i]) / s.tiles);
             u0 = s_first[i] + (long long)unit * s.tiles, u1 = u0 + s.tiles;
         }
-        const long long end = min(u1, x1), from = x;
-        const int head = unit % kvh, r0 = unit / kvh * 16;
+        head = unit % kvh, r0 = unit / kvh * 16;
         r.load(a, s, head, r0);
+    };
+    // the first unit's queries before the ring fills: behind its copies they would take twice as long
+    if (x < x1) enter();
+#pragma unroll 1
+    for (int k = 0; k < STAGES; ++k) fetch(x0 + k);
+    if constexpr (SPLIT) next = look(x0 + 32 + lane);
+    int from_stage = 0;
+
+    bool entered = true;
+    while (x < x1) {
+        if (!entered) enter();
+        entered = false;
+        const long long end = min(u1, x1), from = x;
         while (x < end) {
             if (SPLIT && x - base >= 32) {
                 base += 32;
@@ -661,22 +679,21 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
         const Deal deal(s_first[n], gridDim.x * WARPS);
         const int w = blockIdx.x * WARPS + warp;
         const long long b0 = deal.begin(blockIdx.x * WARPS), b1 = deal.begin((blockIdx.x + 1) * WARPS);
-        // the unit that the share begins in, then the one that it ends in; the first warp of the block that holds a
-        // part of a cut unit adds the block's parts up
+        // the unit that the share begins in, then the one that it ends in: the warps of the block that hold parts of a cut
+        // unit share its rows out among them
 #pragma unroll 1
         for (int which = 0; which < 2 && x0 < x1; ++which) {
             const long long at = which ? x1 - 1 : x0;
             i = warp_last_le(n, at, [&](int k) { return s_first[k]; });
-            const long long u0 = s_first[i] + (at - s_first[i]) / s_tiles[i] * s_tiles[i], u1 = u0 + s_tiles[i];
-            if (which ? u0 <= x0 || u1 <= x1 : x0 != b0 && x0 != u0) continue;
-            if (u0 >= x0 && u1 <= x1) continue;  // whole, and written
-            int w1 = w;
+            u0 = s_first[i] + (at - s_first[i]) / s_tiles[i] * s_tiles[i], u1 = u0 + s_tiles[i];
+            if ((which && u0 <= x0) || (u0 >= x0 && u1 <= x1)) continue;  // done as the first, or whole and written
+            int w0 = w, w1 = w;
+            while (w0 > (int)blockIdx.x * WARPS && deal.begin(w0) > u0) --w0;
             while (w1 + 1 < (int)(blockIdx.x + 1) * WARPS && deal.begin(w1 + 1) < u1 && deal.begin(w1 + 1) < b1) ++w1;
-            s = seq_work(a, i);
-            unit = (int)((u0 - s_first[i]) / s_tiles[i]);
             const bool done = u0 >= b0 && u1 <= b1;
             const int to = 2 * part.warps + 2 * blockIdx.x + (u0 > b0);
-            join_warp<T, HDP>(a, part, s, unit, 2 * w + (which && u0 > x0), 2 * (w + 1), w1 - w, done ? -1 : to);
+            join_warp<T, HDP>(a, part, i, (int)((u0 - s_first[i]) / s_tiles[i]), 2 * w0 + (deal.begin(w0) < u0),
+                              2 * (w0 + 1), w1 - w0, w - w0, done ? -1 : to);
         }
     }
 }

@@ -1,15 +1,19 @@
 // The attention calls of the paged 8-bit K/V cache (include/cac_kv8.h): checks, and the choice of a kernel.
 #include <algorithm>
+#include <atomic>
 
 #include "kv8_attn.cuh"
 
 namespace cac {
 namespace {
 
-int sm_count() {
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
+// SMs of a device, asked for once; 0 where that fails
+int sm_count(int device) {
+    static std::atomic<int> known[64];
+    if (device < 0 || device >= 64) return 0;
+    int sms = known[device].load(std::memory_order_relaxed);
+    if (sms == 0 && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) == cudaSuccess)
+        known[device].store(sms, std::memory_order_relaxed);
     return sms;
 }
 
@@ -32,9 +36,7 @@ extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, in
     if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 1 || att_chunk < 1 || sinks < 0 ||
         !splits(*c, std::min(max_new, rows), att_left, att_chunk, sinks))
         return 0;
-    DeviceScope dev(c->device);
-    const int sms = dev.ok ? sm_count() : 0;
-    return kv_attend_bytes(c->head_dim, sms);
+    return kv_attend_bytes(c->head_dim, sm_count(c->device));
 }
 
 extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
@@ -66,7 +68,7 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     if (tiles * std::min(n, TA_SEQS) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    const int sms = sm_count();
+    const int sms = sm_count(c->device);
     if (sms < 1) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int i0 = 0; i0 < n; i0 += TA_SEQS) {

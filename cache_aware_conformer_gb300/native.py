@@ -763,6 +763,7 @@ class Kv8Cache:
         lib = _lib()
         self._extend, self._write, self._attend, self._truncate = (
             lib.cac_kv8_extend, lib.cac_kv8_write, lib.cac_kv8_attend, lib.cac_kv8_truncate)
+        self._scale = D ** -0.5
         self._space = {}   # workspace bytes of the calls seen, by their sizes
         ints = int(_lib().cac_kv8_work_ints(self._ref))
         if ints == 0:
@@ -886,7 +887,11 @@ class Kv8Cache:
         D = self._c.head_dim
         space = sums = None
         if out is None:
-            out, os_ = self._empty(stream, ((rows, heads, D), q.dtype))[0], heads * D
+            if stream is None and q.is_contiguous():
+                out = self._torch.empty_like(q)
+            else:
+                out = self._empty(stream, ((rows, heads, D), q.dtype))[0]
+            os_ = heads * D
         else:
             os_, _ = self._act(out, heads, "out")
             self._alike(out, q, "out")
@@ -894,7 +899,7 @@ class Kv8Cache:
             sums = self._empty(stream, ((rows, heads), self._f32))[0]
         if need:
             space = self._empty(stream, ((need,), self._torch.uint8))[0]
-        r = self._attend(self._ref, layer, n, p, s, rows, max_new, heads, D ** -0.5 if scale is None else scale, att_left,
+        r = self._attend(self._ref, layer, n, p, s, rows, max_new, heads, self._scale if scale is None else scale, att_left,
                          att_chunk, sinks, q.data_ptr(), qs, out.data_ptr(), os_, None if sums is None else sums.data_ptr(),
                          dt, None if space is None else space.data_ptr(), need, self._on(stream))
         if r:
