@@ -165,10 +165,8 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
             }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            // 2^(14 - floor(log2 amax)), within the exponents that fp32 has
-            const int e = min(268 - (int)(__float_as_uint(amax) >> 23), 254);
-            const float up = __uint_as_float((uint32_t)e << 23);
-            f[h] = a.scale * LOG2E * __uint_as_float((uint32_t)max(254 - e, 1) << 23) * (e == 254 ? 0.5f : 1.f);
+            const float up = lift_to_half(amax);
+            f[h] = a.scale * LOG2E / up;  // a power of two: exact
 #pragma unroll
             for (int k = 0; k < STEPS; ++k) {
                 q[k][h] = pack_half(x[k][0] * up, x[k][1] * up);

@@ -36,6 +36,10 @@ __device__ __forceinline__ uint32_t pack_rest(float a, float b, uint32_t hi) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
     return pack_half(a - f.x, b - f.y);
 }
+// The power of two that brings a row's largest value between 2^14 and 2^15, as far as fp32's exponents go
+__device__ __forceinline__ float lift_to_half(float amax) {
+    return __uint_as_float((uint32_t)min(268 - (int)(__float_as_uint(amax) >> 23), 254) << 23);
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -233,57 +233,62 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             const int low = on && p >= 0 ? a.win.low(p) : 0, high = on && p >= 0 ? a.win.high(p, w.s.len) : 0;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t col_s = tmem + lanes + S::COL_S + x * 128, col_o = tmem + lanes + S::COL_O + x * HDP;
-            // the row's queries: largest value under 2^15, then fp16 (hi, lo)
-            float f;
+            // The warp's 32 rows of queries: largest value of a row under 2^15, then fp16 (hi, lo).  CPR lanes load a row, 16 bytes
+            // each (a thread per row would touch 32 lines of memory with every load).
+            float amax = 0.f;
             {
-                const T* src = static_cast<const T*>(a.q) + (out0 + query) * a.q_stride + (long long)qh * D;
-                constexpr int VEC = 16 / sizeof(T), STEP = 32;  // values of a 16-byte load; values at a time (twice: the second from L1)
-                float y[STEP];
-                auto get = [&](int e0) {
+                constexpr int VEC = 16 / sizeof(T), CPR = HDP / VEC, RPI = 32 / CPR;
+                const int c = lane & (CPR - 1), first = x * PT_ROWS + (warp & 3) * 32;
+                uint8_t* dst0 = smem + x * S::PARTS * S::TILE + (c * VEC >> 6) * S::PANEL;
+                constexpr int GROUP = 8;  // loads on their way at once
+#pragma unroll 1
+                for (int it0 = 0; it0 < CPR; it0 += GROUP) {
+                    uint4 raw[GROUP];
 #pragma unroll
-                    for (int c = 0; c < STEP; c += VEC) {
-                        const uint4 q = on && e0 + c < D ? *reinterpret_cast<const uint4*>(src + e0 + c) : make_uint4(0, 0, 0, 0);
-                        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                    for (int k = 0; k < GROUP; ++k) {
+                        const int row = w.r0 + first + (it0 + k) * RPI + lane / CPR, q = a.query_of(row);
+                        const T* src = static_cast<const T*>(a.q) + (out0 + q) * a.q_stride +
+                                       (long long)(w.head * a.group + row - q * a.group) * D + c * VEC;
+                        raw[k] = row < R && c * VEC < D ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+                    }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < GROUP; ++k) {
+                        const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                        float y[VEC], mx = 0.f;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
                             if constexpr (S::WIDE) {
-                                y[c + k] = __uint_as_float(u[k]);
+                                y[b] = __uint_as_float(u[b]);
                             } else {
-                                y[c + 2 * k] = __uint_as_float(u[k] << 16);
-                                y[c + 2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+                                y[2 * b] = __uint_as_float(u[b] << 16);
+                                y[2 * b + 1] = __uint_as_float(u[b] & 0xffff0000u);
                             }
                         }
-                    }
-                };
-                float amax = 0.f;
-#pragma unroll 2
-                for (int e0 = 0; e0 < HDP; e0 += STEP) {
-                    get(e0);
 #pragma unroll
-                    for (int k = 0; k < STEP; ++k) amax = fmaxf(amax, fabsf(y[k]));
-                }
-                const int e = min(268 - (int)(__float_as_uint(amax) >> 23), 254);
-                const float up = __uint_as_float((uint32_t)e << 23) * (a.scale < 0.f ? -1.f : 1.f);
-                f = fabsf(a.scale) * LOG2E * __uint_as_float((uint32_t)max(254 - e, 1) << 23) * (e == 254 ? 0.5f : 1.f);
-#pragma unroll 1
-                for (int e0 = 0; e0 < HDP; e0 += STEP) {
-                    get(e0);
+                        for (int b = 0; b < VEC; ++b) mx = fmaxf(mx, fabsf(y[b]));
 #pragma unroll
-                    for (int k8 = 0; k8 < STEP / 8; ++k8) {
-                        const int c = e0 / 8 + k8;
-                        uint32_t hi[4], lo[4];
+                        for (int d = CPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float of_mine = __shfl_sync(0xffffffffu, mx, (lane & (RPI - 1)) * CPR);
+                        if (lane / RPI == it0 + k) amax = of_mine;
+                        const float up = lift_to_half(mx) * (a.scale < 0.f ? -1.f : 1.f);
+                        const int rr = (warp & 3) * 32 + (it0 + k) * RPI + lane / CPR;
+                        uint8_t* dst = dst0 + rr * 128 + (((c * VEC >> 3 & 7) ^ (rr & 7)) << 4);
+                        uint32_t hi[VEC / 2], lo[VEC / 2];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float y0 = y[8 * k8 + 2 * k] * up, y1 = y[8 * k8 + 2 * k + 1] * up;
-                            hi[k] = pack_half(y0, y1);
-                            if constexpr (S::WIDE) lo[k] = pack_rest(y0, y1, hi[k]);
+                        for (int b = 0; b < VEC / 2; ++b) {
+                            hi[b] = pack_half(y[2 * b] * up, y[2 * b + 1] * up);
+                            if constexpr (S::WIDE) lo[b] = pack_rest(y[2 * b] * up, y[2 * b + 1] * up, hi[b]);
                         }
-                        uint8_t* dst = smem + x * S::PARTS * S::TILE + (c >> 3) * S::PANEL + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-                        *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        if constexpr (S::WIDE) *reinterpret_cast<uint4*>(dst + S::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        if constexpr (S::WIDE) {
+                            *reinterpret_cast<uint2*>(dst + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(dst + S::TILE + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        }
                     }
                 }
             }
+            const float f = fabsf(a.scale) * LOG2E / lift_to_half(amax);  // a power of two: exact
             fence_proxy_async_smem();
             warp_arrive(q_full);
 
@@ -455,7 +460,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
         };
         uint4 raw[2][NL];
         load(cw, __shfl_sync(0xffffffffu, here.at, 0), raw[0]);
-        Spot then = look(cw + S::CONV * (32 + lane));
+        Spot then = here;
         int q = 0;  // the piece's place among the 32
         auto piece = [&](int n, uint4 (&cur)[NL], uint4 (&nxt)[NL]) {
             const float ks = __shfl_sync(0xffffffffu, here.ks, q), lv = __shfl_sync(0xffffffffu, here.lv, q),
@@ -463,8 +468,8 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             if (++q == 32) {
                 q = 0;
                 here = then;
-                then = look(n + S::CONV * (33 + lane));
             }
+            if (q == 8) then = look(n + S::CONV * (25 + lane));  // the 32 after these: not before the first are on their way
             load(n + S::CONV, __shfl_sync(0xffffffffu, here.at, q), nxt);
             const int j = n >> 4, st = j & 1, block = n & 7;
             const bool v = n & 8;
