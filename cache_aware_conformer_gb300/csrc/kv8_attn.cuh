@@ -82,7 +82,8 @@ extern template cudaError_t kv_launch_attend<CAC_KV8_INT8>(const KvAttend&, int,
 extern template cudaError_t kv_launch_attend<CAC_KV8_E4M3>(const KvAttend&, int, bool, int, int, void*, cudaStream_t);
 size_t kv_attend_bytes(int head_dim, int sms);
 // kv8_prompt.cu
-bool kv_prompt_takes(const KvAttend& a, int dtype);
+// whether it takes a call whose sequences have `rows` query rows to a K/V head on average
+bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows);
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s);
 
 }  // namespace cac

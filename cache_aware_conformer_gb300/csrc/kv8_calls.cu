@@ -17,12 +17,14 @@ int sm_count(int device) {
     return sms;
 }
 
-// Whether units are cut: not where the window leaves at most SHORT tiles to any of them.
-constexpr int SHORT = 16;
-bool splits(const cac_kv8& c, int max_new, int left, int chunk, int sinks) {
+// Whether units are cut and dealt out, or a warp takes a whole one: the latter saves the deal and the join, but takes about 0.45 us
+// a tile.  Measured (2 bf16 queries, windows of 220 / 450 / 900 tokens, us): 16 sequences of 8 heads 11.5 / 18.7 / 31.8 whole, 22.9 /
+// 24.1 / 24.8 dealt out; 256 sequences 18.0 / 32.8 / 56.5 and 36.3 / 52.5 / 75.4.
+bool splits(const cac_kv8& c, int n, int sms, int max_new, int left, int chunk, int sinks) {
     long long tokens = (long long)c.max_pages * c.page_tokens;
     if (left >= 0) tokens = std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);
-    return tokens > SHORT * KV_BLOCK;
+    const int tiles = (long long)n * c.kv_heads >= 8ll * sms ? 64 : 36;
+    return tokens > tiles * KV_BLOCK;
 }
 
 }  // namespace
@@ -34,7 +36,7 @@ extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, in
                                            int att_chunk, int sinks) {
     (void)heads;
     if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 1 || att_chunk < 1 || sinks < 0 ||
-        !splits(*c, std::min(max_new, rows), att_left, att_chunk, sinks))
+        !splits(*c, n, sm_count(c->device), std::min(max_new, rows), att_left, att_chunk, sinks))
         return 0;
     return kv_attend_bytes(c->head_dim, sm_count(c->device));
 }
@@ -59,7 +61,9 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
         ((q_stride * size | out_stride * size) & 15) || (words & 3))
         return CAC_E_ALIGN;
     const int group = heads / c->kv_heads, most = starts ? std::min(max_new, rows) : rows / n;
-    const bool split = splits(*c, most, att_left, att_chunk, sinks);
+    const int sms = sm_count(c->device);
+    if (sms < 1) return CAC_E_CUDA;
+    const bool split = splits(*c, n, sms, most, att_left, att_chunk, sinks);
     if (split && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
                   workspace_bytes < cac_kv8_attend_workspace(c, n, rows, most, heads, att_left, att_chunk, sinks)))
         return CAC_E_INVAL;
@@ -68,15 +72,14 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     if (tiles * std::min(n, TA_SEQS) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    const int sms = sm_count(c->device);
-    if (sms < 1) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int i0 = 0; i0 < n; i0 += TA_SEQS) {
         const int each = rows / n, part = std::min(n - i0, TA_SEQS);
         const KvAttend a{*c, {starts ? starts + i0 : nullptr, each, part, rows, each * i0}, {att_left, att_chunk, sinks},
-                         ids + i0, q, out, lse, q_stride, out_stride, scale, layer, heads, group, most, group > 1 ? (uint32_t)((1ull << 32) / group) + 1 : 0u};
+                         ids + i0, q, out, lse, q_stride, out_stride, scale, layer, heads, group, most,
+                         group > 1 ? (uint32_t)((1ull << 32) / group) + 1 : 0u};
         cudaError_t e;
-        if (kv_prompt_takes(a, dtype))
+        if (kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
             e = kv_launch_prompt(a, dtype, s);
         else
             e = c->code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, split, (int)tiles, sms, workspace, s)

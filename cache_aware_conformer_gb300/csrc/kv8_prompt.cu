@@ -582,9 +582,17 @@ template <class T, int CODE> cudaError_t launch_prompt(const KvAttend& a, cudaSt
 
 }  // namespace
 
-bool kv_prompt_takes(const KvAttend& a, int dtype) {
-    (void)dtype;
-    return a.c.head_dim <= 128 && (long long)a.max_new * a.group > 32;
+// Against kv_attend_kernel, which deals 16-row tiles out over the whole card (and re-reads K and V for each): a 128-token tile of a
+// block here takes as long as it takes an SM for 2.6 of its 16-row tiles, but the card fills in steps of a block an SM.  Measured
+// (bf16, group 4, head_dim 128; us for 16 / 32 / 64 / 128 / 256 rows): 32 sequences of 4,000 tokens, 8 K/V heads,
+// 110 / 155 / 249 / 436 / 801 there, 155 / 155 / 153 / 154 / 170 here; 4 of 8,000, 47 / 68 / 99 / 147 / 240 and 128 / 127 /
+// 127 / 121 / 140; one of 30,000, 2 heads, 39 / 35 / 40 / 51 / 77 and 454 / 454 / 455 / 424 / 489.  The ratio at the crossings is 1.5 to 1.7.
+bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows) {
+    if (a.c.head_dim > 128) return false;
+    const int block = dtype == CAC_DTYPE_F32 && a.c.head_dim > 64 ? PT_ROWS : 2 * PT_ROWS;
+    const long long units = (long long)a.rows.n * a.c.kv_heads;
+    const long long waves = (units * ((rows + block - 1) / block) + sms - 1) / sms;
+    return units * ((rows + 15) / 16) * 5 > waves * sms * 8;
 }
 
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s) {
