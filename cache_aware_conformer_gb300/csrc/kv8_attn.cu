@@ -69,7 +69,7 @@ template <int HDP> __device__ __forceinline__ int tile_at(int r, int c) {
 
 struct Tile {
     long long at;              // its codes (K and V alike), -1: nothing there
-    float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale, all for codes as half4 gives them
+    float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale
     int j0;                    // its first token
 };
 template <int CODE>
@@ -82,8 +82,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttend& a, int id, int len, int 
             const int in_page = t.j0 % a.c.page_tokens;
             const long long sc = kv_scale_at(a.c, a.layer, page, head) + in_page / KV_BLOCK;
             t.at = kv_head_at(a.c, a.layer, page, head) + (long long)in_page * a.c.head_dim;
-            t.ks = a.c.k_scale[sc] * code_unit<CODE>();
-            t.lv = log2f(a.c.v_scale[sc]) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
+            t.ks = a.c.k_scale[sc];
+            t.lv = log2f(a.c.v_scale[sc]);
             t.iv = ex2(-t.lv);  // of the rounded logarithm, so that weight and norm have the same factor
         }
     }
@@ -293,6 +293,11 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                         const uint4 e = *reinterpret_cast<const uint4*>(at);
                         w[y][0] = e.x, w[y][1] = e.y, w[y][2] = e.z, w[y][3] = e.w;
                     }
+                    if (CODE == CAC_KV8_E4M3 && d[u].j0 + KV_BLOCK > hi_max && d[u].j0 + t + 4 * y >= hi_max) {
+                        // a token past the end: its codes may be anything, and a weight of 0 times NaN is NaN
+#pragma unroll
+                        for (int x = 0; x < PER / 4; ++x) w[y][x] = 0;
+                    }
                 }
 #pragma unroll
                 for (int x = 0; x < PER / 4; ++x)
@@ -356,14 +361,17 @@ constexpr int LEAST = 4;
 struct Deal {
     long long total;
     int warps;
+    long long share;    // tiles of a share; the first `over` have one more
+    int over;
     __device__ __forceinline__ Deal(long long tiles, int most)
-        : total(tiles), warps(tiles >= (long long)most * LEAST ? most : max((int)(tiles / LEAST), 1)) {}
-    __device__ __forceinline__ long long begin(int w) const { return w < warps ? total * w / warps : total; }
+        : total(tiles), warps(tiles >= (long long)most * LEAST ? most : max((int)(tiles / LEAST), 1)) {
+        share = total / warps;
+        over = (int)(total - share * warps);
+    }
+    __device__ __forceinline__ long long begin(int w) const { return w < warps ? share * w + min(w, over) : total; }
     __device__ __forceinline__ int owner(long long x) const {
-        int w = (int)(x * warps / total);
-        while (begin(w) > x) --w;
-        while (begin(w + 1) <= x) ++w;
-        return w;
+        const long long head = (share + 1) * over;
+        return (int)(x < head ? x / (share + 1) : over + (x - head) / share);
     }
 };
 
@@ -391,10 +399,10 @@ template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, 
 // The parts of a unit in slots `first`, then next, next + 2, ... (`more` of those) are added up: this warp does rows mine, mine +
 // more + 1, ... and writes them out, or, with to >= 0, into that slot.
 template <class T, int HDP>
-__device__ void join_warp(const KvAttend& a, const Partials& p, int i, int unit, int first, int next, int more, int mine, int to) {
+__device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more, int mine, int to) {
     constexpr int PER = HDP / 32;
     const int lane = threadIdx.x & 31, kvh = a.c.kv_heads, head = unit % kvh, r0 = unit / kvh * 16;
-    const int row0 = a.rows.at(i), rows = min(16, (a.rows.at(i + 1) - row0) * a.group - r0);
+    const int rows = min(16, s.m * a.group - r0);
     const int slot = lane == 0 ? first : next + 2 * (lane - 1);
     for (int r = mine; r < rows; r += more + 1) {
         float2 ml = make_float2(-INFINITY, 0.f);
@@ -432,12 +440,12 @@ __device__ void join_warp(const KvAttend& a, const Partials& p, int i, int unit,
         } else {
             const int row = r0 + r, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
             const bool seen = l > 0.f || l != l;
-            T* dst = static_cast<T*>(a.out) + (row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
+            T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
             for (int c = 0; c < PER; ++c)
                 if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[c] / l : 0.f);
             if (lane == 0 && a.lse)
-                a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+                a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
         }
     }
 }
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ long long s_first[SPLIT ? TA_SEQS + 1 : 1];
     __shared__ long long s_part[WARPS];
-    __shared__ int s_tiles[SPLIT ? TA_SEQS : 1], s_lot[SPLIT ? TA_SEQS : 1], s_skt[SPLIT ? TA_SEQS : 1];
+    __shared__ SeqWork s_seq[SPLIT ? TA_SEQS : 1];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n = a.rows.n, kvh = a.c.kv_heads;
@@ -483,7 +491,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             long long mine = 0;
             if (k < n) {
                 const SeqWork w = seq_work(a, k);
-                s_tiles[k] = w.tiles, s_lot[k] = w.lot, s_skt[k] = w.skt;
+                s_seq[k] = w;
                 mine = (long long)w.tiles * kvh * ((w.m * a.group + 15) / 16);
             }
             long long sum = mine;
@@ -530,11 +538,10 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
                 if (s_first[mid] <= x) lo = mid;
                 else hi = mid - 1;
             }
-            const int id = a.ids[lo];
-            const bool ok = id >= 0 && id < a.c.max_seqs && a.rows.at(lo + 1) - a.rows.at(lo) <= a.max_new;
+            const SeqWork& w = s_seq[lo];
             const long long in = x - s_first[lo];
-            const int u = (int)(in / s_tiles[lo]), kt = (int)(in - (long long)u * s_tiles[lo]);
-            return tile_of<CODE>(a, id, ok ? a.c.lens[id] : 0, s_lot[lo], s_skt[lo], kt, u % kvh);
+            const int u = (int)(in / w.tiles), kt = (int)(in - (long long)u * w.tiles);
+            return tile_of<CODE>(a, w.id, w.len, w.lot, w.skt, kt, u % kvh);
         } else {
             return tile_of<CODE>(a, s.id, s.len, s.lot, s.skt, (int)x, unit % kvh);
         }
@@ -579,7 +586,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
     auto enter = [&] {
         if constexpr (SPLIT) {
             i = warp_last_le(n, x, [&](int k) { return s_first[k]; });
-            s = seq_work(a, i);
+            s = s_seq[i];
             unit = (int)((x - s_first[i]) / s.tiles);
             u0 = s_first[i] + (long long)unit * s.tiles, u1 = u0 + s.tiles;
         }
@@ -683,14 +690,16 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
         for (int which = 0; which < 2 && x0 < x1; ++which) {
             const long long at = which ? x1 - 1 : x0;
             i = warp_last_le(n, at, [&](int k) { return s_first[k]; });
-            u0 = s_first[i] + (at - s_first[i]) / s_tiles[i] * s_tiles[i], u1 = u0 + s_tiles[i];
+            s = s_seq[i];
+            unit = (int)((at - s_first[i]) / s.tiles);
+            u0 = s_first[i] + (long long)unit * s.tiles, u1 = u0 + s.tiles;
             if ((which && u0 <= x0) || (u0 >= x0 && u1 <= x1)) continue;  // done as the first, or whole and written
             int w0 = w, w1 = w;
             while (w0 > (int)blockIdx.x * WARPS && deal.begin(w0) > u0) --w0;
             while (w1 + 1 < (int)(blockIdx.x + 1) * WARPS && deal.begin(w1 + 1) < u1 && deal.begin(w1 + 1) < b1) ++w1;
             const bool done = u0 >= b0 && u1 <= b1;
             const int to = 2 * part.warps + 2 * blockIdx.x + (u0 > b0);
-            join_warp<T, HDP>(a, part, i, (int)((u0 - s_first[i]) / s_tiles[i]), 2 * w0 + (deal.begin(w0) < u0),
+            join_warp<T, HDP>(a, part, s, unit, 2 * w0 + (deal.begin(w0) < u0),
                               2 * (w0 + 1), w1 - w0, w - w0, done ? -1 : to);
         }
     }

@@ -439,8 +439,8 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                     t.at = kv_head_at(a.c, a.layer, page, w.head) + (long long)in_page * D;
                     if (!(n & 8)) {
                         const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
-                        t.ks = a.c.k_scale[sc] * code_unit<CODE>();
-                        t.lv = log2f(a.c.v_scale[sc]) + (CODE == CAC_KV8_INT8 ? 0.f : 8.f);
+                        t.ks = a.c.k_scale[sc];
+                        t.lv = log2f(a.c.v_scale[sc]);
                         t.iv = ex2(-t.lv);
                     }
                 }
@@ -452,9 +452,11 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
         const uint8_t *k_lane = static_cast<const uint8_t*>(a.c.k) + lane_at, *v_lane = static_cast<const uint8_t*>(a.c.v) + lane_at;
         auto load = [&](int n, long long at, uint4 (&raw)[NL]) {
             const uint8_t* from = (n & 8 ? v_lane : k_lane) + at;
+            // rows sub and sub + 8, elements of each 64; past the end of the sequence the codes may be anything, NaN among them
+            const int left = at >= 0 ? w.s.len - w.token(n >> 4) - (n & 7) * KV_BLOCK - sub : 0;
 #pragma unroll
-            for (int y = 0; y < NL; ++y)  // rows sub and sub + 8, elements of each 64
-                raw[y] = at >= 0 && ((y >> 1) * 4 + c4) * 16 < D
+            for (int y = 0; y < NL; ++y)
+                raw[y] = left > (y & 1) * 8 && ((y >> 1) * 4 + c4) * 16 < D
                              ? *reinterpret_cast<const uint4*>(from + (y & 1) * 8 * D + (y >> 1) * 64)
                              : make_uint4(0, 0, 0, 0);
         };

@@ -435,6 +435,22 @@ def test_released_pages_are_not_seen():
     b.attend([0], [150])                        # positions whose own pages are gone
 
 
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dim", [64, 80])
+def test_codes_that_no_write_filled_are_never_seen(code, dim):
+    """Pages may hold anything before: 0xff is NaN as e4m3, and the scales are NaN too."""
+    b = Both(code, dim=dim, page=48, dtype=BF16, n_pages=60)
+    for t in (b.cache.k, b.cache.v):
+        t.fill_(-1)
+    for t in (b.cache.k_scale, b.cache.v_scale):
+        t.fill_(float("nan"))
+    b.append([0, 1, 2, 3], [1, 17, 150, 300])
+    b.verify()
+    for counts in ([1] * 4, [1, 2, 3, 4], [1, 17, 150, 300]):
+        b.attend([0, 1, 2, 3], counts)
+        b.attend([0, 1, 2, 3], counts, left=20, sinks=3)
+
+
 def test_more_queries_than_tokens():
     """Positions before 0 see nothing."""
     b = Both(dim=64, page=16)
