@@ -691,26 +691,34 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_compact_plan_kernel(const cac_kv
     const int used = c.n_pages - *c.n_free;
     int32_t *places = work.list, *movers = work.list + (c.n_pages / 2 + 1);
     int holes = 0, moves = 0;
-    for (int base = 0; base < c.n_pages; base += PLAN_T) {
-        const int p = base + threadIdx.x;
-        const bool in_use = p < c.n_pages && c.refs[p] > 0;
-        const Two x = {p < used && !in_use, p >= used && in_use};
+    const int room = c.n_pages / 2 + 1;  // there are at most min(used, n_pages - used) of either
+    constexpr int EACH = 8;              // consecutive pages of a thread: a scan over the block for 8,192 of them
+    for (int base = 0; base < c.n_pages; base += PLAN_T * EACH) {
+        const int p0 = base + threadIdx.x * EACH;
+        unsigned in_use = 0;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) in_use |= (unsigned)(p0 + k < c.n_pages && c.refs[p0 + k] > 0) << k;
+        const unsigned there = p0 >= c.n_pages ? 0u : (1u << min(EACH, c.n_pages - p0)) - 1;
+        const unsigned before = p0 >= used ? 0u : (1u << min(EACH, used - p0)) - 1;  // pages before `used`
+        const unsigned hole = before & there & ~in_use, mover = ~before & in_use;
         Two total;
-        const Two at = block_scan(x, &total);
-        const int room = c.n_pages / 2 + 1;  // there are at most min(used, n_pages - used) of either
-        if (x.a && holes + at.a < room) places[holes + at.a] = p;
-        if (x.b && moves + at.b < room) movers[moves + at.b] = p;
+        Two at = block_scan(Two{__popc(hole), __popc(mover)}, &total);
+        at.a += holes, at.b += moves;
+#pragma unroll
+        for (int k = 0; k < EACH; ++k) {
+            if (hole >> k & 1 && at.a < room) places[at.a++] = p0 + k;
+            if (mover >> k & 1 && at.b < room) movers[at.b++] = p0 + k;
+        }
         holes += total.a;
         moves += total.b;
     }
     __syncthreads();
-    moves = min(min(moves, holes), c.n_pages / 2 + 1);  // equal by construction
+    moves = min(min(moves, holes), room);  // equal by construction
     for (int k = threadIdx.x; k < moves; k += PLAN_T) {
         work.name[movers[k]] = places[k];
         c.refs[places[k]] = c.refs[movers[k]];
         c.refs[movers[k]] = 0;
     }
-    for (int k = threadIdx.x; k < c.n_pages - used; k += PLAN_T) c.free_list[k] = c.n_pages - 1 - k;
     if (threadIdx.x == 0) work.count[1] = moves, work.count[2] = used;
 }
 
@@ -721,6 +729,7 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const cac_kv8 c) {
     const int32_t *places = work.list, *movers = work.list + (c.n_pages / 2 + 1);
     const int moves = work.count[1], used = work.count[2];
     if (moves == 0) return;
+    for (int k = blockIdx.x * 256 + threadIdx.x; k < c.n_pages - used; k += gridDim.x * 256) c.free_list[k] = c.n_pages - 1 - k;
     for (int s = blockIdx.x; s < c.max_seqs; s += gridDim.x) {
         int32_t* row = c.table + (long long)s * c.max_pages;
         for (int j = threadIdx.x; j < pages_of(c.lens[s], c.page_tokens); j += blockDim.x)

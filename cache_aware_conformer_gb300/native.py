@@ -848,8 +848,11 @@ class Kv8Cache:
         n, p, s = self._list(ids, starts)
         heads = self._c.kv_heads
         ks, dt = self._act(k, heads, "k")
-        vs, _ = self._act(v, heads, "v")
-        self._alike(v, k, "v")
+        if v.dtype is k.dtype and v.shape == k.shape and v.stride() == k.stride() and v.get_device() == self._dev:
+            vs = ks
+        else:
+            vs, _ = self._act(v, heads, "v")
+            self._alike(v, k, "v")
         r = self._write(self._ref, layer, n, p, s, k.size(0), k.data_ptr(), v.data_ptr(), ks, vs, dt, self._on(stream))
         if r:
             _check(r, "cac_kv8_write")
