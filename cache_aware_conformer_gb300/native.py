@@ -864,7 +864,7 @@ class Kv8Cache:
         dtype = dtype or torch.float32
         if dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype: bfloat16 or float32")
-        k, v = self._empty(stream, *[((n, count, self.cfg.kv_heads, self.cfg.head_dim), dtype)] * 2)
+        k, v = self._empty(stream, ((2, n, count, self._c.kv_heads, self._c.head_dim), dtype))[0].unbind(0)
         _check(_lib().cac_kv8_read(self._ref, layer, n, p, self._ints(first, n, "first"), count, k.data_ptr(),
                                    v.data_ptr(), 1 if dtype is torch.bfloat16 else 0, self._on(stream)),
                "cac_kv8_read")
