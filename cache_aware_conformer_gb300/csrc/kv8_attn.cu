@@ -308,11 +308,19 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                         half4<CODE>(__byte_perm(w[0][x], w[1][x], sel), a0, b0);
                         half4<CODE>(__byte_perm(w[2][x], w[3][x], sel), a1, b1);
                         const int n = z * PER + 4 * x + 2 * y;
-                        mma_rows(o[n], p[u], a0, a1);
-                        mma_rows(o[n + 1], p[u], b0, b1);
                         if constexpr (WIDE) {
-                            mma_rows(o[n], pl[u], a0, a1);
-                            mma_rows(o[n + 1], pl[u], b0, b1);
+                            // The tensor core cuts sums off where fp32 would round: over a long cache that adds up to more than
+                            // an fp32 result may lose, so its sums are of one tile and are added here.
+                            float a[4] = {}, b[4] = {};
+                            mma_rows(a, pl[u], a0, a1);
+                            mma_rows(b, pl[u], b0, b1);
+                            mma_rows(a, p[u], a0, a1);
+                            mma_rows(b, p[u], b0, b1);
+#pragma unroll
+                            for (int e = 0; e < 2 * H; ++e) o[n][e] += a[e], o[n + 1][e] += b[e];
+                        } else {
+                            mma_rows(o[n], p[u], a0, a1);
+                            mma_rows(o[n + 1], p[u], b0, b1);
                         }
                     }
             }

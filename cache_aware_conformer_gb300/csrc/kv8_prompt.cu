@@ -44,8 +44,11 @@ template <class T, int HDP> struct PShape {
     static constexpr int SOFT = NM * 4, CONV = 6, WARPS = SOFT + CONV + 2, THREADS = WARPS * 32;
     // TMEM columns: scores (two times 64 a row tile, the weights of 64 tokens in their first 32 and, for fp32, the low halves in the
     // other 32), sums (HDP a row tile)
-    static constexpr int COL_S = 0, COL_O = NM * 128;
-    static_assert(COL_O + NM * HDP <= 512, "TMEM");
+    // The tensor core cuts sums off where fp32 would round.  For fp32 results its sums are of FLUSH pieces of 64 tokens, which are
+    // added up in columns of their own (measured over windows of 2,047 tokens: off by 4.3e-6 of the result without that).
+    static constexpr int FLUSH = WIDE ? 4 : 1 << 30;
+    static constexpr int COL_S = 0, COL_O = NM * 128, COL_SUM = COL_O + NM * HDP;
+    static_assert(COL_SUM + (WIDE ? NM * HDP : 0) <= 512, "TMEM");
     static constexpr float SLACK = WIDE ? 2.f : 8.f, LIFT = 15.f - SLACK;
 };
 
@@ -131,6 +134,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 16 columns of the thread's lane times r
+__device__ __forceinline__ void scale16(uint32_t col, float r) {
+    float o[16];
+    uint32_t u[16];
+    tmem_ld16(col, o);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * r);
+    tmem_st16(col, u);
+}
 
 // mbar_wait and mbar_arrive for a whole warp, with one answer for all of it.  All lanes poll (one polling for the others measured 3 %
 // slower); one arrives.
@@ -233,6 +246,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
             const int low = on && p >= 0 ? a.win.low(p) : 0, high = on && p >= 0 ? a.win.high(p, w.s.len) : 0;
             const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
             const uint32_t col_s = tmem + lanes + S::COL_S + x * 128, col_o = tmem + lanes + S::COL_O + x * HDP;
+            const uint32_t col_sum = tmem + lanes + S::COL_SUM + x * HDP;
             // The warp's 32 rows of queries: largest value of a row under 2^15, then fp16 (hi, lo).  CPR lanes load a row, 16 bytes
             // each (a thread per row would touch 32 lines of memory with every load).
             float amax = 0.f;
@@ -330,13 +344,23 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                         tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < HDP; c += 16) {
-                            float o[16];
-                            uint32_t u[16];
-                            tmem_ld16(col_o + c, o);
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * r);
-                            tmem_st16(col_o + c, u);
+                            scale16(col_o + c, r);
+                            if (S::WIDE && h > S::FLUSH) scale16(col_sum + c, r);
                         }
+                    }
+                }
+                if (S::WIDE && h > 0 && h % S::FLUSH == 0) {
+                    if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < HDP; c += 16) {
+                        float o[16], sum[16] = {};
+                        uint32_t u[16];
+                        if (h > S::FLUSH) tmem_ld16(col_sum + c, sum);
+                        tmem_ld16(col_o + c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] + sum[k]);
+                        tmem_st16(col_sum + c, u);
                     }
                 }
                 const float base = m == -INFINITY ? -S::LIFT : m - S::LIFT;
@@ -390,6 +414,12 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 for (int c = 0; c < HDP / 32; ++c) {
                     float v[32];
                     tmem_ld32(col_o + c * 32, v);
+                    if (S::WIDE && w.halves > S::FLUSH) {
+                        float sum[32];
+                        tmem_ld32(col_sum + c * 32, sum);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] += sum[k];
+                    }
                     if (!on) continue;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -551,7 +581,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < PT_HALF / 16; ++k)
                         mma_ts(tmem + S::COL_O + x * HDP, tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF + part * 32 + 8 * k,
-                               vd + k * (2048 >> 4), pv, h > 0 || part > 0 || k > 0);
+                               vd + k * (2048 >> 4), pv, h % S::FLUSH > 0 || part > 0 || k > 0);
                 tc_commit(o_done + 2 * x + (h & 1));
                 if (h & 1) tc_commit(v_empty + st);
             }
