@@ -118,6 +118,24 @@ struct KvAttend {
         const int q = (int)__umulhi((uint32_t)row, group_mul);
         return q - (q * group > row);
     }
+
+    // The query rows of a K/V head (a sequence has m * group) in tiles of `size`: sequence i's are numbers first(i) = rows before
+    // it * group / size + i and on, where counts differ; m * group rows fill at most that many, first(i + 1) - first(i).
+    __host__ __device__ int tiles_of_all(int size) const {
+        return (int)(rows.starts ? (long long)rows.rows * group / size + rows.n
+                                 : (long long)rows.n * (((long long)max_new * group + size - 1) / size));
+    }
+    // Sequence and tile of number b, for a whole warp; a sequence of -1 where there is none.
+    __device__ __forceinline__ int2 tile_at(int b, int size) const {
+        if (!rows.starts) {
+            const int per = (int)(((long long)max_new * group + size - 1) / size);
+            return make_int2(b / per, b % per);
+        }
+        const long long before = rows.at(0);
+        auto first = [&](int i) { return (rows.at(i) - before) * group / size + i; };
+        const int i = warp_last_le(rows.n, b, first);
+        return make_int2(i, i < 0 ? 0 : b - (int)first(i));
+    }
 };
 
 // The device of a cache as the current one for the life of this object.

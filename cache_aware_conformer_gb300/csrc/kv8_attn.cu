@@ -472,7 +472,7 @@ template <class T, int HDP, bool SPLIT> struct Shape {
 // whole unit (short windows, where a unit has a handful of tiles): nothing has to be joined.
 template <class T, int CODE, int HDP, bool LOW, bool SPLIT>
 __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HDP, SPLIT>::BLOCKS))
-    kv_attend_kernel(const __grid_constant__ KvAttend a, int row_tiles, void* space) {
+    kv_attend_kernel(const __grid_constant__ KvAttend a, void* space) {
     using R = Rows<T, CODE, HDP, LOW>;
     using S = Shape<T, HDP, SPLIT>;
     constexpr int STAGES = S::STAGES, STAGE = S::STAGE, WARPS = S::WARPS, CH = HDP / 16;
@@ -527,12 +527,12 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
         if (before == 0) return;
         x0 = deal.begin(blockIdx.x * WARPS + warp), x1 = deal.begin(blockIdx.x * WARPS + warp + 1);
     } else {
-        const long long u = (long long)blockIdx.x * WARPS + warp;
-        const int per = kvh * row_tiles;
-        i = (int)(u / per), unit = (int)(u - (long long)i * per);   // unit = row tile * kv_heads + head
-        if (i >= n) return;
+        const int u = (int)blockIdx.x * WARPS + warp;
+        const int2 tile = a.tile_at(u / kvh, 16);
+        i = tile.x, unit = tile.y * kvh + u % kvh;   // unit = row tile * kv_heads + head
+        if (i < 0 || i >= n) return;
         s = seq_work(a, i);
-        if (unit / kvh * 16 >= s.m * a.group) return;
+        if (tile.y * 16 >= s.m * a.group) return;
         x1 = s.tiles;
     }
 
@@ -680,11 +680,6 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
                 if (t == 0 && a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] = -INFINITY;
             }
         }
-        if constexpr (!SPLIT) {
-            // rows that a count above max_new adds: they see nothing, and are written as that
-            unit += kvh * row_tiles;
-            if (unit / kvh * 16 < s.m * a.group) x = 0;  // their one tile holds nothing
-        }
     }
     cp_wait<0>();
     if constexpr (SPLIT) {
@@ -771,7 +766,7 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
 }
 
 template <class T, int CODE, int HDP, bool LOW>
-cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
+cudaError_t launch_attend(const KvAttend& a, bool split, int sms, void* space, cudaStream_t s) {
     using S1 = Shape<T, HDP, true>;
     using S0 = Shape<T, HDP, false>;
     const int smem = split ? S1::BYTES : S0::BYTES;
@@ -785,36 +780,35 @@ cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms,
         ready[split].fetch_or(bit, std::memory_order_relaxed);
     }
     if (!split) {
-        const long long units = (long long)a.rows.n * a.c.kv_heads * row_tiles;
-        return launch_k(kernel, dim3((unsigned)((units + S0::WARPS - 1) / S0::WARPS)), dim3(S0::WARPS * 32), smem, s, 1, a,
-                        row_tiles, space);
+        const unsigned units = (unsigned)a.tiles_of_all(16) * a.c.kv_heads;
+        return launch_k(kernel, dim3((units + S0::WARPS - 1) / S0::WARPS), dim3(S0::WARPS * 32), smem, s, 1, a, space);
     }
-    e = launch_k(kernel, dim3(sms), dim3(S1::WARPS * 32), smem, s, 1, a, row_tiles, space);
+    e = launch_k(kernel, dim3(sms), dim3(S1::WARPS * 32), smem, s, 1, a, space);
     if (e != cudaSuccess || sms < 2) return e;
-    return launch_k(kv_join_kernel<T, HDP>, dim3(sms - 1, std::min(16, a.max_new * a.group)), dim3(HDP, JOIN_Y), 0, s, 1, a,
+    return launch_k(kv_join_kernel<T, HDP>, dim3(sms - 1, std::max(1, std::min(16, a.max_new * a.group))), dim3(HDP, JOIN_Y), 0, s, 1, a,
                     sms, S1::WARPS, space);
 }
 template <class T, int CODE, int HDP>
-cudaError_t launch_attend(const KvAttend& a, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
-    return (long long)a.max_new * a.group <= 8 ? launch_attend<T, CODE, HDP, true>(a, split, row_tiles, sms, space, s)
-                                               : launch_attend<T, CODE, HDP, false>(a, split, row_tiles, sms, space, s);
+cudaError_t launch_attend(const KvAttend& a, bool split, int sms, void* space, cudaStream_t s) {
+    return (long long)a.max_new * a.group <= 8 ? launch_attend<T, CODE, HDP, true>(a, split, sms, space, s)
+                                               : launch_attend<T, CODE, HDP, false>(a, split, sms, space, s);
 }
 
 }  // namespace
 
 // kv8_attn.cu is compiled once for each kind of code (kv8_attn_e4m3.cu includes it)
 template <int CODE>
-cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int row_tiles, int sms, void* space, cudaStream_t s) {
+cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int sms, void* space, cudaStream_t s) {
     const int d = a.c.head_dim;
     if (dtype == CAC_DTYPE_BF16)
-        return d <= 64    ? launch_attend<bf16, CODE, 64>(a, split, row_tiles, sms, space, s)
-               : d <= 128 ? launch_attend<bf16, CODE, 128>(a, split, row_tiles, sms, space, s)
-                          : launch_attend<bf16, CODE, 256>(a, split, row_tiles, sms, space, s);
-    return d <= 64    ? launch_attend<float, CODE, 64>(a, split, row_tiles, sms, space, s)
-           : d <= 128 ? launch_attend<float, CODE, 128>(a, split, row_tiles, sms, space, s)
-                      : launch_attend<float, CODE, 256>(a, split, row_tiles, sms, space, s);
+        return d <= 64    ? launch_attend<bf16, CODE, 64>(a, split, sms, space, s)
+               : d <= 128 ? launch_attend<bf16, CODE, 128>(a, split, sms, space, s)
+                          : launch_attend<bf16, CODE, 256>(a, split, sms, space, s);
+    return d <= 64    ? launch_attend<float, CODE, 64>(a, split, sms, space, s)
+           : d <= 128 ? launch_attend<float, CODE, 128>(a, split, sms, space, s)
+                      : launch_attend<float, CODE, 256>(a, split, sms, space, s);
 }
-template cudaError_t kv_launch_attend<KV8_ATTN_CODE>(const KvAttend&, int, bool, int, int, void*, cudaStream_t);
+template cudaError_t kv_launch_attend<KV8_ATTN_CODE>(const KvAttend&, int, bool, int, void*, cudaStream_t);
 
 #if KV8_ATTN_CODE == 0
 size_t kv_attend_bytes(int head_dim, int sms) {

@@ -75,9 +75,9 @@ constexpr int TA_SEQS = 512;     // sequences of one launch of kv8_attn.cu's ker
 
 // kv8_attn.cu: few query rows to a K/V head.  split: units may be cut, with workspace of kv_attend_bytes
 template <int CODE>
-cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int row_tiles, int sms, void* space, cudaStream_t s);
-extern template cudaError_t kv_launch_attend<CAC_KV8_INT8>(const KvAttend&, int, bool, int, int, void*, cudaStream_t);
-extern template cudaError_t kv_launch_attend<CAC_KV8_E4M3>(const KvAttend&, int, bool, int, int, void*, cudaStream_t);
+cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int sms, void* space, cudaStream_t s);
+extern template cudaError_t kv_launch_attend<CAC_KV8_INT8>(const KvAttend&, int, bool, int, void*, cudaStream_t);
+extern template cudaError_t kv_launch_attend<CAC_KV8_E4M3>(const KvAttend&, int, bool, int, void*, cudaStream_t);
 size_t kv_attend_bytes(int head_dim, int sms);
 // kv8_prompt.cu
 // whether it takes a call whose sequences have `rows` query rows to a K/V head on average

@@ -36,8 +36,8 @@ using namespace cac;
 extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
                                            int att_chunk, int sinks) {
     (void)heads;
-    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 1 || att_chunk < 1 || sinks < 0 ||
-        !splits(*c, n, sm_count(c->device), std::min(max_new, rows), att_left, att_chunk, sinks))
+    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || att_chunk < 1 || sinks < 0 ||
+        !splits(*c, n, sm_count(c->device), std::max(std::min(max_new, rows), 1), att_left, att_chunk, sinks))
         return 0;
     return kv_attend_bytes(c->head_dim, sm_count(c->device));
 }
@@ -61,16 +61,14 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
         ((q_stride * size | out_stride * size) & 15) || (words & 3))
         return CAC_E_ALIGN;
-    const int group = heads / c->kv_heads, most = starts ? std::min(max_new, rows) : rows / n;
+    const int group = heads / c->kv_heads, most = starts ? std::max(std::min(max_new, rows), 1) : rows / n;
     const int sms = sm_count(c->device);
     if (sms < 1) return CAC_E_CUDA;
     const bool split = splits(*c, n, sms, most, att_left, att_chunk, sinks);
     if (split && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
                   workspace_bytes < cac_kv8_attend_workspace(c, n, rows, most, heads, att_left, att_chunk, sinks)))
         return CAC_E_INVAL;
-    const long long tiles = ((long long)most * group + 15) / 16;
-    if (tiles == 0) return CAC_OK;
-    if (tiles * std::min(n, TA_SEQS) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
+    if (((long long)rows * group / 16 + n) * c->kv_heads > INT32_MAX / 32) return CAC_E_LIMIT;
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -83,8 +81,8 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
         if (kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
             e = kv_launch_prompt(a, dtype, s);
         else
-            e = c->code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, split, (int)tiles, sms, workspace, s)
-                                        : kv_launch_attend<CAC_KV8_E4M3>(a, dtype, split, (int)tiles, sms, workspace, s);
+            e = c->code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, split, sms, workspace, s)
+                                        : kv_launch_attend<CAC_KV8_E4M3>(a, dtype, split, sms, workspace, s);
         if (e != cudaSuccess) return CAC_E_CUDA;
     }
     return CAC_OK;

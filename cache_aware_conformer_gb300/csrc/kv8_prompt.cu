@@ -166,7 +166,7 @@ struct PWork {
 
 template <class T, int CODE, int HDP>
 __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
-    kv_prompt_kernel(const __grid_constant__ KvAttend a, int row_tiles) {
+    kv_prompt_kernel(const __grid_constant__ KvAttend a) {
     using S = PShape<T, HDP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -178,14 +178,23 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.head_dim, kvh = a.c.kv_heads;
     pdl_wait();
 
-    // the last row tiles see the most tokens and go first
+    // a sequence's last row tiles see the most tokens and go first
     PWork w;
-    const int per = a.rows.n * kvh;
-    int tile = row_tiles - 1 - (int)(blockIdx.x / per);
-    w.head = (int)(blockIdx.x % per) % kvh;
-    w.s = seq_work(a, (int)(blockIdx.x % per) / kvh);
+    const int number = (int)(blockIdx.x / kvh), all = (int)(gridDim.x / kvh);
+    int2 tile;
+    if (a.rows.starts) {
+        tile = a.tile_at(all - 1 - number, S::NM * PT_ROWS);
+    } else {
+        tile = make_int2(number % a.rows.n, all / a.rows.n - 1 - number / a.rows.n);
+    }
+    if (tile.x < 0) {
+        pdl_trigger();
+        return;
+    }
+    w.head = (int)(blockIdx.x % kvh);
+    w.s = seq_work(a, tile.x);
     const int R = w.s.m * a.group;
-    w.r0 = tile * S::NM * PT_ROWS;
+    w.r0 = tile.y * S::NM * PT_ROWS;
     w.rows = min(S::NM * PT_ROWS, R - w.r0);
     w.lot = w.skt = w.tiles = w.halves = 0;
     if (w.rows > 0 && w.s.len > 0) {
@@ -201,13 +210,11 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
     const long long out0 = w.s.row0;
     if (w.tiles == 0) {  // nothing is seen: an empty sequence, one that the call may not name, positions before 0
         pdl_trigger();
-        const int step = w.s.len > 0 ? 1 << 30 : row_tiles * S::NM * PT_ROWS;  // a count above max_new has rows past the last tile
-        for (long long r0 = w.r0; r0 < R; r0 += step)
-            for (int e = threadIdx.x; e < min(S::NM * PT_ROWS, (int)(R - r0)) * D; e += S::THREADS) {
-                const int row = (int)r0 + e / D, query = a.query_of(row), qh = w.head * a.group + row - query * a.group;
-                static_cast<T*>(a.out)[(out0 + query) * a.out_stride + (long long)qh * D + e % D] = from_f<T>(0.f);
-                if (a.lse && e % D == 0) a.lse[(out0 + query) * a.heads + qh] = -INFINITY;
-            }
+        for (int e = threadIdx.x; e < max(w.rows, 0) * D; e += S::THREADS) {
+            const int row = w.r0 + e / D, query = a.query_of(row), qh = w.head * a.group + row - query * a.group;
+            static_cast<T*>(a.out)[(out0 + query) * a.out_stride + (long long)qh * D + e % D] = from_f<T>(0.f);
+            if (a.lse && e % D == 0) a.lse[(out0 + query) * a.heads + qh] = -INFINITY;
+        }
         return;
     }
     const int nm = w.rows > PT_ROWS ? 2 : 1;
@@ -604,9 +611,8 @@ template <class T, int CODE, int HDP> cudaError_t launch_prompt(const KvAttend& 
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int row_tiles = (int)(((long long)a.max_new * a.group + S::NM * PT_ROWS - 1) / (S::NM * PT_ROWS));
-    const long long blocks = (long long)a.rows.n * a.c.kv_heads * row_tiles;
-    return launch_k(kernel, dim3((unsigned)blocks), dim3(S::THREADS), S::SMEM, s, 1, a, row_tiles);
+    const unsigned blocks = (unsigned)a.tiles_of_all(S::NM * PT_ROWS) * a.c.kv_heads;
+    return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::SMEM, s, 1, a);
 }
 template <class T, int CODE> cudaError_t launch_prompt(const KvAttend& a, cudaStream_t s) {
     return a.c.head_dim <= 64 ? launch_prompt<T, CODE, 64>(a, s) : launch_prompt<T, CODE, 128>(a, s);

@@ -796,6 +796,13 @@ class Kv8Cache:
     def _on(self, stream):
         return stream.cuda_stream if stream is not None else self._current(self._dev)
 
+    @staticmethod
+    def _used_on(stream, *tensors):
+        """Memory of tensors that a call on an explicit stream uses is not given out again before the call has run."""
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
     def _empty(self, stream, *specs):
         """Uninitialised tensors (shape, dtype) that belong to the stream that the call runs on."""
         empty = self._torch.empty
@@ -839,6 +846,8 @@ class Kv8Cache:
     def extend(self, ids, each: int = 1, starts=None, max_new=None, stream=None):
         """Room for `each` (or starts[i+1] - starts[i]) new tokens of each sequence (cac_kv8_extend)."""
         n, p, s = self._list(ids, starts)
+        if stream is not None:
+            self._used_on(stream, ids, starts)
         r = self._extend(self._ref, n, p, s, each, self._on(stream))
         if r:
             _check(r, "cac_kv8_extend")
@@ -853,6 +862,8 @@ class Kv8Cache:
         else:
             vs, _ = self._act(v, heads, "v")
             self._alike(v, k, "v")
+        if stream is not None:
+            self._used_on(stream, ids, starts, k, v)
         r = self._write(self._ref, layer, n, p, s, k.size(0), k.data_ptr(), v.data_ptr(), ks, vs, dt, self._on(stream))
         if r:
             _check(r, "cac_kv8_write")
@@ -865,6 +876,8 @@ class Kv8Cache:
         if dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("dtype: bfloat16 or float32")
         k, v = self._empty(stream, ((2, n, count, self._c.kv_heads, self._c.head_dim), dtype))[0].unbind(0)
+        if stream is not None:
+            self._used_on(stream, ids, first)
         _check(_lib().cac_kv8_read(self._ref, layer, n, p, self._ints(first, n, "first"), count, k.data_ptr(),
                                    v.data_ptr(), 1 if dtype is torch.bfloat16 else 0, self._on(stream)),
                "cac_kv8_read")
@@ -902,6 +915,8 @@ class Kv8Cache:
             sums = self._empty(stream, ((rows, heads), self._f32))[0]
         if need:
             space = self._empty(stream, ((need,), self._torch.uint8))[0]
+        if stream is not None:
+            self._used_on(stream, ids, starts, q, out)
         r = self._attend(self._ref, layer, n, p, s, rows, max_new, heads, self._scale if scale is None else scale, att_left,
                          att_chunk, sinks, q.data_ptr(), qs, out.data_ptr(), os_, None if sums is None else sums.data_ptr(),
                          dt, None if space is None else space.data_ptr(), need, self._on(stream))
@@ -912,6 +927,8 @@ class Kv8Cache:
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] becomes a copy of src[i] that shares its pages (cac_kv8_fork)."""
         n = src.numel()
+        if stream is not None:
+            self._used_on(stream, src, dst)
         _check(_lib().cac_kv8_fork(self._ref, n, self._ints(src, n, "src"), self._ints(dst, n, "dst"),
                                    self._on(stream)), "cac_kv8_fork")
 
@@ -919,6 +936,8 @@ class Kv8Cache:
         """Shorten to new_len tokens (an int, or int32 cuda tensor [n]); 0 frees the sequence (cac_kv8_truncate)."""
         n, p, _ = self._list(ids, None)
         one = isinstance(new_len, int)
+        if stream is not None:
+            self._used_on(stream, ids, None if one else new_len)
         r = self._truncate(self._ref, n, p, None if one else self._ints(new_len, n, "new_len"), new_len if one else 0,
                            self._on(stream))
         if r:
@@ -927,6 +946,8 @@ class Kv8Cache:
     def trim(self, ids, att_left: int, att_chunk: int = 1, sinks: int = 0, stream=None):
         """Release the pages that no later query sees under this window (cac_kv8_trim)."""
         n, p, _ = self._list(ids, None)
+        if stream is not None:
+            self._used_on(stream, ids)
         _check(_lib().cac_kv8_trim(self._ref, n, p, att_left, att_chunk, sinks, self._on(stream)), "cac_kv8_trim")
 
     def compact(self, stream=None):

@@ -132,10 +132,15 @@ int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const i
  *         seen (-inf where there is none), or NULL
  *   score = scale * q . k; pointers and row strides multiples of 16 bytes
  *   max_new: no sequence has more rows than this (one that has latches
- *         CAC_E_BOUNDS, and its rows are zero); used where starts is given
+ *         CAC_E_BOUNDS, and its rows are zero); used where starts is given.  A
+ *         sequence whose rows pass `rows` latches CAC_E_BOUNDS too, and its rows are
+ *         left as they were
  *   workspace: cac_kv8_attend_workspace bytes, 16-byte aligned, this call's own
  *         until it has run (NULL where that is 0)
- * Rows of out and lse that belong to no sequence are left as they were. */
+ * Rows of out and lse that belong to no sequence are left as they were.  Tokens
+ * that an extend made room for and no write has filled have unspecified values.
+ * A bounded wait inside the kernels that gives up latches CAC_E_TIMEOUT.
+ * CAC_E_LIMIT: more than 2^26 tiles of 16 query rows (rows * heads / 16). */
 int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
                    int max_new, int heads, float scale, int att_left, int att_chunk, int sinks, const void* q,
                    long long q_stride, void* out, long long out_stride, float* lse, int dtype, void* workspace,

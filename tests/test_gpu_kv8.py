@@ -539,9 +539,142 @@ def test_the_same_sequence_twice_and_deterministic():
     assert (a1[0].float() - a1[2].float()).abs().max() <= tol
 
 
+@pytest.mark.parametrize("counts", ["ones", "ragged", "prompts"])
+def test_more_sequences_than_one_launch_takes(counts):
+    """1,300 sequences in one call: extend plans 1,024 at a time, attention launches 512 at a time."""
+    n = 1300
+    b = Both(heads=1, dim=16, page=16, n_pages=8000, seqs=n + 20, max_pages=6, dtype=F32)
+    rng = np.random.RandomState(3)
+    ids = rng.permutation(n)
+    first = rng.randint(1, 40, n)
+    b.append(ids, list(first))
+    b.fork(list(ids[:20]), list(range(n, n + 20)))          # shared pages in the next extend, some in each chunk
+    new = {"ones": np.ones(n, int), "ragged": rng.randint(0, 4, n), "prompts": rng.randint(0, 40, n)}[counts]
+    all_ids = list(ids) + list(range(n, n + 20))
+    all_new = list(new) + [int(x) for x in new[:20]]
+    b.append(all_ids, all_new)
+    b.verify()
+    b.attend(all_ids, all_new, uniform=counts == "ones")
+    b.attend(all_ids, all_new, left=7, sinks=2, uniform=counts == "ones")
+
+
+def test_pools_past_two_gigabytes():
+    """Page numbers whose byte offsets pass 2^31 and 2^32."""
+    from cache_aware_conformer_gb300 import native
+    b = Both(heads=1, dim=16, page=16, n_pages=4, seqs=3, max_pages=4, dtype=BF16)
+    cfg = Kv8Config(2, 16, 256, 64, 9000, 3, 6, "int8")     # 2.4 GB a layer for K and as much for V
+    pages = torch.arange(9000, dtype=torch.int32, device="cuda")
+    b.cfg, b.seqs = cfg, [Seq(2, 16, 256) for _ in range(3)]
+    b.cache = native.Kv8Cache(cfg, tensors={
+        "table": torch.full((3, 6), -1, dtype=torch.int32, device="cuda"), "lens": torch.zeros(3, dtype=torch.int32, device="cuda"),
+        "refs": torch.zeros(9000, dtype=torch.int32, device="cuda"), "free": pages, "n_free": pages[:1] + 9000})
+    b.append([0, 1], [70, 130])                              # the pool's last pages
+    assert int(b.cache.table[0, 0]) > 8900
+    b.verify()
+    b.attend([0, 1], [1, 1], layer=1)
+    b.attend([0, 1], [2, 40], layer=1)
+    b.fork([1], [2])
+    b.append([1, 2], [3, 5])
+    b.cache.compact()
+    assert int(b.cache.table.max()) < 10
+    b.verify()
+
+
+@pytest.mark.parametrize("heads,group", [(1, 128), (2, 40), (5, 7)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_query_heads_to_a_kv_head(heads, group, dtype):
+    b = Both(heads=heads, dim=64, page=32, dtype=dtype)
+    b.append([0, 1, 2], [5, 64, 150])
+    b.attend([0, 1, 2], [1, 1, 1], group=group, uniform=True)
+    b.attend([2, 1], [7, 3], group=group, left=40)
+
+
+def test_extremes_of_the_window():
+    big = 2 ** 31 - 1
+    b = Both(dim=64, page=16)
+    b.append([0, 1], [100, 37])
+    for left, chunk, sinks in ((big, 1, 0), (0, 1, big), (3, big, 0), (big, big, big), (0, 1, 0)):
+        b.attend([0, 1], [1, 1], left=left, chunk=chunk, sinks=sinks)
+        b.attend([0, 1], [40, 37], left=left, chunk=chunk, sinks=sinks)
+    b.trim([0], big, big, 0)
+    b.trim([1], 0, 1, big)
+    b.verify()
+
+
+def test_empty_calls():
+    b = Both(dim=64, page=16)
+    b.append([0], [5])
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    q = torch.empty(0, 4, 64, device="cuda")
+    assert b.cache.attend(0, none, q).shape == (0, 4, 64)
+    assert b.cache.attend(0, b.ids([0, 1]), q, starts=b.ids([0, 0, 0])).shape == (0, 4, 64)
+    out, lse = b.cache.attend(0, b.ids([0]), torch.randn(3, 4, 64, device="cuda"), starts=b.ids([1, 1]), max_new=0, lse=True,
+                              out=torch.full((3, 4, 64), 2.0, device="cuda"))
+    assert (out == 2).all()
+    x = torch.empty(0, 2, 64, device="cuda")
+    b.cache.extend(none), b.cache.write(0, none, x, x), b.cache.fork(none, none), b.cache.truncate(none), b.cache.trim(none, 3)
+    b.cache.extend(b.ids([0]), each=0), b.cache.write(0, b.ids([0]), x, x)
+    assert b.cache.read(0, none, none, 4)[0].shape == (0, 4, 2, 64) and b.cache.read(0, b.ids([0]), b.ids([0]), 0)[1].shape[1] == 0
+    b.verify()
+
+
+def test_starts_past_the_rows_touch_nothing():
+    b = Both(dim=64, page=16)
+    b.append([0, 1], [30, 40])
+    for rows, starts in ((8, [0, 5, 9]), (30, [0, 25, 60]), (8, [0, 5, -3])):
+        q = torch.randn(rows, 4, 64, device="cuda")
+        out = torch.full_like(q, 9.0)
+        b.cache.attend(0, b.ids([0, 1]), q, starts=b.ids(starts), max_new=40, out=out)
+        with pytest.raises(b.native.CacError) as e:
+            b.cache.check()
+        assert e.value.code == BOUNDS
+        assert (out[starts[1]:] == 9).all() and (out[:starts[1]] != 9).any()
+
+
 # ---------------------------------------------------------------------------
 # streams, graphs, a step
 # ---------------------------------------------------------------------------
+@pytest.mark.parametrize("m", [1, 60])
+def test_a_first_call_inside_a_capture(m):
+    """Nothing has to be set up outside: kernels of a head size that no other test of this process uses."""
+    b = Both("e4m3", heads=1, dim=112 if m > 1 else 48, page=16, dtype=BF16, n_pages=60)
+    b.append([0, 1], [70, 300])
+    q = b.rand(2 * m, 3, b.cfg.head_dim).cuda()
+    ids = b.ids([0, 1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = b.cache.attend(0, ids, q)
+    graph.replay()
+    first = out.clone()
+    graph.replay()
+    b.cache.check()
+    assert torch.equal(out, first) and torch.equal(b.cache.attend(0, ids, q), first)
+
+
+def test_two_captured_graphs_replayed_at_once():
+    """Attention captured twice, replayed on two streams at the same time: each has a workspace of its own."""
+    b = Both(dim=128, page=32, dtype=BF16, n_pages=700, max_pages=660, seqs=3)
+    b.append([0, 1], [20000, 900])
+    ids, graphs, outs, want = b.ids([0, 1]), [], [], []
+    for _ in range(2):
+        q = b.rand(2, 8, 128).cuda()
+        want.append(b.cache.attend(0, ids, q))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(b.cache.attend(0, ids, q))
+        graphs.append((g, q))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(10):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    b.cache.check()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
 def test_a_captured_step_replays():
     """Extend, write and attend captured once; each replay goes one token further."""
     b = Both(dim=64, page=16, dtype=BF16, n_pages=200, layers=2)
@@ -595,6 +728,33 @@ def test_attention_on_several_streams_at_once():
         torch.cuda.synchronize()
         for a, w in zip(got, want):
             assert torch.equal(a, w)
+
+
+def test_calls_on_another_stream_than_the_tensors_own():
+    """Everything on a side stream, its inputs dropped at once: their memory is not given out again before it has been read."""
+    b = Both(dim=128, page=32, dtype=BF16, n_pages=300, max_pages=200)
+    side = torch.cuda.Stream()
+    outs, qs = [], []
+    for step in range(6):
+        kk, vv, qq = b.rand(400, 2, 128), b.rand(400, 2, 128), b.rand(2, 8, 128)
+        k, v, q, ids = kk.cuda(), vv.cuda(), qq.cuda(), b.ids([1, 3])
+        side.wait_stream(torch.cuda.current_stream())
+        b.cache.extend(ids, each=200, stream=side)
+        b.cache.write(0, ids, k, v, stream=side)
+        outs.append(b.cache.attend(0, ids, q, stream=side))
+        del k, v, q, ids
+        torch.full((2, 400, 2, 128), float("nan"), device="cuda", dtype=BF16)      # takes what is free
+        for n, i in enumerate((1, 3)):
+            b.seqs[i].append(0, "k", kk[200 * n:200 * n + 200].float().numpy(), "int8")
+            b.seqs[i].append(0, "v", vv[200 * n:200 * n + 200].float().numpy(), "int8")
+            b.seqs[i].len += 200
+        qs.append(qq)
+    torch.cuda.synchronize()
+    b.verify()
+    for n, i in enumerate((1, 3)):
+        ref = attend64(b.seqs[i], 0, qs[-1][n:n + 1].double().numpy(), 4, 128 ** -0.5, -1, 1, 0, 32)
+        tol, _ = bounds(*ref, 128, 1200, BF16)
+        assert (np.abs(outs[-1][n:n + 1].double().cpu().numpy() - ref[0]) <= tol).all()
 
 
 def test_binding_refuses_bad_tensors():
