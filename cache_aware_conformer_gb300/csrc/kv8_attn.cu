@@ -466,6 +466,8 @@ template <class T, int HDP, bool SPLIT> struct Shape {
     static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : 196608 / (WARPS * STAGE);
     static constexpr int BYTES = WARPS * STAGES * STAGE;
     static constexpr int BLOCKS = !SPLIT && HDP == 64 ? 4 : 1;  // of an SM
+    static_assert(WARPS <= MOST_WARPS, "the workspace has room for the parts of so many");
+    static_assert(BYTES + (SPLIT ? 20 * 1024 : 0) <= 227 * 1024, "shared memory");
 };
 
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
