@@ -28,6 +28,7 @@
 // but its own copies.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kv8_attn.cuh"
 
@@ -38,8 +39,9 @@
 namespace cac {
 namespace {
 
-constexpr float LIFT = 15.f;     // weights are held times 2^15: the largest is then 32,768, and fp16 keeps 11 bits of every
-                                 // weight down to 2^-29 of it (a small weight may meet a large value)
+// Weights are held times 2^LIFT: fp16 keeps 11 bits of every weight down to 2^-27 of the largest (a small weight may meet a large
+// value).  SLACK is what a maximum may lag behind (RowsLow): at LIFT + SLACK = 15 a weight is 32,768 at most.
+constexpr float LIFT = 13.f, SLACK = 2.f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -47,13 +49,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// with A's rows 8 .. 15 zero
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[2], uint32_t b0, uint32_t b1) {
-    const uint32_t full[4] = {a[0], 0u, a[1], 0u};
-    mma_f16(d, full, b0, b1);
-}
-template <int N> __device__ __forceinline__ void mma_rows(float (&d)[4], const uint32_t (&a)[N], uint32_t b0, uint32_t b1) {
-    mma_f16(d, a, b0, b1);
+// an 8 x 8 matrix of fp16 spread over a warp, two neighbours of a row to a thread, transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -99,91 +99,168 @@ __device__ __forceinline__ Tile tile_from(const Tile& t, int lane) {
     return r;
 }
 
-// Sixteen query rows and their running sums, spread over a warp as the tensor core's
-// fragments: a thread has rows g and g + 8 (g = lane / 4, t = lane % 4).
-template <class T, int CODE, int HDP, bool LOW> struct Rows {
-    static constexpr int H = LOW ? 1 : 2;                 // row halves: LOW holds rows 0 .. 7 only, the other eight are zero
+// A row's queries in the order of the fragments: contraction step s = 4 j + x, thread t of a row's four has elements 64 j + 16 t + 4 x +
+// {0, 1} in a[s] and + {2, 3} in b[s], times the power of two that is returned; al, bl: what fp16 left over.
+template <class T, int HDP, int LO>
+__device__ __forceinline__ float load_query(const T* src, bool on, int t, int D, uint32_t (&a)[HDP / 16], uint32_t (&b)[HDP / 16],
+                                            uint32_t (&al)[LO], uint32_t (&bl)[LO]) {
+    constexpr int STEPS = HDP / 16;
+    float x[STEPS][4];
+    float amax = 0.f;
+#pragma unroll
+    for (int j = 0; j < HDP / 64; ++j) {
+        const int e = 64 * j + 16 * t;
+        if (on && e < D) {
+            if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float4 v = *reinterpret_cast<const float4*>(src + e + 4 * k);
+                    x[4 * j + k][0] = v.x, x[4 * j + k][1] = v.y, x[4 * j + k][2] = v.z, x[4 * j + k][3] = v.w;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + e + 8 * k);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        x[4 * j + 2 * k + (c >> 1)][2 * (c & 1)] = __uint_as_float(w[c] << 16);
+                        x[4 * j + 2 * k + (c >> 1)][2 * (c & 1) + 1] = __uint_as_float(w[c] & 0xffff0000u);
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[4 * j + k][0] = x[4 * j + k][1] = x[4 * j + k][2] = x[4 * j + k][3] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[4 * j + (k >> 2)][k & 3]));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float up = lift_to_half(amax);
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        a[k] = pack_half(x[k][0] * up, x[k][1] * up);
+        b[k] = pack_half(x[k][2] * up, x[k][3] * up);
+        if constexpr (LO > 1) {
+            al[k] = pack_rest(x[k][0] * up, x[k][1] * up, a[k]);
+            bl[k] = pack_rest(x[k][2] * up, x[k][3] * up, b[k]);
+        }
+    }
+    return up;
+}
 
-    static constexpr bool WIDE = sizeof(T) == 4;          // hi + lo
-    static constexpr int STEPS = HDP / 16, NT = HDP / 8;
-    uint32_t q[STEPS][2 * H], ql[WIDE ? STEPS : 1][2 * H];
-    float o[NT][4];
-    float m[H], l[H], f[H];                               // maximum, sum, score factor of rows g, g + 8
-    int low[H], high[H];
-    int lo_max, hi_min, lo_min, hi_max;                   // over the rows
-
-    // Queries of K/V head `head`, rows r0 .. r0 + 15 of the sequence's m * group.
-    // Contraction step s = 4 j + x, thread t: elements 64 j + 16 t + 4 x + {0, 1} and + {2, 3}.
-    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
-        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim, R = s.m * a.group;
+// The tokens that rows r0 .. r0 + size - 1 (of those there are) see: a tile is looked at from hi_max and lo_min, and whole
+// for all of them between lo_max and hi_min.
+struct Seen {
+    int lo_max, hi_min, lo_min, hi_max;
+    __device__ __forceinline__ void set(const KvAttend& a, const SeqWork& s, int r0, int size) {
         // rows in order of their positions: the first and last bound the windows
-        const int p0 = s.len - s.m + a.query_of(r0), p1 = s.len - s.m + a.query_of(min(r0 + 16, R) - 1);
+        const int p0 = s.len - s.m + a.query_of(r0), p1 = s.len - s.m + a.query_of(min(r0 + size, s.m * a.group) - 1);
         const bool any = s.len > 0 && p1 >= 0;
         hi_min = any && p0 >= 0 ? a.win.high(p0, s.len) : 0;
         hi_max = any ? a.win.high(p1, s.len) : 0;
         lo_max = any ? a.win.low(p1) : 0;
         lo_min = any ? a.win.low(max(p0, 0)) : 0;
+    }
+    // whether a tile holds a token that one of the rows sees, and whether all see all of it
+    __device__ __forceinline__ bool sees(const Tile& d, int sinks) const {
+        return d.at >= 0 && d.j0 < hi_max && (d.j0 + KV_BLOCK > lo_min || d.j0 < sinks);
+    }
+    __device__ __forceinline__ bool whole(const Tile& d, int sinks) const {
+        return d.j0 + KV_BLOCK <= hi_min && (d.j0 >= lo_max || d.j0 + KV_BLOCK <= sinks);
+    }
+};
+
+// RUN consecutive results of a row
+template <class T, int RUN> __device__ __forceinline__ void store_run(T* dst, const float (&x)[RUN]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
+        for (int k = 0; k < RUN; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < RUN; k += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[k + 2 * b], x[k + 2 * b + 1]);
+                w[b] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+constexpr int MOST_WARPS = 12;   // of a block
+
+// Partial sums of units that were cut.  Slot 2 w: the unit that warp w's share begins in; slot 2 w + 1: the one that it ends in,
+// when that is another.  After the warps' slots the same for the blocks.
+struct Partials {
+    float *o, *ml;               // [slot][16][HDP], [slot][16][2]
+    long long* first;            // [TA_SEQS + 1] tiles before each sequence
+    int warps;
+};
+// RUN elements from e on of row `row` of a unit whose rows begin at r0: the result itself, or, with cut, its part in slot `slot`
+template <class T, int HDP, int RUN>
+__device__ __forceinline__ void put_run(const KvAttend& a, const SeqWork& s, int head, int row, int r0, int e, float (&y)[RUN], float l,
+                                        const Partials* cut, int slot) {
+    if (cut) {
+        store_run<float, RUN>(cut->o + ((size_t)slot * 16 + row - r0) * HDP + e, y);
+    } else if (e < a.c.head_dim) {
+        const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+#pragma unroll
+        for (int k = 0; k < RUN; ++k) y[k] *= inv;
+        store_run<T, RUN>(static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + e, y);
+    }
+}
+template <class T, int HDP>
+__device__ __forceinline__ void put_sums(const KvAttend& a, const SeqWork& s, int head, int row, int r0, float m, float l,
+                                         const Partials* cut, int slot) {
+    if (cut) {
+        cut->ml[((size_t)slot * 16 + row - r0) * 2] = m;
+        cut->ml[((size_t)slot * 16 + row - r0) * 2 + 1] = l;
+    } else if (a.lse) {
+        const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+        a.lse[(s.row0 + (long long)query) * a.heads + qh] =
+            l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+    }
+}
+
+// Sixteen query rows and their running sums, spread over a warp as the tensor core's
+// fragments: a thread has rows g and g + 8 (g = lane / 4, t = lane % 4).
+template <class T, int CODE, int HDP> struct Rows : Seen {
+    static constexpr bool WIDE = sizeof(T) == 4;          // hi + lo
+    static constexpr int STEPS = HDP / 16, NT = HDP / 8, LO = WIDE ? STEPS : 1;
+    uint32_t q[STEPS][4], ql[LO][4];
+    float o[NT][4];
+    float m[2], l[2], f[2];                               // maximum, sum, score factor of rows g, g + 8
+    int low[2], high[2];
+
+    // Queries of K/V head `head`, rows r0 .. r0 + 15 of the sequence's m * group
+    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim;
+        set(a, s, r0, 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
             const int r = r0 + g + 8 * h, query = a.query_of(r), p = s.len - s.m + query;
-            const bool on = r < R;
+            const bool on = r < s.m * a.group;
             m[h] = -INFINITY, l[h] = 0.f;
             low[h] = on && p >= 0 ? a.win.low(p) : 0;
             high[h] = on && p >= 0 && s.len > 0 ? a.win.high(p, s.len) : 0;
-            const T* src = static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
-                           (long long)(head * a.group + r - query * a.group) * D;
-            float x[STEPS][4];
-            float amax = 0.f;
+            uint32_t x[STEPS], y[STEPS], xl[LO], yl[LO];
+            f[h] = a.scale * LOG2E / load_query<T, HDP>(static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
+                                                            (long long)(head * a.group + r - query * a.group) * D,
+                                                        on, t, D, x, y, xl, yl);  // by a power of two: exact
 #pragma unroll
-            for (int j = 0; j < HDP / 64; ++j) {
-                const int e = 64 * j + 16 * t;
-                if (on && e < D) {
-                    if constexpr (WIDE) {
+            for (int k = 0; k < STEPS; ++k) q[k][h] = x[k], q[k][2 + h] = y[k];
+            if constexpr (WIDE)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 v = *reinterpret_cast<const float4*>(src + e + 4 * k);
-                            x[4 * j + k][0] = v.x, x[4 * j + k][1] = v.y, x[4 * j + k][2] = v.z, x[4 * j + k][3] = v.w;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint4 v = *reinterpret_cast<const uint4*>(src + e + 8 * k);
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) {
-                                x[4 * j + 2 * k + (b >> 1)][2 * (b & 1)] = __uint_as_float(w[b] << 16);
-                                x[4 * j + 2 * k + (b >> 1)][2 * (b & 1) + 1] = __uint_as_float(w[b] & 0xffff0000u);
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[4 * j + k][0] = x[4 * j + k][1] = x[4 * j + k][2] = x[4 * j + k][3] = 0.f;
-                }
-#pragma unroll
-                for (int k = 0; k < 16; ++k) amax = fmaxf(amax, fabsf(x[4 * j + (k >> 2)][k & 3]));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const float up = lift_to_half(amax);
-            f[h] = a.scale * LOG2E / up;  // a power of two: exact
-#pragma unroll
-            for (int k = 0; k < STEPS; ++k) {
-                q[k][h] = pack_half(x[k][0] * up, x[k][1] * up);
-                q[k][H + h] = pack_half(x[k][2] * up, x[k][3] * up);
-                if constexpr (WIDE) {
-                    ql[k][h] = pack_rest(x[k][0] * up, x[k][1] * up, q[k][h]);
-                    ql[k][H + h] = pack_rest(x[k][2] * up, x[k][3] * up, q[k][H + h]);
-                }
-            }
+                for (int k = 0; k < STEPS; ++k) ql[k][h] = xl[k], ql[k][2 + h] = yl[k];
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
-    }
-
-    // Whether a tile holds a token that one of the rows sees
-    __device__ __forceinline__ bool sees(const Tile& d, int sinks) const {
-        return d.at >= 0 && d.j0 < hi_max && (d.j0 + KV_BLOCK > lo_min || d.j0 < sinks);
     }
 
     // Two tiles of 16 tokens, their codes at shared addresses k[u] (V after K); on[u]: take part.  Column n of score tile i is
@@ -207,14 +284,14 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                     for (int x = 0; x < 4; ++x) {
                         uint32_t b0, b1;
                         half4<CODE>(ww[x], b0, b1);
-                        mma_rows(s[u][i], q[4 * j + x], b0, b1);
-                        if constexpr (WIDE) mma_rows(s[u][i], ql[4 * j + x], b0, b1);
+                        mma_f16(s[u][i], q[4 * j + x], b0, b1);
+                        if constexpr (WIDE) mma_f16(s[u][i], ql[4 * j + x], b0, b1);
                     }
                 }
             }
-            const bool full = d[u].j0 + KV_BLOCK <= hi_min && (d[u].j0 >= lo_max || d[u].j0 + KV_BLOCK <= sinks);
+            const bool full = whole(d[u], sinks);
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 const float c = f[h] * d[u].ks;
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
@@ -223,7 +300,7 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
             }
             if (!full) {
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -233,10 +310,10 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                         }
             }
         }
-        float top[H];
+        float top[2];
         bool moved = false;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
+        for (int h = 0; h < 2; ++h) {
             float mx = fmaxf(fmaxf(s[0][0][2 * h], s[0][0][2 * h + 1]), fmaxf(s[0][1][2 * h], s[0][1][2 * h + 1]));
             mx = fmaxf(mx, fmaxf(fmaxf(s[1][0][2 * h], s[1][0][2 * h + 1]), fmaxf(s[1][1][2 * h], s[1][1][2 * h + 1])));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -246,7 +323,7 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 const float r = top[h] == -INFINITY ? 1.f : ex2(m[h] - top[h]);
                 m[h] = top[h];
                 l[h] *= r;
@@ -254,9 +331,9 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                 for (int n = 0; n < NT; ++n) o[n][2 * h] *= r, o[n][2 * h + 1] *= r;
             }
         }
-        uint32_t p[2][2 * H], pl[2][2 * H];
+        uint32_t p[2][4], pl[2][4];
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
+        for (int h = 0; h < 2; ++h) {
             const float base = m[h] == -INFINITY ? 0.f : m[h] - LIFT;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -268,8 +345,8 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                 l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), d[u].iv, l[h]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    p[u][H * i + h] = pack_half(w[i][0], w[i][1]);
-                    if constexpr (WIDE) pl[u][H * i + h] = pack_rest(w[i][0], w[i][1], p[u][H * i + h]);
+                    p[u][2 * i + h] = pack_half(w[i][0], w[i][1]);
+                    if constexpr (WIDE) pl[u][2 * i + h] = pack_rest(w[i][0], w[i][1], p[u][2 * i + h]);
                 }
             }
         }
@@ -312,15 +389,15 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
                             // The tensor core cuts sums off where fp32 would round: over a long cache that adds up to more than
                             // an fp32 result may lose, so its sums are of one tile and are added here.
                             float a[4] = {}, b[4] = {};
-                            mma_rows(a, pl[u], a0, a1);
-                            mma_rows(b, pl[u], b0, b1);
-                            mma_rows(a, p[u], a0, a1);
-                            mma_rows(b, p[u], b0, b1);
+                            mma_f16(a, pl[u], a0, a1);
+                            mma_f16(b, pl[u], b0, b1);
+                            mma_f16(a, p[u], a0, a1);
+                            mma_f16(b, p[u], b0, b1);
 #pragma unroll
-                            for (int e = 0; e < 2 * H; ++e) o[n][e] += a[e], o[n + 1][e] += b[e];
+                            for (int e = 0; e < 4; ++e) o[n][e] += a[e], o[n + 1][e] += b[e];
                         } else {
-                            mma_rows(o[n], p[u], a0, a1);
-                            mma_rows(o[n + 1], p[u], b0, b1);
+                            mma_f16(o[n], p[u], a0, a1);
+                            mma_f16(o[n + 1], p[u], b0, b1);
                         }
                     }
             }
@@ -333,34 +410,208 @@ template <class T, int CODE, int HDP, bool LOW> struct Rows {
     }
     static constexpr int RUN = HDP == 64 ? 8 : 16;
 
-    // the sums of a row's four threads
-    __device__ __forceinline__ void finish() {
+    // The rows' results, or, cut, their parts in slot `slot`
+    __device__ __forceinline__ void emit(const KvAttend& a, const SeqWork& s, int head, int r0, const Partials* cut, int slot) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int h = 0; h < H; ++h) {
+        for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const int row = r0 + g + 8 * h;
+            if (row >= s.m * a.group) continue;
+#pragma unroll
+            for (int z = 0; z < HDP / (8 * RUN); ++z)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float y[RUN];
+#pragma unroll
+                    for (int k = 0; k < RUN; ++k) y[k] = o[z * RUN + k][2 * h + b];
+                    put_run<T, HDP, RUN>(a, s, head, row, r0, element(2 * t + b, z), y, l[h], cut, slot);
+                }
+            if (t == 0) put_sums<T, HDP>(a, s, head, row, r0, m[h], l[h], cut, slot);
         }
     }
 };
 
-// RUN consecutive results of a row
-template <class T, int RUN> __device__ __forceinline__ void store_run(T* dst, const float (&x)[RUN]) {
-    if constexpr (sizeof(T) == 4) {
+// At most eight query rows: the other way round, tokens and elements are the rows of the tensor core's operand A and the queries the
+// eight columns of B, which halves its instructions and the registers of the sums.  A thread (g, t) has tokens g / 2 + 4 (g % 2) and 8 more of
+// the scores of query rows 2 t and 2 t + 1.  The maximum is only moved (and the sums rescaled, and the warp's lanes asked) when
+// it has grown by 2^SLACK; until then weights may pass 1, and LIFT leaves room for it.
+template <class T, int CODE, int HDP> struct RowsLow : Seen {
+    static constexpr bool WIDE = sizeof(T) == 4;          // hi + lo
+    static constexpr int STEPS = HDP / 16, LO = WIDE ? STEPS : 1, MT = HDP / 16;
+    static constexpr int PER = HDP == 64 ? 8 : 16;        // elements that a thread has of a piece of the values
+    uint32_t q0[STEPS], q1[STEPS], l0[LO], l1[LO];
+    float o[MT][4];                                       // pairs of elements (0, 1 and 2, 3) of rows 2 t (0, 2) and 2 t + 1 (1, 3)
+    float m[2], l[2], f[2];                               // of rows 2 t, 2 t + 1
+    int low[2], high[2];
+
+    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim;
+        set(a, s, r0, 8);
+        const int r = r0 + g, query = a.query_of(r);
+        const float up = load_query<T, HDP>(static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
+                                                (long long)(head * a.group + r - query * a.group) * D,
+                                            r < s.m * a.group, t, D, q0, q1, l0, l1);
 #pragma unroll
-        for (int k = 0; k < RUN; k += 4) *reinterpret_cast<float4*>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-    } else {
+        for (int b = 0; b < 2; ++b) {
+            const int row = r0 + 2 * t + b, p = s.len - s.m + a.query_of(row);
+            const bool on = row < s.m * a.group && p >= 0 && s.len > 0;
+            f[b] = a.scale * LOG2E / __shfl_sync(0xffffffffu, up, 4 * (2 * t + b));  // by a power of two: exact
+            m[b] = -INFINITY, l[b] = 0.f;
+            low[b] = on ? a.win.low(p) : 0;
+            high[b] = on ? a.win.high(p, s.len) : 0;
+        }
 #pragma unroll
-        for (int k = 0; k < RUN; k += 8) {
-            uint32_t w[4];
+        for (int n = 0; n < MT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+    }
+
+    __device__ __forceinline__ void tiles(const Tile (&d)[2], const uint8_t* const (&k)[2], const bool (&on)[2], int sinks) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, tok = (g >> 1) + 4 * (g & 1);
+        float s[2][4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(x[k + 2 * b], x[k + 2 * b + 1]);
-                w[b] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int u = 0; u < 2; ++u) {
+            s[u][0] = s[u][1] = s[u][2] = s[u][3] = on[u] ? 0.f : -INFINITY;
+            if (!on[u]) continue;
+#pragma unroll
+            for (int j = 0; j < HDP / 64; ++j) {
+                const uint4 wa = *reinterpret_cast<const uint4*>(k[u] + tile_at<HDP>(tok, 4 * j + t));
+                const uint4 wb = *reinterpret_cast<const uint4*>(k[u] + tile_at<HDP>(tok + 8, 4 * j + t));
+                const uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    uint32_t kk[4];
+                    half4<CODE>(a[x], kk[0], kk[2]);
+                    half4<CODE>(b[x], kk[1], kk[3]);
+                    if constexpr (WIDE) mma_f16(s[u], kk, l0[4 * j + x], l1[4 * j + x]);
+                    mma_f16(s[u], kk, q0[4 * j + x], q1[4 * j + x]);
+                }
             }
-            *reinterpret_cast<uint4*>(dst + k) = make_uint4(w[0], w[1], w[2], w[3]);
+            const bool full = whole(d[u], sinks);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const float c = f[b] * d[u].ks;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) s[u][2 * i + b] = fmaf(s[u][2 * i + b], c, d[u].lv);
+            }
+            if (!full) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = d[u].j0 + tok + 8 * i;
+                        if (!(j < high[b] && (j >= low[b] || j < sinks))) s[u][2 * i + b] = -INFINITY;
+                    }
+            }
+        }
+        float top[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) top[b] = fmaxf(fmaxf(s[0][b], s[0][2 + b]), fmaxf(s[1][b], s[1][2 + b]));
+        if (__any_sync(0xffffffffu, top[0] > m[0] + SLACK || top[1] > m[1] + SLACK)) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], x));
+                if (top[b] > m[b] + SLACK) {
+                    const float r = ex2(m[b] - top[b]);
+                    m[b] = top[b];
+                    l[b] *= r;
+#pragma unroll
+                    for (int n = 0; n < MT; ++n) o[n][b] *= r, o[n][2 + b] *= r;
+                }
+            }
+        }
+        uint32_t p[2][2], pl[2][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = ex2(s[u][e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1] - LIFT));
+            l[0] = fmaf(w[0] + w[2], d[u].iv, l[0]);
+            l[1] = fmaf(w[1] + w[3], d[u].iv, l[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {  // tokens by rows -> rows by tokens: what operand B takes
+                const uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
+                p[u][i] = transpose8(hi);
+                if constexpr (WIDE) pl[u][i] = transpose8(pack_rest(w[2 * i], w[2 * i + 1], hi));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (!on[u]) continue;
+            const uint8_t* v = k[u] + KV_BLOCK * HDP;
+#pragma unroll
+            for (int z = 0; z < HDP / (8 * PER); ++z) {
+                const int c = HDP == 64 ? g >> 1 : (((g & 1) << 2) | (g >> 1)) + 8 * z;
+                uint32_t w[4][PER / 4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const uint8_t* at = v + tile_at<HDP>(t + 4 * y, c);
+                    if constexpr (HDP == 64) {
+                        const uint2 e = *reinterpret_cast<const uint2*>(at + (g & 1) * 8);
+                        w[y][0] = e.x, w[y][1] = e.y;
+                    } else {
+                        const uint4 e = *reinterpret_cast<const uint4*>(at);
+                        w[y][0] = e.x, w[y][1] = e.y, w[y][2] = e.z, w[y][3] = e.w;
+                    }
+                    if (CODE == CAC_KV8_E4M3 && d[u].j0 + KV_BLOCK > hi_max && d[u].j0 + t + 4 * y >= hi_max) {
+                        // a token past the end: its codes may be anything, and a weight of 0 times NaN is NaN
+#pragma unroll
+                        for (int x = 0; x < PER / 4; ++x) w[y][x] = 0;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < PER / 4; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {  // elements 4 x + 2 y and 4 x + 2 y + 1 of four tokens
+                        const uint32_t sel = y ? 0x7362 : 0x5140;
+                        uint32_t vv[4];
+                        half4<CODE>(__byte_perm(w[0][x], w[1][x], sel), vv[0], vv[1]);
+                        half4<CODE>(__byte_perm(w[2][x], w[3][x], sel), vv[2], vv[3]);
+                        float(&sum)[4] = o[(z * PER + 4 * x + 2 * y) / 2];
+                        if constexpr (WIDE) {
+                            // sums of one tile, added here: the tensor core cuts sums off where fp32 would round
+                            float part[4] = {};
+                            mma_f16(part, vv, pl[u][0], pl[u][1]);
+                            mma_f16(part, vv, p[u][0], p[u][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum[e] += part[e];
+                        } else {
+                            mma_f16(sum, vv, p[u][0], p[u][1]);
+                        }
+                    }
+            }
         }
     }
-}
+
+    __device__ __forceinline__ void emit(const KvAttend& a, const SeqWork& s, int head, int r0, const Partials* cut, int slot) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) l[b] += __shfl_xor_sync(0xffffffffu, l[b], x);
+            const int row = r0 + 2 * t + b;
+            if (row >= s.m * a.group) continue;
+#pragma unroll
+            for (int z = 0; z < HDP / (8 * PER); ++z) {
+                float y[PER];
+#pragma unroll
+                for (int k = 0; k < PER; ++k) y[k] = o[(z * PER + k) / 2][2 * (k & 1) + b];
+                put_run<T, HDP, PER>(a, s, head, row, r0, HDP == 64 ? g * 8 : (((g & 1) << 2) | (g >> 1)) * 16 + 128 * z, y, l[b],
+                                     cut, slot);
+            }
+            if (g == 0) put_sums<T, HDP>(a, s, head, row, r0, m[b], l[b], cut, slot);
+        }
+        // only a sequence with more rows than max_new has rows 8 .. 15: they see nothing
+        const int row = r0 + 8 + g;
+        if (row < s.m * a.group && !cut) {
+            const int D = a.c.head_dim, query = a.query_of(row), qh = head * a.group + row - query * a.group;
+            T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D;
+            for (int e = t; e < D; e += 4) dst[e] = from_f<T>(0.f);
+            if (t == 0 && a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] = -INFINITY;
+        }
+    }
+};
 
 // The call's split over warps: tile x of `total` belongs to the warp w with
 // begin(w) <= x < begin(w + 1).
@@ -383,15 +634,6 @@ struct Deal {
     }
 };
 
-constexpr int MOST_WARPS = 12;   // of a block
-
-// Partial sums of units that were cut.  Slot 2 w: the unit that warp w's share begins in; slot 2 w + 1: the one that it ends in,
-// when that is another.  After the warps' slots the same for the blocks.
-struct Partials {
-    float *o, *ml;               // [slot][16][HDP], [slot][16][2]
-    long long* first;            // [TA_SEQS + 1] tiles before each sequence
-    int warps;
-};
 template <int HDP> inline size_t partial_bytes(int sms) {
     return (size_t)sms * (MOST_WARPS + 1) * 2 * 16 * (HDP + 2) * 4 + (TA_SEQS + 2) * 8;
 }
@@ -475,7 +717,7 @@ template <class T, int HDP, bool SPLIT> struct Shape {
 template <class T, int CODE, int HDP, bool LOW, bool SPLIT>
 __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HDP, SPLIT>::BLOCKS))
     kv_attend_kernel(const __grid_constant__ KvAttend a, void* space) {
-    using R = Rows<T, CODE, HDP, LOW>;
+    using R = std::conditional_t<LOW, RowsLow<T, CODE, HDP>, Rows<T, CODE, HDP>>;
     using S = Shape<T, HDP, SPLIT>;
     constexpr int STAGES = S::STAGES, STAGE = S::STAGE, WARPS = S::WARPS, CH = HDP / 16;
     extern __shared__ __align__(128) uint8_t ring_all[];
@@ -635,53 +877,8 @@ __global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HD
             x += 1 + two;
             from_stage = two ? (s1 + 1 == STAGES ? 0 : s1 + 1) : s1;
         }
-        r.finish();
-        const int g = lane >> 2, t = lane & 3;
         const bool whole = from == u0 && end == u1;
-#pragma unroll
-        for (int h = 0; h < R::H; ++h) {
-            const int row = r0 + g + 8 * h;
-            if (row >= s.m * a.group) continue;
-            const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
-            const float inv = r.l[h] > 0.f || r.l[h] != r.l[h] ? 1.f / r.l[h] : 0.f;
-            const int slot = 2 * (blockIdx.x * WARPS + warp) + (from != x0);
-#pragma unroll
-            for (int z = 0; z < HDP / (8 * R::RUN); ++z)
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int e = R::element(2 * t + b, z);
-                    float y[R::RUN];
-#pragma unroll
-                    for (int k = 0; k < R::RUN; ++k) y[k] = r.o[z * R::RUN + k][2 * h + b];
-                    if (whole) {
-                        if (e >= D) continue;
-#pragma unroll
-                        for (int k = 0; k < R::RUN; ++k) y[k] *= inv;
-                        store_run<T, R::RUN>(static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride +
-                                                 (long long)qh * D + e, y);
-                    } else {
-                        store_run<float, R::RUN>(part.o + ((size_t)slot * 16 + g + 8 * h) * HDP + e, y);
-                    }
-                }
-            if (t == 0) {
-                if (whole) {
-                    if (a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] =
-                        r.l[h] > 0.f || r.l[h] != r.l[h] ? (r.m[h] - LIFT + log2f(r.l[h])) * LN2 : -INFINITY;
-                } else {
-                    part.ml[((size_t)slot * 16 + g + 8 * h) * 2] = r.m[h];
-                    part.ml[((size_t)slot * 16 + g + 8 * h) * 2 + 1] = r.l[h];
-                }
-            }
-        }
-        if constexpr (LOW) {
-            const int row = r0 + 8 + g;  // only a sequence with more rows than max_new has any: they see nothing
-            if (row < s.m * a.group) {
-                const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
-                T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D;
-                for (int e = t; e < D; e += 4) dst[e] = from_f<T>(0.f);
-                if (t == 0 && a.lse) a.lse[(s.row0 + (long long)query) * a.heads + qh] = -INFINITY;
-            }
-        }
+        r.emit(a, s, head, r0, whole ? nullptr : &part, 2 * (blockIdx.x * WARPS + warp) + (from != x0));
     }
     cp_wait<0>();
     if constexpr (SPLIT) {

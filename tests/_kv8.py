@@ -121,7 +121,7 @@ def bounds(out, lse, mass, size, D, keys, dtype):
     score, so a relative error of its weight).  The exponent's argument, a difference of numbers no larger than the
     score's bound + 128, adds 2^-23 of those, and the exponential 2^-21.  Weights enter the product with V rounded to
     11 bits for bf16 activations (2^-11), to 21 for fp32 (hi + lo); each is a relative error of a weight (of those over
-    2^-29 of the largest; the others are off by 2^-40 of it, far under what is allowed here).  Sums over the keys in fp32 add keys * 2^-24 at most.  Weight errors
+    2^-21 of the largest; the others are off by 2^-32 of it at most, 2^-38 for fp32, far under what is allowed here).  Sums over the keys in fp32 add keys * 2^-24 at most.  Weight errors
     reach the output twice, in the sum and in its norm.  The output is rounded once."""
     w = (D + 8) * 2.0 ** -24 * size + 2.0 ** -23 * (size + 128) + 2.0 ** -21
     e = w + (2.0 ** -11 if dtype == torch.bfloat16 else 2.0 ** -20) + (keys + 16) * 2.0 ** -24

@@ -512,6 +512,22 @@ def test_unlike_scales_of_blocks():
     b.attend([0], [3], scale=-0.3)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim,group", [(64, 8), (128, 4), (256, 7), (64, 12)])
+def test_maxima_that_rise_and_fall(dtype, dim, group):
+    """Logits that climb by less or more than a few powers of two a block, fall, or stand still, in rows side by side."""
+    b = Both(dim=dim, page=32, dtype=dtype, n_pages=64)
+    line = torch.randn(dim, generator=torch.Generator().manual_seed(3))
+    line /= line.norm()
+    tokens = 430
+    k = b.rand(tokens, 2, dim, gain=0.05) + (torch.arange(tokens) / 16.0)[:, None, None].to(dtype) * line.to(dtype)
+    b.append([0], [tokens], k=k.to(dtype))
+    step = torch.tensor([0.0, 0.3, 0.7, 1.0, 1.5, 4.0, -0.7, -4.0, 12.0, -12.0, 2.0, 1.9])   # powers of two a block
+    q = step[torch.arange(2 * group) % 12, None] * 0.6931 * dim ** 0.5 * line
+    b.attend([0], [1], group=group, q=q[None].to(dtype))
+    b.attend([0], [1], group=group, q=q[None].to(dtype), left=100, sinks=20)
+
+
 def test_non_finite_queries_stay_in_their_rows():
     b = Both(dim=64, page=16, dtype=F32)
     b.append([0], [40])
