@@ -702,8 +702,8 @@ __device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s
 
 // Warps of a block, and the tiles that each has in flight or at hand (two matrices of 16 rows of HDP bytes).  The sums of 16 rows
 // take HDP / 2 registers and an fp32 query's two halves HDP / 2 more, which leaves room for 12 warps, or 8.
-template <class T, int HDP, bool SPLIT> struct Shape {
-    static constexpr int WARPS = !SPLIT ? 4 : HDP == 64 ? 12 : 8;
+template <class T, int HDP, bool LOW, bool SPLIT> struct Shape {
+    static constexpr int WARPS = !SPLIT ? 4 : HDP == 64 || (HDP == 128 && LOW && sizeof(T) == 2) ? 12 : 8;
     static constexpr int STAGE = 2 * KV_BLOCK * HDP;
     static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : 196608 / (WARPS * STAGE);
     static constexpr int BYTES = WARPS * STAGES * STAGE;
@@ -715,10 +715,10 @@ template <class T, int HDP, bool SPLIT> struct Shape {
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
 // whole unit (short windows, where a unit has a handful of tiles): nothing has to be joined.
 template <class T, int CODE, int HDP, bool LOW, bool SPLIT>
-__global__ void __launch_bounds__(Shape<T, HDP, SPLIT>::WARPS * 32, (Shape<T, HDP, SPLIT>::BLOCKS))
+__global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<T, HDP, LOW, SPLIT>::BLOCKS))
     kv_attend_kernel(const __grid_constant__ KvAttend a, void* space) {
     using R = std::conditional_t<LOW, RowsLow<T, CODE, HDP>, Rows<T, CODE, HDP>>;
-    using S = Shape<T, HDP, SPLIT>;
+    using S = Shape<T, HDP, LOW, SPLIT>;
     constexpr int STAGES = S::STAGES, STAGE = S::STAGE, WARPS = S::WARPS, CH = HDP / 16;
     extern __shared__ __align__(128) uint8_t ring_all[];
     __shared__ long long s_first[SPLIT ? TA_SEQS + 1 : 1];
@@ -966,8 +966,8 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
 
 template <class T, int CODE, int HDP, bool LOW>
 cudaError_t launch_attend(const KvAttend& a, bool split, int sms, void* space, cudaStream_t s) {
-    using S1 = Shape<T, HDP, true>;
-    using S0 = Shape<T, HDP, false>;
+    using S1 = Shape<T, HDP, LOW, true>;
+    using S0 = Shape<T, HDP, LOW, false>;
     const int smem = split ? S1::BYTES : S0::BYTES;
     const auto kernel = split ? kv_attend_kernel<T, CODE, HDP, LOW, true> : kv_attend_kernel<T, CODE, HDP, LOW, false>;
     static std::atomic<uint64_t> ready[2];  // devices on which the kernels may use their shared memory
