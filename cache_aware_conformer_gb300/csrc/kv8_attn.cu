@@ -192,7 +192,7 @@ template <class T, int RUN> __device__ __forceinline__ void store_run(T* dst, co
     }
 }
 
-constexpr int MOST_WARPS = 12;   // of a block
+constexpr int MOST_WARPS = 12;   // of a block (16 at most: join_warp has a lane for each)
 
 // Partial sums of units that were cut.  Slot 2 w: the unit that warp w's share begins in; slot 2 w + 1: the one that it ends in,
 // when that is another.  After the warps' slots the same for the blocks.
@@ -647,57 +647,94 @@ template <int HDP> __device__ __forceinline__ Partials partials_at(void* space, 
 }
 
 // The parts of a unit in slots `first`, then next, next + 2, ... (`more` of those) are added up: this warp does rows mine, mine +
-// more + 1, ... and writes them out, or, with to >= 0, into that slot.
-template <class T, int HDP>
-__device__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more, int mine, int to) {
+// more, ... and writes them out, or, with to >= 0, into that slot.  ROWS rows and PARTS parts are on their way at once.
+template <class T, int HDP, int ROWS, int PARTS>
+__device__ __forceinline__ void join_rows(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more,
+                                          int mine, int to) {
     constexpr int PER = HDP / 32;
-    const int lane = threadIdx.x & 31, kvh = a.c.kv_heads, head = unit % kvh, r0 = unit / kvh * 16;
+    const int lane = threadIdx.x & 31, kvh = a.c.kv_heads, head = unit % kvh, r0 = unit / kvh * 16, step = more;
     const int rows = min(16, s.m * a.group - r0);
-    const int slot = lane == 0 ? first : next + 2 * (lane - 1);
-    for (int r = mine; r < rows; r += more + 1) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane <= more) ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + (size_t)slot * 16 + r);
-        float v[MOST_WARPS][PER];  // all parts on their way at once
+    auto slot = [&](int k) { return (size_t)(k == 0 ? first : next + 2 * (k - 1)) * 16; };
+#pragma unroll 1
+    for (int r = mine; r < rows; r += ROWS * step) {
+        float2 ml[ROWS];
 #pragma unroll
-        for (int k = 0; k < MOST_WARPS; ++k)
-            if (k <= more) {
-                const float* src = p.o + ((size_t)(k == 0 ? first : next + 2 * (k - 1)) * 16 + r) * HDP + lane * PER;
-#pragma unroll
-                for (int c = 0; c < PER; c += 2) {
-                    const float2 y = __ldcg(reinterpret_cast<const float2*>(src + c));
-                    v[k][c] = y.x, v[k][c + 1] = y.y;
-                }
-            }
-        float top = ml.x;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float f = ex2(ml.x - (top == -INFINITY ? 0.f : top));
-        float l = lane <= more ? ml.y * f : 0.f;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-        float o[PER] = {};
-#pragma unroll
-        for (int k = 0; k < MOST_WARPS; ++k) {
-            const float w = __shfl_sync(0xffffffffu, f, k);
-            if (k <= more)
-#pragma unroll
-                for (int c = 0; c < PER; ++c) o[c] = fmaf(v[k][c], w, o[c]);
+        for (int b = 0; b < ROWS; ++b) {
+            ml[b] = make_float2(-INFINITY, 0.f);
+            if (lane <= more && r + b * step < rows) ml[b] = __ldcg(reinterpret_cast<const float2*>(p.ml) + slot(lane) + r + b * step);
         }
-        if (to >= 0) {
+        float o[ROWS][PER] = {}, f[ROWS], top[ROWS], l[ROWS];
+#pragma unroll 1
+        for (int k0 = 0; k0 <= more; k0 += PARTS) {
+            float v[PARTS][ROWS][PER];
 #pragma unroll
-            for (int c = 0; c < PER; ++c) p.o[((size_t)to * 16 + r) * HDP + lane * PER + c] = o[c];
-            if (lane == 0) p.ml[((size_t)to * 16 + r) * 2] = top, p.ml[((size_t)to * 16 + r) * 2 + 1] = l;
-        } else {
-            const int row = r0 + r, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
-            const bool seen = l > 0.f || l != l;
-            T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
+            for (int k = 0; k < PARTS; ++k)
 #pragma unroll
-            for (int c = 0; c < PER; ++c)
-                if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[c] / l : 0.f);
-            if (lane == 0 && a.lse)
-                a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+                for (int b = 0; b < ROWS; ++b)
+#pragma unroll
+                    for (int c = 0; c < PER; c += 2) {
+                        float2 y = make_float2(0.f, 0.f);
+                        if (k0 + k <= more && r + b * step < rows)
+                            y = __ldcg(reinterpret_cast<const float2*>(p.o + (slot(k0 + k) + r + b * step) * HDP + lane * PER + c));
+                        v[k][b][c] = y.x, v[k][b][c + 1] = y.y;
+                    }
+            if (k0 == 0) {
+#pragma unroll
+                for (int b = 0; b < ROWS; ++b) top[b] = ml[b].x;
+#pragma unroll
+                for (int d = 8; d; d >>= 1)  // lanes 0 .. 15 hold the parts
+#pragma unroll
+                    for (int b = 0; b < ROWS; ++b) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], d, 16));
+#pragma unroll
+                for (int b = 0; b < ROWS; ++b) f[b] = ex2(ml[b].x - (top[b] == -INFINITY ? 0.f : top[b])), l[b] = ml[b].y * f[b];
+#pragma unroll
+                for (int d = 8; d; d >>= 1)
+#pragma unroll
+                    for (int b = 0; b < ROWS; ++b) l[b] += __shfl_xor_sync(0xffffffffu, l[b], d, 16);
+#pragma unroll
+                for (int b = 0; b < ROWS; ++b) top[b] = __shfl_sync(0xffffffffu, top[b], 0), l[b] = __shfl_sync(0xffffffffu, l[b], 0);
+            }
+#pragma unroll
+            for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+                for (int b = 0; b < ROWS; ++b) {
+                    const float w = __shfl_sync(0xffffffffu, f[b], k0 + k);
+                    if (k0 + k <= more)
+#pragma unroll
+                        for (int c = 0; c < PER; ++c) o[b][c] = fmaf(v[k][b][c], w, o[b][c]);
+                }
+        }
+#pragma unroll
+        for (int b = 0; b < ROWS; ++b) {
+            const int at = r + b * step;
+            if (at >= rows) break;
+            if (to >= 0) {
+#pragma unroll
+                for (int c = 0; c < PER; ++c) p.o[((size_t)to * 16 + at) * HDP + lane * PER + c] = o[b][c];
+                if (lane == 0) p.ml[((size_t)to * 16 + at) * 2] = top[b], p.ml[((size_t)to * 16 + at) * 2 + 1] = l[b];
+            } else {
+                const int row = r0 + at, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
+                const bool seen = l[b] > 0.f || l[b] != l[b];
+                T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
+#pragma unroll
+                for (int c = 0; c < PER; ++c)
+                    if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[b][c] / l[b] : 0.f);
+                if (lane == 0 && a.lse)
+                    a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top[b] - LIFT + log2f(l[b])) * LN2 : -INFINITY;
+            }
         }
     }
+}
+
+// While other blocks still stream, each wait for memory takes 4 us: many warps have few rows each and few have many, and either
+// way all of a warp's loads should be on their way at once.
+template <class T, int HDP>
+__device__ __forceinline__ void join_warp(const KvAttend& a, const Partials& p, const SeqWork& s, int unit, int first, int next, int more,
+                                          int mine, int to) {
+    constexpr int WIDTH = HDP > 128 ? 2 : 1;
+    if (more == 1) join_rows<T, HDP, 8 / WIDTH, 2>(a, p, s, unit, first, next, more, mine, to);
+    else if (more < 4) join_rows<T, HDP, 4 / WIDTH, 4>(a, p, s, unit, first, next, more, mine, to);
+    else join_rows<T, HDP, 1, MOST_WARPS>(a, p, s, unit, first, next, more, mine, to);
 }
 
 // Warps of a block, and the tiles that each has in flight or at hand (two matrices of 16 rows of HDP bytes).  The sums of 16 rows
@@ -708,7 +745,7 @@ template <class T, int HDP, bool LOW, bool SPLIT> struct Shape {
     static constexpr int STAGES = !SPLIT ? (HDP == 256 ? 3 : 4) : 196608 / (WARPS * STAGE);
     static constexpr int BYTES = WARPS * STAGES * STAGE;
     static constexpr int BLOCKS = !SPLIT && HDP == 64 ? 4 : 1;  // of an SM
-    static_assert(WARPS <= MOST_WARPS, "the workspace has room for the parts of so many");
+    static_assert(WARPS <= MOST_WARPS && MOST_WARPS <= 16, "the workspace has room for the parts of so many");
     static_assert(BYTES + (SPLIT ? 20 * 1024 : 0) <= 227 * 1024, "shared memory");
 };
 
@@ -877,8 +914,12 @@ __global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<
             x += 1 + two;
             from_stage = two ? (s1 + 1 == STAGES ? 0 : s1 + 1) : s1;
         }
-        const bool whole = from == u0 && end == u1;
-        r.emit(a, s, head, r0, whole ? nullptr : &part, 2 * (blockIdx.x * WARPS + warp) + (from != x0));
+        const bool begins = from == u0, ends = end == u1;
+        int slot = 2 * (blockIdx.x * WARPS + warp) + (from != x0);
+        // a part that no other warp of the block has one to add to: the block's
+        if (!begins && ends && warp == 0) slot = 2 * part.warps + 2 * blockIdx.x;
+        if (begins && !ends && warp == WARPS - 1) slot = 2 * part.warps + 2 * blockIdx.x + 1;
+        r.emit(a, s, head, r0, begins && ends ? nullptr : &part, slot);
     }
     cp_wait<0>();
     if constexpr (SPLIT) {
@@ -886,23 +927,15 @@ __global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<
         const Deal deal(s_first[n], gridDim.x * WARPS);
         const int w = blockIdx.x * WARPS + warp;
         const long long b0 = deal.begin(blockIdx.x * WARPS), b1 = deal.begin((blockIdx.x + 1) * WARPS);
-        // the unit that the share begins in, then the one that it ends in: the warps of the block that hold parts of a cut
-        // unit share its rows out among them
-#pragma unroll 1
-        for (int which = 0; which < 2 && x0 < x1; ++which) {
-            const long long at = which ? x1 - 1 : x0;
-            i = warp_last_le(n, at, [&](int k) { return s_first[k]; });
-            s = s_seq[i];
-            unit = (int)((at - s_first[i]) / s.tiles);
-            u0 = s_first[i] + (long long)unit * s.tiles, u1 = u0 + s.tiles;
-            if ((which && u0 <= x0) || (u0 >= x0 && u1 <= x1)) continue;  // done as the first, or whole and written
-            int w0 = w, w1 = w;
+        // The unit that the share ends in, if the block's next warp goes on with it: the warps of the block that hold parts of it, but
+        // the last, share its rows out among them, so that no warp has rows of two units.
+        if (x0 < x1 && u1 > x1 && x1 < b1) {
+            int w0 = w, w1 = w + 1;
             while (w0 > (int)blockIdx.x * WARPS && deal.begin(w0) > u0) --w0;
-            while (w1 + 1 < (int)(blockIdx.x + 1) * WARPS && deal.begin(w1 + 1) < u1 && deal.begin(w1 + 1) < b1) ++w1;
+            while (w1 + 1 < (int)(blockIdx.x + 1) * WARPS && deal.begin(w1 + 1) < min(u1, b1)) ++w1;
             const bool done = u0 >= b0 && u1 <= b1;
             const int to = 2 * part.warps + 2 * blockIdx.x + (u0 > b0);
-            join_warp<T, HDP>(a, part, s, unit, 2 * w0 + (deal.begin(w0) < u0),
-                              2 * (w0 + 1), w1 - w0, w - w0, done ? -1 : to);
+            join_warp<T, HDP>(a, part, s, unit, 2 * w0 + (deal.begin(w0) < u0), 2 * (w0 + 1), w1 - w0, w - w0, done ? -1 : to);
         }
     }
 }
