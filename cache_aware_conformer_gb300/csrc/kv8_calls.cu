@@ -18,8 +18,9 @@ int sm_count(int device) {
 }
 
 // Whether units are cut and dealt out, or a warp takes a whole one: the latter saves the deal and the join, but takes about 0.45 us
-// a tile.  Measured (2 bf16 queries, windows of 220 / 450 / 900 tokens, us): 16 sequences of 8 heads 11.5 / 18.7 / 31.8 whole, 22.9 /
-// 24.1 / 24.8 dealt out; 256 sequences 18.0 / 32.8 / 56.5 and 36.3 / 52.5 / 75.4; one of 500 tokens 23.9 and 16.4.
+// a tile.  Measured (2 bf16 queries, windows of 220 / 450 / 900 tokens, us): 16 sequences of 8 heads 11 / 17 / 28 whole, 18 /
+// 19 / 20 dealt out; 256 sequences 17 / 30 / 50 and 28 / 45 / 66; 64 of heads 128 wide 15 / 26 / 45 and 21 / 26 / 38; one of 500 tokens 21
+// and 17.
 bool splits(const cac_kv8& c, int n, int sms, int max_new, int left, int chunk, int sinks) {
     long long tokens = (long long)c.max_pages * c.page_tokens;
     if (left >= 0) tokens = std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);

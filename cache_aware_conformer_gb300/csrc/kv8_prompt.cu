@@ -18,6 +18,10 @@
 // until then weights may pass 1, and their lift leaves room for it.
 //
 // Every wait is bounded; one that gives up latches CAC_E_TIMEOUT, and the block unwinds.
+// Measured: two prompts of 5,001 and 8,000 tokens, 8 K/V heads, group 4, 128 wide, int8, bf16: 681 us, 1.0 PFLOP/s of the
+// arithmetic under the mask, tensor core active 43 % of the time.  A 128-token tile takes 4,280 clocks where its products alone take 2,048:
+// the scores' operands pass through shared memory at 128 KB a tile beside the converters' 64 KB, and a softmax warp waits for TMEM, the
+// maximum and the exponentials in turn.  Some 16,000 clocks of a block are its beginning and end.
 // Shared and tensor memory allow one block an SM.  The TMEM is taken after the wait on the
 // kernel before and before the next kernel may start, so that no block can hold it
 // while it waits for one that needs it.
@@ -621,16 +625,17 @@ template <class T, int CODE> cudaError_t launch_prompt(const KvAttend& a, cudaSt
 }  // namespace
 
 // Against kv_attend_kernel, which deals 16-row tiles out over the whole card (and re-reads K and V for each): a 128-token tile of a
-// block here takes as long as it takes an SM for 2.6 of its 16-row tiles, but the card fills in steps of a block an SM.  Measured
+// block here takes as long as it takes an SM for two to three of its 16-row tiles, but the card fills in steps of a block an SM.  Measured
 // (bf16, group 4, head_dim 128; us for 16 / 32 / 64 / 128 / 256 rows): 32 sequences of 4,000 tokens, 8 K/V heads,
-// 110 / 155 / 249 / 436 / 801 there, 155 / 155 / 153 / 154 / 170 here; 4 of 8,000, 47 / 68 / 99 / 147 / 240 and 128 / 127 /
-// 127 / 121 / 140; one of 30,000, 2 heads, 39 / 35 / 40 / 51 / 77 and 454 / 454 / 455 / 424 / 489.  The ratio at the crossings is 1.5 to 1.7.
+// 87 / 130 / 223 / 404 / 764 there, 155 / 156 / 155 / 155 / 172 here; 4 of 8,000, 41 / 55 / 81 / 128 / 217 and 128 / 127 /
+// 127 / 122 / 140; one of 30,000, 2 heads, 31 / 33 / 38 / 49 / 70 and 454 / 454 / 455 / 424 / 489; 64 of 1,000, 8 heads of 64, group 1,
+// 39 / 53 / 84 for 16 / 32 / 64 rows and 75 here.  The ratio at the crossings is 1.6 to 2.8.
 bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows) {
     if (a.c.head_dim > 128) return false;
     const int block = dtype == CAC_DTYPE_F32 && a.c.head_dim > 64 ? PT_ROWS : 2 * PT_ROWS;
     const long long units = (long long)a.rows.n * a.c.kv_heads;
     const long long waves = (units * ((rows + block - 1) / block) + sms - 1) / sms;
-    return units * ((rows + 15) / 16) * 5 > waves * sms * 8;
+    return units * ((rows + 15) / 16) > 2 * waves * sms;
 }
 
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s) {
