@@ -893,7 +893,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<
     if (x < x1) enter();
 #pragma unroll 1
     for (int k = 0; k < STAGES; ++k) fetch(x0 + k);
-    if constexpr (SPLIT) next = look(x0 + 32 + lane);
+    if (SPLIT || x1 > 32) next = look(x0 + 32 + lane);
     int from_stage = 0;
 
     bool entered = true;
@@ -902,7 +902,7 @@ __global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<
         entered = false;
         const long long end = min(u1, x1), from = x;
         while (x < end) {
-            if (SPLIT && x - base >= 32) {
+            if (x - base >= 32) {
                 base += 32;
                 now = next;
                 next = look(base + 32 + lane);

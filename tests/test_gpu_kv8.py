@@ -543,6 +543,80 @@ def test_non_finite_queries_stay_in_their_rows():
     assert torch.isfinite(got[9, 3]).all()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_non_finite_queries_of_few_rows(dtype, bad):
+    b = Both(dim=128, page=16, dtype=dtype, n_pages=100)
+    b.append([0, 1], [600, 33])
+    b.cache.check()
+    q = torch.randn(4, 4, 128, device="cuda").to(dtype)              # two tokens each, two heads to a K/V head: four rows
+    want = b.cache.attend(0, b.ids([0, 1]), q)
+    q2 = q.clone()
+    q2[1, 2, 5] = bad
+    got = b.cache.attend(0, b.ids([0, 1]), q2)
+    ok = torch.ones(4, 4, dtype=torch.bool, device="cuda")
+    ok[1, 2] = False
+    assert not torch.isfinite(got[1, 2]).any() and torch.equal(got[ok], want[ok])
+
+
+@pytest.mark.parametrize("n,longest,left,group,dim", [(160, 900, 950, 4, 64), (20, 480, 500, 12, 64), (21, 470, 490, 1, 128),
+                                                      (40, 450, 470, 7, 128), (13, 400, 420, 16, 64)])
+def test_units_cut_anywhere_and_whole_units_agree(n, longest, left, group, dim):
+    """A window that shows everything makes a warp take whole units; without one the tiles are dealt out over the card and
+    joined.  Both are within bounds() of the exact result: with sums of |q k| of at most 8 that is 1.4e-4 of sum p |v| <= 4 for each
+    weight, twice for each side."""
+    cfg = Kv8Config(1, 8, dim, 16, n * (longest // 16 + 1), n, 4096)
+    from cache_aware_conformer_gb300 import native
+    cache = native.Kv8Cache(cfg)
+    gen = torch.Generator().manual_seed(n)
+    ids = torch.randperm(n, generator=gen).to(torch.int32).cuda()
+    counts = torch.randint(1, longest + 1, (n,), generator=gen, dtype=torch.int32)
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32), counts.cumsum(0).to(torch.int32)]).cuda()
+    k = torch.randn(int(counts.sum()), 8, dim, generator=gen).clamp(-4, 4).cuda() / 2
+    v = torch.randn(int(counts.sum()), 8, dim, generator=gen).clamp(-4, 4).cuda()
+    cache.extend(ids, starts=starts)
+    cache.write(0, ids, k, v, starts=starts)
+    q = torch.randn(n, 8 * group, dim, generator=gen).clamp(-4, 4).cuda() / 2
+    whole, wl = cache.attend(0, ids, q, att_left=left, lse=True)
+    dealt, dl = cache.attend(0, ids, q, lse=True)
+    cache.check()
+    assert torch.isfinite(whole).all() and torch.isfinite(wl).all()
+    assert (whole - dealt).abs().max() <= 4 * 1.4e-4 * 4 and (wl - dl).abs().max() <= 4e-4
+    assert not torch.equal(whole, dealt)     # the two ways are two ways
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("code,dim,group,left,chunk,sinks", [("int8", 64, 2, -1, 1, 0), ("e4m3", 128, 3, 500, 4, 5), ("int8", 80, 1, 1700, 1, 33),
+                                                             ("e4m3", 64, 8, 1001, 16, 0)])
+def test_queries_of_a_prompt_and_alone_agree(dtype, code, dim, group, left, chunk, sinks):
+    """The last queries of long pieces against the same queries asked for alone, which other kernels answer.  Tolerances as in
+    bounds(): sums of |q k| of at most 8, sum p |v| <= 4.1, 3,600 keys."""
+    n, heads = 5, 4
+    counts = torch.tensor([3600, 1201, 2222, 1500, 2999], dtype=torch.int32)
+    from cache_aware_conformer_gb300 import native
+    cache = native.Kv8Cache(Kv8Config(1, heads, dim, 16, 760, n, 240, code))
+    gen = torch.Generator().manual_seed(dim + group)
+    ids = torch.tensor([3, 0, 4, 1, 2], dtype=torch.int32, device="cuda")
+    starts = torch.cat([torch.zeros(1, dtype=torch.int32), counts.cumsum(0).to(torch.int32)]).cuda()
+    k = (torch.randn(int(counts.sum()), heads, dim, generator=gen).clamp(-4, 4) / 2).cuda().to(dtype)
+    v = torch.randn(int(counts.sum()), heads, dim, generator=gen).clamp(-4, 4).cuda().to(dtype)
+    cache.extend(ids, starts=starts)
+    cache.write(0, ids, k, v, starts=starts)
+    q = (torch.randn(n, 1200, heads * group, dim, generator=gen).clamp(-4, 4) / 2).cuda().to(dtype)
+    args = dict(att_left=left, att_chunk=chunk, sinks=sinks, lse=True)
+    out, lse = cache.attend(0, ids, q.reshape(n * 1200, -1, dim), **args)
+    out, lse = out.reshape(n, 1200, -1, dim).float(), lse.reshape(n, 1200, -1)
+    w = (dim + 8) * 2.0 ** -24 * 8 + 2.0 ** -23 * 136 + 2.0 ** -21 + 3600 * 2.0 ** -24
+    e = w + (2.0 ** -11 if dtype == BF16 else 2.0 ** -20)
+    for m in (1, 2, 5, 40):
+        o, s = cache.attend(0, ids, q[:, -m:].reshape(n * m, -1, dim), **args)
+        o, s = o.reshape(n, m, -1, dim).float(), s.reshape(n, m, -1)
+        cache.check()
+        assert torch.isfinite(s).all()
+        assert ((o - out[:, -m:]).abs() <= 4 * e * 4.1 + torch.finfo(dtype).eps * o.abs()).all(), m
+        assert (s - lse[:, -m:]).abs().max() <= 2 * (w + 2.0 ** -22 * 140), m
+
+
 def test_the_same_sequence_twice_and_deterministic():
     b = Both(dim=128, page=32, dtype=BF16, n_pages=300, max_pages=200)
     b.append([0, 1], [4000, 50])
