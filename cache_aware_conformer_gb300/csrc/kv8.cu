@@ -385,12 +385,12 @@ __device__ __forceinline__ KvPlace place_of(const KvWrite& a, int b) {
     const int row0 = a.rows.at(i), m = a.rows.at(i + 1) - row0, id = a.ids[i];
     if (m == 0) return p;
     int error = 0;
-    if (id < 0 || id >= c.max_seqs || row0 < 0 || m < 0 || row0 + (long long)m > a.rows.rows) {
+    if (id < 0 || id >= c.max_seqs || row0 < 0 || m < 0 || row0 + (long long)m > a.rows.rows || nth < 0) {  // nth < 0: starts that fall
         error = CAC_E_BOUNDS;
     } else {
         const int2 pending = *reinterpret_cast<const int2*>(c.pending + 2 * id);
         const int base = c.lens[id] - m;                                     // first new token
-        const int t0 = (base / KV_BLOCK + nth) * KV_BLOCK;  // first token of the block
+        const int t0 = (base / KV_BLOCK + min(nth, m / KV_BLOCK + 2)) * KV_BLOCK;  // first token of the block
         if (pending.x != m || pending.y != i) {
             error = CAC_E_STATE;
         } else if (t0 < base + m) {

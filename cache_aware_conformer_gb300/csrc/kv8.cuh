@@ -34,8 +34,8 @@ struct KvRows {
     __device__ __forceinline__ int at(int i) const { return starts ? __ldg(starts + i) : base + each * i; }
 };
 
-// The last i in [0, n) with f(i) <= x, for a function that never falls; -1 where
-// f(0) > x.  A whole warp calls it: 32 places are tried at once.
+// The last i in [0, n) with f(i) <= x, for a function that never falls (one that does may give an i with
+// f(i) > x); -1 where f(0) > x.  A whole warp calls it: 32 places are tried at once.
 template <class F> __device__ __forceinline__ int warp_last_le(int n, long long x, F f) {
     const int lane = threadIdx.x & 31;
     int lo = 0, len = n;  // the answer is lo - 1 or in [lo, lo + len)
@@ -134,7 +134,12 @@ struct KvAttend {
         const long long before = rows.at(0);
         auto first = [&](int i) { return (rows.at(i) - before) * group / size + i; };
         const int i = warp_last_le(rows.n, b, first);
-        return make_int2(i, i < 0 ? 0 : b - (int)first(i));
+        const long long y = i < 0 ? 0 : b - first(i);
+        if (y < 0) {  // starts that fall
+            latch_error(c.status, CAC_E_BOUNDS);
+            return make_int2(-1, 0);
+        }
+        return make_int2(i, (int)y);
     }
 };
 

@@ -134,7 +134,7 @@ int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const i
  *   max_new: no sequence has more rows than this (one that has latches
  *         CAC_E_BOUNDS, and its rows are zero); used where starts is given.  A
  *         sequence whose rows pass `rows` latches CAC_E_BOUNDS too, and its rows are
- *         left as they were
+ *         left as they were, as do starts that fall
  *   workspace: cac_kv8_attend_workspace bytes, 16-byte aligned, this call's own
  *         until it has run (NULL where that is 0)
  * Rows of out and lse that belong to no sequence are left as they were.  Tokens

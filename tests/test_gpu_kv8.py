@@ -724,6 +724,35 @@ def test_starts_past_the_rows_touch_nothing():
 # ---------------------------------------------------------------------------
 # streams, graphs, a step
 # ---------------------------------------------------------------------------
+@pytest.mark.parametrize("left", [-1, 8, 5000])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_starts_that_fall_are_refused(dtype, left):
+    """Between starts that fall, a tile or block number may stand before its sequence's first: nothing there is touched."""
+    b = Both(dim=64, page=16, dtype=dtype, n_pages=60)
+    good, bad = b.ids([0, 160, 192, 232, 252]), b.ids([0, 160, 192, 20, 40])
+    ids = b.ids([3, 0, 1, 2])
+    b.cache.extend(ids, starts=good)
+    x = torch.randn(252, 2, 64, device="cuda").to(dtype)
+    tables, k_scale = b.cache.table.clone(), b.cache.k_scale.clone()
+    b.cache.write(0, ids, x, x, starts=bad)
+    with pytest.raises(b.native.CacError) as e:
+        b.cache.check()
+    assert e.value.code in (BOUNDS, STATE) and torch.equal(tables, b.cache.table)
+    b.cache.write(0, ids, x, x, starts=good)
+    b.cache.check()
+    q = torch.randn(252, 4, 64, device="cuda").to(dtype)
+    fence = torch.full((252 + 200, 4, 64), 7.0, device="cuda", dtype=dtype)
+    out = fence[100:352]
+    b.cache.attend(0, ids, q, att_left=left, starts=bad, max_new=160, out=out)
+    with pytest.raises(b.native.CacError) as e:
+        b.cache.check()
+    assert e.value.code == BOUNDS
+    assert (fence[:100] == 7).all() and (fence[352:] == 7).all()
+    out2, lse = b.cache.attend(0, ids, q, att_left=left, starts=good, max_new=160, lse=True)
+    b.cache.check()
+    assert torch.isfinite(lse).all()
+
+
 @pytest.mark.parametrize("m", [1, 60])
 def test_a_first_call_inside_a_capture(m):
     """Nothing has to be set up outside: kernels of a head size that no other test of this process uses."""
