@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                             scale16(col_o + c, r);
                             if (S::WIDE && h > S::FLUSH) scale16(col_sum + c, r);
                         }
+                        if (S::WIDE) tmem_st_wait();  // the flush below loads these columns, and loads do not wait for stores
                     }
                 }
                 if (S::WIDE && h > 0 && h % S::FLUSH == 0) {

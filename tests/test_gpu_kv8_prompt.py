@@ -1,0 +1,51 @@
+"""Attention over the 8-bit K/V cache by the kernel for many query rows, against the plain model in 64 bits.  Which kernel
+answers a call depends on how it fills the card, so every test here asserts that it was this one."""
+import warnings
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_kv8 import F32, Both  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+class Prompts(Both):
+    """A cache whose attention calls have to be answered by kv_prompt_kernel: each is captured first, and the graph's kernels
+    are looked at."""
+
+    def __init__(self, tmp_path, *args, **kw):
+        super().__init__(*args, **kw)
+        attend, path = self.cache.attend, str(tmp_path / "call.dot")
+
+        def checked(*args, **kw):
+            graph = torch.cuda.CUDAGraph(keep_graph=True)
+            graph.enable_debug_mode()
+            with torch.cuda.graph(graph):
+                attend(*args, **kw)
+            with warnings.catch_warnings():
+                warnings.simplefilter("ignore")      # it warns that it writes a file
+                graph.debug_dump(path)
+            with open(path) as f:
+                dot = f.read()
+            assert "kv_prompt_kernel" in dot and "kv_attend_kernel" not in dot
+            return attend(*args, **kw)
+
+        self.cache.attend = checked
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 8), (128, 6), (16, 8)])
+def test_maxima_that_jump_where_sums_are_flushed(tmp_path, dim, heads):
+    """fp32 sums move to their second place every 256 tokens; here the logits of each 256 tokens lie a few powers of two
+    above (or below) those before, so that the sums are rescaled just there."""
+    b = Prompts(tmp_path, heads=heads, dim=dim, page=64, dtype=F32, n_pages=40, max_pages=20)
+    tokens = 1100
+    gen = torch.Generator().manual_seed(dim)
+    line = torch.randn(dim, generator=gen)
+    line /= line.norm()
+    level = torch.tensor([0.0, 1.0, 2.0, 1.5, 3.0])[torch.arange(tokens) // 256]
+    b.append([0], [tokens], k=b.rand(tokens, heads, dim, gain=0.05) + level[:, None, None] * line)
+    step = torch.tensor([4.0, 6.0, 3.0, 10.0, -5.0])[torch.arange(tokens) % 5]      # powers of two a level
+    q = (step * 0.6931 * dim ** 0.5)[:, None, None] * line.expand(tokens, heads, dim)
+    b.attend([0], [tokens], group=1, q=q.contiguous())
