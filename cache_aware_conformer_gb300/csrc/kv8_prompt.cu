@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 const bool grown = top > m + S::SLACK || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grown)) {
                     const float r = grown ? ex2(m - top) : 1.f;
-                    if (grown) m = top, l *= r;
+                    m = grown ? top : m, l *= r;  // no branch: what follows is for a converged warp
                     if (h > 0) {
                         if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }  // the sums so far are in
                         tc_fence_after();
@@ -425,6 +425,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < HDP / 32; ++c) {
                     float v[32];
+                    __syncwarp();  // rows past the last one stored nothing; the loads are for a converged warp
                     tmem_ld32(col_o + c * 32, v);
                     if (S::WIDE && w.halves > S::FLUSH) {
                         float sum[32];

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from test_gpu_kv8 import F32, Both  # noqa: E402
+from test_gpu_kv8 import BF16, F32, Both  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,15 @@ def test_maxima_that_jump_where_sums_are_flushed(tmp_path, dim, heads):
     step = torch.tensor([4.0, 6.0, 3.0, 10.0, -5.0])[torch.arange(tokens) % 5]      # powers of two a level
     q = (step * 0.6931 * dim ** 0.5)[:, None, None] * line.expand(tokens, heads, dim)
     b.attend([0], [tokens], group=1, q=q.contiguous())
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim,page,group", [(64, 48, 4), (128, 32, 3), (80, 16, 5), (16, 64, 8)])
+def test_ragged_rows(tmp_path, code, dtype, dim, page, group):
+    """As many queries as keys and fewer, odd counts: row tiles whose last warp, or last row tile, is not full."""
+    b = Prompts(tmp_path, code, heads=8, dim=dim, page=page, dtype=dtype, n_pages=100, seed=dim)
+    lens = [131, 260, 1, 77, 16]
+    b.append(range(5), lens)
+    b.attend(range(5), lens, group=group)
+    b.attend([3, 1, 4, 0], [59, 201, 16, 123], group=group)
