@@ -325,8 +325,11 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 if (!warp_wait(s_full + 2 * x + (h & 1), j & 1)) { ok = false; break; }
                 tc_fence_after();
                 const float4 ks4 = sc[0], lv4 = sc[2], iv4 = sc[4];
-                const float ks[4] = {ks4.x * f, ks4.y * f, ks4.z * f, ks4.w * f}, lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w},
-                            iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                // Above 0 even where the product underflows (a query of zeros over a block of zeros) or the call's scale is 0: unseen
+                // tokens score -inf before they are multiplied.  A score is under 2^31 there, so FLT_MIN times it is nothing.
+                const float ks[4] = {fmaxf(ks4.x * f, FLT_MIN), fmaxf(ks4.y * f, FLT_MIN), fmaxf(ks4.z * f, FLT_MIN),
+                                     fmaxf(ks4.w * f, FLT_MIN)},
+                            lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
                 float v[PT_HALF];
                 tmem_ld64(col, v);
                 // a token that the row does not see scores -inf

@@ -61,3 +61,26 @@ def test_ragged_rows(tmp_path, code, dtype, dim, page, group):
     b.append(range(5), lens)
     b.attend(range(5), lens, group=group)
     b.attend([3, 1, 4, 0], [59, 201, 16, 123], group=group)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.0, -0.0, 1e-44, -0.3])
+def test_scales_of_zero_and_below(tmp_path, dtype, scale):
+    b = Prompts(tmp_path, heads=8, dim=64, page=16, dtype=dtype, n_pages=100)
+    b.append([0, 1], [150, 60])
+    b.attend([0, 1], [150, 60], group=4, scale=scale)
+    b.attend([0, 1], [150, 60], group=4, scale=scale, left=20, sinks=3)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("keys", [0.0, 1e-38, 1e-6, 1e-3, 1.0])
+def test_queries_of_zeros(tmp_path, dtype, keys):
+    """Padding: rows of zeros, over keys of zeros and of tiny values, beside rows that are not."""
+    b = Prompts(tmp_path, heads=8, dim=64, page=16, dtype=dtype, n_pages=100)
+    b.append([0, 1], [170, 75], k=b.rand(245, 8, 64, gain=keys) if keys else torch.zeros(245, 8, 64, dtype=dtype))
+    q = b.rand(260, 32, 64)
+    q[20:40] = 0
+    q[60:260:3] = 0
+    b.attend([0, 1], [170, 90], group=4, q=q)                     # the second's first 15 stand before its position 0
+    b.attend([0, 1], [170, 90], group=4, q=q, left=33, chunk=4, sinks=20)
+    b.attend([0, 1], [170, 90], group=4, q=torch.zeros_like(q))
