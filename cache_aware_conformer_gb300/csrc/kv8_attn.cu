@@ -268,7 +268,8 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
         for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
-    // Two tiles of 16 tokens, their codes at shared addresses k[u] (V after K); on[u]: take part.  Column n of score tile i is
+    // Two tiles of 16 tokens, their codes at shared addresses k[u] (V after K); on[u]: take part (one that does not may be another
+    // sequence's, and its scales anything).  Column n of score tile i is
     // token (n / 2) + 4 (2 i + n % 2), so that a thread's four weights of a row are tokens t, t + 4, t + 8, t + 12.
     __device__ __forceinline__ void tiles(const Tile (&d)[2], const uint8_t* const (&k)[2], const bool (&on)[2], int sinks) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -347,7 +348,7 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[u][i][2 * h + b] - base);
-                l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), d[u].iv, l[h]);
+                l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), on[u] ? d[u].iv : 0.f, l[h]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     p[u][2 * i + h] = pack_half(w[i][0], w[i][1]);
@@ -532,8 +533,9 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
             float w[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2(s[u][e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1] - LIFT));
-            l[0] = fmaf(w[0] + w[2], d[u].iv, l[0]);
-            l[1] = fmaf(w[1] + w[3], d[u].iv, l[1]);
+            const float iv = on[u] ? d[u].iv : 0.f;
+            l[0] = fmaf(w[0] + w[2], iv, l[0]);
+            l[1] = fmaf(w[1] + w[3], iv, l[1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // tokens by rows -> rows by tokens: what operand B takes
                 const uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
