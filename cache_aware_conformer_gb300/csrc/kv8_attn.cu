@@ -3,7 +3,7 @@
 //
 //   t_j = scale log2(e) ks_b (q . kc_j)      kc, vc: codes of token j; ks_b, vs_b: scales of its block of 16
 //   w_j = 2^(t_j + log2(vs_b) - m),  m the running maximum of t_j + log2(vs_b)
-//   out = sum_j w_j vc_j / sum_j w_j / vs_b
+//   out = sum_j w_j vc_j / (sum_j w_j / vs_b)
 //
 // With the value scale inside the exponent, the codes enter both products as they
 // are (whole numbers or e4m3 values, exact in fp16), no product of a weight and a
@@ -46,7 +46,7 @@ namespace {
 
 // Weights are held times 2^LIFT: fp16 keeps 11 bits of every weight down to 2^-27 of the largest (a small weight may meet a large
 // value).  SLACK is what a maximum may lag behind (RowsLow): at LIFT + SLACK = 15 a weight is 32,768 at most.
-constexpr float LIFT = 13.f, SLACK = 2.f;
+constexpr float LIFT = 13.f, SLACK = 2.f, NORM = norm_factor(13);
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
@@ -216,7 +216,7 @@ __device__ __forceinline__ void put_run(const KvAttend& a, const SeqWork& s, int
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
-        for (int k = 0; k < RUN; ++k) y[k] *= inv;
+        for (int k = 0; k < RUN; ++k) y[k] = y[k] * NORM * inv;  // NORM * inv may be too small a number
         store_run<T, RUN>(static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + e, y);
     }
 }
@@ -229,7 +229,7 @@ __device__ __forceinline__ void put_sums(const KvAttend& a, const SeqWork& s, in
     } else if (a.lse) {
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
         a.lse[(s.row0 + (long long)query) * a.heads + qh] =
-            l > 0.f || l != l ? (m - LIFT + log2f(l)) * LN2 : -INFINITY;
+            l > 0.f || l != l ? (m + NORM_LOG2 + log2f(l)) * LN2 : -INFINITY;
     }
 }
 
@@ -348,7 +348,7 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[u][i][2 * h + b] - base);
-                l[h] = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), on[u] ? d[u].iv : 0.f, l[h]);
+                l[h] = fmaf(((w[0][0] + w[0][1]) + (w[1][0] + w[1][1])) * NORM, on[u] ? d[u].iv : 0.f, l[h]);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     p[u][2 * i + h] = pack_half(w[i][0], w[i][1]);
@@ -534,8 +534,8 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = ex2(s[u][e] - (m[e & 1] == -INFINITY ? 0.f : m[e & 1] - LIFT));
             const float iv = on[u] ? d[u].iv : 0.f;
-            l[0] = fmaf(w[0] + w[2], iv, l[0]);
-            l[1] = fmaf(w[1] + w[3], iv, l[1]);
+            l[0] = fmaf((w[0] + w[2]) * NORM, iv, l[0]);
+            l[1] = fmaf((w[1] + w[3]) * NORM, iv, l[1]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // tokens by rows -> rows by tokens: what operand B takes
                 const uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
@@ -725,9 +725,9 @@ __device__ __forceinline__ void join_rows(const KvAttend& a, const Partials& p, 
                 T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
-                    if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[b][c] / l[b] : 0.f);
+                    if (lane * PER + c < D) dst[c] = from_f<T>(seen ? o[b][c] * NORM / l[b] : 0.f);
                 if (lane == 0 && a.lse)
-                    a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top[b] - LIFT + log2f(l[b])) * LN2 : -INFINITY;
+                    a.lse[(s.row0 + (long long)query) * a.heads + qh] = seen ? (top[b] + NORM_LOG2 + log2f(l[b])) * LN2 : -INFINITY;
             }
         }
     }
@@ -1001,9 +1001,9 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
     const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
     if (d < a.c.head_dim)
         static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + d] =
-            from_f<T>(seen ? o / l : 0.f);
+            from_f<T>(seen ? o * NORM / l : 0.f);
     if (d == 0 && a.lse)
-        a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top - LIFT + log2f(l)) * LN2 : -INFINITY;
+        a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top + NORM_LOG2 + log2f(l)) * LN2 : -INFINITY;
 }
 
 template <class T, int CODE, int HDP, bool LOW>

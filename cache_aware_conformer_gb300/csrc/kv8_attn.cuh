@@ -7,6 +7,13 @@ namespace cac {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// A row's norm is a sum of weight / V scale.  The weights are held times 2^lift and reach 2^15 at most, a scale is between 2^-100 (a
+// block of zeros) and 2^121, so the norm is held times 2^-(lift + 4): one seen token leaves at least 2^-125, whose reciprocal is
+// a number too, and the sum over zero values stays within fp32's range (where lift is 7 and every weight is at its highest, up
+// to 2^24 tokens).
+__host__ __device__ constexpr float norm_factor(int lift) { return 1.f / (float)(1ll << (lift + 4)); }
+constexpr float NORM_LOG2 = 4.f;  // log2 of what the norm lacks when the lift is taken off the maximum
+
 // ---------------------------------------------------------------------------
 // codes to fp16, exactly: the four bytes of a word as two pairs.  For e4m3 the conversion instruction (its bits moved into place by
 // hand, which no NaN could come out of, took 249 us where this takes 216 in 128 windows of 4,096 tokens); so whoever reads

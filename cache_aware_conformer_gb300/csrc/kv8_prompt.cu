@@ -53,7 +53,7 @@ template <class T, int HDP> struct PShape {
     static constexpr int FLUSH = WIDE ? 4 : 1 << 30;
     static constexpr int COL_S = 0, COL_O = NM * 128, COL_SUM = COL_O + NM * HDP;
     static_assert(COL_SUM + (WIDE ? NM * HDP : 0) <= 512, "TMEM");
-    static constexpr float SLACK = WIDE ? 2.f : 8.f, LIFT = 15.f - SLACK;
+    static constexpr float SLACK = WIDE ? 2.f : 8.f, LIFT = 15.f - SLACK, NORM = norm_factor(WIDE ? 13 : 7);
 };
 
 // D[tmem] (+)= A[smem] B[smem], fp16 operands
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                             sum[k & 3] = k < 4 ? y : add2(sum[k & 3], y);
                         }
                         const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-                        l = fmaf(all.x + all.y, iv[b], l);
+                        l = fmaf((all.x + all.y) * S::NORM, iv[b], l);
                     }
                 }
                 tmem_st_wait();
@@ -436,6 +436,8 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] += sum[k];
                     }
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] *= S::NORM;
                     if (!on) continue;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                         }
                     }
                 }
-                if (on && a.lse) a.lse[(out0 + query) * a.heads + qh] = seen ? (m - S::LIFT + log2f(l)) * LN2 : -INFINITY;
+                if (on && a.lse) a.lse[(out0 + query) * a.heads + qh] = seen ? (m + NORM_LOG2 + log2f(l)) * LN2 : -INFINITY;
             }
         }
     } else if (warp < S::SOFT + S::CONV) {

@@ -33,3 +33,31 @@ def test_a_sequence_that_no_write_has_filled_leaves_its_neighbours_alone(code, d
         tol, tol_lse = bounds(*ref, dim, lens[i], dtype)
         assert (np.abs(out[2 * i:2 * i + 1].double().cpu().numpy() - ref[0]) <= tol).all(), i
         assert (np.abs(lse[2 * i:2 * i + 1].double().cpu().numpy() - ref[1]) <= tol_lse).all(), i
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("dim,group", [(64, 1), (128, 12), (256, 2)])
+def test_lse_over_values_of_zero(dtype, dim, group):
+    """A head whose V is zero throughout, scores all alike: lse = log of the count, whichever warps share the tokens."""
+    tokens = 70000
+    b = Both(heads=2, dim=dim, page=64, dtype=dtype, n_pages=1200, seqs=2, max_pages=1100)
+    zero = torch.zeros(tokens, 2, dim, dtype=dtype, device="cuda")
+    for i, m in ((0, tokens), (1, 300)):
+        b.cache.extend(b.ids([i]), each=m)
+        b.cache.write(0, b.ids([i]), zero[:m], zero[:m])
+    for left in (-1, 200):
+        out, lse = b.cache.attend(0, b.ids([0, 1]), b.rand(2, 2 * group, dim).cuda(), att_left=left, lse=True)
+        b.cache.check()
+        want = torch.tensor([tokens, 300] if left < 0 else [left + 1, left + 1], dtype=torch.float64).log()
+        # sums over the keys in fp32, and the logarithm's own rounding (see bounds())
+        assert (lse.double().cpu() - want[:, None]).abs().max() <= tokens * 2.0 ** -24 + 2.0 ** -22 * 140
+        assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("m,group", [(1, 1), (5, 4)])
+def test_values_near_the_largest_float(dtype, m, group):
+    b = Both(heads=2, dim=64, page=16, dtype=dtype)
+    b.append([0, 1], [90, 1], v=torch.full((91, 2, 64), 3e38).to(dtype))
+    b.attend([0, 1], [m, 1], group=group)
+    b.attend([0, 1], [m, 1], group=group, left=20)

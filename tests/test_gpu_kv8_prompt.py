@@ -84,3 +84,24 @@ def test_queries_of_zeros(tmp_path, dtype, keys):
     b.attend([0, 1], [170, 90], group=4, q=q)                     # the second's first 15 stand before its position 0
     b.attend([0, 1], [170, 90], group=4, q=q, left=33, chunk=4, sinks=20)
     b.attend([0, 1], [170, 90], group=4, q=torch.zeros_like(q))
+
+
+@pytest.mark.parametrize("dtype,tokens,m,heads,group,dim", [(F32, 70000, 400, 2, 8, 64), (BF16, 2 ** 21 + 2 ** 20, 350, 1, 16, 16)])
+def test_lse_over_values_of_zero(tmp_path, dtype, tokens, m, heads, group, dim):
+    """V of zeros throughout, scores all alike: lse = log of the count.  Sums over the keys in fp32 as in bounds()."""
+    b = Prompts(tmp_path, heads=heads, dim=dim, page=64, dtype=dtype, n_pages=tokens // 64 + 1, seqs=1, max_pages=tokens // 64 + 1)
+    zero = torch.zeros(tokens, heads, dim, dtype=dtype, device="cuda")
+    b.cache.extend(b.ids([0]), each=tokens)
+    b.cache.write(0, b.ids([0]), zero, zero)
+    out, lse = b.cache.attend(0, b.ids([0]), b.rand(m, heads * group, dim).cuda(), lse=True)
+    b.cache.check()
+    want = torch.arange(tokens - m + 1, tokens + 1, dtype=torch.float64).log()
+    assert (lse.double().cpu() - want[:, None]).abs().max() <= tokens * 2.0 ** -24 + 2.0 ** -22 * 143
+    assert (out == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_values_near_the_largest_float(tmp_path, dtype):
+    b = Prompts(tmp_path, heads=8, dim=64, page=16, dtype=dtype, n_pages=100)
+    b.append([0, 1], [150, 60], v=torch.full((210, 8, 64), 3e38).to(dtype))
+    b.attend([0, 1], [150, 60], group=4)
