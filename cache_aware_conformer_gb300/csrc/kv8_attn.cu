@@ -74,7 +74,7 @@ template <int HDP> __device__ __forceinline__ int tile_at(int r, int c) {
 
 struct Tile {
     long long at;              // its codes (K and V alike), -1: nothing there
-    float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale
+    float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale (0 where that is FAR)
     int j0;                    // its first token
 };
 template <int CODE>
@@ -89,7 +89,7 @@ __device__ __forceinline__ Tile tile_of(const KvAttend& a, int id, int len, int 
             t.at = kv_head_at(a.c, a.layer, page, head) + (long long)in_page * a.c.head_dim;
             t.ks = a.c.k_scale[sc];
             t.lv = log2f(a.c.v_scale[sc]);
-            t.iv = ex2(-t.lv);  // of the rounded logarithm, so that weight and norm have the same factor
+            t.iv = t.lv < FAR ? 0.f : ex2(-t.lv);  // of the rounded logarithm, so that weight and norm have the same factor
         }
     }
     return t;
@@ -330,9 +330,9 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float r = top[h] == -INFINITY ? 1.f : ex2(m[h] - top[h]);
+                const float d = top[h] == -INFINITY ? 0.f : m[h] - top[h], r = ex2(d);
                 m[h] = top[h];
-                l[h] *= r;
+                l[h] = move_norm(l[h], d, r);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) o[n][2 * h] *= r, o[n][2 * h + 1] *= r;
             }
@@ -349,6 +349,12 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
 #pragma unroll
                     for (int b = 0; b < 2; ++b) w[i][b] = ex2(s[u][i][2 * h + b] - base);
                 l[h] = fmaf(((w[0][0] + w[0][1]) + (w[1][0] + w[1][1])) * NORM, on[u] ? d[u].iv : 0.f, l[h]);
+                if (on[u] && d[u].lv < FAR) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) x += ex2(s[u][i][2 * h] - d[u].lv - base) + ex2(s[u][i][2 * h + 1] - d[u].lv - base);
+                    l[h] = fmaf(x, NORM, l[h]);
+                }
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     p[u][2 * i + h] = pack_half(w[i][0], w[i][1]);
@@ -519,9 +525,9 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], x));
                 if (top[b] > m[b] + SLACK) {
-                    const float r = ex2(m[b] - top[b]);
+                    const float d = m[b] - top[b], r = ex2(d);
                     m[b] = top[b];
-                    l[b] *= r;
+                    l[b] = move_norm(l[b], d, r);
 #pragma unroll
                     for (int n = 0; n < MT; ++n) o[n][b] *= r, o[n][2 + b] *= r;
                 }
@@ -536,6 +542,11 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
             const float iv = on[u] ? d[u].iv : 0.f;
             l[0] = fmaf((w[0] + w[2]) * NORM, iv, l[0]);
             l[1] = fmaf((w[1] + w[3]) * NORM, iv, l[1]);
+            if (on[u] && d[u].lv < FAR) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    l[e & 1] = fmaf(ex2(s[u][e] - d[u].lv - (m[e & 1] == -INFINITY ? 0.f : m[e & 1] - LIFT)), NORM, l[e & 1]);
+            }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {  // tokens by rows -> rows by tokens: what operand B takes
                 const uint32_t hi = pack_half(w[2 * i], w[2 * i + 1]);
@@ -693,7 +704,10 @@ __device__ __forceinline__ void join_rows(const KvAttend& a, const Partials& p, 
 #pragma unroll
                     for (int b = 0; b < ROWS; ++b) top[b] = fmaxf(top[b], __shfl_xor_sync(0xffffffffu, top[b], d, 16));
 #pragma unroll
-                for (int b = 0; b < ROWS; ++b) f[b] = ex2(ml[b].x - (top[b] == -INFINITY ? 0.f : top[b])), l[b] = ml[b].y * f[b];
+                for (int b = 0; b < ROWS; ++b) {
+                    const float d = ml[b].x - (top[b] == -INFINITY ? 0.f : top[b]);
+                    f[b] = ex2(d), l[b] = move_norm(ml[b].y, d, f[b]);
+                }
 #pragma unroll
                 for (int d = 8; d; d >>= 1)
 #pragma unroll
@@ -986,8 +1000,8 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
     const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll 4
     for (int b = b0 + y; b <= b1; b += JOIN_Y) {
-        const float f = ex2(__ldcg(part.ml + slot(b) * 2) - base);
-        l = fmaf(__ldcg(part.ml + slot(b) * 2 + 1), f, l);
+        const float away = __ldcg(part.ml + slot(b) * 2) - base, f = ex2(away);
+        l += move_norm(__ldcg(part.ml + slot(b) * 2 + 1), away, f);
         o = fmaf(__ldcg(part.o + slot(b) * HDP + d), f, o);
     }
     s_o[y][d] = o;

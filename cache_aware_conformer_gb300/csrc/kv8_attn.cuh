@@ -51,6 +51,19 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// A token's part of the norm, weight / V scale, may be large where its weight is under the smallest float: its V block is then far
+// smaller than the largest one, a block of zeros beside ordinary values above all.  The norms' parts of blocks whose log2 scale is
+// under FAR are therefore exponentials of their own, and a norm that moves to another maximum does so in two steps where one factor
+// would be 0.  Results are exact this way for scales up to 2^75 beside any; next to larger ones, tokens of blocks 2^115 times
+// smaller start to be lost.
+constexpr float FAR = -40.f;
+// l times r = 2^d
+__device__ __forceinline__ float move_norm(float l, float d, float r) {
+    if (d > -100.f) return l * r;
+    const float half = ex2(0.5f * d);
+    return l * half * half;
+}
+
 // What a sequence of the call asks for.
 struct SeqWork {
     int id, len, m, row0;      // len 0: nothing is seen

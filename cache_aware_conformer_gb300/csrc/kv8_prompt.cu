@@ -351,8 +351,10 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                 for (int b = 0; b < 4; ++b) top = fmaxf(top, fmaf(mb[b], ks[b], lv[b]));
                 const bool grown = top > m + S::SLACK || (m == -INFINITY && top > m);
                 if (__any_sync(0xffffffffu, grown)) {
-                    const float r = grown ? ex2(m - top) : 1.f;
-                    m = grown ? top : m, l *= r;  // no branch: what follows is for a converged warp
+                    const float d = grown ? m - top : 0.f, r = ex2(d);
+                    l = move_norm(l, d, r);
+                    m = grown ? top : m;
+                    __syncwarp();  // the tensor-memory instructions are for a converged warp
                     if (h > 0) {
                         if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }  // the sums so far are in
                         tc_fence_after();
@@ -389,6 +391,16 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                         const float2 y = fma2(make_float2(v[k], v[k + 1]), make_float2(ks[b], ks[b]), make_float2(off, off));
                         v[k] = y.x, v[k + 1] = y.y;
                     }
+                }
+                if (fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < FAR) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (lv[b] < FAR && lv[b] != -INFINITY) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int k = 16 * b; k < 16 * b + 16; ++k) x += ex2(v[k] - lv[b]);
+                            l = fmaf(x, S::NORM, l);
+                        }
                 }
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
@@ -489,7 +501,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1)
                         const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
                         t.ks = a.c.k_scale[sc];
                         t.lv = log2f(a.c.v_scale[sc]);
-                        t.iv = ex2(-t.lv);
+                        t.iv = t.lv < FAR ? 0.f : ex2(-t.lv);
                     }
                 }
             }

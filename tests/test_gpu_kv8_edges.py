@@ -61,3 +61,29 @@ def test_values_near_the_largest_float(dtype, m, group):
     b.append([0, 1], [90, 1], v=torch.full((91, 2, 64), 3e38).to(dtype))
     b.attend([0, 1], [m, 1], group=group)
     b.attend([0, 1], [m, 1], group=group, left=20)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("big", [1.0, 1e3, 1e6, 1e10, 1e15, 1e20])
+@pytest.mark.parametrize("m,group,dim", [(1, 1, 64), (5, 4, 64), (1, 6, 128), (2, 9, 256)])
+def test_blocks_of_zero_values_beside_large_ones(dtype, big, m, group, dim):
+    """V blocks of zeros and of tiny values, before and after large ones: their tokens count in the norm with their full weight."""
+    b = Both(heads=2, dim=dim, page=16, dtype=dtype, n_pages=100, max_pages=100)
+    v = b.rand(400, 2, dim, gain=big)
+    v[:16] *= 1e-25
+    v[16:48] = 0
+    v[96:320] = 0
+    v[320:336] *= 1e-18
+    b.append([0], [400], v=v)
+    for kw in ({}, {"qgain": 4.0}, {"left": 250}, {"left": 350, "sinks": 30}):
+        b.attend([0], [m], group=group, **kw)
+
+
+def test_blocks_of_zero_values_in_parts_that_are_joined():
+    """... where warps and blocks each hold a part of the sequence, some of nothing but zeros."""
+    b = Both(heads=1, dim=64, page=64, dtype=F32, n_pages=600, seqs=2, max_pages=500)
+    v = b.rand(30000, 1, 64, gain=1e12)
+    v[1000:29000] = 0
+    b.append([0], [30000], v=v)
+    b.attend([0], [1], group=2)
+    b.attend([0], [3], group=4, qgain=4.0)

@@ -2,10 +2,12 @@
 answers a call depends on how it fills the card, so every test here asserts that it was this one."""
 import warnings
 
+import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
+from _kv8 import attend64, bounds  # noqa: E402
 from test_gpu_kv8 import BF16, F32, Both  # noqa: E402
 
 pytestmark = pytest.mark.gpu
@@ -105,3 +107,37 @@ def test_values_near_the_largest_float(tmp_path, dtype):
     b = Prompts(tmp_path, heads=8, dim=64, page=16, dtype=dtype, n_pages=100)
     b.append([0, 1], [150, 60], v=torch.full((210, 8, 64), 3e38).to(dtype))
     b.attend([0, 1], [150, 60], group=4)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("big", [1.0, 1e3, 1e6, 1e10, 1e15, 1e20])
+def test_blocks_of_zero_values_beside_large_ones(tmp_path, dtype, big):
+    """V blocks of zeros and of tiny values, before and after large ones: their tokens count in the norm with their full weight."""
+    b = Prompts(tmp_path, heads=8, dim=64, page=16, dtype=dtype, n_pages=100)
+    v = b.rand(400, 8, 64, gain=big)
+    v[:16] *= 1e-25
+    v[16:48] = 0
+    v[96:320] = 0
+    v[320:336] *= 1e-18
+    b.append([0], [400], v=v)
+    codes, scales = b.seqs[0].values(0, "k")
+    K = codes.astype(np.float64) * scales[..., None]
+    vs = b.seqs[0].values(0, "v")[1].astype(np.float64)
+    for m, qgain, left in ((400, 1.0, -1), (160, 4.0, -1), (160, 1.0, 250)):
+        q = b.rand(m, 32, 64, gain=qgain)
+        out, lse = b.cache.attend(0, b.ids([0]), q.cuda(), att_left=left, lse=True)
+        b.cache.check()
+        qd = q.double().numpy()
+        ref = attend64(b.seqs[0], 0, qd, 4, 0.125, left, 1, 0, 16)
+        tol, tol_lse = bounds(*ref, 64, 400, dtype)
+        # Weights times V scale are held in fp16 relative to the largest of the row, times 2^7 at least: what lies under fp16's
+        # smallest number is off by half of it, 2^-25, which is 2^-32 of the largest for each key and code.  Where the tokens of
+        # the largest have a code of 0, that is all of the error that there may be, and bounds() has no term for it.
+        p, t = np.arange(400 - m, 400)[:, None], np.arange(400)
+        unseen = (t > p) | ((t < p - left) if left >= 0 else False)
+        for h in range(32):
+            s = np.where(unseen, -np.inf, 0.125 * qd[:, h] @ K[:, h // 4].T)
+            w = np.exp(s - ref[1][:, h, None]) * vs[:, h // 4]
+            tol[:, h] += 400 * 2.0 ** -32 * 127 * w.max(1)[:, None]
+        assert (np.abs(out.double().cpu().numpy() - ref[0]) <= tol).all()
+        assert (np.abs(lse.double().cpu().numpy() - ref[1]) <= tol_lse).all()
