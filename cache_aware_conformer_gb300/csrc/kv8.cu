@@ -154,19 +154,27 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
         for (int i = tid; i < n; i += PLAN_T) {
             const Want w = want(i);
             if (c.pending[2 * w.id + 1] != i) atomicCAS(&error, 0, CAC_E_INVAL);
-            if (w.shared) {  // how many of this call's sequences end in the page, and the last of those
+            if (w.shared) {  // how many of this call's sequences end in the page, and how far the longest of those fills it
                 atomicAdd(work.named + w.last, 1);
-                atomicMax(work.keeper + w.last, i + 1);
+                atomicMax(work.keeper + w.last, w.len % c.page_tokens);
+                work.last_of[w.last] = 0;
             }
         }
     __syncthreads();
     failed = error;
-    // A shared page stays with the last of this call's sequences that end in it when no other table names it; the
-    // others (all of them, when one does) get a copy.  Neither depends on the order of the atomics.
+    if (count_shared && !failed)
+        for (int i = tid; i < n; i += PLAN_T) {  // the last of those that fill it as far
+            const Want w = want(i);
+            if (w.shared && __ldcg(work.keeper + w.last) == w.len % c.page_tokens) atomicMax(work.last_of + w.last, i + 1);
+        }
+    __syncthreads();
+    // A shared page stays with one of this call's sequences that end in it when no other table names it; the others (all of
+    // them, when one does) get a copy.  It stays with the longest, whose new blocks lie behind all that is copied.  Neither
+    // depends on the order of the atomics.
     auto decide = [&](int i) {
         Want w = want(i);
         if (w.shared)
-            w.copy = __ldcg(c.refs + w.last) > __ldcg(work.named + w.last) || __ldcg(work.keeper + w.last) != i + 1;
+            w.copy = __ldcg(c.refs + w.last) > __ldcg(work.named + w.last) || __ldcg(work.last_of + w.last) != i + 1;
         return w;
     };
     long long sum = 0;
@@ -197,6 +205,7 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
                 const int to = c.free_list[top - at.b];
                 work.copy_from[copies + at.b] = w.last;
                 work.copy_to[copies + at.b] = to;
+                work.copy_blocks[copies + at.b] = (w.len % c.page_tokens + KV_BLOCK - 1) / KV_BLOCK;
                 c.table[(long long)w.id * c.max_pages + w.len / c.page_tokens] = to;
                 c.refs[to] = 1;
             }
@@ -252,8 +261,8 @@ __global__ void __launch_bounds__(PLAN_T, 1) kv_extend_kernel(const cac_kv8 c, c
     }
 }
 
-// Whole pages, all layers: K, V and their scales.  Unit u of a copy is (layer, K or V).
-__device__ __forceinline__ void copy_page(const cac_kv8& c, int from, int to, int u) {
+// Whole pages, all layers: K, V and the scales of a page's first blocks.  Unit u of a copy is (layer, K or V).
+__device__ __forceinline__ void copy_page(const cac_kv8& c, int from, int to, int u, int blocks) {
     const int layer = u >> 1;
     uint8_t* codes = static_cast<uint8_t*>(u & 1 ? c.v : c.k);
     float* scales = u & 1 ? c.v_scale : c.k_scale;
@@ -271,17 +280,39 @@ __device__ __forceinline__ void copy_page(const cac_kv8& c, int from, int to, in
     for (; i < vecs; i += blockDim.x) b[i] = a[i];
     const float* sa = scales + kv_scale_at(c, layer, from, 0);
     float* sb = scales + kv_scale_at(c, layer, to, 0);
-    for (int k = threadIdx.x; k < c.kv_heads * (c.page_tokens / KV_BLOCK); k += blockDim.x) sb[k] = sa[k];
+    const int per = c.page_tokens / KV_BLOCK;
+    for (int k = threadIdx.x; k < c.kv_heads * per; k += blockDim.x)
+        if (k % per < blocks) sb[k] = sa[k];
 }
 
-__global__ void __launch_bounds__(256) kv_copy_kernel(const cac_kv8 c) {
+// After an extend: the copies that it decided on, and scale 0 for every block that begins with new tokens.  A write gives such a
+// block its scale; where none does, the pool's left-over scale is not taken for that of older tokens by a later write.  The new
+// blocks of a sequence are dealt out to `parts` blocks of the grid.
+__global__ void __launch_bounds__(256) kv_copy_kernel(const cac_kv8 c, const KvRows rows, const int32_t* ids, int parts) {
     pdl_trigger();
     pdl_wait();
     const KvWork work = kv_work(c);
     const long long units = (long long)work.count[0] * c.n_layers * 2;
+    for (int u = blockIdx.x; u < rows.n * parts; u += gridDim.x) {
+        const int i = u / parts, part = u - i * parts, id = ids[i], m = rows.at(i + 1) - rows.at(i);
+        if (m <= 0 || id < 0 || id >= c.max_seqs) continue;
+        const int2 pending = *reinterpret_cast<const int2*>(c.pending + 2 * id);
+        const int len = c.lens[id];
+        if (pending.x != m || pending.y != i) continue;  // the call was refused
+        const int first = (len - m + KV_BLOCK - 1) / KV_BLOCK, end = (len + KV_BLOCK - 1) / KV_BLOCK;
+        const int share = (end - first + parts - 1) / parts, b0 = first + part * share, n = min(share, end - b0);
+        if (n <= 0) continue;
+        for (long long e = threadIdx.x; e < 2ll * c.n_layers * c.kv_heads * n; e += blockDim.x) {
+            const long long r = e / n;
+            const int b = b0 + (int)(e - r * n), head = (int)(r % c.kv_heads), w = (int)(r / c.kv_heads);
+            const int token = b * KV_BLOCK, page = c.table[(long long)id * c.max_pages + token / c.page_tokens];
+            if (page < 0) continue;
+            (w & 1 ? c.v_scale : c.k_scale)[kv_scale_at(c, w >> 1, page, head) + token % c.page_tokens / KV_BLOCK] = 0.f;
+        }
+    }
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int k = (int)(u / (c.n_layers * 2));
-        copy_page(c, work.copy_from[k], work.copy_to[k], (int)(u % (c.n_layers * 2)));
+        copy_page(c, work.copy_from[k], work.copy_to[k], (int)(u % (c.n_layers * 2)), work.copy_blocks[k]);
     }
 }
 
@@ -480,13 +511,13 @@ __global__ void __launch_bounds__(WRITE_WARPS * 32, NIT <= 8 ? 2 : 1) kv_write_k
             float scale = fmaxf(__uint_as_float(top) * (1.f / kv_top<CODE>()), KV_MIN_SCALE);
             if (before[w] >= scale) {
                 scale = before[w];
-            } else if (on && p.lo > 0) {  // the older codes at the larger scale
+            } else if (on && p.lo > 0) {  // the older codes at the larger scale; zeros where no write has filled the block
                 const float r = before[w] / scale;
 #pragma unroll 1
                 for (int e = lane; e < p.lo * vec; e += 32) {
                     uint2* q = reinterpret_cast<uint2*>(codes + e * 8);
                     decode8<CODE>(*q, x);
-                    *q = encode8<CODE>(x, r);
+                    *q = before[w] > 0.f ? encode8<CODE>(x, r) : make_uint2(0, 0);
                 }
             }
             const float inv = 1.f / scale;
@@ -745,7 +776,7 @@ __global__ void __launch_bounds__(256) kv_compact_kernel(const cac_kv8 c) {
     const long long units = (long long)moves * c.n_layers * 2;
     for (long long u = blockIdx.x; u < units; u += gridDim.x) {
         const int k = (int)(u / (c.n_layers * 2));
-        copy_page(c, movers[k], places[k], (int)(u % (c.n_layers * 2)));
+        copy_page(c, movers[k], places[k], (int)(u % (c.n_layers * 2)), c.page_tokens / KV_BLOCK);
     }
 }
 
@@ -805,9 +836,12 @@ extern "C" int cac_kv8_extend(const cac_kv8* c, int n, const int32_t* ids, const
     const KvRows rows{starts, each, n, INT32_MAX};
     r = launched(launch_k(kv_extend_kernel, dim3(1), dim3(PLAN_T), 0, s, 1, *c, rows, ids));
     if (r != CAC_OK) return r;
-    const long long units = (long long)n * c->n_layers * 2;
-    return launched(launch_k(kv_copy_kernel, dim3((unsigned)std::min<long long>(units, COPY_BLOCKS)), dim3(256), 0, s,
-                             1, *c));
+    // a long prompt's new blocks go to as many blocks of the grid as leave each sequence one
+    const long long blocks = starts ? (long long)c->max_pages * (c->page_tokens / KV_BLOCK) : (each + 2 * KV_BLOCK - 2) / KV_BLOCK;
+    const int parts = (int)std::max<long long>(1, std::min<long long>(COPY_BLOCKS / n, blocks));
+    const long long units = (long long)n * std::max(c->n_layers * 2, parts);
+    return launched(launch_k(kv_copy_kernel, dim3((unsigned)std::min<long long>(units, COPY_BLOCKS)), dim3(256), 0, s, 1, *c,
+                             rows, ids, parts));
 }
 
 extern "C" int cac_kv8_write(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,

@@ -57,9 +57,11 @@ template <class F> __device__ __forceinline__ int warp_last_le(int n, long long 
 // layout of `work`
 // ---------------------------------------------------------------------------
 struct KvWork {
-    int32_t *named, *keeper;    // [n_pages] zero between calls: extend's entries that end in this page; the last of them + 1
+    int32_t *named, *keeper;    // [n_pages] zero between calls: extend's entries that end in this page; the most tokens of it that one has
+    int32_t* last_of;           // in place of name: the last entry with as many, + 1
     int32_t *name, *list;       // [n_pages] compact: a moved page's new place; [2][n_pages / 2] places and their movers
     int32_t *copy_from, *copy_to;  // [max_seqs] last pages to be copied
+    int32_t* copy_blocks;       // in place of list: the blocks of those that hold tokens (a copy takes a free page, so n_pages are enough)
     int32_t* count;             // [0] copies of extend, [1] moves of compact, [2] pages in use at compact
 };
 inline size_t kv_work_ints(const cac_kv8& c) { return (size_t)4 * c.n_pages + 2 + (size_t)2 * c.max_seqs + 16; }
@@ -71,6 +73,8 @@ __host__ __device__ inline KvWork kv_work(const cac_kv8& c) {
     w.list = w.name + c.n_pages;
     w.copy_from = w.list + c.n_pages + 2;
     w.copy_to = w.copy_from + c.max_seqs;
+    w.last_of = w.name;
+    w.copy_blocks = w.list;
     w.count = w.copy_to + c.max_seqs;
     return w;
 }

@@ -169,9 +169,9 @@ struct Seen {
         lo_max = any ? a.win.low(p1) : 0;
         lo_min = any ? a.win.low(max(p0, 0)) : 0;
     }
-    // whether a tile holds a token that one of the rows sees, and whether all see all of it
+    // whether a tile holds a token that one of the rows sees (nothing where its V scale is 0: no write has filled it), and whether all see all of it
     __device__ __forceinline__ bool sees(const Tile& d, int sinks) const {
-        return d.at >= 0 && d.j0 < hi_max && (d.j0 + KV_BLOCK > lo_min || d.j0 < sinks);
+        return d.at >= 0 && d.lv != -INFINITY && d.j0 < hi_max && (d.j0 + KV_BLOCK > lo_min || d.j0 < sinks);
     }
     __device__ __forceinline__ bool whole(const Tile& d, int sinks) const {
         return d.j0 + KV_BLOCK <= hi_min && (d.j0 >= lo_max || d.j0 + KV_BLOCK <= sinks);

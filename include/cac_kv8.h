@@ -99,7 +99,8 @@ int cac_kv8_init(const cac_kv8* c, void* stream);
  * get their pages, or none does: CAC_E_NOMEM (not enough free pages),
  * CAC_E_LIMIT (longer than max_pages), CAC_E_BOUNDS (id out of range or negative
  * count), CAC_E_INVAL (an id twice), CAC_E_STATE (the last page was released by
- * trim before a truncate into it) are latched. */
+ * trim before a truncate into it) are latched.  Tokens that no write fills have
+ * unspecified values in that layer; tokens added after them do not suffer. */
 int cac_kv8_extend(const cac_kv8* c, int n, const int32_t* ids, const int32_t* starts, int each, void* stream);
 
 /* Quantise one layer's K and V of the tokens that the last extend made room
@@ -137,8 +138,9 @@ int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const i
  *         left as they were, as do starts that fall
  *   workspace: cac_kv8_attend_workspace bytes, 16-byte aligned, this call's own
  *         until it has run (NULL where that is 0)
- * Rows of out and lse that belong to no sequence are left as they were.  Tokens
- * that an extend made room for and no write has filled have unspecified values.
+ * Rows of out and lse that belong to no sequence are left as they were.  Rows of
+ * a sequence that has tokens that an extend made room for and no write has filled
+ * have unspecified values where a query of the call sees one of the same block.
  * A bounded wait inside the kernels that gives up latches CAC_E_TIMEOUT.
  * CAC_E_LIMIT: more than 2^26 tiles of 16 query rows (rows * heads / 16). */
 int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,

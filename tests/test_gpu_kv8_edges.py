@@ -87,3 +87,117 @@ def test_blocks_of_zero_values_in_parts_that_are_joined():
     b.append([0], [30000], v=v)
     b.attend([0], [1], group=2)
     b.attend([0], [3], group=4, qgain=4.0)
+
+
+class Holes(Both):
+    """A cache in which some tokens are never written; what the others hold is compared token by token."""
+
+    def __init__(self, *args, left_over=1e30, **kw):
+        super().__init__(*args, **kw)
+        for t in (self.cache.k_scale, self.cache.v_scale):
+            t.fill_(left_over)
+        for t in (self.cache.k, self.cache.v):
+            t.fill_(-1)
+        self.filled = [np.zeros(0, bool) for _ in self.seqs]
+
+    def hole(self, ids, counts):
+        """Room for tokens that no write fills: in the model, codes of 0, and scales of 0 for the blocks that they begin."""
+        self.cache.extend(self.ids(ids), starts=self.starts(counts))
+        for i, m in zip(ids, counts):
+            s = self.seqs[i]
+            for key in s.code:
+                s.code[key] = np.concatenate([s.code[key][:s.len], np.zeros((m,) + s.code[key].shape[1:], np.float32)])
+                old = s.scale[key][:-(-s.len // 16)]
+                s.scale[key] = np.concatenate([old, np.zeros((-(-(s.len + m) // 16) - len(old),) + old.shape[1:], np.float32)])
+            s.len += m
+            self.filled[i] = np.concatenate([self.filled[i], np.zeros(m, bool)])
+
+    def append(self, ids, counts, **kw):
+        super().append(ids, counts, **kw)
+        for i, m in zip(ids, counts):
+            self.filled[i] = np.concatenate([self.filled[i], np.ones(m, bool)])
+
+    def truncate(self, ids, lens):
+        super().truncate(ids, lens)
+        for i in ids:
+            self.filled[i] = self.filled[i][:self.seqs[i].len]
+
+    def fork(self, src, dst):
+        super().fork(src, dst)
+        for s, d in zip(src, dst):
+            self.filled[d] = self.filled[s].copy()
+
+    def verify(self):
+        self.cache.check()
+        for layer in range(self.cfg.n_layers):
+            for i, s in enumerate(self.seqs):
+                if s.len == 0:
+                    continue
+                got = self.cache.read(layer, self.ids([i]), self.ids([0]), s.len)
+                for which, x in zip("kv", got):
+                    codes, scales = s.values(layer, which)
+                    assert np.array_equal(x[0].cpu().numpy()[self.filled[i]], (codes * scales[..., None])[self.filled[i]]), (layer, i)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("left_over", [1e30, float("inf"), float("nan"), 0.0, 1e-30])
+def test_tokens_after_unwritten_ones_have_their_own_scale(code, left_over):
+    b = Holes(code, dim=32, page=32, layers=2, seqs=6, left_over=left_over)
+    b.hole([0, 1, 2], [5, 16, 40])
+    b.append([2, 0, 1], [3, 1, 7])
+    b.verify()
+    b.hole([0, 1], [20, 1])
+    b.append([0, 1], [2, 40], gain=0.1)
+    b.verify()
+    b.append([3], [50], gain=1e4)               # a left-over of the cache's own
+    b.truncate([3], [16])
+    b.hole([3], [3])
+    b.append([3], [2])
+    b.verify()
+
+
+def test_unwritten_blocks_of_shared_pages():
+    """Sequences of unlike lengths share a page, are extended at once, and not all of them are written."""
+    for parent in (True, False):
+        b = Holes("int8", dim=32, page=64, layers=2, seqs=8, n_pages=60)
+        b.append([0], [64 + 50], gain=100.0)
+        b.fork([0, 0, 0, 0], [1, 2, 3, 4])
+        b.truncate([1, 2, 4], [64 + 10, 64 + 33, 64 + 49])
+        if not parent:
+            b.truncate([0], [0])
+        b.hole([1, 3, 2, 4], [30, 5, 2, 10])
+        b.append([4, 2, 1, 3], [3, 20, 2, 9])
+        b.verify()
+        b.cache.compact()
+        b.append([4, 2, 1, 3], [1, 1, 1, 1])
+        b.verify()
+
+
+@pytest.mark.parametrize("n,each", [(1, 3000), (300, 2), (40, 70)])
+def test_unwritten_blocks_of_even_calls(n, each):
+    b = Holes("int8", heads=1, dim=16, page=16, layers=3, seqs=n, n_pages=n * (each // 16 + 4), max_pages=each // 16 + 4)
+    b.hole(range(n), [each - 1] * n)
+    b.append(range(n), [3] * n)
+    b.cache.extend(b.ids(range(n)), each=each % 29 + 1)
+    b.cache.check()
+    assert b.cache.lens.tolist() == [each + 2 + each % 29 + 1] * n
+    t = each + 2                                 # the first of the new blocks of every sequence has scale 0 in every layer
+    t += -t % 16
+    if t < each + 2 + each % 29 + 1:
+        page = b.cache.table[:, t // 16].long()
+        assert (b.cache.k_scale[:, page] == 0).all() and (b.cache.v_scale[:, page] == 0).all()
+    b.truncate(range(n), [each + 2] * n)
+    b.verify()
+
+
+def test_unwritten_tokens_are_not_seen_from_other_sequences_of_a_prompt_call():
+    b = Holes("e4m3", heads=8, dim=64, page=16, n_pages=200, seqs=3, dtype=BF16, left_over=float("nan"))
+    b.append([0, 1], [200, 90])
+    b.hole([2], [150])
+    q = b.rand(440, 32, 64)
+    out = b.cache.attend(0, b.ids([0, 2, 1]), q.cuda(), starts=b.ids([0, 200, 350, 440]), max_new=200)
+    b.cache.check()
+    for i, rows in ((0, slice(0, 200)), (1, slice(350, 440))):
+        ref = attend64(b.seqs[i], 0, q[rows].double().numpy(), 4, 0.125, -1, 1, 0, 16)
+        tol, _ = bounds(*ref, 64, 200, BF16)
+        assert (np.abs(out[rows].double().cpu().numpy() - ref[0]) <= tol).all()
