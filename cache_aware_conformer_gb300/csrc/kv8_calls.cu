@@ -37,9 +37,10 @@ using namespace cac;
 extern "C" size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
                                            int att_chunk, int sinks) {
     (void)heads;
-    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || att_chunk < 1 || sinks < 0 ||
-        !splits(*c, n, sm_count(c->device), std::max(std::min(max_new, rows), 1), att_left, att_chunk, sinks))
-        return 0;
+    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || att_chunk < 1 || sinks < 0) return 0;
+    // A call without starts has rows / n queries of each sequence, whatever max_new is; one with starts needs no more for it.
+    const int most = std::max(std::max(std::min(max_new, rows), rows / n), 1);
+    if (!splits(*c, n, sm_count(c->device), most, att_left, att_chunk, sinks)) return 0;
     return kv_attend_bytes(c->head_dim, sm_count(c->device));
 }
 

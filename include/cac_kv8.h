@@ -147,6 +147,8 @@ int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const
                    int max_new, int heads, float scale, int att_left, int att_chunk, int sinks, const void* q,
                    long long q_stride, void* out, long long out_stride, float* lse, int dtype, void* workspace,
                    size_t workspace_bytes, void* stream);
+/* Enough for a call with these arguments, with starts or (then for rows / n
+ * queries of each sequence, whatever max_new is) without. */
 size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
                                 int att_chunk, int sinks);
 

@@ -201,3 +201,23 @@ def test_unwritten_tokens_are_not_seen_from_other_sequences_of_a_prompt_call():
         ref = attend64(b.seqs[i], 0, q[rows].double().numpy(), 4, 0.125, -1, 1, 0, 16)
         tol, _ = bounds(*ref, 64, 200, BF16)
         assert (np.abs(out[rows].double().cpu().numpy() - ref[0]) <= tol).all()
+
+
+def test_workspace_is_asked_for_with_any_max_new():
+    """The C call without starts ignores max_new, and so does the size that it is told."""
+    import ctypes
+    b = Both(heads=1, dim=64, page=16, max_pages=100, n_pages=100)
+    b.append([0], [700])
+    lib, ref = b.native.lib(), ctypes.addressof(b.cache._c)
+    q = b.rand(8, 1, 64).cuda()
+    want = b.cache.attend(0, b.ids([0]), q, att_left=280)
+    for max_new in (0, 1, 8, 100):
+        need = lib.cac_kv8_attend_workspace(ref, 1, 8, max_new, 1, 280, 1, 0)
+        space = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+        out = torch.empty_like(q)
+        ids = b.ids([0])
+        r = lib.cac_kv8_attend(ref, 0, 1, ids.data_ptr(), None, 8, max_new, 1, 0.125, 280, 1, 0, q.data_ptr(), 64, out.data_ptr(), 64,
+                               None, 0, space.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+        assert r == 0, max_new
+        b.cache.check()
+        assert torch.equal(out, want)

@@ -136,6 +136,17 @@ def test_bad_attention_calls_are_refused(native, kw, code):
                                        None) == code
 
 
+@pytest.mark.parametrize("heads,left", [(4, 250), (4, 540), (4, 980), (1, 280)])
+@pytest.mark.parametrize("n,rows", [(1, 64), (3, 150), (8, 8 * 64)])
+def test_workspace_of_calls_without_starts(native, heads, left, n, rows):
+    """Such a call has rows / n queries of each sequence; the size that is asked for must not go by a smaller max_new."""
+    c = make(native, kv_heads=heads, max_pages=4000, max_seqs=600)
+    ask = lambda m, left: native.lib().cac_kv8_attend_workspace(ctypes.addressof(c), n, rows, m, heads, left, 1, 0)  # noqa: E731
+    for near in range(left - 40, left + 41):     # the border between whole units and shares lies in one of these
+        want = ask(rows // n, near)
+        assert ask(0, near) == want and ask(1, near) == want and ask(rows, near) >= want
+
+
 def test_binding_refuses_a_bad_config(native):
     cfg = Kv8Config(1, 4, 64, 32, 10, 4, 4)
     with pytest.raises(ValueError):
