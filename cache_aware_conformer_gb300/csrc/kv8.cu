@@ -889,7 +889,7 @@ extern "C" int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* i
     // a token to a warp while that leaves warps' places free (8,192 of them: 256 x 16 tokens 9.6 -> 6.5 us); four where there are
     // more, which look four tokens' places up at once (72,000 tokens: 60 us against 65)
     const int tokens = (long long)n * count <= 8192 ? 1 : 4;
-    const int pieces = (count + tokens - 1) / tokens;
+    const int pieces = count / tokens + (count % tokens != 0);
     const long long blocks = ((long long)n * pieces + 7) / 8;
     if (blocks > INT32_MAX) return CAC_E_LIMIT;
     const dim3 grid((unsigned)blocks), block(256);

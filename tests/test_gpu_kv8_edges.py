@@ -221,3 +221,22 @@ def test_workspace_is_asked_for_with_any_max_new():
         assert r == 0, max_new
         b.cache.check()
         assert torch.equal(out, want)
+
+
+def test_a_read_of_as_many_tokens_as_an_int_counts():
+    """2^31 - 1 tokens, all but the last few before the sequence's first: 69 GB of zeros."""
+    import ctypes
+    count, tokens = 2 ** 31 - 1, 20
+    b = Both(heads=1, dim=16, page=16, dtype=BF16)
+    b.append([0], [tokens])
+    k = torch.full((count, 16), 3.0, dtype=BF16, device="cuda")
+    ids, first = b.ids([0]), b.ids([tokens - count])
+    r = b.native.lib().cac_kv8_read(ctypes.addressof(b.cache._c), 0, 1, ids.data_ptr(), first.data_ptr(), count, k.data_ptr(), None, 1,
+                                    torch.cuda.current_stream().cuda_stream)
+    assert r == 0
+    want, _ = b.cache.read(0, ids, torch.zeros_like(ids), tokens, dtype=BF16)
+    b.cache.check()
+    assert torch.equal(k[-tokens:], want[0, :, 0])
+    assert not any(bool(x.any()) for x in k[:-tokens].split(2 ** 27))
+    del k
+    torch.cuda.empty_cache()
