@@ -768,6 +768,7 @@ class Kv8Cache:
         ints = int(_lib().cac_kv8_work_ints(self._ref))
         if ints == 0:
             raise ValueError(f"{cfg}: a shape outside what the kernels implement")
+        self._own, self._streams = [], {torch.cuda.current_stream(self.device).cuda_stream}   # its tensors, and who uses them
         i8, f32, i32 = torch.int8, torch.float32, torch.int32
         shapes = {"k": (i8, (L, P, H, PT, D)), "v": (i8, (L, P, H, PT, D)),
                   "k_scale": (f32, (L, P, H, PT // 16)), "v_scale": (f32, (L, P, H, PT // 16)),
@@ -785,6 +786,7 @@ class Kv8Cache:
             elif t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() or t.device != self.device:
                 raise ValueError(f"{name}: a contiguous {dt} tensor {shape} on {self.device} is needed")
             setattr(self, name, t)
+            self._own.append(t)
             setattr(self._c, "free_list" if name == "free" else name, t.data_ptr())
         if not tensors:
             self.init()
@@ -794,7 +796,11 @@ class Kv8Cache:
     # The checks below stand on the path of every call of a step, so they avoid what is slow in Python: building shape
     # tuples and device objects, stream contexts, looking functions up.
     def _on(self, stream):
-        return stream.cuda_stream if stream is not None else self._current(self._dev)
+        handle = stream.cuda_stream if stream is not None else self._current(self._dev)
+        if handle not in self._streams:   # the cache's memory is not given out again before this stream's calls have run
+            self._used_on(stream if stream is not None else self._torch.cuda.current_stream(self.device), *self._own)
+            self._streams.add(handle)
+        return handle
 
     @staticmethod
     def _used_on(stream, *tensors):

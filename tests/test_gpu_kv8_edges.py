@@ -1,4 +1,6 @@
 """Edges of the 8-bit K/V cache: what lies beside a sequence, blocks that no write has filled, extreme scales and sizes."""
+import contextlib
+
 import numpy as np
 import pytest
 
@@ -240,3 +242,26 @@ def test_a_read_of_as_many_tokens_as_an_int_counts():
     assert not any(bool(x.any()) for x in k[:-tokens].split(2 ** 27))
     del k
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("how", ["argument", "current"])
+def test_a_cache_dropped_behind_its_calls_on_a_side_stream(how):
+    """Its memory is not given out again before they have run."""
+    b = Both(heads=2, dim=64, page=16, n_pages=700, max_pages=64)
+    side = torch.cuda.Stream()
+    ids, x = b.ids([0, 1]), torch.randn(2000, 2, 64, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(10 ** 9)                                   # about half a second in front of the calls
+    kw = {"stream": side} if how == "argument" else {}
+    with contextlib.nullcontext() if kw else torch.cuda.stream(side):
+        b.cache.extend(ids, each=1000, **kw)
+        b.cache.write(0, ids, x, x, **kw)
+        b.cache.compact(**kw)
+    own = {t.data_ptr() for t in b.cache._own}
+    sizes = [(t.shape, t.dtype) for t in b.cache._own]
+    b.cache = None
+    assert not side.query()                                          # the calls are still to come
+    taken = [torch.empty(s, dtype=d, device="cuda") for s, d in sizes]
+    assert not own & {t.data_ptr() for t in taken}
+    torch.cuda.synchronize()
