@@ -91,8 +91,8 @@ __global__ void kv_init_kernel(cac_kv8 c, long long work_ints) {
 // ---------------------------------------------------------------------------
 // extend.  One block decides for all sequences of the call: it needs the sum of
 // what they ask before it may change anything.  Latency bounds it (a few
-// dependent reads and two scans: 5.8 us for 256 sequences, 9.8 with the truncate before it; copies of shared pages are a kernel
-// of their own, at the memory's rate).
+// dependent reads and two scans; with the kernel behind it, which copies shared pages at the memory's rate and sets the new
+// blocks' scales to 0, 6.5 us for 256 sequences that ask for nothing, 11.6 with a token each and the truncate before it).
 // ---------------------------------------------------------------------------
 struct Want {
     int id, len, count, have, fresh;  // pages it has, pages it needs past those

@@ -739,7 +739,8 @@ class Kv8Cache:
     starts[i] .. starts[i+1]-1 with `starts` an int32 cuda tensor [n + 1] and
     `max_new` no less than the longest.  Calls queue on `stream` (the current one
     by default), never wait, and can be captured into CUDA graphs; errors that
-    only the device sees are raised by check()."""
+    only the device sees are raised by check().  It is for models with plain scaled
+    dot products; this library's encoder and decoders have states of their own."""
 
     def __init__(self, cfg, device=None, tensors=None):
         import torch

@@ -3,12 +3,15 @@
  * over it (C ABI).  Same conventions as cac.h: status codes, device pointers
  * owned by the caller, asynchronous on `stream`, row-major layouts.
  *
- * The encoder's own K/V rings hold the last att_left rows of each stream in
- * bf16.  This cache holds sequences of any length in one byte per value, in
- * pages that forked sequences (beam hypotheses, migrated streams) share, and is
- * read under the same chunked-causal mask ("True streaming encode", §Why this
- * is provably correct: left context and chunk on absolute positions),
- * optionally with the first tokens kept visible.
+ * Sequences of any length in one byte per value, in pages that forked sequences
+ * share, read under a chunked-causal mask with optional first tokens that stay
+ * visible.  The mask is the one of the streaming encoder ("True streaming
+ * encode", §Why this is provably correct: left context and chunk on absolute
+ * positions); the scores are not: here they are scale * q . k, where the
+ * encoder's attention has a term for relative positions, and its beam's
+ * hypotheses are LSTM states without K and V.  So the encoder and the decoders
+ * of this library go on with their own states and call nothing of this; it is
+ * for models beside them whose attention has the plain form.
  *
  * Layout.  Token t of sequence s lies in page table[s][t / page_tokens], row
  * t % page_tokens.  A page holds, for each layer and K/V head, page_tokens rows
@@ -23,7 +26,8 @@
  * older ones, its scale is the larger of the old one and what the new tokens
  * need; where that grows, the older codes are rounded again from code *
  * (old scale / new scale).  An infinite input takes the block's largest code, a
- * NaN takes code 0, and either latches CAC_E_NONFINITE in *status.
+ * NaN takes code 0, and either latches CAC_E_NONFINITE in *status.  A scale of 0
+ * marks a block that an extend began and no write has filled.
  *
  * Nothing here reads device state on the host: lengths, tables and free pages
  * live on the device, so every call can be captured into a CUDA graph and
@@ -100,7 +104,9 @@ int cac_kv8_init(const cac_kv8* c, void* stream);
  * CAC_E_LIMIT (longer than max_pages), CAC_E_BOUNDS (id out of range or negative
  * count), CAC_E_INVAL (an id twice), CAC_E_STATE (the last page was released by
  * trim before a truncate into it) are latched.  Tokens that no write fills have
- * unspecified values in that layer; tokens added after them do not suffer. */
+ * unspecified values in that layer; tokens added after them do not suffer.  A
+ * refused call ends the right to write of the sequences that it names, so that a
+ * write behind it does not go to the tokens before. */
 int cac_kv8_extend(const cac_kv8* c, int n, const int32_t* ids, const int32_t* starts, int each, void* stream);
 
 /* Quantise one layer's K and V of the tokens that the last extend made room
@@ -141,6 +147,8 @@ int cac_kv8_read(const cac_kv8* c, int layer, int n, const int32_t* ids, const i
  * Rows of out and lse that belong to no sequence are left as they were.  Rows of
  * a sequence that has tokens that an extend made room for and no write has filled
  * have unspecified values where a query of the call sees one of the same block.
+ * V blocks may differ in size by any amount up to largest values of 2^80; beside
+ * larger ones, tokens of blocks 2^115 times smaller may be lost from the norm.
  * A bounded wait inside the kernels that gives up latches CAC_E_TIMEOUT.
  * CAC_E_LIMIT: more than 2^26 tiles of 16 query rows (rows * heads / 16). */
 int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
