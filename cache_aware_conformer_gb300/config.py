@@ -127,6 +127,22 @@ class Kv8Config:
     code: str = "int8"            # "int8" or "e4m3"
 
 
+@dataclass(frozen=True)
+class RotaryConfig:
+    """Rotation of queries and keys by their position (include/cac_ops.h)."""
+    head_dim: int                 # multiple of 16, at most 256
+    rot_dim: int = -1             # elements of a head that are turned, even; -1: all
+    layout: str = "half"          # pairs (i, i + rot_dim / 2) or, "pairs", (2 i, 2 i + 1)
+    base: float = 10000.0         # frequencies base^(-2 i / rot_dim)
+    scaling: str = "none"         # "none", "linear", "base" or "ramp": for contexts `factor` times longer
+    factor: float = 1.0
+    original: int = 0             # "ramp": tokens of the context that the frequencies were made for
+    low: float = 1.0              # "ramp": turns over it up to which a frequency is divided by factor
+    high: float = 32.0            # "ramp": turns from which it stays
+    amplitude: float = 1.0        # of cosine and sine
+    eps: float = 1e-6             # of the norm
+
+
 def subsampled_len(t_mel: int) -> int:
     """Encoder frames produced from t_mel mel frames: ceil(.) three times."""
     t = t_mel

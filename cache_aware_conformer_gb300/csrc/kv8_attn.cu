@@ -78,11 +78,11 @@ struct Tile {
     int j0;                    // its first token
 };
 template <int CODE>
-__device__ __forceinline__ Tile tile_of(const KvAttend& a, int id, int len, int lot, int skt, int kt, int head) {
+__device__ __forceinline__ Tile tile_of(const KvAttend& a, const SeqWork& s, int kt, int head) {
     Tile t{-1, 0.f, 0.f, 0.f, 0};
-    t.j0 = (kt < skt ? kt : lot + kt - skt) * KV_BLOCK;
-    if (t.j0 < len) {
-        const int page = a.c.table[(long long)id * a.c.max_pages + t.j0 / a.c.page_tokens];
+    t.j0 = s.block(kt) * KV_BLOCK;
+    if (t.j0 < s.len) {
+        const int page = a.c.table[(long long)s.id * a.c.max_pages + t.j0 / a.c.page_tokens];
         if (page >= 0) {
             const int in_page = t.j0 % a.c.page_tokens;
             const long long sc = kv_scale_at(a.c, a.layer, page, head) + in_page / KV_BLOCK;
@@ -161,6 +161,10 @@ __device__ __forceinline__ float load_query(const T* src, bool on, int t, int D,
 struct Seen {
     int lo_max, hi_min, lo_min, hi_max;
     __device__ __forceinline__ void set(const KvAttend& a, const SeqWork& s, int r0, int size) {
+        if (a.shared) {
+            hi_min = hi_max = s.len, lo_max = lo_min = s.lot * KV_BLOCK;
+            return;
+        }
         // rows in order of their positions: the first and last bound the windows
         const int p0 = s.len - s.m + a.query_of(r0), p1 = s.len - s.m + a.query_of(min(r0 + size, s.m * a.group) - 1);
         const bool any = s.len > 0 && p1 >= 0;
@@ -214,6 +218,12 @@ __device__ __forceinline__ void put_run(const KvAttend& a, const SeqWork& s, int
         store_run<float, RUN>(cut->o + ((size_t)slot * 16 + row - r0) * HDP + e, y);
     } else if (e < a.c.head_dim) {
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+        if (a.part_o) {
+#pragma unroll
+            for (int k = 0; k < RUN; ++k) y[k] *= NORM;
+            store_run<float, RUN>(a.part_o + ((s.row0 + (long long)query) * a.heads + qh) * a.c.head_dim + e, y);
+            return;
+        }
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
         for (int k = 0; k < RUN; ++k) y[k] = y[k] * NORM * inv;  // NORM * inv may be too small a number
@@ -226,6 +236,9 @@ __device__ __forceinline__ void put_sums(const KvAttend& a, const SeqWork& s, in
     if (cut) {
         cut->ml[((size_t)slot * 16 + row - r0) * 2] = m;
         cut->ml[((size_t)slot * 16 + row - r0) * 2 + 1] = l;
+    } else if (a.part_o) {
+        const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+        a.part_ml[(s.row0 + (long long)query) * a.heads + qh] = make_float2(m, l);
     } else if (a.lse) {
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
         a.lse[(s.row0 + (long long)query) * a.heads + qh] =
@@ -249,11 +262,12 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
         set(a, s, r0, 16);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int r = r0 + g + 8 * h, query = a.query_of(r), p = s.len - s.m + query;
+            const int r = r0 + g + 8 * h, query = a.query_of(r);
             const bool on = r < s.m * a.group;
+            const RowSeen see = row_seen(a, s, r);
             m[h] = -INFINITY, l[h] = 0.f;
-            low[h] = on && p >= 0 ? a.win.low(p) : 0;
-            high[h] = on && p >= 0 && s.len > 0 ? a.win.high(p, s.len) : 0;
+            low[h] = see.on ? see.low : 0;
+            high[h] = see.on ? see.high : 0;
             uint32_t x[STEPS], y[STEPS], xl[LO], yl[LO];
             f[h] = a.scale * LOG2E / load_query<T, HDP>(static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
                                                             (long long)(head * a.group + r - query * a.group) * D,
@@ -467,12 +481,11 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
                                             r < s.m * a.group, t, D, q0, q1, l0, l1);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-            const int row = r0 + 2 * t + b, p = s.len - s.m + a.query_of(row);
-            const bool on = row < s.m * a.group && p >= 0 && s.len > 0;
+            const RowSeen see = row_seen(a, s, r0 + 2 * t + b);
             f[b] = a.scale * LOG2E / __shfl_sync(0xffffffffu, up, 4 * (2 * t + b));  // by a power of two: exact
             m[b] = -INFINITY, l[b] = 0.f;
-            low[b] = on ? a.win.low(p) : 0;
-            high[b] = on ? a.win.high(p, s.len) : 0;
+            low[b] = see.on ? see.low : 0;
+            high[b] = see.on ? see.high : 0;
         }
 #pragma unroll
         for (int n = 0; n < MT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
@@ -622,7 +635,7 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
         }
         // only a sequence with more rows than max_new has rows 8 .. 15: they see nothing
         const int row = r0 + 8 + g;
-        if (row < s.m * a.group && !cut) {
+        if (row < s.m * a.group && !cut && !a.part_o) {
             const int D = a.c.head_dim, query = a.query_of(row), qh = head * a.group + row - query * a.group;
             T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D;
             for (int e = t; e < D; e += 4) dst[e] = from_f<T>(0.f);
@@ -736,6 +749,14 @@ __device__ __forceinline__ void join_rows(const KvAttend& a, const Partials& p, 
             } else {
                 const int row = r0 + at, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
                 const bool seen = l[b] > 0.f || l[b] != l[b];
+                if (a.part_o) {
+                    const long long part = (s.row0 + (long long)query) * a.heads + qh;
+#pragma unroll
+                    for (int c = 0; c < PER; ++c)
+                        if (lane * PER + c < D) a.part_o[part * D + lane * PER + c] = o[b][c] * NORM;
+                    if (lane == 0) a.part_ml[part] = make_float2(top[b], l[b]);
+                    continue;
+                }
                 T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
@@ -769,7 +790,7 @@ template <class T, int HDP, bool LOW, bool SPLIT> struct Shape {
     static constexpr int BYTES = WARPS * STAGES * STAGE;
     static constexpr int BLOCKS = !SPLIT && HDP == 64 ? 4 : 1;  // of an SM
     static_assert(WARPS <= MOST_WARPS && MOST_WARPS <= 16, "the workspace has room for the parts of so many");
-    static_assert(BYTES + (SPLIT ? 20 * 1024 : 0) <= 227 * 1024, "shared memory");
+    static_assert(BYTES + (SPLIT ? 24 * 1024 : 0) <= 227 * 1024, "shared memory");
 };
 
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
@@ -853,9 +874,9 @@ __global__ void __launch_bounds__(Shape<T, HDP, LOW, SPLIT>::WARPS * 32, (Shape<
             const SeqWork& w = s_seq[lo];
             const long long in = x - s_first[lo];
             const int u = (int)(in / w.tiles), kt = (int)(in - (long long)u * w.tiles);
-            return tile_of<CODE>(a, w.id, w.len, w.lot, w.skt, kt, u % kvh);
+            return tile_of<CODE>(a, w, kt, u % kvh);
         } else {
-            return tile_of<CODE>(a, s.id, s.len, s.lot, s.skt, (int)x, unit % kvh);
+            return tile_of<CODE>(a, s, (int)x, unit % kvh);
         }
     };
     Tile now = look(x0 + lane);
@@ -1013,6 +1034,12 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
     for (int k = 0; k < JOIN_Y; ++k) o += s_o[k][d], l += s_l[k];
     const bool seen = l > 0.f || l != l;
     const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
+    if (a.part_o) {
+        const long long at = (row0 + (long long)query) * a.heads + qh;
+        if (d < a.c.head_dim) a.part_o[at * a.c.head_dim + d] = o * NORM;
+        if (d == 0) a.part_ml[at] = make_float2(top, l);
+        return;
+    }
     if (d < a.c.head_dim)
         static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + d] =
             from_f<T>(seen ? o * NORM / l : 0.f);

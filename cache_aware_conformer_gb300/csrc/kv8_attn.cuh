@@ -68,13 +68,26 @@ __device__ __forceinline__ float move_norm(float l, float d, float r) {
 struct SeqWork {
     int id, len, m, row0;      // len 0: nothing is seen
     int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1)
+    int gap0, gap;             // from block gap0 on, gap blocks are left out
+    __device__ __forceinline__ int block(int kt) const {
+        if (kt < skt) return kt;
+        const int b = lot + kt - skt;
+        return b < gap0 ? b : b + gap;
+    }
 };
 __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
     SeqWork s;
     s.row0 = a.rows.at(i);
     s.m = a.rows.at(i + 1) - s.row0;
+    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1, s.gap0 = 0, s.gap = 0;
+    if (a.shared) {
+        const int4 g = a.shared[i];
+        s.id = g.x;
+        if (g.z > g.y) s.len = g.z * KV_BLOCK, s.lot = g.y, s.tiles = g.z - g.y;
+        else s.m = 0;
+        return s;
+    }
     s.id = a.ids[i];
-    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1;
     const bool rows_ok = s.m >= 0 && s.row0 >= 0 && s.row0 + (long long)s.m <= a.rows.rows;
     if (!rows_ok) s.m = 0;
     if (s.id >= 0 && s.id < a.c.max_seqs && s.m <= a.max_new && rows_ok) {
@@ -87,8 +100,25 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
         s.lot = low / KV_BLOCK;
         s.skt = min((min(a.win.sinks, high) + KV_BLOCK - 1) / KV_BLOCK, s.lot);
         s.tiles = s.skt + (high + KV_BLOCK - 1) / KV_BLOCK - s.lot;
+        if (a.skip) {
+            const int2 k = a.skip[i];
+            s.gap0 = k.x, s.gap = k.y - k.x;
+            s.tiles = max(s.tiles - s.gap, 1);   // one that lies past the end where nothing else is left
+        }
     }
     return s;
+}
+
+// The position of a row's query, and the tokens that it sees.
+struct RowSeen {
+    bool on;
+    int low, high;
+};
+__device__ __forceinline__ RowSeen row_seen(const KvAttend& a, const SeqWork& s, int row) {
+    if (a.shared) return {row < s.m * a.group, s.lot * KV_BLOCK, s.len};
+    const int p = s.len - s.m + a.query_of(row);
+    const bool on = row < s.m * a.group && p >= 0 && s.len > 0;
+    return {on, on ? a.win.low(p) : 0, on ? a.win.high(p, s.len) : 0};
 }
 
 constexpr int TA_SEQS = 512;     // sequences of one launch of kv8_attn.cu's kernels
@@ -103,5 +133,9 @@ size_t kv_attend_bytes(int head_dim, int sms);
 // whether it takes a call whose sequences have `rows` query rows to a K/V head on average
 bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows);
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s);
+// kv8_shared.cu: a.rows and a.ids are the whole call's; workspace of kv_shared_bytes; split as above, for what is not shared
+cudaError_t kv_attend_shared(const KvAttend& a, int dtype, const int32_t* groups, int n_groups, bool split, int sms, void* workspace,
+                             cudaStream_t s);
+size_t kv_shared_bytes(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms);
 
 }  // namespace cac

@@ -29,6 +29,44 @@ bool splits(const cac_kv8& c, int n, int sms, int max_new, int left, int chunk, 
     return tokens > tiles * KV_BLOCK;
 }
 
+// CAC_OK or what is wrong with the arguments that both attention calls have
+int check_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows, int max_new, int heads,
+                 float scale, int att_chunk, int sinks, const void* q, long long q_stride, void* out, long long out_stride,
+                 float* lse, int dtype) {
+    const int r = kv_check_cache(c);
+    if (r != CAC_OK) return r;
+    if (n < 0 || (n > 0 && !ids) || layer < 0 || layer >= c->n_layers || rows < 0 || heads < 1 || att_chunk < 1 ||
+        sinks < 0 || (dtype != CAC_DTYPE_F32 && dtype != CAC_DTYPE_BF16) || !(scale - scale == 0.f))
+        return CAC_E_INVAL;
+    if (heads % c->kv_heads || heads > 65535) return CAC_E_INVAL;
+    if (n == 0 || rows == 0) return CAC_OK;
+    if ((!starts && rows % n) || (starts && max_new < 0)) return CAC_E_INVAL;
+    const long long width = (long long)heads * c->head_dim, size = dtype == CAC_DTYPE_BF16 ? 2 : 4;
+    if (!q || !out || q == out || q_stride < width || out_stride < width) return CAC_E_INVAL;
+    const uintptr_t words = reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(starts) |
+                            reinterpret_cast<uintptr_t>(lse);
+    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
+        ((q_stride * size | out_stride * size) & 15) || (words & 3))
+        return CAC_E_ALIGN;
+    return CAC_OK;
+}
+
+// Part of a call: sequences i0 .. i0 + part - 1.
+KvAttend part_of(const cac_kv8& c, int layer, int n, int i0, int part, const int32_t* ids, const int32_t* starts, int rows, int most,
+                 int heads, float scale, const KvWindow& win, const void* q, long long q_stride, void* out, long long out_stride,
+                 float* lse) {
+    const int each = rows / n, group = heads / c.kv_heads;
+    KvAttend a{};
+    a.c = c;
+    a.rows = {starts ? starts + i0 : nullptr, each, part, rows, each * i0};
+    a.win = win;
+    a.ids = ids + i0;
+    a.q = q, a.out = out, a.lse = lse, a.q_stride = q_stride, a.out_stride = out_stride;
+    a.scale = scale, a.layer = layer, a.heads = heads, a.group = group, a.max_new = most;
+    a.group_mul = group > 1 ? (uint32_t)((1ull << 32) / group) + 1 : 0u;
+    return a;
+}
+
 }  // namespace
 }  // namespace cac
 
@@ -48,21 +86,9 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
                               int max_new, int heads, float scale, int att_left, int att_chunk, int sinks,
                               const void* q, long long q_stride, void* out, long long out_stride, float* lse,
                               int dtype, void* workspace, size_t workspace_bytes, void* stream) {
-    const int r = kv_check_cache(c);
-    if (r != CAC_OK) return r;
-    if (n < 0 || (n > 0 && !ids) || layer < 0 || layer >= c->n_layers || rows < 0 || heads < 1 || att_chunk < 1 ||
-        sinks < 0 || (dtype != CAC_DTYPE_F32 && dtype != CAC_DTYPE_BF16) || !(scale - scale == 0.f))
-        return CAC_E_INVAL;
-    if (heads % c->kv_heads || heads > 65535) return CAC_E_INVAL;
-    if (n == 0 || rows == 0) return CAC_OK;
-    if ((!starts && rows % n) || (starts && max_new < 0)) return CAC_E_INVAL;
-    const long long width = (long long)heads * c->head_dim, size = dtype == CAC_DTYPE_BF16 ? 2 : 4;
-    if (!q || !out || q == out || q_stride < width || out_stride < width) return CAC_E_INVAL;
-    const uintptr_t words = reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(starts) |
-                            reinterpret_cast<uintptr_t>(lse);
-    if (((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15) ||
-        ((q_stride * size | out_stride * size) & 15) || (words & 3))
-        return CAC_E_ALIGN;
+    const int r = check_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_chunk, sinks, q, q_stride, out, out_stride,
+                               lse, dtype);
+    if (r != CAC_OK || n == 0 || rows == 0) return r;
     const int group = heads / c->kv_heads, most = starts ? std::max(std::min(max_new, rows), 1) : rows / n;
     const int sms = sm_count(c->device);
     if (sms < 1) return CAC_E_CUDA;
@@ -75,10 +101,8 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
     if (!dev.ok) return CAC_E_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     for (int i0 = 0; i0 < n; i0 += TA_SEQS) {
-        const int each = rows / n, part = std::min(n - i0, TA_SEQS);
-        const KvAttend a{*c, {starts ? starts + i0 : nullptr, each, part, rows, each * i0}, {att_left, att_chunk, sinks},
-                         ids + i0, q, out, lse, q_stride, out_stride, scale, layer, heads, group, most,
-                         group > 1 ? (uint32_t)((1ull << 32) / group) + 1 : 0u};
+        const KvAttend a = part_of(*c, layer, n, i0, std::min(n - i0, TA_SEQS), ids, starts, rows, most, heads, scale,
+                                   {att_left, att_chunk, sinks}, q, q_stride, out, out_stride, lse);
         cudaError_t e;
         if (kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
             e = kv_launch_prompt(a, dtype, s);
@@ -88,4 +112,44 @@ extern "C" int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t*
         if (e != cudaSuccess) return CAC_E_CUDA;
     }
     return CAC_OK;
+}
+
+extern "C" size_t cac_kv8_attend_shared_workspace(const cac_kv8* c, int n, int rows, int max_new, int n_groups, int heads,
+                                                  int att_left, int att_chunk, int sinks) {
+    (void)att_left;
+    if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || n_groups < 0 || heads < 1 || att_chunk < 1 || sinks < 0)
+        return 0;
+    return kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sm_count(c->device));
+}
+
+extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
+                                     int max_new, int n_groups, const int32_t* groups, int heads, float scale, int att_left,
+                                     int att_chunk, int sinks, const void* q, long long q_stride, void* out,
+                                     long long out_stride, float* lse, int dtype, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+    const int r = check_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_chunk, sinks, q, q_stride, out, out_stride,
+                               lse, dtype);
+    if (r != CAC_OK) return r;
+    if (n_groups < 0 || (n_groups > 0 && !groups) || (n_groups == 0 && groups)) return CAC_E_INVAL;
+    if (reinterpret_cast<uintptr_t>(groups) & 3) return CAC_E_ALIGN;
+    if (n == 0 || rows == 0) return CAC_OK;
+    const int group = heads / c->kv_heads, most = starts ? std::max(std::min(max_new, rows), 1) : rows / n;
+    const int sms = sm_count(c->device);
+    if (sms < 1) return CAC_E_CUDA;
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
+        workspace_bytes < kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sms))
+        return CAC_E_INVAL;
+    if (((long long)rows * group / 16 + n) * c->kv_heads > INT32_MAX / 32 || n_groups > (1 << 28)) return CAC_E_LIMIT;
+    const KvAttend a = part_of(*c, layer, n, 0, n, ids, starts, rows, most, heads, scale, {att_left, att_chunk, sinks}, q, q_stride,
+                               out, out_stride, lse);
+    // Sequences with many query rows each: their products bound the call, and every row tile reads the tokens anyway.
+    if (kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
+        return cac_kv8_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_left, att_chunk, sinks, q, q_stride, out,
+                              out_stride, lse, dtype, workspace, workspace_bytes, stream);
+    DeviceScope dev(c->device);
+    if (!dev.ok) return CAC_E_CUDA;
+    return kv_attend_shared(a, dtype, groups, std::max(n_groups, 1), splits(*c, n, sms, most, att_left, att_chunk, sinks), sms, workspace,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? CAC_OK
+               : CAC_E_CUDA;
 }

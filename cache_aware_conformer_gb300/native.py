@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_longlong, c_size_t, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_longlong, c_size_t, c_void_p
 
 import numpy as np
 
@@ -38,7 +38,7 @@ SYMBOLS = ["cac_weights_size", "cac_model_create", "cac_model_create_palette", "
            # include/cac_decode.h
            "cac_decoder_create", "cac_decoder_destroy", "cac_decoder_reset", "cac_decoder_step",
            "cac_decoder_check", "cac_decoder_get_state",
-           "cac_op_wait_selftest", "cac_op_gemm_palette",
+           "cac_op_wait_selftest", "cac_op_gemm_palette", "cac_op_gemm_w4", "cac_op_rotary_steps", "cac_op_rotate",
            # include/cac_frontend.h
            "cac_frontend_create", "cac_frontend_destroy", "cac_frontend_reset", "cac_frontend_push",
            "cac_frontend_flush", "cac_frontend_get_state", "cac_frontend_schedule", "cac_frontend_tables",
@@ -48,7 +48,8 @@ SYMBOLS = ["cac_weights_size", "cac_model_create", "cac_model_create_palette", "
 
 # every symbol include/cac_kv8.h declares
 KV8_SYMBOLS = ["cac_kv8_work_ints", "cac_kv8_init", "cac_kv8_extend", "cac_kv8_write", "cac_kv8_read",
-               "cac_kv8_attend", "cac_kv8_attend_workspace", "cac_kv8_fork", "cac_kv8_truncate", "cac_kv8_trim",
+               "cac_kv8_attend", "cac_kv8_attend_workspace", "cac_kv8_attend_shared", "cac_kv8_attend_shared_workspace",
+               "cac_kv8_rotate", "cac_kv8_fork", "cac_kv8_truncate", "cac_kv8_trim",
                "cac_kv8_compact", "cac_kv8_check"]
 
 
@@ -79,6 +80,16 @@ class CacKv8(ctypes.Structure):
                                         "max_pages", "code", "device", "reserved")] +
                 [(n, c_void_p) for n in ("k", "v", "k_scale", "v_scale", "table", "lens", "refs", "free_list", "n_free",
                                          "pending", "work", "status")])
+
+
+class CacW4(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("n", "k", "group", "device")] + [(n, c_void_p) for n in ("packed", "scale", "zero")]
+
+
+class CacRotary(ctypes.Structure):
+    _fields_ = ([(n, c_int32) for n in ("head_dim", "rot_dim", "layout", "dtype", "device")] +
+                [("amplitude", c_float), ("eps", c_float), ("reserved", c_int32)] +
+                [(n, c_void_p) for n in ("steps", "q_gain", "k_gain")])
 
 
 _LIB = None
@@ -135,6 +146,10 @@ def _lib():
             "cac_decoder_get_state": (c_int, [vp, c_int, fp, fp, fp, ip]),
             "cac_op_wait_selftest": (c_int, [c_int, vp]),
             "cac_op_gemm_palette": (c_int, [c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp]),
+            "cac_op_gemm_w4": (c_int, [vp, c_int, vp, c_longlong, vp, vp, c_longlong, c_int, vp]),
+            "cac_op_rotary_steps": (c_int, [c_int, c_double, c_int, c_double, c_double, c_double, c_double, vp]),
+            "cac_op_rotate": (c_int, [vp, c_int, vp, c_int, vp, c_longlong, vp, c_longlong, c_int, vp, c_longlong, vp,
+                                      c_longlong, vp]),
             "cac_frontend_create": (c_int, [c_int, POINTER(vp)]),
             "cac_frontend_destroy": (None, [vp]),
             "cac_frontend_reset": (c_int, [vp, c_int, ip]),
@@ -157,6 +172,11 @@ def _lib():
             "cac_kv8_attend": (c_int, [vp, c_int, c_int, vp, vp, c_int, c_int, c_int, c_float, c_int, c_int, c_int, vp,
                                        c_longlong, vp, c_longlong, vp, c_int, vp, c_size_t, vp]),
             "cac_kv8_attend_workspace": (c_size_t, [vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+            "cac_kv8_attend_shared": (c_int, [vp, c_int, c_int, vp, vp, c_int, c_int, c_int, vp, c_int, c_float, c_int, c_int,
+                                              c_int, vp, c_longlong, vp, c_longlong, vp, c_int, vp, c_size_t, vp]),
+            "cac_kv8_attend_shared_workspace": (c_size_t, [vp, c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_int]),
+            "cac_kv8_rotate": (c_int, [vp, vp, c_int, vp, vp, c_int, c_int, vp, c_longlong, vp, c_longlong, vp, c_longlong,
+                                       vp, c_longlong, vp]),
             "cac_kv8_fork": (c_int, [vp, c_int, vp, vp, vp]),
             "cac_kv8_truncate": (c_int, [vp, c_int, vp, vp, c_int, vp]),
             "cac_kv8_trim": (c_int, [vp, c_int, vp, c_int, c_int, c_int, vp]),
@@ -492,6 +512,138 @@ def gemm_palette(A, packed, table, bias=None, out=None, status=None, stream=None
     return out
 
 
+def gemm_w4(A, packed, scale, zero=None, bias=None, out=None, stream=None):
+    """C = A W^T (+ bias) with weights at 4 bits (cac_op_gemm_w4): W[n][k] = scale[n][k / group] * (code - zero[n][k / group]),
+    two codes to a byte, the even k in the low half.  A: cuda bf16 or fp32 [M, K], rows may be strided; packed: uint8
+    [N, K/2]; scale: bf16 [N, K/group], group 32, 64 or 128; zero: uint8 as scale, or None for 8; bias: fp32 [N].  Returns
+    [M, N] of A's type.  `w4.quantize` makes packed, scale and zero."""
+    import torch
+    if A.dim() != 2 or packed.dim() != 2 or scale.dim() != 2 or A.size(1) != 2 * packed.size(1) or \
+            scale.size(0) != packed.size(0) or scale.size(1) < 1 or A.size(1) % scale.size(1) or not A.is_cuda:
+        raise ValueError("A [M, K], packed [N, K / 2] and scale [N, K / group] are needed")
+    (M, K), (N, G) = A.shape, scale.shape
+    dev, dt = A.device, A.dtype
+    for t, want, what in ((packed, torch.uint8, "packed"), (scale, torch.bfloat16, "scale"), (zero, torch.uint8, "zero"),
+                          (bias, torch.float32, "bias")):
+        if t is not None and (t.dtype is not want or t.device != dev or not t.is_contiguous()):
+            raise ValueError(f"{what}: a contiguous {want} tensor on {dev} is needed")
+    if zero is not None and zero.shape != scale.shape or bias is not None and tuple(bias.shape) != (N,):
+        raise ValueError("zero has the shape of scale, bias is [N]")
+    if dt is not torch.bfloat16 and dt is not torch.float32 or (K > 1 and A.stride(1) != 1):
+        raise ValueError("A: bfloat16 or float32, with the elements of a row next to each other")
+    on = stream if stream is not None else torch.cuda.current_stream(dev)
+    if out is None:
+        if stream is None:
+            out = torch.empty((M, N), dtype=dt, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                out = torch.empty((M, N), dtype=dt, device=dev)
+    elif out.dtype is not dt or tuple(out.shape) != (M, N) or out.device != dev or (N > 1 and out.stride(1) != 1):
+        raise ValueError(f"out: a tensor [{M}, {N}] of A's type on {dev}")
+    if M == 0:
+        return out
+    if stream is not None:
+        Kv8Cache._used_on(stream, A, packed, scale, zero, bias, out)
+    w = CacW4(N, K, K // G, dev.index, _ptr(packed), _ptr(scale), _ptr(zero))
+    _check(_lib().cac_op_gemm_w4(ctypes.addressof(w), M, _ptr(A), A.stride(0) if M > 1 else K, _ptr(bias), _ptr(out),
+                                 out.stride(0) if M > 1 else N, 1 if dt is torch.bfloat16 else 0, on.cuda_stream),
+           "cac_op_gemm_w4")
+    return out
+
+
+class Rotary:
+    """Rotation of queries and keys by their position, with an optional norm for each head before it (cac_op_rotate):
+    holds the frequencies and the gains on the device.  `rotate` takes positions; Kv8Cache.rotate finds them in the
+    cache."""
+
+    SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+
+    def __init__(self, cfg, q_gain=None, k_gain=None, device=None):
+        import torch
+        rot = cfg.head_dim if cfg.rot_dim < 0 else cfg.rot_dim
+        if cfg.layout not in ("half", "pairs") or cfg.scaling not in self.SCALINGS:
+            raise ValueError(f"{cfg}: layout half or pairs, scaling {sorted(self.SCALINGS)}")
+        if cfg.head_dim < 16 or cfg.head_dim > 256 or cfg.head_dim % 16 or rot > cfg.head_dim or rot % 2:
+            raise ValueError(f"{cfg}: a head of 16 to 256 elements, a multiple of 16, of which an even number is turned")
+        steps = (ctypes.c_uint64 * max(rot // 2, 1))()
+        if _lib().cac_op_rotary_steps(rot, cfg.base, self.SCALINGS[cfg.scaling], cfg.factor, cfg.original, cfg.low, cfg.high,
+                                      ctypes.addressof(steps)):
+            raise ValueError(f"{cfg}: no such frequencies")
+        self.cfg, self.device = cfg, torch.device("cuda" if device is None else device)
+        if self.device.type != "cuda":
+            raise ValueError("a Rotary lives on a CUDA device")
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.steps = torch.from_numpy(np.frombuffer(steps, dtype=np.int64).copy()).to(self.device)
+        gains = []
+        for g, what in ((q_gain, "q_gain"), (k_gain, "k_gain")):
+            if g is not None and tuple(g.shape) != (cfg.head_dim,):
+                raise ValueError(f"{what}: [{cfg.head_dim}]")
+            gains.append(None if g is None else g.to(self.device, torch.float32).contiguous().clone())
+        self.q_gain, self.k_gain = gains
+        self._c = [CacRotary(cfg.head_dim, rot, 0 if cfg.layout == "half" else 1, dt, self.device.index, cfg.amplitude, cfg.eps, 0,
+                             self.steps.data_ptr(), _ptr(self.q_gain), _ptr(self.k_gain)) for dt in (0, 1)]
+        self._refs = [ctypes.addressof(c) for c in self._c]
+        self._streams = {torch.cuda.current_stream(self.device).cuda_stream}
+
+    def _side(self, t, out, what, stream):
+        """(heads, pointer, stride, pointer and stride of the result, the result, dtype code) of q or k."""
+        import torch
+        if t is None:
+            if out is not None:
+                raise ValueError(f"{what}: no input for its output")
+            return 0, None, 0, None, 0, None, None
+        D = self.cfg.head_dim
+        if out is None:
+            if stream is None:
+                out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+            else:
+                with torch.cuda.stream(stream):
+                    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+        for x in (t, out):
+            if x.dim() != 3 or x.shape != t.shape or x.size(2) != D or x.get_device() != self.device.index or x.dtype is not t.dtype or \
+                    x.dtype not in (torch.bfloat16, torch.float32):
+                raise ValueError(f"{what}: bfloat16 or float32 [rows, heads, {D}] on {self.device}")
+            if x.stride(2) != 1 or (x.size(1) > 1 and x.stride(1) != D):
+                raise ValueError(f"{what}: the heads of a row have to lie one after another")
+        stride = lambda x: x.stride(0) if x.size(0) > 1 else x.size(1) * D  # noqa: E731
+        return t.size(1), t.data_ptr(), stride(t), out.data_ptr(), stride(out), out, 1 if t.dtype is torch.bfloat16 else 0
+
+    def _sides(self, q, k, out, stream):
+        """Both sides of a call: its rows, the dtype's struct, and what the entry points take."""
+        import torch
+        if q is None and k is None:
+            raise ValueError("queries, keys or both")
+        qo, ko = out if out is not None else (None, None)
+        one, two = self._side(q, qo, "q", stream), self._side(k, ko, "k", stream)
+        rows = (q if q is not None else k).size(0)
+        if q is not None and k is not None and (k.size(0) != rows or one[6] != two[6]):
+            raise ValueError("q and k have the same rows and type")
+        handle = (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        if handle not in self._streams:   # its memory is not given out again before this stream's calls have run
+            Kv8Cache._used_on(stream if stream is not None else torch.cuda.current_stream(self.device), self.steps, self.q_gain,
+                              self.k_gain)
+            self._streams.add(handle)
+        if stream is not None:
+            Kv8Cache._used_on(stream, q, k, one[5], two[5])
+        return rows, self._refs[one[6] if q is not None else two[6]], one, two, handle
+
+    def rotate(self, positions, q=None, k=None, out=None, stream=None):
+        """(q, k) turned: q [rows, heads, head_dim], k [rows, kv_heads, head_dim] (either may be None), positions an int32
+        cuda tensor [rows].  out: (q_out, k_out), which may be the inputs."""
+        import torch
+        rows, ref, a, b, handle = self._sides(q, k, out, stream)
+        if positions.dtype is not torch.int32 or positions.dim() != 1 or positions.numel() != rows or \
+                positions.get_device() != self.device.index or not positions.is_contiguous():
+            raise ValueError(f"positions: a contiguous int32 tensor [{rows}] on {self.device} is needed")
+        if stream is not None:
+            Kv8Cache._used_on(stream, positions)
+        r = _lib().cac_op_rotate(ref, rows, positions.data_ptr(), *a[:5], *b[:5], handle)
+        if r:
+            _check(r, "cac_op_rotate")
+        return a[5], b[5]
+
+
 def build_checked() -> bool:
     """True when the loaded library is the CAC_CHECKED build."""
     return bool(_lib().cac_build_checked())
@@ -764,6 +916,7 @@ class Kv8Cache:
         lib = _lib()
         self._extend, self._write, self._attend, self._truncate = (
             lib.cac_kv8_extend, lib.cac_kv8_write, lib.cac_kv8_attend, lib.cac_kv8_truncate)
+        self._attend_shared, self._rotate = lib.cac_kv8_attend_shared, lib.cac_kv8_rotate
         self._scale = D ** -0.5
         self._space = {}   # workspace bytes of the calls seen, by their sizes
         ints = int(_lib().cac_kv8_work_ints(self._ref))
@@ -930,6 +1083,68 @@ class Kv8Cache:
         if r:
             _check(r, "cac_kv8_attend")
         return (out, sums) if lse else out
+
+    def attend_shared(self, layer: int, ids, q, groups=None, att_left: int = -1, att_chunk: int = 1, sinks: int = 0, scale=None,
+                      starts=None, max_new=None, lse: bool = False, out=None, stream=None):
+        """attend for sequences that share a prefix, as forks do (cac_kv8_attend_shared): the tokens that all queries of a
+        group see in the same pages are read once.  groups: int32 cuda tensor [n_groups + 1], group g being the call's
+        sequences groups[g] .. groups[g+1]-1; None: all of them are one."""
+        n, p, s = self._list(ids, starts)
+        rows, heads = (q.size(0), q.size(1)) if q.dim() == 3 else (0, 0)
+        qs, dt = self._act(q, heads, "q")
+        n_groups = 0 if groups is None else groups.numel() - 1
+        g = None if groups is None else self._ints(groups, max(n_groups, 0) + 1, "groups")
+        if s is None:
+            max_new = rows // n if n else 0
+        elif max_new is None:
+            max_new = rows
+        key = (n, rows, max_new, n_groups, heads, att_left, att_chunk, sinks)
+        need = self._space.get(key)
+        if need is None:
+            if len(self._space) >= 256:
+                self._space.clear()
+            need = self._space[key] = int(_lib().cac_kv8_attend_shared_workspace(self._ref, *key))
+        D = self._c.head_dim
+        space = sums = None
+        if out is None:
+            if stream is None and q.is_contiguous():
+                out = self._torch.empty_like(q)
+            else:
+                out = self._empty(stream, ((rows, heads, D), q.dtype))[0]
+            os_ = heads * D
+        else:
+            os_, _ = self._act(out, heads, "out")
+            self._alike(out, q, "out")
+        if lse:
+            sums = self._empty(stream, ((rows, heads), self._f32))[0]
+        if need:
+            space = self._empty(stream, ((need,), self._torch.uint8))[0]
+        if stream is not None:
+            self._used_on(stream, ids, starts, q, out, groups)
+        r = self._attend_shared(self._ref, layer, n, p, s, rows, max_new, n_groups, g, heads, self._scale if scale is None else scale,
+                                att_left, att_chunk, sinks, q.data_ptr(), qs, out.data_ptr(), os_,
+                                None if sums is None else sums.data_ptr(), dt, None if space is None else space.data_ptr(), need,
+                                self._on(stream))
+        if r:
+            _check(r, "cac_kv8_attend_shared")
+        return (out, sums) if lse else out
+
+    def rotate(self, ids, rotary, q=None, k=None, starts=None, max_new=None, out=None, stream=None):
+        """(q, k) of each sequence's last tokens turned by their positions in the cache (cac_kv8_rotate); arguments as
+        Rotary.rotate's.  Extend first, then rotate, write the keys and attend with the queries."""
+        if rotary.device != self.device:
+            raise ValueError(f"rotary: one on {self.device} is needed")
+        n, p, s = self._list(ids, starts)
+        rows, ref, a, b, handle = rotary._sides(q, k, out, stream)
+        if k is not None and k.size(1) != self._c.kv_heads:
+            raise ValueError(f"k: {self._c.kv_heads} heads")
+        if stream is not None:
+            self._used_on(stream, ids, starts)
+        self._on(stream)
+        r = self._rotate(self._ref, ref, n, p, s, rows, *a[:5], *b[1:5], handle)
+        if r:
+            _check(r, "cac_kv8_rotate")
+        return a[5], b[5]
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] becomes a copy of src[i] that shares its pages (cac_kv8_fork)."""

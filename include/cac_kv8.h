@@ -49,6 +49,7 @@
 #include <stdint.h>
 
 #include "cac.h"
+#include "cac_ops.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -159,6 +160,38 @@ int cac_kv8_attend(const cac_kv8* c, int layer, int n, const int32_t* ids, const
  * queries of each sequence, whatever max_new is) without. */
 size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, int heads, int att_left,
                                 int att_chunk, int sinks);
+
+/* cac_kv8_attend for sequences that begin with the same tokens: the sequences of a
+ * group whose tables name the same pages, as forks of one sequence do, and which
+ * all see their tokens, have these read once for all of their queries.  The result
+ * is cac_kv8_attend's but for rounding, whatever the tables hold: what is shared is
+ * found in the call, on the device, and what is not shared is read for each sequence.
+ *   groups  device int32 [n_groups + 1], 0 <= groups[0], never falling, <= n: the
+ *           sequences groups[g] .. groups[g+1]-1 of the call form a group, those
+ *           outside all of them share nothing.  NULL with n_groups 0: all form one.
+ *           Groups that break this latch CAC_E_BOUNDS, and nothing is shared.
+ *   out_stride, lse, max_new, workspace and the rest as there, with
+ *           cac_kv8_attend_shared_workspace bytes
+ * Tokens are shared in blocks of 16, up to the first page in which the tables of a
+ * group differ; a group of one sequence shares nothing. */
+int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
+                          int max_new, int n_groups, const int32_t* groups, int heads, float scale, int att_left,
+                          int att_chunk, int sinks, const void* q, long long q_stride, void* out, long long out_stride,
+                          float* lse, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+/* Enough for a call with these arguments, as cac_kv8_attend_workspace; never 0 for
+ * valid ones. */
+size_t cac_kv8_attend_shared_workspace(const cac_kv8* c, int n, int rows, int max_new, int n_groups, int heads,
+                                       int att_left, int att_chunk, int sinks);
+
+/* cac_op_rotate for the rows of a call on the cache: row j of a sequence with m
+ * rows is at position len - m + j (extend first, then rotate, write the keys and
+ * attend with the queries).  r->head_dim, r->device and the number of key heads are
+ * the cache's.  Rows of a sequence whose id is out of range or whose rows pass
+ * `rows` latch CAC_E_BOUNDS; they and rows that belong to no sequence are left as
+ * they were in the outputs. */
+int cac_kv8_rotate(const cac_kv8* c, const cac_rotary* r, int n, const int32_t* ids, const int32_t* starts, int rows,
+                   int heads, const void* q, long long q_stride, void* q_out, long long q_out_stride, const void* k,
+                   long long k_stride, void* k_out, long long k_out_stride, void* stream);
 
 /* Make sequence dst[i] a copy of src[i] (device int32 [n]) that shares its
  * pages; what dst[i] held is released.  A source may be forked several times.
