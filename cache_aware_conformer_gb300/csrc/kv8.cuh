@@ -167,6 +167,7 @@ struct DeviceScope {
     }
 };
 
+int sm_count(int device);                 // 0 where that cannot be told
 int kv_check_shape(const cac_kv8* c);     // CAC_OK or the error of a bad shape
 int kv_check_cache(const cac_kv8* c);     // shape and pointers
 

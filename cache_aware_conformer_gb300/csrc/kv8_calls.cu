@@ -5,7 +5,6 @@
 #include "kv8_attn.cuh"
 
 namespace cac {
-namespace {
 
 // SMs of a device, asked for once; 0 where that fails
 int sm_count(int device) {
@@ -16,6 +15,8 @@ int sm_count(int device) {
         known[device].store(sms, std::memory_order_relaxed);
     return sms;
 }
+
+namespace {
 
 // Whether units are cut and dealt out, or a warp takes a whole one: the latter saves the deal and the join, but takes about 0.45 us
 // a tile.  Measured (2 bf16 queries, windows of 220 / 450 / 900 tokens, us): 16 sequences of 8 heads 11 / 17 / 28 whole, 18 /

@@ -44,6 +44,10 @@ int cac_op_gemm_bf16(int M, int N, int K, const void* A, const void* B, const fl
 int cac_op_gemm_palette(int M, int N, int K, const void* A, const void* packed, const void* table,
                         const float* bias, float* C, int* status, void* stream);
 
+/* Bounds of cac_op_gemm_w4. */
+#define CAC_W4_MAX_K 131072
+#define CAC_W4_MAX_M 65535
+
 /* Weights at 4 bits with a scale for each group of consecutive k:
  *   W[n][k] = scale[n][k / group] * (code[n][k] - zero[n][k / group])
  * Code k of row n is the low half of byte k / 2 where k is even, the high half
@@ -57,8 +61,8 @@ typedef struct cac_w4 {
     const uint8_t* zero;   /* device [n][k / group], 0 .. 15; NULL: 8 everywhere */
 } cac_w4;
 
-/* C[M][n] = A[M][k] W^T (+ bias[n]), for the few rows of a decoding step (M >= 1;
- * the weights are read once for each 64 rows or fewer, and any M is computed).
+/* C[M][n] = A[M][k] W^T (+ bias[n]), for the few rows of a decoding step (the
+ * weights are read once for each 32 rows or fewer).
  *   A, C  device, both CAC_DTYPE_BF16 or both CAC_DTYPE_F32; a row every a_stride /
  *         c_stride elements (>= k / n); A 16-byte aligned with a_stride a multiple
  *         of 16 bytes, C aligned to its elements.  C may not overlap A.
@@ -68,7 +72,8 @@ typedef struct cac_w4 {
  * result does not depend on timing.  A row of A with an infinity or NaN gives
  * infinities or NaNs in its row of C and touches no other row.
  * Nothing is allocated; the call can be captured into a CUDA graph.
- * CAC_E_INVAL / CAC_E_ALIGN for arguments outside the above. */
+ * CAC_E_INVAL / CAC_E_ALIGN for arguments outside the above, CAC_E_LIMIT for k or M
+ * past their bounds. */
 int cac_op_gemm_w4(const cac_w4* w, int M, const void* A, long long a_stride, const float* bias, void* C,
                    long long c_stride, int dtype, void* stream);
 

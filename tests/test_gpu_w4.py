@@ -165,3 +165,10 @@ def test_binding_refuses_bad_tensors(native):
     with pytest.raises(native.CacError):
         run(a, packed, scale[:, :1].contiguous().expand(8, 1).contiguous().repeat(1, 8))    # groups of 16
     assert run(a[:0], packed, scale).shape == (0, 8)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M,K", [(1, 131072), (3, 131072), (9, 65536), (31, 40960)])
+def test_deep_rows(native, dtype, M, K):
+    """Depths that a cluster of blocks shares, with fewer rows at a time where they do not fit."""
+    check(native, *make(M, 40, K, 128, True, False, dtype))

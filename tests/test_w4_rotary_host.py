@@ -12,7 +12,7 @@ torch = pytest.importorskip("torch")
 from cache_aware_conformer_gb300 import w4  # noqa: E402
 from cache_aware_conformer_gb300.config import RotaryConfig  # noqa: E402
 
-INVAL, ALIGN = -1, -2
+INVAL, ALIGN, LIMIT = -1, -2, -10
 OK = 0x10000
 
 
@@ -72,7 +72,7 @@ def test_bad_weights_are_refused():
     ({"packed": None}, INVAL), ({"scale": None}, INVAL), ({"M": 0}, INVAL), ({"A": None}, INVAL), ({"C": None}, INVAL),
     ({"C": OK}, INVAL), ({"a_stride": 127}, INVAL), ({"c_stride": 9}, INVAL), ({"dtype": 2}, INVAL), ({"packed": OK + 8}, ALIGN),
     ({"scale": OK + 1}, ALIGN), ({"A": OK + 8}, ALIGN), ({"a_stride": 132}, ALIGN), ({"C": 2 * OK + 1}, ALIGN),
-    ({"bias": OK + 2}, ALIGN), ({"dtype": 0, "C": 2 * OK + 2}, ALIGN)])
+    ({"bias": OK + 2}, ALIGN), ({"dtype": 0, "C": 2 * OK + 2}, ALIGN), ({"k": 131072 + 64, "a_stride": 200000}, LIMIT), ({"M": 65536}, LIMIT)])
 def test_bad_products_are_refused(native, kw, code):
     a = {"n": 10, "k": 128, "group": 64, "device": 0, "packed": OK, "scale": OK, "zero": None, "M": 1, "A": OK, "a_stride": 128,
          "bias": None, "C": 2 * OK, "c_stride": 10, "dtype": 1, **kw}
