@@ -135,6 +135,9 @@ cudaError_t launch_gemm_tc(const CUtensorMap* tmA, const CUtensorMap* tmB, int M
 // stream, row_bytes = 3K/4 a multiple of 16), box 48 bytes x 64 rows.
 bool make_tmap_packed(CUtensorMap* tm, const void* base, uint64_t row_bytes, uint64_t rows);
 
+// Rows of bytes [rows][row_bytes] (base and row_bytes multiples of 16), box 128 bytes x box_rows, 128-byte swizzle.
+bool make_tmap_bytes(CUtensorMap* tm, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_rows);
+
 // Persistent tcgen05 GEMM for many output tiles (128 x 128 tiles, one CTA per
 // SM, two TMEM accumulators so epilogue and main loop overlap).  tmB128: the
 // weight map with 128-row boxes.  N % 128 == 0; other rules as launch_gemm_tc

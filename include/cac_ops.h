@@ -57,8 +57,8 @@ typedef struct cac_w4 {
     int32_t group;         /* 32, 64 or 128 */
     int32_t device;        /* CUDA device of every pointer of the call */
     const void* packed;    /* device bytes [n][k / 2], 16-byte aligned */
-    const void* scale;     /* device bf16 [n][k / group] */
-    const uint8_t* zero;   /* device [n][k / group], 0 .. 15; NULL: 8 everywhere */
+    const void* scale;     /* device bf16 [n][k / group], 4-byte aligned */
+    const uint8_t* zero;   /* device [n][k / group], 0 .. 15, 4-byte aligned; NULL: 8 everywhere */
 } cac_w4;
 
 /* C[M][n] = A[M][k] W^T (+ bias[n]), for the few rows of a decoding step (the
@@ -67,10 +67,12 @@ typedef struct cac_w4 {
  *         c_stride elements (>= k / n); A 16-byte aligned with a_stride a multiple
  *         of 16 bytes, C aligned to its elements.  C may not overlap A.
  *   bias  device fp32 [n] or NULL
- * A group's products are summed with the codes as they are (exact in the
- * operands' type) and scaled in fp32; sums are fp32, C is rounded once.  The
- * result does not depend on timing.  A row of A with an infinity or NaN gives
- * infinities or NaNs in its row of C and touches no other row.
+ * A group's products are summed with the codes less their zero points as they
+ * are and scaled in fp32; sums are fp32, C is rounded once.  An element of A is
+ * exact (bf16) or held to 22 bits (fp32), but for elements 2^29 and 2^17 times
+ * smaller than the largest among k of the same 256: those are off by up to 2^-39
+ * of it.  The result does not depend on timing.  A row of A with an infinity or
+ * NaN gives infinities or NaNs in its row of C and touches no other row.
  * Nothing is allocated; the call can be captured into a CUDA graph.
  * CAC_E_INVAL / CAC_E_ALIGN for arguments outside the above, CAC_E_LIMIT for k or M
  * past their bounds. */

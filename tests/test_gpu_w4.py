@@ -30,16 +30,16 @@ def make(M, N, K, group, zeros, bias, dtype, seed=0):
 def exact(a, packed, scale, zero, bias):
     """(result, bound of the kernel's arithmetic) in 64 bits.
 
-    Codes less zero points are exact.  A bf16 operand is exact; an fp32 one enters as parts that hold it to 2^-22 of
-    itself, or 2^-39 of the row's largest where it is far smaller.  Sums of a group's products (128 at most) on the tensor
-    cores lose 2^-23 of the partial sum a step at most (they cut off), the groups' sums are scaled and added in fp32, at
+    Codes less zero points are exact.  Activations enter as fp16 after a power of two that brings the largest of 256 of a row
+    to 2^14 or more: bf16 ones (8 bits) exactly and fp32 ones as two parts that hold 22 bits, but for those so small that
+    fp16's last step, 2^-24, counts: off by half of it, 2^-39 of the largest.  Sums of a group's products (128 at most) on the
+    tensor cores lose 2^-23 of the partial sum a step at most (they cut off), the groups' sums are scaled and added in fp32, at
     most K / 32 + 32 of them with the parts of a split, the bias once more."""
     w = w4.dequantize(packed, scale, zero)
     x = a.double()
     out, mass = x @ w.T, x.abs() @ w.abs().T
     tol = (2.0 ** -22 + (128 + a.size(1) / 32 + 32) * 2.0 ** -23) * mass
-    if a.dtype is F32:
-        tol = tol + 2.0 ** -39 * x.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    tol = tol + 2.0 ** -39 * x.abs().amax(1, keepdim=True) * w.abs().sum(1)
     if bias is not None:
         out = out + bias.double()
         tol = tol + 2.0 ** -24 * (out.abs() + bias.double().abs())

@@ -71,7 +71,7 @@ def test_bad_weights_are_refused():
     ({"n": 0}, INVAL), ({"k": 0}, INVAL), ({"k": 96}, INVAL), ({"group": 16}, INVAL), ({"group": 0}, INVAL), ({"device": -1}, INVAL),
     ({"packed": None}, INVAL), ({"scale": None}, INVAL), ({"M": 0}, INVAL), ({"A": None}, INVAL), ({"C": None}, INVAL),
     ({"C": OK}, INVAL), ({"a_stride": 127}, INVAL), ({"c_stride": 9}, INVAL), ({"dtype": 2}, INVAL), ({"packed": OK + 8}, ALIGN),
-    ({"scale": OK + 1}, ALIGN), ({"A": OK + 8}, ALIGN), ({"a_stride": 132}, ALIGN), ({"C": 2 * OK + 1}, ALIGN),
+    ({"scale": OK + 2}, ALIGN), ({"zero": OK + 1}, ALIGN), ({"A": OK + 8}, ALIGN), ({"a_stride": 132}, ALIGN), ({"C": 2 * OK + 1}, ALIGN),
     ({"bias": OK + 2}, ALIGN), ({"dtype": 0, "C": 2 * OK + 2}, ALIGN), ({"k": 131072 + 64, "a_stride": 200000}, LIMIT), ({"M": 65536}, LIMIT)])
 def test_bad_products_are_refused(native, kw, code):
     a = {"n": 10, "k": 128, "group": 64, "device": 0, "packed": OK, "scale": OK, "zero": None, "M": 1, "A": OK, "a_stride": 128,
