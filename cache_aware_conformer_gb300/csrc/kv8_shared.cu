@@ -11,8 +11,9 @@
 // first page in which the tables differ.  Nothing but the sequences' tables is compared, so a result never hangs on what
 // the caller believes of them.
 #include <algorithm>
+#include <atomic>
 
-#include "kv8_attn.cuh"
+#include "kv8_tc.cuh"
 
 namespace cac {
 namespace {
@@ -25,6 +26,7 @@ struct SharedCall {
     const int32_t* groups;     // [n_groups + 1], NULL: one group
     int n_groups;              // at least 1
     int2* skip;                // [n]
+    int32_t* group_of;         // [n] of those that share
     int4* shared;              // [n_groups]
     int32_t* group_rows;       // [n_groups + 1]
 };
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
     const int2 range = share ? make_int2(first_block, end_block) : make_int2(0, 0);
 
     const int step = PLAN_BLOCKS * PLAN_THREADS, me = rank * PLAN_THREADS + t;
-    for (int i = g0 + me; i < g1; i += step) p.skip[i] = range;
+    for (int i = g0 + me; i < g1; i += step) p.skip[i] = range, p.group_of[i] = g;
     if (g == 0) {  // sequences of no group
         const int before = fine ? group_at(0) : n, after = fine ? group_at(p.n_groups) : n;
         for (int i = me; i < before; i += step) p.skip[i] = make_int2(0, 0);
@@ -131,12 +133,513 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
     if (rank == 0 && t == 0) p.shared[g] = make_int4(share ? a.ids[s_leader] : 0, range.x, range.y, 0);
 }
 
+// ---------------------------------------------------------------------------
+// The shared tokens of groups with many query rows, on the 5th-generation tensor cores: the roles and the mathematics of
+// kv_prompt_kernel (kv8_prompt.cu), without masks, since every row sees every token.  A unit is 128 or 256 query rows of a group (row
+// = query * heads of a K/V head + head) and a K/V head; its 128-token tiles are cut into pieces, one to a block, so that all SMs have
+// the same number of tiles: few rows over a long prefix would leave most of them idle otherwise.  A unit that is cut leaves sums for
+// kv_join_shared_kernel.
+// ---------------------------------------------------------------------------
+struct PrefixCall {
+    KvAttend a;             // rows: the groups'; shared; part_o, part_ml: of units in one piece
+    float* slot_o;          // [block][rows of a block][head_dim] of units that are cut, and
+    float2* slot_ml;        // [block][rows of a block]
+    int2* cut;              // [n_groups] first block and pieces of each unit of a group
+    int most;               // blocks that units may be cut for
+};
+
+// Which piece is block b's
+struct Piece {
+    int id, head, row0, r0, rows;    // whose table; K/V head; the group's first row in the call; rows r0 .. r0 + rows - 1 of the group's
+    int block0, blocks;              // of 16 tokens
+    bool cut;
+    int halves;                      // of 64 tokens
+};
+struct PieceSpace {
+    int units[TA_SEQS], tiles[TA_SEQS];
+    Piece piece;
+};
+template <int ROWS> __device__ __forceinline__ void find_piece(const PrefixCall& p, PieceSpace& s) {
+    const KvAttend& a = p.a;
+    const int n = a.rows.n, kvh = a.c.kv_heads, lane = threadIdx.x & 31;
+    for (int g = threadIdx.x; g < n; g += blockDim.x) {
+        const int4 sh = a.shared[g];
+        const int rows = (a.rows.at(g + 1) - a.rows.at(g)) * a.group;
+        s.units[g] = sh.z > sh.y ? (rows + ROWS - 1) / ROWS * kvh : 0;
+        s.tiles[g] = (sh.z - sh.y + 7) / 8;
+    }
+    __syncthreads();
+    if (threadIdx.x >= 32) return;
+    // the least share of a block for which there are no more than `most` pieces; whole units where there are as many
+    int units = 0, longest = 0;
+    long long tiles = 0;
+    for (int g = lane; g < n; g += 32)
+        if (s.units[g]) units += s.units[g], longest = max(longest, s.tiles[g]), tiles += (long long)s.units[g] * s.tiles[g];
+    units = __reduce_add_sync(0xffffffffu, units), longest = __reduce_max_sync(0xffffffffu, longest);
+    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+    int share = units >= p.most ? longest : (int)min((long long)longest, max(2ll, (tiles + p.most - 1) / p.most));
+    while (share < longest) {
+        long long pieces = 0;
+        for (int g = lane; g < n; g += 32)
+            if (s.units[g]) pieces += (long long)s.units[g] * ((s.tiles[g] + share - 1) / share);
+        for (int d = 16; d; d >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, d);
+        if (pieces <= p.most) break;
+        share += share / 16 + 1;
+    }
+    long long before = 0;
+    if (lane == 0) s.piece.blocks = 0;
+    __syncwarp();
+    for (int g0 = 0; g0 < n; g0 += 32) {
+        const int g = g0 + lane, cuts = g < n && s.units[g] ? max((s.tiles[g] + share - 1) / max(share, 1), 1) : 0;
+        const long long mine = cuts ? (long long)s.units[g] * cuts : 0;
+        long long sum = mine;
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += u;
+        }
+        const long long first = before + sum - mine;
+        if (g < n && blockIdx.x == 0) p.cut[g] = make_int2((int)first, cuts);
+        if (cuts && blockIdx.x >= first && blockIdx.x < first + mine) {
+            const int in = (int)(blockIdx.x - first), unit = in / cuts, k = in - unit * cuts;
+            const int4 sh = a.shared[g];
+            const int t0 = (int)((long long)s.tiles[g] * k / cuts), t1 = (int)((long long)s.tiles[g] * (k + 1) / cuts);
+            Piece q;
+            q.id = sh.x, q.head = unit % kvh, q.row0 = a.rows.at(g), q.r0 = unit / kvh * ROWS;
+            q.rows = min(ROWS, (a.rows.at(g + 1) - q.row0) * a.group - q.r0);
+            q.block0 = sh.y + 8 * t0;
+            q.blocks = min(sh.y + 8 * t1, sh.z) - q.block0;
+            q.cut = cuts > 1;
+            q.halves = (q.blocks + 3) / 4;
+            s.piece = q;
+        }
+        before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+}
+
+template <class T, int CODE, int HDP>
+__global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(const __grid_constant__ PrefixCall p) {
+    using S = PShape<T, HDP>;
+    constexpr int ROWS = S::NM * PT_ROWS;
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset: shared memory to the compiler too
+    float* s_scale = reinterpret_cast<float*>(smem + S::OFF_SC);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR);
+    uint64_t *q_full = bar, *k_full = bar + 1, *k_empty = bar + 3, *v_full = bar + 5, *v_empty = bar + 7;
+    uint64_t *s_full = bar + 9, *p_full = bar + 13, *o_done = bar + 17;  // s_full, p_full, o_done: [row tile][place]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
+    const KvAttend& a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.head_dim;
+    PieceSpace* space = reinterpret_cast<PieceSpace*>(smem);    // before anything else is there
+    static_assert(sizeof(PieceSpace) <= S::OFF_SC, "");
+    pdl_wait();
+    find_piece<ROWS>(p, *space);
+    __syncthreads();
+    const Piece w = space->piece;
+    __syncthreads();
+    if (w.blocks == 0) {
+        pdl_trigger();
+        return;
+    }
+    const int R = w.r0 + w.rows, nm = w.rows > PT_ROWS ? 2 : 1;
+
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, nm * 4);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(k_full + k, 8);
+            mbar_init(v_full + k, 8);
+            mbar_init(k_empty + k, nm);
+            mbar_init(v_empty + k, nm);
+            mbar_init(s_full + k, 1);
+            mbar_init(s_full + 2 + k, 1);
+            mbar_init(p_full + k, 4);
+            mbar_init(p_full + 2 + k, 4);
+            mbar_init(o_done + k, 1);
+            mbar_init(o_done + 2 + k, 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == S::WARPS - 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();
+    const uint32_t tmem = *tmem_slot;
+    bool ok = true;
+
+    if (warp < S::SOFT) {
+        // -------------------------------------------------------------- softmax: a thread per row
+        const int x = warp >> 2, r = (warp & 3) * 32 + lane, row = w.r0 + x * PT_ROWS + r;
+        if (x < nm) {
+            const bool on = row < R;
+            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+            const uint32_t col_s = tmem + lanes + S::COL_S + x * 128, col_o = tmem + lanes + S::COL_O + x * HDP;
+            const uint32_t col_sum = tmem + lanes + S::COL_SUM + x * HDP;
+            // The warp's 32 rows of queries: largest value of a row under 2^15, then fp16 (hi, lo).  CPR lanes load a row, 16 bytes
+            // each (a thread per row would touch 32 lines of memory with every load).
+            float amax = 0.f;
+            {
+                constexpr int VEC = 16 / sizeof(T), CPR = HDP / VEC, RPI = 32 / CPR;
+                const int c = lane & (CPR - 1), first = x * PT_ROWS + (warp & 3) * 32;
+                uint8_t* dst0 = smem + x * S::PARTS * S::TILE + (c * VEC >> 6) * S::PANEL;
+                constexpr int GROUP = 8;  // loads on their way at once
+#pragma unroll 1
+                for (int it0 = 0; it0 < CPR; it0 += GROUP) {
+                    uint4 raw[GROUP];
+#pragma unroll
+                    for (int k = 0; k < GROUP; ++k) {
+                        const int row = w.r0 + first + (it0 + k) * RPI + lane / CPR, q = a.query_of(row);
+                        const T* src = static_cast<const T*>(a.q) + (w.row0 + (long long)q) * a.q_stride +
+                                       (long long)(w.head * a.group + row - q * a.group) * D + c * VEC;
+                        raw[k] = row < R && c * VEC < D ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int k = 0; k < GROUP; ++k) {
+                        const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+                        float y[VEC], mx = 0.f;
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) {
+                            if constexpr (S::WIDE) {
+                                y[b] = __uint_as_float(u[b]);
+                            } else {
+                                y[2 * b] = __uint_as_float(u[b] << 16);
+                                y[2 * b + 1] = __uint_as_float(u[b] & 0xffff0000u);
+                            }
+                        }
+#pragma unroll
+                        for (int b = 0; b < VEC; ++b) mx = fmaxf(mx, fabsf(y[b]));
+#pragma unroll
+                        for (int d = CPR / 2; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                        const float of_mine = __shfl_sync(0xffffffffu, mx, (lane & (RPI - 1)) * CPR);
+                        if (lane / RPI == it0 + k) amax = of_mine;
+                        const float up = lift_to_half(mx) * (a.scale < 0.f ? -1.f : 1.f);
+                        const int rr = (warp & 3) * 32 + (it0 + k) * RPI + lane / CPR;
+                        uint8_t* dst = dst0 + rr * 128 + (((c * VEC >> 3 & 7) ^ (rr & 7)) << 4);
+                        uint32_t hi[VEC / 2], lo[VEC / 2];
+#pragma unroll
+                        for (int b = 0; b < VEC / 2; ++b) {
+                            hi[b] = pack_half(y[2 * b] * up, y[2 * b + 1] * up);
+                            if constexpr (S::WIDE) lo[b] = pack_rest(y[2 * b] * up, y[2 * b + 1] * up, hi[b]);
+                        }
+                        if constexpr (S::WIDE) {
+                            *reinterpret_cast<uint2*>(dst + (c & 1) * 8) = make_uint2(hi[0], hi[1]);
+                            *reinterpret_cast<uint2*>(dst + S::TILE + (c & 1) * 8) = make_uint2(lo[0], lo[1]);
+                        } else {
+                            *reinterpret_cast<uint4*>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        }
+                    }
+                }
+            }
+            const float f = fabsf(a.scale) * LOG2E / lift_to_half(amax);  // a power of two: exact
+            fence_proxy_async_smem();
+            warp_arrive(q_full);
+
+            float m = -INFINITY, l = 0.f;
+            for (int h = 0; h < w.halves; ++h) {
+                const int j = h >> 1;
+                const uint32_t col = col_s + (h & 1) * PT_HALF;
+                const float4* sc = reinterpret_cast<const float4*>(s_scale + (j & 3) * 24 + (h & 1) * 4);
+                if (!warp_wait(s_full + 2 * x + (h & 1), j & 1)) { ok = false; break; }
+                tc_fence_after();
+                const float4 ks4 = sc[0], lv4 = sc[2], iv4 = sc[4];
+                // Above 0 even where the product underflows (a query of zeros over a block of zeros) or the call's scale is 0: unseen
+                // tokens score -inf before they are multiplied.  A score is under 2^31 there, so FLT_MIN times it is nothing.
+                const float ks[4] = {fmaxf(ks4.x * f, FLT_MIN), fmaxf(ks4.y * f, FLT_MIN), fmaxf(ks4.z * f, FLT_MIN),
+                                     fmaxf(ks4.w * f, FLT_MIN)},
+                            lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, iv[4] = {iv4.x, iv4.y, iv4.z, iv4.w};
+                float v[PT_HALF];
+                tmem_ld64(col, v);
+                float top = -INFINITY, mb[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) mb[b] = fmaxf(v[16 * b], v[16 * b + 1]);
+#pragma unroll
+                for (int k = 2; k < 16; k += 2)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) mb[b] = max3(mb[b], v[16 * b + k], v[16 * b + k + 1]);
+#pragma unroll
+                for (int b = 0; b < 4; ++b) top = fmaxf(top, fmaf(mb[b], ks[b], lv[b]));
+                const bool grown = top > m + S::SLACK || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, grown)) {
+                    const float d = grown ? m - top : 0.f, r = ex2(d);
+                    l = move_norm(l, d, r);
+                    m = grown ? top : m;
+                    __syncwarp();  // the tensor-memory instructions are for a converged warp
+                    if (h > 0) {
+                        if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }  // the sums so far are in
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < HDP; c += 16) {
+                            scale16(col_o + c, r);
+                            if (S::WIDE && h > S::FLUSH) scale16(col_sum + c, r);
+                        }
+                        if (S::WIDE) tmem_st_wait();  // the flush below loads these columns, and loads do not wait for stores
+                    }
+                }
+                if (S::WIDE && h > 0 && h % S::FLUSH == 0) {
+                    if (!warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < HDP; c += 16) {
+                        float o[16], sum[16] = {};
+                        uint32_t u[16];
+                        if (h > S::FLUSH) tmem_ld16(col_sum + c, sum);
+                        tmem_ld16(col_o + c, o);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] + sum[k]);
+                        tmem_st16(col_sum + c, u);
+                    }
+                }
+                const float base = m == -INFINITY ? -S::LIFT : m - S::LIFT;
+                // one kind of instruction at a time, none of which waits for another of its kind: a warp has little else to hide
+                // their latencies behind
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float off = lv[b] - base;
+#pragma unroll
+                    for (int k = 16 * b; k < 16 * b + 16; k += 2) {
+                        const float2 y = fma2(make_float2(v[k], v[k + 1]), make_float2(ks[b], ks[b]), make_float2(off, off));
+                        v[k] = y.x, v[k + 1] = y.y;
+                    }
+                }
+                if (fminf(fminf(lv[0], lv[1]), fminf(lv[2], lv[3])) < FAR) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        if (lv[b] < FAR && lv[b] != -INFINITY) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int k = 16 * b; k < 16 * b + 16; ++k) x += ex2(v[k] - lv[b]);
+                            l = fmaf(x, S::NORM, l);
+                        }
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int k = 32 * c; k < 32 * c + 32; ++k) v[k] = ex2(v[k]);
+                    uint32_t hi[16], lo[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        hi[k] = pack_half(v[32 * c + 2 * k], v[32 * c + 2 * k + 1]);
+                        if constexpr (S::WIDE) lo[k] = pack_rest(v[32 * c + 2 * k], v[32 * c + 2 * k + 1], hi[k]);
+                    }
+                    tmem_st16(col + c * 16, hi);
+                    if constexpr (S::WIDE) tmem_st16(col + 32 + c * 16, lo);
+#pragma unroll
+                    for (int b = 2 * c; b < 2 * c + 2; ++b) {
+                        float2 sum[4];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float2 y = make_float2(v[16 * b + 2 * k], v[16 * b + 2 * k + 1]);
+                            sum[k & 3] = k < 4 ? y : add2(sum[k & 3], y);
+                        }
+                        const float2 all = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                        l = fmaf((all.x + all.y) * S::NORM, iv[b], l);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(p_full + 2 * x + (h & 1));
+            }
+            for (int h = max(w.halves - 2, 0); h < w.halves; ++h)
+                if (ok && !warp_wait(o_done + 2 * x + (h & 1), h >> 1 & 1)) ok = false;
+            tc_fence_after();
+            if (ok) {
+                const int query = on ? a.query_of(row) : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
+                const long long at = w.cut ? (long long)blockIdx.x * ROWS + x * PT_ROWS + r : (w.row0 + (long long)query) * a.heads + qh;
+                float* dst = (w.cut ? p.slot_o : a.part_o) + at * D;
+#pragma unroll
+                for (int c = 0; c < HDP / 32; ++c) {
+                    float v[32];
+                    __syncwarp();  // rows past the last one stored nothing; the loads are for a converged warp
+                    tmem_ld32(col_o + c * 32, v);
+                    if (S::WIDE && w.halves > S::FLUSH) {
+                        float sum[32];
+                        tmem_ld32(col_sum + c * 32, sum);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] += sum[k];
+                    }
+                    if (!on) continue;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4)
+                        if (c * 32 + k < D)
+                            *reinterpret_cast<float4*>(dst + c * 32 + k) =
+                                make_float4(v[k] * S::NORM, v[k + 1] * S::NORM, v[k + 2] * S::NORM, v[k + 3] * S::NORM);
+                }
+                if (on) (w.cut ? p.slot_ml : a.part_ml)[at] = make_float2(m, l);
+            }
+        }
+    } else if (warp < S::SOFT + S::CONV) {
+        // -------------------------------------------------------------- converters
+        // piece n: 16 tokens (block n % 8) of tile n / 16, K where n / 8 is even, else V; warp cw takes every CONV-th
+        const int cw = warp - S::SOFT, pieces = (w.blocks + 7) / 8 * 16;
+        const int sub = lane >> 2, c4 = lane & 3;   // token % 8 and chunk % 4 of a lane's loads
+        constexpr int NL = HDP / 32;
+        // Lane l knows where the warp's l-th piece of the next 32 lies, and its scales (with K: the scores need both).
+        struct Spot {
+            long long at;      // -1: past the end, or no page
+            float ks, lv, iv;
+        };
+        auto look = [&](int n) {
+            Spot t{-1, 1.f, -INFINITY, 0.f};  // a block that is not there: any K scale will do, its weights are 2^-inf
+            const int block = (n >> 4) * 8 + (n & 7);
+            if (n < pieces && block < w.blocks) {
+                const int tok = (w.block0 + block) * KV_BLOCK;
+                const int page = a.c.table[(long long)w.id * a.c.max_pages + tok / a.c.page_tokens];
+                if (page >= 0) {
+                    const int in_page = tok % a.c.page_tokens;
+                    t.at = kv_head_at(a.c, a.layer, page, w.head) + (long long)in_page * D;
+                    if (!(n & 8)) {
+                        const long long sc = kv_scale_at(a.c, a.layer, page, w.head) + in_page / KV_BLOCK;
+                        t.ks = a.c.k_scale[sc];
+                        t.lv = log2f(a.c.v_scale[sc]);
+                        t.iv = t.lv < FAR ? 0.f : ex2(-t.lv);
+                    }
+                }
+            }
+            return t;
+        };
+        Spot here = look(cw + S::CONV * lane);
+        const int lane_at = sub * D + c4 * 16;
+        const uint8_t *k_lane = static_cast<const uint8_t*>(a.c.k) + lane_at, *v_lane = static_cast<const uint8_t*>(a.c.v) + lane_at;
+        auto load = [&](int n, long long at, uint4 (&raw)[NL]) {
+            const uint8_t* from = (n & 8 ? v_lane : k_lane) + at;
+            // rows sub and sub + 8, elements of each 64
+#pragma unroll
+            for (int y = 0; y < NL; ++y)
+                raw[y] = at >= 0 && ((y >> 1) * 4 + c4) * 16 < D ? *reinterpret_cast<const uint4*>(from + (y & 1) * 8 * D + (y >> 1) * 64)
+                                                                 : make_uint4(0, 0, 0, 0);
+        };
+        uint4 raw[2][NL];
+        load(cw, __shfl_sync(0xffffffffu, here.at, 0), raw[0]);
+        Spot then = here;
+        int q = 0;  // the piece's place among the 32
+        auto piece = [&](int n, uint4 (&cur)[NL], uint4 (&nxt)[NL]) {
+            const float ks = __shfl_sync(0xffffffffu, here.ks, q), lv = __shfl_sync(0xffffffffu, here.lv, q),
+                        iv = __shfl_sync(0xffffffffu, here.iv, q);
+            if (++q == 32) {
+                q = 0;
+                here = then;
+            }
+            if (q == 8) then = look(n + S::CONV * (25 + lane));  // the 32 after these: not before the first are on their way
+            load(n + S::CONV, __shfl_sync(0xffffffffu, here.at, q), nxt);
+            const int j = n >> 4, st = j & 1, block = n & 7;
+            const bool v = n & 8;
+            if (j >= 2 && !warp_wait((v ? v_empty : k_empty) + st, (j / 2 - 1) & 1)) return false;
+            uint8_t* to = smem + (v ? S::OFF_V : S::OFF_K) + st * S::TILE + (block * 16 + sub) * 128;
+#pragma unroll
+            for (int y = 0; y < NL; ++y) {
+                const uint32_t u[4] = {cur[y].x, cur[y].y, cur[y].z, cur[y].w};
+                uint32_t h[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) half4<CODE>(u[k], h[2 * k], h[2 * k + 1]);
+                uint8_t* dst = to + (y >> 1) * S::PANEL + (y & 1) * 1024;
+                *reinterpret_cast<uint4*>(dst + (((2 * c4) ^ sub) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(dst + (((2 * c4 + 1) ^ sub) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (!v) {
+                    float* sc = s_scale + (j & 3) * 24 + block;
+                    sc[0] = ks, sc[8] = lv, sc[16] = iv;
+                }
+                mbar_arrive((v ? v_full : k_full) + st);
+            }
+            return true;
+        };
+#pragma unroll 1
+        for (int n = cw; n < pieces; n += 2 * S::CONV) {
+            if (!piece(n, raw[0], raw[1])) { ok = false; break; }
+            if (n + S::CONV < pieces && !piece(n + S::CONV, raw[1], raw[0])) { ok = false; break; }
+        }
+    } else {
+        // -------------------------------------------------------------- MMA: a thread per row tile
+        const int x = warp - S::SOFT - S::CONV;
+        if (lane == 0 && x < nm) {
+            constexpr uint32_t qk = idesc_f16(128, PT_HALF, false), pv = idesc_f16(128, HDP, true);
+            auto scores = [&](int h) {
+                const uint64_t kd = sdesc_k_sw128(smem + S::OFF_K + (h >> 1 & 1) * S::TILE + (h & 1) * (PT_HALF * 128));
+#pragma unroll
+                for (int part = 0; part < S::PARTS; ++part) {
+                    const uint64_t qd = sdesc_k_sw128(smem + (x * S::PARTS + part) * S::TILE);
+#pragma unroll
+                    for (int k = 0; k < HDP / 16; ++k) {
+                        const uint32_t step = (k >> 2) * (S::PANEL >> 4) + 2 * (k & 3);
+                        mma_ss(tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF, qd + step, kd + step, qk, part > 0 || k > 0);
+                    }
+                }
+                tc_commit(s_full + 2 * x + (h & 1));
+                if (h & 1) tc_commit(k_empty + (h >> 1 & 1));
+            };
+            ok = mbar_wait(q_full, 0) && mbar_wait(k_full, 0);
+            if (ok) {
+                tc_fence_after();
+                scores(0);
+            }
+            for (int h = 0; ok && h < w.halves; ++h) {
+                const int st = h >> 1 & 1, next = h + 1;
+                if (next < w.halves) {
+                    // the next scores take the place of the weights before these: products into other accumulators need
+                    // not run in order
+                    if ((!(next & 1) && !mbar_wait(k_full + (next >> 1 & 1), next >> 2 & 1)) ||
+                        (h > 0 && !mbar_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    scores(next);
+                }
+                if ((!(h & 1) && !mbar_wait(v_full + st, h >> 2 & 1)) || !mbar_wait(p_full + 2 * x + (h & 1), h >> 1 & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t vd = sdesc_mn_sw128(smem + S::OFF_V + st * S::TILE + (h & 1) * (PT_HALF * 128), S::PANEL);
+#pragma unroll
+                for (int part = 0; part < S::PARTS; ++part)
+#pragma unroll
+                    for (int k = 0; k < PT_HALF / 16; ++k)
+                        mma_ts(tmem + S::COL_O + x * HDP, tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF + part * 32 + 8 * k,
+                               vd + k * (2048 >> 4), pv, h % S::FLUSH > 0 || part > 0 || k > 0);
+                tc_commit(o_done + 2 * x + (h & 1));
+                if (h & 1) tc_commit(v_empty + st);
+            }
+        }
+    }
+    if (!ok) latch_error(a.c.status, CAC_E_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == S::WARPS - 1) tmem_dealloc(tmem, 512);
+}
+
+template <class T, int CODE, int HDP> cudaError_t launch_prefix(const PrefixCall& p, unsigned blocks, cudaStream_t s) {
+    using S = PShape<T, HDP>;
+    const auto kernel = kv_prefix_kernel<T, CODE, HDP>;
+    static std::atomic<uint64_t> ready{0};
+    const uint64_t bit = 1ull << (p.a.c.device & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::SMEM, s, 1, p);
+}
+template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, unsigned blocks, cudaStream_t s) {
+    return p.a.c.head_dim <= 64 ? launch_prefix<T, CODE, 64>(p, blocks, s) : launch_prefix<T, CODE, 128>(p, blocks, s);
+}
+// rows of a block
+int prefix_rows(const cac_kv8& c, int dtype) { return dtype == CAC_DTYPE_F32 && c.head_dim > 64 ? PT_ROWS : 2 * PT_ROWS; }
+
 // A warp for each row and head: the parts of a group's shared tokens and of the sequence's own become the result.
 struct JoinCall {
     KvAttend a;
     const int2* skip;
-    const float *o0, *o1;      // own, shared: [rows][heads][head_dim]
+    const int32_t *group_of, *group_rows;
+    const float *o0, *o1;      // own; shared, of units in one piece: [rows][heads][head_dim]
     const float2 *ml0, *ml1;
+    const int2* cut;           // NULL: shared ones are all in one piece
+    const float* slot_o;       // the others' pieces
+    const float2* slot_ml;
+    int block_rows;            // rows of a unit
 };
 constexpr int JOIN_WARPS = 8;
 template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
@@ -152,30 +655,74 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
     const bool named = id >= 0 && id < a.c.max_seqs && r1 - r0 <= a.max_new;
     const int2 k = p.skip[i];
     const bool two = named && k.y > k.x;
+    int first = 0, pieces = two ? 1 : 0, in_group = 0;
+    if (two && p.cut) {
+        const int g = p.group_of[i];
+        const int2 c = p.cut[g];
+        first = c.x, pieces = c.y;
+        in_group = row - p.group_rows[g];
+    }
     for (int h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); h < a.heads; h += gridDim.y * JOIN_WARPS) {
         const long long at = (long long)row * a.heads + h;
-        const float2 x = named ? p.ml0[at] : make_float2(-INFINITY, 0.f), y = two ? p.ml1[at] : make_float2(-INFINITY, 0.f);
-        const float top = fmaxf(x.x, y.x), base = top == -INFINITY ? 0.f : top;
-        const float fx = ex2(x.x - base), fy = ex2(y.x - base);
-        const float l = move_norm(x.y, x.x - base, fx) + (two ? move_norm(y.y, y.x - base, fy) : 0.f);
+        // where the shared part k lies: row `at` of o1, or its row of the block that had it
+        long long slot = at;
+        if (pieces > 1) {
+            const int kvh = h / a.group, r = in_group * a.group + h - kvh * a.group, unit = r / p.block_rows * a.c.kv_heads + kvh;
+            slot = ((long long)first + (long long)unit * pieces) * p.block_rows + r % p.block_rows;
+        }
+        const float2* ml = pieces > 1 ? p.slot_ml : p.ml1;
+        const float* parts = pieces > 1 ? p.slot_o : p.o1;
+        const float2 x = named ? p.ml0[at] : make_float2(-INFINITY, 0.f);
+        float top = x.x;
+        for (int k0 = lane; k0 < pieces; k0 += 32) top = fmaxf(top, ml[slot + (long long)k0 * p.block_rows].x);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float base = top == -INFINITY ? 0.f : top, fx = ex2(x.x - base);
+        float l = lane == 0 ? move_norm(x.y, x.x - base, fx) : 0.f;
+        float4 o[2] = {};
+        const int e0 = lane * 4, e1 = 128 + lane * 4;
+        if (named && x.x != -INFINITY) {
+            if (e0 < D) o[0] = *reinterpret_cast<const float4*>(p.o0 + at * D + e0);
+            if (e1 < D) o[1] = *reinterpret_cast<const float4*>(p.o0 + at * D + e1);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) o[b].x *= fx, o[b].y *= fx, o[b].z *= fx, o[b].w *= fx;
+        }
+        for (int k0 = 0; k0 < pieces; k0 += 32) {
+            float f = 0.f;
+            if (k0 + lane < pieces) {
+                const float2 y = ml[slot + (long long)(k0 + lane) * p.block_rows];
+                f = ex2(y.x - base);
+                l += move_norm(y.y, y.x - base, f);
+            }
+            const int n = min(32, pieces - k0);
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const float w = __shfl_sync(0xffffffffu, f, j);
+                const float* src = parts + (slot + (long long)(k0 + j) * p.block_rows) * D;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int e = b ? e1 : e0;
+                    if (e < D) {
+                        const float4 q = *reinterpret_cast<const float4*>(src + e);
+                        o[b].x = fmaf(q.x, w, o[b].x), o[b].y = fmaf(q.y, w, o[b].y), o[b].z = fmaf(q.z, w, o[b].z), o[b].w = fmaf(q.w, w, o[b].w);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         const bool seen = l > 0.f || l != l;
         const float inv = seen ? 1.f / l : 0.f;
         T* dst = static_cast<T*>(a.out) + row * a.out_stride + (long long)h * D;
-        for (int e = lane * 4; e < D; e += 128) {
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (seen) {
-                o = *reinterpret_cast<const float4*>(p.o0 + at * D + e);
-                o.x *= fx, o.y *= fx, o.z *= fx, o.w *= fx;
-                if (two) {
-                    const float4 q = *reinterpret_cast<const float4*>(p.o1 + at * D + e);
-                    o.x = fmaf(q.x, fy, o.x), o.y = fmaf(q.y, fy, o.y), o.z = fmaf(q.z, fy, o.z), o.w = fmaf(q.w, fy, o.w);
-                }
-                o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-            }
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int e = b ? e1 : e0;
+            if (e >= D) continue;
+            const float4 y = seen ? make_float4(o[b].x * inv, o[b].y * inv, o[b].z * inv, o[b].w * inv) : make_float4(0.f, 0.f, 0.f, 0.f);
             if constexpr (sizeof(T) == 4) {
-                *reinterpret_cast<float4*>(dst + e) = o;
+                *reinterpret_cast<float4*>(dst + e) = y;
             } else {
-                const __nv_bfloat162 u = __floats2bfloat162_rn(o.x, o.y), v = __floats2bfloat162_rn(o.z, o.w);
+                const __nv_bfloat162 u = __floats2bfloat162_rn(y.x, y.y), v = __floats2bfloat162_rn(y.z, y.w);
                 *reinterpret_cast<uint2*>(dst + e) =
                     make_uint2(*reinterpret_cast<const uint32_t*>(&u), *reinterpret_cast<const uint32_t*>(&v));
             }
@@ -188,7 +735,7 @@ size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 // Where things lie in the workspace.
 struct Space {
-    size_t skip, shared, group_rows, split, ml0, ml1, o0, o1, bytes;
+    size_t skip, group_of, shared, group_rows, cut, split, ml0, ml1, o0, o1, slot_ml, slot_o, bytes;
 };
 Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms) {
     Space s;
@@ -198,13 +745,19 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
         at += up16(bytes);
         return was;
     };
-    const size_t units = (size_t)rows * heads;
-    s.skip = take((size_t)n * 8), s.shared = take((size_t)n_groups * 16), s.group_rows = take(((size_t)n_groups + 1) * 4);
+    const size_t units = (size_t)rows * heads, slots = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
+    s.skip = take((size_t)n * 8), s.group_of = take((size_t)n * 4), s.shared = take((size_t)n_groups * 16);
+    s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 8);
     s.split = take(kv_attend_bytes(c.head_dim, sms));
-    s.ml0 = take(units * 8), s.ml1 = take(units * 8);
-    s.o0 = take(units * c.head_dim * 4), s.o1 = take(units * c.head_dim * 4);
+    s.ml0 = take(units * 8), s.ml1 = take(units * 8), s.slot_ml = take(slots * 8);
+    s.o0 = take(units * c.head_dim * 4), s.o1 = take(units * c.head_dim * 4), s.slot_o = take(slots * c.head_dim * 4);
     s.bytes = at;
     return s;
+}
+
+// Whether kv_prefix_kernel reads the shared tokens, or kv_attend_kernel, 16 rows at a time.
+bool prefix_takes(const KvAttend& a, int n_groups) {
+    return a.c.head_dim <= 128 && (long long)a.rows.rows * a.group > 16ll * n_groups;
 }
 
 }  // namespace
@@ -215,23 +768,39 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     const int n = call.rows.n, rows = call.rows.rows;
     const Space at = space_of(c, n, rows, n_groups, call.heads, sms);
     uint8_t* base = static_cast<uint8_t*>(workspace);
-    const SharedCall plan{call, groups, n_groups, reinterpret_cast<int2*>(base + at.skip), reinterpret_cast<int4*>(base + at.shared),
-                          reinterpret_cast<int32_t*>(base + at.group_rows)};
+    auto place = [&](size_t x) { return static_cast<void*>(base + x); };
+    const SharedCall plan{call, groups, n_groups, static_cast<int2*>(place(at.skip)), static_cast<int32_t*>(place(at.group_of)),
+                          static_cast<int4*>(place(at.shared)), static_cast<int32_t*>(place(at.group_rows))};
     cudaError_t e = launch_k(kv_plan_shared_kernel, dim3(n_groups, 1, PLAN_BLOCKS), dim3(PLAN_THREADS), 0, s, PLAN_BLOCKS, plan);
     if (e != cudaSuccess) return e;
 
     auto part = [&](const KvAttend& a, bool cut) {
-        return c.code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, cut, sms, base + at.split, s)
-                                      : kv_launch_attend<CAC_KV8_E4M3>(a, dtype, cut, sms, base + at.split, s);
+        return c.code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, cut, sms, place(at.split), s)
+                                      : kv_launch_attend<CAC_KV8_E4M3>(a, dtype, cut, sms, place(at.split), s);
     };
+    const bool prefix = prefix_takes(call, n_groups);
     for (int g0 = 0; g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
         KvAttend a = call;
         a.rows = {plan.group_rows + g0, 0, std::min(n_groups - g0, TA_SEQS), rows};
         a.ids = nullptr;
         a.shared = plan.shared + g0;
         a.max_new = rows;
-        a.part_o = reinterpret_cast<float*>(base + at.o1), a.part_ml = reinterpret_cast<float2*>(base + at.ml1);
-        if ((e = part(a, true)) != cudaSuccess) return e;
+        a.part_o = static_cast<float*>(place(at.o1)), a.part_ml = static_cast<float2*>(place(at.ml1));
+        if (prefix) {
+            // Units may be cut where one launch has all groups: the slots are the blocks'.
+            const int block = prefix_rows(c, dtype);
+            const PrefixCall p{a, static_cast<float*>(place(at.slot_o)), static_cast<float2*>(place(at.slot_ml)),
+                               static_cast<int2*>(place(at.cut)) + g0, n_groups <= TA_SEQS ? sms : 0};
+            const long long units = ((long long)rows * call.group / block + a.rows.n) * c.kv_heads;
+            const unsigned blocks = (unsigned)std::max<long long>(units, sms);
+            if (c.code == CAC_KV8_INT8)
+                e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, blocks, s);
+            else
+                e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_E4M3>(p, blocks, s) : launch_prefix<float, CAC_KV8_E4M3>(p, blocks, s);
+        } else {
+            e = part(a, true);
+        }
+        if (e != cudaSuccess) return e;
     }
     for (int i0 = 0; i0 < n; i0 += TA_SEQS) {          // the others, of each sequence
         KvAttend a = call;
@@ -240,11 +809,21 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
         a.rows.base = call.rows.each * i0;
         a.ids = call.ids + i0;
         a.skip = plan.skip + i0;
-        a.part_o = reinterpret_cast<float*>(base + at.o0), a.part_ml = reinterpret_cast<float2*>(base + at.ml0);
+        a.part_o = static_cast<float*>(place(at.o0)), a.part_ml = static_cast<float2*>(place(at.ml0));
         if ((e = part(a, split)) != cudaSuccess) return e;
     }
-    const JoinCall join{call, plan.skip, reinterpret_cast<const float*>(base + at.o0), reinterpret_cast<const float*>(base + at.o1),
-                        reinterpret_cast<const float2*>(base + at.ml0), reinterpret_cast<const float2*>(base + at.ml1)};
+    const JoinCall join{call,
+                        plan.skip,
+                        plan.group_of,
+                        plan.group_rows,
+                        static_cast<const float*>(place(at.o0)),
+                        static_cast<const float*>(place(at.o1)),
+                        static_cast<const float2*>(place(at.ml0)),
+                        static_cast<const float2*>(place(at.ml1)),
+                        prefix ? static_cast<const int2*>(place(at.cut)) : nullptr,
+                        static_cast<const float*>(place(at.slot_o)),
+                        static_cast<const float2*>(place(at.slot_ml)),
+                        prefix_rows(c, dtype)};
     const dim3 grid(rows, std::min((call.heads + JOIN_WARPS - 1) / JOIN_WARPS, 8));
     return dtype == CAC_DTYPE_BF16 ? launch_k(kv_join_shared_kernel<bf16>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join)
                                    : launch_k(kv_join_shared_kernel<float>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join);
