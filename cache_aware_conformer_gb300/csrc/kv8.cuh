@@ -116,13 +116,7 @@ struct KvAttend {
     float scale;
     int layer, heads, group, max_new;
     uint32_t group_mul;  // 2^32 / group, rounded down, + 1 (0 for a group of 1)
-    // A prefix that sequences share (kv8_shared.cu).  skip: the blocks [x, y) of each sequence that another launch reads.  shared: this is
-    // that launch, over groups of sequences: who to read and which blocks [y, z), all of them seen by all rows; rows holds the groups' rows.
-    // part_o, part_ml: where results go that are to be joined: [rows][heads][head_dim] sums times the norm's factor, and their maxima and norms.
-    const int2* skip;
-    const int4* shared;
-    float* part_o;
-    float2* part_ml;
+    const int2* skip;    // blocks [x, y) of each sequence that are left out, or null (kv8_shared.cu)
     // row / group of a row below 2^32: the product is the quotient or one more
     __device__ __forceinline__ int query_of(int row) const {
         if (group_mul == 0) return row;

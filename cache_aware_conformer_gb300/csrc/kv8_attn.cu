@@ -161,7 +161,7 @@ __device__ __forceinline__ float load_query(const T* src, bool on, int t, int D,
 struct Seen {
     int lo_max, hi_min, lo_min, hi_max;
     __device__ __forceinline__ void set(const KvAttend& a, const SeqWork& s, int r0, int size) {
-        if (a.shared) {
+        if (s.whole) {
             hi_min = hi_max = s.len, lo_max = lo_min = s.lot * KV_BLOCK;
             return;
         }
@@ -218,12 +218,6 @@ __device__ __forceinline__ void put_run(const KvAttend& a, const SeqWork& s, int
         store_run<float, RUN>(cut->o + ((size_t)slot * 16 + row - r0) * HDP + e, y);
     } else if (e < a.c.head_dim) {
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
-        if (a.part_o) {
-#pragma unroll
-            for (int k = 0; k < RUN; ++k) y[k] *= NORM;
-            store_run<float, RUN>(a.part_o + ((s.row0 + (long long)query) * a.heads + qh) * a.c.head_dim + e, y);
-            return;
-        }
         const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
 #pragma unroll
         for (int k = 0; k < RUN; ++k) y[k] = y[k] * NORM * inv;  // NORM * inv may be too small a number
@@ -236,9 +230,6 @@ __device__ __forceinline__ void put_sums(const KvAttend& a, const SeqWork& s, in
     if (cut) {
         cut->ml[((size_t)slot * 16 + row - r0) * 2] = m;
         cut->ml[((size_t)slot * 16 + row - r0) * 2 + 1] = l;
-    } else if (a.part_o) {
-        const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
-        a.part_ml[(s.row0 + (long long)query) * a.heads + qh] = make_float2(m, l);
     } else if (a.lse) {
         const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
         a.lse[(s.row0 + (long long)query) * a.heads + qh] =
@@ -266,8 +257,7 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
             const bool on = r < s.m * a.group;
             const RowSeen see = row_seen(a, s, r);
             m[h] = -INFINITY, l[h] = 0.f;
-            low[h] = see.on ? see.low : 0;
-            high[h] = see.on ? see.high : 0;
+            low[h] = see.low, high[h] = see.high;
             uint32_t x[STEPS], y[STEPS], xl[LO], yl[LO];
             f[h] = a.scale * LOG2E / load_query<T, HDP>(static_cast<const T*>(a.q) + (s.row0 + (long long)query) * a.q_stride +
                                                             (long long)(head * a.group + r - query * a.group) * D,
@@ -484,8 +474,7 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
             const RowSeen see = row_seen(a, s, r0 + 2 * t + b);
             f[b] = a.scale * LOG2E / __shfl_sync(0xffffffffu, up, 4 * (2 * t + b));  // by a power of two: exact
             m[b] = -INFINITY, l[b] = 0.f;
-            low[b] = see.on ? see.low : 0;
-            high[b] = see.on ? see.high : 0;
+            low[b] = see.low, high[b] = see.high;
         }
 #pragma unroll
         for (int n = 0; n < MT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
@@ -635,7 +624,7 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
         }
         // only a sequence with more rows than max_new has rows 8 .. 15: they see nothing
         const int row = r0 + 8 + g;
-        if (row < s.m * a.group && !cut && !a.part_o) {
+        if (row < s.m * a.group && !cut) {
             const int D = a.c.head_dim, query = a.query_of(row), qh = head * a.group + row - query * a.group;
             T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D;
             for (int e = t; e < D; e += 4) dst[e] = from_f<T>(0.f);
@@ -749,14 +738,6 @@ __device__ __forceinline__ void join_rows(const KvAttend& a, const Partials& p, 
             } else {
                 const int row = r0 + at, query = a.query_of(row), qh = head * a.group + row - query * a.group, D = a.c.head_dim;
                 const bool seen = l[b] > 0.f || l[b] != l[b];
-                if (a.part_o) {
-                    const long long part = (s.row0 + (long long)query) * a.heads + qh;
-#pragma unroll
-                    for (int c = 0; c < PER; ++c)
-                        if (lane * PER + c < D) a.part_o[part * D + lane * PER + c] = o[b][c] * NORM;
-                    if (lane == 0) a.part_ml[part] = make_float2(top[b], l[b]);
-                    continue;
-                }
                 T* dst = static_cast<T*>(a.out) + (s.row0 + (long long)query) * a.out_stride + (long long)qh * D + lane * PER;
 #pragma unroll
                 for (int c = 0; c < PER; ++c)
@@ -790,7 +771,7 @@ template <class T, int HDP, bool LOW, bool SPLIT> struct Shape {
     static constexpr int BYTES = WARPS * STAGES * STAGE;
     static constexpr int BLOCKS = !SPLIT && HDP == 64 ? 4 : 1;  // of an SM
     static_assert(WARPS <= MOST_WARPS && MOST_WARPS <= 16, "the workspace has room for the parts of so many");
-    static_assert(BYTES + (SPLIT ? 24 * 1024 : 0) <= 227 * 1024, "shared memory");
+    static_assert(BYTES + (SPLIT ? 25 * 1024 : 0) <= 227 * 1024, "shared memory");
 };
 
 // SPLIT: tiles are dealt out over a grid of one block per SM.  Otherwise each warp takes one
@@ -1034,17 +1015,153 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
     for (int k = 0; k < JOIN_Y; ++k) o += s_o[k][d], l += s_l[k];
     const bool seen = l > 0.f || l != l;
     const int query = a.query_of(row), qh = head * a.group + row - query * a.group;
-    if (a.part_o) {
-        const long long at = (row0 + (long long)query) * a.heads + qh;
-        if (d < a.c.head_dim) a.part_o[at * a.c.head_dim + d] = o * NORM;
-        if (d == 0) a.part_ml[at] = make_float2(top, l);
-        return;
-    }
     if (d < a.c.head_dim)
         static_cast<T*>(a.out)[(row0 + (long long)query) * a.out_stride + (long long)qh * a.c.head_dim + d] =
             from_f<T>(seen ? o * NORM / l : 0.f);
     if (d == 0 && a.lse)
         a.lse[(row0 + (long long)query) * a.heads + qh] = seen ? (top + NORM_LOG2 + log2f(l)) * LN2 : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------
+// Pieces of units, a block each (kv8_shared.cu): the block's warps take even shares of a piece's tiles and join their sums in
+// shared memory.  Where units are many and short this has a quarter of kv_attend_kernel's latency: a block looks up one entry and not the
+// lengths of all sequences, and nothing goes through global memory twice.  Rows at most 8: tokens as the rows of operand A.
+// ---------------------------------------------------------------------------
+template <class T, int HDP> struct PieceShape {
+    static constexpr int STAGE = 2 * KV_BLOCK * HDP, STAGES = HDP == 256 ? 3 : 4;
+    static constexpr int RING = PIECE_WARPS * STAGES * STAGE, SUMS = PIECE_WARPS * 16 * (HDP + 2) * 4;
+    static constexpr int BYTES = RING > SUMS ? RING : SUMS, BLOCKS = piece_blocks(HDP);
+};
+template <class T, int CODE, int HDP, bool LOW>
+__device__ __forceinline__ void piece_sums(const KvAttend& a, const SeqWork& s, int head, int r0, int x0, int x1, uint8_t* ring,
+                                           const Partials& sums) {
+    using P = PieceShape<T, HDP>;
+    constexpr int STAGES = P::STAGES, STAGE = P::STAGE, CH = HDP / 16;
+    const int lane = threadIdx.x & 31, D = a.c.head_dim;
+    auto look = [&](int x) { return x < x1 ? tile_of<CODE>(a, s, x, head) : Tile{-1, 0.f, 0.f, 0.f, 0}; };
+    // Lane l knows tile base + l (now) and the 32 after those (next).
+    Tile now = look(x0 + lane), next = now;
+    int base = x0, into = 0;
+    auto fetch = [&](int x) {  // queue the copies of tile x; always one group
+        const int k = x - base;
+        const long long at = __shfl_sync(0xffffffffu, k < 32 ? now.at : next.at, k & 31);
+        if (x < x1 && at >= 0) {
+            const uint32_t dst = smem_u32(ring) + into * STAGE;
+            const uint8_t *ks = static_cast<const uint8_t*>(a.c.k) + at, *vs = static_cast<const uint8_t*>(a.c.v) + at;
+#pragma unroll
+            for (int e0 = 0; e0 < KV_BLOCK * CH; e0 += 32) {
+                const int e = e0 + lane, r = e / CH, c = e % CH;
+                if (c * 16 < D) {
+                    cp16(dst + tile_at<HDP>(r, c), ks + r * D + c * 16);
+                    cp16(dst + KV_BLOCK * HDP + tile_at<HDP>(r, c), vs + r * D + c * 16);
+                }
+            }
+        }
+        cp_commit();
+        into = into + 1 == STAGES ? 0 : into + 1;
+    };
+    if (D < HDP) {  // chunks past the head's width stay zero
+        for (int st = 0; st < STAGES; ++st)
+            for (int e = lane; e < 2 * KV_BLOCK * CH; e += 32) {
+                const int r = e / CH % KV_BLOCK, c = e % CH;
+                if (c * 16 >= D)
+                    *reinterpret_cast<uint4*>(ring + st * STAGE + e / (KV_BLOCK * CH) * (KV_BLOCK * HDP) + tile_at<HDP>(r, c)) =
+                        make_uint4(0, 0, 0, 0);
+            }
+        __syncwarp();
+    }
+#pragma unroll 1
+    for (int k = 0; k < STAGES; ++k) fetch(x0 + k);
+    std::conditional_t<LOW, RowsLow<T, CODE, HDP>, Rows<T, CODE, HDP>> r;
+    r.load(a, s, head, r0);
+    if (x1 - x0 > 32) next = look(x0 + 32 + lane);
+    int from = 0;
+    for (int x = x0; x < x1;) {
+        if (x - base >= 32) {
+            base += 32;
+            now = next;
+            next = look(base + 32 + lane);
+        }
+        cp_wait<STAGES - 2>();  // tiles x and x + 1 are there
+        __syncwarp();
+        const bool two = x + 1 < x1;
+        const int k0 = x - base, s1 = from + 1 == STAGES ? 0 : from + 1;
+        const Tile d[2] = {tile_from(now, k0), k0 < 31 ? tile_from(now, k0 + 1) : tile_from(next, 0)};
+        const uint8_t* const k[2] = {ring + from * STAGE, ring + s1 * STAGE};
+        const bool on[2] = {r.sees(d[0], a.win.sinks), two && r.sees(d[1], a.win.sinks)};
+        if (on[0] || on[1]) r.tiles(d, k, on, a.win.sinks);
+        __syncwarp();  // the stages are read before their next copies are queued
+        fetch(x + STAGES);
+        if (two) fetch(x + STAGES + 1);
+        x += 1 + two;
+        from = two ? (s1 + 1 == STAGES ? 0 : s1 + 1) : s1;
+    }
+    cp_wait<0>();
+    __syncthreads();   // all rings have been read: the sums take their place
+    r.emit(a, s, head, r0, &sums, threadIdx.x >> 5);
+}
+
+template <class T, int CODE, int HDP>
+__global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP>::BLOCKS))
+    kv_piece_kernel(const __grid_constant__ KvAttend a, const __grid_constant__ KvPieces p) {
+    using P = PieceShape<T, HDP>;
+    extern __shared__ __align__(128) uint8_t ring_all[];
+    pdl_trigger();
+    pdl_wait();
+    const int b = (int)blockIdx.x, warp = threadIdx.x >> 5, kvh = a.c.kv_heads, D = a.c.head_dim;
+    if (b >= *p.total) return;
+    const int i = warp_last_le(p.count, b, [&](int k) { return __ldg(p.first + k); });   // entries without pieces are before those with
+    const KvEntry e = p.entries[i];
+    const int in = b - e.first, unit = in / e.cuts, k = in - unit * e.cuts, head = unit % kvh, r0 = unit / kvh * 16;
+    const int t0 = (int)((long long)e.s.tiles * k / e.cuts), n = (int)((long long)e.s.tiles * (k + 1) / e.cuts) - t0;
+    const int x0 = t0 + n * warp / PIECE_WARPS, x1 = t0 + n * (warp + 1) / PIECE_WARPS;
+    const int rows = min(16, e.s.m * a.group - r0);
+    Partials sums;
+    sums.o = reinterpret_cast<float*>(ring_all);
+    sums.ml = sums.o + PIECE_WARPS * 16 * HDP;
+    uint8_t* ring = ring_all + warp * P::STAGES * P::STAGE;
+    if (rows <= 8) piece_sums<T, CODE, HDP, true>(a, e.s, head, r0, x0, x1, ring, sums);
+    else piece_sums<T, CODE, HDP, false>(a, e.s, head, r0, x0, x1, ring, sums);
+    __syncthreads();
+    // the warps' parts become the block's: 4 elements of a row to a thread
+    const float2* ml = reinterpret_cast<const float2*>(sums.ml);
+    for (int x = threadIdx.x; x < rows * (HDP / 4); x += PIECE_WARPS * 32) {
+        const int r = x / (HDP / 4), c = x % (HDP / 4) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < PIECE_WARPS; ++w) top = fmaxf(top, ml[w * 16 + r].x);
+        const float base = top == -INFINITY ? 0.f : top;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < PIECE_WARPS; ++w) {
+            const float2 y = ml[w * 16 + r];
+            const float f = ex2(y.x - base);
+            const float4 q = *reinterpret_cast<const float4*>(sums.o + (w * 16 + r) * HDP + c);
+            l += move_norm(y.y, y.x - base, f);
+            o.x = fmaf(q.x, f, o.x), o.y = fmaf(q.y, f, o.y), o.z = fmaf(q.z, f, o.z), o.w = fmaf(q.w, f, o.w);
+        }
+        const int row = r0 + r, query = a.query_of(row), qh = head * a.group + row - query * a.group;
+        long long at = (e.s.row0 + (long long)query) * a.heads + qh;
+        float* to = i < p.own ? p.o0 : p.o1;
+        float2* to_ml = i < p.own ? p.ml0 : p.ml1;
+        if (e.cuts > 1) at = (long long)(e.slot + in) * 16 + r, to = p.slot_o, to_ml = p.slot_ml;
+        if (c < D) *reinterpret_cast<float4*>(to + at * D + c) = make_float4(o.x * NORM, o.y * NORM, o.z * NORM, o.w * NORM);
+        if (c == 0) to_ml[at] = make_float2(top, l);
+    }
+}
+
+template <class T, int CODE, int HDP> cudaError_t launch_pieces(const KvAttend& a, const KvPieces& p, unsigned blocks, cudaStream_t s) {
+    using P = PieceShape<T, HDP>;
+    const auto kernel = kv_piece_kernel<T, CODE, HDP>;
+    static std::atomic<uint64_t> ready{0};
+    const uint64_t bit = 1ull << (a.c.device & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_k(kernel, dim3(blocks), dim3(PIECE_WARPS * 32), P::BYTES, s, 1, a, p);
 }
 
 template <class T, int CODE, int HDP, bool LOW>
@@ -1091,6 +1208,19 @@ cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int sms, 
                       : launch_attend<float, CODE, 256>(a, split, sms, space, s);
 }
 template cudaError_t kv_launch_attend<KV8_ATTN_CODE>(const KvAttend&, int, bool, int, void*, cudaStream_t);
+
+template <int CODE>
+cudaError_t kv_launch_pieces(const KvAttend& a, const KvPieces& p, int dtype, unsigned blocks, cudaStream_t s) {
+    const int d = a.c.head_dim;
+    if (dtype == CAC_DTYPE_BF16)
+        return d <= 64    ? launch_pieces<bf16, CODE, 64>(a, p, blocks, s)
+               : d <= 128 ? launch_pieces<bf16, CODE, 128>(a, p, blocks, s)
+                          : launch_pieces<bf16, CODE, 256>(a, p, blocks, s);
+    return d <= 64    ? launch_pieces<float, CODE, 64>(a, p, blocks, s)
+           : d <= 128 ? launch_pieces<float, CODE, 128>(a, p, blocks, s)
+                      : launch_pieces<float, CODE, 256>(a, p, blocks, s);
+}
+template cudaError_t kv_launch_pieces<KV8_ATTN_CODE>(const KvAttend&, const KvPieces&, int, unsigned, cudaStream_t);
 
 #if KV8_ATTN_CODE == 0
 size_t kv_attend_bytes(int head_dim, int sms) {

@@ -67,8 +67,9 @@ __device__ __forceinline__ float move_norm(float l, float d, float r) {
 // What a sequence of the call asks for.
 struct SeqWork {
     int id, len, m, row0;      // len 0: nothing is seen
-    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1)
+    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1, where none are left out)
     int gap0, gap;             // from block gap0 on, gap blocks are left out
+    bool whole;                // rows of several sequences that all see all of these blocks (kv8_shared.cu)
     __device__ __forceinline__ int block(int kt) const {
         if (kt < skt) return kt;
         const int b = lot + kt - skt;
@@ -79,14 +80,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
     SeqWork s;
     s.row0 = a.rows.at(i);
     s.m = a.rows.at(i + 1) - s.row0;
-    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1, s.gap0 = 0, s.gap = 0;
-    if (a.shared) {
-        const int4 g = a.shared[i];
-        s.id = g.x;
-        if (g.z > g.y) s.len = g.z * KV_BLOCK, s.lot = g.y, s.tiles = g.z - g.y;
-        else s.m = 0;
-        return s;
-    }
+    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1, s.gap0 = 0, s.gap = 0, s.whole = false;
     s.id = a.ids[i];
     const bool rows_ok = s.m >= 0 && s.row0 >= 0 && s.row0 + (long long)s.m <= a.rows.rows;
     if (!rows_ok) s.m = 0;
@@ -103,7 +97,7 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
         if (a.skip) {
             const int2 k = a.skip[i];
             s.gap0 = k.x, s.gap = k.y - k.x;
-            s.tiles = max(s.tiles - s.gap, 1);   // one that lies past the end where nothing else is left
+            s.tiles -= s.gap;
         }
     }
     return s;
@@ -115,7 +109,7 @@ struct RowSeen {
     int low, high;
 };
 __device__ __forceinline__ RowSeen row_seen(const KvAttend& a, const SeqWork& s, int row) {
-    if (a.shared) return {row < s.m * a.group, s.lot * KV_BLOCK, s.len};
+    if (s.whole) return {row < s.m * a.group, s.lot * KV_BLOCK, s.len};
     const int p = s.len - s.m + a.query_of(row);
     const bool on = row < s.m * a.group && p >= 0 && s.len > 0;
     return {on, on ? a.win.low(p) : 0, on ? a.win.high(p, s.len) : 0};
@@ -129,13 +123,34 @@ cudaError_t kv_launch_attend(const KvAttend& a, int dtype, bool split, int sms, 
 extern template cudaError_t kv_launch_attend<CAC_KV8_INT8>(const KvAttend&, int, bool, int, void*, cudaStream_t);
 extern template cudaError_t kv_launch_attend<CAC_KV8_E4M3>(const KvAttend&, int, bool, int, void*, cudaStream_t);
 size_t kv_attend_bytes(int head_dim, int sms);
+// Units of a call cut into pieces, a block each (kv8_shared.cu): an entry is a sequence or a group of them, its units are its K/V heads and
+// tiles of 16 query rows.
+struct KvEntry {
+    SeqWork s;
+    int cuts;              // pieces of each unit; 0: the entry has none
+    int first, slot;       // its first piece, and slot of its results where it is cut
+};
+struct KvPieces {
+    const KvEntry* entries;
+    const int32_t* first;  // [count] the entries' again
+    const int32_t* total;  // pieces in all
+    int count, own;        // entries; those from own on go to o1, ml1
+    float *o0, *o1, *slot_o;       // [rows][heads][head_dim]; [slot][16][head_dim]: sums times the norm's factor
+    float2 *ml0, *ml1, *slot_ml;   // their maxima and norms
+};
+constexpr int PIECE_WARPS = 4;
+// blocks of an SM that take pieces at once
+constexpr int piece_blocks(int head_dim) { return head_dim <= 128 ? 3 : 1; }
+template <int CODE>
+cudaError_t kv_launch_pieces(const KvAttend& a, const KvPieces& p, int dtype, unsigned blocks, cudaStream_t s);
+extern template cudaError_t kv_launch_pieces<CAC_KV8_INT8>(const KvAttend&, const KvPieces&, int, unsigned, cudaStream_t);
+extern template cudaError_t kv_launch_pieces<CAC_KV8_E4M3>(const KvAttend&, const KvPieces&, int, unsigned, cudaStream_t);
 // kv8_prompt.cu
 // whether it takes a call whose sequences have `rows` query rows to a K/V head on average
 bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows);
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s);
-// kv8_shared.cu: a.rows and a.ids are the whole call's; workspace of kv_shared_bytes; split as above, for what is not shared
-cudaError_t kv_attend_shared(const KvAttend& a, int dtype, const int32_t* groups, int n_groups, bool split, int sms, void* workspace,
-                             cudaStream_t s);
+// kv8_shared.cu: a.rows and a.ids are the whole call's; workspace of kv_shared_bytes
+cudaError_t kv_attend_shared(const KvAttend& a, int dtype, const int32_t* groups, int n_groups, int sms, void* workspace, cudaStream_t s);
 size_t kv_shared_bytes(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms);
 
 }  // namespace cac

@@ -120,7 +120,9 @@ extern "C" size_t cac_kv8_attend_shared_workspace(const cac_kv8* c, int n, int r
     (void)att_left;
     if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || n_groups < 0 || heads < 1 || att_chunk < 1 || sinks < 0)
         return 0;
-    return kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sm_count(c->device));
+    // attend's too: a call that it answers better goes to it
+    return std::max(kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sm_count(c->device)),
+                    kv_attend_bytes(c->head_dim, sm_count(c->device)));
 }
 
 extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
@@ -138,7 +140,7 @@ extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const i
     const int sms = sm_count(c->device);
     if (sms < 1) return CAC_E_CUDA;
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15) ||
-        workspace_bytes < kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sms))
+        workspace_bytes < cac_kv8_attend_shared_workspace(c, n, rows, most, n_groups, heads, att_left, att_chunk, sinks))
         return CAC_E_INVAL;
     if (((long long)rows * group / 16 + n) * c->kv_heads > INT32_MAX / 32 || n_groups > (1 << 28)) return CAC_E_LIMIT;
     const KvAttend a = part_of(*c, layer, n, 0, n, ids, starts, rows, most, heads, scale, {att_left, att_chunk, sinks}, q, q_stride,
@@ -149,8 +151,7 @@ extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const i
                               out_stride, lse, dtype, workspace, workspace_bytes, stream);
     DeviceScope dev(c->device);
     if (!dev.ok) return CAC_E_CUDA;
-    return kv_attend_shared(a, dtype, groups, std::max(n_groups, 1), splits(*c, n, sms, most, att_left, att_chunk, sinks), sms, workspace,
-                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+    return kv_attend_shared(a, dtype, groups, std::max(n_groups, 1), sms, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? CAC_OK
                : CAC_E_CUDA;
 }

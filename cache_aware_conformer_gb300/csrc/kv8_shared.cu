@@ -4,8 +4,9 @@
 // A softmax over a sequence's tokens is a join of softmaxes over any parts of them: with a part's maximum m, its sum
 // l of 2^(t - m) and its sum o of the weighted values, M = max m over the parts,
 //   out = sum o 2^(m - M) / sum l 2^(m - M).
-// So the tokens that all queries of a group see in the same pages are read once, by one launch whose rows are all queries of the
-// group; a second launch reads what each sequence has to itself, and a third joins the two.
+// So the tokens that all queries of a group see in the same pages are read once, with all queries of the group as rows: on the
+// tensor cores of the 5th generation where these are many, together with the other tokens where they are few.  What each sequence has
+// to itself is read for it, in pieces of even length, a block each; a last launch joins the parts.
 //
 // What is shared is looked up on the device in each call: blocks of 16 tokens that every query of the group sees whole, in front of the
 // first page in which the tables differ.  Nothing but the sequences' tables is compared, so a result never hangs on what
@@ -141,7 +142,10 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
 // kv_join_shared_kernel.
 // ---------------------------------------------------------------------------
 struct PrefixCall {
-    KvAttend a;             // rows: the groups'; shared; part_o, part_ml: of units in one piece
+    KvAttend a;             // rows: the groups'
+    const int4* shared;     // of each group: whose table, and the blocks [y, z)
+    float* part_o;          // units in one piece: [rows][heads][head_dim]
+    float2* part_ml;
     float* slot_o;          // [block][rows of a block][head_dim] of units that are cut, and
     float2* slot_ml;        // [block][rows of a block]
     int2* cut;              // [n_groups] first block and pieces of each unit of a group
@@ -163,7 +167,7 @@ template <int ROWS> __device__ __forceinline__ void find_piece(const PrefixCall&
     const KvAttend& a = p.a;
     const int n = a.rows.n, kvh = a.c.kv_heads, lane = threadIdx.x & 31;
     for (int g = threadIdx.x; g < n; g += blockDim.x) {
-        const int4 sh = a.shared[g];
+        const int4 sh = p.shared[g];
         const int rows = (a.rows.at(g + 1) - a.rows.at(g)) * a.group;
         s.units[g] = sh.z > sh.y ? (rows + ROWS - 1) / ROWS * kvh : 0;
         s.tiles[g] = (sh.z - sh.y + 7) / 8;
@@ -201,7 +205,7 @@ template <int ROWS> __device__ __forceinline__ void find_piece(const PrefixCall&
         if (g < n && blockIdx.x == 0) p.cut[g] = make_int2((int)first, cuts);
         if (cuts && blockIdx.x >= first && blockIdx.x < first + mine) {
             const int in = (int)(blockIdx.x - first), unit = in / cuts, k = in - unit * cuts;
-            const int4 sh = a.shared[g];
+            const int4 sh = p.shared[g];
             const int t0 = (int)((long long)s.tiles[g] * k / cuts), t1 = (int)((long long)s.tiles[g] * (k + 1) / cuts);
             Piece q;
             q.id = sh.x, q.head = unit % kvh, q.row0 = a.rows.at(g), q.r0 = unit / kvh * ROWS;
@@ -444,7 +448,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
             if (ok) {
                 const int query = on ? a.query_of(row) : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
                 const long long at = w.cut ? (long long)blockIdx.x * ROWS + x * PT_ROWS + r : (w.row0 + (long long)query) * a.heads + qh;
-                float* dst = (w.cut ? p.slot_o : a.part_o) + at * D;
+                float* dst = (w.cut ? p.slot_o : p.part_o) + at * D;
 #pragma unroll
                 for (int c = 0; c < HDP / 32; ++c) {
                     float v[32];
@@ -463,7 +467,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
                             *reinterpret_cast<float4*>(dst + c * 32 + k) =
                                 make_float4(v[k] * S::NORM, v[k + 1] * S::NORM, v[k + 2] * S::NORM, v[k + 3] * S::NORM);
                 }
-                if (on) (w.cut ? p.slot_ml : a.part_ml)[at] = make_float2(m, l);
+                if (on) (w.cut ? p.slot_ml : p.part_ml)[at] = make_float2(m, l);
             }
         }
     } else if (warp < S::SOFT + S::CONV) {
@@ -629,17 +633,96 @@ template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, unsi
 // rows of a block
 int prefix_rows(const cac_kv8& c, int dtype) { return dtype == CAC_DTYPE_F32 && c.head_dim > 64 ? PT_ROWS : 2 * PT_ROWS; }
 
+// ---------------------------------------------------------------------------
+// The other tokens, and the shared ones of groups with few rows: units cut into pieces of even length (kv_piece_kernel).  One block looks
+// up every sequence's work and deals it out.
+// ---------------------------------------------------------------------------
+struct DealCall {
+    KvAttend a;                // the whole call's, with skip
+    const int4* shared;
+    const int32_t* group_rows;
+    KvEntry* entries;          // [n + n_groups]
+    int32_t *first, *total;
+    int n_groups, most;        // groups whose shared tokens are dealt out too (0: another launch reads them); pieces to aim at
+};
+constexpr int DEAL_THREADS = 1024, LEAST_TILES = 8;
+__global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_constant__ DealCall p) {
+    __shared__ long long s_tiles[32];
+    __shared__ int s_pieces[32], s_slots[32];
+    pdl_trigger();
+    pdl_wait();
+    const KvAttend& a = p.a;
+    const int n = a.rows.n, count = n + p.n_groups, t = threadIdx.x, lane = t & 31, warp = t >> 5, kvh = a.c.kv_heads;
+    auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
+    long long tiles = 0;
+    for (int i = t; i < count; i += DEAL_THREADS) {
+        KvEntry e;
+        if (i < n) {
+            e.s = seq_work(a, i);
+        } else {
+            const int g = i - n;
+            const int4 sh = p.shared[g];
+            e.s = SeqWork{sh.x, sh.z * KV_BLOCK, p.group_rows[g + 1] - p.group_rows[g], p.group_rows[g], sh.y, 0, sh.z - sh.y, 0, 0, true};
+        }
+        tiles += (long long)units_of(e.s) * e.s.tiles;
+        p.entries[i].s = e.s;
+    }
+    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+    if (lane == 0) s_tiles[warp] = tiles;
+    __syncthreads();
+    tiles = s_tiles[lane];
+    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
+    // Pieces of `share` tiles: `most` of them and one more for each unit at the most, twice `most` of units that are cut.
+    const long long share = max((long long)LEAST_TILES, (tiles + p.most - 1) / p.most);
+    int pieces = 0, slots = 0;   // before this round's entries
+    for (int i0 = 0; i0 < count; i0 += DEAL_THREADS) {
+        const int i = i0 + t;
+        int units = 0, cuts = 0;
+        if (i < count) {
+            units = units_of(p.entries[i].s);
+            if (units) cuts = (int)((p.entries[i].s.tiles + share - 1) / share);
+        }
+        const int mine = units * cuts, held = cuts > 1 ? mine : 0;
+        int x = mine, y = held;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) x += u, y += v;
+        }
+        if (lane == 31) s_pieces[warp] = x, s_slots[warp] = y;
+        __syncthreads();
+        int all_x = 0, all_y = 0;
+        for (int w = 0; w < DEAL_THREADS / 32; ++w) {
+            if (w == warp) x += all_x, y += all_y;
+            all_x += s_pieces[w], all_y += s_slots[w];
+        }
+        if (i < count) {
+            p.entries[i].cuts = cuts, p.entries[i].first = pieces + x - mine, p.entries[i].slot = slots + y - held;
+            p.first[i] = pieces + x - mine;
+        }
+        pieces += all_x, slots += all_y;
+        __syncthreads();
+    }
+    if (t == 0) *p.total = pieces;
+}
+
 // A warp for each row and head: the parts of a group's shared tokens and of the sequence's own become the result.
 struct JoinCall {
     KvAttend a;
     const int2* skip;
     const int32_t *group_of, *group_rows;
-    const float *o0, *o1;      // own; shared, of units in one piece: [rows][heads][head_dim]
-    const float2 *ml0, *ml1;
-    const int2* cut;           // NULL: shared ones are all in one piece
-    const float* slot_o;       // the others' pieces
+    const KvEntry* entries;
+    KvPieces pieces;           // where the parts of entries are
+    const int2* cut;           // kv_prefix_kernel's cuts of the shared tokens, or null: they are entries
+    const float* slot_o;       // and its pieces
     const float2* slot_ml;
-    int block_rows;            // rows of a unit
+    int block_rows;            // rows of its units
+};
+// Parts of a row: `count` of them, `step` rows apart
+struct PartList {
+    const float* o;
+    const float2* ml;
+    long long at;
+    int step, count;
 };
 constexpr int JOIN_WARPS = 8;
 template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
@@ -653,58 +736,60 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
     if (row < r0 || row >= r1 || r0 < 0 || r1 > a.rows.rows) return;   // no sequence's, or of one whose rows pass the end
     const int id = a.ids[i];
     const bool named = id >= 0 && id < a.c.max_seqs && r1 - r0 <= a.max_new;
-    const int2 k = p.skip[i];
-    const bool two = named && k.y > k.x;
-    int first = 0, pieces = two ? 1 : 0, in_group = 0;
-    if (two && p.cut) {
-        const int g = p.group_of[i];
-        const int2 c = p.cut[g];
-        first = c.x, pieces = c.y;
-        in_group = row - p.group_rows[g];
+    const int2 skip = p.skip[i];
+    const int g = named && skip.y > skip.x ? p.group_of[i] : -1;
+    // (pieces of a unit, first slot) of the own and of the shared tokens
+    const int2 own = named ? make_int2(p.entries[i].cuts, p.entries[i].slot) : make_int2(0, 0);
+    int2 common = make_int2(0, 0);
+    if (g >= 0) {
+        if (p.cut) common = make_int2(p.cut[g].y, p.cut[g].x);
+        else common = make_int2(p.entries[a.rows.n + g].cuts, p.entries[a.rows.n + g].slot);
     }
+    const int in_group = g >= 0 ? row - p.group_rows[g] : 0;
     for (int h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); h < a.heads; h += gridDim.y * JOIN_WARPS) {
         const long long at = (long long)row * a.heads + h;
-        // where the shared part k lies: row `at` of o1, or its row of the block that had it
-        long long slot = at;
-        if (pieces > 1) {
-            const int kvh = h / a.group, r = in_group * a.group + h - kvh * a.group, unit = r / p.block_rows * a.c.kv_heads + kvh;
-            slot = ((long long)first + (long long)unit * pieces) * p.block_rows + r % p.block_rows;
-        }
-        const float2* ml = pieces > 1 ? p.slot_ml : p.ml1;
-        const float* parts = pieces > 1 ? p.slot_o : p.o1;
-        const float2 x = named ? p.ml0[at] : make_float2(-INFINITY, 0.f);
-        float top = x.x;
-        for (int k0 = lane; k0 < pieces; k0 += 32) top = fmaxf(top, ml[slot + (long long)k0 * p.block_rows].x);
+        const int kvh = h / a.group, hh = h - kvh * a.group;
+        auto list = [&](const int2& cuts, const float* o, const float2* ml, int r, int size, const float* slot_o, const float2* slot_ml) {
+            if (cuts.x <= 1) return PartList{o, ml, at, 0, cuts.x};
+            const int unit = r / size * a.c.kv_heads + kvh;
+            return PartList{slot_o, slot_ml, ((long long)cuts.y + (long long)unit * cuts.x) * size + r % size, size, cuts.x};
+        };
+        const PartList lists[2] = {
+            list(own, p.pieces.o0, p.pieces.ml0, (row - r0) * a.group + hh, 16, p.pieces.slot_o, p.pieces.slot_ml),
+            list(common, p.pieces.o1, p.pieces.ml1, in_group * a.group + hh, p.cut ? p.block_rows : 16, p.cut ? p.slot_o : p.pieces.slot_o,
+                 p.cut ? p.slot_ml : p.pieces.slot_ml)};
+        float top = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            for (int k = lane; k < lists[q].count; k += 32) top = fmaxf(top, lists[q].ml[lists[q].at + (long long)k * lists[q].step].x);
 #pragma unroll
         for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const float base = top == -INFINITY ? 0.f : top, fx = ex2(x.x - base);
-        float l = lane == 0 ? move_norm(x.y, x.x - base, fx) : 0.f;
-        float4 o[2] = {};
+        const float base = top == -INFINITY ? 0.f : top;
         const int e0 = lane * 4, e1 = 128 + lane * 4;
-        if (named && x.x != -INFINITY) {
-            if (e0 < D) o[0] = *reinterpret_cast<const float4*>(p.o0 + at * D + e0);
-            if (e1 < D) o[1] = *reinterpret_cast<const float4*>(p.o0 + at * D + e1);
+        float l = 0.f;
+        float4 o[2] = {};
 #pragma unroll
-            for (int b = 0; b < 2; ++b) o[b].x *= fx, o[b].y *= fx, o[b].z *= fx, o[b].w *= fx;
-        }
-        for (int k0 = 0; k0 < pieces; k0 += 32) {
-            float f = 0.f;
-            if (k0 + lane < pieces) {
-                const float2 y = ml[slot + (long long)(k0 + lane) * p.block_rows];
-                f = ex2(y.x - base);
-                l += move_norm(y.y, y.x - base, f);
-            }
-            const int n = min(32, pieces - k0);
+        for (int q = 0; q < 2; ++q) {
+            const PartList& x = lists[q];
+            for (int k0 = 0; k0 < x.count; k0 += 32) {
+                float f = 0.f;
+                if (k0 + lane < x.count) {
+                    const float2 y = x.ml[x.at + (long long)(k0 + lane) * x.step];
+                    f = ex2(y.x - base);
+                    l += move_norm(y.y, y.x - base, f);
+                }
+                const int n = min(32, x.count - k0);
 #pragma unroll 8
-            for (int j = 0; j < n; ++j) {
-                const float w = __shfl_sync(0xffffffffu, f, j);
-                const float* src = parts + (slot + (long long)(k0 + j) * p.block_rows) * D;
+                for (int j = 0; j < n; ++j) {
+                    const float w = __shfl_sync(0xffffffffu, f, j);
+                    const float* src = x.o + (x.at + (long long)(k0 + j) * x.step) * D;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int e = b ? e1 : e0;
-                    if (e < D) {
-                        const float4 q = *reinterpret_cast<const float4*>(src + e);
-                        o[b].x = fmaf(q.x, w, o[b].x), o[b].y = fmaf(q.y, w, o[b].y), o[b].z = fmaf(q.z, w, o[b].z), o[b].w = fmaf(q.w, w, o[b].w);
+                    for (int b = 0; b < 2; ++b) {
+                        const int e = b ? e1 : e0;
+                        if (e < D) {
+                            const float4 v = *reinterpret_cast<const float4*>(src + e);
+                            o[b].x = fmaf(v.x, w, o[b].x), o[b].y = fmaf(v.y, w, o[b].y), o[b].z = fmaf(v.z, w, o[b].z), o[b].w = fmaf(v.w, w, o[b].w);
+                        }
                     }
                 }
             }
@@ -735,7 +820,7 @@ size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 // Where things lie in the workspace.
 struct Space {
-    size_t skip, group_of, shared, group_rows, cut, split, ml0, ml1, o0, o1, slot_ml, slot_o, bytes;
+    size_t skip, group_of, shared, group_rows, cut, entries, first, total, ml0, ml1, slot_ml, prefix_ml, o0, o1, slot_o, prefix_o, bytes;
 };
 Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms) {
     Space s;
@@ -745,25 +830,26 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
         at += up16(bytes);
         return was;
     };
-    const size_t units = (size_t)rows * heads, slots = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
+    const size_t units = (size_t)rows * heads, D = c.head_dim;
+    const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim) * 16, prefix = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
     s.skip = take((size_t)n * 8), s.group_of = take((size_t)n * 4), s.shared = take((size_t)n_groups * 16);
     s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 8);
-    s.split = take(kv_attend_bytes(c.head_dim, sms));
-    s.ml0 = take(units * 8), s.ml1 = take(units * 8), s.slot_ml = take(slots * 8);
-    s.o0 = take(units * c.head_dim * 4), s.o1 = take(units * c.head_dim * 4), s.slot_o = take(slots * c.head_dim * 4);
+    s.entries = take(((size_t)n + n_groups) * sizeof(KvEntry)), s.first = take(((size_t)n + n_groups) * 4), s.total = take(4);
+    s.ml0 = take(units * 8), s.ml1 = take(units * 8), s.slot_ml = take(slots * 8), s.prefix_ml = take(prefix * 8);
+    s.o0 = take(units * D * 4), s.o1 = take(units * D * 4), s.slot_o = take(slots * D * 4), s.prefix_o = take(prefix * D * 4);
     s.bytes = at;
     return s;
 }
 
-// Whether kv_prefix_kernel reads the shared tokens, or kv_attend_kernel, 16 rows at a time.
+// Whether kv_prefix_kernel reads the shared tokens, 128 rows at a time, or kv_piece_kernel, 16.
 bool prefix_takes(const KvAttend& a, int n_groups) {
     return a.c.head_dim <= 128 && (long long)a.rows.rows * a.group > 16ll * n_groups;
 }
 
 }  // namespace
 
-cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* groups, int n_groups, bool split, int sms,
-                             void* workspace, cudaStream_t s) {
+cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* groups, int n_groups, int sms, void* workspace,
+                             cudaStream_t s) {
     const cac_kv8& c = call.c;
     const int n = call.rows.n, rows = call.rows.rows;
     const Space at = space_of(c, n, rows, n_groups, call.heads, sms);
@@ -774,56 +860,44 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     cudaError_t e = launch_k(kv_plan_shared_kernel, dim3(n_groups, 1, PLAN_BLOCKS), dim3(PLAN_THREADS), 0, s, PLAN_BLOCKS, plan);
     if (e != cudaSuccess) return e;
 
-    auto part = [&](const KvAttend& a, bool cut) {
-        return c.code == CAC_KV8_INT8 ? kv_launch_attend<CAC_KV8_INT8>(a, dtype, cut, sms, place(at.split), s)
-                                      : kv_launch_attend<CAC_KV8_E4M3>(a, dtype, cut, sms, place(at.split), s);
-    };
     const bool prefix = prefix_takes(call, n_groups);
-    for (int g0 = 0; g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
-        KvAttend a = call;
-        a.rows = {plan.group_rows + g0, 0, std::min(n_groups - g0, TA_SEQS), rows};
-        a.ids = nullptr;
-        a.shared = plan.shared + g0;
-        a.max_new = rows;
-        a.part_o = static_cast<float*>(place(at.o1)), a.part_ml = static_cast<float2*>(place(at.ml1));
-        if (prefix) {
-            // Units may be cut where one launch has all groups: the slots are the blocks'.
-            const int block = prefix_rows(c, dtype);
-            const PrefixCall p{a, static_cast<float*>(place(at.slot_o)), static_cast<float2*>(place(at.slot_ml)),
-                               static_cast<int2*>(place(at.cut)) + g0, n_groups <= TA_SEQS ? sms : 0};
-            const long long units = ((long long)rows * call.group / block + a.rows.n) * c.kv_heads;
-            const unsigned blocks = (unsigned)std::max<long long>(units, sms);
-            if (c.code == CAC_KV8_INT8)
-                e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, blocks, s);
-            else
-                e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_E4M3>(p, blocks, s) : launch_prefix<float, CAC_KV8_E4M3>(p, blocks, s);
-        } else {
-            e = part(a, true);
-        }
+    KvAttend a = call;
+    a.skip = plan.skip;
+    const int most = sms * piece_blocks(c.head_dim), dealt = prefix ? 0 : n_groups;
+    const DealCall deal{a,     plan.shared, plan.group_rows, static_cast<KvEntry*>(place(at.entries)), static_cast<int32_t*>(place(at.first)),
+                        static_cast<int32_t*>(place(at.total)), dealt, most};
+    e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
+    if (e != cudaSuccess) return e;
+
+    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n,
+                          static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
+                          static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
+    const int block = prefix_rows(c, dtype);
+    for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
+        KvAttend b = call;
+        b.rows = {plan.group_rows + g0, 0, std::min(n_groups - g0, TA_SEQS), rows};
+        b.ids = nullptr;
+        // Units may be cut where one launch has all groups: the slots are the blocks'.
+        const PrefixCall p{b, plan.shared + g0, pieces.o1, pieces.ml1, static_cast<float*>(place(at.prefix_o)),
+                           static_cast<float2*>(place(at.prefix_ml)), static_cast<int2*>(place(at.cut)) + g0, n_groups <= TA_SEQS ? sms : 0};
+        const long long units = ((long long)rows * call.group / block + b.rows.n) * c.kv_heads;
+        const unsigned blocks = (unsigned)std::max<long long>(units, sms);
+        if (c.code == CAC_KV8_INT8)
+            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, blocks, s);
+        else
+            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_E4M3>(p, blocks, s) : launch_prefix<float, CAC_KV8_E4M3>(p, blocks, s);
         if (e != cudaSuccess) return e;
     }
-    for (int i0 = 0; i0 < n; i0 += TA_SEQS) {          // the others, of each sequence
-        KvAttend a = call;
-        a.rows.starts = call.rows.starts ? call.rows.starts + i0 : nullptr;
-        a.rows.n = std::min(n - i0, TA_SEQS);
-        a.rows.base = call.rows.each * i0;
-        a.ids = call.ids + i0;
-        a.skip = plan.skip + i0;
-        a.part_o = static_cast<float*>(place(at.o0)), a.part_ml = static_cast<float2*>(place(at.ml0));
-        if ((e = part(a, split)) != cudaSuccess) return e;
-    }
-    const JoinCall join{call,
-                        plan.skip,
-                        plan.group_of,
-                        plan.group_rows,
-                        static_cast<const float*>(place(at.o0)),
-                        static_cast<const float*>(place(at.o1)),
-                        static_cast<const float2*>(place(at.ml0)),
-                        static_cast<const float2*>(place(at.ml1)),
-                        prefix ? static_cast<const int2*>(place(at.cut)) : nullptr,
-                        static_cast<const float*>(place(at.slot_o)),
-                        static_cast<const float2*>(place(at.slot_ml)),
-                        prefix_rows(c, dtype)};
+    // the others, of each sequence: as many blocks as there may be pieces
+    const long long units = ((long long)rows * call.group / 16 + n) * c.kv_heads + (prefix ? 0 : ((long long)rows * call.group / 16 + n_groups) * c.kv_heads);
+    const unsigned blocks = (unsigned)(units + most);
+    e = c.code == CAC_KV8_INT8 ? kv_launch_pieces<CAC_KV8_INT8>(a, pieces, dtype, blocks, s)
+                               : kv_launch_pieces<CAC_KV8_E4M3>(a, pieces, dtype, blocks, s);
+    if (e != cudaSuccess) return e;
+
+    const JoinCall join{call, plan.skip, plan.group_of, plan.group_rows, deal.entries, pieces,
+                        prefix ? static_cast<const int2*>(place(at.cut)) : nullptr, static_cast<const float*>(place(at.prefix_o)),
+                        static_cast<const float2*>(place(at.prefix_ml)), block};
     const dim3 grid(rows, std::min((call.heads + JOIN_WARPS - 1) / JOIN_WARPS, 8));
     return dtype == CAC_DTYPE_BF16 ? launch_k(kv_join_shared_kernel<bf16>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join)
                                    : launch_k(kv_join_shared_kernel<float>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join);
