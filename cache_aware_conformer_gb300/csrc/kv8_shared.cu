@@ -220,9 +220,29 @@ template <int ROWS> __device__ __forceinline__ void find_piece(const PrefixCall&
     }
 }
 
-template <class T, int CODE, int HDP>
-__global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(const __grid_constant__ PrefixCall p) {
-    using S = PShape<T, HDP>;
+// The prompts' kernel has its tokens from L2, where other blocks' loads have brought them; here they come from memory, and a load
+// into registers ahead of each piece left an SM with 12 KB on its way (a tile took 3.4 us; with three ahead, 3.8: the compiler waits for
+// all of them).  So the converters have their codes brought by bulk copies, a piece of 16 tokens each, `SLOTS` ahead.
+template <class T, int HDP, int TILES> struct XShape : PShape<T, HDP, TILES> {
+    using P = PShape<T, HDP, TILES>;
+    static constexpr int PIECE = KV_BLOCK * HDP, ROOM = (225 * 1024 - P::BYTES) / (P::CONV * (PIECE + 8));
+    static constexpr int SLOTS = ROOM < 6 ? ROOM : 6, OFF_RAW = (P::OFF_BAR + 21 * 8 + 16 + 127) / 128 * 128;
+    static constexpr int OFF_RAW_BAR = OFF_RAW + P::CONV * SLOTS * PIECE;
+    static constexpr int XBYTES = OFF_RAW_BAR + P::CONV * SLOTS * 8 + 1024;
+    static constexpr int XSMEM = XBYTES > 120 * 1024 ? XBYTES : 120 * 1024;  // one block an SM
+    static_assert(SLOTS >= 2 && XSMEM <= 227 * 1024, "shared memory");
+};
+
+// one thread of a converged warp, the same each time
+__device__ __forceinline__ bool elected() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
+
+template <class T, int CODE, int HDP, int TILES>
+__global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_kernel(const __grid_constant__ PrefixCall p) {
+    using S = XShape<T, HDP, TILES>;
     constexpr int ROWS = S::NM * PT_ROWS;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + (-smem_u32(smem_raw) & 1023u);   // an offset: shared memory to the compiler too
@@ -232,7 +252,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
     uint64_t *s_full = bar + 9, *p_full = bar + 13, *o_done = bar + 17;  // s_full, p_full, o_done: [row tile][place]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
     const KvAttend& a = p.a;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.c.head_dim;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, D = a.c.head_dim;
     PieceSpace* space = reinterpret_cast<PieceSpace*>(smem);    // before anything else is there
     static_assert(sizeof(PieceSpace) <= S::OFF_SC, "");
     pdl_wait();
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
         pdl_trigger();
         return;
     }
-    const int R = w.r0 + w.rows, nm = w.rows > PT_ROWS ? 2 : 1;
+    const int R = w.r0 + w.rows, nm = __shfl_sync(0xffffffffu, w.rows > PT_ROWS ? 2 : 1, 0), halves = __shfl_sync(0xffffffffu, w.halves, 0);
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, nm * 4);
@@ -267,7 +287,7 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
     __syncthreads();
     tc_fence_after();
     pdl_trigger();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     bool ok = true;
 
     if (warp < S::SOFT) {
@@ -501,29 +521,50 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
             return t;
         };
         Spot here = look(cw + S::CONV * lane);
-        const int lane_at = sub * D + c4 * 16;
-        const uint8_t *k_lane = static_cast<const uint8_t*>(a.c.k) + lane_at, *v_lane = static_cast<const uint8_t*>(a.c.v) + lane_at;
-        auto load = [&](int n, long long at, uint4 (&raw)[NL]) {
-            const uint8_t* from = (n & 8 ? v_lane : k_lane) + at;
-            // rows sub and sub + 8, elements of each 64
-#pragma unroll
-            for (int y = 0; y < NL; ++y)
-                raw[y] = at >= 0 && ((y >> 1) * 4 + c4) * 16 < D ? *reinterpret_cast<const uint4*>(from + (y & 1) * 8 * D + (y >> 1) * 64)
-                                                                 : make_uint4(0, 0, 0, 0);
+        uint8_t* slots = smem + S::OFF_RAW + cw * S::SLOTS * S::PIECE;
+        uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + S::OFF_RAW_BAR) + cw * S::SLOTS;
+        if (lane == 0)
+            for (int k = 0; k < S::SLOTS; ++k) mbar_init(raw_full + k, 1);
+        fence_mbar_init();
+        __syncwarp();
+        auto copy = [&](int n, int slot, long long at) {   // lane 0
+            if (n >= pieces) return;
+            if (at < 0) {
+                mbar_arrive(raw_full + slot);
+                return;
+            }
+            mbar_expect_tx(raw_full + slot, KV_BLOCK * D);
+            bulk_g2s(slots + slot * S::PIECE, static_cast<const uint8_t*>(n & 8 ? a.c.v : a.c.k) + at, KV_BLOCK * D, raw_full + slot);
         };
-        uint4 raw[2][NL];
-        load(cw, __shfl_sync(0xffffffffu, here.at, 0), raw[0]);
+#pragma unroll
+        for (int d = 0; d < S::SLOTS; ++d) {
+            const long long at = __shfl_sync(0xffffffffu, here.at, d);
+            if (lane == 0) copy(cw + S::CONV * d, d, at);
+        }
         Spot then = here;
-        int q = 0;  // the piece's place among the 32
-        auto piece = [&](int n, uint4 (&cur)[NL], uint4 (&nxt)[NL]) {
+        int q = 0, slot = 0, phase = 0;  // the piece's place among the 32; its slot
+        auto piece = [&](int n) {
             const float ks = __shfl_sync(0xffffffffu, here.ks, q), lv = __shfl_sync(0xffffffffu, here.lv, q),
                         iv = __shfl_sync(0xffffffffu, here.iv, q);
+            const bool there = __shfl_sync(0xffffffffu, here.at, q) >= 0;
+            if (q == 8) then = look(n + S::CONV * (24 + lane));  // the 32 after these: not before the first are on their way
+            const int ahead = q + S::SLOTS;
+            const long long ahead_at = __shfl_sync(0xffffffffu, ahead < 32 ? here.at : then.at, ahead & 31);
             if (++q == 32) {
                 q = 0;
                 here = then;
             }
-            if (q == 8) then = look(n + S::CONV * (25 + lane));  // the 32 after these: not before the first are on their way
-            load(n + S::CONV, __shfl_sync(0xffffffffu, here.at, q), nxt);
+            if (!warp_wait(raw_full + slot, phase)) return false;
+            uint4 cur[NL];
+            // rows sub and sub + 8, elements of each 64
+#pragma unroll
+            for (int y = 0; y < NL; ++y)
+                cur[y] = there && ((y >> 1) * 4 + c4) * 16 < D
+                             ? *reinterpret_cast<const uint4*>(slots + slot * S::PIECE + (sub + (y & 1) * 8) * D + c4 * 16 + (y >> 1) * 64)
+                             : make_uint4(0, 0, 0, 0);
+            __syncwarp();
+            if (lane == 0) copy(n + S::CONV * S::SLOTS, slot, ahead_at);
+            if (++slot == S::SLOTS) slot = 0, phase ^= 1;
             const int j = n >> 4, st = j & 1, block = n & 7;
             const bool v = n & 8;
             if (j >= 2 && !warp_wait((v ? v_empty : k_empty) + st, (j / 2 - 1) & 1)) return false;
@@ -549,62 +590,77 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
             }
             return true;
         };
+        int n = cw;
 #pragma unroll 1
-        for (int n = cw; n < pieces; n += 2 * S::CONV) {
-            if (!piece(n, raw[0], raw[1])) { ok = false; break; }
-            if (n + S::CONV < pieces && !piece(n + S::CONV, raw[1], raw[0])) { ok = false; break; }
-        }
+        for (; n < pieces; n += S::CONV)
+            if (!piece(n)) {
+                ok = false;
+                break;
+            }
+        // after a wait that gave up: copies in flight land before the block's memory is another's
+        for (int k = 0; !ok && k < S::SLOTS; ++k)
+            if (!mbar_wait(raw_full + k, k < slot ? phase ^ 1 : phase)) break;
     } else {
-        // -------------------------------------------------------------- MMA: a thread per row tile
+        // -------------------------------------------------------------- MMA: a warp per row tile, which an elected thread issues for.
+        // The whole warp goes round, and what the operands' addresses are made of is the same in all of its threads to the compiler too
+        // (the index and the counts by a broadcast): they stay in uniform registers.  From one thread's own registers each
+        // instruction took 160 clocks to issue, which was most of a tile's time.
         const int x = warp - S::SOFT - S::CONV;
-        if (lane == 0 && x < nm) {
+        if (x < nm) {
             constexpr uint32_t qk = idesc_f16(128, PT_HALF, false), pv = idesc_f16(128, HDP, true);
+            const uint64_t q0 = sdesc_k_sw128(smem + x * S::PARTS * S::TILE), k0 = sdesc_k_sw128(smem + S::OFF_K),
+                           v0 = sdesc_mn_sw128(smem + S::OFF_V, S::PANEL);
+            const uint32_t s0 = tmem + S::COL_S + x * 128, o0 = tmem + S::COL_O + x * HDP;
             auto scores = [&](int h) {
-                const uint64_t kd = sdesc_k_sw128(smem + S::OFF_K + (h >> 1 & 1) * S::TILE + (h & 1) * (PT_HALF * 128));
+                if (elected()) {
+                    const uint64_t kd = k0 + (((h >> 1 & 1) * S::TILE + (h & 1) * (PT_HALF * 128)) >> 4);
 #pragma unroll
-                for (int part = 0; part < S::PARTS; ++part) {
-                    const uint64_t qd = sdesc_k_sw128(smem + (x * S::PARTS + part) * S::TILE);
+                    for (int part = 0; part < S::PARTS; ++part)
 #pragma unroll
-                    for (int k = 0; k < HDP / 16; ++k) {
-                        const uint32_t step = (k >> 2) * (S::PANEL >> 4) + 2 * (k & 3);
-                        mma_ss(tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF, qd + step, kd + step, qk, part > 0 || k > 0);
-                    }
+                        for (int k = 0; k < HDP / 16; ++k) {
+                            const uint32_t step = (k >> 2) * (S::PANEL >> 4) + 2 * (k & 3);
+                            mma_ss(s0 + (h & 1) * PT_HALF, q0 + part * (S::TILE >> 4) + step, kd + step, qk, part > 0 || k > 0);
+                        }
+                    tc_commit(s_full + 2 * x + (h & 1));
+                    if (h & 1) tc_commit(k_empty + (h >> 1 & 1));
                 }
-                tc_commit(s_full + 2 * x + (h & 1));
-                if (h & 1) tc_commit(k_empty + (h >> 1 & 1));
+                __syncwarp();
             };
-            ok = mbar_wait(q_full, 0) && mbar_wait(k_full, 0);
+            ok = warp_wait(q_full, 0) && warp_wait(k_full, 0);
             if (ok) {
                 tc_fence_after();
                 scores(0);
             }
-            for (int h = 0; ok && h < w.halves; ++h) {
+            for (int h = 0; ok && h < halves; ++h) {
                 const int st = h >> 1 & 1, next = h + 1;
-                if (next < w.halves) {
+                if (next < halves) {
                     // the next scores take the place of the weights before these: products into other accumulators need
                     // not run in order
-                    if ((!(next & 1) && !mbar_wait(k_full + (next >> 1 & 1), next >> 2 & 1)) ||
-                        (h > 0 && !mbar_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1))) {
+                    if ((!(next & 1) && !warp_wait(k_full + (next >> 1 & 1), next >> 2 & 1)) ||
+                        (h > 0 && !warp_wait(o_done + 2 * x + ((h - 1) & 1), (h - 1) >> 1 & 1))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     scores(next);
                 }
-                if ((!(h & 1) && !mbar_wait(v_full + st, h >> 2 & 1)) || !mbar_wait(p_full + 2 * x + (h & 1), h >> 1 & 1)) {
+                if ((!(h & 1) && !warp_wait(v_full + st, h >> 2 & 1)) || !warp_wait(p_full + 2 * x + (h & 1), h >> 1 & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint64_t vd = sdesc_mn_sw128(smem + S::OFF_V + st * S::TILE + (h & 1) * (PT_HALF * 128), S::PANEL);
+                if (elected()) {
+                    const uint64_t vd = v0 + ((st * S::TILE + (h & 1) * (PT_HALF * 128)) >> 4);
 #pragma unroll
-                for (int part = 0; part < S::PARTS; ++part)
+                    for (int part = 0; part < S::PARTS; ++part)
 #pragma unroll
-                    for (int k = 0; k < PT_HALF / 16; ++k)
-                        mma_ts(tmem + S::COL_O + x * HDP, tmem + S::COL_S + x * 128 + (h & 1) * PT_HALF + part * 32 + 8 * k,
-                               vd + k * (2048 >> 4), pv, h % S::FLUSH > 0 || part > 0 || k > 0);
-                tc_commit(o_done + 2 * x + (h & 1));
-                if (h & 1) tc_commit(v_empty + st);
+                        for (int k = 0; k < PT_HALF / 16; ++k)
+                            mma_ts(o0, s0 + (h & 1) * PT_HALF + part * 32 + 8 * k, vd + k * (2048 >> 4), pv,
+                                   h % S::FLUSH > 0 || part > 0 || k > 0);
+                    tc_commit(o_done + 2 * x + (h & 1));
+                    if (h & 1) tc_commit(v_empty + st);
+                }
+                __syncwarp();
             }
         }
     }
@@ -615,23 +671,28 @@ __global__ void __launch_bounds__(PShape<T, HDP>::THREADS, 1) kv_prefix_kernel(c
     if (warp == S::WARPS - 1) tmem_dealloc(tmem, 512);
 }
 
-template <class T, int CODE, int HDP> cudaError_t launch_prefix(const PrefixCall& p, unsigned blocks, cudaStream_t s) {
-    using S = PShape<T, HDP>;
-    const auto kernel = kv_prefix_kernel<T, CODE, HDP>;
+template <class T, int CODE, int HDP, int TILES> cudaError_t launch_prefix(const PrefixCall& p, unsigned blocks, cudaStream_t s) {
+    using S = XShape<T, HDP, TILES>;
+    const auto kernel = kv_prefix_kernel<T, CODE, HDP, TILES>;
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = 1ull << (p.a.c.device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::XSMEM);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::SMEM, s, 1, p);
+    return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::XSMEM, s, 1, p);
 }
-template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, unsigned blocks, cudaStream_t s) {
-    return p.a.c.head_dim <= 64 ? launch_prefix<T, CODE, 64>(p, blocks, s) : launch_prefix<T, CODE, 128>(p, blocks, s);
+// Row tiles of a block: one for groups of 128 rows and fewer on average, which leaves room for more copies ahead.
+int prefix_tiles(const KvAttend& a, int dtype, int n_groups) {
+    return (dtype == CAC_DTYPE_F32 && a.c.head_dim > 64) || (long long)a.rows.rows * a.group <= (long long)PT_ROWS * n_groups ? 1 : 2;
 }
-// rows of a block
-int prefix_rows(const cac_kv8& c, int dtype) { return dtype == CAC_DTYPE_F32 && c.head_dim > 64 ? PT_ROWS : 2 * PT_ROWS; }
+template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, int tiles, unsigned blocks, cudaStream_t s) {
+    if (p.a.c.head_dim <= 64) return tiles == 1 ? launch_prefix<T, CODE, 64, 1>(p, blocks, s) : launch_prefix<T, CODE, 64, 2>(p, blocks, s);
+    if constexpr (sizeof(T) == 2)
+        if (tiles == 2) return launch_prefix<T, CODE, 128, 2>(p, blocks, s);
+    return launch_prefix<T, CODE, 128, 1>(p, blocks, s);
+}
 
 // ---------------------------------------------------------------------------
 // The other tokens, and the shared ones of groups with few rows: units cut into pieces of even length (kv_piece_kernel).  One block looks
@@ -705,7 +766,8 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
     if (t == 0) *p.total = pieces;
 }
 
-// A warp for each row and head: the parts of a group's shared tokens and of the sequence's own become the result.
+// The parts of a group's shared tokens and of the sequence's own become the result: a team of warps for each row and head, which take the
+// parts in turn.  One warp is enough where rows fill the card; 57 parts of few rows took one 15 us.
 struct JoinCall {
     KvAttend a;
     const int2* skip;
@@ -716,6 +778,7 @@ struct JoinCall {
     const float* slot_o;       // and its pieces
     const float2* slot_ml;
     int block_rows;            // rows of its units
+    int team;                  // warps: 1, 2, 4 or 8
 };
 // Parts of a row: `count` of them, `step` rows apart
 struct PartList {
@@ -728,8 +791,10 @@ constexpr int JOIN_WARPS = 8;
 template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
     pdl_trigger();
     pdl_wait();
+    __shared__ __align__(16) float s_o[JOIN_WARPS][256];
+    __shared__ float s_l[JOIN_WARPS];
     const KvAttend& a = p.a;
-    const int lane = threadIdx.x & 31, row = blockIdx.x, D = a.c.head_dim;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x, D = a.c.head_dim, team = p.team, mate = warp & (team - 1);
     const int i = a.rows.starts ? warp_last_le(a.rows.n, row, [&](int k) { return a.rows.at(k); }) : row / a.rows.each;
     if (i < 0) return;
     const int r0 = a.rows.at(i), r1 = a.rows.at(i + 1);
@@ -746,7 +811,9 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
         else common = make_int2(p.entries[a.rows.n + g].cuts, p.entries[a.rows.n + g].slot);
     }
     const int in_group = g >= 0 ? row - p.group_rows[g] : 0;
-    for (int h = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); h < a.heads; h += gridDim.y * JOIN_WARPS) {
+    const int heads = JOIN_WARPS / team;   // of the block at a time
+    for (int h0 = blockIdx.y * heads; h0 < a.heads; h0 += gridDim.y * heads) {
+        const int h = min(h0 + warp / team, a.heads - 1);   // the last one more than once, alike
         const long long at = (long long)row * a.heads + h;
         const int kvh = h / a.group, hh = h - kvh * a.group;
         auto list = [&](const int2& cuts, const float* o, const float2* ml, int r, int size, const float* slot_o, const float2* slot_ml) {
@@ -771,18 +838,18 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const PartList& x = lists[q];
-            for (int k0 = 0; k0 < x.count; k0 += 32) {
+            for (int k0 = mate; k0 < x.count; k0 += 32 * team) {   // lane j: part k0 + j * team
                 float f = 0.f;
-                if (k0 + lane < x.count) {
-                    const float2 y = x.ml[x.at + (long long)(k0 + lane) * x.step];
+                if (k0 + lane * team < x.count) {
+                    const float2 y = x.ml[x.at + (long long)(k0 + lane * team) * x.step];
                     f = ex2(y.x - base);
                     l += move_norm(y.y, y.x - base, f);
                 }
-                const int n = min(32, x.count - k0);
+                const int n = min(32, (x.count - k0 + team - 1) / team);
 #pragma unroll 8
                 for (int j = 0; j < n; ++j) {
                     const float w = __shfl_sync(0xffffffffu, f, j);
-                    const float* src = x.o + (x.at + (long long)(k0 + j) * x.step) * D;
+                    const float* src = x.o + (x.at + (long long)(k0 + j * team) * x.step) * D;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int e = b ? e1 : e0;
@@ -796,6 +863,25 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
         }
 #pragma unroll
         for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        if (team > 1) {   // the first of a team adds the others' sums up
+            __syncthreads();
+            if (e0 < D) *reinterpret_cast<float4*>(&s_o[warp][e0]) = o[0];
+            if (e1 < D) *reinterpret_cast<float4*>(&s_o[warp][e1]) = o[1];
+            if (lane == 0) s_l[warp] = l;
+            __syncthreads();
+            if (mate) continue;
+            for (int w = warp + 1; w < warp + team; ++w) {
+                l += s_l[w];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int e = b ? e1 : e0;
+                    if (e >= D) continue;
+                    const float4 v = *reinterpret_cast<const float4*>(&s_o[w][e]);
+                    o[b].x += v.x, o[b].y += v.y, o[b].z += v.z, o[b].w += v.w;
+                }
+            }
+        }
+        if (h0 + warp / team >= a.heads) continue;
         const bool seen = l > 0.f || l != l;
         const float inv = seen ? 1.f / l : 0.f;
         T* dst = static_cast<T*>(a.out) + row * a.out_stride + (long long)h * D;
@@ -843,7 +929,7 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
 
 // Whether kv_prefix_kernel reads the shared tokens, 128 rows at a time, or kv_piece_kernel, 16.
 bool prefix_takes(const KvAttend& a, int n_groups) {
-    return a.c.head_dim <= 128 && (long long)a.rows.rows * a.group > 16ll * n_groups;
+    return a.c.head_dim <= 128 && (long long)a.rows.rows * a.group > 32ll * n_groups;
 }
 
 }  // namespace
@@ -872,7 +958,7 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
-    const int block = prefix_rows(c, dtype);
+    const int tiles = prefix_tiles(call, dtype, n_groups), block = tiles * PT_ROWS;
     for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
         KvAttend b = call;
         b.rows = {plan.group_rows + g0, 0, std::min(n_groups - g0, TA_SEQS), rows};
@@ -883,9 +969,9 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
         const long long units = ((long long)rows * call.group / block + b.rows.n) * c.kv_heads;
         const unsigned blocks = (unsigned)std::max<long long>(units, sms);
         if (c.code == CAC_KV8_INT8)
-            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, blocks, s);
+            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, tiles, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, tiles, blocks, s);
         else
-            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_E4M3>(p, blocks, s) : launch_prefix<float, CAC_KV8_E4M3>(p, blocks, s);
+            e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_E4M3>(p, tiles, blocks, s) : launch_prefix<float, CAC_KV8_E4M3>(p, tiles, blocks, s);
         if (e != cudaSuccess) return e;
     }
     // the others, of each sequence: as many blocks as there may be pieces
@@ -895,10 +981,12 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
                                : kv_launch_pieces<CAC_KV8_E4M3>(a, pieces, dtype, blocks, s);
     if (e != cudaSuccess) return e;
 
+    const long long results = (long long)rows * call.heads;
+    const int team = results > 8 * sms ? 1 : results > 4 * sms ? 2 : results > 2 * sms ? 4 : 8;
     const JoinCall join{call, plan.skip, plan.group_of, plan.group_rows, deal.entries, pieces,
                         prefix ? static_cast<const int2*>(place(at.cut)) : nullptr, static_cast<const float*>(place(at.prefix_o)),
-                        static_cast<const float2*>(place(at.prefix_ml)), block};
-    const dim3 grid(rows, std::min((call.heads + JOIN_WARPS - 1) / JOIN_WARPS, 8));
+                        static_cast<const float2*>(place(at.prefix_ml)), block, team};
+    const dim3 grid(rows, std::min((call.heads * team + JOIN_WARPS - 1) / JOIN_WARPS, 64));
     return dtype == CAC_DTYPE_BF16 ? launch_k(kv_join_shared_kernel<bf16>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join)
                                    : launch_k(kv_join_shared_kernel<float>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join);
 }

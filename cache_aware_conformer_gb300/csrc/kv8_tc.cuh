@@ -8,9 +8,10 @@ namespace cac {
 
 constexpr int PT_ROWS = 128, PT_KEYS = 128, PT_HALF = 64;
 
-template <class T, int HDP> struct PShape {
+// TILES: row tiles of a block, two at most: what shared memory and TMEM hold
+template <class T, int HDP, int TILES = sizeof(T) == 4 && HDP == 128 ? 1 : 2> struct PShape {
     static constexpr bool WIDE = sizeof(T) == 4;             // queries and weights as hi + lo
-    static constexpr int NM = WIDE && HDP == 128 ? 1 : 2;    // row tiles of a block: what shared memory and TMEM hold
+    static constexpr int NM = TILES;
     static constexpr int PARTS = WIDE ? 2 : 1;
     static constexpr int PANEL = 128 * 128;                  // 128 rows of 64 fp16
     static constexpr int TILE = HDP / 64 * PANEL;
