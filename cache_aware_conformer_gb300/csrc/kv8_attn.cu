@@ -1027,15 +1027,17 @@ __global__ void __launch_bounds__(HDP * JOIN_Y)
 // shared memory.  Where units are many and short this has a quarter of kv_attend_kernel's latency: a block looks up one entry and not the
 // lengths of all sequences, and nothing goes through global memory twice.  Rows at most 8: tokens as the rows of operand A.
 // ---------------------------------------------------------------------------
-template <class T, int HDP> struct PieceShape {
-    static constexpr int STAGE = 2 * KV_BLOCK * HDP, STAGES = HDP == 256 ? 3 : 4;
+template <class T, int HDP, bool LOW> struct PieceShape {
+    static constexpr int BLOCKS = piece_blocks(HDP, LOW);
+    static constexpr int STAGE = 2 * KV_BLOCK * HDP, STAGES = HDP == 256 || (HDP == 128 && LOW) ? 3 : 4;
     static constexpr int RING = PIECE_WARPS * STAGES * STAGE, SUMS = PIECE_WARPS * 16 * (HDP + 2) * 4;
-    static constexpr int BYTES = RING > SUMS ? RING : SUMS, BLOCKS = piece_blocks(HDP);
+    static constexpr int BYTES = RING > SUMS ? RING : SUMS;
+    static_assert(BLOCKS * (BYTES + 1024) <= 227 * 1024, "shared memory");
 };
-template <class T, int CODE, int HDP, bool LOW>
+template <class T, int CODE, int HDP, bool LOW, bool ALL_LOW>
 __device__ __forceinline__ void piece_sums(const KvAttend& a, const SeqWork& s, int head, int r0, int x0, int x1, uint8_t* ring,
                                            const Partials& sums) {
-    using P = PieceShape<T, HDP>;
+    using P = PieceShape<T, HDP, ALL_LOW>;
     constexpr int STAGES = P::STAGES, STAGE = P::STAGE, CH = HDP / 16;
     const int lane = threadIdx.x & 31, D = a.c.head_dim;
     auto look = [&](int x) { return x < x1 ? tile_of<CODE>(a, s, x, head) : Tile{-1, 0.f, 0.f, 0.f, 0}; };
@@ -1101,10 +1103,11 @@ __device__ __forceinline__ void piece_sums(const KvAttend& a, const SeqWork& s, 
     r.emit(a, s, head, r0, &sums, threadIdx.x >> 5);
 }
 
-template <class T, int CODE, int HDP>
-__global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP>::BLOCKS))
+// ALL_LOW: no unit has more than 8 rows, which takes fewer registers
+template <class T, int CODE, int HDP, bool ALL_LOW>
+__global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP, ALL_LOW>::BLOCKS))
     kv_piece_kernel(const __grid_constant__ KvAttend a, const __grid_constant__ KvPieces p) {
-    using P = PieceShape<T, HDP>;
+    using P = PieceShape<T, HDP, ALL_LOW>;
     extern __shared__ __align__(128) uint8_t ring_all[];
     pdl_trigger();
     pdl_wait();
@@ -1120,8 +1123,12 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP>::BLOCKS)
     sums.o = reinterpret_cast<float*>(ring_all);
     sums.ml = sums.o + PIECE_WARPS * 16 * HDP;
     uint8_t* ring = ring_all + warp * P::STAGES * P::STAGE;
-    if (rows <= 8) piece_sums<T, CODE, HDP, true>(a, e.s, head, r0, x0, x1, ring, sums);
-    else piece_sums<T, CODE, HDP, false>(a, e.s, head, r0, x0, x1, ring, sums);
+    if constexpr (ALL_LOW) {
+        piece_sums<T, CODE, HDP, true, true>(a, e.s, head, r0, x0, x1, ring, sums);
+    } else {
+        if (rows <= 8) piece_sums<T, CODE, HDP, true, false>(a, e.s, head, r0, x0, x1, ring, sums);
+        else piece_sums<T, CODE, HDP, false, false>(a, e.s, head, r0, x0, x1, ring, sums);
+    }
     __syncthreads();
     // the warps' parts become the block's: 4 elements of a row to a thread
     const float2* ml = reinterpret_cast<const float2*>(sums.ml);
@@ -1151,9 +1158,10 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP>::BLOCKS)
     }
 }
 
-template <class T, int CODE, int HDP> cudaError_t launch_pieces(const KvAttend& a, const KvPieces& p, unsigned blocks, cudaStream_t s) {
-    using P = PieceShape<T, HDP>;
-    const auto kernel = kv_piece_kernel<T, CODE, HDP>;
+template <class T, int CODE, int HDP, bool ALL_LOW>
+cudaError_t launch_pieces(const KvAttend& a, const KvPieces& p, unsigned blocks, cudaStream_t s) {
+    using P = PieceShape<T, HDP, ALL_LOW>;
+    const auto kernel = kv_piece_kernel<T, CODE, HDP, ALL_LOW>;
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = 1ull << (a.c.device & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
@@ -1162,6 +1170,9 @@ template <class T, int CODE, int HDP> cudaError_t launch_pieces(const KvAttend& 
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     return launch_k(kernel, dim3(blocks), dim3(PIECE_WARPS * 32), P::BYTES, s, 1, a, p);
+}
+template <class T, int CODE, int HDP> cudaError_t launch_pieces(const KvAttend& a, const KvPieces& p, unsigned blocks, cudaStream_t s) {
+    return p.low ? launch_pieces<T, CODE, HDP, true>(a, p, blocks, s) : launch_pieces<T, CODE, HDP, false>(a, p, blocks, s);
 }
 
 template <class T, int CODE, int HDP, bool LOW>

@@ -135,12 +135,13 @@ struct KvPieces {
     const int32_t* first;  // [count] the entries' again
     const int32_t* total;  // pieces in all
     int count, own;        // entries; those from own on go to o1, ml1
+    bool low;              // no unit has more than 8 rows
     float *o0, *o1, *slot_o;       // [rows][heads][head_dim]; [slot][16][head_dim]: sums times the norm's factor
     float2 *ml0, *ml1, *slot_ml;   // their maxima and norms
 };
 constexpr int PIECE_WARPS = 4;
-// blocks of an SM that take pieces at once
-constexpr int piece_blocks(int head_dim) { return head_dim <= 128 ? 3 : 1; }
+// blocks of an SM that take pieces at once; low: of units of 8 rows at most
+constexpr int piece_blocks(int head_dim, bool low) { return head_dim <= 64 ? (low ? 5 : 3) : head_dim <= 128 ? (low ? 4 : 3) : 1; }
 template <int CODE>
 cudaError_t kv_launch_pieces(const KvAttend& a, const KvPieces& p, int dtype, unsigned blocks, cudaStream_t s);
 extern template cudaError_t kv_launch_pieces<CAC_KV8_INT8>(const KvAttend&, const KvPieces&, int, unsigned, cudaStream_t);

@@ -18,13 +18,18 @@ int sm_count(int device) {
 
 namespace {
 
+// Tokens that the queries of a sequence see at most
+long long longest(const cac_kv8& c, int max_new, int left, int chunk, int sinks) {
+    const long long tokens = (long long)c.max_pages * c.page_tokens;
+    return left < 0 ? tokens : std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);
+}
+
 // Whether units are cut and dealt out, or a warp takes a whole one: the latter saves the deal and the join, but takes about 0.45 us
 // a tile.  Measured (2 bf16 queries, windows of 220 / 450 / 900 tokens, us): 16 sequences of 8 heads 11 / 17 / 28 whole, 18 /
 // 19 / 20 dealt out; 256 sequences 17 / 30 / 50 and 28 / 45 / 66; 64 of heads 128 wide 15 / 26 / 45 and 21 / 26 / 38; one of 500 tokens 21
 // and 17.
 bool splits(const cac_kv8& c, int n, int sms, int max_new, int left, int chunk, int sinks) {
-    long long tokens = (long long)c.max_pages * c.page_tokens;
-    if (left >= 0) tokens = std::min(tokens, (long long)left + 2ll * chunk + max_new + sinks + 2 * KV_BLOCK);
+    const long long tokens = longest(c, max_new, left, chunk, sinks);
     const long long units = (long long)n * c.kv_heads;
     const int tiles = units >= 8ll * sms ? 64 : units >= sms / 2 ? 36 : 20;
     return tokens > tiles * KV_BLOCK;
@@ -145,8 +150,13 @@ extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const i
     if (((long long)rows * group / 16 + n) * c->kv_heads > INT32_MAX / 32 || n_groups > (1 << 28)) return CAC_E_LIMIT;
     const KvAttend a = part_of(*c, layer, n, 0, n, ids, starts, rows, most, heads, scale, {att_left, att_chunk, sinks}, q, q_stride,
                                out, out_stride, lse);
-    // Sequences with many query rows each: their products bound the call, and every row tile reads the tokens anyway.
-    if (kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
+    // Two kinds of call are attend's.  Sequences with many query rows each: their products bound the call, and every row tile reads the
+    // tokens anyway.  And those that have less than 100 MB to read even with nothing shared, which takes 15 us: finding out what is,
+    // the parts and their join take as long.  Measured (sequences behind a prefix, own tokens up to 60; us of attend / with the prefix read once):
+    // 8 K/V heads of 128, group 4, bf16: 8 sequences 34 MB 24 / 26, 132 MB 36 / 37, 263 MB 53 / 45; 32 of them 69 MB 29 / 36, 266 MB
+    // 55 / 39, 1,053 MB 156 / 50; 8 heads of 64, fp32: 8 sequences 66 MB 29 / 29, 132 MB 43 / 32; 32 of them 68 MB 30 / 27.
+    const long long bytes = (long long)n * c->kv_heads * longest(*c, most, att_left, att_chunk, sinks) * 2 * c->head_dim;
+    if (bytes < 100000000 || kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
         return cac_kv8_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_left, att_chunk, sinks, q, q_stride, out,
                               out_stride, lse, dtype, workspace, workspace_bytes, stream);
     DeviceScope dev(c->device);

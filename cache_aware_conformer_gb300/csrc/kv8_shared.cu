@@ -231,6 +231,7 @@ template <class T, int HDP, int TILES> struct XShape : PShape<T, HDP, TILES> {
     static constexpr int XBYTES = OFF_RAW_BAR + P::CONV * SLOTS * 8 + 1024;
     static constexpr int XSMEM = XBYTES > 120 * 1024 ? XBYTES : 120 * 1024;  // one block an SM
     static_assert(SLOTS >= 2 && XSMEM <= 227 * 1024, "shared memory");
+    static_assert(4 * 32 * 32 * 4 <= P::PARTS * P::TILE, "results on their way out take the place of a row tile's queries");
 };
 
 // one thread of a converged warp, the same each time
@@ -468,11 +469,14 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
             if (ok) {
                 const int query = on ? a.query_of(row) : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
                 const long long at = w.cut ? (long long)blockIdx.x * ROWS + x * PT_ROWS + r : (w.row0 + (long long)query) * a.heads + qh;
-                float* dst = (w.cut ? p.slot_o : p.part_o) + at * D;
+                // 32 columns at a time by way of shared memory, where the row tile's queries were: eight threads store 128 bytes of a row (a
+                // row to a thread took 7 us)
+                float* pad = reinterpret_cast<float*>(smem + x * S::PARTS * S::TILE) + (warp & 3) * 32 * 32;
+                float* to = w.cut ? p.slot_o : p.part_o;
 #pragma unroll
                 for (int c = 0; c < HDP / 32; ++c) {
                     float v[32];
-                    __syncwarp();  // rows past the last one stored nothing; the loads are for a converged warp
+                    __syncwarp();  // the loads are for a converged warp
                     tmem_ld32(col_o + c * 32, v);
                     if (S::WIDE && w.halves > S::FLUSH) {
                         float sum[32];
@@ -480,12 +484,19 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
 #pragma unroll
                         for (int k = 0; k < 32; ++k) v[k] += sum[k];
                     }
-                    if (!on) continue;
 #pragma unroll
                     for (int k = 0; k < 32; k += 4)
-                        if (c * 32 + k < D)
-                            *reinterpret_cast<float4*>(dst + c * 32 + k) =
-                                make_float4(v[k] * S::NORM, v[k + 1] * S::NORM, v[k + 2] * S::NORM, v[k + 3] * S::NORM);
+                        *reinterpret_cast<float4*>(pad + lane * 32 + (k ^ (lane & 7) << 2)) =
+                            make_float4(v[k] * S::NORM, v[k + 1] * S::NORM, v[k + 2] * S::NORM, v[k + 3] * S::NORM);
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int of = 4 * k + (lane >> 3), e = c * 32 + (lane & 7) * 4;
+                        const long long row_at = __shfl_sync(0xffffffffu, at, of);
+                        const bool there = __shfl_sync(0xffffffffu, on, of);
+                        if (there && e < D) *reinterpret_cast<float4*>(to + row_at * D + e) =
+                                *reinterpret_cast<const float4*>(pad + of * 32 + (((lane ^ of) & 7) << 2));
+                    }
                 }
                 if (on) (w.cut ? p.slot_ml : p.part_ml)[at] = make_float2(m, l);
             }
@@ -917,7 +928,7 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
         return was;
     };
     const size_t units = (size_t)rows * heads, D = c.head_dim;
-    const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim) * 16, prefix = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
+    const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim, true) * 16, prefix = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
     s.skip = take((size_t)n * 8), s.group_of = take((size_t)n * 4), s.shared = take((size_t)n_groups * 16);
     s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 8);
     s.entries = take(((size_t)n + n_groups) * sizeof(KvEntry)), s.first = take(((size_t)n + n_groups) * 4), s.total = take(4);
@@ -949,13 +960,14 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     const bool prefix = prefix_takes(call, n_groups);
     KvAttend a = call;
     a.skip = plan.skip;
-    const int most = sms * piece_blocks(c.head_dim), dealt = prefix ? 0 : n_groups;
+    const bool low = (long long)call.max_new * call.group <= 8 && (prefix || (long long)rows * call.group <= 8);
+    const int most = sms * piece_blocks(c.head_dim, low), dealt = prefix ? 0 : n_groups;
     const DealCall deal{a,     plan.shared, plan.group_rows, static_cast<KvEntry*>(place(at.entries)), static_cast<int32_t*>(place(at.first)),
                         static_cast<int32_t*>(place(at.total)), dealt, most};
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
-    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n,
+    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
     const int tiles = prefix_tiles(call, dtype, n_groups), block = tiles * PT_ROWS;

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int, c_int32, c_longlong, c_size_t, c_void_p
 
 import numpy as np
@@ -86,6 +87,9 @@ class CacW4(ctypes.Structure):
     _fields_ = [(n, c_int32) for n in ("n", "k", "group", "device")] + [(n, c_void_p) for n in ("packed", "scale", "zero")]
 
 
+_W4 = struct.Struct("@iiiiPPP")   # CacW4's bytes, without the object
+
+
 class CacRotary(ctypes.Structure):
     _fields_ = ([(n, c_int32) for n in ("head_dim", "rot_dim", "layout", "dtype", "device")] +
                 [("amplitude", c_float), ("eps", c_float), ("reserved", c_int32)] +
@@ -93,6 +97,7 @@ class CacRotary(ctypes.Structure):
 
 
 _LIB = None
+_torch = None
 
 
 def _lib():
@@ -517,37 +522,50 @@ def gemm_w4(A, packed, scale, zero=None, bias=None, out=None, stream=None):
     two codes to a byte, the even k in the low half.  A: cuda bf16 or fp32 [M, K], rows may be strided; packed: uint8
     [N, K/2]; scale: bf16 [N, K/group], group 32, 64 or 128; zero: uint8 as scale, or None for 8; bias: fp32 [N].  Returns
     [M, N] of A's type.  `w4.quantize` makes packed, scale and zero."""
-    import torch
-    if A.dim() != 2 or packed.dim() != 2 or scale.dim() != 2 or A.size(1) != 2 * packed.size(1) or \
-            scale.size(0) != packed.size(0) or scale.size(1) < 1 or A.size(1) % scale.size(1) or not A.is_cuda:
-        raise ValueError("A [M, K], packed [N, K / 2] and scale [N, K / group] are needed")
-    (M, K), (N, G) = A.shape, scale.shape
-    dev, dt = A.device, A.dtype
-    for t, want, what in ((packed, torch.uint8, "packed"), (scale, torch.bfloat16, "scale"), (zero, torch.uint8, "zero"),
-                          (bias, torch.float32, "bias")):
-        if t is not None and (t.dtype is not want or t.device != dev or not t.is_contiguous()):
-            raise ValueError(f"{what}: a contiguous {want} tensor on {dev} is needed")
-    if zero is not None and zero.shape != scale.shape or bias is not None and tuple(bias.shape) != (N,):
-        raise ValueError("zero has the shape of scale, bias is [N]")
-    if dt is not torch.bfloat16 and dt is not torch.float32 or (K > 1 and A.stride(1) != 1):
-        raise ValueError("A: bfloat16 or float32, with the elements of a row next to each other")
-    on = stream if stream is not None else torch.cuda.current_stream(dev)
+    # what is slow in Python (device objects, stream contexts, structures, imports) stays off the path of a step's products
+    global _torch
+    if _torch is None:
+        import torch as _torch
+    torch, bf16 = _torch, _torch.bfloat16
+    (M, K), (N, half), (rows, G) = A.shape, packed.shape, scale.shape
+    dt, dev = A.dtype, A.get_device()
+    if 2 * half != K or rows != N or G < 1 or K % G or dev < 0 or (dt is not bf16 and dt is not torch.float32):
+        raise ValueError("A [M, K] of bfloat16 or float32, packed [N, K / 2] and scale [N, K / group] are needed, on a GPU")
+    if packed.dtype is not torch.uint8 or scale.dtype is not bf16 or packed.get_device() != dev or scale.get_device() != dev or \
+            not packed.is_contiguous() or not scale.is_contiguous():
+        raise ValueError("packed: uint8, scale: bfloat16, both contiguous and on A's device")
+    if zero is not None and (zero.dtype is not torch.uint8 or zero.shape != scale.shape or zero.get_device() != dev or
+                             not zero.is_contiguous()):
+        raise ValueError("zero: contiguous uint8 of scale's shape, on A's device")
+    if bias is not None and (bias.dtype is not torch.float32 or bias.dim() != 1 or bias.size(0) != N or
+                             bias.get_device() != dev or not bias.is_contiguous()):
+        raise ValueError("bias: contiguous float32 [N] on A's device")
+    a_stride, one = A.stride()
+    if one != 1 and K > 1:
+        raise ValueError("A: the elements of a row have to lie next to each other")
     if out is None:
         if stream is None:
-            out = torch.empty((M, N), dtype=dt, device=dev)
+            out = A.new_empty((M, N))
         else:
             with torch.cuda.stream(stream):
-                out = torch.empty((M, N), dtype=dt, device=dev)
-    elif out.dtype is not dt or tuple(out.shape) != (M, N) or out.device != dev or (N > 1 and out.stride(1) != 1):
-        raise ValueError(f"out: a tensor [{M}, {N}] of A's type on {dev}")
+                out = A.new_empty((M, N))
+        c_stride = N
+    else:
+        if out.dtype is not dt or out.shape != (M, N) or out.get_device() != dev or (N > 1 and out.stride(1) != 1):
+            raise ValueError(f"out: a tensor [{M}, {N}] of A's type on its device")
+        c_stride = out.stride(0) if M > 1 else N
     if M == 0:
         return out
-    if stream is not None:
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        handle = stream.cuda_stream
         Kv8Cache._used_on(stream, A, packed, scale, zero, bias, out)
-    w = CacW4(N, K, K // G, dev.index, _ptr(packed), _ptr(scale), _ptr(zero))
-    _check(_lib().cac_op_gemm_w4(ctypes.addressof(w), M, _ptr(A), A.stride(0) if M > 1 else K, _ptr(bias), _ptr(out),
-                                 out.stride(0) if M > 1 else N, 1 if dt is torch.bfloat16 else 0, on.cuda_stream),
-           "cac_op_gemm_w4")
+    w = _W4.pack(N, K, K // G, dev, packed.data_ptr(), scale.data_ptr(), 0 if zero is None else zero.data_ptr())
+    r = _lib().cac_op_gemm_w4(w, M, A.data_ptr(), a_stride if M > 1 else K, None if bias is None else bias.data_ptr(),
+                              out.data_ptr(), c_stride, 1 if dt is bf16 else 0, handle)
+    if r:
+        _check(r, "cac_op_gemm_w4")
     return out
 
 
@@ -557,6 +575,7 @@ class Rotary:
     cache."""
 
     SCALINGS = {"none": 0, "linear": 1, "base": 2, "ramp": 3}
+    NONE = (0, None, 0, None, 0)   # a side that a call does not have
 
     def __init__(self, cfg, q_gain=None, k_gain=None, device=None):
         import torch
@@ -584,64 +603,71 @@ class Rotary:
         self._c = [CacRotary(cfg.head_dim, rot, 0 if cfg.layout == "half" else 1, dt, self.device.index, cfg.amplitude, cfg.eps, 0,
                              self.steps.data_ptr(), _ptr(self.q_gain), _ptr(self.k_gain)) for dt in (0, 1)]
         self._refs = [ctypes.addressof(c) for c in self._c]
+        self._torch, self._D, self._dev, self._current = torch, cfg.head_dim, self.device.index, torch._C._cuda_getCurrentRawStream
+        self._bf16, self._f32, self._i32, self._call = torch.bfloat16, torch.float32, torch.int32, _lib().cac_op_rotate
         self._streams = {torch.cuda.current_stream(self.device).cuda_stream}
 
     def _side(self, t, out, what, stream):
-        """(heads, pointer, stride, pointer and stride of the result, the result, dtype code) of q or k."""
-        import torch
-        if t is None:
-            if out is not None:
-                raise ValueError(f"{what}: no input for its output")
-            return 0, None, 0, None, 0, None, None
-        D = self.cfg.head_dim
+        """(heads, pointer, stride, pointer and stride of the result) of q or k, and the result."""
+        D, dt = self._D, t.dtype
+        if t.dim() != 3 or t.get_device() != self._dev or (dt is not self._bf16 and dt is not self._f32):
+            raise ValueError(f"{what}: bfloat16 or float32 [rows, heads, {D}] on {self.device}")
+        rows, heads, width = t.shape
+        row, head, one = t.stride()
+        if width != D or one != 1 or (head != D and heads > 1):
+            raise ValueError(f"{what}: [rows, heads, {D}], the heads of a row one after another")
+        if rows <= 1:
+            row = heads * D
         if out is None:
             if stream is None:
-                out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+                out = t.new_empty((rows, heads, D))
             else:
-                with torch.cuda.stream(stream):
-                    out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-        for x in (t, out):
-            if x.dim() != 3 or x.shape != t.shape or x.size(2) != D or x.get_device() != self.device.index or x.dtype is not t.dtype or \
-                    x.dtype not in (torch.bfloat16, torch.float32):
-                raise ValueError(f"{what}: bfloat16 or float32 [rows, heads, {D}] on {self.device}")
-            if x.stride(2) != 1 or (x.size(1) > 1 and x.stride(1) != D):
-                raise ValueError(f"{what}: the heads of a row have to lie one after another")
-        stride = lambda x: x.stride(0) if x.size(0) > 1 else x.size(1) * D  # noqa: E731
-        return t.size(1), t.data_ptr(), stride(t), out.data_ptr(), stride(out), out, 1 if t.dtype is torch.bfloat16 else 0
+                with self._torch.cuda.stream(stream):
+                    out = t.new_empty((rows, heads, D))
+            to = heads * D
+        else:
+            if out.shape != t.shape or out.dtype is not dt or out.get_device() != self._dev:
+                raise ValueError(f"{what}: an output of its shape and type")
+            to, head, one = out.stride()
+            if one != 1 or (head != D and heads > 1):
+                raise ValueError(f"{what}: the heads of an output's row one after another")
+            if rows <= 1:
+                to = heads * D
+        return (heads, t.data_ptr(), row, out.data_ptr(), to), out
 
     def _sides(self, q, k, out, stream):
-        """Both sides of a call: its rows, the dtype's struct, and what the entry points take."""
-        import torch
-        if q is None and k is None:
-            raise ValueError("queries, keys or both")
+        """Both sides of a call: its rows, the type's struct, what the entry points take, and the stream."""
         qo, ko = out if out is not None else (None, None)
-        one, two = self._side(q, qo, "q", stream), self._side(k, ko, "k", stream)
-        rows = (q if q is not None else k).size(0)
-        if q is not None and k is not None and (k.size(0) != rows or one[6] != two[6]):
+        if (q is None and k is None) or (q is None and qo is not None) or (k is None and ko is not None):
+            raise ValueError("queries, keys or both, and no output without its input")
+        one, qo = self._side(q, qo, "q", stream) if q is not None else (self.NONE, None)
+        two, ko = self._side(k, ko, "k", stream) if k is not None else (self.NONE, None)
+        of = q if q is not None else k
+        rows, dt = of.size(0), of.dtype
+        if q is not None and k is not None and (k.size(0) != rows or k.dtype is not dt):
             raise ValueError("q and k have the same rows and type")
-        handle = (stream if stream is not None else torch.cuda.current_stream(self.device)).cuda_stream
+        handle = stream.cuda_stream if stream is not None else self._current(self._dev)
         if handle not in self._streams:   # its memory is not given out again before this stream's calls have run
-            Kv8Cache._used_on(stream if stream is not None else torch.cuda.current_stream(self.device), self.steps, self.q_gain,
-                              self.k_gain)
+            Kv8Cache._used_on(stream if stream is not None else self._torch.cuda.current_stream(self.device), self.steps,
+                              self.q_gain, self.k_gain)
             self._streams.add(handle)
         if stream is not None:
-            Kv8Cache._used_on(stream, q, k, one[5], two[5])
-        return rows, self._refs[one[6] if q is not None else two[6]], one, two, handle
+            Kv8Cache._used_on(stream, q, k, qo, ko)
+        return rows, self._refs[1 if dt is self._bf16 else 0], one, two, (qo, ko), handle
 
     def rotate(self, positions, q=None, k=None, out=None, stream=None):
         """(q, k) turned: q [rows, heads, head_dim], k [rows, kv_heads, head_dim] (either may be None), positions an int32
         cuda tensor [rows].  out: (q_out, k_out), which may be the inputs."""
-        import torch
-        rows, ref, a, b, handle = self._sides(q, k, out, stream)
-        if positions.dtype is not torch.int32 or positions.dim() != 1 or positions.numel() != rows or \
-                positions.get_device() != self.device.index or not positions.is_contiguous():
+        rows, ref, a, b, got, handle = self._sides(q, k, out, stream)
+        if positions.dtype is not self._i32 or positions.dim() != 1 or positions.size(0) != rows or \
+                positions.get_device() != self._dev or not positions.is_contiguous():
             raise ValueError(f"positions: a contiguous int32 tensor [{rows}] on {self.device} is needed")
         if stream is not None:
             Kv8Cache._used_on(stream, positions)
-        r = _lib().cac_op_rotate(ref, rows, positions.data_ptr(), *a[:5], *b[:5], handle)
+        r = self._call(ref, rows, positions.data_ptr(), *a, *b, handle)
         if r:
             _check(r, "cac_op_rotate")
-        return a[5], b[5]
+        return got
 
 
 def build_checked() -> bool:
@@ -1092,8 +1118,11 @@ class Kv8Cache:
         n, p, s = self._list(ids, starts)
         rows, heads = (q.size(0), q.size(1)) if q.dim() == 3 else (0, 0)
         qs, dt = self._act(q, heads, "q")
-        n_groups = 0 if groups is None else groups.numel() - 1
-        g = None if groups is None else self._ints(groups, max(n_groups, 0) + 1, "groups")
+        if groups is None:
+            n_groups, g = 0, None
+        else:
+            n_groups = max(groups.numel() - 1, 0)
+            g = self._ints(groups, n_groups + 1, "groups")
         if s is None:
             max_new = rows // n if n else 0
         elif max_new is None:
@@ -1107,10 +1136,7 @@ class Kv8Cache:
         D = self._c.head_dim
         space = sums = None
         if out is None:
-            if stream is None and q.is_contiguous():
-                out = self._torch.empty_like(q)
-            else:
-                out = self._empty(stream, ((rows, heads, D), q.dtype))[0]
+            out = q.new_empty((rows, heads, D)) if stream is None else self._empty(stream, ((rows, heads, D), q.dtype))[0]
             os_ = heads * D
         else:
             os_, _ = self._act(out, heads, "out")
@@ -1132,19 +1158,20 @@ class Kv8Cache:
     def rotate(self, ids, rotary, q=None, k=None, starts=None, max_new=None, out=None, stream=None):
         """(q, k) of each sequence's last tokens turned by their positions in the cache (cac_kv8_rotate); arguments as
         Rotary.rotate's.  Extend first, then rotate, write the keys and attend with the queries."""
-        if rotary.device != self.device:
+        if rotary._dev != self._dev:
             raise ValueError(f"rotary: one on {self.device} is needed")
         n, p, s = self._list(ids, starts)
-        rows, ref, a, b, handle = rotary._sides(q, k, out, stream)
-        if k is not None and k.size(1) != self._c.kv_heads:
+        rows, ref, a, b, got, handle = rotary._sides(q, k, out, stream)
+        if k is not None and b[0] != self._c.kv_heads:
             raise ValueError(f"k: {self._c.kv_heads} heads")
         if stream is not None:
             self._used_on(stream, ids, starts)
-        self._on(stream)
-        r = self._rotate(self._ref, ref, n, p, s, rows, *a[:5], *b[1:5], handle)
+        if handle not in self._streams:
+            self._on(stream)
+        r = self._rotate(self._ref, ref, n, p, s, rows, *a, *b[1:], handle)
         if r:
             _check(r, "cac_kv8_rotate")
-        return a[5], b[5]
+        return got
 
     def fork(self, src, dst, stream=None):
         """Sequence dst[i] becomes a copy of src[i] that shares its pages (cac_kv8_fork)."""

@@ -1,5 +1,10 @@
 """Attention of sequences that share a prefix on the GPU: against the plain model in 64
-bits, sequence by sequence, and against what may and may not be shared."""
+bits, sequence by sequence, and against what may and may not be shared.  A call that has
+less than 100 MB to read even if it shares nothing is cac_kv8_attend's, so the caches here have
+tables for far longer sequences than they hold, and calls are asserted to be the shared
+kernels' by the kernels of a captured graph."""
+import warnings
+
 import numpy as np
 import pytest
 
@@ -14,6 +19,24 @@ BOUNDS = -11
 
 
 class Shared(Both):
+    def __init__(self, code="int8", layers=1, heads=2, dim=64, page=32, n_pages=64, seqs=6, dtype=F32, seed=0, least=2):
+        """least: the tables have room for 100 MB of so many sequences."""
+        room = 100_000_000 // (least * heads * 2 * dim * page) + 1
+        super().__init__(code, layers, heads, dim, page, n_pages, seqs, room, dtype, seed)
+
+    def kernels(self, call):
+        """Names in the graph of a captured call."""
+        import tempfile
+        graph = torch.cuda.CUDAGraph(keep_graph=True)
+        graph.enable_debug_mode()
+        with torch.cuda.graph(graph):
+            call()
+        with tempfile.NamedTemporaryFile(suffix=".dot") as f:
+            with warnings.catch_warnings():
+                warnings.simplefilter("ignore")      # it warns that it writes a file
+                graph.debug_dump(f.name)
+            return open(f.name).read()
+
     def family(self, groups, first=0, gain=1.0):
         """groups: (prefix, [own tokens of each member]).  A member is a fork of its group's prefix, extended.  Returns the
         groups' starts; members are sequences first, first + 1, ..."""
@@ -32,13 +55,21 @@ class Shared(Both):
         return starts
 
     def check_shared(self, ids, counts, groups, group=2, left=-1, chunk=1, sinks=0, scale=None, layer=0, q=None, qgain=1.0,
-                     uniform=False, verify=True, **kw):
+                     uniform=False, shares=True, prefix=None, **kw):
+        """shares: whether the call is the shared kernels' (None: either).  prefix: whether the shared tokens are read by the kernel for
+        many rows (None: either)."""
         cfg = self.cfg
         T, heads = int(np.sum(counts)), group * cfg.kv_heads
         q = self.rand(T, heads, cfg.head_dim, gain=qgain) if q is None else q
         rag = {} if uniform else {"starts": self.starts(counts), "max_new": max(counts, default=0)}
-        out, lse = self.cache.attend_shared(layer, self.ids(ids), q.cuda(), groups=None if groups is None else self.ids(groups),
-                                            att_left=left, att_chunk=chunk, sinks=sinks, scale=scale, lse=True, **rag, **kw)
+        dev, dq, dg = self.ids(ids), q.cuda(), None if groups is None else self.ids(groups)
+        call = lambda: self.cache.attend_shared(layer, dev, dq, groups=dg, att_left=left, att_chunk=chunk, sinks=sinks, scale=scale,  # noqa: E731
+                                                lse=True, **rag, **kw)
+        if shares is not None or prefix is not None:
+            names = self.kernels(call)
+            assert shares is None or ("kv_plan_shared_kernel" in names) == shares
+            assert prefix is None or ("kv_prefix_kernel" in names) == prefix
+        out, lse = call()
         self.cache.check()
         assert out.dtype == q.dtype and out.shape == q.shape and lse.shape == (T, heads)
         sc = scale if scale is not None else cfg.head_dim ** -0.5
@@ -70,7 +101,7 @@ class Shared(Both):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("dim,page,group", [(64, 16, 1), (128, 32, 4), (80, 48, 3), (16, 16, 8), (256, 64, 2), (64, 64, 17), (144, 16, 5)])
 def test_one_group(code, dtype, dim, page, group):
-    b = Shared(code, heads=2, dim=dim, page=page, n_pages=200, seqs=8, max_pages=60, dtype=dtype, seed=dim)
+    b = Shared(code, heads=2, dim=dim, page=page, n_pages=200, seqs=8, dtype=dtype, seed=dim)
     b.family([(5 * page + 7, [1, 3, 17, 2 * page + 1, 5, 40, 1, 9])])
     b.check_shared(range(8), [1] * 8, None, group=group, uniform=True)
     b.check_shared(range(8), [1, 3, 2, 5, 1, 0, 1, 9], [0, 8], group=group)
@@ -78,21 +109,23 @@ def test_one_group(code, dtype, dim, page, group):
 
 
 @pytest.mark.parametrize("code,dtype", [("int8", BF16), ("e4m3", F32), ("int8", F32), ("e4m3", BF16)])
-@pytest.mark.parametrize("n,group,dim", [(24, 1, 64), (9, 8, 128), (40, 4, 64), (40, 8, 128), (70, 1, 128), (33, 5, 80), (20, 3, 256)])
+@pytest.mark.parametrize("n,group,dim", [(24, 1, 64), (9, 8, 128), (40, 4, 64), (40, 8, 128), (70, 1, 128), (33, 5, 80), (20, 3, 256), (60, 1, 64),
+                                         (12, 4, 128), (17, 8, 128), (33, 8, 64), (300, 1, 32)])
 def test_many_rows(code, dtype, n, group, dim):
     """Groups of more rows than a tile has, of 8 to 350 rows."""
     rng = np.random.default_rng(n)
     own = rng.integers(1, 90, n).tolist()
-    b = Shared(code, heads=2, dim=dim, page=32, n_pages=600, seqs=n, max_pages=60, dtype=dtype, seed=n)
+    b = Shared(code, heads=2, dim=dim, page=32, n_pages=600 + 4 * n, seqs=n, dtype=dtype, seed=n)
     b.family([(1100, own)])
-    b.check_shared(range(n), [1] * n, None, group=group, uniform=True)
+    rows = n * group
+    b.check_shared(range(n), [1] * n, None, group=group, uniform=True, prefix=rows > 32 and dim <= 128)
     b.check_shared(range(n), rng.integers(0, 3, n).tolist(), [0, n], group=group, qgain=4.0)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("group", [1, 4])
 def test_several_groups_and_sequences_of_none(dtype, group):
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=500, seqs=20, max_pages=80, dtype=dtype, seed=3)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=500, seqs=20, dtype=dtype, seed=3)
     st = b.family([(300, [5, 6, 7]), (20, [1]), (900, [30, 1, 1, 80, 2, 4]), (16, [2, 3]), (0, [4, 5, 6]), (333, [1, 2, 3, 4, 5])])
     assert st[-1] == 20
     b.check_shared(range(20), [1] * 20, st, group=group)
@@ -104,52 +137,67 @@ def test_several_groups_and_sequences_of_none(dtype, group):
     b.check_shared([4, 5, 6, 4, 9, 5], [1] * 6, None, group=group)       # a sequence more than once
 
 
-@pytest.mark.parametrize("left,chunk,sinks", [(-1, 1, 0), (-1, 4, 0), (70, 2, 0), (10, 1, 4), (400, 1, 4), (500, 8, 40), (350, 1, 0), (0, 1, 0),
-                                              (5, 1000, 2), (100000, 1, 3)])
+@pytest.mark.parametrize("left,chunk,sinks", [(-1, 1, 0), (-1, 4, 0), (70, 2, 0), (10, 1, 4), (0, 1, 0), (5, 1000, 2), (100000, 1, 3)])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_windows_and_sinks(dtype, left, chunk, sinks):
-    """Windows that the prefix fills, reaches into, or has left."""
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=300, seqs=6, max_pages=60, dtype=dtype, seed=left + chunk)
+    """Small windows are attend's, chunks and windows that the sequence never fills the shared kernels'."""
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=300, seqs=6, dtype=dtype, seed=left + chunk)
     b.family([(389, [1, 20, 60, 130, 2, 7])])
-    b.check_shared(range(6), [1] * 6, None, left=left, chunk=chunk, sinks=sinks, uniform=True)
-    b.check_shared(range(6), [1, 4, 2, 1, 2, 3], [0, 6], left=left, chunk=chunk, sinks=sinks)
-    b.check_shared([4, 0], [2, 1], [0, 2], left=left, chunk=chunk, sinks=sinks, group=9)
+    args = {"left": left, "chunk": chunk, "sinks": sinks, "shares": None if left >= 0 else True}
+    b.check_shared(range(6), [1] * 6, None, uniform=True, **args)
+    b.check_shared(range(6), [1, 4, 2, 1, 2, 3], [0, 6], **args)
+    b.check_shared([4, 0], [2, 1], [0, 2], group=9, **args)
+
+
+@pytest.mark.parametrize("dtype,code", [(F32, "e4m3"), (BF16, "int8")])
+@pytest.mark.parametrize("left,chunk,sinks,counts", [(800, 1, 4, "one"), (800, 8, 40, "some"), (790, 1, 0, "some"), (1010, 2, 0, "one"), (870, 1, 900, "some")])
+def test_windows_that_end_within_the_prefix(dtype, code, left, chunk, sinks, counts):
+    """Enough sequences for the shared kernels: windows that begin before the prefix, within it, and for some of a group only."""
+    n = 70
+    rng = np.random.default_rng(left)
+    own = rng.integers(1, 140, n)
+    own[3], own[40] = 700, 1
+    b = Shared(code, heads=8, dim=128, page=32, n_pages=1200, seqs=n, dtype=dtype, seed=left, least=20)
+    st = b.family([(901, own[:30].tolist()), (640, own[30:].tolist())])
+    many = [1] * n if counts == "one" else rng.integers(0, 4, n).tolist()
+    b.check_shared(range(n), many, st, group=2, left=left, chunk=chunk, sinks=sinks, uniform=counts == "one")
 
 
 def test_queries_inside_the_prefix_and_nothing_of_ones_own():
     """Sequences that are copies of one another: the last query sees to the end, the first ones do not."""
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=100, seqs=5, max_pages=40)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=100, seqs=5)
     b.family([(160, [0, 0, 0, 0, 0])])
     for counts in ([1] * 5, [1, 160, 3, 30, 2], [170, 1, 1, 1, 1]):
         b.check_shared(range(5), counts, None)
     b.check_shared(range(5), [1] * 5, None, chunk=16)
-    b.check_shared(range(5), [1] * 5, None, chunk=7, left=20)
+    b.check_shared(range(5), [1] * 5, None, chunk=7, left=20, shares=False)
 
 
 def test_released_pages_and_truncated_members():
-    b = Shared("e4m3", heads=2, dim=64, page=16, n_pages=200, seqs=6, max_pages=60, dtype=BF16)
+    b = Shared("e4m3", heads=2, dim=64, page=16, n_pages=200, seqs=6, dtype=BF16)
     b.family([(400, [3, 4, 5, 6, 7, 8])])
     b.trim(range(6), 100, 1, 20)                     # the same pages of all: still one group
-    b.check_shared(range(6), [1] * 6, None, left=100, sinks=20)
+    b.check_shared(range(6), [1] * 6, None, left=100, sinks=20, shares=False)
     b.check_shared(range(6), [1] * 6, None)          # released pages are not seen
     b.truncate([2, 4], [330, 0])                     # into a page that the window has not passed
-    b.check_shared([0, 1, 2, 3, 5], [1] * 5, None, left=100, sinks=20)
+    b.check_shared([0, 1, 2, 3, 5], [1] * 5, None, left=100, sinks=20, shares=False)
     b.append([2, 4], [90, 30])                       # other pages from there on
     b.check_shared(range(6), [1] * 6, None)
     b.check_shared(range(6), [1, 2, 1, 1, 30, 1], None)
+    b.check_shared(range(6), [1] * 6, None, group=9)  # released pages in front of the kernel for many rows
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("group", [1, 12])
 def test_a_token_that_outweighs_the_rest_on_either_side(dtype, group):
     """Maxima far apart between the parts, and V blocks of unlike sizes."""
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=4, max_pages=40, dtype=dtype)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=4, dtype=dtype)
     b.family([(200, [20, 30, 40, 50])])
     q = b.rand(4, group, 64)
     big = q[1:2, :1].float() * 40
     b.append([1], [1], k=big.to(dtype), v=b.rand(1, 1, 64, gain=100.0))
     b.check_shared(range(4), [1] * 4, None, group=group, q=q, uniform=True)
-    c = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=4, max_pages=40, dtype=dtype)
+    c = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=4, dtype=dtype)
     c.append([0], [100])
     c.append([0], [1], k=big.to(dtype), v=c.rand(1, 1, 64, gain=1e-4))
     c.append([0], [16], k=c.rand(16, 1, 64), v=torch.zeros(16, 1, 64, dtype=dtype))
@@ -161,7 +209,7 @@ def test_a_token_that_outweighs_the_rest_on_either_side(dtype, group):
 
 
 def test_non_finite_queries_stay_in_their_rows():
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=30, max_pages=40, dtype=BF16)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=30, dtype=BF16)
     b.family([(600, [2] * 30)])
     q = b.rand(30, 6, 64)
     want, _ = b.check_shared(range(30), [1] * 30, None, group=6, q=q, uniform=True)
@@ -175,14 +223,14 @@ def test_non_finite_queries_stay_in_their_rows():
 
 
 def test_long_prefix_split_over_the_card():
-    b = Shared("int8", heads=2, dim=64, page=64, n_pages=700, seqs=8, max_pages=600, dtype=BF16)
+    b = Shared("int8", heads=2, dim=64, page=64, n_pages=700, seqs=8, dtype=BF16)
     b.family([(30011, [5, 900, 33, 1, 2, 64, 8, 12])])
     b.check_shared(range(8), [1] * 8, None, group=4, uniform=True)
 
 
 @pytest.mark.parametrize("bad", [[0, 3, 2, 6], [-1, 6], [0, 7], [5, 3]])
 def test_bad_groups_are_refused_and_share_nothing(bad):
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6, max_pages=40)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6)
     b.family([(200, [1, 2, 3, 4, 5, 6])])
     q = b.rand(6, 2, 64).cuda()
     want = b.cache.attend(0, b.ids(range(6)), q)
@@ -195,7 +243,7 @@ def test_bad_groups_are_refused_and_share_nothing(bad):
 
 def test_bad_ids_and_counts_as_in_attend():
     """Rows of such sequences are zero, or left where their rows pass the end; the others of the group are right."""
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6, max_pages=40)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6)
     b.family([(200, [1, 2, 3, 4, 5, 6])])
     for ids, counts, max_new in (([0, 1, 9, 3], [1, 1, 2, 1], 2), ([0, -1, 2, 3], [1, 1, 1, 1], 1), ([0, 1, 2, 3], [1, 12, 1, 1], 3)):
         q = b.rand(int(np.sum(counts)), 2, 64).cuda()
@@ -213,7 +261,7 @@ def test_bad_ids_and_counts_as_in_attend():
 
 
 def test_rows_of_no_sequence_are_left_alone():
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6, max_pages=40)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=200, seqs=6)
     b.family([(200, [1, 2, 3, 4, 5, 6])])
     q = b.rand(12, 2, 64).cuda()
     out = torch.full_like(q, 7.0)
@@ -230,7 +278,7 @@ def test_rows_of_no_sequence_are_left_alone():
 
 
 def test_strided_queries_and_outputs():
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=200, seqs=5, max_pages=40, dtype=BF16)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=200, seqs=5, dtype=BF16)
     b.family([(200, [1, 2, 3, 4, 5])])
     wide = b.rand(5, 9, 64).cuda()
     out = torch.full((5, 7, 64), 3.0, dtype=BF16, device="cuda")
@@ -240,7 +288,7 @@ def test_strided_queries_and_outputs():
 
 
 def test_the_same_result_each_time():
-    b = Shared("int8", heads=2, dim=128, page=32, n_pages=400, seqs=40, max_pages=200, dtype=F32)
+    b = Shared("int8", heads=2, dim=128, page=32, n_pages=400, seqs=40, dtype=F32)
     b.family([(3000, list(range(1, 41)))])
     q = b.rand(40, 8, 128).cuda()
     first = b.cache.attend_shared(0, b.ids(range(40)), q, lse=True)
@@ -251,7 +299,7 @@ def test_the_same_result_each_time():
 
 def test_more_sequences_and_groups_than_one_launch_takes():
     n = 1100
-    b = Shared("int8", heads=1, dim=64, page=16, n_pages=2400, seqs=n, max_pages=20, dtype=BF16)
+    b = Shared("int8", heads=1, dim=64, page=16, n_pages=2400, seqs=n, dtype=BF16)
     st = b.family([(64, [1] * 4), (150, [2] * 700), (40, [1] * 396)])
     ids = list(range(n))
     q = b.rand(n, 2, 64)
@@ -271,7 +319,7 @@ def test_more_sequences_and_groups_than_one_launch_takes():
 @pytest.mark.parametrize("group,counts", [(4, [1] * 10), (4, [1, 2, 0, 3, 1, 1, 1, 1, 1, 7])])
 def test_two_captured_graphs_replayed_at_once(group, counts):
     """Each has its workspace; the tables and lengths may change in between."""
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=400, seqs=10, max_pages=60, dtype=BF16)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=400, seqs=10, dtype=BF16)
     b.family([(500, list(range(1, 11)))])
     T = int(np.sum(counts))
     qs = [b.rand(T, 2 * group, 64) for _ in range(2)]
@@ -297,7 +345,7 @@ def test_two_captured_graphs_replayed_at_once(group, counts):
 
 
 def test_on_another_stream():
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=400, seqs=10, max_pages=60, dtype=BF16)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=400, seqs=10, dtype=BF16)
     b.family([(500, list(range(1, 11)))])
     q, ids, groups = b.rand(10, 8, 64).cuda(), b.ids(range(10)), b.ids([0, 10])
     want = b.cache.attend_shared(0, ids, q, groups=groups)
@@ -312,7 +360,7 @@ def test_on_another_stream():
 
 def test_prompts_behind_a_prefix_go_to_the_prompts_kernel():
     """Sequences of many query rows: attend itself, bit for bit."""
-    b = Shared("int8", heads=2, dim=64, page=32, n_pages=400, seqs=80, max_pages=40, dtype=BF16)
+    b = Shared("int8", heads=2, dim=64, page=32, n_pages=400, seqs=80, dtype=BF16)
     b.family([(300, [100] * 80)])
     q, st = b.rand(8000, 4, 64).cuda(), b.starts([100] * 80)
     got = b.cache.attend_shared(0, b.ids(range(80)), q, starts=st, max_new=100)
@@ -320,7 +368,7 @@ def test_prompts_behind_a_prefix_go_to_the_prompts_kernel():
 
 
 def test_empty_calls():
-    b = Shared("int8", heads=2, dim=64, page=16, n_pages=40, seqs=4, max_pages=10)
+    b = Shared("int8", heads=2, dim=64, page=16, n_pages=40, seqs=4)
     b.family([(20, [1, 2])])
     none = torch.empty(0, 2, 64, device="cuda")
     assert b.cache.attend_shared(0, b.ids([]), none).shape == (0, 2, 64)
@@ -344,7 +392,7 @@ def test_a_decoding_step(dtype, graph):
     from test_gpu_w4 import exact as exact_w4
     H, G, D, n, L = 2, 4, 64, 6, 2
     width = H * G * D
-    b = Shared("int8", layers=L, heads=H, dim=D, page=16, n_pages=200, seqs=n, max_pages=40, dtype=dtype, seed=31)
+    b = Shared("int8", layers=L, heads=H, dim=D, page=16, n_pages=200, seqs=n, dtype=dtype, seed=31)
     b.family([(150, [3, 4, 5, 6, 7, 8])])
     g = torch.Generator().manual_seed(7)
     weights = [[w4.quantize(torch.randn(o, i, generator=g) * i ** -0.5, 64, z) for o, i, z in ((width + 2 * H * D, width, True), (width, width, False))]
