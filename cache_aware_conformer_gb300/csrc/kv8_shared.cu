@@ -95,16 +95,17 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
             if (row_at(i + 1) == row_at(i)) continue;
             const int32_t* other = a.c.table + (long long)a.ids[i] * a.c.max_pages;
             if (other == own) continue;
-            for (int b = 0; b < same; b += 128) {
-                int x[4], y[4];
+            constexpr int GO = 8;
+            for (int b = 0; b < same; b += 32 * GO) {
+                int x[GO], y[GO];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < GO; ++u) {
                     const int k = b + u * 32 + lane;
                     x[u] = k < same ? own[k] : 0, y[u] = k < same ? other[k] : 0;
                 }
                 int mine = INT32_MAX;
 #pragma unroll
-                for (int u = 3; u >= 0; --u)
+                for (int u = GO - 1; u >= 0; --u)
                     if (x[u] != y[u]) mine = b + u * 32 + lane;
                 mine = __reduce_min_sync(0xffffffffu, mine);
                 if (mine < same) same = mine;   // ends the loop too
@@ -144,80 +145,41 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
 struct PrefixCall {
     KvAttend a;             // rows: the groups'
     const int4* shared;     // of each group: whose table, and the blocks [y, z)
+    const int2* cut;        // of each group: first piece, and pieces of each unit
+    int groups;             // of this launch
     float* part_o;          // units in one piece: [rows][heads][head_dim]
     float2* part_ml;
     float* slot_o;          // [block][rows of a block][head_dim] of units that are cut, and
     float2* slot_ml;        // [block][rows of a block]
-    int2* cut;              // [n_groups] first block and pieces of each unit of a group
-    int most;               // blocks that units may be cut for
 };
 
 // Which piece is block b's
 struct Piece {
     int id, head, row0, r0, rows;    // whose table; K/V head; the group's first row in the call; rows r0 .. r0 + rows - 1 of the group's
-    int block0, blocks;              // of 16 tokens
+    int block0, blocks;              // of 16 tokens; 0: there is no such piece
     bool cut;
     int halves;                      // of 64 tokens
 };
-struct PieceSpace {
-    int units[TA_SEQS], tiles[TA_SEQS];
-    Piece piece;
-};
-template <int ROWS> __device__ __forceinline__ void find_piece(const PrefixCall& p, PieceSpace& s) {
+template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall& p) {
     const KvAttend& a = p.a;
-    const int n = a.rows.n, kvh = a.c.kv_heads, lane = threadIdx.x & 31;
-    for (int g = threadIdx.x; g < n; g += blockDim.x) {
-        const int4 sh = p.shared[g];
-        const int rows = (a.rows.at(g + 1) - a.rows.at(g)) * a.group;
-        s.units[g] = sh.z > sh.y ? (rows + ROWS - 1) / ROWS * kvh : 0;
-        s.tiles[g] = (sh.z - sh.y + 7) / 8;
-    }
-    __syncthreads();
-    if (threadIdx.x >= 32) return;
-    // the least share of a block for which there are no more than `most` pieces; whole units where there are as many
-    int units = 0, longest = 0;
-    long long tiles = 0;
-    for (int g = lane; g < n; g += 32)
-        if (s.units[g]) units += s.units[g], longest = max(longest, s.tiles[g]), tiles += (long long)s.units[g] * s.tiles[g];
-    units = __reduce_add_sync(0xffffffffu, units), longest = __reduce_max_sync(0xffffffffu, longest);
-    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-    int share = units >= p.most ? longest : (int)min((long long)longest, max(2ll, (tiles + p.most - 1) / p.most));
-    while (share < longest) {
-        long long pieces = 0;
-        for (int g = lane; g < n; g += 32)
-            if (s.units[g]) pieces += (long long)s.units[g] * ((s.tiles[g] + share - 1) / share);
-        for (int d = 16; d; d >>= 1) pieces += __shfl_xor_sync(0xffffffffu, pieces, d);
-        if (pieces <= p.most) break;
-        share += share / 16 + 1;
-    }
-    long long before = 0;
-    if (lane == 0) s.piece.blocks = 0;
-    __syncwarp();
-    for (int g0 = 0; g0 < n; g0 += 32) {
-        const int g = g0 + lane, cuts = g < n && s.units[g] ? max((s.tiles[g] + share - 1) / max(share, 1), 1) : 0;
-        const long long mine = cuts ? (long long)s.units[g] * cuts : 0;
-        long long sum = mine;
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += u;
-        }
-        const long long first = before + sum - mine;
-        if (g < n && blockIdx.x == 0) p.cut[g] = make_int2((int)first, cuts);
-        if (cuts && blockIdx.x >= first && blockIdx.x < first + mine) {
-            const int in = (int)(blockIdx.x - first), unit = in / cuts, k = in - unit * cuts;
-            const int4 sh = p.shared[g];
-            const int t0 = (int)((long long)s.tiles[g] * k / cuts), t1 = (int)((long long)s.tiles[g] * (k + 1) / cuts);
-            Piece q;
-            q.id = sh.x, q.head = unit % kvh, q.row0 = a.rows.at(g), q.r0 = unit / kvh * ROWS;
-            q.rows = min(ROWS, (a.rows.at(g + 1) - q.row0) * a.group - q.r0);
-            q.block0 = sh.y + 8 * t0;
-            q.blocks = min(sh.y + 8 * t1, sh.z) - q.block0;
-            q.cut = cuts > 1;
-            q.halves = (q.blocks + 3) / 4;
-            s.piece = q;
-        }
-        before += __shfl_sync(0xffffffffu, sum, 31);
-    }
+    const int kvh = a.c.kv_heads, b = (int)blockIdx.x;
+    Piece q{};
+    const int first0 = __ldg(&p.cut[0].x);
+    const int g = warp_last_le(p.groups, (long long)b + first0, [&](int k) { return __ldg(&p.cut[k].x); });   // groups without pieces are before those with
+    const int2 cut = p.cut[g];
+    const int4 sh = p.shared[g];
+    const int row0 = a.rows.at(g), rows = (a.rows.at(g + 1) - row0) * a.group, tiles = (sh.z - sh.y + 7) / 8;
+    const int in = b + first0 - cut.x;
+    if (cut.y == 0 || in >= (rows + ROWS - 1) / ROWS * kvh * cut.y) return q;
+    const int unit = in / cut.y, k = in - unit * cut.y;
+    const int t0 = (int)((long long)tiles * k / cut.y), t1 = (int)((long long)tiles * (k + 1) / cut.y);
+    q.id = sh.x, q.head = unit % kvh, q.row0 = row0, q.r0 = unit / kvh * ROWS;
+    q.rows = min(ROWS, rows - q.r0);
+    q.block0 = sh.y + 8 * t0;
+    q.blocks = min(sh.y + 8 * t1, sh.z) - q.block0;
+    q.cut = cut.y > 1;
+    q.halves = (q.blocks + 3) / 4;
+    return q;
 }
 
 // The prompts' kernel has its tokens from L2, where other blocks' loads have brought them; here they come from memory, and a load
@@ -254,13 +216,8 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
     const KvAttend& a = p.a;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, D = a.c.head_dim;
-    PieceSpace* space = reinterpret_cast<PieceSpace*>(smem);    // before anything else is there
-    static_assert(sizeof(PieceSpace) <= S::OFF_SC, "");
     pdl_wait();
-    find_piece<ROWS>(p, *space);
-    __syncthreads();
-    const Piece w = space->piece;
-    __syncthreads();
+    const Piece w = find_piece<ROWS>(p);
     if (w.blocks == 0) {
         pdl_trigger();
         return;
@@ -709,84 +666,154 @@ template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, int 
 // The other tokens, and the shared ones of groups with few rows: units cut into pieces of even length (kv_piece_kernel).  One block looks
 // up every sequence's work and deals it out.
 // ---------------------------------------------------------------------------
+// What the join needs to know of a sequence
+struct __align__(16) KvJoin {
+    int own_cuts, own_slot;          // pieces of a unit of its own tokens, and its first slot where these are several
+    int common_cuts, common_slot;    // the same of the shared tokens
+    int common_row;                  // first row of its group
+    int named;                       // 0: the call may not name it, its rows are zero
+    int pad[2];
+};
 struct DealCall {
     KvAttend a;                // the whole call's, with skip
     const int4* shared;
-    const int32_t* group_rows;
+    const int32_t *group_rows, *group_of;
     KvEntry* entries;          // [n + n_groups]
     int32_t *first, *total;
-    int n_groups, most;        // groups whose shared tokens are dealt out too (0: another launch reads them); pieces to aim at
+    int2* cut;                 // [n_groups] kv_prefix_kernel's pieces: first, and of each unit
+    KvJoin* join;              // [n]
+    int n_groups, most;        // pieces to aim at
+    int prefix_rows;           // query rows of kv_prefix_kernel's units; 0: the groups are entries
+    int prefix_most;           // pieces that units may be cut for there; 0: none are cut
 };
 constexpr int DEAL_THREADS = 1024, LEAST_TILES = 8;
-__global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_constant__ DealCall p) {
+
+// One list of units dealt out: entry i has units(i) of tiles(i) tiles, of which each is cut into ceil(tiles / share) pieces; put(i, cuts,
+// pieces before, pieces of cut units before).  The share is that of `most` even pieces, at least `least`, or up to twice
+// as much where no more than `most` pieces come of it, which run at once (each begins with some us of dependent reads).  Returns the
+// pieces in all.  strict: no more than `most` pieces where units are cut at all.  A whole block calls it.
+template <class F, class G, class P> __device__ __forceinline__ int deal_out(int count, int most, int least, bool strict, F units, G tiles, P put) {
     __shared__ long long s_tiles[32];
-    __shared__ int s_pieces[32], s_slots[32];
-    pdl_trigger();
-    pdl_wait();
-    const KvAttend& a = p.a;
-    const int n = a.rows.n, count = n + p.n_groups, t = threadIdx.x, lane = t & 31, warp = t >> 5, kvh = a.c.kv_heads;
-    auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
-    long long tiles = 0;
-    for (int i = t; i < count; i += DEAL_THREADS) {
-        KvEntry e;
-        if (i < n) {
-            e.s = seq_work(a, i);
-        } else {
-            const int g = i - n;
-            const int4 sh = p.shared[g];
-            e.s = SeqWork{sh.x, sh.z * KV_BLOCK, p.group_rows[g + 1] - p.group_rows[g], p.group_rows[g], sh.y, 0, sh.z - sh.y, 0, 0, true};
-        }
-        tiles += (long long)units_of(e.s) * e.s.tiles;
-        p.entries[i].s = e.s;
-    }
-    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-    if (lane == 0) s_tiles[warp] = tiles;
+    __shared__ int s_tries[32], s_pieces[32], s_slots[32];
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    long long all = 0;
+    for (int i = t; i < count; i += DEAL_THREADS) all += (long long)units(i) * tiles(i);
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
     __syncthreads();
-    tiles = s_tiles[lane];
-    for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(0xffffffffu, tiles, d);
-    // Pieces of `share` tiles: `most` of them and one more for each unit at the most, twice `most` of units that are cut.
-    const long long share = max((long long)LEAST_TILES, (tiles + p.most - 1) / p.most);
-    int pieces = 0, slots = 0;   // before this round's entries
+    if (lane == 0) s_tiles[warp] = all;
+    if (t < 32) s_tries[t] = 0;
+    __syncthreads();
+    all = s_tiles[lane];
+    for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+    // lane k tries 1 + k / 32 of the least share
+    const long long base = max((long long)least, (all + max(most, 1) - 1) / max(most, 1)), mine = base + base * lane / 32;
+    int pieces = 0;
+    for (int i = warp; i < count; i += 32) {
+        const int u = units(i);
+        if (u) pieces += u * (int)((tiles(i) + mine - 1) / mine);
+    }
+    atomicAdd(&s_tries[lane], pieces);
+    __syncthreads();
+    const uint32_t fit = __ballot_sync(0xffffffffu, s_tries[lane] <= most);
+    const long long share = __shfl_sync(0xffffffffu, mine, fit ? __ffs(fit) - 1 : 0);
+    pieces = 0;
+    int slots = 0;   // before this round's entries
     for (int i0 = 0; i0 < count; i0 += DEAL_THREADS) {
-        const int i = i0 + t;
-        int units = 0, cuts = 0;
-        if (i < count) {
-            units = units_of(p.entries[i].s);
-            if (units) cuts = (int)((p.entries[i].s.tiles + share - 1) / share);
-        }
-        const int mine = units * cuts, held = cuts > 1 ? mine : 0;
-        int x = mine, y = held;
+        const int i = i0 + t, u = i < count ? units(i) : 0, cuts = u ? fit || !strict ? (int)((tiles(i) + share - 1) / share) : 1 : 0;
+        const int n = u * cuts, held = cuts > 1 ? n : 0;
+        int x = n, y = held;
         for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, x, d), v = __shfl_up_sync(0xffffffffu, y, d);
-            if (lane >= d) x += u, y += v;
+            const int v = __shfl_up_sync(0xffffffffu, x, d), w = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) x += v, y += w;
         }
         if (lane == 31) s_pieces[warp] = x, s_slots[warp] = y;
         __syncthreads();
-        int all_x = 0, all_y = 0;
-        for (int w = 0; w < DEAL_THREADS / 32; ++w) {
-            if (w == warp) x += all_x, y += all_y;
-            all_x += s_pieces[w], all_y += s_slots[w];
+        int bx = s_pieces[lane], by = s_slots[lane];
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, bx, d), w = __shfl_up_sync(0xffffffffu, by, d);
+            if (lane >= d) bx += v, by += w;
         }
-        if (i < count) {
-            p.entries[i].cuts = cuts, p.entries[i].first = pieces + x - mine, p.entries[i].slot = slots + y - held;
-            p.first[i] = pieces + x - mine;
-        }
+        const int all_x = __shfl_sync(0xffffffffu, bx, 31), all_y = __shfl_sync(0xffffffffu, by, 31);
+        const int px = __shfl_sync(0xffffffffu, bx, (warp + 31) & 31), py = __shfl_sync(0xffffffffu, by, (warp + 31) & 31);
+        if (warp) x += px, y += py;
+        if (i < count) put(i, cuts, pieces + x - n, slots + y - held);
         pieces += all_x, slots += all_y;
         __syncthreads();
     }
+    return pieces;
+}
+
+__global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_constant__ DealCall p) {
+    __shared__ int s_units[DEAL_THREADS], s_tiles[DEAL_THREADS], s_cut[2][DEAL_THREADS];   // of the first entries, or groups
+    pdl_trigger();
+    pdl_wait();
+    const KvAttend& a = p.a;
+    const int n = a.rows.n, groups = p.n_groups, count = n + (p.prefix_rows ? 0 : groups), t = threadIdx.x, kvh = a.c.kv_heads;
+    auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
+    for (int i = t; i < count; i += DEAL_THREADS) {
+        SeqWork s;
+        if (i < n) {
+            s = seq_work(a, i);
+            p.join[i].named = s.id >= 0 && s.id < a.c.max_seqs && s.m <= a.max_new;
+        } else {
+            const int4 sh = p.shared[i - n];
+            const int row0 = p.group_rows[i - n];
+            s = SeqWork{sh.x, sh.z * KV_BLOCK, p.group_rows[i - n + 1] - row0, row0, sh.y, 0, sh.z - sh.y, 0, 0, true};
+        }
+        p.entries[i].s = s;
+        if (i < DEAL_THREADS) s_units[i] = units_of(s), s_tiles[i] = s.tiles;
+    }
+    __syncthreads();
+    const int pieces = deal_out(
+        count, p.most, LEAST_TILES, false, [&](int i) { return i < DEAL_THREADS ? s_units[i] : units_of(p.entries[i].s); },
+        [&](int i) { return i < DEAL_THREADS ? s_tiles[i] : p.entries[i].s.tiles; },
+        [&](int i, int cuts, int first, int slot) {
+            KvEntry& e = p.entries[i];
+            e.cuts = cuts, e.first = first, e.slot = slot, p.first[i] = first;
+            if (i < n) p.join[i].own_cuts = cuts, p.join[i].own_slot = slot;
+            else if (i - n < DEAL_THREADS) s_cut[0][i - n] = cuts, s_cut[1][i - n] = slot;
+        });
     if (t == 0) *p.total = pieces;
+    if (p.prefix_rows) {
+        auto group_units = [&](int g) {
+            const int4 sh = p.shared[g];
+            return sh.z > sh.y ? ((p.group_rows[g + 1] - p.group_rows[g]) * a.group + p.prefix_rows - 1) / p.prefix_rows * kvh : 0;
+        };
+        auto group_tiles = [&](int g) { return (p.shared[g].z - p.shared[g].y + 7) / 8; };
+        __syncthreads();
+        for (int g = t; g < min(groups, DEAL_THREADS); g += DEAL_THREADS) s_units[g] = group_units(g), s_tiles[g] = group_tiles(g);
+        __syncthreads();
+        deal_out(
+            groups, p.prefix_most, 2, true, [&](int g) { return g < DEAL_THREADS ? s_units[g] : group_units(g); },
+            [&](int g) { return g < DEAL_THREADS ? s_tiles[g] : group_tiles(g); },
+            [&](int g, int cuts, int first, int) {
+                p.cut[g] = make_int2(first, cuts);
+                if (g < DEAL_THREADS) s_cut[0][g] = cuts, s_cut[1][g] = first;
+            });
+    }
+    __syncthreads();   // what the block has written to memory is read back below
+    for (int i = t; i < n; i += DEAL_THREADS) {
+        const int2 skip = a.skip[i];
+        KvJoin& j = p.join[i];
+        int cuts = 0, slot = 0, row = 0;
+        if (skip.y > skip.x) {
+            const int g = p.group_of[i];
+            row = p.group_rows[g];
+            if (g < DEAL_THREADS) cuts = s_cut[0][g], slot = s_cut[1][g];
+            else if (p.prefix_rows) cuts = p.cut[g].y, slot = p.cut[g].x;
+            else cuts = p.entries[n + g].cuts, slot = p.entries[n + g].slot;
+        }
+        j.common_cuts = cuts, j.common_slot = slot, j.common_row = row;
+    }
 }
 
 // The parts of a group's shared tokens and of the sequence's own become the result: a team of warps for each row and head, which take the
 // parts in turn.  One warp is enough where rows fill the card; 57 parts of few rows took one 15 us.
 struct JoinCall {
     KvAttend a;
-    const int2* skip;
-    const int32_t *group_of, *group_rows;
-    const KvEntry* entries;
+    const KvJoin* join;        // [n]
     KvPieces pieces;           // where the parts of entries are
-    const int2* cut;           // kv_prefix_kernel's cuts of the shared tokens, or null: they are entries
-    const float* slot_o;       // and its pieces
+    const float* slot_o;       // kv_prefix_kernel's pieces, or null: the groups are entries
     const float2* slot_ml;
     int block_rows;            // rows of its units
     int team;                  // warps: 1, 2, 4 or 8
@@ -810,18 +837,10 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
     if (i < 0) return;
     const int r0 = a.rows.at(i), r1 = a.rows.at(i + 1);
     if (row < r0 || row >= r1 || r0 < 0 || r1 > a.rows.rows) return;   // no sequence's, or of one whose rows pass the end
-    const int id = a.ids[i];
-    const bool named = id >= 0 && id < a.c.max_seqs && r1 - r0 <= a.max_new;
-    const int2 skip = p.skip[i];
-    const int g = named && skip.y > skip.x ? p.group_of[i] : -1;
+    const KvJoin j = p.join[i];
     // (pieces of a unit, first slot) of the own and of the shared tokens
-    const int2 own = named ? make_int2(p.entries[i].cuts, p.entries[i].slot) : make_int2(0, 0);
-    int2 common = make_int2(0, 0);
-    if (g >= 0) {
-        if (p.cut) common = make_int2(p.cut[g].y, p.cut[g].x);
-        else common = make_int2(p.entries[a.rows.n + g].cuts, p.entries[a.rows.n + g].slot);
-    }
-    const int in_group = g >= 0 ? row - p.group_rows[g] : 0;
+    const int2 own = make_int2(j.named ? j.own_cuts : 0, j.own_slot), common = make_int2(j.named ? j.common_cuts : 0, j.common_slot);
+    const int in_group = row - j.common_row;
     const int heads = JOIN_WARPS / team;   // of the block at a time
     for (int h0 = blockIdx.y * heads; h0 < a.heads; h0 += gridDim.y * heads) {
         const int h = min(h0 + warp / team, a.heads - 1);   // the last one more than once, alike
@@ -834,8 +853,8 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
         };
         const PartList lists[2] = {
             list(own, p.pieces.o0, p.pieces.ml0, (row - r0) * a.group + hh, 16, p.pieces.slot_o, p.pieces.slot_ml),
-            list(common, p.pieces.o1, p.pieces.ml1, in_group * a.group + hh, p.cut ? p.block_rows : 16, p.cut ? p.slot_o : p.pieces.slot_o,
-                 p.cut ? p.slot_ml : p.pieces.slot_ml)};
+            list(common, p.pieces.o1, p.pieces.ml1, in_group * a.group + hh, p.slot_o ? p.block_rows : 16, p.slot_o ? p.slot_o : p.pieces.slot_o,
+                 p.slot_o ? p.slot_ml : p.pieces.slot_ml)};
         float top = -INFINITY;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -917,7 +936,7 @@ size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 
 // Where things lie in the workspace.
 struct Space {
-    size_t skip, group_of, shared, group_rows, cut, entries, first, total, ml0, ml1, slot_ml, prefix_ml, o0, o1, slot_o, prefix_o, bytes;
+    size_t skip, group_of, shared, group_rows, cut, join, entries, first, total, ml0, ml1, slot_ml, prefix_ml, o0, o1, slot_o, prefix_o, bytes;
 };
 Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms) {
     Space s;
@@ -931,6 +950,7 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
     const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim, true) * 16, prefix = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
     s.skip = take((size_t)n * 8), s.group_of = take((size_t)n * 4), s.shared = take((size_t)n_groups * 16);
     s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 8);
+    s.join = take((size_t)n * sizeof(KvJoin));
     s.entries = take(((size_t)n + n_groups) * sizeof(KvEntry)), s.first = take(((size_t)n + n_groups) * 4), s.total = take(4);
     s.ml0 = take(units * 8), s.ml1 = take(units * 8), s.slot_ml = take(slots * 8), s.prefix_ml = take(prefix * 8);
     s.o0 = take(units * D * 4), s.o1 = take(units * D * 4), s.slot_o = take(slots * D * 4), s.prefix_o = take(prefix * D * 4);
@@ -962,22 +982,23 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     a.skip = plan.skip;
     const bool low = (long long)call.max_new * call.group <= 8 && (prefix || (long long)rows * call.group <= 8);
     const int most = sms * piece_blocks(c.head_dim, low), dealt = prefix ? 0 : n_groups;
-    const DealCall deal{a,     plan.shared, plan.group_rows, static_cast<KvEntry*>(place(at.entries)), static_cast<int32_t*>(place(at.first)),
-                        static_cast<int32_t*>(place(at.total)), dealt, most};
+    const int tiles = prefix_tiles(call, dtype, n_groups), block = tiles * PT_ROWS;
+    // Units of kv_prefix_kernel may be cut where one launch has all groups: the slots are the blocks'.
+    const DealCall deal{a, plan.shared, plan.group_rows, plan.group_of, static_cast<KvEntry*>(place(at.entries)),
+                        static_cast<int32_t*>(place(at.first)), static_cast<int32_t*>(place(at.total)), static_cast<int2*>(place(at.cut)),
+                        static_cast<KvJoin*>(place(at.join)), n_groups, most, prefix ? block : 0, n_groups <= TA_SEQS ? sms : 0};
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
     const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
-    const int tiles = prefix_tiles(call, dtype, n_groups), block = tiles * PT_ROWS;
     for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
         KvAttend b = call;
         b.rows = {plan.group_rows + g0, 0, std::min(n_groups - g0, TA_SEQS), rows};
         b.ids = nullptr;
-        // Units may be cut where one launch has all groups: the slots are the blocks'.
-        const PrefixCall p{b, plan.shared + g0, pieces.o1, pieces.ml1, static_cast<float*>(place(at.prefix_o)),
-                           static_cast<float2*>(place(at.prefix_ml)), static_cast<int2*>(place(at.cut)) + g0, n_groups <= TA_SEQS ? sms : 0};
+        const PrefixCall p{b, plan.shared + g0, deal.cut + g0, b.rows.n, pieces.o1, pieces.ml1, static_cast<float*>(place(at.prefix_o)),
+                           static_cast<float2*>(place(at.prefix_ml))};
         const long long units = ((long long)rows * call.group / block + b.rows.n) * c.kv_heads;
         const unsigned blocks = (unsigned)std::max<long long>(units, sms);
         if (c.code == CAC_KV8_INT8)
@@ -994,9 +1015,8 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     if (e != cudaSuccess) return e;
 
     const long long results = (long long)rows * call.heads;
-    const int team = results > 8 * sms ? 1 : results > 4 * sms ? 2 : results > 2 * sms ? 4 : 8;
-    const JoinCall join{call, plan.skip, plan.group_of, plan.group_rows, deal.entries, pieces,
-                        prefix ? static_cast<const int2*>(place(at.cut)) : nullptr, static_cast<const float*>(place(at.prefix_o)),
+    const int team = results > 16 * sms ? 1 : results > 8 * sms ? 2 : results > 4 * sms ? 4 : 8;
+    const JoinCall join{call, deal.join, pieces, prefix ? static_cast<const float*>(place(at.prefix_o)) : nullptr,
                         static_cast<const float2*>(place(at.prefix_ml)), block, team};
     const dim3 grid(rows, std::min((call.heads * team + JOIN_WARPS - 1) / JOIN_WARPS, 64));
     return dtype == CAC_DTYPE_BF16 ? launch_k(kv_join_shared_kernel<bf16>, grid, dim3(JOIN_WARPS * 32), 0, s, 1, join)
