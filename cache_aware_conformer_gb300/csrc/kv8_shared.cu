@@ -651,9 +651,11 @@ template <class T, int CODE, int HDP, int TILES> cudaError_t launch_prefix(const
     }
     return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::XSMEM, s, 1, p);
 }
-// Row tiles of a block: one for groups of 128 rows and fewer on average, which leaves room for more copies ahead.
+// Row tiles of a block: one, which leaves room for more copies ahead, for a group of 128 rows, or several of half as many on average (a larger
+// one among them has its tokens read once more for each 128 of its rows).
 int prefix_tiles(const KvAttend& a, int dtype, int n_groups) {
-    return (dtype == CAC_DTYPE_F32 && a.c.head_dim > 64) || (long long)a.rows.rows * a.group <= (long long)PT_ROWS * n_groups ? 1 : 2;
+    const long long rows = (long long)a.rows.rows * a.group;
+    return (dtype == CAC_DTYPE_F32 && a.c.head_dim > 64) || rows <= (n_groups == 1 ? PT_ROWS : PT_ROWS / 2 * (long long)n_groups) ? 1 : 2;
 }
 template <class T, int CODE> cudaError_t launch_prefix(const PrefixCall& p, int tiles, unsigned blocks, cudaStream_t s) {
     if (p.a.c.head_dim <= 64) return tiles == 1 ? launch_prefix<T, CODE, 64, 1>(p, blocks, s) : launch_prefix<T, CODE, 64, 2>(p, blocks, s);
@@ -826,7 +828,7 @@ struct PartList {
     int step, count;
 };
 constexpr int JOIN_WARPS = 8;
-template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
+template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
     pdl_trigger();
     pdl_wait();
     __shared__ __align__(16) float s_o[JOIN_WARPS][256];
@@ -876,19 +878,23 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32) kv_join_sh
                     l += move_norm(y.y, y.x - base, f);
                 }
                 const int n = min(32, (x.count - k0 + team - 1) / team);
-#pragma unroll 8
-                for (int j = 0; j < n; ++j) {
-                    const float w = __shfl_sync(0xffffffffu, f, j);
-                    const float* src = x.o + (x.at + (long long)(k0 + j * team) * x.step) * D;
+                constexpr int GO = 2;   // loads on their way at once: each takes a microsecond
+                for (int j0 = 0; j0 < n; j0 += GO)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
                         const int e = b ? e1 : e0;
-                        if (e < D) {
-                            const float4 v = *reinterpret_cast<const float4*>(src + e);
-                            o[b].x = fmaf(v.x, w, o[b].x), o[b].y = fmaf(v.y, w, o[b].y), o[b].z = fmaf(v.z, w, o[b].z), o[b].w = fmaf(v.w, w, o[b].w);
+                        if (b && D <= 128) break;
+                        float4 v[GO];
+#pragma unroll
+                        for (int j = 0; j < GO; ++j)
+                            v[j] = j0 + j < n && e < D ? *reinterpret_cast<const float4*>(x.o + (x.at + (long long)(k0 + (j0 + j) * team) * x.step) * D + e)
+                                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int j = 0; j < GO; ++j) {
+                            const float w = __shfl_sync(0xffffffffu, f, j0 + j);   // 0 past the last
+                            o[b].x = fmaf(v[j].x, w, o[b].x), o[b].y = fmaf(v[j].y, w, o[b].y), o[b].z = fmaf(v[j].z, w, o[b].z), o[b].w = fmaf(v[j].w, w, o[b].w);
                         }
                     }
-                }
             }
         }
 #pragma unroll
