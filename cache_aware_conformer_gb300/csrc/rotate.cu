@@ -18,13 +18,16 @@
 namespace cac {
 namespace {
 
-constexpr int ROT_THREADS = 256, ROT_ROWS = 8;   // of a block at most
+constexpr int ROT_THREADS = 128, ROT_ROWS = 32;   // of a block at most
 
+// queries or keys: blocks of their own, which have the rows and heads that keep their threads busy
 struct RotSide {
     const void* in;
     void* out;
     long long in_stride, out_stride;
     const float* gain;
+    int heads, block_rows, blocks;
+    uint32_t heads_mul;                // 2^32 / heads, rounded down, + 1
 };
 struct RotArgs {
     RotSide q, k;
@@ -33,10 +36,9 @@ struct RotArgs {
     KvRows seqs;                       // the rows' sequences there
     const int32_t *ids, *lens;
     int* status;
-    int max_seqs, rows, heads, all;    // query heads; with the key heads
+    int max_seqs, rows;
     int head_dim, rot, lanes_log2;     // lanes of a head, a power of two
-    int block_rows;
-    float amplitude, eps;
+    float amplitude, eps, inv_dim;     // 1 / head_dim
 };
 
 enum { HALF_PIECES, PAIRS, HALF_ANY };
@@ -113,17 +115,21 @@ __device__ __forceinline__ float group_sum(float x, int log2) {
 }
 
 template <class T, int HOW>
-__global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_constant__ RotArgs a) {
+__global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_constant__ RotArgs a) {
     constexpr int N = Piece<T>::N;
-    extern __shared__ __align__(16) float2 s_turn[];   // [block_rows][rot / 2], then the exchange
+    extern __shared__ __align__(16) float2 s_turn[];   // [block_rows][turns of a row], then the exchange
     __shared__ int s_pos[ROT_ROWS], s_there[ROT_ROWS];
     pdl_trigger();
     pdl_wait();
+    const bool keys = (int)blockIdx.x >= a.q.blocks;
+    const RotSide s = keys ? a.k : a.q;
     const int D = a.head_dim, R = a.rot, half = R >> 1, pieces = D / N;
-    const int row0 = blockIdx.x * a.block_rows, rows = min(a.block_rows, a.rows - row0);
+    const int row0 = ((int)blockIdx.x - (keys ? a.q.blocks : 0)) * s.block_rows, rows = min(s.block_rows, a.rows - row0);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int l = threadIdx.x & ((1 << a.lanes_log2) - 1);           // the thread's place in its head's group
-    const int stride = (int)(gridDim.y * blockDim.x) >> a.lanes_log2, units = rows * a.all;
+    const int stride = (int)(gridDim.y * blockDim.x) >> a.lanes_log2, units = rows * s.heads;   // units: a row's head
+    const int rounds = (units - ((int)(blockIdx.y * blockDim.x + warp * 32) >> a.lanes_log2) + stride - 1) / stride;
+    if ((int)(blockIdx.y * blockDim.x) >> a.lanes_log2 >= units) return;
 
     // the thread's two pieces
     int c0, c1;
@@ -137,15 +143,19 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
         c0 = 2 * l, c1 = 2 * l + 1;
     }
     const bool mine = c0 < pieces;
+    // A thread's own pairs are N in a row, l N and on: two of them to 16 bytes, neighbours' next to each other
+    const int owners = (half + N - 1) / N, row_turns = HOW == HALF_ANY ? half : owners * N;
+    auto turn_at = [&](int i) { return HOW == HALF_ANY ? i : ((i % N >> 1) * owners + i / N) * 2 + (i & 1); };
 
-    auto side = [&](int head) -> const RotSide& { return head < a.heads ? a.q : a.k; };
-    auto offset = [&](int head) { return (head < a.heads ? head : head - a.heads) * D; };
+    auto row_of = [&](int u) {   // u / heads: units of a block are below 2^21, where the product is the quotient or one more
+        const int r = s.heads == 1 ? u : (int)__umulhi((uint32_t)u, s.heads_mul);
+        return r - (r * s.heads > u);
+    };
     uint4 in[2] = {};
     auto load = [&](int u) {
         if (u < units && mine) {
-            const int r = u / a.all, head = u - r * a.all;
-            const RotSide& s = side(head);
-            const T* src = static_cast<const T*>(s.in) + (long long)(row0 + r) * s.in_stride + offset(head);
+            const int r = row_of(u);
+            const T* src = static_cast<const T*>(s.in) + (long long)(row0 + r) * s.in_stride + (u - r * s.heads) * D;
             in[0] = *reinterpret_cast<const uint4*>(src + c0 * N);
             in[1] = *reinterpret_cast<const uint4*>(src + c1 * N);
         }
@@ -160,23 +170,27 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
     }
     __syncthreads();
     for (int e = threadIdx.x; e < rows * half; e += blockDim.x) {
-        const int r = e / half;
-        s_turn[e] = turn(s_pos[r], a.steps[e - r * half], a.amplitude);
+        const int r = e / half, i = e - r * half;
+        s_turn[r * row_turns + turn_at(i)] = turn(s_pos[r], a.steps[i], a.amplitude);
     }
+    float gain[2][N];
+    if (s.gain && mine)
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int j = 0; j < N; ++j) gain[b][j] = __ldg(s.gain + (b ? c1 : c0) * N + j);
     __syncthreads();
 
     // whole warps go round together: the groups' sums are shuffles
-    const int rounds = (units - ((int)(blockIdx.y * blockDim.x + warp * 32) >> a.lanes_log2) + stride - 1) / stride;
     for (int k = 0; k < rounds; ++k, u += stride) {
         const bool on = u < units && mine;
-        const int r = on ? u / a.all : 0, head = on ? u - r * a.all : 0;
-        const RotSide& s = side(head);
+        const int r = on ? row_of(u) : 0, head = on ? u - r * s.heads : 0;
         float x[2][N];
         unpack<T>(in[0], x[0]);
         unpack<T>(in[1], x[1]);
         const bool store = on && s_there[r];
         load(u + stride);
-        if (a.q.gain || a.k.gain) {
+        if (s.gain) {
             float sum = 0.f;
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -192,52 +206,25 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        if (huge && s.gain) x[b][j] *= 8.271806125530277e-25f;
+                        if (huge) x[b][j] *= 8.271806125530277e-25f;
                         again = fmaf(x[b][j], x[b][j], again);
                     }
                 again = group_sum(on ? again : 0.f, a.lanes_log2);
                 if (huge) sum = again, eps = 0.f;
             }
-            if (s.gain && on) {
-                const float inv = 1.f / sqrtf(sum / (float)D + eps);
+            // the approximate root (2 units in the last place) and one step of Newton's method
+            const float mean = sum * a.inv_dim + eps, y = rsqrtf(mean), inv = fmaf(y, 0.5f * fmaf(-mean * y, y, 1.f), y);
+            if (mine)
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float4* g = reinterpret_cast<const float4*>(s.gain + (b ? c1 : c0) * N);
+                for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int j = 0; j < N; j += 4) {
-                        const float4 v = __ldg(g + j / 4);
-                        x[b][j] *= inv * v.x, x[b][j + 1] *= inv * v.y, x[b][j + 2] *= inv * v.z, x[b][j + 3] *= inv * v.w;
-                    }
-                }
-            }
+                    for (int j = 0; j < N; ++j) x[b][j] *= inv * gain[b][j];
         }
-        const float2* t = s_turn + r * half;
-        if constexpr (HOW == HALF_PIECES) {
-            if (turned) {
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float2 cs = t[c0 * N + j];
-                    const float p = x[0][j], q = x[1][j];
-                    x[0][j] = p * cs.x - q * cs.y;
-                    x[1][j] = p * cs.y + q * cs.x;
-                }
-            }
-        } else if constexpr (HOW == PAIRS) {
-#pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int j = 0; j < N; j += 2) {
-                    const int e = (b ? c1 : c0) * N + j;
-                    if (e < R) {
-                        const float2 cs = t[e >> 1];
-                        const float p = x[b][j], q = x[b][j + 1];
-                        x[b][j] = p * cs.x - q * cs.y;
-                        x[b][j + 1] = p * cs.y + q * cs.x;
-                    }
-                }
-        } else {
+        const float2* t = s_turn + r * row_turns;
+        if constexpr (HOW == HALF_ANY) {
             // the head's values in shared memory, a group's own piece of it
-            float* ex = reinterpret_cast<float*>(s_turn + ((a.block_rows * half + 1) & ~1)) + (threadIdx.x >> a.lanes_log2) * (2 * N << a.lanes_log2);
+            float* ex = reinterpret_cast<float*>(s_turn + ((s.block_rows * row_turns + 1) & ~1)) +
+                        (threadIdx.x >> a.lanes_log2) * (2 * N << a.lanes_log2);
             __syncwarp();
             if (on)
 #pragma unroll
@@ -259,9 +246,30 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
                             x[b][j] = ex[e - half] * cs.y + x[b][j] * cs.x;
                         }
                     }
+        } else if (HOW == HALF_PIECES ? turned : l < owners) {
+            const float4* own = reinterpret_cast<const float4*>(t) + l;
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const float4 cs = own[j / 2 * owners];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float c = b ? cs.z : cs.x, sn = b ? cs.w : cs.y;
+                    const int i = j + b;
+                    if constexpr (HOW == HALF_PIECES) {
+                        const float p = x[0][i], q = x[1][i];
+                        x[0][i] = p * c - q * sn;
+                        x[1][i] = p * sn + q * c;
+                    } else if (l * N + i < half) {
+                        float &p = x[i / (N / 2)][2 * i % N], &q = x[i / (N / 2)][2 * i % N + 1];
+                        const float was = p;
+                        p = was * c - q * sn;
+                        q = was * sn + q * c;
+                    }
+                }
+            }
         }
         if (store) {
-            T* dst = static_cast<T*>(s.out) + (long long)(row0 + r) * s.out_stride + offset(head);
+            T* dst = static_cast<T*>(s.out) + (long long)(row0 + r) * s.out_stride + head * D;
             *reinterpret_cast<uint4*>(dst + c0 * N) = pack<T>(x[0]);
             *reinterpret_cast<uint4*>(dst + c1 * N) = pack<T>(x[1]);
         }
@@ -270,30 +278,42 @@ __global__ void __launch_bounds__(ROT_THREADS) rotate_kernel(const __grid_consta
 
 template <class T> cudaError_t launch_rotate(const RotArgs& a, int layout, dim3 grid, int threads, cudaStream_t s) {
     constexpr int N = Piece<T>::N;
-    const int half = a.rot / 2;
-    const size_t turns = (size_t)((a.block_rows * half + 1) & ~1) * 8;
+    const int half = a.rot / 2, rows = std::max(a.q.block_rows, a.k.block_rows);
+    const size_t turns = (size_t)rows * ((half + N - 1) / N * N) * 8;
     if (layout == CAC_ROTARY_PAIRS) return launch_k(rotate_kernel<T, PAIRS>, grid, dim3(threads), turns, s, 1, a);
     if (half % N == 0) return launch_k(rotate_kernel<T, HALF_PIECES>, grid, dim3(threads), turns, s, 1, a);
     return launch_k(rotate_kernel<T, HALF_ANY>, grid, dim3(threads), turns + (size_t)threads * 2 * N * 4, s, 1, a);
 }
 
-int rotate(const cac_rotary* r, RotArgs& a, int kv_heads, void* stream) {
-    const int D = r->head_dim;
-    const int pieces = D / (r->dtype == CAC_DTYPE_BF16 ? 8 : 4);     // even: D is a multiple of 16
+int rotate(const cac_rotary* r, RotArgs& a, int heads, int kv_heads, void* stream) {
+    if (a.rows >= 1 << 30) return CAC_E_LIMIT;   // blocks of both sides are counted in 31 bits
+    const int D = r->head_dim, N = r->dtype == CAC_DTYPE_BF16 ? 8 : 4;
     a.steps = r->steps;
     a.q.gain = r->q_gain, a.k.gain = r->k_gain;
-    a.all = a.heads + kv_heads;
     a.head_dim = D, a.rot = r->rot_dim;
-    a.amplitude = r->amplitude, a.eps = r->eps;
+    a.amplitude = r->amplitude, a.eps = r->eps, a.inv_dim = 1.f / (float)D;
     a.lanes_log2 = 0;
-    while (2 << a.lanes_log2 < pieces) ++a.lanes_log2;
-    // A block has up to 8 rows, since it begins with 4 us of dependent reads and sines (3 rows of 40 heads: 117 us for 22,000 rows), but
-    // not so many that SMs stay empty; the heads of few rows are dealt out over several blocks.
-    const long long items = (long long)a.all << a.lanes_log2;        // threads' work of a row
-    a.block_rows = std::max(1, std::min(ROT_ROWS, a.rows / (152 * 4)));
-    const long long most = items * a.block_rows;
-    const int threads = (int)std::min<long long>(ROT_THREADS, (most + 31) / 32 * 32);
-    const unsigned blocks = (unsigned)((a.rows + a.block_rows - 1) / a.block_rows);
+    while (2 << a.lanes_log2 < D / N) ++a.lanes_log2;                // an even number of pieces: D is a multiple of 16
+    // A block has rows enough for some rounds of its threads, since it begins with 4 us of dependent reads and sines (three rows of 40
+    // heads: 117 us for 22,000 rows), but not so many that SMs stay empty, and no more than 36 KB of sines; the heads of few rows are dealt
+    // out over several blocks.
+    const int room = std::max(1, std::min(ROT_ROWS, 36 * 1024 / std::max((a.rot / 2 + N) * 8, 1)));
+    int threads = 32;
+    long long most = 0;
+    for (RotSide* s : {&a.q, &a.k}) {
+        s->heads = s == &a.q ? heads : kv_heads;
+        s->heads_mul = s->heads > 1 ? (uint32_t)((1ull << 32) / s->heads) + 1 : 0u;
+        const long long items = (long long)s->heads << a.lanes_log2; // threads' work of a row
+        if (items == 0) {
+            s->block_rows = 1, s->blocks = 0;
+            continue;
+        }
+        s->block_rows = (int)std::max(1ll, std::min({(long long)room, a.rows / (152ll * 4), (10ll * ROT_THREADS + items - 1) / items}));
+        s->blocks = (a.rows + s->block_rows - 1) / s->block_rows;
+        most = std::max(most, items * s->block_rows);
+        threads = std::max(threads, (int)std::min<long long>(ROT_THREADS, (items * s->block_rows + 31) / 32 * 32));
+    }
+    const unsigned blocks = (unsigned)a.q.blocks + (unsigned)a.k.blocks;
     const unsigned split = blocks >= 152 * 2 ? 1u : (unsigned)((most + threads - 1) / threads);
     DeviceScope dev(r->device);
     if (!dev.ok) return CAC_E_CUDA;
@@ -359,15 +379,15 @@ extern "C" int cac_op_rotate(const cac_rotary* r, int rows, const int32_t* posit
                              long long k_stride, void* k_out, long long k_out_stride, void* stream) {
     int e = check(r);
     if (e != CAC_OK) return e;
-    if (rows < 0 || heads < 0 || kv_heads < 0 || heads + (long long)kv_heads > 65535 || (rows > 0 && !positions)) return CAC_E_INVAL;
+    if (rows < 0 || heads < 0 || kv_heads < 0 || heads > 65535 || kv_heads > 65535 || (rows > 0 && !positions)) return CAC_E_INVAL;
     if (reinterpret_cast<uintptr_t>(positions) & 3) return CAC_E_ALIGN;
     RotArgs a{};
-    a.q = {q, q_out, q_stride, q_out_stride, nullptr}, a.k = {k, k_out, k_stride, k_out_stride, nullptr};
+    a.q = {q, q_out, q_stride, q_out_stride}, a.k = {k, k_out, k_stride, k_out_stride};
     if (rows == 0 || heads + kv_heads == 0) return CAC_OK;
     if ((e = check(r, heads, a.q)) != CAC_OK || (e = check(r, kv_heads, a.k)) != CAC_OK) return e;
     a.positions = positions;
-    a.rows = rows, a.heads = heads;
-    return rotate(r, a, kv_heads, stream);
+    a.rows = rows;
+    return rotate(r, a, heads, kv_heads, stream);
 }
 
 extern "C" int cac_kv8_rotate(const cac_kv8* c, const cac_rotary* r, int n, const int32_t* ids, const int32_t* starts, int rows,
@@ -377,15 +397,15 @@ extern "C" int cac_kv8_rotate(const cac_kv8* c, const cac_rotary* r, int n, cons
     if (e != CAC_OK || (e = check(r)) != CAC_OK) return e;
     if (n < 0 || (n > 0 && !ids) || rows < 0 || heads < 0 || r->head_dim != c->head_dim || r->device != c->device) return CAC_E_INVAL;
     const int kv_heads = k || k_out ? c->kv_heads : 0;
-    if (heads + (long long)kv_heads > 65535) return CAC_E_INVAL;
+    if (heads > 65535) return CAC_E_INVAL;
     if ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(starts)) & 3) return CAC_E_ALIGN;
     if (n == 0 || rows == 0 || heads + kv_heads == 0) return CAC_OK;
     if (!starts && rows % n) return CAC_E_INVAL;
     RotArgs a{};
-    a.q = {q, q_out, q_stride, q_out_stride, nullptr}, a.k = {k, k_out, k_stride, k_out_stride, nullptr};
+    a.q = {q, q_out, q_stride, q_out_stride}, a.k = {k, k_out, k_stride, k_out_stride};
     if ((e = check(r, heads, a.q)) != CAC_OK || (e = check(r, kv_heads, a.k)) != CAC_OK) return e;
     a.seqs = {starts, rows / n, n, rows};
     a.ids = ids, a.lens = c->lens, a.status = c->status, a.max_seqs = c->max_seqs;
-    a.rows = rows, a.heads = heads;
-    return rotate(r, a, kv_heads, stream);
+    a.rows = rows;
+    return rotate(r, a, heads, kv_heads, stream);
 }

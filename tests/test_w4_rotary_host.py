@@ -163,7 +163,7 @@ def test_bad_rotations_are_refused(native, kw, code):
 
 
 @pytest.mark.parametrize("kw,code", [
-    ({"rows": -1}, INVAL), ({"heads": -1}, INVAL), ({"kv_heads": -1}, INVAL), ({"heads": 65535}, INVAL), ({"positions": None}, INVAL),
+    ({"rows": -1}, INVAL), ({"heads": -1}, INVAL), ({"kv_heads": -1}, INVAL), ({"heads": 65536}, INVAL), ({"rows": 1 << 30}, LIMIT), ({"positions": None}, INVAL),
     ({"positions": OK + 2}, ALIGN), ({"q": None}, INVAL), ({"q_out": None}, INVAL), ({"k": None}, INVAL), ({"k_out": None}, INVAL),
     ({"q_stride": 255}, INVAL), ({"k_out_stride": 64}, INVAL), ({"q_out": OK, "q_out_stride": 512}, INVAL), ({"q": OK + 8}, ALIGN),
     ({"k_out": 4 * OK + 2}, ALIGN), ({"q_stride": 260}, ALIGN), ({"rows": 0}, 0), ({"heads": 0, "kv_heads": 0}, 0)])
