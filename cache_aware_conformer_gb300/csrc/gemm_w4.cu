@@ -431,9 +431,10 @@ struct Plan {
 constexpr int W4_SMEM = 225 * 1024;
 bool plan_w4(int N, int K, int M, int size, int group, int sms, const int* clusters, Plan& best) {
     const int parts = size == 4 ? 2 : 1, chunks = (M + 31) / 32, tiles = (N + 15) / 16;
-    for (int chunk = (M + chunks - 1) / chunks; chunk >= 1; chunk /= 2) {   // fewer rows at a time where a deep A does not fit
+    float least = 0.f;
+    // fewer rows at a time where more of them leave less room for copies, or where a deep A does not fit
+    for (int chunk = (M + chunks - 1) / chunks; chunk >= 8 || (chunk >= 1 && least == 0.f); chunk = chunk > 8 && chunk < 16 ? 8 : chunk / 2) {
         const int mt = chunk <= 8 ? 1 : chunk <= 16 ? 2 : 4;
-        float least = 0.f;
         for (int boxes = 1; boxes <= 2; ++boxes) {
             const int all = (K + boxes * BOX_K - 1) / (boxes * BOX_K), blocks_of = boxes * 256 / group;
             const int raw = 16 * (((blocks_of / 2 + 1) * 4 + 15) / 16 * 16 + ((blocks_of + 6) / 4 * 4 + 15) / 16 * 16);
@@ -442,20 +443,26 @@ bool plan_w4(int N, int K, int M, int size, int group, int sms, const int* clust
                 if (stages * (slices - 1) >= all) continue;   // a slice would be empty
                 for (int warps = 16; warps >= 8; warps /= 2) {
                     for (int wn = 1; wn <= warps; wn *= 2) {
-                        const int blocks = std::min((tiles + wn - 1) / wn, slices == 1 ? sms : clusters[slices]), wk = warps / wn;
+                        const int room = slices == 1 ? sms : clusters[slices], blocks = std::min((tiles + wn - 1) / wn, room), wk = warps / wn;
                         const int turns = (tiles + blocks * wn - 1) / (blocks * wn);
                         const long long fixed = 1024 + (long long)parts * chunk * (stages * boxes * BOX_K * 2 + 64) +
                                                 2ll * warps * mt * 8 * PART_ROW * 4 + stages * boxes * mt * 8 * 4 +
                                                 (slices > 1 ? (long long)turns * wn * chunk * 64 : 0);
                         const int ring = (int)std::min<long long>(4, (W4_SMEM - fixed) / (warps * (boxes * BOX + raw)));
                         if (ring < 2) continue;
-                        // Boxes that a block's warps go through, and half of one (less beside more rows) for a stage's own work and a tile's.  Eight warps
-                        // hide less of each other's latencies, and less than 64 KB on their way less of memory's; a cluster's
-                        // sums cost about 32.
-                        const float far = (float)((ring - 1) * warps * boxes * BOX) / 65536.f;
-                        const float slow = (warps == 8 ? 1.4f : 1.f) * (far < 1.f ? 1.f + 0.5f * (1.f - far) : 1.f);
-                        const float cost = turns * warps * ((float)((stages + wk - 1) / wk) * (boxes + 0.5f / mt) * slow + 0.5f / mt) +
-                                           (slices > 1 ? 32.f : 0.f);
+                        // Microseconds, as fitted to 2,300 timings of every cut of 25 shapes (1 to 128 rows; the cut that it takes runs 1.01
+                        // times as long as the fastest on average, 1.12 at worst).  A box is instructions, twice as slow with eight warps, which
+                        // hide less of each other's latencies, and slower with less than 64 KB on their way; then come a stage's own
+                        // work, a tile's, the copy of A, the rounds of blocks that several chunks of rows make, and a cluster's
+                        // sums.  Without A's copy, rounds and sums, cuts were taken that ran 1.4 times as long as the fastest, 2.1 at worst.
+                        const int rounds = (blocks * ((M + chunk - 1) / chunk) + room - 1) / room, steps = (stages + wk - 1) / wk;
+                        const int box = 150 + blocks_of / boxes * (24 + 4 * mt) + (24 * parts + 5) * mt;
+                        const float far = std::min(1.f, (float)((ring - 1) * warps * boxes * BOX) / 65536.f), few = warps == 8 ? 1.f : 0.f;
+                        const float most = (float)turns * warps * steps;
+                        const float cost = rounds * (most * boxes * box * 1e-3f * (0.167f + 0.156f * few + 0.032f * (1.f - far)) + most * 0.044f +
+                                                     turns * 0.17f + (float)chunk * stages * boxes * parts * (0.0205f + 0.0123f * few) + 0.9f) +
+                                           (slices > 1 ? 1.05f + rounds * (slices * slices * (0.0103f + 0.0009f * slices) +
+                                                                           (float)turns * wn * chunk * 0.011f) : 0.f);
                         if (least == 0.f || cost < least) {
                             least = cost;
                             best = {chunk, mt, boxes, warps, wn, slices, stages, tiles, blocks, ring, turns,
@@ -465,9 +472,8 @@ bool plan_w4(int N, int K, int M, int size, int group, int sms, const int* clust
                 }
             }
         }
-        if (least > 0.f) return true;
     }
-    return false;
+    return least > 0.f;
 }
 
 template <class T, int W, int MT, int HB> cudaError_t launch_w4(const CUtensorMap& map, const W4Args& a, const Plan& p, cudaStream_t s) {
