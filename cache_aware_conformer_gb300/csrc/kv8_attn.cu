@@ -1110,9 +1110,15 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP, ALL_LOW>
     using P = PieceShape<T, HDP, ALL_LOW>;
     extern __shared__ __align__(128) uint8_t ring_all[];
     pdl_trigger();
-    pdl_wait();
+    // Beside the launch before, which takes nothing from here nor gives: pieces start where its blocks have ended.  That launch has
+    // waited for the one that dealt the pieces out before any block of this one could start.  Each block waits for it at its end, so
+    // that whatever waits for this launch waits for both.
+    if (!p.beside) pdl_wait();
     const int b = (int)blockIdx.x, warp = threadIdx.x >> 5, kvh = a.c.kv_heads, D = a.c.head_dim;
-    if (b >= *p.total) return;
+    if (b >= *p.total) {
+        pdl_wait();
+        return;
+    }
     const int i = warp_last_le(p.count, b, [&](int k) { return __ldg(p.first + k); });   // entries without pieces are before those with
     const KvEntry e = p.entries[i];
     const int in = b - e.first, unit = in / e.cuts, k = in - unit * e.cuts, head = unit % kvh, r0 = unit / kvh * 16;
@@ -1156,6 +1162,7 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP, ALL_LOW>
         if (c < D) *reinterpret_cast<float4*>(to + at * D + c) = make_float4(o.x * NORM, o.y * NORM, o.z * NORM, o.w * NORM);
         if (c == 0) to_ml[at] = make_float2(top, l);
     }
+    pdl_wait();
 }
 
 template <class T, int CODE, int HDP, bool ALL_LOW>

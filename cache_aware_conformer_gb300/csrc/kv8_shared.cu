@@ -996,7 +996,7 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
-    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low,
+    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low, prefix,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
     for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens
