@@ -524,11 +524,13 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
             }
             if (!warp_wait(raw_full + slot, phase)) return false;
             uint4 cur[NL];
-            // rows sub and sub + 8, elements of each 64
+            // Rows sub and sub + 8, elements of each 64: with two such parts, odd rows' other part first, so that the two rows of eight
+            // threads touch all banks.
+            const int odd = NL > 2 ? sub & 1 : 0;
 #pragma unroll
             for (int y = 0; y < NL; ++y)
-                cur[y] = there && ((y >> 1) * 4 + c4) * 16 < D
-                             ? *reinterpret_cast<const uint4*>(slots + slot * S::PIECE + (sub + (y & 1) * 8) * D + c4 * 16 + (y >> 1) * 64)
+                cur[y] = there && ((y >> 1 ^ odd) * 4 + c4) * 16 < D
+                             ? *reinterpret_cast<const uint4*>(slots + slot * S::PIECE + (sub + (y & 1) * 8) * D + c4 * 16 + (y >> 1 ^ odd) * 64)
                              : make_uint4(0, 0, 0, 0);
             __syncwarp();
             if (lane == 0) copy(n + S::CONV * S::SLOTS, slot, ahead_at);
@@ -543,7 +545,7 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
                 uint32_t h[8];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) half4<CODE>(u[k], h[2 * k], h[2 * k + 1]);
-                uint8_t* dst = to + (y >> 1) * S::PANEL + (y & 1) * 1024;
+                uint8_t* dst = to + (y >> 1 ^ odd) * S::PANEL + (y & 1) * 1024;
                 *reinterpret_cast<uint4*>(dst + (((2 * c4) ^ sub) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                 *reinterpret_cast<uint4*>(dst + (((2 * c4 + 1) ^ sub) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
             }
