@@ -1109,17 +1109,29 @@ __global__ void __launch_bounds__(PIECE_WARPS * 32, (PieceShape<T, HDP, ALL_LOW>
     kv_piece_kernel(const __grid_constant__ KvAttend a, const __grid_constant__ KvPieces p) {
     using P = PieceShape<T, HDP, ALL_LOW>;
     extern __shared__ __align__(128) uint8_t ring_all[];
-    pdl_trigger();
     // Beside the launch before, which takes nothing from here nor gives: pieces start where its blocks have ended.  That launch has
     // waited for the one that dealt the pieces out before any block of this one could start.  Each block waits for it at its end, so
-    // that whatever waits for this launch waits for both.
+    // that whatever waits for this launch waits for both; and what the pieces were dealt from is there for the next launch from its start.
     if (!p.beside) pdl_wait();
+    pdl_trigger();
     const int b = (int)blockIdx.x, warp = threadIdx.x >> 5, kvh = a.c.kv_heads, D = a.c.head_dim;
-    if (b >= *p.total) {
+    // Entries without pieces are before those with.  Reads that hang on others take a microsecond each: of a few entries all are read at once.
+    const int total = __ldg(p.total);
+    int i = -1;
+    if (p.count <= 128) {
+        const int lane = threadIdx.x & 31;
+        int at[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) at[k] = k * 32 + lane < p.count ? __ldg(p.first + k * 32 + lane) : INT32_MAX;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) i += __popc(__ballot_sync(0xffffffffu, at[k] <= b));
+    } else {
+        i = warp_last_le(p.count, b, [&](int k) { return __ldg(p.first + k); });
+    }
+    if (b >= total) {
         pdl_wait();
         return;
     }
-    const int i = warp_last_le(p.count, b, [&](int k) { return __ldg(p.first + k); });   // entries without pieces are before those with
     const KvEntry e = p.entries[i];
     const int in = b - e.first, unit = in / e.cuts, k = in - unit * e.cuts, head = unit % kvh, r0 = unit / kvh * 16;
     const int t0 = (int)((long long)e.s.tiles * k / e.cuts), n = (int)((long long)e.s.tiles * (k + 1) / e.cuts) - t0;

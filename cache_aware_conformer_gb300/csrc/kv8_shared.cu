@@ -36,8 +36,8 @@ struct SharedCall {
 __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __grid_constant__ SharedCall p) {
     __shared__ int s_lo, s_hi, s_bad, s_leader, s_members, s_same;
     __shared__ int s_all[PLAN_BLOCKS];
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();   // what the caller gave is there for the next launch from its start
     const KvAttend& a = p.a;
     const int n = a.rows.n, g = blockIdx.x, rank = blockIdx.z, t = threadIdx.x, lane = t & 31;
     if (t == 0) s_lo = 0, s_hi = INT32_MAX, s_bad = 0, s_leader = INT32_MAX, s_members = 0, s_same = INT32_MAX;
@@ -164,11 +164,24 @@ template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall
     const KvAttend& a = p.a;
     const int kvh = a.c.kv_heads, b = (int)blockIdx.x;
     Piece q{};
-    const int first0 = __ldg(&p.cut[0].x);
-    const int g = warp_last_le(p.groups, (long long)b + first0, [&](int k) { return __ldg(&p.cut[k].x); });   // groups without pieces are before those with
-    const int2 cut = p.cut[g];
-    const int4 sh = p.shared[g];
-    const int row0 = a.rows.at(g), rows = (a.rows.at(g + 1) - row0) * a.group, tiles = (sh.z - sh.y + 7) / 8;
+    // groups without pieces are before those with
+    int2 cut;
+    int4 sh;
+    int first0, row0, row1;
+    if (p.groups <= 32) {   // all at once: reads that hang on others take a microsecond each
+        const int lane = threadIdx.x & 31, at = min(lane, p.groups - 1);
+        cut = p.cut[at], sh = p.shared[at], row0 = a.rows.at(at), row1 = a.rows.at(at + 1);
+        first0 = __shfl_sync(0xffffffffu, cut.x, 0);
+        const int g = __popc(__ballot_sync(0xffffffffu, lane < p.groups && cut.x <= b + first0)) - 1;
+        cut.x = __shfl_sync(0xffffffffu, cut.x, g), cut.y = __shfl_sync(0xffffffffu, cut.y, g);
+        sh.x = __shfl_sync(0xffffffffu, sh.x, g), sh.y = __shfl_sync(0xffffffffu, sh.y, g), sh.z = __shfl_sync(0xffffffffu, sh.z, g);
+        row0 = __shfl_sync(0xffffffffu, row0, g), row1 = __shfl_sync(0xffffffffu, row1, g);
+    } else {
+        first0 = __ldg(&p.cut[0].x);
+        const int g = warp_last_le(p.groups, (long long)b + first0, [&](int k) { return __ldg(&p.cut[k].x); });
+        cut = p.cut[g], sh = p.shared[g], row0 = a.rows.at(g), row1 = a.rows.at(g + 1);
+    }
+    const int rows = (row1 - row0) * a.group, tiles = (sh.z - sh.y + 7) / 8;
     const int in = b + first0 - cut.x;
     if (cut.y == 0 || in >= (rows + ROWS - 1) / ROWS * kvh * cut.y) return q;
     const int unit = in / cut.y, k = in - unit * cut.y;
@@ -710,20 +723,22 @@ template <class F, class G, class P> __device__ __forceinline__ int deal_out(int
     all = s_tiles[lane];
     for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
     // lane k tries 1 + k / 32 of the least share
-    const long long base = max((long long)least, (all + max(most, 1) - 1) / max(most, 1)), mine = base + base * lane / 32;
+    const uint32_t aim = max(most, 1);
+    const long long even = all >> 31 ? (all + aim - 1) / aim : ((uint32_t)all + aim - 1) / aim;   // 64-bit divisions take their time
+    const uint32_t base = (uint32_t)min(max((long long)least, even), 1ll << 29), mine = base + (base >> 5) * lane + ((base & 31) * lane >> 5);
     int pieces = 0;
     for (int i = warp; i < count; i += 32) {
         const int u = units(i);
-        if (u) pieces += u * (int)((tiles(i) + mine - 1) / mine);
+        if (u) pieces += u * (int)(((uint32_t)tiles(i) + mine - 1) / mine);
     }
     atomicAdd(&s_tries[lane], pieces);
     __syncthreads();
     const uint32_t fit = __ballot_sync(0xffffffffu, s_tries[lane] <= most);
-    const long long share = __shfl_sync(0xffffffffu, mine, fit ? __ffs(fit) - 1 : 0);
+    const uint32_t share = __shfl_sync(0xffffffffu, mine, fit ? __ffs(fit) - 1 : 0);
     pieces = 0;
     int slots = 0;   // before this round's entries
     for (int i0 = 0; i0 < count; i0 += DEAL_THREADS) {
-        const int i = i0 + t, u = i < count ? units(i) : 0, cuts = u ? fit || !strict ? (int)((tiles(i) + share - 1) / share) : 1 : 0;
+        const int i = i0 + t, u = i < count ? units(i) : 0, cuts = u ? fit || !strict ? (int)(((uint32_t)tiles(i) + share - 1) / share) : 1 : 0;
         const int n = u * cuts, held = cuts > 1 ? n : 0;
         int x = n, y = held;
         for (int d = 1; d < 32; d <<= 1) {
@@ -750,8 +765,13 @@ template <class F, class G, class P> __device__ __forceinline__ int deal_out(int
 __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_constant__ DealCall p) {
     __shared__ int s_units[DEAL_THREADS], s_tiles[DEAL_THREADS], s_cut[2][DEAL_THREADS];   // of the first entries, or groups
     pdl_trigger();
-    pdl_wait();
     const KvAttend& a = p.a;
+    for (int i = threadIdx.x; i < a.rows.n; i += DEAL_THREADS) {   // the sequences' tokens: on their way to L1 while the plan is made
+        const int id = a.ids[i];
+        if (a.rows.starts) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.rows.starts + i) : "memory");
+        if (id >= 0 && id < a.c.max_seqs) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.c.lens + id) : "memory");
+    }
+    pdl_wait();
     const int n = a.rows.n, groups = p.n_groups, count = n + (p.prefix_rows ? 0 : groups), t = threadIdx.x, kvh = a.c.kv_heads;
     auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
     for (int i = t; i < count; i += DEAL_THREADS) {
@@ -767,6 +787,16 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
         p.entries[i].s = s;
         if (i < DEAL_THREADS) s_units[i] = units_of(s), s_tiles[i] = s.tiles;
     }
+    // What the join needs of the first sequences, and the groups' rows: read here, beside the rest
+    int2 my_skip = make_int2(0, 0);
+    int my_group = 0, my_row = 0;
+    if (t < n) {
+        my_skip = a.skip[t];
+        if (my_skip.y > my_skip.x) my_group = p.group_of[t], my_row = p.group_rows[my_group];
+    }
+    int4 my_shared = make_int4(0, 0, 0, 0);
+    int my_rows = 0;
+    if (p.prefix_rows && t < groups) my_shared = p.shared[t], my_rows = p.group_rows[t + 1] - p.group_rows[t];
     __syncthreads();
     const int pieces = deal_out(
         count, p.most, LEAST_TILES, false, [&](int i) { return i < DEAL_THREADS ? s_units[i] : units_of(p.entries[i].s); },
@@ -779,13 +809,12 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
         });
     if (t == 0) *p.total = pieces;
     if (p.prefix_rows) {
-        auto group_units = [&](int g) {
-            const int4 sh = p.shared[g];
-            return sh.z > sh.y ? ((p.group_rows[g + 1] - p.group_rows[g]) * a.group + p.prefix_rows - 1) / p.prefix_rows * kvh : 0;
-        };
-        auto group_tiles = [&](int g) { return (p.shared[g].z - p.shared[g].y + 7) / 8; };
+        auto units = [&](const int4& sh, int rows) { return sh.z > sh.y ? (rows * a.group + p.prefix_rows - 1) / p.prefix_rows * kvh : 0; };
+        auto tiles = [](const int4& sh) { return (sh.z - sh.y + 7) / 8; };
+        auto group_units = [&](int g) { return units(p.shared[g], p.group_rows[g + 1] - p.group_rows[g]); };
+        auto group_tiles = [&](int g) { return tiles(p.shared[g]); };
         __syncthreads();
-        for (int g = t; g < min(groups, DEAL_THREADS); g += DEAL_THREADS) s_units[g] = group_units(g), s_tiles[g] = group_tiles(g);
+        if (t < groups) s_units[t] = units(my_shared, my_rows), s_tiles[t] = tiles(my_shared);
         __syncthreads();
         deal_out(
             groups, p.prefix_most, 2, true, [&](int g) { return g < DEAL_THREADS ? s_units[g] : group_units(g); },
@@ -797,12 +826,12 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
     }
     __syncthreads();   // what the block has written to memory is read back below
     for (int i = t; i < n; i += DEAL_THREADS) {
-        const int2 skip = a.skip[i];
+        const int2 skip = i == t ? my_skip : a.skip[i];
         KvJoin& j = p.join[i];
         int cuts = 0, slot = 0, row = 0;
         if (skip.y > skip.x) {
-            const int g = p.group_of[i];
-            row = p.group_rows[g];
+            const int g = i == t ? my_group : p.group_of[i];
+            row = i == t ? my_row : p.group_rows[g];
             if (g < DEAL_THREADS) cuts = s_cut[0][g], slot = s_cut[1][g];
             else if (p.prefix_rows) cuts = p.cut[g].y, slot = p.cut[g].x;
             else cuts = p.entries[n + g].cuts, slot = p.entries[n + g].slot;
@@ -832,16 +861,16 @@ struct PartList {
 constexpr int JOIN_WARPS = 8;
 template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
     pdl_trigger();
-    pdl_wait();
     __shared__ __align__(16) float s_o[JOIN_WARPS][256];
     __shared__ float s_l[JOIN_WARPS];
     const KvAttend& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x, D = a.c.head_dim, team = p.team, mate = warp & (team - 1);
+    // What the parts were dealt from is older than the launch before, whose blocks had waited for it when this one could start.
     const int i = a.rows.starts ? warp_last_le(a.rows.n, row, [&](int k) { return a.rows.at(k); }) : row / a.rows.each;
-    if (i < 0) return;
-    const int r0 = a.rows.at(i), r1 = a.rows.at(i + 1);
+    const int r0 = i < 0 ? 0 : a.rows.at(i), r1 = i < 0 ? 0 : a.rows.at(i + 1);
+    const KvJoin j = p.join[max(i, 0)];
+    pdl_wait();
     if (row < r0 || row >= r1 || r0 < 0 || r1 > a.rows.rows) return;   // no sequence's, or of one whose rows pass the end
-    const KvJoin j = p.join[i];
     // (pieces of a unit, first slot) of the own and of the shared tokens
     const int2 own = make_int2(j.named ? j.own_cuts : 0, j.own_slot), common = make_int2(j.named ? j.common_cuts : 0, j.common_slot);
     const int in_group = row - j.common_row;
