@@ -10,6 +10,10 @@
 // 16-byte pieces of it, chosen so that both elements of a pair are the thread's own (the pieces rot_dim / 2 apart, or
 // next to each other); where rot_dim / 2 is no whole number of pieces the group exchanges its values
 // through shared memory.  The pieces are loaded before the block looks up its positions.
+//
+// Measured (us; in brackets what the bytes take at a copy's rate): prompts of 22,000 rows, 40 heads of 128 bf16 with norms: 94 (67), issue slots
+// and a block's start of dependent reads; 9,100 rows of 20 heads of 128 fp32, half of each rotated in pairs, at positions to 10^6: 34 (27); two
+// rows of each of 256 sequences, 16 heads of 64 fp32: 3.4 (0.6), which are three dependent reads and a launch.
 #include <algorithm>
 
 #include "cac_ops.h"

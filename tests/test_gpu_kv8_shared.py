@@ -1,6 +1,6 @@
 """Attention of sequences that share a prefix on the GPU: against the plain model in 64
 bits, sequence by sequence, and against what may and may not be shared.  A call that has
-less than 100 MB to read even if it shares nothing is cac_kv8_attend's, so the caches here have
+less than 70 MB to read even if it shares nothing is cac_kv8_attend's, so the caches here have
 tables for far longer sequences than they hold, and calls are asserted to be the shared
 kernels' by the kernels of a captured graph."""
 import warnings
@@ -447,3 +447,42 @@ def test_a_decoding_step(dtype, graph):
         for s in b.seqs:
             s.len += 1
         b.verify()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group,prefix", [(2, True), (1, False)])
+def test_nothing_of_ones_own_at_all(dtype, group, prefix):
+    """Everything is shared: there are no pieces of the sequences' own tokens, and what joins the parts still waits for the shared ones'."""
+    n = 40 if prefix else 9
+    b = Shared("int8", heads=2, dim=64, page=32, n_pages=300, seqs=n, dtype=dtype, seed=n)
+    b.family([(1024, [0] * n)])
+    for _ in range(3):
+        b.check_shared(range(n), [1] * n, None, group=group, uniform=True, prefix=prefix)
+
+
+def test_calls_of_unlike_sizes_one_behind_the_other():
+    """Launches start before those before them have ended: calls that follow each other in a graph, in one workspace, keep apart."""
+    n = 64
+    b = Shared("e4m3", heads=2, dim=128, page=32, n_pages=900, seqs=n, dtype=BF16, seed=5)
+    rng = np.random.default_rng(5)
+    b.family([(1500, rng.integers(0, 90, n // 2).tolist()), (700, rng.integers(0, 300, n // 2).tolist())])
+    cases = []
+    for ids, groups, group in [(range(n), [0, n // 2, n], 4), (range(3), None, 2), (range(20, 50), [0, 12, 30], 8), (range(n), None, 1)]:
+        q = b.rand(len(ids), group * 2, 128).cuda()
+        cases.append((b.ids(ids), q, None if groups is None else b.ids(groups)))
+    attend = lambda: [b.cache.attend_shared(0, ids, q, groups=groups) for ids, q, groups in cases]  # noqa: E731
+    want = []
+    for ids, q, groups in cases:
+        want.append(b.cache.attend_shared(0, ids, q, groups=groups).clone())
+        torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [y for _ in range(3) for y in attend()]
+    for _ in range(10):
+        for y in got:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, y in enumerate(got):
+            assert torch.equal(y, want[k % len(want)]), k
+    b.cache.check()
