@@ -11,7 +11,7 @@
 // next to each other); where rot_dim / 2 is no whole number of pieces the group exchanges its values
 // through shared memory.  The pieces are loaded before the block looks up its positions.
 //
-// Measured (us; in brackets what the bytes take at a copy's rate): prompts of 22,000 rows, 40 heads of 128 bf16 with norms: 94 (67), issue slots
+// Measured (us; in brackets what the bytes take at a copy's rate): prompts of 22,000 rows, 40 heads of 128 bf16 with norms: 92 (67), issue slots
 // and a block's start of dependent reads; 9,100 rows of 20 heads of 128 fp32, half of each rotated in pairs, at positions to 10^6: 34 (27); two
 // rows of each of 256 sequences, 16 heads of 64 fp32: 3.4 (0.6), which are three dependent reads and a launch.
 #include <algorithm>
@@ -112,6 +112,20 @@ template <class T> __device__ __forceinline__ uint4 pack(const float (&x)[16 / s
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// two products, or sums of products, in one instruction
+__device__ __forceinline__ float2 mul_two(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma_two(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\tfma.rn.f32x2 w, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
 // sum over a group of 2^log2 lanes
 __device__ __forceinline__ float group_sum(float x, int log2) {
     for (int d = 1 << log2 >> 1; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
@@ -147,9 +161,8 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
         c0 = 2 * l, c1 = 2 * l + 1;
     }
     const bool mine = c0 < pieces;
-    // A thread's own pairs are N in a row, l N and on: two of them to 16 bytes, neighbours' next to each other
+    // A thread's own pairs are N in a row, l N and on: two cosines and two sines to 16 bytes, neighbours' next to each other
     const int owners = (half + N - 1) / N, row_turns = HOW == HALF_ANY ? half : owners * N;
-    auto turn_at = [&](int i) { return HOW == HALF_ANY ? i : ((i % N >> 1) * owners + i / N) * 2 + (i & 1); };
 
     auto row_of = [&](int u) {   // u / heads: units of a block are below 2^21, where the product is the quotient or one more
         const int r = s.heads == 1 ? u : (int)__umulhi((uint32_t)u, s.heads_mul);
@@ -175,7 +188,13 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
     __syncthreads();
     for (int e = threadIdx.x; e < rows * half; e += blockDim.x) {
         const int r = e / half, i = e - r * half;
-        s_turn[r * row_turns + turn_at(i)] = turn(s_pos[r], a.steps[i], a.amplitude);
+        const float2 cs = turn(s_pos[r], a.steps[i], a.amplitude);
+        if constexpr (HOW == HALF_ANY) {
+            s_turn[r * row_turns + i] = cs;
+        } else {
+            float* to = reinterpret_cast<float*>(s_turn + r * row_turns) + ((i % N >> 1) * owners + i / N) * 4 + (i & 1);
+            to[0] = cs.x, to[2] = cs.y;
+        }
     }
     float gain[2][N];
     if (s.gain && mine)
@@ -195,12 +214,12 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
         const bool store = on && s_there[r];
         load(u + stride);
         if (s.gain) {
-            float sum = 0.f;
+            float2 two = make_float2(0.f, 0.f);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int j = 0; j < N; ++j) sum = fmaf(x[b][j], x[b][j], sum);
-            sum = group_sum(on ? sum : 0.f, a.lanes_log2);
+                for (int j = 0; j < N; j += 2) two = fma_two(make_float2(x[b][j], x[b][j + 1]), make_float2(x[b][j], x[b][j + 1]), two);
+            float sum = group_sum(on ? two.x + two.y : 0.f, a.lanes_log2);
             // squares of values over 2^60 or so leave fp32: such a head is brought down by 2^80 first (and its eps with it)
             const bool huge = !(sum < 1.3e36f);
             float eps = a.eps;
@@ -222,7 +241,11 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
-                    for (int j = 0; j < N; ++j) x[b][j] *= inv * gain[b][j];
+                    for (int j = 0; j < N; j += 2) {
+                        const float2 y = mul_two(make_float2(x[b][j], x[b][j + 1]),
+                                                 mul_two(make_float2(inv, inv), make_float2(gain[b][j], gain[b][j + 1])));
+                        x[b][j] = y.x, x[b][j + 1] = y.y;
+                    }
         }
         const float2* t = s_turn + r * row_turns;
         if constexpr (HOW == HALF_ANY) {
@@ -255,19 +278,21 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 const float4 cs = own[j / 2 * owners];
+                const float2 c = make_float2(cs.x, cs.y), sn = make_float2(cs.z, cs.w);
+                if constexpr (HOW == HALF_PIECES) {
+                    const float2 p = make_float2(x[0][j], x[0][j + 1]), q = make_float2(x[1][j], x[1][j + 1]);
+                    const float2 y = fma_two(p, c, mul_two(make_float2(-q.x, -q.y), sn)), z = fma_two(p, sn, mul_two(q, c));
+                    x[0][j] = y.x, x[0][j + 1] = y.y, x[1][j] = z.x, x[1][j + 1] = z.y;
+                } else {
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const float c = b ? cs.z : cs.x, sn = b ? cs.w : cs.y;
-                    const int i = j + b;
-                    if constexpr (HOW == HALF_PIECES) {
-                        const float p = x[0][i], q = x[1][i];
-                        x[0][i] = p * c - q * sn;
-                        x[1][i] = p * sn + q * c;
-                    } else if (l * N + i < half) {
-                        float &p = x[i / (N / 2)][2 * i % N], &q = x[i / (N / 2)][2 * i % N + 1];
-                        const float was = p;
-                        p = was * c - q * sn;
-                        q = was * sn + q * c;
+                    for (int b = 0; b < 2; ++b) {
+                        const int i = j + b;
+                        if (l * N + i < half) {
+                            float &p = x[i / (N / 2)][2 * i % N], &q = x[i / (N / 2)][2 * i % N + 1];
+                            const float was = p;
+                            p = was * (b ? c.y : c.x) - q * (b ? sn.y : sn.x);
+                            q = was * (b ? sn.y : sn.x) + q * (b ? c.y : c.x);
+                        }
                     }
                 }
             }
