@@ -151,13 +151,14 @@ extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const i
     const KvAttend a = part_of(*c, layer, n, 0, n, ids, starts, rows, most, heads, scale, {att_left, att_chunk, sinks}, q, q_stride,
                                out, out_stride, lse);
     // Two kinds of call are attend's.  Sequences with many query rows each: their products bound the call, and every row tile reads the
-    // tokens anyway.  And those that have less than 70 MB to read even with nothing shared, which takes 11 us: finding out what is,
-    // the parts and their join take as long.  Measured (sequences behind a prefix, own tokens up to 60; us of attend / with the prefix read once):
-    // 8 K/V heads of 128, group 4, bf16: 8 sequences 34 MB 24 / 25, 67 MB 28 / 28, 132 MB 36 / 32; 32 of them 30 MB 23 / 30, 69 MB 30 / 30,
-    // 266 MB 55 / 36, 1,053 MB 156 / 47; 4 heads of 64, group 8: 32 sequences 34 MB 25 / 29, 67 MB 30 / 30, 132 MB 43 / 35; 8 heads of 64,
-    // fp32: 8 sequences 33 MB 23 / 21, 66 MB 30 / 24.
+    // tokens anyway.  And those that have less than 70 MB (fp32, where a row takes two products: 50) to read even with nothing shared, which
+    // takes 11 us: finding out what is, the parts and their join take as long.  Measured (sequences behind a prefix, own tokens up to 60; us of attend /
+    // with the prefix read once): bf16, 8 K/V heads of 128, group 4: 8 sequences 34 MB 24 / 25, 67 MB 28 / 28, 132 MB 36 / 32; 32 of them
+    // 30 MB 23 / 30, 69 MB 30 / 30, 266 MB 55 / 36, 1,053 MB 156 / 47; 4 heads of 64, group 8: 32 sequences 34 MB 25 / 29, 67 MB 30 / 30,
+    // 132 MB 43 / 35.  fp32, 8 heads of 64: 4 sequences 33 MB 23 / 24, 66 MB 30 / 27; 8 of them 33 MB 23 / 21, 66 MB 30 / 24; 4 heads, group 4, 24
+    // sequences of up to 8 queries, 66 MB: 45 / 41.
     const long long bytes = (long long)n * c->kv_heads * longest(*c, most, att_left, att_chunk, sinks) * 2 * c->head_dim;
-    if (bytes < 70000000 || kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
+    if (bytes < (dtype == CAC_DTYPE_F32 ? 50000000 : 70000000) || kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
         return cac_kv8_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_left, att_chunk, sinks, q, q_stride, out,
                               out_stride, lse, dtype, workspace, workspace_bytes, stream);
     DeviceScope dev(c->device);
