@@ -303,7 +303,8 @@ __global__ void __launch_bounds__(MOST_W4_WARPS * 32, 1)
     for (int tile = tile0; wk < stages && tile < a.tiles; tile += tile_step, ++turn) {
         float acc[MT][4] = {};
         // where in a word a row's scales and zero points begin
-        const int odd[2] = {min(tile * 16 + row_of<W>(g), N - 1) * groups & 3, min(tile * 16 + row_of<W>(g) + 8, N - 1) * groups & 3};
+        const uint32_t odd[2] = {(uint32_t)min(tile * 16 + row_of<W>(g), N - 1) * (uint32_t)groups & 3u,
+                                 (uint32_t)min(tile * 16 + row_of<W>(g) + 8, N - 1) * (uint32_t)groups & 3u};
         for (int stage = wk; stage < stages; stage += WK) {
             __syncwarp();   // the stage before this one has been read
             if (ok) fetch();

@@ -124,8 +124,8 @@ int cac_op_rotary_steps(int rot_dim, double base, int scaling, double factor, do
  *                 every q_stride / k_stride elements; either may be NULL with 0 heads
  *   q_out, k_out  the same shapes, with strides of their own; an output may be its
  *                 input (same pointer and stride) and may not overlap it otherwise
- * Pointers and row strides are multiples of 16 bytes; heads, kv_heads <= 65535, rows < 2^30
- * (CAC_E_LIMIT). */
+ * Pointers and row strides are multiples of 16 bytes; heads, kv_heads <= 65535
+ * (CAC_E_INVAL beyond), rows < 2^30 (CAC_E_LIMIT). */
 int cac_op_rotate(const cac_rotary* r, int rows, const int32_t* positions, int heads, const void* q, long long q_stride,
                   void* q_out, long long q_out_stride, int kv_heads, const void* k, long long k_stride, void* k_out,
                   long long k_out_stride, void* stream);
