@@ -172,3 +172,37 @@ def test_binding_refuses_bad_tensors(native):
 def test_deep_rows(native, dtype, M, K):
     """Depths that a cluster of blocks shares, with fewer rows at a time where they do not fit."""
     check(native, *make(M, 40, K, 128, True, False, dtype))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("group,K", [(32, 64), (32, 192), (64, 128), (64, 1152), (128, 768)])
+def test_slices_of_larger_weights(native, dtype, group, K):
+    """Rows 2 and on of weights: scales and zero points that begin anywhere on 4 bytes, and whose neighbours are not this call's."""
+    N = 50
+    a, packed, scale, zero, _ = make(5, N + 6, K, group, True, False, dtype)
+    scale[:2], scale[N + 2:] = float("nan"), float("inf")
+    put = [t.cuda() for t in (packed, scale, zero)]
+    cut = [t[2:N + 2] for t in put]
+    got = native.gemm_w4(a.cuda(), cut[0], cut[1], zero=cut[2])
+    want, tol = exact(a, packed[2:N + 2], scale[2:N + 2], zero[2:N + 2], None)
+    assert ((got.double().cpu() - want).abs() <= tol).all()
+
+
+def test_two_streams_at_once(native):
+    """Nothing is shared between calls: two graphs replayed side by side give what each gives alone."""
+    cases = []
+    for M, N, K, group, dtype in [(3, 3000, 4096, 64, F32), (16, 2048, 8192, 32, BF16)]:
+        args = [None if t is None else t.cuda() for t in make(M, N, K, group, True, True, dtype)]
+        want = native.gemm_w4(args[0], args[1], args[2], zero=args[3], bias=args[4])
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            got = [native.gemm_w4(args[0], args[1], args[2], zero=args[3], bias=args[4]) for _ in range(8)]
+        cases.append((args, want, got, graph, stream))
+    for _ in range(5):
+        for *_, graph, stream in cases:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, want, got, *_ in cases:
+        assert all(torch.equal(g, want) for g in got)
