@@ -544,11 +544,11 @@ def gemm_w4(A, packed, scale, zero=None, bias=None, out=None, stream=None):
     if one != 1 and K > 1:
         raise ValueError("A: the elements of a row have to lie next to each other")
     if out is None:
-        if stream is None:
-            out = A.new_empty((M, N))
+        if stream is None:   # (new_empty takes 2 us longer between launches)
+            out = torch.empty((M, N), dtype=dt, device=A.device)
         else:
             with torch.cuda.stream(stream):
-                out = A.new_empty((M, N))
+                out = torch.empty((M, N), dtype=dt, device=A.device)
         c_stride = N
     else:
         if out.dtype is not dt or out.shape != (M, N) or out.get_device() != dev or (N > 1 and out.stride(1) != 1):
@@ -620,10 +620,10 @@ class Rotary:
             row = heads * D
         if out is None:
             if stream is None:
-                out = t.new_empty((rows, heads, D))
+                out = self._torch.empty((rows, heads, D), dtype=dt, device=self.device)
             else:
                 with self._torch.cuda.stream(stream):
-                    out = t.new_empty((rows, heads, D))
+                    out = self._torch.empty((rows, heads, D), dtype=dt, device=self.device)
             to = heads * D
         else:
             if out.shape != t.shape or out.dtype is not dt or out.get_device() != self._dev:
@@ -1136,7 +1136,7 @@ class Kv8Cache:
         D = self._c.head_dim
         space = sums = None
         if out is None:
-            out = q.new_empty((rows, heads, D)) if stream is None else self._empty(stream, ((rows, heads, D), q.dtype))[0]
+            out = self._empty(stream, ((rows, heads, D), q.dtype))[0]
             os_ = heads * D
         else:
             os_, _ = self._act(out, heads, "out")
