@@ -136,7 +136,6 @@ struct KvPieces {
     const int32_t* total;  // pieces in all
     int count, own;        // entries; those from own on go to o1, ml1
     bool low;              // no unit has more than 8 rows
-    bool beside;           // may run beside the launch before it, which has waited for the pieces' entries
     float *o0, *o1, *slot_o;       // [rows][heads][head_dim]; [slot][16][head_dim]: sums times the norm's factor
     float2 *ml0, *ml1, *slot_ml;   // their maxima and norms
 };

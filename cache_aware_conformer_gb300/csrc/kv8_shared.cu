@@ -43,8 +43,8 @@ struct SharedCall {
 __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __grid_constant__ SharedCall p) {
     __shared__ int s_lo, s_hi, s_bad, s_leader, s_members, s_same;
     __shared__ int s_all[PLAN_BLOCKS];
+    pdl_trigger();
     pdl_wait();
-    pdl_trigger();   // what the caller gave is there for the next launch from its start
     const KvAttend& a = p.a;
     const int n = a.rows.n, g = blockIdx.x, rank = blockIdx.z, t = threadIdx.x, lane = t & 31;
     if (t == 0) s_lo = 0, s_hi = INT32_MAX, s_bad = 0, s_leader = INT32_MAX, s_members = 0, s_same = INT32_MAX;
@@ -772,13 +772,8 @@ template <class F, class G, class P> __device__ __forceinline__ int deal_out(int
 __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_constant__ DealCall p) {
     __shared__ int s_units[DEAL_THREADS], s_tiles[DEAL_THREADS], s_cut[2][DEAL_THREADS];   // of the first entries, or groups
     pdl_trigger();
-    const KvAttend& a = p.a;
-    for (int i = threadIdx.x; i < a.rows.n; i += DEAL_THREADS) {   // the sequences' tokens: on their way to L1 while the plan is made
-        const int id = a.ids[i];
-        if (a.rows.starts) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.rows.starts + i) : "memory");
-        if (id >= 0 && id < a.c.max_seqs) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.c.lens + id) : "memory");
-    }
     pdl_wait();
+    const KvAttend& a = p.a;
     const int n = a.rows.n, groups = p.n_groups, count = n + (p.prefix_rows ? 0 : groups), t = threadIdx.x, kvh = a.c.kv_heads;
     auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
     for (int i = t; i < count; i += DEAL_THREADS) {
@@ -867,16 +862,15 @@ struct PartList {
 };
 constexpr int JOIN_WARPS = 8;
 template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_join_shared_kernel(const __grid_constant__ JoinCall p) {
-    pdl_trigger();
     __shared__ __align__(16) float s_o[JOIN_WARPS][256];
     __shared__ float s_l[JOIN_WARPS];
+    pdl_trigger();
+    pdl_wait();
     const KvAttend& a = p.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x, D = a.c.head_dim, team = p.team, mate = warp & (team - 1);
-    // What the parts were dealt from is older than the launch before, whose blocks had waited for it when this one could start.
     const int i = a.rows.starts ? warp_last_le(a.rows.n, row, [&](int k) { return a.rows.at(k); }) : row / a.rows.each;
     const int r0 = i < 0 ? 0 : a.rows.at(i), r1 = i < 0 ? 0 : a.rows.at(i + 1);
     const KvJoin j = p.join[max(i, 0)];
-    pdl_wait();
     if (row < r0 || row >= r1 || r0 < 0 || r1 > a.rows.rows) return;   // no sequence's, or of one whose rows pass the end
     // (pieces of a unit, first slot) of the own and of the shared tokens
     const int2 own = make_int2(j.named ? j.own_cuts : 0, j.own_slot), common = make_int2(j.named ? j.common_cuts : 0, j.common_slot);
@@ -1034,7 +1028,7 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
-    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low, prefix,
+    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
     for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens

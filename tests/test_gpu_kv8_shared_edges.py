@@ -1,0 +1,56 @@
+"""Attention behind a shared prefix, in a workspace that the test holds: what a call reads of it, and what it finds to be shared."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from test_gpu_kv8_shared import Shared  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+class Call:
+    """A call of cac_kv8_attend_shared with a row for each sequence, into an output and a workspace of its own."""
+
+    def __init__(self, b, ids, q, groups=None, left=-1, chunk=1, sinks=0):
+        self.b, self.n, self.q = b, len(ids), q.cuda()
+        self.ids, self.groups = b.ids(ids), None if groups is None else b.ids(groups)
+        self.n_groups = 0 if groups is None else len(groups) - 1
+        self.out = torch.empty_like(self.q)
+        self.window = (left, chunk, sinks)
+        self.lib, self.ref = b.native.lib(), b.cache._ref
+        need = self.lib.cac_kv8_attend_shared_workspace(self.ref, self.n, self.n, 1, self.n_groups, q.shape[1], *self.window)
+        self.space = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def run(self):
+        q, out = self.q, self.out
+        r = self.lib.cac_kv8_attend_shared(
+            self.ref, 0, self.n, self.ids.data_ptr(), None, self.n, 1, self.n_groups, None if self.groups is None else self.groups.data_ptr(),
+            q.shape[1], q.shape[2] ** -0.5, *self.window, q.data_ptr(), q.stride(0), out.data_ptr(), out.stride(0), None,
+            1 if q.dtype is BF16 else 0, self.space.data_ptr(), self.space.numel(), torch.cuda.current_stream().cuda_stream)
+        assert r == 0
+        return out
+
+
+@pytest.mark.parametrize("n,heads,dim", [(64, 8, 128), (9, 2, 64), (20, 6, 144)])
+def test_nothing_of_a_workspace_is_read_before_the_call_has_written_it(n, heads, dim):
+    """Calls behind one another over a workspace that is filled with other bytes before each: whatever a launch reads of it, it has
+    waited for."""
+    b = Shared("int8", heads=2, dim=dim, page=32, n_pages=700, seqs=n, dtype=BF16, seed=n)
+    rng = np.random.default_rng(n)
+    st = b.family([(1500, rng.integers(0, 200, n // 2).tolist()), (700, rng.integers(0, 90, n - n // 2).tolist())])
+    call = Call(b, range(n), b.rand(n, heads, dim), st)
+    want = call.run().clone()
+    b.check_shared(range(n), [1] * n, st, group=heads // 2, uniform=True, q=call.q.cpu())
+    graph, outs = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        for fill in (0, 255, 1, 127):
+            call.space.fill_(fill)
+            outs.append(call.run().clone())
+            outs.append(call.run().clone())
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    b.cache.check()
+    assert all(torch.equal(x, want) for x in outs)
