@@ -151,6 +151,7 @@ extern template cudaError_t kv_launch_pieces<CAC_KV8_E4M3>(const KvAttend&, cons
 bool kv_prompt_takes(const KvAttend& a, int dtype, int sms, long long rows);
 cudaError_t kv_launch_prompt(const KvAttend& a, int dtype, cudaStream_t s);
 // kv8_shared.cu: a.rows and a.ids are the whole call's; workspace of kv_shared_bytes
+bool kv_prefix_takes(const KvAttend& a, int n_groups);   // whether the shared tokens have a launch of their own
 cudaError_t kv_attend_shared(const KvAttend& a, int dtype, const int32_t* groups, int n_groups, int sms, void* workspace, cudaStream_t s);
 size_t kv_shared_bytes(const cac_kv8& c, int n, int rows, int n_groups, int heads, int sms);
 

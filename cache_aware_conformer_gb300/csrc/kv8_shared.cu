@@ -996,12 +996,12 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
     return s;
 }
 
+}  // namespace
+
 // Whether kv_prefix_kernel reads the shared tokens, 128 rows at a time, or kv_piece_kernel, 16.
-bool prefix_takes(const KvAttend& a, int n_groups) {
+bool kv_prefix_takes(const KvAttend& a, int n_groups) {
     return a.c.head_dim <= 128 && (long long)a.rows.rows * a.group > 32ll * n_groups;
 }
-
-}  // namespace
 
 cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* groups, int n_groups, int sms, void* workspace,
                              cudaStream_t s) {
@@ -1015,7 +1015,7 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     cudaError_t e = launch_k(kv_plan_shared_kernel, dim3(n_groups, 1, PLAN_BLOCKS), dim3(PLAN_THREADS), 0, s, PLAN_BLOCKS, plan);
     if (e != cudaSuccess) return e;
 
-    const bool prefix = prefix_takes(call, n_groups);
+    const bool prefix = kv_prefix_takes(call, n_groups);
     KvAttend a = call;
     a.skip = plan.skip;
     const bool low = (long long)call.max_new * call.group <= 8 && (prefix || (long long)rows * call.group <= 8);

@@ -170,9 +170,10 @@ size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, 
  *           sequences groups[g] .. groups[g+1]-1 of the call form a group, those
  *           outside all of them share nothing.  NULL with n_groups 0: all form one.
  *           Where groups break this nothing is shared, and CAC_E_BOUNDS is latched
- *           if the call looks at them: one whose sequences have less than 70 MB (fp32
- *           queries: 50) of codes between them at most (n, max_pages and the window tell), or which
- *           cac_kv8_attend takes for prompts, is done as cac_kv8_attend does it.
+ *           if the call looks at them: one whose sequences have less than 100 MB (50 for
+ *           fp32 queries of up to 32 rows a group) of codes between them at most (n,
+ *           max_pages and the window tell), or which cac_kv8_attend takes for prompts, is
+ *           done as cac_kv8_attend does it.
  *   out_stride, lse, max_new, workspace and the rest as there, with
  *           cac_kv8_attend_shared_workspace bytes
  * Tokens are shared in blocks of 16, up to the first page in which the tables of a

@@ -4,10 +4,18 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from test_gpu_kv8 import Both  # noqa: E402
 from test_gpu_kv8_shared import Shared  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 BF16, F32 = torch.bfloat16, torch.float32
+
+
+class Sized(Shared):
+    """With tables for so many tokens."""
+
+    def __init__(self, tokens, code="int8", layers=1, heads=2, dim=64, page=32, n_pages=64, seqs=6, dtype=F32, seed=0):
+        Both.__init__(self, code, layers, heads, dim, page, n_pages, seqs, -(-tokens // page), dtype, seed)
 
 
 class Call:
@@ -54,3 +62,19 @@ def test_nothing_of_a_workspace_is_read_before_the_call_has_written_it(n, heads,
     torch.cuda.synchronize()
     b.cache.check()
     assert all(torch.equal(x, want) for x in outs)
+
+
+@pytest.mark.parametrize("dtype,n,group,heads,dim,tokens,shares", [
+    (F32, 24, 16, 4, 64, 6000, False), (F32, 24, 16, 4, 64, 8300, True), (BF16, 32, 4, 8, 128, 1500, False), (BF16, 32, 4, 8, 128, 1600, True),
+    (F32, 8, 1, 8, 64, 6000, False), (F32, 8, 1, 8, 64, 6400, True), (BF16, 8, 1, 8, 64, 6400, False)])
+def test_calls_that_attend_answers_sooner_go_to_it(dtype, n, group, heads, dim, tokens, shares):
+    """By what the tables have room for: 100 MB, or 50 where fp32 queries are few."""
+    b = Sized(tokens, heads=heads, dim=dim, page=16, n_pages=3 * n + 20, seqs=n, dtype=dtype)
+    b.family([(100, [1] * n)])
+    q, ids = b.rand(n, heads * group, dim).cuda(), b.ids(range(n))
+    names = b.kernels(lambda: b.cache.attend_shared(0, ids, q))
+    assert ("kv_plan_shared_kernel" in names) == shares
+    want = b.cache.attend(0, ids, q)
+    got = b.cache.attend_shared(0, ids, q)
+    b.cache.check()
+    assert torch.equal(got, want) or shares
