@@ -48,8 +48,8 @@ inline bool pdl_enabled() {
     return on;
 }
 template <class... KArgs, class... Args>
-inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                            int cluster_z, Args... args) {
+inline cudaError_t launch_as(bool early, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                             int cluster_z, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
@@ -57,7 +57,7 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
     cfg.stream = s;
     cudaLaunchAttribute at[2];
     int n = 0;
-    if (pdl_enabled()) {
+    if (early) {
         at[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         at[n].val.programmaticStreamSerializationAllowed = 1;
         ++n;
@@ -72,6 +72,16 @@ inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_
     cfg.attrs = at;
     cfg.numAttrs = n;
     return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+template <class... KArgs, class... Args>
+inline cudaError_t launch_k(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                            int cluster_z, Args... args) {
+    return launch_as(pdl_enabled(), kern, grid, block, smem, s, cluster_z, args...);
+}
+// Begins when everything before it in the stream has ended.
+template <class... KArgs, class... Args>
+inline cudaError_t launch_after(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
+    return launch_as(false, kern, grid, block, smem, s, 1, args...);
 }
 
 // ---------------------------------------------------------------------------

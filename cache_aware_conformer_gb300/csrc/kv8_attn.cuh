@@ -136,6 +136,7 @@ struct KvPieces {
     const int32_t* total;  // pieces in all
     int count, own;        // entries; those from own on go to o1, ml1
     bool low;              // no unit has more than 8 rows
+    bool beside;           // runs beside the launch before it (kv8_attn.cu says what that one has to be)
     float *o0, *o1, *slot_o;       // [rows][heads][head_dim]; [slot][16][head_dim]: sums times the norm's factor
     float2 *ml0, *ml1, *slot_ml;   // their maxima and norms
 };

@@ -151,17 +151,17 @@ extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const i
     const KvAttend a = part_of(*c, layer, n, 0, n, ids, starts, rows, most, heads, scale, {att_left, att_chunk, sinks}, q, q_stride,
                                out, out_stride, lse);
     // Two kinds of call are attend's.  Sequences with many query rows each: their products bound the call, and every row tile reads the
-    // tokens anyway.  And those that have less than 100 MB to read even with nothing shared, which takes 15 us: finding out what is, the parts and
-    // their join take as long.  50 MB for fp32 (where a row takes two products) with few rows, whose shared tokens need no launch of
-    // their own.  Measured (sequences behind a prefix, own tokens up to 60; us of attend / with the prefix read once): bf16, 8 K/V heads of 128,
-    // group 4: 4 sequences 67 MB 28 / 31, 132 MB 38 / 37; 8 of them 67 MB 28 / 30, 100 MB 33 / 32, 132 MB 37 / 35; 32 of them 69 MB 30 / 39,
-    // 100 MB 33 / 39, 132 MB 37 / 39, 266 MB 55 / 42; 4 heads of 64, group 8: 32 sequences 67 MB 30 / 36, 100 MB 36 / 37, 132 MB 42 / 39.  fp32, 8
-    // heads of 128, group 4: 8 sequences 66 MB 31 / 34, 100 MB 37 / 37, 132 MB 43 / 42; 4 heads of 64, group 4: 24 of up to 8 queries, 66 MB 44 / 47,
-    // 104 MB 53 / 51, 139 MB 63 / 56; few rows, 8 heads of 64: 4 sequences 33 MB 23 / 24, 50 MB 28 / 27, 66 MB 30 / 28, 100 MB 38 / 32; 8 of them 33 MB
-    // 23 / 23, 50 MB 27 / 24, 66 MB 29 / 25; 24 of them 50 MB 27 / 25, 66 MB 30 / 26.
+    // tokens anyway.  And those that have less than 70 MB to read even with nothing shared, which takes 11 us: finding out what is, the
+    // parts and their join take as long; 50 MB for fp32 (where a row takes two products) with rows so few that they have no launch of their own.
+    // Measured (sequences behind a prefix, own tokens up to 60; us of attend / with the prefix read once): bf16, 8 K/V heads of 128, group 4:
+    // 4 sequences 67 MB 28 / 31, 132 MB 38 / 37; 8 of them 34 MB 24 / 28, 67 MB 28 / 30, 100 MB 33 / 32, 132 MB 37 / 35; 32 of them 30 MB
+    // 24 / 29, 69 MB 30 / 30, 100 MB 34 / 30, 132 MB 37 / 30, 266 MB 55 / 38; 4 heads of 64, group 8: 32 sequences 34 MB 25 / 29, 67 MB 30 / 30,
+    // 100 MB 36 / 31, 132 MB 42 / 34.  fp32, 4 heads of 64, group 4: 24 sequences of up to 8 queries 52 MB 40 / 40, 69 MB 45 / 41, 104 MB
+    // 52 / 45; few rows, 8 heads of 64: 4 sequences 33 MB 23 / 25, 50 MB 28 / 28, 66 MB 30 / 29, 100 MB 38 / 32; 8 of them 33 MB 23 / 23, 50 MB 26 / 24,
+    // 66 MB 29 / 25; 24 of them 50 MB 27 / 25, 66 MB 30 / 26; but 8 heads of 128, group 4: 8 sequences 66 MB 31 / 35, 100 MB 37 / 37.
     const long long bytes = (long long)n * c->kv_heads * longest(*c, most, att_left, att_chunk, sinks) * 2 * c->head_dim;
     const bool few = dtype == CAC_DTYPE_F32 && !kv_prefix_takes(a, std::max(n_groups, 1));
-    if (bytes < (few ? 50000000 : 100000000) || kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
+    if (bytes < (few ? 50000000 : 70000000) || kv_prompt_takes(a, dtype, sms, ((long long)rows * group + n - 1) / n))
         return cac_kv8_attend(c, layer, n, ids, starts, rows, max_new, heads, scale, att_left, att_chunk, sinks, q, q_stride, out,
                               out_stride, lse, dtype, workspace, workspace_bytes, stream);
     DeviceScope dev(c->device);

@@ -236,8 +236,7 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 21);
     const KvAttend& a = p.a;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, D = a.c.head_dim;
-    pdl_wait();
-    const Piece w = find_piece<ROWS>(p);
+    const Piece w = find_piece<ROWS>(p);   // no wait: an ordinary launch (launch_prefix)
     if (w.blocks == 0) {
         pdl_trigger();
         return;
@@ -671,7 +670,7 @@ template <class T, int CODE, int HDP, int TILES> cudaError_t launch_prefix(const
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_k(kernel, dim3(blocks), dim3(S::THREADS), S::XSMEM, s, 1, p);
+    return launch_after(kernel, dim3(blocks), dim3(S::THREADS), S::XSMEM, s, p);   // the pieces run beside it
 }
 // Row tiles of a block: one, which leaves room for more copies ahead, for a group of 128 rows, or several of half as many on average (a larger
 // one among them has its tokens read once more for each 128 of its rows).
@@ -1028,7 +1027,7 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
-    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low,
+    const KvPieces pieces{deal.entries, deal.first, deal.total, n + dealt, n, low, prefix,
                           static_cast<float*>(place(at.o0)), static_cast<float*>(place(at.o1)), static_cast<float*>(place(at.slot_o)),
                           static_cast<float2*>(place(at.ml0)), static_cast<float2*>(place(at.ml1)), static_cast<float2*>(place(at.slot_ml))};
     for (int g0 = 0; prefix && g0 < n_groups; g0 += TA_SEQS) {   // the groups' shared tokens

@@ -170,7 +170,7 @@ size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, 
  *           sequences groups[g] .. groups[g+1]-1 of the call form a group, those
  *           outside all of them share nothing.  NULL with n_groups 0: all form one.
  *           Where groups break this nothing is shared, and CAC_E_BOUNDS is latched
- *           if the call looks at them: one whose sequences have less than 100 MB (50 for
+ *           if the call looks at them: one whose sequences have less than 70 MB (50 for
  *           fp32 queries of up to 32 rows a group) of codes between them at most (n,
  *           max_pages and the window tell), or which cac_kv8_attend takes for prompts, is
  *           done as cac_kv8_attend does it.

@@ -1,6 +1,6 @@
 """Attention of sequences that share a prefix on the GPU: against the plain model in 64
 bits, sequence by sequence, and against what may and may not be shared.  A call that has
-less than 100 MB to read even if it shares nothing is cac_kv8_attend's, so the caches here have
+less than 70 MB to read even if it shares nothing is cac_kv8_attend's, so the caches here have
 tables for far longer sequences than they hold, and calls are asserted to be the shared
 kernels' by the kernels of a captured graph."""
 import warnings
