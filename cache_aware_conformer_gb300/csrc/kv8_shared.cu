@@ -16,7 +16,7 @@
 // the arithmetic of the conversion, it takes as long.
 //
 // What is shared is looked up on the device in each call: blocks of 16 tokens that every query of the group sees whole, in front of the
-// first page in which the tables differ.  Nothing but the sequences' tables is compared, so a result never hangs on what
+// first page of those in which the tables differ.  Nothing but the sequences' tables is compared, so a result never hangs on what
 // the caller believes of them.
 #include <algorithm>
 #include <atomic>
@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
     const int first_block = (s_lo + KV_BLOCK - 1) / KV_BLOCK;
     const bool some = fine && !s_bad && s_members >= 2 && s_hi / KV_BLOCK - first_block >= LEAST_BLOCKS;
 
-    // pages in front of the first one in which a table differs from the leader's: warps take the members in turn
+    // Pages from that of the first block on, in front of the first one in which a table differs from the leader's: warps take the members in
+    // turn.  Pages before those are not read as shared: one sequence may have released more of them than another.
     if (some) {
         const int pages = min((s_hi + a.c.page_tokens - 1) / a.c.page_tokens, a.c.max_pages);
         const int32_t* own = a.c.table + (long long)a.ids[s_leader] * a.c.max_pages;
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
             const int32_t* other = a.c.table + (long long)a.ids[i] * a.c.max_pages;
             if (other == own) continue;
             constexpr int GO = 8;
-            for (int b = 0; b < same; b += 32 * GO) {
+            for (int b = first_block * KV_BLOCK / a.c.page_tokens; b < same; b += 32 * GO) {
                 int x[GO], y[GO];
 #pragma unroll
                 for (int u = 0; u < GO; ++u) {
@@ -971,7 +972,7 @@ template <class T> __global__ void __launch_bounds__(JOIN_WARPS * 32, 4) kv_join
 
 size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
 
-// Where things lie in the workspace.
+// Where things lie in the workspace, each from the next multiple of 16 bytes on.
 struct Space {
     size_t skip, group_of, shared, group_rows, cut, join, entries, first, total, ml0, ml1, slot_ml, prefix_ml, o0, o1, slot_o, prefix_o, bytes;
 };

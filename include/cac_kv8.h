@@ -176,8 +176,9 @@ size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, 
  *           done as cac_kv8_attend does it.
  *   out_stride, lse, max_new, workspace and the rest as there, with
  *           cac_kv8_attend_shared_workspace bytes
- * Tokens are shared in blocks of 16, up to the first page in which the tables of a
- * group differ; a group of one sequence shares nothing. */
+ * Tokens are shared in blocks of 16, from the first that all queries of a group see
+ * up to the first page from there on in which the tables differ; a group of one
+ * sequence shares nothing. */
 int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,
                           int max_new, int n_groups, const int32_t* groups, int heads, float scale, int att_left,
                           int att_chunk, int sinks, const void* q, long long q_stride, void* out, long long out_stride,

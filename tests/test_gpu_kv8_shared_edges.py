@@ -78,3 +78,30 @@ def test_calls_that_attend_answers_sooner_go_to_it(dtype, n, group, heads, dim, 
     got = b.cache.attend_shared(0, ids, q)
     b.cache.check()
     assert torch.equal(got, want) or shares
+
+
+def shared_blocks(call):
+    """The blocks of 16 tokens of each sequence that its group shares, with which the workspace begins."""
+    return call.space[:8 * call.n].view(torch.int32).view(-1, 2).cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype,code", [(F32, "e4m3"), (BF16, "int8")])
+@pytest.mark.parametrize("left,sinks", [(800, 0), (800, 40)])
+def test_members_that_have_released_different_pages_share_the_others(dtype, code, left, sinks):
+    """A sliding window with trim: longer members have released pages that shorter ones still hold, in front of what all see."""
+    n, page = 70, 32
+    rng = np.random.default_rng(7)
+    own = rng.integers(1, 190, n)
+    b = Shared(code, heads=8, dim=128, page=page, n_pages=1200, seqs=n, dtype=dtype, seed=9, least=20)
+    prefixes = [901, 1000]
+    st = b.family([(prefixes[0], own[:30].tolist()), (prefixes[1], own[30:].tolist())])
+    b.trim(range(n), left, 1, sinks)
+    table = b.cache.table.cpu().numpy()
+    assert all(len({tuple(t) for t in table[x:y, :8] < 0}) > 1 for x, y in zip(st, st[1:]))
+    call = Call(b, range(n), b.rand(n, 16, 128), st, left, 1, sinks)
+    call.run()
+    blocks = shared_blocks(call)
+    for (x, y), prefix in zip(zip(st, st[1:]), prefixes):
+        low = prefix + own[x:y].max() - 1 - left
+        assert (blocks[x:y] == [-(-low // 16), prefix // page * page // 16]).all()
+    b.check_shared(range(n), [1] * n, st, left=left, sinks=sinks, uniform=True, q=call.q.cpu())
