@@ -153,19 +153,19 @@ __global__ void __launch_bounds__(PLAN_THREADS) kv_plan_shared_kernel(const __gr
 struct PrefixCall {
     KvAttend a;             // rows: the groups'
     const int4* shared;     // of each group: whose table, and the blocks [y, z)
-    const int2* cut;        // of each group: first piece, and pieces of each unit
+    const int4* cut;        // of each group: first piece, pieces of each unit, first slot of units that are cut
     int groups;             // of this launch
     float* part_o;          // units in one piece: [rows][heads][head_dim]
     float2* part_ml;
-    float* slot_o;          // [block][rows of a block][head_dim] of units that are cut, and
-    float2* slot_ml;        // [block][rows of a block]
+    float* slot_o;          // [slot][rows of a block][head_dim] of pieces of units that are cut, and
+    float2* slot_ml;        // [slot][rows of a block]
 };
 
 // Which piece is block b's
 struct Piece {
     int id, head, row0, r0, rows;    // whose table; K/V head; the group's first row in the call; rows r0 .. r0 + rows - 1 of the group's
     int block0, blocks;              // of 16 tokens; 0: there is no such piece
-    bool cut;
+    int slot;                        // of its results; -1: its unit is not cut
     int halves;                      // of 64 tokens
 };
 template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall& p) {
@@ -173,7 +173,7 @@ template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall
     const int kvh = a.c.kv_heads, b = (int)blockIdx.x;
     Piece q{};
     // groups without pieces are before those with
-    int2 cut;
+    int4 cut;
     int4 sh;
     int first0, row0, row1;
     if (p.groups <= 32) {   // all at once: reads that hang on others take a microsecond each
@@ -181,7 +181,7 @@ template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall
         cut = p.cut[at], sh = p.shared[at], row0 = a.rows.at(at), row1 = a.rows.at(at + 1);
         first0 = __shfl_sync(0xffffffffu, cut.x, 0);
         const int g = __popc(__ballot_sync(0xffffffffu, lane < p.groups && cut.x <= b + first0)) - 1;
-        cut.x = __shfl_sync(0xffffffffu, cut.x, g), cut.y = __shfl_sync(0xffffffffu, cut.y, g);
+        cut.x = __shfl_sync(0xffffffffu, cut.x, g), cut.y = __shfl_sync(0xffffffffu, cut.y, g), cut.z = __shfl_sync(0xffffffffu, cut.z, g);
         sh.x = __shfl_sync(0xffffffffu, sh.x, g), sh.y = __shfl_sync(0xffffffffu, sh.y, g), sh.z = __shfl_sync(0xffffffffu, sh.z, g);
         row0 = __shfl_sync(0xffffffffu, row0, g), row1 = __shfl_sync(0xffffffffu, row1, g);
     } else {
@@ -198,7 +198,7 @@ template <int ROWS> __device__ __forceinline__ Piece find_piece(const PrefixCall
     q.rows = min(ROWS, rows - q.r0);
     q.block0 = sh.y + 8 * t0;
     q.blocks = min(sh.y + 8 * t1, sh.z) - q.block0;
-    q.cut = cut.y > 1;
+    q.slot = cut.y > 1 ? cut.z + in : -1;
     q.halves = (q.blocks + 3) / 4;
     return q;
 }
@@ -445,11 +445,11 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
             tc_fence_after();
             if (ok) {
                 const int query = on ? a.query_of(row) : 0, qh = w.head * a.group + (on ? row - query * a.group : 0);
-                const long long at = w.cut ? (long long)blockIdx.x * ROWS + x * PT_ROWS + r : (w.row0 + (long long)query) * a.heads + qh;
+                const long long at = w.slot >= 0 ? (long long)w.slot * ROWS + x * PT_ROWS + r : (w.row0 + (long long)query) * a.heads + qh;
                 // 32 columns at a time by way of shared memory, where the row tile's queries were: eight threads store 128 bytes of a row (a
                 // row to a thread took 7 us)
                 float* pad = reinterpret_cast<float*>(smem + x * S::PARTS * S::TILE) + (warp & 3) * 32 * 32;
-                float* to = w.cut ? p.slot_o : p.part_o;
+                float* to = w.slot >= 0 ? p.slot_o : p.part_o;
 #pragma unroll
                 for (int c = 0; c < HDP / 32; ++c) {
                     float v[32];
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(PShape<T, HDP, TILES>::THREADS, 1) kv_prefix_k
                                 *reinterpret_cast<const float4*>(pad + of * 32 + (((lane ^ of) & 7) << 2));
                     }
                 }
-                if (on) (w.cut ? p.slot_ml : p.part_ml)[at] = make_float2(m, l);
+                if (on) (w.slot >= 0 ? p.slot_ml : p.part_ml)[at] = make_float2(m, l);
             }
         }
     } else if (warp < S::SOFT + S::CONV) {
@@ -704,19 +704,21 @@ struct DealCall {
     const int32_t *group_rows, *group_of;
     KvEntry* entries;          // [n + n_groups]
     int32_t *first, *total;
-    int2* cut;                 // [n_groups] kv_prefix_kernel's pieces: first, and of each unit
+    int4* cut;                 // [n_groups] kv_prefix_kernel's pieces: first, of each unit, first slot
     KvJoin* join;              // [n]
     int n_groups, most;        // pieces to aim at
     int prefix_rows;           // query rows of kv_prefix_kernel's units; 0: the groups are entries
-    int prefix_most;           // pieces that units may be cut for there; 0: none are cut
+    int prefix_most;           // pieces to aim at there
 };
 constexpr int DEAL_THREADS = 1024, LEAST_TILES = 8;
 
 // One list of units dealt out: entry i has units(i) of tiles(i) tiles, of which each is cut into ceil(tiles / share) pieces; put(i, cuts,
 // pieces before, pieces of cut units before).  The share is that of `most` even pieces, at least `least`, or up to twice
-// as much where no more than `most` pieces come of it, which run at once (each begins with some us of dependent reads).  Returns the
-// pieces in all.  strict: no more than `most` pieces where units are cut at all.  A whole block calls it.
-template <class F, class G, class P> __device__ __forceinline__ int deal_out(int count, int most, int least, bool strict, F units, G tiles, P put) {
+// as much where no more than `most` pieces come of it, which run at once (each begins with some us of dependent reads).  Where that many
+// do not come out, because units alone are as many, longer ones are still cut: no block has more than an even share at a time.  Returns the pieces
+// in all, at most the units and `most`; pieces of cut units are 2 `most` at most, since a unit of more than a share has less than twice as many
+// pieces as shares.  A whole block calls it.
+template <class F, class G, class P> __device__ __forceinline__ int deal_out(int count, int most, int least, F units, G tiles, P put) {
     __shared__ long long s_tiles[32];
     __shared__ int s_tries[32], s_pieces[32], s_slots[32];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -745,7 +747,7 @@ template <class F, class G, class P> __device__ __forceinline__ int deal_out(int
     pieces = 0;
     int slots = 0;   // before this round's entries
     for (int i0 = 0; i0 < count; i0 += DEAL_THREADS) {
-        const int i = i0 + t, u = i < count ? units(i) : 0, cuts = u ? fit || !strict ? (int)(((uint32_t)tiles(i) + share - 1) / share) : 1 : 0;
+        const int i = i0 + t, u = i < count ? units(i) : 0, cuts = u ? (int)(((uint32_t)tiles(i) + share - 1) / share) : 0;
         const int n = u * cuts, held = cuts > 1 ? n : 0;
         int x = n, y = held;
         for (int d = 1; d < 32; d <<= 1) {
@@ -801,7 +803,7 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
     if (p.prefix_rows && t < groups) my_shared = p.shared[t], my_rows = p.group_rows[t + 1] - p.group_rows[t];
     __syncthreads();
     const int pieces = deal_out(
-        count, p.most, LEAST_TILES, false, [&](int i) { return i < DEAL_THREADS ? s_units[i] : units_of(p.entries[i].s); },
+        count, p.most, LEAST_TILES, [&](int i) { return i < DEAL_THREADS ? s_units[i] : units_of(p.entries[i].s); },
         [&](int i) { return i < DEAL_THREADS ? s_tiles[i] : p.entries[i].s.tiles; },
         [&](int i, int cuts, int first, int slot) {
             KvEntry& e = p.entries[i];
@@ -819,11 +821,11 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
         if (t < groups) s_units[t] = units(my_shared, my_rows), s_tiles[t] = tiles(my_shared);
         __syncthreads();
         deal_out(
-            groups, p.prefix_most, 2, true, [&](int g) { return g < DEAL_THREADS ? s_units[g] : group_units(g); },
+            groups, p.prefix_most, 2, [&](int g) { return g < DEAL_THREADS ? s_units[g] : group_units(g); },
             [&](int g) { return g < DEAL_THREADS ? s_tiles[g] : group_tiles(g); },
-            [&](int g, int cuts, int first, int) {
-                p.cut[g] = make_int2(first, cuts);
-                if (g < DEAL_THREADS) s_cut[0][g] = cuts, s_cut[1][g] = first;
+            [&](int g, int cuts, int first, int slot) {
+                p.cut[g] = make_int4(first, cuts, slot, 0);
+                if (g < DEAL_THREADS) s_cut[0][g] = cuts, s_cut[1][g] = slot;
             });
     }
     __syncthreads();   // what the block has written to memory is read back below
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
             const int g = i == t ? my_group : p.group_of[i];
             row = i == t ? my_row : p.group_rows[g];
             if (g < DEAL_THREADS) cuts = s_cut[0][g], slot = s_cut[1][g];
-            else if (p.prefix_rows) cuts = p.cut[g].y, slot = p.cut[g].x;
+            else if (p.prefix_rows) cuts = p.cut[g].y, slot = p.cut[g].z;
             else cuts = p.entries[n + g].cuts, slot = p.entries[n + g].slot;
         }
         j.common_cuts = cuts, j.common_slot = slot, j.common_row = row;
@@ -985,9 +987,9 @@ Space space_of(const cac_kv8& c, int n, int rows, int n_groups, int heads, int s
         return was;
     };
     const size_t units = (size_t)rows * heads, D = c.head_dim;
-    const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim, true) * 16, prefix = c.head_dim <= 128 ? (size_t)sms * 2 * PT_ROWS : 0;
+    const size_t slots = (size_t)2 * sms * piece_blocks(c.head_dim, true) * 16, prefix = c.head_dim <= 128 ? (size_t)2 * sms * 2 * PT_ROWS : 0;
     s.skip = take((size_t)n * 8), s.group_of = take((size_t)n * 4), s.shared = take((size_t)n_groups * 16);
-    s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 8);
+    s.group_rows = take(((size_t)n_groups + 1) * 4), s.cut = take((size_t)n_groups * 16);
     s.join = take((size_t)n * sizeof(KvJoin));
     s.entries = take(((size_t)n + n_groups) * sizeof(KvEntry)), s.first = take(((size_t)n + n_groups) * 4), s.total = take(4);
     s.ml0 = take(units * 8), s.ml1 = take(units * 8), s.slot_ml = take(slots * 8), s.prefix_ml = take(prefix * 8);
@@ -1021,10 +1023,9 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
     const bool low = (long long)call.max_new * call.group <= 8 && (prefix || (long long)rows * call.group <= 8);
     const int most = sms * piece_blocks(c.head_dim, low), dealt = prefix ? 0 : n_groups;
     const int tiles = prefix_tiles(call, dtype, n_groups), block = tiles * PT_ROWS;
-    // Units of kv_prefix_kernel may be cut where one launch has all groups: the slots are the blocks'.
     const DealCall deal{a, plan.shared, plan.group_rows, plan.group_of, static_cast<KvEntry*>(place(at.entries)),
-                        static_cast<int32_t*>(place(at.first)), static_cast<int32_t*>(place(at.total)), static_cast<int2*>(place(at.cut)),
-                        static_cast<KvJoin*>(place(at.join)), n_groups, most, prefix ? block : 0, n_groups <= TA_SEQS ? sms : 0};
+                        static_cast<int32_t*>(place(at.first)), static_cast<int32_t*>(place(at.total)), static_cast<int4*>(place(at.cut)),
+                        static_cast<KvJoin*>(place(at.join)), n_groups, most, prefix ? block : 0, sms};
     e = launch_k(kv_deal_kernel, dim3(1), dim3(DEAL_THREADS), 0, s, 1, deal);
     if (e != cudaSuccess) return e;
 
@@ -1038,7 +1039,9 @@ cudaError_t kv_attend_shared(const KvAttend& call, int dtype, const int32_t* gro
         const PrefixCall p{b, plan.shared + g0, deal.cut + g0, b.rows.n, pieces.o1, pieces.ml1, static_cast<float*>(place(at.prefix_o)),
                            static_cast<float2*>(place(at.prefix_ml))};
         const long long units = ((long long)rows * call.group / block + b.rows.n) * c.kv_heads;
-        const unsigned blocks = (unsigned)std::max<long long>(units, sms);
+        // As many blocks as there may be pieces.  A third as many units as SMs or less, all in this launch, can always be cut into one piece an SM
+        // (the largest share that is tried is one and a half times the even one at least).
+        const unsigned blocks = (unsigned)(n_groups <= TA_SEQS && units <= sms / 3 ? sms : units + sms);
         if (c.code == CAC_KV8_INT8)
             e = dtype == CAC_DTYPE_BF16 ? launch_prefix<bf16, CAC_KV8_INT8>(p, tiles, blocks, s) : launch_prefix<float, CAC_KV8_INT8>(p, tiles, blocks, s);
         else

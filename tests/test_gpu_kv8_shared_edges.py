@@ -4,6 +4,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+from _kv8 import attend64, bounds  # noqa: E402
 from test_gpu_kv8 import Both  # noqa: E402
 from test_gpu_kv8_shared import Shared  # noqa: E402
 
@@ -80,6 +81,17 @@ def test_calls_that_attend_answers_sooner_go_to_it(dtype, n, group, heads, dim, 
     assert torch.equal(got, want) or shares
 
 
+def at64(b, i, out, q, group):
+    """The result of sequence i's one query against 64 bits, with the bounds of Shared.check_shared."""
+    c = b.cfg
+    ref = attend64(b.seqs[i], 0, q.double().cpu().numpy(), group, c.head_dim ** -0.5, -1, 1, 0, c.page_tokens)
+    tol, _ = bounds(*ref, c.head_dim, b.seqs[i].len, b.dtype)
+    top = float(b.seqs[i].values(0, "v")[1].max()) * (127 if c.code == "int8" else 448)
+    tol = tol + 2 * (2.0 ** -21 + 2.0 ** -22) * ref[2] + b.seqs[i].len * top * (2.0 ** -32 if b.dtype is BF16 else 2.0 ** -38)
+    err = np.abs(out.double().cpu().numpy() - ref[0])
+    assert (err <= tol).all(), (i, float((err / tol).max()), float(err.max()))
+
+
 def shared_blocks(call):
     """The blocks of 16 tokens of each sequence that its group shares, with which the workspace begins."""
     return call.space[:8 * call.n].view(torch.int32).view(-1, 2).cpu().numpy()
@@ -105,3 +117,46 @@ def test_members_that_have_released_different_pages_share_the_others(dtype, code
         low = prefix + own[x:y].max() - 1 - left
         assert (blocks[x:y] == [-(-low // 16), prefix // page * page // 16]).all()
     b.check_shared(range(n), [1] * n, st, left=left, sinks=sinks, uniform=True, q=call.q.cpu())
+
+
+def pieces_of_units(call):
+    """Into how many pieces the kernel for many rows cuts each unit of a group's shared tokens: the workspace has 8 bytes and 4 for each
+    sequence, 16 and 4 for each group and 4 more, then (first piece, pieces, first slot, 0) of each group."""
+    up, g = lambda x: -(-x // 16) * 16, max(call.n_groups, 1)  # noqa: E731
+    at = up(8 * call.n) + up(4 * call.n) + up(16 * g) + up(4 * (g + 1))
+    return call.space[at:at + 16 * g].view(torch.int32).view(-1, 4)[:, 1].cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("code,heads,dim,group,each", [("int8", 8, 64, 4, 9), ("e4m3", 7, 128, 16, 20), ("int8", 8, 32, 32, 10)])
+def test_a_long_prefix_among_short_ones_is_cut(dtype, code, heads, dim, group, each):
+    """More units than SMs, of groups of which one is far longer: no block gets all of its tokens."""
+    groups, long = 24, 5
+    n = groups * each
+    rng = np.random.default_rng(groups)
+    b = Shared(code, heads=heads, dim=dim, page=64, n_pages=700 + 3 * n, seqs=n, dtype=dtype, seed=dim)
+    st = b.family([(12000 if g == long else int(rng.integers(64, 500)), rng.integers(1, 60, each).tolist()) for g in range(groups)])
+    call = Call(b, range(n), b.rand(n, heads * group, dim), st)
+    got = call.run()
+    cuts = pieces_of_units(call)
+    assert cuts[long] > 4 and (np.delete(cuts, long) == 1).all()
+    b.cache.check()
+    for x, y in ((st[long], st[long + 1]), (0, st[2])):
+        for i in range(x, y, 7):
+            at64(b, i, got[i:i + 1], call.q[i:i + 1], group)
+
+
+@pytest.mark.parametrize("long", [3, 540])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_more_groups_than_a_launch_takes_with_a_long_one(dtype, long):
+    """550 groups over two launches, one of them far longer than the others: in the first launch, or the last."""
+    groups, group = 550, 20
+    b = Shared("int8", heads=1, dim=32, page=16, n_pages=9000, seqs=2 * groups, dtype=dtype, seed=long)
+    st = b.family([(30000 if g == long else 16 + g % 50, [1 + g % 3, 2]) for g in range(groups)])
+    call = Call(b, range(2 * groups), b.rand(2 * groups, group, 32), st)
+    got = call.run()
+    b.cache.check()
+    cuts = pieces_of_units(call)
+    assert cuts[long] > 20 and (np.delete(cuts, long) == 1).all()
+    for i in (0, 1, 2 * long - 1, 2 * long, 2 * long + 1, 2 * long + 2, 1023, 1024, 1025, 1099):
+        at64(b, i, got[i:i + 1], call.q[i:i + 1], group)
