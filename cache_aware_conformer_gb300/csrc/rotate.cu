@@ -235,8 +235,10 @@ __global__ void __launch_bounds__(ROT_THREADS, 8) rotate_kernel(const __grid_con
                 again = group_sum(on ? again : 0.f, a.lanes_log2);
                 if (huge) sum = again, eps = 0.f;
             }
-            // the approximate root (2 units in the last place) and one step of Newton's method
-            const float mean = sum * a.inv_dim + eps, y = rsqrtf(mean), inv = fmaf(y, 0.5f * fmaf(-mean * y, y, 1.f), y);
+            // The approximate root (2 units in the last place) and one step of Newton's method; beside an infinity finite elements become 0, and
+            // the step would make a NaN of the root's 0.
+            const float mean = sum * a.inv_dim + eps, y = rsqrtf(mean);
+            const float inv = mean < INFINITY ? fmaf(y, 0.5f * fmaf(-mean * y, y, 1.f), y) : y;
             if (mine)
 #pragma unroll
                 for (int b = 0; b < 2; ++b)

@@ -87,9 +87,10 @@ int cac_op_gemm_w4(const cac_w4* w, int M, const void* A, long long a_stride, co
  *     b' = amplitude * (a sin(p f_i) + b cos(p f_i))
  *   CAC_ROTARY_HALF:  a, b = elements i and i + rot_dim / 2
  *   CAC_ROTARY_PAIRS: a, b = elements 2 i and 2 i + 1
- * Elements from rot_dim on are u's.  Arithmetic is fp32, rounded once; the angle
- * p f_i is a whole product of p and steps[i], exact to 2^-33 of a turn at any
- * position. */
+ * Elements from rot_dim on are u's.  With a gain, a NaN makes its head NaN; an
+ * infinity becomes NaN itself (in its pair), and the finite elements beside it 0.
+ * Arithmetic is fp32, rounded once; the angle p f_i is a whole product of p and
+ * steps[i], exact to 2^-33 of a turn at any position. */
 #define CAC_ROTARY_HALF  0
 #define CAC_ROTARY_PAIRS 1
 

@@ -164,6 +164,32 @@ def test_norms_of_zero_tiny_huge_and_non_finite_heads(native, dtype):
     assert torch.equal(got.cpu()[~hit], want.cpu()[~hit]) and not torch.isfinite(got.cpu()[hit]).any()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout,R", [("half", 64), ("half", 34), ("pairs", 64), ("pairs", 20), ("half", 0)])
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_norm_of_a_head_with_an_infinity(native, dtype, layout, R, bad):
+    """x / infinity: 0 where x is finite, NaN for the infinity, which reaches the other element of its pair."""
+    g = torch.Generator().manual_seed(14)
+    D = 64
+    r = native.Rotary(RotaryConfig(head_dim=D, rot_dim=R, layout=layout), (1 + 0.2 * torch.randn(D, generator=g)).cuda())
+    q = rows(g, 6, 3, D, dtype)
+    pos = torch.arange(6, dtype=torch.int32).cuda() * 77
+    want, _ = r.rotate(pos, q.cuda())
+    for e in (0, 3, 16, 17, 33, 63):
+        x = q.clone()
+        x[2, 1, e] = bad
+        got, _ = r.rotate(pos, x.cuda())
+        half = R // 2
+        pair = {e} if e >= R else {e, e ^ 1} if layout == "pairs" else {e, e + half if e < half else e - half}
+        hit = torch.zeros(D, dtype=torch.bool)
+        hit[sorted(pair)] = True
+        head = got[2, 1].float().cpu()
+        assert torch.isnan(head[hit]).all() and (head[~hit] == 0).all(), e
+        keep = torch.ones(6, 3, dtype=torch.bool)
+        keep[2, 1] = False
+        assert torch.equal(got.cpu()[keep], want.cpu()[keep])
+
+
 def make_cache(native, lens, heads=2, dim=64, page=16):
     cfg = Kv8Config(1, heads, dim, page, 1, len(lens), max(max(lens) // page + 1, 1))
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
