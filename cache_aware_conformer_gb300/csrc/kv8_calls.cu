@@ -125,9 +125,17 @@ extern "C" size_t cac_kv8_attend_shared_workspace(const cac_kv8* c, int n, int r
     (void)att_left;
     if (kv_check_shape(c) != CAC_OK || n < 1 || rows < 1 || max_new < 0 || n_groups < 0 || heads < 1 || att_chunk < 1 || sinks < 0)
         return 0;
-    // attend's too: a call that it answers better goes to it
-    return std::max(kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sm_count(c->device)),
-                    kv_attend_bytes(c->head_dim, sm_count(c->device)));
+    // attend's too: a call that it answers better goes to it.  Prompts always do, whose sums of both kinds would take twice what their results
+    // in fp32 take (80 of 1,000 rows with 64 heads of 128: 5.2 GB).
+    const int sms = sm_count(c->device);
+    if (sms >= 1) {
+        KvAttend a{};
+        a.c = *c, a.rows.n = n;
+        const long long each = ((long long)rows * (heads / c->kv_heads) + n - 1) / n;
+        if (kv_prompt_takes(a, CAC_DTYPE_BF16, sms, each) && kv_prompt_takes(a, CAC_DTYPE_F32, sms, each))
+            return kv_attend_bytes(c->head_dim, sms);
+    }
+    return std::max(kv_shared_bytes(*c, n, rows, std::max(n_groups, 1), heads, sms), kv_attend_bytes(c->head_dim, sms));
 }
 
 extern "C" int cac_kv8_attend_shared(const cac_kv8* c, int layer, int n, const int32_t* ids, const int32_t* starts, int rows,

@@ -160,3 +160,18 @@ def test_more_groups_than_a_launch_takes_with_a_long_one(dtype, long):
     assert cuts[long] > 20 and (np.delete(cuts, long) == 1).all()
     for i in (0, 1, 2 * long - 1, 2 * long, 2 * long + 1, 2 * long + 2, 1023, 1024, 1025, 1099):
         at64(b, i, got[i:i + 1], call.q[i:i + 1], group)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_prompts_need_no_workspace_of_their_own_kind(dtype):
+    """Calls that attend's kernel for prompts takes ask for attend's workspace, not for sums of all of their rows."""
+    b = Shared("int8", heads=2, dim=64, page=32, n_pages=400, seqs=80, dtype=dtype)
+    b.family([(300, [100] * 80)])
+    lib, ref = b.native.lib(), b.cache._ref
+    for rows, heads in ((8000, 4), (80000, 64)):
+        need = lib.cac_kv8_attend_shared_workspace(ref, 80, rows, rows // 80, 0, heads, -1, 1, 0)
+        assert need == lib.cac_kv8_attend_workspace(ref, 80, rows, rows // 80, heads, -1, 1, 0) > 0
+    q = b.rand(8000, 4, 64).cuda()
+    got = b.cache.attend_shared(0, b.ids(range(80)), q)
+    assert torch.equal(got, b.cache.attend(0, b.ids(range(80)), q))
+    b.cache.check()
