@@ -206,3 +206,45 @@ def test_two_streams_at_once(native):
     torch.cuda.synchronize()
     for _, want, got, *_ in cases:
         assert all(torch.equal(g, want) for g in got)
+
+
+def spread(a, packed, scale, zero):
+    """(result in 64 bits, root of the sum of squares of its products) of fp32 rows."""
+    w = w4.dequantize(packed, scale, zero)
+    x = a.double()
+    return x @ w.T, torch.sqrt((x * x) @ (w * w).T)
+
+
+def rms_bound(K):
+    """Largest root mean square of a deep fp32 result's error, over the root of the sum of squares S of its products, whose signs are
+    random.
+
+    An element of A as two fp16 parts is off by 2^-22 of itself at most: 2^-22 S together, since signs are random.  A sum of 32
+    products takes four tensor-core steps (two of each part) that cut off 2^-23 of the partial sum at most; the sums of 32 are of random
+    signs too, and their squares add up to S^2: 2^-21 S.  K / 32 + 32 sums are added in fp32, each rounded by 2^-24 of the running
+    sum at most, which grows with the root of its length: 2^-24 S sqrt(sum of j / n) = 2^-24 S sqrt(n / 2).  The scale's product and the last
+    sums: 2^-22 S.  A mean over 40 or more results is within twice its expectation."""
+    n = K / 32 + 32
+    return 2 * (2.0 ** -22 + 2.0 ** -21 + 2.0 ** -24 * (n / 2) ** 0.5 + 2.0 ** -22)
+
+
+def fp16_part(a):
+    """What the first of the two fp16 parts holds of fp32 rows: 11 bits under the largest of 256."""
+    x = a.view(a.size(0), -1, 256)
+    up = torch.exp2(14 - torch.floor(torch.log2(x.abs().amax(-1, keepdim=True))))
+    return ((x * up).half().float() / up).view_as(a)
+
+
+@pytest.mark.parametrize("M,N,K,group", [(24, 500, 8192, 32), (5, 48, 32768, 64), (9, 40, 65536, 128), (31, 40, 40960, 128), (3, 40, 131072, 128),
+                                         (1, 64, 131072, 128), (2, 600, 16384, 64)])
+def test_deep_fp32_rows_keep_both_parts(native, M, N, K, group):
+    """The bound of test_deep_rows, a worst case that grows with the depth, would not see the low parts left out; the mean error does."""
+    a, packed, scale, zero, _ = make(M, N, K, group, True, False, F32)
+    want, S = spread(a, packed, scale, zero)
+    off = lambda y: float(((y.double() - want) / S).square().mean().sqrt())  # noqa: E731
+    # the oracle without the low parts, and without one group: both are far outside
+    w = w4.dequantize(packed, scale, zero)
+    assert off(fp16_part(a).double() @ w.T) > 20 * rms_bound(K)
+    assert off(a[:, group:].double() @ w[:, group:].T) > 20 * rms_bound(K)
+    got = native.gemm_w4(a.cuda(), packed.cuda(), scale.cuda(), zero=zero.cuda())
+    assert off(got.cpu()) <= rms_bound(K), (off(got.cpu()), rms_bound(K))
