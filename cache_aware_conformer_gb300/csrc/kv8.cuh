@@ -116,7 +116,7 @@ struct KvAttend {
     float scale;
     int layer, heads, group, max_new;
     uint32_t group_mul;  // 2^32 / group, rounded down, + 1 (0 for a group of 1)
-    const int2* skip;    // blocks [x, y) of each sequence that are left out, or null (kv8_shared.cu)
+    const int2* skip;    // blocks [x, y) of each sequence that are read apart (kv8_shared.cu)
     // row / group of a row below 2^32: the product is the quotient or one more
     __device__ __forceinline__ int query_of(int row) const {
         if (group_mul == 0) return row;

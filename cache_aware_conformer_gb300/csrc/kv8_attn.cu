@@ -77,8 +77,8 @@ struct Tile {
     float ks, lv, iv;          // K scale; log2 and reciprocal of the V scale (0 where that is FAR)
     int j0;                    // its first token
 };
-template <int CODE>
-__device__ __forceinline__ Tile tile_of(const KvAttend& a, const SeqWork& s, int kt, int head) {
+template <int CODE, class W>
+__device__ __forceinline__ Tile tile_of(const KvAttend& a, const W& s, int kt, int head) {
     Tile t{-1, 0.f, 0.f, 0.f, 0};
     t.j0 = s.block(kt) * KV_BLOCK;
     if (t.j0 < s.len) {
@@ -160,11 +160,11 @@ __device__ __forceinline__ float load_query(const T* src, bool on, int t, int D,
 // for all of them between lo_max and hi_min.
 struct Seen {
     int lo_max, hi_min, lo_min, hi_max;
+    __device__ __forceinline__ void set(const KvAttend& a, const PieceWork& s, int r0, int size) {
+        if (s.whole) hi_min = hi_max = s.len, lo_max = lo_min = s.lot * KV_BLOCK;
+        else set(a, static_cast<const SeqWork&>(s), r0, size);
+    }
     __device__ __forceinline__ void set(const KvAttend& a, const SeqWork& s, int r0, int size) {
-        if (s.whole) {
-            hi_min = hi_max = s.len, lo_max = lo_min = s.lot * KV_BLOCK;
-            return;
-        }
         // rows in order of their positions: the first and last bound the windows
         const int p0 = s.len - s.m + a.query_of(r0), p1 = s.len - s.m + a.query_of(min(r0 + size, s.m * a.group) - 1);
         const bool any = s.len > 0 && p1 >= 0;
@@ -248,7 +248,7 @@ template <class T, int CODE, int HDP> struct Rows : Seen {
     int low[2], high[2];
 
     // Queries of K/V head `head`, rows r0 .. r0 + 15 of the sequence's m * group
-    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
+    template <class W> __device__ __forceinline__ void load(const KvAttend& a, const W& s, int head, int r0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim;
         set(a, s, r0, 16);
 #pragma unroll
@@ -462,7 +462,7 @@ template <class T, int CODE, int HDP> struct RowsLow : Seen {
     float m[2], l[2], f[2];                               // of rows 2 t, 2 t + 1
     int low[2], high[2];
 
-    __device__ __forceinline__ void load(const KvAttend& a, const SeqWork& s, int head, int r0) {
+    template <class W> __device__ __forceinline__ void load(const KvAttend& a, const W& s, int head, int r0) {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, D = a.c.head_dim;
         set(a, s, r0, 8);
         const int r = r0 + g, query = a.query_of(r);
@@ -1035,7 +1035,7 @@ template <class T, int HDP, bool LOW> struct PieceShape {
     static_assert(BLOCKS * (BYTES + 1024) <= 227 * 1024, "shared memory");
 };
 template <class T, int CODE, int HDP, bool LOW, bool ALL_LOW>
-__device__ __forceinline__ void piece_sums(const KvAttend& a, const SeqWork& s, int head, int r0, int x0, int x1, uint8_t* ring,
+__device__ __forceinline__ void piece_sums(const KvAttend& a, const PieceWork& s, int head, int r0, int x0, int x1, uint8_t* ring,
                                            const Partials& sums) {
     using P = PieceShape<T, HDP, ALL_LOW>;
     constexpr int STAGES = P::STAGES, STAGE = P::STAGE, CH = HDP / 16;

@@ -67,20 +67,14 @@ __device__ __forceinline__ float move_norm(float l, float d, float r) {
 // What a sequence of the call asks for.
 struct SeqWork {
     int id, len, m, row0;      // len 0: nothing is seen
-    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1, where none are left out)
-    int gap0, gap;             // from block gap0 on, gap blocks are left out
-    bool whole;                // rows of several sequences that all see all of these blocks (kv8_shared.cu)
-    __device__ __forceinline__ int block(int kt) const {
-        if (kt < skt) return kt;
-        const int b = lot + kt - skt;
-        return b < gap0 ? b : b + gap;
-    }
+    int lot, skt, tiles;       // its window's first block, the sink blocks before it, blocks in all (at least 1)
+    __device__ __forceinline__ int block(int kt) const { return kt < skt ? kt : lot + kt - skt; }
 };
 __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
     SeqWork s;
     s.row0 = a.rows.at(i);
     s.m = a.rows.at(i + 1) - s.row0;
-    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1, s.gap0 = 0, s.gap = 0, s.whole = false;
+    s.len = 0, s.lot = 0, s.skt = 0, s.tiles = 1;
     s.id = a.ids[i];
     const bool rows_ok = s.m >= 0 && s.row0 >= 0 && s.row0 + (long long)s.m <= a.rows.rows;
     if (!rows_ok) s.m = 0;
@@ -94,25 +88,42 @@ __device__ __forceinline__ SeqWork seq_work(const KvAttend& a, int i) {
         s.lot = low / KV_BLOCK;
         s.skt = min((min(a.win.sinks, high) + KV_BLOCK - 1) / KV_BLOCK, s.lot);
         s.tiles = s.skt + (high + KV_BLOCK - 1) / KV_BLOCK - s.lot;
-        if (a.skip) {
-            const int2 k = a.skip[i];
-            s.gap0 = k.x, s.gap = k.y - k.x;
-            s.tiles -= s.gap;
-        }
     }
     return s;
 }
-
-// The position of a row's query, and the tokens that it sees.
+// The tokens that a row's query sees.
 struct RowSeen {
-    bool on;
     int low, high;
 };
 __device__ __forceinline__ RowSeen row_seen(const KvAttend& a, const SeqWork& s, int row) {
-    if (s.whole) return {row < s.m * a.group, s.lot * KV_BLOCK, s.len};
     const int p = s.len - s.m + a.query_of(row);
     const bool on = row < s.m * a.group && p >= 0 && s.len > 0;
-    return {on, on ? a.win.low(p) : 0, on ? a.win.high(p, s.len) : 0};
+    return {on ? a.win.low(p) : 0, on ? a.win.high(p, s.len) : 0};
+}
+
+// Of a call that reads some blocks apart (kv8_shared.cu): a sequence's work without those, which may leave it no blocks, or the work on those, as
+// rows of several sequences.  A type of its own: the other calls do without the tests (windows of 4,095 tokens took 0.7 % longer with them).
+struct PieceWork : SeqWork {
+    int gap0, gap;             // from block gap0 on, gap blocks are left out
+    bool whole;                // the rows all see all of the blocks
+    __device__ __forceinline__ int block(int kt) const {
+        if (kt < skt) return kt;
+        const int b = lot + kt - skt;
+        return b < gap0 ? b : b + gap;
+    }
+};
+__device__ __forceinline__ PieceWork piece_work(const KvAttend& a, int i) {
+    PieceWork s{seq_work(a, i), 0, 0, false};
+    if (s.len > 0 && s.m > 0) {
+        const int2 k = a.skip[i];
+        s.gap0 = k.x, s.gap = k.y - k.x;
+        s.tiles -= s.gap;
+    }
+    return s;
+}
+__device__ __forceinline__ RowSeen row_seen(const KvAttend& a, const PieceWork& s, int row) {
+    if (s.whole) return {s.lot * KV_BLOCK, s.len};
+    return row_seen(a, static_cast<const SeqWork&>(s), row);
 }
 
 constexpr int TA_SEQS = 512;     // sequences of one launch of kv8_attn.cu's kernels
@@ -126,7 +137,7 @@ size_t kv_attend_bytes(int head_dim, int sms);
 // Units of a call cut into pieces, a block each (kv8_shared.cu): an entry is a sequence or a group of them, its units are its K/V heads and
 // tiles of 16 query rows.
 struct KvEntry {
-    SeqWork s;
+    PieceWork s;
     int cuts;              // pieces of each unit; 0: the entry has none
     int first, slot;       // its first piece, and slot of its results where it is cut
 };

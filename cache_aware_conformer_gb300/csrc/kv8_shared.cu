@@ -777,16 +777,16 @@ __global__ void __launch_bounds__(DEAL_THREADS) kv_deal_kernel(const __grid_cons
     pdl_wait();
     const KvAttend& a = p.a;
     const int n = a.rows.n, groups = p.n_groups, count = n + (p.prefix_rows ? 0 : groups), t = threadIdx.x, kvh = a.c.kv_heads;
-    auto units_of = [&](const SeqWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
+    auto units_of = [&](const PieceWork& s) { return s.len > 0 && s.tiles > 0 ? (s.m * a.group + 15) / 16 * kvh : 0; };
     for (int i = t; i < count; i += DEAL_THREADS) {
-        SeqWork s;
+        PieceWork s;
         if (i < n) {
-            s = seq_work(a, i);
+            s = piece_work(a, i);
             p.join[i].named = s.id >= 0 && s.id < a.c.max_seqs && s.m <= a.max_new;
         } else {
             const int4 sh = p.shared[i - n];
             const int row0 = p.group_rows[i - n];
-            s = SeqWork{sh.x, sh.z * KV_BLOCK, p.group_rows[i - n + 1] - row0, row0, sh.y, 0, sh.z - sh.y, 0, 0, true};
+            s = PieceWork{{sh.x, sh.z * KV_BLOCK, p.group_rows[i - n + 1] - row0, row0, sh.y, 0, sh.z - sh.y}, 0, 0, true};
         }
         p.entries[i].s = s;
         if (i < DEAL_THREADS) s_units[i] = units_of(s), s_tiles[i] = s.tiles;
