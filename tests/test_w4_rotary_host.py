@@ -124,6 +124,12 @@ def test_bad_frequencies_are_refused(native, kw):
     assert native.lib().cac_op_rotary_steps(64, 10.0, 0, 1.0, 0.0, 0.0, 1.0, None) == INVAL
 
 
+@pytest.mark.parametrize("low,high", [(-math.inf, 32.0), (1.0, math.inf), (-math.inf, math.inf), (math.nan, 32.0), (1.0, math.nan), (-1e308, 1e308)])
+def test_a_ramp_between_turns_that_are_no_numbers_is_refused(native, low, high):
+    """Its share of a frequency would be a NaN, and the step any number."""
+    assert steps(native, 64, scaling=3, factor=4.0, original=1000.0, low=low, high=high)[0] == INVAL
+
+
 def test_no_rotation_has_no_steps(native):
     assert steps(native, 0)[0] == 0
 
