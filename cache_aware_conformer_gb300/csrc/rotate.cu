@@ -389,7 +389,7 @@ extern "C" int cac_op_rotary_steps(int rot_dim, double base, int scaling, double
                                    double high, uint64_t* steps) {
     if (rot_dim < 0 || rot_dim % 2 || rot_dim > 256 || !(base > 1.0) || !(factor >= 1.0) || base > 1e300 || factor > 1e300 ||
         scaling < CAC_ROTARY_NONE || scaling > CAC_ROTARY_RAMP || (rot_dim && !steps) ||
-        (scaling == CAC_ROTARY_BASE && rot_dim == 2) || (scaling == CAC_ROTARY_RAMP && (!(original > 0.0) || !(high > low) || !(high - low <= 1e300))))
+        (scaling == CAC_ROTARY_BASE && rot_dim == 2) || (scaling == CAC_ROTARY_RAMP && (!(original > 0.0) || !(high > low) || !(low >= -1e300))))
         return CAC_E_INVAL;
     const double two_pi = 6.283185307179586476925286766559;
     if (scaling == CAC_ROTARY_BASE && rot_dim > 2) base *= pow(factor, (double)rot_dim / (rot_dim - 2));

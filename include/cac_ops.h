@@ -116,7 +116,7 @@ typedef struct cac_rotary {
 #define CAC_ROTARY_RAMP   3 /* f * (r + (1 - r) / factor), r from 0 to 1 as f's turns over `original` tokens go from low to high */
 
 /* Writes rot_dim / 2 steps to host memory.  base > 1, factor >= 1; original > 0
- * and finite low < high for CAC_ROTARY_RAMP.  No GPU is needed. */
+ * and high > low >= -1e300 for CAC_ROTARY_RAMP.  No GPU is needed. */
 int cac_op_rotary_steps(int rot_dim, double base, int scaling, double factor, double original, double low, double high,
                         uint64_t* steps);
 

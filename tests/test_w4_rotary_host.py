@@ -124,7 +124,11 @@ def test_bad_frequencies_are_refused(native, kw):
     assert native.lib().cac_op_rotary_steps(64, 10.0, 0, 1.0, 0.0, 0.0, 1.0, None) == INVAL
 
 
-@pytest.mark.parametrize("low,high", [(-math.inf, 32.0), (1.0, math.inf), (-math.inf, math.inf), (math.nan, 32.0), (1.0, math.nan), (-1e308, 1e308)])
+def test_a_ramp_without_an_upper_end_divides_all(native):
+    assert steps(native, 64, scaling=3, factor=4.0, original=1000.0, high=math.inf) == steps(native, 64, scaling=1, factor=4.0)
+
+
+@pytest.mark.parametrize("low,high", [(-math.inf, 32.0), (-math.inf, math.inf), (math.nan, 32.0), (1.0, math.nan), (-1e308, 1e308)])
 def test_a_ramp_between_turns_that_are_no_numbers_is_refused(native, low, high):
     """Its share of a frequency would be a NaN, and the step any number."""
     assert steps(native, 64, scaling=3, factor=4.0, original=1000.0, low=low, high=high)[0] == INVAL
