@@ -318,6 +318,8 @@ template <class T> cudaError_t launch_rotate(const RotArgs& a, int layout, dim3 
 
 int rotate(const cac_rotary* r, RotArgs& a, int heads, int kv_heads, void* stream) {
     if (a.rows >= 1 << 30) return CAC_E_LIMIT;   // blocks of both sides are counted in 31 bits
+    const int sms = sm_count(r->device);
+    if (sms < 1) return CAC_E_CUDA;
     const int D = r->head_dim, N = r->dtype == CAC_DTYPE_BF16 ? 8 : 4;
     a.steps = r->steps;
     a.q.gain = r->q_gain, a.k.gain = r->k_gain;
@@ -339,13 +341,13 @@ int rotate(const cac_rotary* r, RotArgs& a, int heads, int kv_heads, void* strea
             s->block_rows = 1, s->blocks = 0;
             continue;
         }
-        s->block_rows = (int)std::max(1ll, std::min({(long long)room, a.rows / (152ll * 4), (10ll * ROT_THREADS + items - 1) / items}));
+        s->block_rows = (int)std::max(1ll, std::min({(long long)room, a.rows / (sms * 4ll), (10ll * ROT_THREADS + items - 1) / items}));
         s->blocks = (a.rows + s->block_rows - 1) / s->block_rows;
         most = std::max(most, items * s->block_rows);
         threads = std::max(threads, (int)std::min<long long>(ROT_THREADS, (items * s->block_rows + 31) / 32 * 32));
     }
     const unsigned blocks = (unsigned)a.q.blocks + (unsigned)a.k.blocks;
-    const unsigned split = blocks >= 152 * 2 ? 1u : (unsigned)((most + threads - 1) / threads);
+    const unsigned split = blocks >= 2u * sms ? 1u : (unsigned)((most + threads - 1) / threads);
     DeviceScope dev(r->device);
     if (!dev.ok) return CAC_E_CUDA;
     const dim3 grid(blocks, split);
