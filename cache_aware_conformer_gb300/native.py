@@ -1157,7 +1157,8 @@ class Kv8Cache:
 
     def rotate(self, ids, rotary, q=None, k=None, starts=None, max_new=None, out=None, stream=None):
         """(q, k) of each sequence's last tokens turned by their positions in the cache (cac_kv8_rotate); arguments as
-        Rotary.rotate's.  Extend first, then rotate, write the keys and attend with the queries."""
+        Rotary.rotate's.  Extend first, then rotate, write the keys and attend with the queries.  max_new is there for what
+        attend's callers pass, and limits nothing here."""
         if rotary._dev != self._dev:
             raise ValueError(f"rotary: one on {self.device} is needed")
         n, p, s = self._list(ids, starts)
