@@ -175,3 +175,24 @@ def test_prompts_need_no_workspace_of_their_own_kind(dtype):
     got = b.cache.attend_shared(0, b.ids(range(80)), q)
     assert torch.equal(got, b.cache.attend(0, b.ids(range(80)), q))
     b.cache.check()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,group,dim", [(30, 6, 64), (9, 1, 64), (12, 8, 128), (12, 4, 144)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_non_finite_queries_of_both_types_and_kernels(dtype, n, group, dim, bad):
+    """Their own row and head become NaN, and no other changes."""
+    b = Shared("int8", heads=1, dim=dim, page=16, n_pages=60 + 2 * n, seqs=n, dtype=dtype)
+    b.family([(600, [2] * n)])
+    q, ids = b.rand(n, group, dim), b.ids(range(n))
+    want, lse = b.cache.attend_shared(0, ids, q.cuda(), lse=True)
+    x = q.clone()
+    x[3, group - 1, 5] = bad
+    got, s = b.cache.attend_shared(0, ids, x.cuda(), lse=True)
+    b.cache.check()
+    keep = torch.ones(n, group, dtype=torch.bool)
+    keep[3, group - 1] = False
+    assert torch.equal(got.cpu()[keep], want.cpu()[keep]) and torch.equal(s.cpu()[keep], lse.cpu()[keep])
+    assert torch.isnan(got[3, group - 1]).all() and torch.isnan(s[3, group - 1])
+    alone = b.cache.attend(0, ids, x.cuda())
+    assert torch.equal(torch.isnan(alone), torch.isnan(got))
