@@ -9,11 +9,16 @@
 // to itself is read for it, in pieces of even length, a block each; a last launch joins the parts.
 //
 // Measured (bf16, 8 K/V heads of 128, us; in brackets what the bytes take at a copy's rate): 64 sequences of up to 1,000 tokens behind 32,000, group
-// 4, int8: 88 (19.5), of which 11 go into finding and dealing out what is shared, 42 into its tokens, 27 into the others, 8 into the join; 4
-// sequences behind 60,000: 62 (19.6); 96 sequences in 6 groups behind up to 12,000, group 8, e4m3: 95 (21.7).  The shared tokens' kernel issues
-// in 51 % of its cycles and its tensor cores work in 40 %; shared memory bounds it, through which a tile of 128 tokens and 256 rows brings 32 KB
+// 4, int8: 87 (19.5); launch by launch, as a profiler runs them, finding 8, dealing out 11, the shared tokens 40, the others 25, the join 11 (the
+// shared tokens and the others overlap in part); 4 sequences behind 60,000: 64 (19.6); 96 sequences in 6 groups behind up to 12,000, group 8, e4m3: 91
+// (21.7).  In the first, the shared tokens' kernel issues in 52 % of the cycles in which an SM is active, and its tensor cores work in 39 % of them (34 %
+// of the launch); shared memory bounds it, through which a tile of 128 tokens and 256 rows brings 32 KB
 // of codes in and out, 64 KB of fp16, and 260 KB as operands: about 3,100 of the 4,000 clocks that it takes.  Without the exponentials, or without
 // the arithmetic of the conversion, it takes as long.
+//
+// What enters the tensor cores is fp16: codes exactly; for bf16 calls queries exactly after a power of two, and weights with 11 bits, three more than a
+// result has; for fp32 calls both as two parts, 22 bits.  Maxima, norms and sums are fp32.  Against 64 bits the results are off by 0.0016 for bf16, its
+// own rounding, and by 1.0e-6 to 2.1e-6 for fp32, where weights and sums in fp32 give 0.7e-6 to 2.4e-6 and cac_kv8_attend 0.6e-6 to 1.6e-6.
 //
 // What is shared is looked up on the device in each call: blocks of 16 tokens that every query of the group sees whole, in front of the
 // first page of those in which the tables differ.  Nothing but the sequences' tables is compared, so a result never hangs on what

@@ -3,7 +3,7 @@
 //
 // The angle of pair i at position p is p f_i.  f_i is held as a 64-bit fraction of a turn, so that p f_i modulo a
 // turn is one integer product, as good at position 10^9 as at 1; its nearest quarter turn is taken off in integers, and what is left, at
-// most an eighth of a turn, goes to fp32 with an error of 2^-26 of itself before sine and cosine.  These are computed
+// most an eighth of a turn, goes to fp32 with an error of 2^-24 of itself before sine and cosine.  These are computed
 // once for a row and serve all of its heads.
 //
 // The work is one read and one write of q and k: memory bounds it.  A group of threads has a head: each of them two
@@ -11,9 +11,10 @@
 // next to each other); where rot_dim / 2 is no whole number of pieces the group exchanges its values
 // through shared memory.  The pieces are loaded before the block looks up its positions.
 //
-// Measured (us; in brackets what the bytes take at a copy's rate): prompts of 22,000 rows, 40 heads of 128 bf16 with norms: 92 (67), issue slots
-// and a block's start of dependent reads; 9,100 rows of 20 heads of 128 fp32, half of each rotated in pairs, at positions to 10^6: 34 (27); two
-// rows of each of 256 sequences, 16 heads of 64 fp32: 3.4 (0.6), which are three dependent reads and a launch.
+// Measured (us; in brackets what the bytes take at a copy's rate): prompts of 22,000 rows, 40 heads of 128 bf16 with norms: 93 (67), where no pipe
+// is full (issue slots 67 %) and warps wait for their loads and for the instructions before; 9,100 rows of 20 heads of 128 fp32, half of each rotated
+// in pairs, at positions to 10^6: 34 (27); two rows of each of 256 sequences, 16 heads of 64 fp32: 3.3 (0.6), which are three dependent reads and
+// a launch.
 #include <algorithm>
 
 #include "cac_ops.h"

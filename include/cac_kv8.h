@@ -163,7 +163,9 @@ size_t cac_kv8_attend_workspace(const cac_kv8* c, int n, int rows, int max_new, 
 
 /* cac_kv8_attend for sequences that begin with the same tokens: the sequences of a
  * group whose tables name the same pages, as forks of one sequence do, and which
- * all see their tokens, have these read once for all of their queries.  The result
+ * all see their tokens, have these read once for many queries: for each 256 query
+ * rows of a K/V head (128 for fp32 with heads over 64), or for each 16 where heads
+ * are over 128 or groups have 32 rows or fewer on average.  The result
  * is cac_kv8_attend's but for rounding, whatever the tables hold: what is shared is
  * found in the call, on the device, and what is not shared is read for each sequence.
  *   groups  device int32 [n_groups + 1], 0 <= groups[0], never falling, <= n: the

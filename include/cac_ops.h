@@ -57,7 +57,7 @@ typedef struct cac_w4 {
     int32_t group;         /* 32, 64 or 128 */
     int32_t device;        /* CUDA device of every pointer of the call */
     const void* packed;    /* device bytes [n][k / 2], 16-byte aligned */
-    const void* scale;     /* device bf16 [n][k / group], 4-byte aligned */
+    const void* scale;     /* device bf16 [n][k / group], 4-byte aligned; below 2^100 in size */
     const uint8_t* zero;   /* device [n][k / group], 0 .. 15, 4-byte aligned; NULL: 8 everywhere */
 } cac_w4;
 
